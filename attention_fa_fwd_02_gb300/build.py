@@ -19,7 +19,7 @@ CSRC = os.path.join(PKG, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 OUT = os.path.join(PKG, "libfa.so")
 OBJ_DIR = os.path.join(PKG, "_build")
-SOURCES = ["fa_fwd.cu", "fa_bwd.cu", "fa_api.cu"]
+SOURCES = ["fa_fwd.cu", "fa_bwd.cu", "fa_api.cu", "kv_api.cu", "kv_rope.cu", "kv_pages.cu", "kv_rows.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 
 
@@ -36,7 +36,7 @@ def _flags(extra=()):
 
 
 def _deps_mtime() -> float:
-    files = [os.path.join(CSRC, f) for f in os.listdir(CSRC)] + [os.path.join(INCLUDE, "fa.h")]
+    files = [os.path.join(CSRC, f) for f in os.listdir(CSRC)] + [os.path.join(INCLUDE, f) for f in os.listdir(INCLUDE)]
     return max(os.path.getmtime(f) for f in files)
 
 

@@ -1,0 +1,77 @@
+// kv_common.cuh -- what the paged-cache kernels share: finding a row's sequence, table
+// look-ups with their checks, launch declarations.
+#pragma once
+#include <cstdint>
+#include "fa_common.cuh"
+#include "fakv.h"
+#include "ptx.cuh"
+
+namespace fa {
+namespace kv {
+
+__device__ __forceinline__ void raise(int* status, int bit) {
+  if (status) atomicOr(status, bit);
+}
+
+// A sequence of a call as the kernels see it. A slot out of range, or a length outside
+// the row, leaves an empty one.
+struct Seq {
+  int slot;   // -1: none
+  int len;    // tokens, the new ones included
+  int row0;   // first row of q
+  int n;      // new tokens
+};
+
+__device__ __forceinline__ Seq load_seq(const fakv_cache& c, const int* cu, const int* slots, int b,
+                                        int T) {
+  Seq s;
+  const int r0 = cu[b], r1 = cu[b + 1];
+  const int slot = slots ? slots[b] : b;
+  s.row0 = max(0, min(r0, T));
+  s.n = max(0, min(r1, T) - s.row0);
+  s.slot = (slot >= 0 && slot < c.max_slots) ? slot : -1;
+  s.len = 0;
+  if (s.slot >= 0) {
+    const int len = c.lens[slot];
+    if (len >= 0 && (long long)len <= (long long)c.max_pages * c.page_size) s.len = len;
+    else if (s.n > 0) raise(c.status, FAKV_BAD_LENGTH);
+  } else if (s.n > 0) {
+    raise(c.status, FAKV_BAD_SLOT);
+  }
+  return s;
+}
+
+// page of token position `pos` of slot `slot` (both in range), or -1 with the status bit
+__device__ __forceinline__ int page_of(const fakv_cache& c, int slot, int pos, int shift) {
+  const int p = c.table[(long long)slot * c.table_stride + (pos >> shift)];
+  if ((unsigned)p < (unsigned)c.num_pages) return p;
+  raise(c.status, FAKV_BAD_PAGE);
+  return -1;
+}
+
+inline int log2_of(int x) {
+  int s = 0;
+  while ((1 << s) < x) ++s;
+  return s;
+}
+
+inline int esize(fa_dtype t) { return t == FA_BF16 ? 2 : 4; }
+
+// launchers (arguments validated in kv_api.cu)
+fa_status launch_rope(const void* q, const void* k, void* qo, void* ko, const void* pos,
+                      const fakv_rope& r, const fakv_rope_params& p, cudaStream_t s);
+fa_status launch_append(const void* q, const void* k, const void* v, void* qo, const int* cu,
+                        const int* slots, const fakv_rope* r, const fakv_cache& c,
+                        const fakv_tokens& p, cudaStream_t s);
+fa_status launch_attend_rows(const void* q, void* O, float* LSE, const int* cu, const int* slots,
+                             const fakv_cache& c, const fakv_tokens& p, cudaStream_t s);
+fa_status launch_attend_tiles(const void* q, void* O, float* LSE, const int* cu, const int* slots,
+                              const fakv_cache& c, const fakv_tokens& p, cudaStream_t s);
+fa_status launch_grow(const fakv_cache& c, const int* slots, const int* add, int n, cudaStream_t s);
+fa_status launch_fork(const fakv_cache& c, const int* src, const int* dst, int n, cudaStream_t s);
+fa_status launch_free(const fakv_cache& c, const int* slots, const int* keep, int n, cudaStream_t s);
+fa_status launch_compact(const fakv_cache& c, cudaStream_t s);
+unsigned int read_and_clear_kv_status(cudaError_t* err);
+
+}  // namespace kv
+}  // namespace fa

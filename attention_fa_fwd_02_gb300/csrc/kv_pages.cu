@@ -1,0 +1,484 @@
+// kv_pages.cu -- the pages of a paged cache: growing, forking, freeing, compacting.
+//
+// The book-keeping is a few thousand integers and is bound by the latency of its
+// dependent steps, so each list is planned by one block in one launch and the pages that
+// have to move are copied by a second, launched as its programmatic dependent. Page
+// copies are bound by bandwidth (2 x the bytes of the pages). Every choice depends on the
+// list and on page numbers alone (prefix sums, no first-come atomics), so results are
+// the same on every run.
+#include "kv_common.cuh"
+
+namespace fa {
+namespace kv {
+namespace {
+
+constexpr int PLAN = 1024;   // threads of a planning block
+constexpr int SCAN = 4;      // reference counts per thread and step
+
+// Sums saturate: no list can be served more than 2^28 pages, and beyond them only "too
+// many" matters.
+constexpr unsigned MANY = 1u << 30;
+__device__ __forceinline__ unsigned sat(unsigned x, unsigned y) { return min(x + y, MANY); }
+
+// Exclusive prefix sum over the block (PLAN threads, values up to MANY); *total: the sum.
+__device__ __forceinline__ unsigned block_scan(unsigned x, unsigned* total) {
+  __shared__ unsigned sums[PLAN / 32], before[PLAN / 32 + 1];
+  const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
+  unsigned y = x;
+#pragma unroll
+  for (int d = 1; d < 32; d <<= 1) {
+    const unsigned v = __shfl_up_sync(0xffffffffu, y, d);
+    if (lane >= d) y = sat(y, v);
+  }
+  if (lane == 31) sums[w] = y;
+  __syncthreads();
+  if (w == 0) {
+    unsigned z = sums[lane];
+#pragma unroll
+    for (int d = 1; d < 32; d <<= 1) {
+      const unsigned u = __shfl_up_sync(0xffffffffu, z, d);
+      if (lane >= d) z = sat(z, u);
+    }
+    before[lane + 1] = z;
+    if (lane == 0) before[0] = 0;
+  }
+  __syncthreads();
+  y = __shfl_up_sync(0xffffffffu, y, 1);
+  const unsigned r = sat(before[w], lane ? y : 0u);
+  *total = before[PLAN / 32];
+  __syncthreads();
+  return r;
+}
+
+__device__ __forceinline__ int pages_of(int tokens, int shift) {
+  return (int)(((long long)tokens + (1 << shift) - 1) >> shift);
+}
+
+// a slot's length, 0 and the status bit where it is no length of a row
+__device__ __forceinline__ int length_of(const fakv_cache& c, int slot) {
+  const int len = c.lens[slot];
+  if (len >= 0 && (long long)len <= (long long)c.max_pages * c.page_size) return len;
+  raise(c.status, FAKV_BAD_LENGTH);
+  return 0;
+}
+
+// ------------------------------------------------------------------ page copies
+struct CopyArgs {
+  char* base[2];           // K, V
+  long long plane_bytes, page_bytes;  // strides
+  int planes, chunk, chunks;          // `chunk` bytes per block step, `chunks` to a page
+  int bytes;                          // of a page
+};
+
+constexpr int COPY_THREADS = 256;
+constexpr int COPY_UNROLL = 4;
+constexpr int COPY_CHUNK = COPY_THREADS * COPY_UNROLL * 16;
+
+// pages pair[i].x -> pair[i].y for i < n, in every plane of K and V
+__device__ __forceinline__ void copy_pages(const CopyArgs& a, const int2* pair, int n) {
+  const long long per = 2ll * a.planes * a.chunks;
+  for (long long w = blockIdx.x; w < n * per; w += gridDim.x) {
+    const int i = (int)(w / per);
+    int r = (int)(w - i * per);
+    const int ch = r % a.chunks;
+    r /= a.chunks;
+    const int2 p = pair[i];
+    char* base = a.base[r & 1] + (r >> 1) * a.plane_bytes;
+    const uint4* src = reinterpret_cast<const uint4*>(base + p.x * a.page_bytes);
+    uint4* dst = reinterpret_cast<uint4*>(base + p.y * a.page_bytes);
+    const int end = a.bytes / 16;
+    const int at = ch * (COPY_CHUNK / 16) + threadIdx.x;
+    uint4 v[COPY_UNROLL];
+#pragma unroll
+    for (int k = 0; k < COPY_UNROLL; ++k)
+      if (at + k * COPY_THREADS < end) v[k] = src[at + k * COPY_THREADS];
+#pragma unroll
+    for (int k = 0; k < COPY_UNROLL; ++k)
+      if (at + k * COPY_THREADS < end) dst[at + k * COPY_THREADS] = v[k];
+  }
+}
+
+CopyArgs copy_args(const fakv_cache& c) {
+  const long long es = esize(c.dtype);
+  CopyArgs a;
+  a.base[0] = static_cast<char*>(c.K);
+  a.base[1] = static_cast<char*>(c.V);
+  a.plane_bytes = c.plane_stride * es;
+  a.page_bytes = c.page_stride * es;
+  a.planes = c.planes;
+  a.bytes = (int)((long long)c.page_size * c.HKV * c.D * es);
+  a.chunk = COPY_CHUNK;
+  a.chunks = (a.bytes + COPY_CHUNK - 1) / COPY_CHUNK;
+  return a;
+}
+
+int copy_grid(long long pages_at_most, const CopyArgs& a) {
+  const long long w = pages_at_most * 2 * a.planes * a.chunks, most = 8ll * host::sm_count();
+  return (int)(w < 1 ? 1 : w < most ? w : most);
+}
+
+// ------------------------------------------------------------------ grow
+struct GrowArgs {
+  fakv_cache c;
+  const int* slots;
+  const int* add;
+  int n, shift;
+  int* mark;   // scratch [max_slots]: first place of a slot in the list
+  int* fresh;  // scratch [num_pages]: the free pages, in order
+  int2* pair;  // scratch [n]: pages to copy
+  int* count;  // scratch: how many
+};
+
+// Entry i needs pages for its new tokens, and one for a shared last page with room in it.
+// Prefix sums of the needs over the list give each entry its place among the free pages;
+// these are ranked by walking refs upwards until the list is served. Ranks then go to
+// (entry, column) by a search in the prefix, so one long entry is as parallel as many
+// short ones. Released shares are taken off at the end: no page that is a copy's source
+// becomes free before the copies. Lists longer than the block are taken part by part.
+__global__ void __launch_bounds__(PLAN) grow_kernel(const __grid_constant__ GrowArgs a) {
+  __shared__ unsigned first[PLAN];
+  __shared__ int col0[PLAN], slot_of[PLAN];  // slot_of: -1 where nothing is given
+  __shared__ int from_sh;
+  ptx::grid_launch_dependents();
+  const int tid = threadIdx.x;
+  for (int i = tid; i < a.n; i += PLAN) {
+    const int s = a.slots[i];
+    if ((unsigned)s < (unsigned)a.c.max_slots) a.mark[s] = a.n;
+  }
+  __syncthreads();
+  for (int i = tid; i < a.n; i += PLAN) {
+    const int s = a.slots[i];
+    if ((unsigned)s < (unsigned)a.c.max_slots) atomicMin(&a.mark[s], i);
+  }
+  __syncthreads();
+  int copies = 0;         // copies listed so far
+  int from = 0;           // first page not yet walked past
+  bool exhausted = false; // an entry was not served: none that needs pages is, from there on
+  for (int e0 = 0; e0 < a.n; e0 += PLAN) {
+    const int i = e0 + tid;
+    int slot = -1, len = 0, add = 0, old = 0, tail = -1;
+    unsigned need = 0;
+    if (i < a.n) {
+      slot = a.slots[i];
+      if ((unsigned)slot >= (unsigned)a.c.max_slots) { raise(a.c.status, FAKV_BAD_SLOT); slot = -1; }
+      else if (a.mark[slot] != i) { raise(a.c.status, FAKV_REPEATED); slot = -1; }
+    }
+    if (slot >= 0) {
+      len = length_of(a.c, slot);
+      add = a.add[i];
+      if (add < 0) { raise(a.c.status, FAKV_BAD_LENGTH); slot = -1; }
+    }
+    if (slot >= 0) {
+      old = pages_of(len, a.shift);
+      if ((long long)len + add > (long long)a.c.max_pages * a.c.page_size) {
+        raise(a.c.status, FAKV_ROW_FULL);
+        slot = -1;
+      } else {
+        if (add > 0 && (len & (a.c.page_size - 1))) {
+          const int p = page_of(a.c, slot, len, a.shift);
+          if (p >= 0 && a.c.refs[p] > 1) tail = p;
+        }
+        need = pages_of(len + add, a.shift) - old + (tail >= 0);
+      }
+    }
+    unsigned total;
+    const unsigned place = block_scan(need, &total);
+    first[tid] = place;
+    if (tid == 0) from_sh = from;
+    // rank the free pages until there are `total`
+    unsigned got = 0;
+    for (int at = from; !exhausted && got < total && at < a.c.num_pages; at += PLAN * SCAN) {
+      bool open[SCAN];
+      unsigned mine = 0, here;
+#pragma unroll
+      for (int k = 0; k < SCAN; ++k) {
+        const int page = at + tid * SCAN + k;
+        open[k] = page < a.c.num_pages && a.c.refs[page] == 0;
+        mine += open[k];
+      }
+      unsigned rank = got + block_scan(mine, &here);
+#pragma unroll
+      for (int k = 0; k < SCAN; ++k) {
+        if (!open[k] || rank >= total) continue;
+        const int page = at + tid * SCAN + k;
+        a.fresh[rank] = page;
+        if (++rank == total) from_sh = page + 1;
+      }
+      got += here;
+    }
+    const unsigned found = min(got, total);
+    const bool served = slot >= 0 && (need == 0 || place + need <= found);
+    if (slot >= 0 && !served) raise(a.c.status, FAKV_NO_PAGES);
+    if (found < total) exhausted = true;
+    col0[tid] = old - (tail >= 0);
+    slot_of[tid] = served ? slot : -1;
+    __syncthreads();
+    from = from_sh;
+    for (unsigned r = tid; r < found; r += PLAN) {
+      int lo = 0, hi = PLAN;  // the entry of rank r: the last with first <= r
+      while (hi - lo > 1) {
+        const int mid = (lo + hi) / 2;
+        if (first[mid] <= r) lo = mid; else hi = mid;
+      }
+      if (slot_of[lo] < 0) continue;
+      const int page = a.fresh[r];
+      a.c.table[(long long)slot_of[lo] * a.c.table_stride + col0[lo] + (int)(r - first[lo])] = page;
+      a.c.refs[page] = 1;
+    }
+    const bool copy = served && tail >= 0;
+    unsigned n_copy;
+    const unsigned c_at = block_scan(copy, &n_copy);
+    if (copy) a.pair[copies + c_at] = make_int2(tail, a.fresh[place]);
+    copies += (int)n_copy;
+    if (served) a.c.lens[slot] = len + add;
+    __syncthreads();
+  }
+  for (int i = tid; i < copies; i += PLAN) atomicSub(&a.c.refs[a.pair[i].x], 1);
+  if (tid == 0) *a.count = copies;
+}
+
+__global__ void __launch_bounds__(COPY_THREADS) copy_kernel(const __grid_constant__ CopyArgs a,
+                                                            const int2* pair, const int* count) {
+  ptx::grid_dependency_wait();
+  copy_pages(a, pair, *count);
+}
+
+// ------------------------------------------------------------------ fork, free
+struct ListArgs {
+  fakv_cache c;
+  const int* src;  // fork
+  const int* dst;  // fork: destinations; free: the slots
+  const int* keep; // free, may be null
+  int n, shift;
+  int* rows;       // fork scratch [n][max_pages]
+  int* lens;       // fork scratch [n]: the sources' lengths, -1: entry left out
+};
+
+// whether entry i's slot in `list` is in range and named by no earlier entry (one block)
+__device__ __forceinline__ bool entry_ok(const fakv_cache& c, const int* list, int i, int slot) {
+  if ((unsigned)slot >= (unsigned)c.max_slots) {
+    if (threadIdx.x == 0) raise(c.status, FAKV_BAD_SLOT);
+    return false;
+  }
+  bool seen = false;
+  for (int j = threadIdx.x; j < i; j += blockDim.x) seen |= list[j] == slot;
+  if (__syncthreads_or(seen)) {
+    if (threadIdx.x == 0) raise(c.status, FAKV_REPEATED);
+    return false;
+  }
+  return true;
+}
+
+// Takes the sources' rows and counts one more holder for their pages, before anything is
+// released: a page that moves from one slot of the list to another stays in use.
+__global__ void __launch_bounds__(256) fork_take_kernel(const __grid_constant__ ListArgs a) {
+  ptx::grid_launch_dependents();
+  for (int i = blockIdx.x; i < a.n; i += gridDim.x) {
+    const int src = a.src[i], dst = a.dst[i];
+    bool ok = entry_ok(a.c, a.dst, i, dst);
+    if (ok && (unsigned)src >= (unsigned)a.c.max_slots) {
+      if (threadIdx.x == 0) raise(a.c.status, FAKV_BAD_SLOT);
+      ok = false;
+    }
+    const int len = ok ? length_of(a.c, src) : -1;
+    if (threadIdx.x == 0) a.lens[i] = len;
+    const int* row = a.c.table + (long long)src * a.c.table_stride;
+    for (int k = threadIdx.x; ok && k < pages_of(len, a.shift); k += blockDim.x) {
+      const int p = row[k];
+      a.rows[(long long)i * a.c.max_pages + k] = p;
+      if ((unsigned)p < (unsigned)a.c.num_pages) atomicAdd(&a.c.refs[p], 1);
+      else raise(a.c.status, FAKV_BAD_PAGE);
+    }
+  }
+}
+
+// columns [from, to) of a slot's row released
+__device__ __forceinline__ void release(const fakv_cache& c, int* row, int from, int to) {
+  for (int k = from + threadIdx.x; k < to; k += blockDim.x) {
+    const int p = row[k];
+    if ((unsigned)p < (unsigned)c.num_pages) atomicSub(&c.refs[p], 1);
+    else raise(c.status, FAKV_BAD_PAGE);
+    row[k] = -1;
+  }
+}
+
+__global__ void __launch_bounds__(256) fork_give_kernel(const __grid_constant__ ListArgs a) {
+  ptx::grid_dependency_wait();
+  for (int i = blockIdx.x; i < a.n; i += gridDim.x) {
+    const int len = a.lens[i];
+    if (len < 0) continue;
+    const int dst = a.dst[i];
+    int* row = a.c.table + (long long)dst * a.c.table_stride;
+    release(a.c, row, 0, pages_of(length_of(a.c, dst), a.shift));
+    __syncthreads();
+    for (int k = threadIdx.x; k < pages_of(len, a.shift); k += blockDim.x)
+      row[k] = a.rows[(long long)i * a.c.max_pages + k];
+    if (threadIdx.x == 0) a.c.lens[dst] = len;
+  }
+}
+
+__global__ void __launch_bounds__(256) free_kernel(const __grid_constant__ ListArgs a) {
+  for (int i = blockIdx.x; i < a.n; i += gridDim.x) {
+    const int slot = a.dst[i];
+    if (!entry_ok(a.c, a.dst, i, slot)) continue;
+    const int len = length_of(a.c, slot);
+    int keep = a.keep ? a.keep[i] : 0;
+    if (keep < 0) {
+      if (threadIdx.x == 0) raise(a.c.status, FAKV_BAD_LENGTH);
+      keep = 0;
+    }
+    keep = min(keep, len);
+    __syncthreads();  // every thread has read the length
+    release(a.c, a.c.table + (long long)slot * a.c.table_stride, pages_of(keep, a.shift),
+            pages_of(len, a.shift));
+    if (threadIdx.x == 0) a.c.lens[slot] = keep;
+  }
+}
+
+// ------------------------------------------------------------------ compact
+struct CompactArgs {
+  fakv_cache c;
+  CopyArgs copy;
+  int shift;
+  int* to;     // scratch [num_pages]: where a page went
+  int2* pair;  // scratch [num_pages]
+  int* count;  // scratch: how many moves
+};
+
+__global__ void __launch_bounds__(PLAN) compact_plan_kernel(const __grid_constant__ CompactArgs a) {
+  ptx::grid_launch_dependents();
+  const int tid = threadIdx.x, N = a.c.num_pages;
+  unsigned live = 0;
+  for (int at = tid; at < N; at += PLAN) live += a.c.refs[at] > 0;
+  unsigned L_;
+  block_scan(live, &L_);
+  const int L = (int)L_;
+  int holes = 0, movers = 0;  // ranked so far (equal in the end)
+  for (int at = 0; at < N; at += PLAN * SCAN) {
+    int h = 0, m = 0;
+    bool used[SCAN];
+#pragma unroll
+    for (int k = 0; k < SCAN; ++k) {
+      const int p = at + tid * SCAN + k;
+      used[k] = p < N && a.c.refs[p] > 0;
+      if (p < N) { h += p < L && !used[k]; m += p >= L && used[k]; }
+    }
+    // at most PLAN * SCAN of each in a step: both fit one word
+    unsigned both;
+    const unsigned r = block_scan((unsigned)(h | (m << 16)), &both);
+    int rh = holes + (int)(r & 0xffff), rm = movers + (int)(r >> 16);
+#pragma unroll
+    for (int k = 0; k < SCAN; ++k) {
+      const int p = at + tid * SCAN + k;
+      if (p >= N) break;
+      if (p < L && !used[k]) a.pair[rh++].y = p;
+      if (p >= L && used[k]) a.pair[rm++].x = p;
+      a.to[p] = p;
+    }
+    holes += (int)(both & 0xffff);
+    movers += (int)(both >> 16);
+  }
+  __syncthreads();
+  for (int i = tid; i < movers; i += PLAN) {
+    const int2 p = a.pair[i];
+    a.to[p.x] = p.y;
+    a.c.refs[p.y] = a.c.refs[p.x];
+    a.c.refs[p.x] = 0;
+  }
+  if (tid == 0) a.count[0] = movers;
+}
+
+// the rows renumbered and the pages moved (sources lie above every destination)
+__global__ void __launch_bounds__(COPY_THREADS) compact_move_kernel(const __grid_constant__ CompactArgs a) {
+  ptx::grid_dependency_wait();
+  for (int s = blockIdx.x; s < a.c.max_slots; s += gridDim.x) {
+    int* row = a.c.table + (long long)s * a.c.table_stride;
+    const int n = min(a.c.max_pages, pages_of(max(0, a.c.lens[s]), a.shift));
+    for (int k = threadIdx.x; k < n; k += blockDim.x) {
+      const int p = row[k];
+      if ((unsigned)p < (unsigned)a.c.num_pages) {
+        const int q = a.to[p];
+        if (q != p) row[k] = q;
+      }
+    }
+  }
+  copy_pages(a.copy, a.pair, a.count[0]);
+}
+
+// Stream-ordered scratch that is given back when it goes out of scope.
+struct Scratch {
+  char* p = nullptr;
+  cudaStream_t s;
+  bool ok;
+  Scratch(size_t bytes, cudaStream_t s_) : s(s_) {
+    void* q = nullptr;
+    ok = host::scratch_alloc(&q, bytes, s) == cudaSuccess;
+    p = static_cast<char*>(q);
+  }
+  ~Scratch() { if (ok) host::scratch_free(p, s); }
+};
+
+fa_status done() { return cudaGetLastError() == cudaSuccess ? FA_OK : FA_ERR_CUDA; }
+
+}  // namespace
+
+fa_status launch_grow(const fakv_cache& c, const int* slots, const int* add, int n, cudaStream_t s) {
+  const size_t pair = 16, fresh = pair + (size_t)n * 8, mark = fresh + (size_t)c.num_pages * 4;
+  Scratch w(mark + (size_t)c.max_slots * 4, s);
+  if (!w.ok) return FA_ERR_CUDA;
+  GrowArgs a = {c, slots, add, n, log2_of(c.page_size), reinterpret_cast<int*>(w.p + mark),
+                reinterpret_cast<int*>(w.p + fresh), reinterpret_cast<int2*>(w.p + pair),
+                reinterpret_cast<int*>(w.p)};
+  {
+    host::KernelTimer t("grow", s);
+    grow_kernel<<<1, PLAN, 0, s>>>(a);
+  }
+  const CopyArgs ca = copy_args(c);
+  host::KernelTimer t("grow_copy", s);
+  if (launch_programmatic(copy_kernel, dim3(copy_grid(n, ca)), dim3(COPY_THREADS), s, ca,
+                          (const int2*)a.pair, (const int*)a.count) != cudaSuccess)
+    return FA_ERR_CUDA;
+  return done();
+}
+
+fa_status launch_fork(const fakv_cache& c, const int* src, const int* dst, int n, cudaStream_t s) {
+  const size_t rows = (size_t)n * c.max_pages * 4;
+  Scratch w(rows + (size_t)n * 4, s);
+  if (!w.ok) return FA_ERR_CUDA;
+  ListArgs a = {c, src, dst, nullptr, n, log2_of(c.page_size), reinterpret_cast<int*>(w.p),
+                reinterpret_cast<int*>(w.p + rows)};
+  const int grid = n < 8 * host::sm_count() ? n : 8 * host::sm_count();
+  {
+    host::KernelTimer t("fork_take", s);
+    fork_take_kernel<<<grid, 256, 0, s>>>(a);
+  }
+  host::KernelTimer t("fork_give", s);
+  if (launch_programmatic(fork_give_kernel, dim3(grid), dim3(256), s, a) != cudaSuccess) return FA_ERR_CUDA;
+  return done();
+}
+
+fa_status launch_free(const fakv_cache& c, const int* slots, const int* keep, int n, cudaStream_t s) {
+  ListArgs a = {c, nullptr, slots, keep, n, log2_of(c.page_size), nullptr, nullptr};
+  const int grid = n < 8 * host::sm_count() ? n : 8 * host::sm_count();
+  host::KernelTimer t("free", s);
+  free_kernel<<<grid, 256, 0, s>>>(a);
+  return done();
+}
+
+fa_status launch_compact(const fakv_cache& c, cudaStream_t s) {
+  Scratch w((size_t)c.num_pages * 12 + 16, s);
+  if (!w.ok) return FA_ERR_CUDA;
+  CompactArgs a = {c, copy_args(c), log2_of(c.page_size), reinterpret_cast<int*>(w.p + (size_t)c.num_pages * 8),
+                   reinterpret_cast<int2*>(w.p), reinterpret_cast<int*>(w.p + (size_t)c.num_pages * 12)};
+  {
+    host::KernelTimer t("compact_plan", s);
+    compact_plan_kernel<<<1, PLAN, 0, s>>>(a);
+  }
+  host::KernelTimer t("compact_move", s);
+  if (launch_programmatic(compact_move_kernel, dim3(copy_grid(c.num_pages, a.copy)), dim3(COPY_THREADS), s, a) != cudaSuccess)
+    return FA_ERR_CUDA;
+  return done();
+}
+
+}  // namespace kv
+}  // namespace fa

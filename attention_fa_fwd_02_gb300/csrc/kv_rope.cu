@@ -1,0 +1,325 @@
+// kv_rope.cu -- rotary positions, and new tokens into the paged cache.
+//
+// Pair i of a head turns by the angle p f_i (mod 2 pi). The frequencies are 64-bit
+// fractions of a turn, so p f_i mod 1 is the low word of one 64-bit product, exact for
+// every position. Its nearest quarter turn is taken off in integers and the remainder (at
+// most an eighth of a turn, 32 bits of it kept) goes through sincospif: cos and sin are
+// good to fp32 rounding however far the position.
+//
+// Both operators are bound by the bytes of q, k, v, once in and once out. A block takes
+// a few tokens: it forms their cos / sin once in shared memory (a head would otherwise
+// cost EV sincos per 32 bytes moved, more issue slots than the copy leaves), while every
+// thread's first UB loads are already on their way. A unit is 2 EV columns of one head,
+// two 16-byte accesses: the two halves of EV pairs, or 2 EV adjacent columns.
+#include <cmath>
+#include "kv_common.cuh"
+
+namespace fa {
+namespace kv {
+namespace {
+
+constexpr int THREADS = 256;
+constexpr int UB = 4;          // units in flight per thread
+constexpr int MAX_TOKENS = 4;  // tokens per block
+constexpr int MAX_PAIRS = 64;  // rotary_dim <= 128
+
+struct Stream {  // rows of one tensor
+  const void* src;
+  void* dst;
+  long long s_token, s_head, d_token, d_head;
+};
+
+struct RopeArgs {
+  Stream x[3];  // q, k, v
+  int end[3];   // q: heads [0, end[0]), k: [end[0], end[1]), v: [end[1], end[2])
+  int T, tokens;  // rows; tokens per block
+  int rot, interleaved;
+  int units;      // units of a head that are moved
+  const unsigned long long* freqs;
+  float mscale, sign;
+  const void* positions;
+  int positions_64;
+  // append
+  const int* cu;
+  const int* slots;
+  int B, shift, plane;
+  fakv_cache c;
+};
+
+template <typename E, int EV>
+struct Chunk;  // EV elements: 16 bytes, or one element
+template <>
+struct Chunk<__nv_bfloat16, 8> { using V = uint4; };
+template <>
+struct Chunk<float, 4> { using V = uint4; };
+template <>
+struct Chunk<__nv_bfloat16, 1> { using V = uint16_t; };
+template <>
+struct Chunk<float, 1> { using V = uint32_t; };
+
+template <typename E, int EV>
+__device__ __forceinline__ void unpack(const typename Chunk<E, EV>::V& c, float (&f)[EV]) {
+  if constexpr (EV == 1) {
+    if constexpr (sizeof(E) == 2) f[0] = __uint_as_float((uint32_t)c << 16);
+    else f[0] = __uint_as_float(c);
+  } else {
+    const uint32_t w[4] = {c.x, c.y, c.z, c.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      if constexpr (sizeof(E) == 2) {
+        f[2 * i] = __uint_as_float(w[i] << 16);
+        f[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
+      } else {
+        f[i] = __uint_as_float(w[i]);
+      }
+    }
+  }
+}
+template <typename E, int EV>
+__device__ __forceinline__ typename Chunk<E, EV>::V pack(const float (&f)[EV]) {
+  typename Chunk<E, EV>::V c;
+  if constexpr (EV == 1) {
+    if constexpr (sizeof(E) == 2) c = __bfloat16_as_ushort(__float2bfloat16_rn(f[0]));
+    else c = __float_as_uint(f[0]);
+  } else {
+    uint32_t w[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      if constexpr (sizeof(E) == 2) {
+        const __nv_bfloat162 h = __floats2bfloat162_rn(f[2 * i], f[2 * i + 1]);
+        w[i] = *reinterpret_cast<const uint32_t*>(&h);
+      } else {
+        w[i] = __float_as_uint(f[i]);
+      }
+    }
+    c.x = w[0]; c.y = w[1]; c.z = w[2]; c.w = w[3];
+  }
+  return c;
+}
+
+// cos and sin of pos * freq turns (see the head of this file)
+__device__ __forceinline__ float2 turn(long long pos, unsigned long long freq) {
+  const unsigned long long t = (unsigned long long)pos * freq;
+  const unsigned quarter = (unsigned)((t + (1ull << 61)) >> 62);
+  const long long rest = (long long)(t - ((unsigned long long)quarter << 62));
+  float s, c;
+  sincospif((float)(int)(rest >> 30) * 0x1p-33f, &s, &c);  // the angle in units of pi
+  if (quarter & 1) { const float x = c; c = -s; s = x; }
+  if (quarter & 2) { c = -c; s = -s; }
+  return make_float2(c, s);
+}
+
+// The sequence of row t: the last b with cu[b] <= t (32 probes per round, one warp), or
+// -1 for rows past the last sequence. cu is probed inside [0, B] whatever it holds.
+__device__ __forceinline__ int find_seq(const int* cu, int B, int t) {
+  const int lane = ptx::lane_id();
+  if (t >= cu[B]) return -1;
+  int lo = 0, n = B;  // the answer lies in [lo, lo + n)
+  while (n > 1) {
+    const int step = (n + 31) / 32;
+    const int at = lo + lane * step;
+    const bool below = lane * step < n && cu[at] <= t;
+    const int hits = __popc(__ballot_sync(0xffffffffu, below));
+    if (hits == 0) return -1;
+    const int first = (hits - 1) * step;
+    n = min(step, n - first);
+    lo += first;
+  }
+  return cu[lo] <= t ? lo : -1;
+}
+
+template <typename E, int EV, bool APPEND, bool ROPE>
+__global__ void __launch_bounds__(THREADS) rope_kernel(const __grid_constant__ RopeArgs a) {
+  using V = typename Chunk<E, EV>::V;
+  __shared__ float2 cs[MAX_TOKENS][MAX_PAIRS];
+  __shared__ long long place[MAX_TOKENS];  // append: offset in the cache; -1: not written
+  __shared__ int live[MAX_TOKENS];         // append: the row belongs to a sequence
+  const int t0 = blockIdx.x * a.tokens;
+  const int tokens = min(a.tokens, a.T - t0);
+  const int pairs = a.rot / 2;
+  const int per_token = a.end[2] * a.units;
+  const int total = tokens * per_token;
+
+  struct Unit { int tok, which, head, c0, c1, pair; };
+  auto unit = [&](int u) {
+    Unit r;
+    r.tok = u / per_token;
+    u -= r.tok * per_token;
+    int h = u / a.units;
+    const int x = u - h * a.units;
+    r.which = h < a.end[0] ? 0 : h < a.end[1] ? 1 : 2;
+    r.head = h - (r.which ? a.end[r.which - 1] : 0);
+    const bool turned = ROPE && x < pairs / EV;
+    r.pair = turned && r.which < 2 ? x * EV : -1;
+    if (turned && !a.interleaved) { r.c0 = x * EV; r.c1 = r.c0 + pairs; }
+    else { r.c0 = x * 2 * EV; r.c1 = r.c0 + EV; }
+    return r;
+  };
+  V in[UB][2];
+  auto load = [&](int u0) {
+#pragma unroll
+    for (int i = 0; i < UB; ++i) {
+      const int u = u0 + i * THREADS;
+      if (u < total) {
+        const Unit r = unit(u);
+        const Stream& x = a.x[r.which];
+        const E* p = static_cast<const E*>(x.src) + (t0 + r.tok) * x.s_token + r.head * x.s_head;
+        in[i][0] = *reinterpret_cast<const V*>(p + r.c0);
+        in[i][1] = *reinterpret_cast<const V*>(p + r.c1);
+      }
+    }
+  };
+  load(threadIdx.x);
+
+  // positions, places, cos and sin of this block's tokens, a warp per token
+  for (int k = threadIdx.x / 32; k < tokens; k += THREADS / 32) {
+    const int t = t0 + k;
+    long long pos = 0;
+    if constexpr (APPEND) {
+      const int b = find_seq(a.cu, a.B, t);
+      long long at = -1;
+      if (b >= 0) {
+        const Seq s = load_seq(a.c, a.cu, a.slots, b, a.T);
+        pos = (long long)s.len - s.n + (t - s.row0);
+        if (s.slot >= 0 && pos >= 0) {
+          const int page = page_of(a.c, s.slot, (int)pos, a.shift);
+          if (page >= 0)
+            at = a.plane * a.c.plane_stride + page * a.c.page_stride +
+                 ((int)pos & (a.c.page_size - 1)) * a.c.token_stride;
+        } else if (s.slot >= 0) {
+          raise(a.c.status, FAKV_BAD_LENGTH);
+        }
+      }
+      if (ptx::lane_id() == 0) { place[k] = at; live[k] = b >= 0; }
+    } else {
+      pos = a.positions_64 ? static_cast<const long long*>(a.positions)[t]
+                           : static_cast<const int*>(a.positions)[t];
+    }
+    if constexpr (ROPE) {
+      for (int i = ptx::lane_id(); i < pairs; i += 32) {
+        const float2 v = turn(pos, a.freqs[i]);
+        cs[k][i] = make_float2(v.x * a.mscale, v.y * (a.mscale * a.sign));
+      }
+    }
+  }
+  __syncthreads();
+
+  for (int u0 = threadIdx.x; u0 < total; u0 += UB * THREADS) {
+    if (u0 != (int)threadIdx.x) load(u0);
+#pragma unroll
+    for (int i = 0; i < UB; ++i) {
+      const int u = u0 + i * THREADS;
+      if (u >= total) break;
+      const Unit r = unit(u);
+      const Stream& x = a.x[r.which];
+      E* p = static_cast<E*>(x.dst) + r.head * x.d_head;
+      if (APPEND && r.which > 0) {
+        if (place[r.tok] < 0) continue;
+        p += place[r.tok];
+      } else {
+        if (APPEND && !live[r.tok]) continue;
+        p += (t0 + r.tok) * x.d_token;
+      }
+      if (ROPE && r.pair >= 0) {
+        float f[2][EV], y[2][EV];
+        unpack<E, EV>(in[i][0], f[0]);
+        unpack<E, EV>(in[i][1], f[1]);
+        const float2* w = &cs[r.tok][r.pair];
+#pragma unroll
+        for (int j = 0; j < EV; ++j) {
+          // half: pair j is (f[0][j], f[1][j]); interleaved: columns 2 j, 2 j + 1
+          const float2 q = w[j];
+          const float u_ = a.interleaved ? f[2 * j / EV][2 * j % EV] : f[0][j];
+          const float v_ = a.interleaved ? f[(2 * j + 1) / EV][(2 * j + 1) % EV] : f[1][j];
+          // (written out, so that wide and narrow units round alike)
+          const float yu = __fmaf_rn(-v_, q.y, __fmul_rn(u_, q.x)), yv = __fmaf_rn(u_, q.y, __fmul_rn(v_, q.x));
+          if (a.interleaved) { y[2 * j / EV][2 * j % EV] = yu; y[(2 * j + 1) / EV][(2 * j + 1) % EV] = yv; }
+          else { y[0][j] = yu; y[1][j] = yv; }
+        }
+        in[i][0] = pack<E, EV>(y[0]);
+        in[i][1] = pack<E, EV>(y[1]);
+      }
+      *reinterpret_cast<V*>(p + r.c0) = in[i][0];
+      *reinterpret_cast<V*>(p + r.c1) = in[i][1];
+    }
+  }
+}
+
+template <typename E, int EV, bool APPEND>
+fa_status launch(RopeArgs& a, const char* name, cudaStream_t s) {
+  // Few rows: a token per block spreads them over the SMs; many: four share the set-up.
+  a.tokens = a.T >= 4 * MAX_TOKENS * host::sm_count() ? MAX_TOKENS : 1;
+  const dim3 grid((a.T + a.tokens - 1) / a.tokens);
+  host::KernelTimer t(name, s);
+  if (a.rot) rope_kernel<E, EV, APPEND, true><<<grid, THREADS, 0, s>>>(a);
+  else rope_kernel<E, EV, APPEND, false><<<grid, THREADS, 0, s>>>(a);
+  return cudaGetLastError() == cudaSuccess ? FA_OK : FA_ERR_CUDA;
+}
+
+template <bool APPEND>
+fa_status dispatch(RopeArgs& a, int D, fa_dtype dtype, bool inplace, const char* name, cudaStream_t s) {
+  // 16-byte chunks where the pairs, the strides and the pointers allow them
+  const int ev = dtype == FA_BF16 ? 8 : 4, es = esize(dtype);
+  bool wide = a.rot % (2 * ev) == 0;
+  for (int i = 0; i < 3; ++i) {
+    if (a.end[i] == (i ? a.end[i - 1] : 0)) continue;
+    const Stream& x = a.x[i];
+    for (long long v : {x.s_token, x.s_head, x.d_token, x.d_head}) wide = wide && v % ev == 0;
+    wide = wide && (reinterpret_cast<uintptr_t>(x.src) | reinterpret_cast<uintptr_t>(x.dst)) % 16 == 0;
+  }
+  // in place the columns behind the pairs stay where they are
+  a.units = (inplace ? a.rot : D) / (wide ? 2 * ev : 2);
+  if (es == 2) return wide ? launch<__nv_bfloat16, 8, APPEND>(a, name, s) : launch<__nv_bfloat16, 1, APPEND>(a, name, s);
+  return wide ? launch<float, 4, APPEND>(a, name, s) : launch<float, 1, APPEND>(a, name, s);
+}
+
+}  // namespace
+
+fa_status launch_rope(const void* q, const void* k, void* qo, void* ko, const void* pos,
+                      const fakv_rope& r, const fakv_rope_params& p, cudaStream_t s) {
+  RopeArgs a = {};
+  a.x[0] = {q, qo, p.q_token, p.q_head, p.qo_token, p.qo_head};
+  a.x[1] = {k, ko, p.k_token, p.k_head, p.ko_token, p.ko_head};
+  a.end[0] = p.H;
+  a.end[1] = a.end[2] = p.H + p.HKV;
+  a.T = p.T;
+  a.rot = r.rotary_dim;
+  a.interleaved = r.interleaved;
+  a.freqs = r.freqs;
+  a.mscale = r.mscale;
+  a.sign = p.inverse ? -1.f : 1.f;
+  a.positions = pos;
+  a.positions_64 = p.positions_64;
+  const bool inplace = (p.H == 0 || q == qo) && (p.HKV == 0 || k == ko);
+  return dispatch<false>(a, p.D, p.dtype, inplace, "rope", s);
+}
+
+fa_status launch_append(const void* q, const void* k, const void* v, void* qo, const int* cu,
+                        const int* slots, const fakv_rope* r, const fakv_cache& c,
+                        const fakv_tokens& p, cudaStream_t s) {
+  RopeArgs a = {};
+  a.x[0] = {q, qo, p.q_token, p.q_head, (long long)p.H * c.D, c.D};
+  a.x[1] = {k, c.K, p.k_token, p.k_head, c.token_stride, c.head_stride};
+  a.x[2] = {v, c.V, p.v_token, p.v_head, c.token_stride, c.head_stride};
+  a.end[0] = p.H;
+  a.end[1] = p.H + c.HKV;
+  a.end[2] = p.H + 2 * c.HKV;
+  a.T = p.T;
+  if (r) {
+    a.rot = r->rotary_dim;
+    a.interleaved = r->interleaved;
+    a.freqs = r->freqs;
+    a.mscale = r->mscale;
+  }
+  a.sign = 1.f;
+  a.cu = cu;
+  a.slots = slots;
+  a.B = p.B;
+  a.plane = p.plane;
+  a.shift = log2_of(c.page_size);
+  a.c = c;
+  return dispatch<true>(a, c.D, c.dtype, false, "append", s);
+}
+
+}  // namespace kv
+}  // namespace fa
