@@ -8,6 +8,7 @@
 #include <vector>
 #include <cudaTypedefs.h>
 #include "fa_common.cuh"
+#include "kv_common.cuh"
 
 namespace fa {
 namespace host {
@@ -22,9 +23,7 @@ cudaMemPool_t g_pool[MAX_DEVICES] = {};
 int g_sms[MAX_DEVICES] = {};
 }  // namespace
 
-bool encode_tiled_3d(CUtensorMap* map, CUtensorMapDataType dt, int esize, const void* base,
-                     uint64_t inner, uint64_t rows, uint64_t outer, uint64_t row_stride,
-                     uint32_t box_inner, uint32_t box_rows, int swizzle_bytes) {
+static bool load_encoder() {
   std::call_once(g_encode_once, [] {
     cudaDriverEntryPointQueryResult q;
     void* fn = nullptr;
@@ -33,7 +32,13 @@ bool encode_tiled_3d(CUtensorMap* map, CUtensorMapDataType dt, int esize, const 
         q == cudaDriverEntryPointSuccess)
       g_encode = reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(fn);
   });
-  if (!g_encode) return false;
+  return g_encode != nullptr;
+}
+
+bool encode_tiled_3d(CUtensorMap* map, CUtensorMapDataType dt, int esize, const void* base,
+                     uint64_t inner, uint64_t rows, uint64_t outer, uint64_t row_stride,
+                     uint32_t box_inner, uint32_t box_rows, int swizzle_bytes) {
+  if (!load_encoder()) return false;
   cuuint64_t dims[3] = {inner, rows, outer};
   cuuint64_t strides[2] = {row_stride * esize, row_stride * esize * rows};
   cuuint32_t box[3] = {box_inner, box_rows, 1};
@@ -44,6 +49,17 @@ bool encode_tiled_3d(CUtensorMap* map, CUtensorMapDataType dt, int esize, const 
                   : swizzle_bytes == 64 ? CU_TENSOR_MAP_SWIZZLE_64B
                                         : CU_TENSOR_MAP_SWIZZLE_NONE,
                   CU_TENSOR_MAP_L2_PROMOTION_L2_128B,
+                  CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+bool encode_tiled_4d(CUtensorMap* map, const void* base, const uint64_t (&dims)[4],
+                     const uint64_t (&strides)[3], const uint32_t (&box)[4]) {
+  if (!load_encoder()) return false;
+  const cuuint64_t d[4] = {dims[0], dims[1], dims[2], dims[3]};
+  const cuuint64_t st[3] = {strides[0], strides[1], strides[2]};
+  const cuuint32_t b[4] = {box[0], box[1], box[2], box[3]}, es[4] = {1, 1, 1, 1};
+  return g_encode(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, const_cast<void*>(base), d, st, b, es,
+                  CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_128B,
                   CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
@@ -266,9 +282,10 @@ FA_API fa_status fa_bwd_dsmat(const void* Q, const void* K, const void* V, const
 FA_API fa_status fa_device_status(fa_stream_t stream) {
   if (cudaStreamSynchronize(reinterpret_cast<cudaStream_t>(stream)) != cudaSuccess)
     return FA_ERR_CUDA;
-  cudaError_t e1 = cudaSuccess, e2 = cudaSuccess;
-  const unsigned int v = read_and_clear_fwd_status(&e1) | read_and_clear_bwd_status(&e2);
-  if (e1 != cudaSuccess || e2 != cudaSuccess) return FA_ERR_CUDA;
+  cudaError_t e1 = cudaSuccess, e2 = cudaSuccess, e3 = cudaSuccess;
+  const unsigned int v = read_and_clear_fwd_status(&e1) | read_and_clear_bwd_status(&e2) |
+                         kv::read_and_clear_kv_status(&e3);
+  if (e1 != cudaSuccess || e2 != cudaSuccess || e3 != cudaSuccess) return FA_ERR_CUDA;
   if (v & DEV_LAYOUT) return FA_ERR_LAYOUT;
   return (v & DEV_TIMEOUT) ? FA_ERR_TIMEOUT : FA_OK;
 }

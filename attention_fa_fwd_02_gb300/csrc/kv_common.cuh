@@ -7,6 +7,13 @@
 #include "ptx.cuh"
 
 namespace fa {
+namespace host {
+// A 4-D tensor map of 16-bit elements (innermost dimension without gaps, the others'
+// strides in bytes), 128-byte swizzle, zeros outside.
+bool encode_tiled_4d(CUtensorMap* map, const void* base, const uint64_t (&dims)[4],
+                     const uint64_t (&strides)[3], const uint32_t (&box)[4]);
+}  // namespace host
+
 namespace kv {
 
 __device__ __forceinline__ void raise(int* status, int bit) {

@@ -18,6 +18,7 @@
 //           as its O).
 //   O += P V  bf16: P = hi + lo, two bf16 terms, so that P's rounding (2^-9) does not add
 //           to the output's: the second product is free under the memory time.
+#include <algorithm>
 #include <cfloat>
 #include <cmath>
 #include "kv_sched.cuh"
@@ -143,19 +144,12 @@ __global__ void __launch_bounds__(NTHREADS, RowsCfg<E, D, MT>::CTAS_PER_SM)
   const E* const Kp = static_cast<const E*>(c.K) + a.plane * c.plane_stride;
   const E* const Vp = static_cast<const E*>(c.V) + a.plane * c.plane_stride;
 
-  int b = part.b, t = part.tile, head = part.head, unit = part.unit;
-  long long left = part.units;
-  bool first_seg = true;
-  Seq s = load_seq(c, a.cu, a.slots, b, a.T);
-  while (left > 0) {
-    if (t * R >= s.n * g.rep) {  // the next sequence with rows
-      t = 0;
-      do { s = load_seq(c, a.cu, a.slots, ++b, a.T); } while (s.n == 0);
-    }
-    const Tile x = tile_of(g, s, t);
-    const int take = (int)min((long long)(x.cost - unit), left);
-    const bool starts = unit == 0, ends = unit + take == x.cost;
-    const int n_units = min(take, x.units - unit);  // 0 for an item without keys
+  Walk walk(part);
+  Seg seg;
+  while (walk.next(g, c, a.cu, a.slots, a.T, seg)) {
+    const Seq& s = seg.s;
+    const Tile& x = seg.x;
+    const int head = seg.head;
 
     // ---- q rows into shared memory (zeros behind the item's rows and the tensor's columns)
     for (int i = tid; i < R * CH; i += NTHREADS) {
@@ -170,8 +164,8 @@ __global__ void __launch_bounds__(NTHREADS, RowsCfg<E, D, MT>::CTAS_PER_SM)
     cp_commit();
 
     // ---- this warp's groups of keys: g0, g0 + WARPS, ...
-    const int g_end = min((x.u0 + unit + n_units) * WARPS, (x.hi + GROUP - 1) / GROUP);
-    const int g0 = max((x.u0 + unit) * WARPS, x.lo / GROUP);
+    const int g_end = min((seg.k0 + seg.n) * WARPS, (x.hi + GROUP - 1) / GROUP);
+    const int g0 = max(seg.k0 * WARPS, x.lo / GROUP);
     const int gw = g0 + ((warp - g0) & (WARPS - 1));
     const int n = gw < g_end ? (g_end - gw + WARPS - 1) / WARPS : 0;
     // Pages of the next 32 groups, a group per lane (two pages where they hold 8 tokens),
@@ -431,8 +425,8 @@ __global__ void __launch_bounds__(NTHREADS, RowsCfg<E, D, MT>::CTAS_PER_SM)
         }
     }
     __syncthreads();
-    const bool whole = starts && ends;
-    const int slot = 2 * blockIdx.x + (first_seg ? 0 : 1);
+    const bool whole = seg.starts && seg.ends;
+    const int slot = 2 * blockIdx.x + seg.slot;
     for (int k = tid; k < x.rows * (D / 4); k += NTHREADS) {
       const int r = k / (D / 4), col = k % (D / 4) * 4;
       float M = -FLT_MAX;
@@ -466,103 +460,101 @@ __global__ void __launch_bounds__(NTHREADS, RowsCfg<E, D, MT>::CTAS_PER_SM)
       }
     }
     if (!whole && tid == 0)
-      a.part.left[slot] = {PART_VALID | (starts ? PART_STARTS : 0) | (ends ? PART_ENDS : 0), s.row0, x.rho0, x.rows,
+      a.part.left[slot] = {PART_VALID | (seg.starts ? PART_STARTS : 0) | (seg.ends ? PART_ENDS : 0), s.row0, x.rho0, x.rows,
                            head, {0, 0, 0}};
     __syncthreads();  // the rings are read: the next item may fill them
-    left -= take;
-    unit += take;
-    first_seg = false;
-    if (unit == x.cost) {
-      unit = 0;
-      if (++head == c.HKV) { head = 0; ++t; }
-    }
   }
 }
 
 // An item that several CTAs did parts of: the CTA in whose part it starts left the first
-// one in slot 2 c or 2 c + 1, the following CTAs the others in their slots 2 c', up to the
-// one that ends it. A block per (c, slot) and `JOIN_ROWS` rows; its threads share out the
-// columns and the parts, and the shares are merged in order.
+// one (at most one such per CTA, its last item: slot 1, or 0 if it is its first too), the
+// following CTAs the others in their slots 0, up to the one that ends it. Blocks (c, y)
+// join the item that CTA c left open, y sharing out its rows JOIN_ROWS at a time; a block's
+// threads share out the columns and the parts, and the shares are merged in order.
 constexpr int JOIN_THREADS = 512;
 constexpr int JOIN_ROWS = 4;
+constexpr int JOIN_BLOCKS = 16;
+
+struct Sum {  // sums of exponentials taken against the maximum M
+  float M, L;
+  float4 acc;
+  __device__ __forceinline__ void add(float m, float l, const float4& v) {
+    const float mn = fmaxf(M, m);
+    const float fo = ptx::ex2(M - mn), fn = ptx::ex2(m - mn);
+    M = mn;
+    L = L * fo + l * fn;
+    acc.x = acc.x * fo + v.x * fn;
+    acc.y = acc.y * fo + v.y * fn;
+    acc.z = acc.z * fo + v.z * fn;
+    acc.w = acc.w * fo + v.w * fn;
+  }
+};
 
 __global__ void __launch_bounds__(JOIN_THREADS) attend_join_kernel(const __grid_constant__ JoinArgs a) {
   ptx::grid_dependency_wait();
   __shared__ int parts_sh;
   __shared__ float2 ml[JOIN_THREADS];
   __shared__ float4 acc_sh[JOIN_THREADS];
-  const int cta = blockIdx.x, which = blockIdx.y, tid = threadIdx.x;
+  const int cta = blockIdx.x, tid = threadIdx.x;
+  constexpr int OPEN = PART_STARTS | PART_ENDS;
+  const int open0 = a.part.left[2 * cta].flags & OPEN, open1 = a.part.left[2 * cta + 1].flags & OPEN;
+  if (open0 != PART_STARTS && open1 != PART_STARTS) return;
+  const int which = open1 == PART_STARTS;
   const Left f = a.part.left[2 * cta + which];
-  const int r0 = blockIdx.z * JOIN_ROWS;
-  if ((f.flags & (PART_STARTS | PART_ENDS)) != PART_STARTS || r0 >= f.rows) return;
+  if (blockIdx.y * JOIN_ROWS >= f.rows) return;
   if (tid == 0) parts_sh = a.ctas;
   __syncthreads();
   for (int k = cta + 1 + tid; k < a.ctas; k += JOIN_THREADS)
     if (a.part.left[2 * k].flags & PART_ENDS) { atomicMin(&parts_sh, k); break; }
   __syncthreads();
   const int parts = parts_sh - cta + 1;  // slot 2 cta + which, then 2 (cta + 1), ...
-  const int cols = a.D / 4, rows = min(JOIN_ROWS, f.rows - r0);
-  const int shares = JOIN_THREADS / (JOIN_ROWS * cols);  // >= 4
+  const int cols = a.D / 4;
+  const int shares = JOIN_THREADS / (JOIN_ROWS * cols);  // 4 or 8
   const int col = tid % cols, r = tid / cols % JOIN_ROWS, share = tid / (cols * JOIN_ROWS);
   const int p0 = parts * share / shares, p1 = parts * (share + 1) / shares;
-  float M = -FLT_MAX, L = 0.f;
-  float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-  if (share < shares && r < rows) {
-    constexpr int U = 4;
-    for (int p = p0; p < p1; p += U) {
-      float2 x[U];
-      float4 v[U];
+  for (int r0 = blockIdx.y * JOIN_ROWS; r0 < f.rows; r0 += gridDim.y * JOIN_ROWS) {
+    Sum x = {-FLT_MAX, 0.f, make_float4(0.f, 0.f, 0.f, 0.f)};
+    const bool mine = r0 + r < f.rows;
+    if (mine) {
+      constexpr int U = 4;
+      for (int p = p0; p < p1; p += U) {
+        float2 y[U];
+        float4 v[U];
 #pragma unroll
-      for (int k = 0; k < U; ++k) {
-        if (p + k < p1) {
-          const size_t slot = p + k == 0 ? 2 * cta + which : 2 * (cta + p + k);
-          x[k] = a.part.ml[slot * a.R + r0 + r];
-          v[k] = *reinterpret_cast<const float4*>(a.part.O + (slot * a.R + r0 + r) * a.D + col * 4);
+        for (int k = 0; k < U; ++k) {
+          if (p + k < p1) {
+            const size_t row = (size_t)(p + k == 0 ? 2 * cta + which : 2 * (cta + p + k)) * a.R + r0 + r;
+            y[k] = a.part.ml[row];
+            v[k] = *reinterpret_cast<const float4*>(a.part.O + row * a.D + col * 4);
+          }
         }
-      }
 #pragma unroll
-      for (int k = 0; k < U; ++k) {
-        if (p + k < p1) {
-          const float mn = fmaxf(M, x[k].x);
-          const float fo = ptx::ex2(M - mn), fn = ptx::ex2(x[k].x - mn);
-          M = mn;
-          L = L * fo + x[k].y * fn;
-          acc.x = acc.x * fo + v[k].x * fn;
-          acc.y = acc.y * fo + v[k].y * fn;
-          acc.z = acc.z * fo + v[k].z * fn;
-          acc.w = acc.w * fo + v[k].w * fn;
-        }
+        for (int k = 0; k < U; ++k)
+          if (p + k < p1) x.add(y[k].x, y[k].y, v[k]);
       }
     }
-  }
-  ml[tid] = make_float2(M, L);
-  acc_sh[tid] = acc;
-  __syncthreads();
-  if (share > 0 || r >= rows) return;
-  for (int k = 1; k < shares; ++k) {
-    const int at = tid + k * cols * JOIN_ROWS;
-    const float2 x = ml[at];
-    const float4 v = acc_sh[at];
-    const float mn = fmaxf(M, x.x);
-    const float fo = ptx::ex2(M - mn), fn = ptx::ex2(x.x - mn);
-    M = mn;
-    L = L * fo + x.y * fn;
-    acc.x = acc.x * fo + v.x * fn;
-    acc.y = acc.y * fo + v.y * fn;
-    acc.z = acc.z * fo + v.z * fn;
-    acc.w = acc.w * fo + v.w * fn;
-  }
-  const float inv = L > 0.f ? 1.f / L : 0.f;
-  const int rho = f.rho0 + r0 + r;
-  const size_t at = (size_t)(f.row0 + rho / a.rep) * a.H + f.head * a.rep + rho % a.rep;
-  if (col == 0) a.LSE[at] = L > 0.f ? (M + log2f(L)) * LN2 : -INFINITY;
-  if (col * 4 < a.Dv) {
-    if (a.out_bf16)
-      *reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(a.O) + at * a.Dv + col * 4) =
-          make_uint2(bf2(acc.x * inv, acc.y * inv), bf2(acc.z * inv, acc.w * inv));
-    else
-      *reinterpret_cast<float4*>(static_cast<float*>(a.O) + at * a.Dv + col * 4) =
-          make_float4(acc.x * inv, acc.y * inv, acc.z * inv, acc.w * inv);
+    ml[tid] = make_float2(x.M, x.L);
+    acc_sh[tid] = x.acc;
+    __syncthreads();
+    if (share == 0 && mine) {
+      for (int k = 1; k < shares; ++k) {
+        const int at = tid + k * cols * JOIN_ROWS;
+        x.add(ml[at].x, ml[at].y, acc_sh[at]);
+      }
+      const float inv = x.L > 0.f ? 1.f / x.L : 0.f;
+      const int rho = f.rho0 + r0 + r;
+      const size_t at = (size_t)(f.row0 + rho / a.rep) * a.H + f.head * a.rep + rho % a.rep;
+      if (col == 0) a.LSE[at] = x.L > 0.f ? (x.M + log2f(x.L)) * LN2 : -INFINITY;
+      if (col * 4 < a.Dv) {
+        if (a.out_bf16)
+          *reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(a.O) + at * a.Dv + col * 4) =
+              make_uint2(bf2(x.acc.x * inv, x.acc.y * inv), bf2(x.acc.z * inv, x.acc.w * inv));
+        else
+          *reinterpret_cast<float4*>(static_cast<float*>(a.O) + at * a.Dv + col * 4) =
+              make_float4(x.acc.x * inv, x.acc.y * inv, x.acc.z * inv, x.acc.w * inv);
+      }
+    }
+    __syncthreads();
   }
 }
 
@@ -596,7 +588,7 @@ fa_status run(RowsArgs& a, cudaStream_t s) {
 
 fa_status launch_join(const JoinArgs& a, cudaStream_t s) {
   host::KernelTimer t("attend_join", s);
-  return launch_programmatic(attend_join_kernel, dim3(a.ctas, 2, (a.R + JOIN_ROWS - 1) / JOIN_ROWS),
+  return launch_programmatic(attend_join_kernel, dim3(a.ctas, std::min((a.R + JOIN_ROWS - 1) / JOIN_ROWS, JOIN_BLOCKS)),
                              dim3(JOIN_THREADS), s, a) == cudaSuccess ? FA_OK : FA_ERR_CUDA;
 }
 

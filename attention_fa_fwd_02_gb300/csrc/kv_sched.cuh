@@ -150,6 +150,51 @@ __device__ __forceinline__ Part find_part(const Geo& g, const fakv_cache& c, con
   return sh.part;
 }
 
+// A CTA's way along its part, an item (or what of it lies in the part) at a time.
+struct Seg {
+  Seq s;
+  Tile x;
+  int head;
+  int k0, n;          // units [k0, k0 + n) of keys (n = 0: an item that sees none)
+  bool starts, ends;  // the item begins / ends here
+  int slot;           // of a partial result: 0 or 1
+};
+
+struct Walk {
+  int b, tile, head, unit;
+  long long left;
+  Seq s;
+  bool moved;
+  __device__ __forceinline__ Walk(const Part& p) : b(p.b), tile(p.tile), head(p.head), unit(p.unit), left(p.units), moved(false) {}
+  __device__ __forceinline__ bool next(const Geo& g, const fakv_cache& c, const int* cu, const int* slots, int T, Seg& o) {
+    if (left <= 0) return false;
+    if (!moved) s = load_seq(c, cu, slots, b, T);
+    else if (unit == 0 && head == 0) {
+      while (tile * g.R >= s.n * g.rep) {  // the next sequence with rows
+        tile = 0;
+        s = load_seq(c, cu, slots, ++b, T);
+      }
+    }
+    o.s = s;
+    o.x = tile_of(g, s, tile);
+    o.head = head;
+    o.slot = moved ? 1 : 0;
+    const int take = (int)min((long long)(o.x.cost - unit), left);
+    o.k0 = o.x.u0 + unit;
+    o.n = min(take, o.x.units - unit);
+    o.starts = unit == 0;
+    o.ends = unit + take == o.x.cost;
+    left -= take;
+    unit += take;
+    moved = true;
+    if (o.ends) {
+      unit = 0;
+      if (++head == c.HKV) { head = 0; ++tile; }
+    }
+    return true;
+  }
+};
+
 // What a CTA left of an item that it did not do whole: slot 2 * cta (the item its part
 // begins in) or 2 * cta + 1 (the one it ends in).
 enum { PART_VALID = 1, PART_STARTS = 2, PART_ENDS = 4 };
