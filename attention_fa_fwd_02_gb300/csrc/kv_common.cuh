@@ -1,6 +1,7 @@
 // kv_common.cuh -- what the paged-cache kernels share: finding a row's sequence, table
 // look-ups with their checks, launch declarations.
 #pragma once
+#include <atomic>
 #include <cstdint>
 #include "fa_common.cuh"
 #include "fakv.h"
@@ -60,6 +61,19 @@ inline int log2_of(int x) {
   int s = 0;
   while ((1 << s) < x) ++s;
   return s;
+}
+
+// Dynamic shared memory of `kernel` raised to `bytes`, once per kernel and device (`done`: a
+// word of the kernel's own).
+template <typename K>
+inline bool allow_smem(K* kernel, int bytes, std::atomic<uint64_t>& done) {
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess) return false;
+  const uint64_t bit = 1ull << (dev & 63);
+  if (done.load(std::memory_order_acquire) & bit) return true;
+  if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes) != cudaSuccess) return false;
+  done.fetch_or(bit, std::memory_order_release);
+  return true;
 }
 
 inline int esize(fa_dtype t) { return t == FA_BF16 ? 2 : 4; }

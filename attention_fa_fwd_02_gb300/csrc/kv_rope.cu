@@ -6,11 +6,12 @@
 // most an eighth of a turn, 32 bits of it kept) goes through sincospif: cos and sin are
 // good to fp32 rounding however far the position.
 //
-// Both operators are bound by the bytes of q, k, v, once in and once out. A block takes
-// a few tokens: it forms their cos / sin once in shared memory (a head would otherwise
-// cost EV sincos per 32 bytes moved, more issue slots than the copy leaves), while every
-// thread's first UB loads are already on their way. A unit is 2 EV columns of one head,
-// two 16-byte accesses: the two halves of EV pairs, or 2 EV adjacent columns.
+// Both operators are bound by the bytes of q, k, v, once in and once out. A unit is 2 EV
+// columns of one head, two 16-byte accesses: the two halves of EV pairs, or 2 EV adjacent
+// columns. A thread keeps one unit and takes it through UB tokens, so indices are found
+// once and UB loads are on their way while the block forms the tokens' cos / sin, once for
+// all heads, in shared memory (by itself a unit would need EV sincos per 32 bytes moved,
+// more issue slots than the copy leaves).
 #include <cmath>
 #include "kv_common.cuh"
 
@@ -18,10 +19,10 @@ namespace fa {
 namespace kv {
 namespace {
 
-constexpr int THREADS = 256;
-constexpr int UB = 4;          // units in flight per thread
-constexpr int MAX_TOKENS = 4;  // tokens per block
-constexpr int MAX_PAIRS = 64;  // rotary_dim <= 128
+constexpr int MAX_THREADS = 512;
+constexpr int UB = 4;            // tokens per thread
+constexpr int CS_BYTES = 16384;  // cos / sin of a block's tokens
+constexpr int MAX_TOKENS = 64;   // per block
 
 struct Stream {  // rows of one tensor
   const void* src;
@@ -32,9 +33,12 @@ struct Stream {  // rows of one tensor
 struct RopeArgs {
   Stream x[3];  // q, k, v
   int end[3];   // q: heads [0, end[0]), k: [end[0], end[1]), v: [end[1], end[2])
-  int T, tokens;  // rows; tokens per block
+  int T;          // rows
+  int lanes;      // threads per unit: tokens of a block side by side
+  int deep;       // tokens per thread, 1 .. UB
   int rot, interleaved;
   int units;      // units of a head that are moved
+  int per_token;  // units of a token
   const unsigned long long* freqs;
   float mscale, sign;
   const void* positions;
@@ -129,50 +133,44 @@ __device__ __forceinline__ int find_seq(const int* cu, int B, int t) {
 }
 
 template <typename E, int EV, bool APPEND, bool ROPE>
-__global__ void __launch_bounds__(THREADS) rope_kernel(const __grid_constant__ RopeArgs a) {
+__global__ void __launch_bounds__(MAX_THREADS) rope_kernel(const __grid_constant__ RopeArgs a) {
   using V = typename Chunk<E, EV>::V;
-  __shared__ float2 cs[MAX_TOKENS][MAX_PAIRS];
+  extern __shared__ float2 cs[];           // [tokens][pairs]
   __shared__ long long place[MAX_TOKENS];  // append: offset in the cache; -1: not written
   __shared__ int live[MAX_TOKENS];         // append: the row belongs to a sequence
-  const int t0 = blockIdx.x * a.tokens;
-  const int tokens = min(a.tokens, a.T - t0);
+  const int span = a.lanes * a.deep;       // tokens of a block
+  const int t0 = blockIdx.x * span;
+  const int tokens = min(span, a.T - t0);
   const int pairs = a.rot / 2;
-  const int per_token = a.end[2] * a.units;
-  const int total = tokens * per_token;
 
-  struct Unit { int tok, which, head, c0, c1, pair; };
-  auto unit = [&](int u) {
-    Unit r;
-    r.tok = u / per_token;
-    u -= r.tok * per_token;
-    int h = u / a.units;
-    const int x = u - h * a.units;
-    r.which = h < a.end[0] ? 0 : h < a.end[1] ? 1 : 2;
-    r.head = h - (r.which ? a.end[r.which - 1] : 0);
-    const bool turned = ROPE && x < pairs / EV;
-    r.pair = turned && r.which < 2 ? x * EV : -1;
-    if (turned && !a.interleaved) { r.c0 = x * EV; r.c1 = r.c0 + pairs; }
-    else { r.c0 = x * 2 * EV; r.c1 = r.c0 + EV; }
-    return r;
-  };
+  // this thread's unit: columns c0 .., c1 .. of one head (pair: its first pair, -1: copied)
+  const int lane_t = a.lanes > 1 ? threadIdx.x / a.per_token : 0;
+  const int u = a.lanes > 1 ? threadIdx.x - lane_t * a.per_token : blockIdx.y * blockDim.x + threadIdx.x;
+  const bool any = u < a.per_token && lane_t < a.lanes;
+  const int h = u / a.units, col = u - h * a.units;
+  const int which = h < a.end[0] ? 0 : h < a.end[1] ? 1 : 2;
+  const int head = h - (which ? a.end[which - 1] : 0);
+  const bool turned = ROPE && col < pairs / EV;
+  const int pair = turned && which < 2 ? col * EV : -1;
+  const int c0 = turned && !a.interleaved ? col * EV : col * 2 * EV;
+  const int c1 = turned && !a.interleaved ? c0 + pairs : c0 + EV;
+  const Stream& x = a.x[which];
   V in[UB][2];
-  auto load = [&](int u0) {
+  {
+    const E* p = static_cast<const E*>(x.src) + head * x.s_head;
 #pragma unroll
     for (int i = 0; i < UB; ++i) {
-      const int u = u0 + i * THREADS;
-      if (u < total) {
-        const Unit r = unit(u);
-        const Stream& x = a.x[r.which];
-        const E* p = static_cast<const E*>(x.src) + (t0 + r.tok) * x.s_token + r.head * x.s_head;
-        in[i][0] = *reinterpret_cast<const V*>(p + r.c0);
-        in[i][1] = *reinterpret_cast<const V*>(p + r.c1);
+      const int k = lane_t + i * a.lanes;
+      if (any && i < a.deep && k < tokens) {
+        const E* r = p + (t0 + k) * x.s_token;
+        in[i][0] = *reinterpret_cast<const V*>(r + c0);
+        in[i][1] = *reinterpret_cast<const V*>(r + c1);
       }
     }
-  };
-  load(threadIdx.x);
+  }
 
-  // positions, places, cos and sin of this block's tokens, a warp per token
-  for (int k = threadIdx.x / 32; k < tokens; k += THREADS / 32) {
+  // positions, places, cos and sin of the block's tokens, a warp per token
+  for (int k = threadIdx.x / 32; k < tokens; k += blockDim.x / 32) {
     const int t = t0 + k;
     long long pos = 0;
     if constexpr (APPEND) {
@@ -198,61 +196,70 @@ __global__ void __launch_bounds__(THREADS) rope_kernel(const __grid_constant__ R
     if constexpr (ROPE) {
       for (int i = ptx::lane_id(); i < pairs; i += 32) {
         const float2 v = turn(pos, a.freqs[i]);
-        cs[k][i] = make_float2(v.x * a.mscale, v.y * (a.mscale * a.sign));
+        cs[k * pairs + i] = make_float2(v.x * a.mscale, v.y * (a.mscale * a.sign));
       }
     }
   }
   __syncthreads();
 
-  for (int u0 = threadIdx.x; u0 < total; u0 += UB * THREADS) {
-    if (u0 != (int)threadIdx.x) load(u0);
+  E* const out = static_cast<E*>(x.dst) + head * x.d_head;
 #pragma unroll
-    for (int i = 0; i < UB; ++i) {
-      const int u = u0 + i * THREADS;
-      if (u >= total) break;
-      const Unit r = unit(u);
-      const Stream& x = a.x[r.which];
-      E* p = static_cast<E*>(x.dst) + r.head * x.d_head;
-      if (APPEND && r.which > 0) {
-        if (place[r.tok] < 0) continue;
-        p += place[r.tok];
-      } else {
-        if (APPEND && !live[r.tok]) continue;
-        p += (t0 + r.tok) * x.d_token;
-      }
-      if (ROPE && r.pair >= 0) {
-        float f[2][EV], y[2][EV];
-        unpack<E, EV>(in[i][0], f[0]);
-        unpack<E, EV>(in[i][1], f[1]);
-        const float2* w = &cs[r.tok][r.pair];
-#pragma unroll
-        for (int j = 0; j < EV; ++j) {
-          // half: pair j is (f[0][j], f[1][j]); interleaved: columns 2 j, 2 j + 1
-          const float2 q = w[j];
-          const float u_ = a.interleaved ? f[2 * j / EV][2 * j % EV] : f[0][j];
-          const float v_ = a.interleaved ? f[(2 * j + 1) / EV][(2 * j + 1) % EV] : f[1][j];
-          // (written out, so that wide and narrow units round alike)
-          const float yu = __fmaf_rn(-v_, q.y, __fmul_rn(u_, q.x)), yv = __fmaf_rn(u_, q.y, __fmul_rn(v_, q.x));
-          if (a.interleaved) { y[2 * j / EV][2 * j % EV] = yu; y[(2 * j + 1) / EV][(2 * j + 1) % EV] = yv; }
-          else { y[0][j] = yu; y[1][j] = yv; }
-        }
-        in[i][0] = pack<E, EV>(y[0]);
-        in[i][1] = pack<E, EV>(y[1]);
-      }
-      *reinterpret_cast<V*>(p + r.c0) = in[i][0];
-      *reinterpret_cast<V*>(p + r.c1) = in[i][1];
+  for (int i = 0; i < UB; ++i) {
+    const int k = lane_t + i * a.lanes;
+    if (!any || i >= a.deep || k >= tokens) continue;
+    E* r;
+    if (APPEND && which > 0) {
+      if (place[k] < 0) continue;
+      r = out + place[k];
+    } else {
+      if (APPEND && !live[k]) continue;
+      r = out + (t0 + k) * x.d_token;
     }
+    if (ROPE && pair >= 0) {
+      float f[2][EV], y[2][EV];
+      unpack<E, EV>(in[i][0], f[0]);
+      unpack<E, EV>(in[i][1], f[1]);
+      const float2* w = &cs[k * pairs + pair];
+#pragma unroll
+      for (int j = 0; j < EV; ++j) {
+        // half: pair j is (f[0][j], f[1][j]); interleaved: columns 2 j, 2 j + 1
+        const float2 q = w[j];
+        const float u_ = a.interleaved ? f[2 * j / EV][2 * j % EV] : f[0][j];
+        const float v_ = a.interleaved ? f[(2 * j + 1) / EV][(2 * j + 1) % EV] : f[1][j];
+        // (written out, so that wide and narrow units round alike)
+        const float yu = __fmaf_rn(-v_, q.y, __fmul_rn(u_, q.x)), yv = __fmaf_rn(u_, q.y, __fmul_rn(v_, q.x));
+        if (a.interleaved) { y[2 * j / EV][2 * j % EV] = yu; y[(2 * j + 1) / EV][(2 * j + 1) % EV] = yv; }
+        else { y[0][j] = yu; y[1][j] = yv; }
+      }
+      in[i][0] = pack<E, EV>(y[0]);
+      in[i][1] = pack<E, EV>(y[1]);
+    }
+    *reinterpret_cast<V*>(r + c0) = in[i][0];
+    *reinterpret_cast<V*>(r + c1) = in[i][1];
   }
 }
 
 template <typename E, int EV, bool APPEND>
 fa_status launch(RopeArgs& a, const char* name, cudaStream_t s) {
-  // Few rows: a token per block spreads them over the SMs; many: four share the set-up.
-  a.tokens = a.T >= 4 * MAX_TOKENS * host::sm_count() ? MAX_TOKENS : 1;
-  const dim3 grid((a.T + a.tokens - 1) / a.tokens);
+  // A token's units side by side, in blocks of up to MAX_THREADS; where they are few,
+  // several tokens side by side. Each thread takes UB tokens if that leaves every SM two
+  // blocks, else one: few rows are spread over the SMs.
+  a.per_token = a.end[2] * a.units;
+  const int parts = (a.per_token + MAX_THREADS - 1) / MAX_THREADS;
+  const int pairs = a.rot / 2;
+  int most = MAX_TOKENS;
+  if (pairs && CS_BYTES / 8 / pairs < most) most = CS_BYTES / 8 / pairs;
+  a.lanes = 256 / a.per_token;
+  if (a.lanes > most / UB) a.lanes = most / UB;
+  if (a.lanes < 1) a.lanes = 1;
+  a.deep = a.T >= 2 * UB * a.lanes * host::sm_count() ? UB : 1;
+  const int threads = a.lanes > 1 ? a.lanes * a.per_token : (a.per_token + parts - 1) / parts;
+  const int span = a.lanes * a.deep;
+  const dim3 grid((a.T + span - 1) / span, parts), block((threads + 31) / 32 * 32);
+  const size_t cs = (size_t)span * pairs * sizeof(float2);
   host::KernelTimer t(name, s);
-  if (a.rot) rope_kernel<E, EV, APPEND, true><<<grid, THREADS, 0, s>>>(a);
-  else rope_kernel<E, EV, APPEND, false><<<grid, THREADS, 0, s>>>(a);
+  if (a.rot) rope_kernel<E, EV, APPEND, true><<<grid, block, cs, s>>>(a);
+  else rope_kernel<E, EV, APPEND, false><<<grid, block, cs, s>>>(a);
   return cudaGetLastError() == cudaSuccess ? FA_OK : FA_ERR_CUDA;
 }
 

@@ -275,6 +275,13 @@ __global__ void __launch_bounds__(NTHREADS, RowsCfg<E, D, MT>::CTAS_PER_SM)
           }
         }
       } else {
+        // The tensor core cuts off what it adds to a sum below the sum's last bit: the small
+        // products have sums of their own, so that the large one is cut a third as often.
+        float small[MT][2][4];
+#pragma unroll
+        for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+          for (int nt = 0; nt < 2; ++nt) small[mt][nt][0] = small[mt][nt][1] = small[mt][nt][2] = small[mt][nt][3] = 0.f;
 #pragma unroll
         for (int kp = 0; kp < D / 16; ++kp) {  // two k8 steps: four chunks of four
           uint32_t kh[2][4], kl[2][4];
@@ -295,13 +302,19 @@ __global__ void __launch_bounds__(NTHREADS, RowsCfg<E, D, MT>::CTAS_PER_SM)
               for (int z = 0; z < 4; ++z) split(v[z], qh[z], ql[z]);
 #pragma unroll
               for (int nt = 0; nt < 2; ++nt) {
-                mma_tf32(sc[mt][nt], qh, kl[nt][2 * e], kl[nt][2 * e + 1]);
-                mma_tf32(sc[mt][nt], ql, kh[nt][2 * e], kh[nt][2 * e + 1]);
+                mma_tf32(small[mt][nt], qh, kl[nt][2 * e], kl[nt][2 * e + 1]);
+                mma_tf32(small[mt][nt], ql, kh[nt][2 * e], kh[nt][2 * e + 1]);
                 mma_tf32(sc[mt][nt], qh, kh[nt][2 * e], kh[nt][2 * e + 1]);
               }
             }
           }
         }
+#pragma unroll
+        for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+          for (int nt = 0; nt < 2; ++nt)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) sc[mt][nt][e] += small[mt][nt][e];
       }
       if (j0 < in_lo || j0 + GROUP - 1 > in_hi) {
 #pragma unroll
@@ -376,29 +389,38 @@ __global__ void __launch_bounds__(NTHREADS, RowsCfg<E, D, MT>::CTAS_PER_SM)
           }
         }
       } else {
+        // the eight keys of a k step in the order that a thread's scores have them: k slots
+        // quad and quad + 4 are keys 2 quad and 2 quad + 1
+        uint32_t ph[MT][2][4], pl[MT][2][4];
 #pragma unroll
-        for (int nt = 0; nt < 2; ++nt) {
-          // the eight keys of this step in the order that a thread's scores have them:
-          // k slots quad and quad + 4 are keys 2 quad and 2 quad + 1
-          uint32_t ph[MT][4], pl[MT][4];
+        for (int mt = 0; mt < MT; ++mt)
 #pragma unroll
-          for (int mt = 0; mt < MT; ++mt)
+          for (int nt = 0; nt < 2; ++nt)
 #pragma unroll
             for (int k = 0; k < 4; ++k)
-              split(__float_as_uint(sc[mt][nt][(k & 1) * 2 + (k >> 1)]), ph[mt][k], pl[mt][k]);
+              split(__float_as_uint(sc[mt][nt][(k & 1) * 2 + (k >> 1)]), ph[mt][nt][k], pl[mt][nt][k]);
 #pragma unroll
-          for (int d = 0; d < D / 8; ++d) {
-            const int col = d * 8 + qrow, key = nt * 8 + 2 * quad;
-            uint32_t vh[2], vl[2];
+        for (int d = 0; d < D / 8; ++d) {
+          const int col = d * 8 + qrow;
+          uint32_t vh[2][2], vl[2][2];
+#pragma unroll
+          for (int nt = 0; nt < 2; ++nt)
 #pragma unroll
             for (int e = 0; e < 2; ++e)
-              split(lds32(sv + at_v32<RB>(key + e, col >> 2) + (col & 3) * 4), vh[e], vl[e]);
+              split(lds32(sv + at_v32<RB>(nt * 8 + 2 * quad + e, col >> 2) + (col & 3) * 4), vh[nt][e], vl[nt][e]);
 #pragma unroll
-            for (int mt = 0; mt < MT; ++mt) {
-              mma_tf32(o[mt][d], pl[mt], vh[0], vh[1]);
-              mma_tf32(o[mt][d], ph[mt], vl[0], vl[1]);
-              mma_tf32(o[mt][d], ph[mt], vh[0], vh[1]);
+          for (int mt = 0; mt < MT; ++mt) {
+            // a sum per group, added to O in fp32: O itself is not cut at every step
+            float add[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+            for (int nt = 0; nt < 2; ++nt) {
+              mma_tf32(add, pl[mt][nt], vh[nt][0], vh[nt][1]);
+              mma_tf32(add, ph[mt][nt], vl[nt][0], vl[nt][1]);
             }
+#pragma unroll
+            for (int nt = 0; nt < 2; ++nt) mma_tf32(add, ph[mt][nt], vh[nt][0], vh[nt][1]);
+#pragma unroll
+            for (int e = 0; e < 4; ++e) o[mt][d][e] += add[e];
           }
         }
       }
@@ -469,11 +491,11 @@ __global__ void __launch_bounds__(NTHREADS, RowsCfg<E, D, MT>::CTAS_PER_SM)
 // An item that several CTAs did parts of: the CTA in whose part it starts left the first
 // one (at most one such per CTA, its last item: slot 1, or 0 if it is its first too), the
 // following CTAs the others in their slots 0, up to the one that ends it. Blocks (c, y)
-// join the item that CTA c left open, y sharing out its rows JOIN_ROWS at a time; a block's
-// threads share out the columns and the parts, and the shares are merged in order.
-constexpr int JOIN_THREADS = 512;
-constexpr int JOIN_ROWS = 4;
-constexpr int JOIN_BLOCKS = 16;
+// join the item that CTA c left open, y sharing out its rows. A block's threads stand
+// for the columns, for rows, and, where there are many parts, for shares of the parts, which
+// are merged in order.
+constexpr int JOIN_THREADS = 256;
+constexpr int JOIN_BLOCKS = 32;
 
 struct Sum {  // sums of exponentials taken against the maximum M
   float M, L;
@@ -501,18 +523,19 @@ __global__ void __launch_bounds__(JOIN_THREADS) attend_join_kernel(const __grid_
   if (open0 != PART_STARTS && open1 != PART_STARTS) return;
   const int which = open1 == PART_STARTS;
   const Left f = a.part.left[2 * cta + which];
-  if (blockIdx.y * JOIN_ROWS >= f.rows) return;
   if (tid == 0) parts_sh = a.ctas;
   __syncthreads();
   for (int k = cta + 1 + tid; k < a.ctas; k += JOIN_THREADS)
     if (a.part.left[2 * k].flags & PART_ENDS) { atomicMin(&parts_sh, k); break; }
   __syncthreads();
   const int parts = parts_sh - cta + 1;  // slot 2 cta + which, then 2 (cta + 1), ...
-  const int cols = a.D / 4;
-  const int shares = JOIN_THREADS / (JOIN_ROWS * cols);  // 4 or 8
-  const int col = tid % cols, r = tid / cols % JOIN_ROWS, share = tid / (cols * JOIN_ROWS);
+  const int cols = a.D / 4, groups = JOIN_THREADS / cols;
+  int shares = 1;
+  while (shares < groups && shares * 4 < parts) shares *= 2;
+  const int side = groups / shares;  // rows at a time
+  const int col = tid % cols, r = tid / cols % side, share = tid / (cols * side);
   const int p0 = parts * share / shares, p1 = parts * (share + 1) / shares;
-  for (int r0 = blockIdx.y * JOIN_ROWS; r0 < f.rows; r0 += gridDim.y * JOIN_ROWS) {
+  for (int r0 = blockIdx.y * side; r0 < f.rows; r0 += gridDim.y * side) {
     Sum x = {-FLT_MAX, 0.f, make_float4(0.f, 0.f, 0.f, 0.f)};
     const bool mine = r0 + r < f.rows;
     if (mine) {
@@ -538,7 +561,7 @@ __global__ void __launch_bounds__(JOIN_THREADS) attend_join_kernel(const __grid_
     __syncthreads();
     if (share == 0 && mine) {
       for (int k = 1; k < shares; ++k) {
-        const int at = tid + k * cols * JOIN_ROWS;
+        const int at = tid + k * cols * side;
         x.add(ml[at].x, ml[at].y, acc_sh[at]);
       }
       const float inv = x.L > 0.f ? 1.f / x.L : 0.f;
@@ -562,8 +585,8 @@ template <typename E, int D, int MT>
 fa_status run(RowsArgs& a, cudaStream_t s) {
   using C = RowsCfg<E, D, MT>;
   auto* kernel = attend_rows_kernel<E, D, MT>;
-  if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM) != cudaSuccess)
-    return FA_ERR_CUDA;
+  static std::atomic<uint64_t> done{0};
+  if (!allow_smem(kernel, C::SMEM, done)) return FA_ERR_CUDA;
   const int ctas = host::sm_count() * C::CTAS_PER_SM;
   void* w = nullptr;
   if (host::scratch_alloc(&w, partials_bytes(ctas, C::R, D), s) != cudaSuccess) return FA_ERR_CUDA;
@@ -588,8 +611,7 @@ fa_status run(RowsArgs& a, cudaStream_t s) {
 
 fa_status launch_join(const JoinArgs& a, cudaStream_t s) {
   host::KernelTimer t("attend_join", s);
-  return launch_programmatic(attend_join_kernel, dim3(a.ctas, std::min((a.R + JOIN_ROWS - 1) / JOIN_ROWS, JOIN_BLOCKS)),
-                             dim3(JOIN_THREADS), s, a) == cudaSuccess ? FA_OK : FA_ERR_CUDA;
+  return launch_programmatic(attend_join_kernel, dim3(a.ctas, std::min((a.R + 3) / 4, JOIN_BLOCKS)), dim3(JOIN_THREADS), s, a) == cudaSuccess ? FA_OK : FA_ERR_CUDA;
 }
 
 fa_status launch_attend_rows(const void* q, void* O, float* LSE, const int* cu, const int* slots,

@@ -579,8 +579,8 @@ template <int D>
 fa_status run(TilesArgs& a, const CUtensorMap& q, const CUtensorMap& k, const CUtensorMap& v, cudaStream_t s) {
   using C = TilesCfg<D>;
   auto* kernel = attend_tiles_kernel<D>;
-  if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM) != cudaSuccess)
-    return FA_ERR_CUDA;
+  static std::atomic<uint64_t> done{0};
+  if (!allow_smem(kernel, C::SMEM, done)) return FA_ERR_CUDA;
   const int ctas = host::sm_count();
   void* w = nullptr;
   if (host::scratch_alloc(&w, partials_bytes(ctas, a.g.R, D), s) != cudaSuccess) return FA_ERR_CUDA;

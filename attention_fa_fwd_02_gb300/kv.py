@@ -19,7 +19,7 @@ A training step rotates with ``rope.apply`` and its gradient with ``rope.backwar
 from __future__ import annotations
 
 import ctypes
-import math
+import struct
 
 import torch
 
@@ -72,6 +72,15 @@ class fakv_tokens(ctypes.Structure):
                 + [("scale", ctypes.c_float), ("causal", _i), ("window", _i), ("out_dtype", _i)])
 
 
+# A call of a few microseconds is not to spend as many on asking for its device and stream.
+_current_device = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or \
+    (lambda index: torch.cuda.current_stream(index).cuda_stream)
+
+# fakv_tokens and fakv_rope_params packed in one step (the C side takes a pointer to the bytes)
+_pack_tokens = struct.Struct("@4i6qf3i").pack
+_pack_rope = struct.Struct("@7i4x8q").pack
+
 _bound = None
 
 
@@ -83,9 +92,9 @@ def _lib():
         P = ctypes.POINTER
         for name, args in (
                 ("fakv_rope_freqs", [_i, ctypes.c_double, P(fakv_scaling), _vp, P(ctypes.c_float)]),
-                ("fakv_rope_apply", [_vp, _vp, _vp, _vp, _vp, P(fakv_rope), P(fakv_rope_params), _vp]),
-                ("fakv_append", [_vp] * 6 + [P(fakv_rope), P(fakv_cache), P(fakv_tokens), _vp]),
-                ("fakv_attend", [_vp] * 5 + [P(fakv_cache), P(fakv_tokens), _vp]),
+                ("fakv_rope_apply", [_vp, _vp, _vp, _vp, _vp, P(fakv_rope), _vp, _vp]),
+                ("fakv_append", [_vp] * 6 + [P(fakv_rope), P(fakv_cache), _vp, _vp]),
+                ("fakv_attend", [_vp] * 5 + [P(fakv_cache), _vp, _vp]),
                 ("fakv_grow", [P(fakv_cache), _vp, _vp, _i, _vp]),
                 ("fakv_fork", [P(fakv_cache), _vp, _vp, _i, _vp]),
                 ("fakv_free", [P(fakv_cache), _vp, _vp, _i, _vp]),
@@ -103,24 +112,30 @@ def _check(rc: int, where: str) -> None:
 
 
 class _on:
-    """The device of a call's tensors made current, and its stream: ``stream``, or that device's current one. What
-    the call allocates is marked as used on the stream it runs on."""
+    """The device of a call's tensors made current for as long as the call, and the handle of its stream: ``stream``,
+    or that device's current one."""
 
-    def __init__(self, device, stream):
-        self.device, self.back, self.stream = device.index, -1, stream
-        if torch.cuda.current_device() != self.device:
-            self.back = torch.cuda.current_device()
-            torch.cuda.set_device(self.device)
-        if stream is not None and stream.device_index != self.device:
-            self.leave()
-            raise ValueError("the stream belongs to another device than the tensors")
-        self.handle = (torch.cuda.current_stream() if stream is None else stream).cuda_stream
+    __slots__ = ("back", "stream", "handle")
 
-    def empty(self, shape, dtype):
+    def __init__(self, index, stream):
+        self.back, self.stream = -1, stream
+        current = _current_device()
+        if stream is not None:
+            if stream.device_index != index:
+                raise ValueError("the stream belongs to another device than the tensors")
+            self.handle = stream.cuda_stream
+        else:
+            self.handle = _raw_stream(index)
+        if current != index:
+            self.back = current
+            torch.cuda.set_device(index)
+
+    def empty(self, like, shape, dtype):
+        """An output, allocated in the order of the stream that the call runs on."""
         if self.stream is None:
-            return torch.empty(shape, dtype=dtype, device="cuda")
-        with torch.cuda.stream(self.stream):  # (the allocator then reuses it in this stream's order)
-            t = torch.empty(shape, dtype=dtype, device="cuda")
+            return torch.empty(shape, dtype=dtype, device=like.device)
+        with torch.cuda.stream(self.stream):
+            t = torch.empty(shape, dtype=dtype, device=like.device)
         t.record_stream(torch.cuda.current_stream())
         return t
 
@@ -131,28 +146,31 @@ class _on:
 
 
 def _rows(t, name, dtype, device, heads=None, dim=None, T=None):
-    """A [T, heads, D] tensor whose columns run without gaps."""
-    if t.dim() != 3 or t.dtype != dtype or t.device != device:
+    """Shape and strides of a [T, heads, D] tensor whose columns run without gaps."""
+    shape, stride = t.shape, t.stride()
+    if len(shape) != 3 or t.dtype != dtype or t.device != device:
         raise ValueError(f"{name} must be [T, heads, D], {dtype}, on {device}")
-    T_, h, d = t.shape
-    if (heads is not None and h != heads) or (dim is not None and d != dim) or (T is not None and T_ != T):
-        raise ValueError(f"{name} has shape {tuple(t.shape)}: [{T}, {heads}, {dim}] is wanted")
-    if t.stride(2) != 1 and t.numel():
+    if (heads is not None and shape[1] != heads) or (dim is not None and shape[2] != dim) \
+            or (T is not None and shape[0] != T):
+        raise ValueError(f"{name} has shape {tuple(shape)}: [{T}, {heads}, {dim}] is wanted")
+    if stride[2] != 1 and t.numel():
         raise ValueError(f"the columns of {name} must be contiguous")
-    return t
+    return shape, stride
 
 
 def _out(t, name, shape, dtype, device):
-    if tuple(t.shape) != tuple(shape) or t.dtype != dtype or t.device != device or not t.is_contiguous():
+    if t.shape != shape or t.dtype != dtype or t.device != device or not t.is_contiguous():
         raise ValueError(f"{name} must be contiguous, {tuple(shape)}, {dtype}, on {device}")
     return t
 
 
 def _ints(t, name, n, device):
-    if t.dtype != torch.int32 or t.dim() != 1 or t.device != device or not t.is_contiguous() \
-            or (n is not None and t.shape[0] != n):
+    """Length of a contiguous int32 vector."""
+    shape = t.shape
+    if t.dtype != torch.int32 or len(shape) != 1 or t.device != device or not t.is_contiguous() \
+            or (n is not None and shape[0] != n):
         raise ValueError(f"{name} must be a contiguous int32 vector{'' if n is None else f' of {n}'} on {device}")
-    return t
+    return shape[0]
 
 
 class Rope:
@@ -191,36 +209,37 @@ class Rope:
     def apply(self, q, k, positions, inverse=False, out=None, stream=None):
         """q [T, H, D] and k [T, HKV, D] (or None) rotated by ``positions`` [T] (int32 or int64). ``out``: a pair of
         tensors to write, which may be (q, k) themselves. Returns (q, k) rotated."""
-        dev = q.device
-        _rows(q, "q", q.dtype, dev, None, self.head_dim)
-        if q.dtype not in _DT:
-            raise TypeError(f"unsupported dtype {q.dtype}")
+        dev, dt = q.device, q.dtype
+        (T, H, _), sq = _rows(q, "q", dt, dev, None, self.head_dim)
+        if dt not in _DT:
+            raise TypeError(f"unsupported dtype {dt}")
         if not q.is_cuda or self.freqs.device != dev:
             raise ValueError(f"q must be on {self.freqs.device}, the device of the frequencies")
-        T, H = q.shape[0], q.shape[1]
+        hk, sk, so, sko, kp, kop = 0, (0, 0), None, (0, 0), None, None
         if k is not None:
-            _rows(k, "k", q.dtype, dev, None, self.head_dim, T)
-        if positions.dtype not in (torch.int32, torch.int64) or positions.shape != (T,) or positions.device != dev \
+            (_, hk, _), sk = _rows(k, "k", dt, dev, None, self.head_dim, T)
+            kp = k.data_ptr()
+        wide = positions.dtype == torch.int64
+        if not (wide or positions.dtype == torch.int32) or positions.shape != (T,) or positions.device != dev \
                 or not positions.is_contiguous():
             raise ValueError(f"positions must be a contiguous int32 or int64 vector of {T} on {dev}")
-        on = _on(dev, stream)
+        on = _on(dev.index, stream)
         try:
             if out is None:
-                qo = on.empty(q.shape, q.dtype)
-                ko = None if k is None else on.empty(k.shape, q.dtype)
+                qo, ko = on.empty(q, q.shape, dt), None if k is None else on.empty(q, k.shape, dt)
             else:
-                qo = _rows(out[0], "out[0]", q.dtype, dev, H, self.head_dim, T)
-                ko = None if k is None else _rows(out[1], "out[1]", q.dtype, dev, k.shape[1], self.head_dim, T)
-            x = fakv_rope_params(T, H, 0 if k is None else k.shape[1], self.head_dim, _DT[q.dtype],
-                                 int(positions.dtype == torch.int64), int(bool(inverse)), *q.stride()[:2],
-                                 *(k.stride()[:2] if k is not None else (0, 0)), *qo.stride()[:2],
-                                 *(ko.stride()[:2] if k is not None else (0, 0)))
-            _check(_lib().fakv_rope_apply(q.data_ptr(), None if k is None else k.data_ptr(), qo.data_ptr(),
-                                          None if k is None else ko.data_ptr(), positions.data_ptr(), self._ref,
-                                          ctypes.byref(x), on.handle), "fakv_rope_apply")
+                qo, ko = out
+            _, so = _rows(qo, "out[0]", dt, dev, H, self.head_dim, T)
+            if k is not None:
+                _, sko = _rows(ko, "out[1]", dt, dev, hk, self.head_dim, T)
+                kop = ko.data_ptr()
+            _check(_lib().fakv_rope_apply(
+                q.data_ptr(), kp, qo.data_ptr(), kop, positions.data_ptr(), self._ref,
+                _pack_rope(T, H, hk, self.head_dim, _DT[dt], wide, bool(inverse), sq[0], sq[1], sk[0], sk[1], so[0],
+                           so[1], sko[0], sko[1]), on.handle), "fakv_rope_apply")
         finally:
             on.leave()
-        return qo, ko
+        return qo, None if k is None else ko
 
     def backward(self, dq, dk, positions, out=None, stream=None):
         """Gradients of ``apply``'s inputs from those of its outputs: the inverse rotation (times mscale)."""
@@ -255,6 +274,7 @@ class PagedCache:
             else _ints(status, "status", 1, dev)
         self.k, self.v, self.table, self.lens, self.refs, self.device = k, v, table, lens, refs, dev
         self.planes, self.page_size, self.kv_heads, self.head_dim = k.shape[0], k.shape[t], k.shape[h], k.shape[4]
+        self.slots, self.dtype, self._index = table.shape[0], k.dtype, dev.index
         self._c = fakv_cache(k.data_ptr(), v.data_ptr(), table.data_ptr(), lens.data_ptr(), refs.data_ptr(),
                              self.status.data_ptr(), k.stride(0), k.stride(1), k.stride(t), k.stride(h),
                              table.stride(0), k.shape[0], k.shape[1], k.shape[t], k.shape[h], k.shape[4],
@@ -271,102 +291,101 @@ class PagedCache:
                    torch.zeros(slots, dtype=torch.int32, device=device),
                    torch.zeros(pages, dtype=torch.int32, device=device), layout)
 
-    def _tokens(self, q, cu, slots, layer):
-        dev, T = self.device, q.shape[0]
-        _rows(q, "q", self.k.dtype, dev, None, self.head_dim)
-        _ints(cu, "cu", None, dev)
-        B = cu.shape[0] - 1
+    def _batch(self, cu, slots, layer):
+        """Sequences of a call and the address of its slots."""
+        B = _ints(cu, "cu", None, self.device) - 1
         if B < 0:
             raise ValueError("cu must have an entry more than there are sequences")
-        if slots is None:
-            if B > self.lens.shape[0]:
-                raise ValueError("more sequences than slots")
-        else:
-            _ints(slots, "slots", B, dev)
         if not 0 <= layer < self.planes:
             raise ValueError(f"layer must be in 0 .. {self.planes - 1}")
-        return T, B, q.shape[1]
+        if slots is None:
+            if B > self.slots:
+                raise ValueError("more sequences than slots")
+            return B, None
+        _ints(slots, "slots", B, self.device)
+        return B, slots.data_ptr()
 
     def append(self, q, k, v, cu, slots=None, rope=None, layer=0, out=None, stream=None):
         """Writes the new tokens' k and v [T, HKV, D] into the cache, k rotated by ``rope`` (None: as it is), and
         returns q [T, H, D] rotated likewise (into ``out``, contiguous, where given; q may be None). The slots'
         lengths already count the new tokens (``grow``). Rows of q past cu[-1] are not written. A slot named twice in
         one call would have two tokens for one place: which of them it keeps is not defined."""
-        T, B, H = self._tokens(k if q is None else q, cu, slots, layer)
-        dev, dt = self.device, self.k.dtype
-        _rows(k, "k", dt, dev, self.kv_heads, self.head_dim, T)
-        _rows(v, "v", dt, dev, self.kv_heads, self.head_dim, T)
-        if rope is not None and (rope.head_dim != self.head_dim or rope.freqs.device != dev):
+        dev, dt, D = self.device, self.dtype, self.head_dim
+        (T, _, _), sk = _rows(k, "k", dt, dev, self.kv_heads, D)
+        _, sv = _rows(v, "v", dt, dev, self.kv_heads, D, T)
+        B, sp = self._batch(cu, slots, layer)
+        H, sq, qp, op, o = 0, (0, 0), None, None, None
+        if q is not None:
+            (_, H, _), sq = _rows(q, "q", dt, dev, None, D, T)
+            qp = q.data_ptr()
+        if rope is not None and (rope.head_dim != D or rope.freqs.device != dev):
             raise ValueError("rope is for another head_dim or device")
-        on = _on(dev, stream)
+        on = _on(self._index, stream)
         try:
             if q is not None:
-                o = on.empty(q.shape, dt) if out is None else _out(out, "out", q.shape, dt, dev)
-            x = fakv_tokens(B, T, 0 if q is None else H, layer, *(q.stride()[:2] if q is not None else (0, 0)),
-                            *k.stride()[:2], *v.stride()[:2], 1.0, 1, 0, _DT[dt])
-            _check(_lib().fakv_append(None if q is None else q.data_ptr(), k.data_ptr(), v.data_ptr(),
-                                      None if q is None else o.data_ptr(), cu.data_ptr(),
-                                      None if slots is None else slots.data_ptr(),
-                                      None if rope is None else rope._ref, self._ref, ctypes.byref(x), on.handle),
-                   "fakv_append")
+                o = on.empty(q, q.shape, dt) if out is None else _out(out, "out", q.shape, dt, dev)
+                op = o.data_ptr()
+            _check(_lib().fakv_append(
+                qp, k.data_ptr(), v.data_ptr(), op, cu.data_ptr(), sp, None if rope is None else rope._ref, self._ref,
+                _pack_tokens(B, T, H, layer, sq[0], sq[1], sk[0], sk[1], sv[0], sv[1], 1.0, 1, 0, 0), on.handle),
+                "fakv_append")
         finally:
             on.leave()
-        return None if q is None else o
+        return o
 
     def attend(self, q, cu, slots=None, scale=None, causal=True, window=0, layer=0, out_dtype=None, out=None,
                lse=None, stream=None):
         """O [T, H, D] and LSE [T, H] of the new tokens' queries over their sequences' tokens: key j is visible to
         position p iff j <= p (``causal``) and j > p - window (window 0: all). Rows past cu[-1] are not written."""
-        T, B, H = self._tokens(q, cu, slots, layer)
-        dev = self.device
-        if out is not None and out_dtype is None:
-            out_dtype = out.dtype
-        odt = self.k.dtype if out_dtype is None else out_dtype
+        dev, dt, D = self.device, self.dtype, self.head_dim
+        shape, sq = _rows(q, "q", dt, dev, None, D)
+        B, sp = self._batch(cu, slots, layer)
+        odt = out_dtype if out_dtype is not None else dt if out is None else out.dtype
         if odt not in _DT:
             raise TypeError(f"unsupported output dtype {odt}")
-        on = _on(dev, stream)
+        on = _on(self._index, stream)
         try:
-            o = on.empty(q.shape, odt) if out is None else _out(out, "out", q.shape, odt, dev)
-            lse = on.empty(q.shape[:2], torch.float32) if lse is None \
-                else _out(lse, "lse", q.shape[:2], torch.float32, dev)
-            st = q.stride()
-            x = fakv_tokens(B, T, H, layer, st[0], st[1], 0, 0, 0, 0,
-                            1.0 / math.sqrt(self.head_dim) if scale is None else scale, 1 if causal else 0, window,
-                            _DT[odt])
-            _check(_lib().fakv_attend(q.data_ptr(), o.data_ptr(), lse.data_ptr(), cu.data_ptr(),
-                                      None if slots is None else slots.data_ptr(), self._ref, ctypes.byref(x),
-                                      on.handle), "fakv_attend")
+            out = on.empty(q, shape, odt) if out is None else _out(out, "out", shape, odt, dev)
+            lse = on.empty(q, shape[:2], torch.float32) if lse is None \
+                else _out(lse, "lse", shape[:2], torch.float32, dev)
+            _check(_lib().fakv_attend(
+                q.data_ptr(), out.data_ptr(), lse.data_ptr(), cu.data_ptr(), sp, self._ref,
+                _pack_tokens(B, shape[0], shape[1], layer, sq[0], sq[1], 0, 0, 0, 0,
+                             D ** -0.5 if scale is None else scale, bool(causal), window, _DT[odt]), on.handle),
+                "fakv_attend")
         finally:
             on.leave()
-        return o, lse
+        return out, lse
 
-    def _list(self, f, name, a, b, stream):
-        _ints(a, "slots", None, self.device)
+    def _list(self, call, where, a, names, b, stream):
+        n = _ints(a, names[0], None, self.device)
+        bp = None
         if b is not None:
-            _ints(b, name, a.shape[0], self.device)
-        on = _on(self.device, stream)
+            _ints(b, names[1], n, self.device)
+            bp = b.data_ptr()
+        on = _on(self._index, stream)
         try:
-            _check(f(self._ref, a.data_ptr(), None if b is None else b.data_ptr(), a.shape[0], on.handle), f.__name__)
+            _check(call(self._ref, a.data_ptr(), bp, n, on.handle), where)
         finally:
             on.leave()
 
     def grow(self, slots, add, stream=None):
         """Room for add[i] more tokens in slots[i] (the lengths grow by it): new pages, and a copy of a shared last
         page that has room."""
-        self._list(_lib().fakv_grow, "add", slots, add, stream)
+        self._list(_lib().fakv_grow, "fakv_grow", slots, ("slots", "add"), add, stream)
 
     def fork(self, src, dst, stream=None):
         """Slots dst[i] become copies of slots src[i] that share their pages; sources are read as they were before
         the call."""
-        self._list(_lib().fakv_fork, "dst", src, dst, stream)
+        self._list(_lib().fakv_fork, "fakv_fork", src, ("src", "dst"), dst, stream)
 
     def free(self, slots, keep=None, stream=None):
         """Slots cut to their first keep[i] tokens (None: emptied); pages that no slot holds any more are free."""
-        self._list(_lib().fakv_free, "keep", slots, keep, stream)
+        self._list(_lib().fakv_free, "fakv_free", slots, ("slots", "keep"), keep, stream)
 
     def compact(self, stream=None):
         """Moves pages so that those in use are the lowest-numbered ones, and renumbers the table."""
-        on = _on(self.device, stream)
+        on = _on(self._index, stream)
         try:
             _check(_lib().fakv_compact(self._ref, on.handle), "fakv_compact")
         finally:

@@ -47,6 +47,16 @@ def test_struct_layouts_match_the_header(kv, name, tmp_path):
     assert got == [ctypes.sizeof(t)] + [getattr(t, n).offset for n in names]
 
 
+def test_packed_parameters_are_the_structs(kv):
+    for pack, t, values in (
+            (kv._pack_tokens, kv.fakv_tokens, (1, 2, 3, 4, 5, 6, 7, 8, 9, 1 << 40, 0.5, 1, 12, 1)),
+            (kv._pack_rope, kv.fakv_rope_params, (1, 2, 3, 4, 1, True, False, 8, 9, 10, 11, 12, 13, 14, 1 << 40))):
+        b = pack(*values)
+        assert len(b) == ctypes.sizeof(t)
+        x = t.from_buffer_copy(b)
+        assert [getattr(x, n) for n, _ in t._fields_] == [v for v in values]
+
+
 def cache(kv, **kw):
     d = dict(K=A, V=A, table=A, lens=A, refs=A, status=0, plane_stride=0, page_stride=16 * 2 * 64, token_stride=128,
              head_stride=64, table_stride=10, planes=1, num_pages=100, page_size=16, HKV=2, D=64, max_slots=4,
