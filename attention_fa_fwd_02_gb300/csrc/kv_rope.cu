@@ -133,7 +133,7 @@ __device__ __forceinline__ int find_seq(const int* cu, int B, int t) {
 }
 
 template <typename E, int EV, bool APPEND, bool ROPE>
-__global__ void __launch_bounds__(MAX_THREADS) rope_kernel(const __grid_constant__ RopeArgs a) {
+__global__ void __launch_bounds__(MAX_THREADS, 2) rope_kernel(const __grid_constant__ RopeArgs a) {
   using V = typename Chunk<E, EV>::V;
   extern __shared__ float2 cs[];           // [tokens][pairs]
   __shared__ long long place[MAX_TOKENS];  // append: offset in the cache; -1: not written
@@ -196,7 +196,8 @@ __global__ void __launch_bounds__(MAX_THREADS) rope_kernel(const __grid_constant
     if constexpr (ROPE) {
       for (int i = ptx::lane_id(); i < pairs; i += 32) {
         const float2 v = turn(pos, a.freqs[i]);
-        cs[k * pairs + i] = make_float2(v.x * a.mscale, v.y * (a.mscale * a.sign));
+        // (pair i = c EV + j at j (pairs / EV) + c: neighbouring units read neighbouring words)
+        cs[k * pairs + (i % EV) * (pairs / EV) + i / EV] = make_float2(v.x * a.mscale, v.y * (a.mscale * a.sign));
       }
     }
   }
@@ -219,11 +220,11 @@ __global__ void __launch_bounds__(MAX_THREADS) rope_kernel(const __grid_constant
       float f[2][EV], y[2][EV];
       unpack<E, EV>(in[i][0], f[0]);
       unpack<E, EV>(in[i][1], f[1]);
-      const float2* w = &cs[k * pairs + pair];
+      const float2* w = &cs[k * pairs + pair / EV];
 #pragma unroll
       for (int j = 0; j < EV; ++j) {
         // half: pair j is (f[0][j], f[1][j]); interleaved: columns 2 j, 2 j + 1
-        const float2 q = w[j];
+        const float2 q = w[j * (pairs / EV)];
         const float u_ = a.interleaved ? f[2 * j / EV][2 * j % EV] : f[0][j];
         const float v_ = a.interleaved ? f[(2 * j + 1) / EV][(2 * j + 1) % EV] : f[1][j];
         // (written out, so that wide and narrow units round alike)
