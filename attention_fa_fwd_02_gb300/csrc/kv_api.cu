@@ -200,7 +200,7 @@ FA_API fa_status fakv_attend(const void* q, void* O, float* LSE, const int* cu, 
   if (t.window >= cache->max_pages * cache->page_size) t.window = 0;  // hides nothing
   // Many rows per sequence and kv head (on average: the lengths are on the device): tensor-core
   // tiles, if the copy engine can take the tensors' strides.
-  if (cache->dtype == FA_BF16 && (long long)t.T * (t.H / cache->HKV) > 32ll * t.B) {
+  if (cache->dtype == FA_BF16 && (long long)t.T * (t.H / cache->HKV) > 16ll * t.B) {
     st = launch_attend_tiles(q, O, LSE, cu, slots, *cache, t, reinterpret_cast<cudaStream_t>(stream));
     if (st != FA_ERR_UNSUPPORTED) return st;
   }

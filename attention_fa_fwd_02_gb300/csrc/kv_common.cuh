@@ -32,20 +32,17 @@ struct Seq {
 
 __device__ __forceinline__ Seq load_seq(const fakv_cache& c, const int* cu, const int* slots, int b,
                                         int T) {
-  Seq s;
   const int r0 = cu[b], r1 = cu[b + 1];
   const int slot = slots ? slots[b] : b;
+  const bool ok = slot >= 0 && slot < c.max_slots;
+  const int len = c.lens[ok ? slot : 0];  // (asked for before anything waits)
+  const bool len_ok = len >= 0 && (long long)len <= (long long)c.max_pages * c.page_size;
+  Seq s;
   s.row0 = max(0, min(r0, T));
   s.n = max(0, min(r1, T) - s.row0);
-  s.slot = (slot >= 0 && slot < c.max_slots) ? slot : -1;
-  s.len = 0;
-  if (s.slot >= 0) {
-    const int len = c.lens[slot];
-    if (len >= 0 && (long long)len <= (long long)c.max_pages * c.page_size) s.len = len;
-    else if (s.n > 0) raise(c.status, FAKV_BAD_LENGTH);
-  } else if (s.n > 0) {
-    raise(c.status, FAKV_BAD_SLOT);
-  }
+  s.slot = ok ? slot : -1;
+  s.len = ok && len_ok ? len : 0;
+  if (s.n > 0 && !(ok && len_ok)) raise(c.status, ok ? FAKV_BAD_LENGTH : FAKV_BAD_SLOT);
   return s;
 }
 

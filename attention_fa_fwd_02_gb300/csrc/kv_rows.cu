@@ -2,22 +2,27 @@
 // for fp32 caches: K and V streamed once, mma.sync.
 //
 // Few rows read many keys: 4 D flops per row against 4 D bytes (bf16) per key, so up to a
-// few dozen rows the work is bound by HBM. A CTA (4 warps) walks its part of the work line
-// (kv_sched.cuh) in units of 64 keys, 16 per warp: a warp has its own ring of 16-key
-// stages, filled with cp.async (any page size and stride, no copy descriptor to build on
-// the host), its own running maximum, sum and O, and meets the others only at the end of an
-// item: the loop has no CTA barrier. A 16-row tile of mma.sync holds the rows (two
-// for up to 32): even with 4 rows in it, the tensor work per 16 keys is a third of the time
-// their bytes take, whereas tcgen05's 128-row tile would mean a TMEM round trip per tile
-// for the same bytes.
+// few dozen rows the work is bound by HBM. A warp is a worker (kv_sched.cuh): it walks its
+// part of the line on its own, in groups of keys (4 KB of K, 4 KB of V) that it copies with
+// cp.async (any page size and stride, no copy descriptor to build on the host) into a ring
+// of its own; K and V slots are refilled as soon as each is read. Where one warp changes
+// items, the SM's seven others keep the memory busy, and the loop has no CTA barrier. (With
+// a CTA per item, 64 sequences of 512 tokens on average took 45 us, 20 being the floor: every
+// item drained and refilled the CTA's whole pipeline.) Only where all warps of a CTA end up
+// with one and the same item do they put their results together in shared memory, so that a
+// long sequence leaves a part per CTA to join. A 16-row tile of mma.sync holds the rows
+// (two for up to 32): even with 4 rows in it, the tensor work of a group is a third of the time
+// its bytes take, whereas tcgen05's 128-row tile would mean a TMEM round trip per tile for
+// the same bytes.
 //
-//   scores  S = Q K^T: bf16 m16n8k16, fp32 sums. fp32 caches: x = hi + lo with tf32 terms,
-//           hi hi + hi lo + lo hi (m16n8k8).
-//   softmax online in the exp2 domain; m moves only when it would grow by more than 8
-//           (the sums stay exact: every exponential of an item is taken against the same m
-//           as its O).
-//   O += P V  bf16: P = hi + lo, two bf16 terms, so that P's rounding (2^-9) does not add
-//           to the output's: the second product is free under the memory time.
+//   scores  S^T = K Q^T: the 16 rows of an mma tile are keys, its 8 columns rows of q, so
+//           that eight rows (a decoding step) cost eight rows. bf16 m16n8k16, fp32 sums.
+//           fp32 caches: x = hi + lo with tf32 terms, hi hi + hi lo + lo hi (m16n8k8).
+//   softmax online in the exp2 domain; m moves only when a score would exceed it by more than
+//           8 (the sums stay exact: every exponential of an item is taken against the
+//           same m as its O), so a step asks with one vote and reduces nothing.
+//   O^T += V^T P^T  bf16: P = hi + lo, two bf16 terms, so that P's rounding (2^-8) does not
+//           add to the output's: the second product is free under the memory time.
 #include <algorithm>
 #include <cfloat>
 #include <cmath>
@@ -29,8 +34,6 @@ namespace {
 
 constexpr int WARPS = 4;
 constexpr int NTHREADS = 32 * WARPS;
-constexpr int GROUP = 16;             // keys per warp step
-constexpr int UNIT = GROUP * WARPS;   // keys per unit
 
 struct RowsArgs {
   fakv_cache c;
@@ -47,20 +50,30 @@ struct RowsArgs {
   Partials part;
 };
 
-template <typename E, int D, int MT>
+template <typename E, int D, int NTR>
 struct RowsCfg {
   static constexpr bool F32 = sizeof(E) == 4;
-  static constexpr int R = 16 * MT;
+  static constexpr int R = 8 * NTR;               // rows of an item
   static constexpr int RB = D * (int)sizeof(E);   // bytes of a K / V / Q row
   static constexpr int CH = RB / 16;              // 16-byte chunks of it
-  static constexpr int STAGE = 2 * GROUP * RB;    // K and V of a group
-  static constexpr int WARP_BYTES = 24576 * (F32 && D == 128 ? 2 : 1);
-  static constexpr int S = WARP_BYTES / STAGE;    // stages of a warp's ring
-  static constexpr int OS = D + 8;                // floats of a merged O row (bank spread)
+  static constexpr int GROUP = 4096 / RB > 16 ? 4096 / RB : 16;  // keys of a group
+  static constexpr int KT = GROUP / 16;           // 16-key tiles of it
+  static constexpr int SLOT = GROUP * RB;         // K (or V) of a group
   static constexpr int Q_BYTES = R * RB;
-  static constexpr int SMEM = WARPS * WARP_BYTES + Q_BYTES;
-  static constexpr int CTAS_PER_SM = SMEM > 110 * 1024 ? 1 : 2;
-  static_assert(S >= 3 && R * OS * 4 <= WARP_BYTES, "a warp's ring also holds its O for the merge");
+  // Bytes on their way per SM: 12 warps x 4 slots, or 8 x 6, of 4 KB hold 192 KB, a latency of
+  // 2 us or more at the SM's share of HBM; three CTAs where the registers allow them,
+  // because more warps hide a change of items better.
+  static constexpr int WANT = NTR == 1 && RB < 512 ? 3 : 2;
+  static constexpr int ROOM = WANT == 3 ? 18432 : 28672;
+  static constexpr bool FITS = ROOM - Q_BYTES >= 2 * SLOT;
+  static constexpr int CTAS_PER_SM = FITS ? WANT : 1;
+  static constexpr int NS = ((FITS ? ROOM : 56320) - Q_BYTES) / SLOT;
+  static constexpr int WARP_BYTES = NS * SLOT + Q_BYTES;
+  static constexpr int SMEM = WARPS * WARP_BYTES;
+  static constexpr int OS = D + 4;                // floats of a row of O in shared memory (bank spread)
+  static constexpr bool Q_REGS = !F32 && NTR == 1;
+  static_assert(NS >= 2 && WARP_BYTES >= R * OS * 4, "a warp's ring also holds its O at the end");
+  static_assert(SMEM >= 4 * 16385, "the plan's scratch");
 };
 
 __device__ __forceinline__ void cp16(uint32_t dst, const void* src, bool take) {
@@ -116,386 +129,469 @@ __device__ __forceinline__ uint32_t at_rows(int row, int chunk) {
 }
 template <int RB>
 __device__ __forceinline__ uint32_t at_v32(int row, int chunk) {
-  return (uint32_t)(row * RB + ((chunk ^ (((row >> 1) & 3) << 1)) << 4));
+  return (uint32_t)(row * RB + ((chunk ^ ((row & 3) << 1)) << 4));
 }
 
-template <typename E, int D, int MT>
-__global__ void __launch_bounds__(NTHREADS, RowsCfg<E, D, MT>::CTAS_PER_SM)
+__device__ __forceinline__ uint32_t transpose8(uint32_t x) {  // of an 8 x 8 matrix of 16-bit values
+  uint32_t y;
+  asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
+  return y;
+}
+
+// An item's (or its part's) result from the sums of warps w0 .. w1 of the CTA, each in its own
+// shared memory: O [R][OS] not normalised, m and l in ml. By `threads` threads of which the
+// caller is number i. flags: PART_STARTS, PART_ENDS (both: the whole item), PART_JOINED.
+struct Finish {
+  int row0, rho0, rows, head, ender, flags, slot;
+};
+template <typename C, int D>
+__device__ __forceinline__ void finish(const RowsArgs& a, const Finish& f, const uint8_t* smem,
+                                    const float2 (*ml)[C::R], int w0, int w1, int i, int threads) {
+  const bool whole = (f.flags & PART_STARTS) && (f.flags & PART_ENDS);
+  constexpr int COLS = D / 4;  // threads of a row
+  const int col = i % COLS * 4;
+  for (int r = i / COLS; r < f.rows; r += threads / COLS) {
+    float M = ml[w0][r].x, L = ml[w0][r].y;
+    float4 acc = *reinterpret_cast<const float4*>(
+        reinterpret_cast<const float*>(smem + w0 * C::WARP_BYTES) + r * C::OS + col);
+#pragma unroll 1
+    for (int w = w0 + 1; w <= w1; ++w) {
+      const float2 x = ml[w][r];
+      const float4 v = *reinterpret_cast<const float4*>(
+          reinterpret_cast<const float*>(smem + w * C::WARP_BYTES) + r * C::OS + col);
+      const float mn = fmaxf(M, x.x), fo = ptx::ex2(M - mn), fn = ptx::ex2(x.x - mn);
+      M = mn;
+      L = L * fo + x.y * fn;
+      acc.x = acc.x * fo + v.x * fn;
+      acc.y = acc.y * fo + v.y * fn;
+      acc.z = acc.z * fo + v.z * fn;
+      acc.w = acc.w * fo + v.w * fn;
+    }
+    if (whole) {
+      const float inv = L > 0.f ? __fdividef(1.f, L) : 0.f;
+      const int rho = f.rho0 + r, token = a.g.rep.of(rho);
+      const size_t at = (size_t)(f.row0 + token) * a.H + f.head * a.g.rep.d + rho - token * a.g.rep.d;
+      if (col == 0) a.LSE[at] = L > 0.f ? (M + __log2f(L)) * LN2 : -INFINITY;
+      if (col < a.c.D) {
+        if (a.out_bf16)
+          *reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(a.O) + at * a.c.D + col) =
+              make_uint2(bf2(acc.x * inv, acc.y * inv), bf2(acc.z * inv, acc.w * inv));
+        else
+          *reinterpret_cast<float4*>(static_cast<float*>(a.O) + at * a.c.D + col) =
+              make_float4(acc.x * inv, acc.y * inv, acc.z * inv, acc.w * inv);
+      }
+    } else {
+      *reinterpret_cast<float4*>(a.part.O + ((size_t)f.slot * C::R + r) * D + col) = acc;
+      if (col == 0) a.part.ml[(size_t)f.slot * C::R + r] = make_float2(M, L);
+    }
+  }
+  if (!whole && i == 0)
+    a.part.left[f.slot] = {PART_VALID | f.flags, f.row0, f.rho0, f.rows, f.head, f.ender, {0, 0}};
+}
+
+template <typename E, int D, int NTR>
+__global__ void __launch_bounds__(NTHREADS, RowsCfg<E, D, NTR>::CTAS_PER_SM)
     attend_rows_kernel(const __grid_constant__ RowsArgs a) {
-  using C = RowsCfg<E, D, MT>;
-  constexpr int RB = C::RB, CH = C::CH, R = C::R, S = C::S;
+  using C = RowsCfg<E, D, NTR>;
+  constexpr int RB = C::RB, CH = C::CH, R = C::R, NS = C::NS, GROUP = C::GROUP, KT = C::KT;
+  constexpr int EPC = 16 / (int)sizeof(E);  // elements of a chunk
   extern __shared__ __align__(1024) uint8_t smem[];
-  __shared__ PlanShared plan;
+  __shared__ PlanShared<WARPS> plan;
   __shared__ float2 ml_sh[WARPS][R];
+  __shared__ int4 item_sh[WARPS];  // b, tile, head, and 1: held, 2: no part, 0: neither
+  __shared__ int ends_sh[WARPS];   // a held item's PART_STARTS, PART_ENDS
   ptx::grid_launch_dependents();
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  const int quad = lane & 3, qrow = lane >> 2;
+  const int quad = lane & 3, oct = lane >> 2;  // mma fragments: columns 2 quad, 2 quad + 1; row oct
+  const int mat = lane >> 3, mr = lane & 7;    // ldmatrix: matrix, row
   const fakv_cache& c = a.c;
   const Geo& g = a.g;
-  const Part part = find_part<NTHREADS>(g, c, a.cu, a.slots, a.B, a.T, reinterpret_cast<int*>(smem), plan,
-                                        blockIdx.x, gridDim.x);
-  if (tid < 2) {
-    a.part.left[2 * blockIdx.x + tid].flags = 0;  // (an entry of this CTA's is written below)
-  }
-  if (part.units == 0) return;
-  const uint32_t ring = ptx::smem_u32(smem) + warp * C::WARP_BYTES;
-  const uint32_t sq = ptx::smem_u32(smem) + WARPS * C::WARP_BYTES;
-  const int dv_chunks = c.D * (int)sizeof(E) / 16;
+  Seq seq;
+  const Part part = find_part<NTHREADS, WARPS>(g, c, a.cu, a.slots, a.B, a.T, reinterpret_cast<int*>(smem), plan, seq);
+  Walk walk(part, seq);
+  const int worker = blockIdx.x * WARPS + warp;
+  if (lane < 2) a.part.left[2 * worker + lane].flags = 0;
+  if (lane == 0) item_sh[warp] = make_int4(walk.p.b, walk.p.tile, walk.p.head, 2);
+  uint8_t* const mine = smem + warp * C::WARP_BYTES;
+  const uint32_t sq = ptx::smem_u32(mine);
+  const uint32_t ring = sq + C::Q_BYTES;
+  const int dv_chunks = c.D / EPC;
   const E* const Kp = static_cast<const E*>(c.K) + a.plane * c.plane_stride;
   const E* const Vp = static_cast<const E*>(c.V) + a.plane * c.plane_stride;
+  Seg seg = {};
+  Finish fin;
+  bool held = false;  // the worker's only item, not done whole: its result waits for the others'
 
-  Walk walk(part);
-  Seg seg;
   while (walk.next(g, c, a.cu, a.slots, a.T, seg)) {
     const Seq& s = seg.s;
     const Tile& x = seg.x;
-    const int head = seg.head;
 
-    // ---- q rows into shared memory (zeros behind the item's rows and the tensor's columns)
-    for (int i = tid; i < R * CH; i += NTHREADS) {
+    // ---- pages of the next 32 octets of keys, an octet per lane, and of the 32 after those:
+    // look-ups are never waited for in the loop
+    const int first = seg.k0 * GROUP;
+    const int n = max(0, min(seg.k0 + seg.n, (x.hi + GROUP - 1) / GROUP) - seg.k0);  // groups
+    const int* const row = c.table + (long long)s.slot * c.table_stride;
+    auto lookup = [&](int octet) {
+      const int j = first + octet * 8;
+      if (octet >= n * (GROUP / 8) || j >= x.hi || j + 8 <= x.lo) return -1;  // no row sees it
+      const int p = row[j >> a.shift];
+      if ((unsigned)p < (unsigned)c.num_pages) return p;
+      raise(c.status, FAKV_BAD_PAGE);
+      return -1;
+    };
+    int page = -1, page_next = lookup(lane);
+
+    // ---- q rows (zeros behind the item's rows and the tensor's columns)
+#pragma unroll 1
+    for (int i = lane; i < R * CH; i += 32) {
       const int r = i / CH, ch = i % CH;
-      const int rho = x.rho0 + r;
+      const int rho = x.rho0 + r, token = g.rep.of(rho);
       const bool in = r < x.rows && ch < dv_chunks;
       const E* src = static_cast<const E*>(a.q);
-      if (in)
-        src += (s.row0 + rho / g.rep) * a.q_token + (head * g.rep + rho % g.rep) * a.q_head + ch * (16 / (int)sizeof(E));
+      if (in) src += (s.row0 + token) * a.q_token + (seg.head * g.rep.d + rho - token * g.rep.d) * a.q_head + ch * EPC;
       cp16(sq + at_rows<RB>(r, ch), src, in);
     }
-    cp_commit();
 
-    // ---- this warp's groups of keys: g0, g0 + WARPS, ...
-    const int g_end = min((seg.k0 + seg.n) * WARPS, (x.hi + GROUP - 1) / GROUP);
-    const int g0 = max(seg.k0 * WARPS, x.lo / GROUP);
-    const int gw = g0 + ((warp - g0) & (WARPS - 1));
-    const int n = gw < g_end ? (g_end - gw + WARPS - 1) / WARPS : 0;
-    // Pages of the next 32 groups, a group per lane (two pages where they hold 8 tokens),
-    // and of the 32 after those: look-ups are never waited for in the loop.
-    const int* const row = c.table + (long long)s.slot * c.table_stride;
-    auto lookup = [&](int i, int& p0, int& p1) {
-      p0 = p1 = -1;
-      if (i < n) {
-        const int j = (gw + i * WARPS) * GROUP;
-        if (a.shift > 3) {
-          p0 = p1 = row[j >> a.shift];
-        } else {  // (a half that no row sees is not looked up)
-          p0 = j + 8 > x.lo ? row[j >> 3] : 0;
-          p1 = j + 8 < x.hi ? row[(j + 8) >> 3] : 0;
-        }
-        if ((unsigned)p0 >= (unsigned)c.num_pages || (unsigned)p1 >= (unsigned)c.num_pages)
-          raise(c.status, FAKV_BAD_PAGE);
-      }
-    };
-    int pg0, pg1, nx0, nx1;
-    lookup(lane, pg0, pg1);
-    lookup(32 + lane, nx0, nx1);
-    auto load = [&](int i) {
-      if (i < n) {
-        if (i > 0 && (i & 31) == 0) {
-          pg0 = nx0;
-          pg1 = nx1;
-          lookup(i + 32 + lane, nx0, nx1);
-        }
-        const int p[2] = {__shfl_sync(0xffffffffu, pg0, i & 31), __shfl_sync(0xffffffffu, pg1, i & 31)};
-        const int j0 = (gw + i * WARPS) * GROUP;
-        const uint32_t st = ring + (i % S) * C::STAGE;
+    // ---- copies of half-step j: K (j even) or V of group j / 2, octet by octet, each in a page
+    long long base[GROUP / 8];  // of the group's octets (-1: zeros)
+    uint32_t fill = ring;
+    auto load = [&](int j) {
+      if (j < 2 * n) {
+        const bool is_v = j & 1;
+        const E* const src = (is_v ? Vp : Kp) + seg.head * c.head_stride;
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          const bool page_ok = (unsigned)p[h] < (unsigned)c.num_pages;
-          const long long base = page_ok ? p[h] * c.page_stride + ((j0 + 8 * h) & (c.page_size - 1)) * c.token_stride +
-                                               head * c.head_stride
-                                         : 0;
+        for (int k = 0; k < GROUP / 8; ++k) {
+          const int octet = (j >> 1) * (GROUP / 8) + k;
+          const int key = first + octet * 8;
+          if (!is_v) {
+            if ((octet & 31) == 0) {
+              page = page_next;
+              page_next = lookup(octet + 32 + lane);
+            }
+            const int p = __shfl_sync(0xffffffffu, page, octet & 31);
+            base[k] = p < 0 ? -1 : p * c.page_stride + (key & (c.page_size - 1)) * c.token_stride;
+          }
 #pragma unroll
-          for (int k = 0; k < 8 * CH / 32; ++k) {
-            const int r = (k * 32 + lane) / CH, ch = (k * 32 + lane) % CH;
-            const int j = j0 + 8 * h + r;
-            // nothing that no row sees is read: it may hold anything
-            const bool in = page_ok && j >= x.lo && j < x.hi && ch < dv_chunks;
-            const long long off = in ? base + r * c.token_stride + ch * (16 / (int)sizeof(E)) : 0;
-            cp16(st + at_rows<RB>(8 * h + r, ch), Kp + off, in);
-            if constexpr (C::F32) cp16(st + GROUP * RB + at_v32<RB>(8 * h + r, ch), Vp + off, in);
-            else cp16(st + GROUP * RB + at_rows<RB>(8 * h + r, ch), Vp + off, in);
+          for (int z = 0; z < 8 * CH / 32; ++z) {
+            const int r = (z * 32 + lane) / CH, ch = (z * 32 + lane) % CH;
+            // what no row sees is not read: it may hold anything
+            const bool in = base[k] >= 0 && key + r >= x.lo && key + r < x.hi && ch < dv_chunks;
+            const E* const p = in ? src + base[k] + r * c.token_stride + ch * EPC : src;
+            cp16(fill + (C::F32 && is_v ? at_v32<RB>(8 * k + r, ch) : at_rows<RB>(8 * k + r, ch)), p, in);
           }
         }
+        fill = fill + C::SLOT == ring + NS * C::SLOT ? ring : fill + C::SLOT;
       }
       cp_commit();
     };
-#pragma unroll
-    for (int i = 0; i < S - 1; ++i) load(i);
 
-    // ---- rows' bounds: row qrow + 8 h + 16 mt sees keys [lo_r, hi_r]
-    int lo_r[MT][2], hi_r[MT][2];
-    float m[MT][2], l[MT][2], o[MT][D / 8][4];
+    float m[NTR][2], l[NTR][2], o[D / 16][NTR][4];  // rows 8 nt + 2 quad + e
 #pragma unroll
-    for (int mt = 0; mt < MT; ++mt) {
+    for (int nt = 0; nt < NTR; ++nt) {
+      m[nt][0] = m[nt][1] = -FLT_MAX;
+      l[nt][0] = l[nt][1] = 0.f;
 #pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        const int r = min(mt * 16 + h * 8 + qrow, x.rows - 1);
-        const int p = s.len - s.n + (x.rho0 + r) / g.rep;
-        hi_r[mt][h] = g.causal ? min(p, s.len - 1) : s.len - 1;
-        lo_r[mt][h] = g.window > 0 ? p - g.window + 1 : 0;
-        m[mt][h] = -FLT_MAX;
-        l[mt][h] = 0.f;
-      }
-#pragma unroll
-      for (int d = 0; d < D / 8; ++d) o[mt][d][0] = o[mt][d][1] = o[mt][d][2] = o[mt][d][3] = 0.f;
+      for (int d = 0; d < D / 16; ++d) o[d][nt][0] = o[d][nt][1] = o[d][nt][2] = o[d][nt][3] = 0.f;
     }
     // keys that every row sees need no mask
     int in_lo, in_hi;
     {
-      const int pa = s.len - s.n + x.rho0 / g.rep, pb = s.len - s.n + (x.rho0 + x.rows - 1) / g.rep;
+      const int pa = s.len - s.n + g.rep.of(x.rho0), pb = s.len - s.n + g.rep.of(x.rho0 + x.rows - 1);
       in_hi = g.causal ? min(pa, s.len - 1) : s.len - 1;
       in_lo = g.window > 0 ? pb - g.window + 1 : 0;
     }
-    cp_wait<S - 1>();  // q (committed before the first group)
-    __syncthreads();
 
-    for (int i = 0; i < n; ++i) {
-      cp_wait<S - 2>();
-      __syncwarp();  // the group is here, and every lane has read the one before it:
-      load(i + S - 1);  // its stage is filled again
-      const uint32_t sk = ring + (i % S) * C::STAGE, sv = sk + GROUP * RB;
-      const int j0 = (gw + i * WARPS) * GROUP;
-      float sc[MT][2][4];
+    // Half-steps K_0, V_0, K_1, ...: a slot is filled again as soon as it is read, NS half-steps
+    // ahead. The first NS rounds only load: one copy of the loading code, as every instruction
+    // that is new costs its fetch.
+    uint32_t use = ring;
+    float sc[KT][NTR][4];  // scores, then probabilities: keys 16 kt + oct (+ 8), rows 8 nt + 2 quad + e
+    uint32_t qr[C::Q_REGS ? D / 32 : 1][4];
+#pragma unroll 1
+    for (int j = -NS; j < 2 * n; ++j) {
+      if (j >= 0) {
+        cp_wait<NS - 1>();
+        __syncwarp();
+        if ((j & 1) == 0) {
+          // -------- scores of group j / 2
+          const int j0 = first + (j >> 1) * GROUP;
 #pragma unroll
-      for (int mt = 0; mt < MT; ++mt)
+          for (int kt = 0; kt < KT; ++kt)
 #pragma unroll
-        for (int nt = 0; nt < 2; ++nt) sc[mt][nt][0] = sc[mt][nt][1] = sc[mt][nt][2] = sc[mt][nt][3] = 0.f;
-      const int mat = lane >> 3, mr = lane & 7;
-      if constexpr (!C::F32) {
+            for (int nt = 0; nt < NTR; ++nt) sc[kt][nt][0] = sc[kt][nt][1] = sc[kt][nt][2] = sc[kt][nt][3] = 0.f;
+          if constexpr (!C::F32) {
+            if (C::Q_REGS && j == 0) {
 #pragma unroll
-        for (int ks = 0; ks < D / 16; ++ks) {
-          uint32_t kb[4];  // keys 0-7: k low, high; keys 8-15: k low, high
-          ldsm4(sk + at_rows<RB>((mat >> 1) * 8 + mr, 2 * ks + (mat & 1)), kb);
+              for (int kp = 0; kp < D / 32; ++kp) ldsm4(sq + at_rows<RB>(mr, 4 * kp + mat), qr[C::Q_REGS ? kp : 0]);
+            }
 #pragma unroll
-          for (int mt = 0; mt < MT; ++mt) {
-            uint32_t qa[4];
-            ldsm4(sq + at_rows<RB>(mt * 16 + (mat & 1) * 8 + mr, 2 * ks + (mat >> 1)), qa);
-            mma_bf16(sc[mt][0], qa, kb[0], kb[1]);
-            mma_bf16(sc[mt][1], qa, kb[2], kb[3]);
+            for (int kp = 0; kp < D / 32; ++kp) {  // two k16 steps
+              uint32_t ka[KT][2][4];  // keys 0-7, 8-15 of columns low, then high
+#pragma unroll
+              for (int kt = 0; kt < KT; ++kt)
+#pragma unroll
+                for (int e = 0; e < 2; ++e)
+                  ldsm4(use + at_rows<RB>(kt * 16 + (mat & 1) * 8 + mr, 4 * kp + 2 * e + (mat >> 1)), ka[kt][e]);
+#pragma unroll
+              for (int nt = 0; nt < NTR; ++nt) {
+                uint32_t qb[4];
+                if constexpr (C::Q_REGS) {
+#pragma unroll
+                  for (int e = 0; e < 4; ++e) qb[e] = qr[kp][e];
+                } else {
+                  ldsm4(sq + at_rows<RB>(nt * 8 + mr, 4 * kp + mat), qb);
+                }
+#pragma unroll
+                for (int kt = 0; kt < KT; ++kt) {
+                  mma_bf16(sc[kt][nt], ka[kt][0], qb[0], qb[1]);
+                  mma_bf16(sc[kt][nt], ka[kt][1], qb[2], qb[3]);
+                }
+              }
+            }
+          } else {
+            // The tensor core cuts off what it adds to a sum below the sum's last bit: the small
+            // products have sums of their own, so that the large one is cut a third as often.
+            float lh[KT][NTR][4], hl[KT][NTR][4];
+#pragma unroll
+            for (int kt = 0; kt < KT; ++kt)
+#pragma unroll
+              for (int nt = 0; nt < NTR; ++nt)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) lh[kt][nt][e] = hl[kt][nt][e] = 0.f;
+#pragma unroll
+            for (int kp = 0; kp < D / 16; ++kp) {  // two k8 steps: four chunks of four columns
+              uint32_t kh[KT][2][4], kl[KT][2][4];
+#pragma unroll
+              for (int kt = 0; kt < KT; ++kt)
+#pragma unroll
+                for (int e = 0; e < 2; ++e) {
+                  uint32_t v[4];
+                  ldsm4(use + at_rows<RB>(kt * 16 + (mat & 1) * 8 + mr, 4 * kp + 2 * e + (mat >> 1)), v);
+#pragma unroll
+                  for (int z = 0; z < 4; ++z) split(v[z], kh[kt][e][z], kl[kt][e][z]);
+                }
+#pragma unroll
+              for (int nt = 0; nt < NTR; ++nt) {
+                uint32_t v[4], qh[4], ql[4];
+                ldsm4(sq + at_rows<RB>(nt * 8 + mr, 4 * kp + mat), v);
+#pragma unroll
+                for (int z = 0; z < 4; ++z) split(v[z], qh[z], ql[z]);
+#pragma unroll
+                for (int kt = 0; kt < KT; ++kt)
+#pragma unroll
+                  for (int e = 0; e < 2; ++e) {
+                    mma_tf32(hl[kt][nt], kh[kt][e], ql[2 * e], ql[2 * e + 1]);
+                    mma_tf32(lh[kt][nt], kl[kt][e], qh[2 * e], qh[2 * e + 1]);
+                    mma_tf32(sc[kt][nt], kh[kt][e], qh[2 * e], qh[2 * e + 1]);
+                  }
+              }
+            }
+#pragma unroll
+            for (int kt = 0; kt < KT; ++kt)
+#pragma unroll
+              for (int nt = 0; nt < NTR; ++nt)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) sc[kt][nt][e] += lh[kt][nt][e] + hl[kt][nt][e];
           }
-        }
-      } else {
-        // The tensor core cuts off what it adds to a sum below the sum's last bit: the small
-        // products have sums of their own, so that the large one is cut a third as often.
-        float small[MT][2][4];
+          if (j0 < in_lo || j0 + GROUP - 1 > in_hi) {
 #pragma unroll
-        for (int mt = 0; mt < MT; ++mt)
+            for (int nt = 0; nt < NTR; ++nt)
 #pragma unroll
-          for (int nt = 0; nt < 2; ++nt) small[mt][nt][0] = small[mt][nt][1] = small[mt][nt][2] = small[mt][nt][3] = 0.f;
+              for (int e = 0; e < 2; ++e) {
+                // row 8 nt + 2 quad + e sees keys [lo, hi]
+                const int p = s.len - s.n + g.rep.of(x.rho0 + min(nt * 8 + quad * 2 + e, x.rows - 1));
+                const int hi = g.causal ? min(p, s.len - 1) : s.len - 1;
+                const int lo = g.window > 0 ? p - g.window + 1 : 0;
 #pragma unroll
-        for (int kp = 0; kp < D / 16; ++kp) {  // two k8 steps: four chunks of four
-          uint32_t kh[2][4], kl[2][4];
+                for (int kt = 0; kt < KT; ++kt)
 #pragma unroll
-          for (int nt = 0; nt < 2; ++nt) {
-            uint32_t v[4];
-            ldsm4(sk + at_rows<RB>(nt * 8 + mr, 4 * kp + mat), v);
-#pragma unroll
-            for (int e = 0; e < 4; ++e) split(v[e], kh[nt][e], kl[nt][e]);
+                  for (int z = 0; z < 2; ++z) {
+                    const int key = j0 + kt * 16 + z * 8 + oct;
+                    if (key < lo || key > hi) sc[kt][nt][2 * z + e] = -INFINITY;
+                  }
+              }
           }
+          // -------- probabilities; m where it has to move
+          float mx[NTR][2];
+          bool grow = false;
 #pragma unroll
-          for (int mt = 0; mt < MT; ++mt) {
+          for (int nt = 0; nt < NTR; ++nt)
 #pragma unroll
             for (int e = 0; e < 2; ++e) {
-              uint32_t v[4], qh[4], ql[4];
-              ldsm4(sq + at_rows<RB>(mt * 16 + (mat & 1) * 8 + mr, 4 * kp + 2 * e + (mat >> 1)), v);
+              float v = fmaxf(sc[0][nt][e], sc[0][nt][e + 2]);
 #pragma unroll
-              for (int z = 0; z < 4; ++z) split(v[z], qh[z], ql[z]);
+              for (int kt = 1; kt < KT; ++kt) v = ptx::max3(v, sc[kt][nt][e], sc[kt][nt][e + 2]);
+              mx[nt][e] = v * a.sl2;
+              grow |= mx[nt][e] > m[nt][e] + RESCALE_THRESHOLD;
+            }
+          if (__any_sync(0xffffffffu, grow)) {
 #pragma unroll
-              for (int nt = 0; nt < 2; ++nt) {
-                mma_tf32(small[mt][nt], qh, kl[nt][2 * e], kl[nt][2 * e + 1]);
-                mma_tf32(small[mt][nt], ql, kh[nt][2 * e], kh[nt][2 * e + 1]);
-                mma_tf32(sc[mt][nt], qh, kh[nt][2 * e], kh[nt][2 * e + 1]);
+            for (int nt = 0; nt < NTR; ++nt)
+#pragma unroll
+              for (int e = 0; e < 2; ++e) {
+                float v = fmaxf(mx[nt][e], __shfl_xor_sync(0xffffffffu, mx[nt][e], 4));
+                v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 8));
+                v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 16));
+                const float mn = fmaxf(m[nt][e], v);
+                const float f = ptx::ex2(m[nt][e] - mn);
+                m[nt][e] = mn;
+                l[nt][e] *= f;
+#pragma unroll
+                for (int d = 0; d < D / 16; ++d) {
+                  o[d][nt][e] *= f;
+                  o[d][nt][e + 2] *= f;
+                }
+              }
+          }
+#pragma unroll
+          for (int kt = 0; kt < KT; ++kt)
+#pragma unroll
+            for (int nt = 0; nt < NTR; ++nt)
+#pragma unroll
+              for (int e = 0; e < 4; ++e) {
+                const float p = ptx::ex2(fmaf(sc[kt][nt][e], a.sl2, -m[nt][e & 1]));
+                sc[kt][nt][e] = p;
+                l[nt][e & 1] += p;
+              }
+        } else if constexpr (!C::F32) {
+          // -------- O^T += V^T P^T
+#pragma unroll
+          for (int kt = 0; kt < KT; ++kt) {
+            uint32_t ph[NTR][2], pl[NTR][2];  // keys low, high
+#pragma unroll
+            for (int nt = 0; nt < NTR; ++nt)
+#pragma unroll
+              for (int e = 0; e < 2; ++e) {
+                const float p0 = sc[kt][nt][2 * e], p1 = sc[kt][nt][2 * e + 1];
+                const uint32_t hi = bf2(p0, p1);
+                ph[nt][e] = transpose8(hi);
+                pl[nt][e] = transpose8(bf2(p0 - __uint_as_float(hi << 16), p1 - __uint_as_float(hi & 0xffff0000u)));
+              }
+#pragma unroll
+            for (int d = 0; d < D / 16; ++d) {
+              uint32_t va[4];  // columns 0-7, 8-15 of keys low, then high
+              ldsm4t(use + at_rows<RB>(kt * 16 + (mat >> 1) * 8 + mr, 2 * d + (mat & 1)), va);
+#pragma unroll
+              for (int nt = 0; nt < NTR; ++nt) {
+                mma_bf16(o[d][nt], va, pl[nt][0], pl[nt][1]);
+                mma_bf16(o[d][nt], va, ph[nt][0], ph[nt][1]);
               }
             }
           }
-        }
+        } else {
+          uint32_t ph[NTR][2 * KT][2], pl[NTR][2 * KT][2];  // k8 steps: keys quad, quad + 4
 #pragma unroll
-        for (int mt = 0; mt < MT; ++mt)
+          for (int nt = 0; nt < NTR; ++nt)
 #pragma unroll
-          for (int nt = 0; nt < 2; ++nt)
+            for (int k8 = 0; k8 < 2 * KT; ++k8)
 #pragma unroll
-            for (int e = 0; e < 4; ++e) sc[mt][nt][e] += small[mt][nt][e];
-      }
-      if (j0 < in_lo || j0 + GROUP - 1 > in_hi) {
+              for (int e = 0; e < 2; ++e) {
+                // key quad + 4 e, row oct: in lane 4 key + row / 2, value row & 1
+                const int from = (quad + 4 * e) * 4 + (oct >> 1);
+                const float p0 = __shfl_sync(0xffffffffu, sc[k8 >> 1][nt][2 * (k8 & 1)], from);
+                const float p1 = __shfl_sync(0xffffffffu, sc[k8 >> 1][nt][2 * (k8 & 1) + 1], from);
+                split(__float_as_uint(oct & 1 ? p1 : p0), ph[nt][k8][e], pl[nt][k8][e]);
+              }
 #pragma unroll
-        for (int mt = 0; mt < MT; ++mt)
+          for (int d = 0; d < D / 16; ++d) {
+            uint32_t vh[2 * KT][4], vl[2 * KT][4];  // columns oct, oct + 8 of key quad, then of key quad + 4
 #pragma unroll
-          for (int nt = 0; nt < 2; ++nt)
+            for (int k8 = 0; k8 < 2 * KT; ++k8)
 #pragma unroll
-            for (int e = 0; e < 4; ++e) {
-              const int j = j0 + nt * 8 + quad * 2 + (e & 1);
-              if (j < lo_r[mt][e >> 1] || j > hi_r[mt][e >> 1]) sc[mt][nt][e] = -INFINITY;
-            }
-      }
-      // maxima of the rows, and m where it has to move
-      bool grow = false;
-      float mx[MT][2];
+              for (int e = 0; e < 4; ++e) {
+                const int col = d * 16 + (e & 1) * 8 + oct, key = k8 * 8 + (e >> 1) * 4 + quad;
+                split(lds32(use + at_v32<RB>(key, col >> 2) + (col & 3) * 4), vh[k8][e], vl[k8][e]);
+              }
 #pragma unroll
-      for (int mt = 0; mt < MT; ++mt)
+            for (int nt = 0; nt < NTR; ++nt) {
+              // a sum per group, added to O in fp32: O itself is not cut at every step
+              float add[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          float v = fmaxf(fmaxf(sc[mt][0][2 * h], sc[mt][0][2 * h + 1]), fmaxf(sc[mt][1][2 * h], sc[mt][1][2 * h + 1]));
-          v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 1));
-          v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 2));
-          mx[mt][h] = v * a.sl2;
-          grow |= mx[mt][h] > m[mt][h] + RESCALE_THRESHOLD;
-        }
-      if (__any_sync(0xffffffffu, grow)) {
+              for (int k8 = 0; k8 < 2 * KT; ++k8) {
+                mma_tf32(add, vl[k8], ph[nt][k8][0], ph[nt][k8][1]);
+                mma_tf32(add, vh[k8], pl[nt][k8][0], pl[nt][k8][1]);
+              }
 #pragma unroll
-        for (int mt = 0; mt < MT; ++mt)
+              for (int k8 = 0; k8 < 2 * KT; ++k8) mma_tf32(add, vh[k8], ph[nt][k8][0], ph[nt][k8][1]);
 #pragma unroll
-          for (int h = 0; h < 2; ++h) {
-            const float mn = fmaxf(m[mt][h], mx[mt][h]);
-            const float f = ptx::ex2(m[mt][h] - mn);
-            m[mt][h] = mn;
-            l[mt][h] *= f;
-#pragma unroll
-            for (int d = 0; d < D / 8; ++d) {
-              o[mt][d][2 * h] *= f;
-              o[mt][d][2 * h + 1] *= f;
+              for (int e = 0; e < 4; ++e) o[d][nt][e] += add[e];
             }
           }
-      }
-#pragma unroll
-      for (int mt = 0; mt < MT; ++mt)
-#pragma unroll
-        for (int nt = 0; nt < 2; ++nt)
-#pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            const float p = ptx::ex2(fmaf(sc[mt][nt][e], a.sl2, -m[mt][e >> 1]));
-            sc[mt][nt][e] = p;
-            l[mt][e >> 1] += p;
-          }
-      if constexpr (!C::F32) {
-        uint32_t ph[MT][4], pl[MT][4];
-#pragma unroll
-        for (int mt = 0; mt < MT; ++mt)
-#pragma unroll
-          for (int k = 0; k < 4; ++k) {  // rows r, r + 8 of keys 0-7, then of keys 8-15
-            const float p0 = sc[mt][k >> 1][2 * (k & 1)], p1 = sc[mt][k >> 1][2 * (k & 1) + 1];
-            ph[mt][k] = bf2(p0, p1);
-            pl[mt][k] = bf2(p0 - __uint_as_float(ph[mt][k] << 16), p1 - __uint_as_float(ph[mt][k] & 0xffff0000u));
-          }
-#pragma unroll
-        for (int d = 0; d < D / 16; ++d) {
-          uint32_t vb[4];  // columns 0-7: keys low, high; columns 8-15: keys low, high
-          ldsm4t(sv + at_rows<RB>((mat & 1) * 8 + mr, 2 * d + (mat >> 1)), vb);
-#pragma unroll
-          for (int mt = 0; mt < MT; ++mt) {
-            mma_bf16(o[mt][2 * d], pl[mt], vb[0], vb[1]);
-            mma_bf16(o[mt][2 * d + 1], pl[mt], vb[2], vb[3]);
-            mma_bf16(o[mt][2 * d], ph[mt], vb[0], vb[1]);
-            mma_bf16(o[mt][2 * d + 1], ph[mt], vb[2], vb[3]);
-          }
         }
-      } else {
-        // the eight keys of a k step in the order that a thread's scores have them: k slots
-        // quad and quad + 4 are keys 2 quad and 2 quad + 1
-        uint32_t ph[MT][2][4], pl[MT][2][4];
-#pragma unroll
-        for (int mt = 0; mt < MT; ++mt)
-#pragma unroll
-          for (int nt = 0; nt < 2; ++nt)
-#pragma unroll
-            for (int k = 0; k < 4; ++k)
-              split(__float_as_uint(sc[mt][nt][(k & 1) * 2 + (k >> 1)]), ph[mt][nt][k], pl[mt][nt][k]);
-#pragma unroll
-        for (int d = 0; d < D / 8; ++d) {
-          const int col = d * 8 + qrow;
-          uint32_t vh[2][2], vl[2][2];
-#pragma unroll
-          for (int nt = 0; nt < 2; ++nt)
-#pragma unroll
-            for (int e = 0; e < 2; ++e)
-              split(lds32(sv + at_v32<RB>(nt * 8 + 2 * quad + e, col >> 2) + (col & 3) * 4), vh[nt][e], vl[nt][e]);
-#pragma unroll
-          for (int mt = 0; mt < MT; ++mt) {
-            // a sum per group, added to O in fp32: O itself is not cut at every step
-            float add[4] = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-            for (int nt = 0; nt < 2; ++nt) {
-              mma_tf32(add, pl[mt][nt], vh[nt][0], vh[nt][1]);
-              mma_tf32(add, ph[mt][nt], vl[nt][0], vl[nt][1]);
-            }
-#pragma unroll
-            for (int nt = 0; nt < 2; ++nt) mma_tf32(add, ph[mt][nt], vh[nt][0], vh[nt][1]);
-#pragma unroll
-            for (int e = 0; e < 4; ++e) o[mt][d][e] += add[e];
-          }
-        }
+        __syncwarp();  // the slot is read
+        use = use + C::SLOT == ring + NS * C::SLOT ? ring : use + C::SLOT;
       }
+      load(j + NS);
     }
     cp_wait<0>();
-    __syncthreads();
+    __syncwarp();  // (every lane's copies have landed: the ring may be used for what comes next)
 
-    // ---- the warps' results through shared memory (each in its own ring)
-    {
-      float* mine = reinterpret_cast<float*>(smem + warp * C::WARP_BYTES);
+    // ---- this warp's sums into its shared memory
 #pragma unroll
-      for (int mt = 0; mt < MT; ++mt)
+    for (int nt = 0; nt < NTR; ++nt)
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          float v = l[mt][h];
-          v += __shfl_xor_sync(0xffffffffu, v, 1);
-          v += __shfl_xor_sync(0xffffffffu, v, 2);
-          const int r = mt * 16 + h * 8 + qrow;
-          if (quad == 0) ml_sh[warp][r] = make_float2(m[mt][h], v);
+      for (int e = 0; e < 2; ++e) {
+        float v = l[nt][e];
+        v += __shfl_xor_sync(0xffffffffu, v, 4);
+        v += __shfl_xor_sync(0xffffffffu, v, 8);
+        v += __shfl_xor_sync(0xffffffffu, v, 16);
+        const int r = nt * 8 + quad * 2 + e;
+        if (oct == 0) ml_sh[warp][r] = make_float2(m[nt][e], v);
+        float* const to = reinterpret_cast<float*>(mine) + r * C::OS + oct;
 #pragma unroll
-          for (int d = 0; d < D / 8; ++d)
-            *reinterpret_cast<float2*>(mine + r * C::OS + d * 8 + quad * 2) =
-                make_float2(o[mt][d][2 * h], o[mt][d][2 * h + 1]);
+        for (int d = 0; d < D / 16; ++d) {
+          to[d * 16] = o[d][nt][e];
+          to[d * 16 + 8] = o[d][nt][e + 2];
         }
-    }
-    __syncthreads();
-    const bool whole = seg.starts && seg.ends;
-    const int slot = 2 * blockIdx.x + seg.slot;
-    for (int k = tid; k < x.rows * (D / 4); k += NTHREADS) {
-      const int r = k / (D / 4), col = k % (D / 4) * 4;
-      float M = -FLT_MAX;
-#pragma unroll
-      for (int w = 0; w < WARPS; ++w) M = fmaxf(M, ml_sh[w][r].x);
-      float L = 0.f;
-      float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll
-      for (int w = 0; w < WARPS; ++w) {
-        const float f = ptx::ex2(ml_sh[w][r].x - M);
-        const float4 v = *reinterpret_cast<const float4*>(reinterpret_cast<float*>(smem + w * C::WARP_BYTES) + r * C::OS + col);
-        L += f * ml_sh[w][r].y;
-        acc.x += f * v.x; acc.y += f * v.y; acc.z += f * v.z; acc.w += f * v.w;
       }
-      if (whole) {
-        const float inv = L > 0.f ? 1.f / L : 0.f;
-        const int rho = x.rho0 + r;
-        const size_t at = (size_t)(s.row0 + rho / g.rep) * a.H + head * g.rep + rho % g.rep;
-        if (col == 0) a.LSE[at] = L > 0.f ? (M + log2f(L)) * LN2 : -INFINITY;
-        if (col < c.D) {
-          if (a.out_bf16)
-            *reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(a.O) + at * c.D + col) =
-                make_uint2(bf2(acc.x * inv, acc.y * inv), bf2(acc.z * inv, acc.w * inv));
-          else
-            *reinterpret_cast<float4*>(static_cast<float*>(a.O) + at * c.D + col) =
-                make_float4(acc.x * inv, acc.y * inv, acc.z * inv, acc.w * inv);
-        }
-      } else {
-        *reinterpret_cast<float4*>(a.part.O + ((size_t)slot * R + r) * D + col) = acc;
-        if (col == 0) a.part.ml[(size_t)slot * R + r] = make_float2(M, L);
-      }
+    fin = {s.row0, x.rho0, x.rows, seg.head, walk.p.ender,
+           (seg.starts ? PART_STARTS : 0) | (seg.ends ? PART_ENDS : 0), 2 * worker + seg.slot};
+    __syncwarp();
+    held = seg.slot == 0 && walk.done() && !(seg.starts && seg.ends);
+    if (!held) {
+      finish<C, D>(a, fin, smem, ml_sh, warp, warp, lane, 32);
+      __syncwarp();
     }
-    if (!whole && tid == 0)
-      a.part.left[slot] = {PART_VALID | (seg.starts ? PART_STARTS : 0) | (seg.ends ? PART_ENDS : 0), s.row0, x.rho0, x.rows,
-                           head, {0, 0, 0}};
-    __syncthreads();  // the rings are read: the next item may fill them
   }
+
+  // ---- all warps with parts of one and the same item: one result (or part) for the CTA
+  if (lane == 0 && walk.moved) {
+    item_sh[warp].w = held;
+    ends_sh[warp] = fin.flags;
+  }
+  __syncthreads();
+  bool same = item_sh[0].w == 1;
+  int last = 0;
+#pragma unroll
+  for (int w = 1; w < WARPS; ++w) {
+    const int4 p = item_sh[0], q = item_sh[w];
+    if (q.w == 2) continue;  // no part
+    same = same && last == w - 1 && q.w == 1 && q.x == p.x && q.y == p.y && q.z == p.z;
+    last = w;
+  }
+  if (!held) return;
+  same = same && last > 0;
+  if (same) {
+    fin.flags = (ends_sh[0] & PART_STARTS) | (ends_sh[last] & PART_ENDS) | PART_JOINED;
+    fin.slot = 2 * blockIdx.x * WARPS;
+    // (the join counts the workers up to the one that ends an item: nothing of the others)
+    if (warp > 0 && lane < R && (fin.flags & PART_ENDS))
+      a.part.ml[(size_t)2 * worker * R + lane] = make_float2(-FLT_MAX, 0.f);
+  }
+  finish<C, D>(a, fin, smem, ml_sh, same ? 0 : warp, same ? last : warp, same ? tid : lane, same ? 32 * (last + 1) : 32);
 }
 
-// An item that several CTAs did parts of: the CTA in whose part it starts left the first
-// one (at most one such per CTA, its last item: slot 1, or 0 if it is its first too), the
-// following CTAs the others in their slots 0, up to the one that ends it. Blocks (c, y)
-// join the item that CTA c left open, y sharing out its rows. A block's threads stand
-// for the columns, for rows, and, where there are many parts, for shares of the parts, which
-// are merged in order.
-constexpr int JOIN_THREADS = 256;
-constexpr int JOIN_BLOCKS = 32;
+// An item that several workers did parts of: the worker in whose part it starts left the
+// first one (at most one such per worker, its last item: slot 1, or 0 if it is its first
+// too), those after it the others in their slots 0, up to the one that ends it; a CTA all
+// inside the item left one part for its workers, in the first one's slot. Blocks (c, y) stand
+// for CTA c. At most one of its open items goes on beyond it: the blocks share out its rows,
+// and their warps its parts (of an item of many rows, the rows too). An item that ends in the
+// CTA has few parts: a warp of each block joins them. Lanes are columns. Sums are merged in a fixed
+// order. Most blocks find nothing open and go, so they are small: all of them are on the
+// SMs at once.
+constexpr int JOIN_WARPS = 4;
+constexpr int JOIN_THREADS = 32 * JOIN_WARPS;
 
 struct Sum {  // sums of exponentials taken against the maximum M
   float M, L;
@@ -512,62 +608,68 @@ struct Sum {  // sums of exponentials taken against the maximum M
   }
 };
 
-__global__ void __launch_bounds__(JOIN_THREADS) attend_join_kernel(const __grid_constant__ JoinArgs a) {
-  ptx::grid_dependency_wait();
-  __shared__ int parts_sh;
+// `where`: the worker of the CTA that left the item open, + 16 if in its slot 1. ALL: by all
+// blocks and warps of the CTA, else by the calling warp.
+template <bool ALL>
+__device__ __forceinline__ void join_item(const JoinArgs& a, int where, int last_worker, int warp, int lane) {
   __shared__ float2 ml[JOIN_THREADS];
   __shared__ float4 acc_sh[JOIN_THREADS];
-  const int cta = blockIdx.x, tid = threadIdx.x;
-  constexpr int OPEN = PART_STARTS | PART_ENDS;
-  const int open0 = a.part.left[2 * cta].flags & OPEN, open1 = a.part.left[2 * cta + 1].flags & OPEN;
-  if (open0 != PART_STARTS && open1 != PART_STARTS) return;
-  const int which = open1 == PART_STARTS;
-  const Left f = a.part.left[2 * cta + which];
-  if (tid == 0) parts_sh = a.ctas;
-  __syncthreads();
-  for (int k = cta + 1 + tid; k < a.ctas; k += JOIN_THREADS)
-    if (a.part.left[2 * k].flags & PART_ENDS) { atomicMin(&parts_sh, k); break; }
-  __syncthreads();
-  const int parts = parts_sh - cta + 1;  // slot 2 cta + which, then 2 (cta + 1), ...
-  const int cols = a.D / 4, groups = JOIN_THREADS / cols;
-  int shares = 1;
-  while (shares < groups && shares * 4 < parts) shares *= 2;
-  const int side = groups / shares;  // rows at a time
-  const int col = tid % cols, r = tid / cols % side, share = tid / (cols * side);
-  const int p0 = parts * share / shares, p1 = parts * (share + 1) / shares;
-  for (int r0 = blockIdx.y * side; r0 < f.rows; r0 += gridDim.y * side) {
+  const int k = blockIdx.x * a.per + (where & 15), which = where >> 4;
+  const Left f = a.part.left[2 * k + which];
+  // parts: worker k's, those of the workers after it in its CTA, one of each CTA all inside,
+  // those of the last CTA up to the worker that ends the item
+  const int end = min(f.ender, last_worker), c0 = blockIdx.x, c1 = end / a.per;
+  const int near = (f.flags & PART_JOINED) ? 0 : min(end, c0 * a.per + a.per - 1) - k;
+  const int inside = max(0, c1 - c0 - 1);
+  const int parts = 1 + near + inside + (c1 > c0 ? end - c1 * a.per + 1 : 0);
+  auto slot_of = [&](int p) {
+    if (p == 0) return 2 * k + which;
+    if (p <= near) return 2 * (k + p);
+    p -= near;
+    return p <= inside ? 2 * (c0 + p) * a.per : 2 * (c1 * a.per + p - inside - 1);
+  };
+  const int cols = a.D / 4, side = 32 / cols;  // lanes of a row; rows of a warp
+  const int col = lane % cols, sub = lane / cols;
+  const bool tall = f.rows >= 64;              // warps take rows; else shares of the parts
+  const bool share = ALL && !tall;
+  const int p0 = share ? parts * warp / JOIN_WARPS : 0;
+  const int p1 = share ? parts * (warp + 1) / JOIN_WARPS : parts;
+  const int r_first = ALL && tall ? blockIdx.y * JOIN_WARPS + warp : blockIdx.y;
+  const int r_step = ALL && tall ? gridDim.y * JOIN_WARPS : gridDim.y;
+  for (int g = r_first; g * side < f.rows; g += r_step) {
+    const int r = g * side + sub;
     Sum x = {-FLT_MAX, 0.f, make_float4(0.f, 0.f, 0.f, 0.f)};
-    const bool mine = r0 + r < f.rows;
-    if (mine) {
-      constexpr int U = 4;
+    if (r < f.rows) {
+      constexpr int U = 8;
       for (int p = p0; p < p1; p += U) {
         float2 y[U];
         float4 v[U];
 #pragma unroll
-        for (int k = 0; k < U; ++k) {
-          if (p + k < p1) {
-            const size_t row = (size_t)(p + k == 0 ? 2 * cta + which : 2 * (cta + p + k)) * a.R + r0 + r;
-            y[k] = a.part.ml[row];
-            v[k] = *reinterpret_cast<const float4*>(a.part.O + row * a.D + col * 4);
+        for (int u = 0; u < U; ++u) {
+          if (p + u < p1) {
+            const size_t row = (size_t)slot_of(p + u) * a.R + r;
+            y[u] = a.part.ml[row];
+            v[u] = *reinterpret_cast<const float4*>(a.part.O + row * a.D + col * 4);
           }
         }
 #pragma unroll
-        for (int k = 0; k < U; ++k)
-          if (p + k < p1) x.add(y[k].x, y[k].y, v[k]);
+        for (int u = 0; u < U; ++u)
+          if (p + u < p1 && y[u].y > 0.f) x.add(y[u].x, y[u].y, v[u]);
       }
     }
-    ml[tid] = make_float2(x.M, x.L);
-    acc_sh[tid] = x.acc;
-    __syncthreads();
-    if (share == 0 && mine) {
-      for (int k = 1; k < shares; ++k) {
-        const int at = tid + k * cols * side;
-        x.add(ml[at].x, ml[at].y, acc_sh[at]);
-      }
-      const float inv = x.L > 0.f ? 1.f / x.L : 0.f;
-      const int rho = f.rho0 + r0 + r;
-      const size_t at = (size_t)(f.row0 + rho / a.rep) * a.H + f.head * a.rep + rho % a.rep;
-      if (col == 0) a.LSE[at] = x.L > 0.f ? (x.M + log2f(x.L)) * LN2 : -INFINITY;
+    if (share) {
+      ml[threadIdx.x] = make_float2(x.M, x.L);
+      acc_sh[threadIdx.x] = x.acc;
+      __syncthreads();
+      for (int w = 1; warp == 0 && w < JOIN_WARPS; ++w)
+        x.add(ml[w * 32 + lane].x, ml[w * 32 + lane].y, acc_sh[w * 32 + lane]);
+      __syncthreads();
+    }
+    if (r < f.rows && (!share || warp == 0)) {
+      const float inv = x.L > 0.f ? __fdividef(1.f, x.L) : 0.f;
+      const int rho = f.rho0 + r, token = a.rep.of(rho);
+      const size_t at = (size_t)(f.row0 + token) * a.H + f.head * a.rep.d + rho - token * a.rep.d;
+      if (col == 0) a.LSE[at] = x.L > 0.f ? (x.M + __log2f(x.L)) * LN2 : -INFINITY;
       if (col * 4 < a.Dv) {
         if (a.out_bf16)
           *reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(a.O) + at * a.Dv + col * 4) =
@@ -577,22 +679,45 @@ __global__ void __launch_bounds__(JOIN_THREADS) attend_join_kernel(const __grid_
               make_float4(x.acc.x * inv, x.acc.y * inv, x.acc.z * inv, x.acc.w * inv);
       }
     }
-    __syncthreads();
   }
 }
 
-template <typename E, int D, int MT>
+__global__ void __launch_bounds__(JOIN_THREADS, 5) attend_join_kernel(const __grid_constant__ JoinArgs a) {
+  ptx::grid_dependency_wait();
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  // worker w's open item, if any, in lanes w and w + 16 (slot 0 or 1)
+  const int last_worker = a.ctas * a.per - 1;
+  int open = 0, ender = 0;
+  {
+    const int w = lane & 15, slot = 2 * (blockIdx.x * a.per + w) + (lane >> 4);
+    if (w < a.per) {
+      const Left& f = a.part.left[slot];
+      open = (f.flags & (PART_STARTS | PART_ENDS)) == PART_STARTS;
+      ender = f.ender;
+    }
+  }
+  const int first_after = (blockIdx.x + 1) * a.per;
+  const unsigned far = __ballot_sync(0xffffffffu, open && ender >= first_after);
+  const unsigned near_by = __ballot_sync(0xffffffffu, open && ender < first_after);
+  if (far) join_item<true>(a, __ffs(far) - 1, last_worker, warp, lane);
+  const unsigned me = near_by & (0x10001u << warp);
+  if (warp < a.per && me) join_item<false>(a, __ffs(me) - 1, last_worker, warp, lane);
+}
+
+template <typename E, int D, int NTR>
 fa_status run(RowsArgs& a, cudaStream_t s) {
-  using C = RowsCfg<E, D, MT>;
-  auto* kernel = attend_rows_kernel<E, D, MT>;
+  using C = RowsCfg<E, D, NTR>;
+  auto* kernel = attend_rows_kernel<E, D, NTR>;
   static std::atomic<uint64_t> done{0};
   if (!allow_smem(kernel, C::SMEM, done)) return FA_ERR_CUDA;
   const int ctas = host::sm_count() * C::CTAS_PER_SM;
   void* w = nullptr;
-  if (host::scratch_alloc(&w, partials_bytes(ctas, C::R, D), s) != cudaSuccess) return FA_ERR_CUDA;
-  a.part = partials_at(w, ctas, C::R, D);
+  if (host::scratch_alloc(&w, partials_bytes(ctas * WARPS, C::R, D), s) != cudaSuccess) return FA_ERR_CUDA;
+  a.part = partials_at(w, ctas * WARPS, C::R, D);
   a.g.R = C::R;
-  a.g.U = UNIT;
+  a.g.u_shift = log2_of(C::GROUP);
+  a.g.start = 4;
+  a.g.snap = 4;
   fa_status st = FA_OK;
   {
     host::KernelTimer t("attend_rows", s);
@@ -600,7 +725,7 @@ fa_status run(RowsArgs& a, cudaStream_t s) {
     if (cudaGetLastError() != cudaSuccess) st = FA_ERR_CUDA;
   }
   if (st == FA_OK) {
-    const JoinArgs j = {a.part, a.O, a.LSE, ctas, C::R, D, a.H, a.g.rep, a.c.D, a.out_bf16};
+    const JoinArgs j = {a.part, a.O, a.LSE, ctas, WARPS, C::R, D, a.H, a.c.D, a.out_bf16, a.g.rep};
     st = launch_join(j, s);
   }
   if (host::scratch_free(w, s) != cudaSuccess && st == FA_OK) st = FA_ERR_CUDA;
@@ -611,7 +736,7 @@ fa_status run(RowsArgs& a, cudaStream_t s) {
 
 fa_status launch_join(const JoinArgs& a, cudaStream_t s) {
   host::KernelTimer t("attend_join", s);
-  return launch_programmatic(attend_join_kernel, dim3(a.ctas, std::min((a.R + 3) / 4, JOIN_BLOCKS)), dim3(JOIN_THREADS), s, a) == cudaSuccess ? FA_OK : FA_ERR_CUDA;
+  return launch_programmatic(attend_join_kernel, dim3(a.ctas, a.per > 1 ? a.R / 2 : 16), dim3(JOIN_THREADS), s, a) == cudaSuccess ? FA_OK : FA_ERR_CUDA;
 }
 
 fa_status launch_attend_rows(const void* q, void* O, float* LSE, const int* cu, const int* slots,
@@ -630,19 +755,21 @@ fa_status launch_attend_rows(const void* q, void* O, float* LSE, const int* cu, 
   a.shift = log2_of(c.page_size);
   a.q_token = p.q_token;
   a.q_head = p.q_head;
-  a.g.rep = p.H / c.HKV;
+  const int rep = p.H / c.HKV;
+  a.g.rep = div_by(rep);
   a.g.causal = p.causal;
   a.g.window = p.window;
   a.sl2 = p.scale * LOG2E;
   a.out_bf16 = p.out_dtype == FA_BF16;
-  // one 16-row tile where a sequence's rows fit it on average, else two
-  const bool one = (long long)p.T * a.g.rep <= 16ll * p.B;
+  // Items of 8, 16 or (fp32: a bf16 cache's rows above 16 are the tensor-core tiles') 32 rows: what
+  // a sequence's rows fit on average.
+  const long long rows = ((long long)p.T * rep + p.B - 1) / p.B;
   if (c.dtype == FA_BF16) {
-    if (c.D <= 64) return one ? run<__nv_bfloat16, 64, 1>(a, s) : run<__nv_bfloat16, 64, 2>(a, s);
-    return one ? run<__nv_bfloat16, 128, 1>(a, s) : run<__nv_bfloat16, 128, 2>(a, s);
+    if (c.D <= 64) return rows <= 8 ? run<__nv_bfloat16, 64, 1>(a, s) : run<__nv_bfloat16, 64, 2>(a, s);
+    return rows <= 8 ? run<__nv_bfloat16, 128, 1>(a, s) : run<__nv_bfloat16, 128, 2>(a, s);
   }
-  if (c.D <= 64) return one ? run<float, 64, 1>(a, s) : run<float, 64, 2>(a, s);
-  return one ? run<float, 128, 1>(a, s) : run<float, 128, 2>(a, s);
+  if (c.D <= 64) return rows <= 8 ? run<float, 64, 1>(a, s) : rows <= 16 ? run<float, 64, 2>(a, s) : run<float, 64, 4>(a, s);
+  return rows <= 8 ? run<float, 128, 1>(a, s) : rows <= 16 ? run<float, 128, 2>(a, s) : run<float, 128, 4>(a, s);
 }
 
 }  // namespace kv

@@ -176,7 +176,7 @@ __global__ void __launch_bounds__(TilesCfg<D>::THREADS, 1)
       bar_vempty[VST], bar_grant[NQ], bar_s[NQ], bar_o[NQ], bar_drain;
   __shared__ uint32_t tmem_base_sh;
   __shared__ int abort_sh;
-  __shared__ PlanShared plan;
+  __shared__ PlanShared<1> plan;
   grid_launch_dependents();
   const int warp = warp_id(), lane = lane_id();
   volatile int* abort_flag = &abort_sh;
@@ -200,8 +200,8 @@ __global__ void __launch_bounds__(TilesCfg<D>::THREADS, 1)
     tmem_alloc(&tmem_base_sh, C::TMEM_COLS);
     tmem_relinquish();
   }
-  const Part part = find_part<C::THREADS>(a.g, a.c, a.cu, a.slots, a.B, a.T, reinterpret_cast<int*>(smem), plan,
-                                          blockIdx.x, gridDim.x);
+  Seq seq;
+  const Part part = find_part<C::THREADS, 1>(a.g, a.c, a.cu, a.slots, a.B, a.T, reinterpret_cast<int*>(smem), plan, seq);
   // (the plan's scratch lies in the tiles: its generic accesses before the copies' writes)
   fence_async_shared();
   tc_fence_before();
@@ -219,7 +219,7 @@ __global__ void __launch_bounds__(TilesCfg<D>::THREADS, 1)
     const uint64_t t0 = globaltimer();
     while (!mbar_try_wait(bar, parity) && globaltimer() - t0 < a.limit_ns) {}
   };
-  Walk walk(part);
+  Walk walk(part, seq);
   Seg seg;
   auto next = [&]() { return walk.next(a.g, a.c, a.cu, a.slots, a.T, seg); };
 
@@ -272,7 +272,7 @@ __global__ void __launch_bounds__(TilesCfg<D>::THREADS, 1)
                 mbar_arrive_expect_tx(&bar_q[q], C::NCB * 128u * a.RT);
                 for (int cb = 0; cb < C::NCB; ++cb)
                   tma_load_4d(sQ(q) + cb * C::CB_BYTES, &tmQ, &bar_q[q], cb * 64, 0,
-                              seg.s.row0 + seg.x.rho0 / a.g.rep + q * a.tpt, seg.head);
+                              seg.s.row0 + a.g.rep.of(seg.x.rho0) + q * a.tpt, seg.head);
               }
               __syncwarp();
             }
@@ -439,9 +439,9 @@ __global__ void __launch_bounds__(TilesCfg<D>::THREADS, 1)
       // this tile's rows: rho0 + r, r < rows; row r is token r / rep of the tile
       const int rho0 = seg.x.rho0 + q * a.RT;
       const int rows = max(0, min(a.RT, seg.x.rows - q * a.RT));
-      const int p0 = seg.s.len - seg.s.n + rho0 / a.g.rep;  // position of its first token
-      const int p1 = p0 + max(0, rows - 1) / a.g.rep;
-      const int p = p0 + r_in / a.g.rep;
+      const int p0 = seg.s.len - seg.s.n + a.g.rep.of(rho0);  // position of its first token
+      const int p1 = p0 + a.g.rep.of(max(0, rows - 1));
+      const int p = p0 + a.g.rep.of(r_in);
       const int last = seg.s.len - 1;
       const int hi_i = a.g.causal ? min(p, last) : last;
       const int lo_i = a.g.window > 0 ? p - a.g.window + 1 : 0;
@@ -533,7 +533,8 @@ __global__ void __launch_bounds__(TilesCfg<D>::THREADS, 1)
         if (whole) {
           const float inv = l > 0.f ? 1.f / l : 0.f;
           auto at = [&](int r) {  // row of [T, H] that row r of the tile is
-            return (size_t)(seg.s.row0 + (rho0 + r) / a.g.rep) * a.H + seg.head * a.g.rep + (rho0 + r) % a.g.rep;
+            const int token = a.g.rep.of(rho0 + r);
+            return (size_t)(seg.s.row0 + token) * a.H + seg.head * a.g.rep.d + rho0 + r - token * a.g.rep.d;
           };
           if (r_in < rows) a.LSE[at(r_in)] = l > 0.f ? (m + log2f(l)) * LN2 : -INFINITY;
           const int es = a.out_bf16 ? 2 : 4;
@@ -552,7 +553,7 @@ __global__ void __launch_bounds__(TilesCfg<D>::THREADS, 1)
           if (threadIdx.x == 0)
             a.part.left[2 * blockIdx.x + seg.slot] = {
                 PART_VALID | (seg.starts ? PART_STARTS : 0) | (seg.ends ? PART_ENDS : 0), seg.s.row0, seg.x.rho0,
-                seg.x.rows, seg.head, {0, 0, 0}};
+                seg.x.rows, seg.head, walk.p.ender, {0, 0}};
         }
       }
       if (q < NQ - 1) {
@@ -592,7 +593,7 @@ fa_status run(TilesArgs& a, const CUtensorMap& q, const CUtensorMap& k, const CU
     if (cudaGetLastError() != cudaSuccess) st = FA_ERR_CUDA;
   }
   if (st == FA_OK) {
-    const JoinArgs j = {a.part, a.O, a.LSE, ctas, a.g.R, D, a.H, a.g.rep, a.c.D, a.out_bf16};
+    const JoinArgs j = {a.part, a.O, a.LSE, ctas, 1, a.g.R, D, a.H, a.c.D, a.out_bf16, a.g.rep};
     st = launch_join(j, s);
   }
   if (host::scratch_free(w, s) != cudaSuccess && st == FA_OK) st = FA_ERR_CUDA;
@@ -618,7 +619,7 @@ fa_status launch_attend_tiles(const void* q, void* O, float* LSE, const int* cu,
   a.RT = a.tpt * rep;
   a.box = std::min(c.page_size, BLOCK_N);
   a.boxes = BLOCK_N / a.box;
-  a.g = {rep, 2 * a.RT, BLOCK_N, p.causal, p.window};
+  a.g = {div_by(rep), 2 * a.RT, log2_of(BLOCK_N), 1, 2, p.causal, p.window};
   a.sl2 = p.scale * LOG2E;
   a.out_bf16 = p.out_dtype == FA_BF16;
   a.limit_ns = WAIT_LIMIT_NS;
