@@ -608,6 +608,21 @@ struct Sum {  // sums of exponentials taken against the maximum M
   }
 };
 
+// columns 4 col .. of row r of the item: written from its sums
+__device__ __forceinline__ void join_row(const JoinArgs& a, const Left& f, int r, int col, const Sum& x) {
+  const float inv = x.L > 0.f ? __fdividef(1.f, x.L) : 0.f;
+  const int rho = f.rho0 + r, token = a.rep.of(rho);
+  const size_t at = (size_t)(f.row0 + token) * a.H + f.head * a.rep.d + rho - token * a.rep.d;
+  if (col == 0) a.LSE[at] = x.L > 0.f ? (x.M + __log2f(x.L)) * LN2 : -INFINITY;
+  if (col * 4 >= a.Dv) return;
+  if (a.out_bf16)
+    *reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(a.O) + at * a.Dv + col * 4) =
+        make_uint2(bf2(x.acc.x * inv, x.acc.y * inv), bf2(x.acc.z * inv, x.acc.w * inv));
+  else
+    *reinterpret_cast<float4*>(static_cast<float*>(a.O) + at * a.Dv + col * 4) =
+        make_float4(x.acc.x * inv, x.acc.y * inv, x.acc.z * inv, x.acc.w * inv);
+}
+
 // `where`: the worker of the CTA that left the item open, + 16 if in its slot 1. ALL: by all
 // blocks and warps of the CTA, else by the calling warp.
 template <bool ALL>
@@ -636,6 +651,34 @@ __device__ __forceinline__ void join_item(const JoinArgs& a, int where, int last
   const int p1 = share ? parts * (warp + 1) / JOIN_WARPS : parts;
   const int r_first = ALL && tall ? blockIdx.y * JOIN_WARPS + warp : blockIdx.y;
   const int r_step = ALL && tall ? gridDim.y * JOIN_WARPS : gridDim.y;
+  if (ALL && tall) {
+    // many rows of few parts: ROWS rows of a part at a time
+    constexpr int ROWS = 4;
+    for (int g = r_first * ROWS; g * side < f.rows; g += r_step * ROWS) {
+      Sum x[ROWS];
+#pragma unroll
+      for (int i = 0; i < ROWS; ++i) x[i] = {-FLT_MAX, 0.f, make_float4(0.f, 0.f, 0.f, 0.f)};
+#pragma unroll 2
+      for (int p = 0; p < parts; ++p) {
+        const size_t slot = (size_t)slot_of(p) * a.R;
+        float2 y[ROWS];
+        float4 v[ROWS];
+#pragma unroll
+        for (int i = 0; i < ROWS; ++i) {
+          const size_t row = slot + min((g + i) * side + sub, f.rows - 1);
+          y[i] = a.part.ml[row];
+          v[i] = *reinterpret_cast<const float4*>(a.part.O + row * a.D + col * 4);
+        }
+#pragma unroll
+        for (int i = 0; i < ROWS; ++i)
+          if (y[i].y > 0.f) x[i].add(y[i].x, y[i].y, v[i]);
+      }
+#pragma unroll
+      for (int i = 0; i < ROWS; ++i)
+        if ((g + i) * side + sub < f.rows) join_row(a, f, (g + i) * side + sub, col, x[i]);
+    }
+    return;
+  }
   for (int g = r_first; g * side < f.rows; g += r_step) {
     const int r = g * side + sub;
     Sum x = {-FLT_MAX, 0.f, make_float4(0.f, 0.f, 0.f, 0.f)};
@@ -665,20 +708,7 @@ __device__ __forceinline__ void join_item(const JoinArgs& a, int where, int last
         x.add(ml[w * 32 + lane].x, ml[w * 32 + lane].y, acc_sh[w * 32 + lane]);
       __syncthreads();
     }
-    if (r < f.rows && (!share || warp == 0)) {
-      const float inv = x.L > 0.f ? __fdividef(1.f, x.L) : 0.f;
-      const int rho = f.rho0 + r, token = a.rep.of(rho);
-      const size_t at = (size_t)(f.row0 + token) * a.H + f.head * a.rep.d + rho - token * a.rep.d;
-      if (col == 0) a.LSE[at] = x.L > 0.f ? (x.M + __log2f(x.L)) * LN2 : -INFINITY;
-      if (col * 4 < a.Dv) {
-        if (a.out_bf16)
-          *reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(a.O) + at * a.Dv + col * 4) =
-              make_uint2(bf2(x.acc.x * inv, x.acc.y * inv), bf2(x.acc.z * inv, x.acc.w * inv));
-        else
-          *reinterpret_cast<float4*>(static_cast<float*>(a.O) + at * a.Dv + col * 4) =
-              make_float4(x.acc.x * inv, x.acc.y * inv, x.acc.z * inv, x.acc.w * inv);
-      }
-    }
+    if (r < f.rows && (!share || warp == 0)) join_row(a, f, r, col, x);
   }
 }
 

@@ -114,9 +114,11 @@ __device__ __forceinline__ void store_rows(uint32_t t_addr, bool have, float mul
   const uint32_t lane = lane_id(), sw = lane & 7u;
   const uint32_t row = stage + lane * 128u;
   const int rr = (int)(lane >> 3), ch = (int)(lane & 7u);
+  char* to[8];
 #pragma unroll
-  for (int b = 0; b < D / COLS; ++b) {
-    if (b * COLS >= cols) break;
+  for (int i = 0; i < 8; ++i) to[i] = row_ptr(rr + 4 * i);
+#pragma unroll 1
+  for (int b = 0; b * COLS < cols; ++b) {
     if constexpr (BF) {
       uint32_t r0[32], r1[32];
       if (have) {
@@ -156,8 +158,7 @@ __device__ __forceinline__ void store_rows(uint32_t t_addr, bool have, float mul
     for (int i = 0; i < 8; ++i) {
       const int rl = rr + 4 * i;
       const float4 v = ld_shared_v4(stage + (uint32_t)rl * 128u + (((uint32_t)ch ^ ((uint32_t)rl & 7u)) << 4));
-      char* p = row_ptr(rl);
-      if (p && col < cols) *reinterpret_cast<float4*>(p + col * (BF ? 2 : 4)) = v;
+      if (to[i] && col < cols) *reinterpret_cast<float4*>(to[i] + col * (BF ? 2 : 4)) = v;
     }
     __syncwarp();
   }
@@ -530,31 +531,29 @@ __global__ void __launch_bounds__(TilesCfg<D>::THREADS, 1)
       const bool whole = seg.starts && seg.ends;
       if (ok) {
         const int warp_rows = rows - wq * 32;  // rows of this warp's 32 that exist
-        if (whole) {
-          const float inv = l > 0.f ? 1.f / l : 0.f;
-          auto at = [&](int r) {  // row of [T, H] that row r of the tile is
-            const int token = a.g.rep.of(rho0 + r);
-            return (size_t)(seg.s.row0 + token) * a.H + seg.head * a.g.rep.d + rho0 + r - token * a.g.rep.d;
-          };
-          if (r_in < rows) a.LSE[at(r_in)] = l > 0.f ? (m + log2f(l)) * LN2 : -INFINITY;
-          const int es = a.out_bf16 ? 2 : 4;
-          auto ptr = [&](int r) -> char* {
-            return r < warp_rows ? static_cast<char*>(a.O) + at(wq * 32 + r) * a.c.D * es : nullptr;
-          };
-          if (a.out_bf16) store_rows<D, true>(o_addr, n > 0, inv, stage, a.c.D, ptr);
-          else store_rows<D, false>(o_addr, n > 0, inv, stage, a.c.D, ptr);
-        } else {
-          const size_t row = (size_t)(2 * blockIdx.x + seg.slot) * a.g.R + q * a.RT;
-          if (r_in < rows) a.part.ml[row + r_in] = make_float2(m, l);
-          auto ptr = [&](int r) -> char* {
-            return r < warp_rows ? reinterpret_cast<char*>(a.part.O + (row + wq * 32 + r) * D) : nullptr;
-          };
-          store_rows<D, false>(o_addr, n > 0, 1.f, stage, D, ptr);
-          if (threadIdx.x == 0)
-            a.part.left[2 * blockIdx.x + seg.slot] = {
-                PART_VALID | (seg.starts ? PART_STARTS : 0) | (seg.ends ? PART_ENDS : 0), seg.s.row0, seg.x.rho0,
-                seg.x.rows, seg.head, walk.p.ender, {0, 0}};
+        // rows go to O, or, of a part, to its slot: `at(r)` is row r's place in either
+        const size_t slot_row = (size_t)(2 * blockIdx.x + seg.slot) * a.g.R + q * a.RT;
+        auto at = [&](int r) {
+          if (!whole) return slot_row + r;
+          const int token = a.g.rep.of(rho0 + r);
+          return (size_t)(seg.s.row0 + token) * a.H + seg.head * a.g.rep.d + rho0 + r - token * a.g.rep.d;
+        };
+        char* const to = whole ? static_cast<char*>(a.O) : reinterpret_cast<char*>(a.part.O);
+        const bool bf = whole && a.out_bf16;
+        const int cols = whole ? a.c.D : D;
+        const size_t row_bytes = (size_t)cols * (bf ? 2 : 4);
+        auto ptr = [&](int r) -> char* { return r < warp_rows ? to + at(wq * 32 + r) * row_bytes : nullptr; };
+        const float inv = !whole ? 1.f : l > 0.f ? __fdividef(1.f, l) : 0.f;
+        if (r_in < rows) {
+          if (whole) a.LSE[at(r_in)] = l > 0.f ? (m + __log2f(l)) * LN2 : -INFINITY;
+          else a.part.ml[at(r_in)] = make_float2(m, l);
         }
+        if (bf) store_rows<D, true>(o_addr, n > 0, inv, stage, cols, ptr);
+        else store_rows<D, false>(o_addr, n > 0, inv, stage, cols, ptr);
+        if (!whole && threadIdx.x == 0)
+          a.part.left[2 * blockIdx.x + seg.slot] = {
+              PART_VALID | (seg.starts ? PART_STARTS : 0) | (seg.ends ? PART_ENDS : 0), seg.s.row0, seg.x.rho0,
+              seg.x.rows, seg.head, walk.p.ender, {0, 0}};
       }
       if (q < NQ - 1) {
         if (ok) named_bar_arrive(C::EPI_JOIN, 128 * NQ);
@@ -619,7 +618,7 @@ fa_status launch_attend_tiles(const void* q, void* O, float* LSE, const int* cu,
   a.RT = a.tpt * rep;
   a.box = std::min(c.page_size, BLOCK_N);
   a.boxes = BLOCK_N / a.box;
-  a.g = {div_by(rep), 2 * a.RT, log2_of(BLOCK_N), 1, 2, p.causal, p.window};
+  a.g = {div_by(rep), 2 * a.RT, log2_of(BLOCK_N), 3, 2, p.causal, p.window};
   a.sl2 = p.scale * LOG2E;
   a.out_bf16 = p.out_dtype == FA_BF16;
   a.limit_ns = WAIT_LIMIT_NS;
