@@ -586,10 +586,9 @@ __global__ void __launch_bounds__(NTHREADS, RowsCfg<E, D, NTR>::CTAS_PER_SM)
 // too), those after it the others in their slots 0, up to the one that ends it; a CTA all
 // inside the item left one part for its workers, in the first one's slot. Blocks (c, y) stand
 // for CTA c. At most one of its open items goes on beyond it: the blocks share out its rows,
-// and their warps its parts (of an item of many rows, the rows too). An item that ends in the
-// CTA has few parts: a warp of each block joins them. Lanes are columns. Sums are merged in a fixed
-// order. Most blocks find nothing open and go, so they are small: all of them are on the
-// SMs at once.
+// and their warps its parts. An item that ends in the CTA has few parts: a warp of each block
+// joins them. Lanes are columns. Sums are merged in a fixed order. Most blocks find nothing
+// open and go.
 constexpr int JOIN_WARPS = 4;
 constexpr int JOIN_THREADS = 32 * JOIN_WARPS;
 
@@ -645,41 +644,9 @@ __device__ __forceinline__ void join_item(const JoinArgs& a, int where, int last
   };
   const int cols = a.D / 4, side = 32 / cols;  // lanes of a row; rows of a warp
   const int col = lane % cols, sub = lane / cols;
-  const bool tall = f.rows >= 64;              // warps take rows; else shares of the parts
-  const bool share = ALL && !tall;
-  const int p0 = share ? parts * warp / JOIN_WARPS : 0;
-  const int p1 = share ? parts * (warp + 1) / JOIN_WARPS : parts;
-  const int r_first = ALL && tall ? blockIdx.y * JOIN_WARPS + warp : blockIdx.y;
-  const int r_step = ALL && tall ? gridDim.y * JOIN_WARPS : gridDim.y;
-  if (ALL && tall) {
-    // many rows of few parts: ROWS rows of a part at a time
-    constexpr int ROWS = 4;
-    for (int g = r_first * ROWS; g * side < f.rows; g += r_step * ROWS) {
-      Sum x[ROWS];
-#pragma unroll
-      for (int i = 0; i < ROWS; ++i) x[i] = {-FLT_MAX, 0.f, make_float4(0.f, 0.f, 0.f, 0.f)};
-#pragma unroll 2
-      for (int p = 0; p < parts; ++p) {
-        const size_t slot = (size_t)slot_of(p) * a.R;
-        float2 y[ROWS];
-        float4 v[ROWS];
-#pragma unroll
-        for (int i = 0; i < ROWS; ++i) {
-          const size_t row = slot + min((g + i) * side + sub, f.rows - 1);
-          y[i] = a.part.ml[row];
-          v[i] = *reinterpret_cast<const float4*>(a.part.O + row * a.D + col * 4);
-        }
-#pragma unroll
-        for (int i = 0; i < ROWS; ++i)
-          if (y[i].y > 0.f) x[i].add(y[i].x, y[i].y, v[i]);
-      }
-#pragma unroll
-      for (int i = 0; i < ROWS; ++i)
-        if ((g + i) * side + sub < f.rows) join_row(a, f, (g + i) * side + sub, col, x[i]);
-    }
-    return;
-  }
-  for (int g = r_first; g * side < f.rows; g += r_step) {
+  const int p0 = ALL ? parts * warp / JOIN_WARPS : 0;
+  const int p1 = ALL ? parts * (warp + 1) / JOIN_WARPS : parts;
+  for (int g = blockIdx.y; g * side < f.rows; g += gridDim.y) {
     const int r = g * side + sub;
     Sum x = {-FLT_MAX, 0.f, make_float4(0.f, 0.f, 0.f, 0.f)};
     if (r < f.rows) {
@@ -700,7 +667,7 @@ __device__ __forceinline__ void join_item(const JoinArgs& a, int where, int last
           if (p + u < p1 && y[u].y > 0.f) x.add(y[u].x, y[u].y, v[u]);
       }
     }
-    if (share) {
+    if (ALL) {
       ml[threadIdx.x] = make_float2(x.M, x.L);
       acc_sh[threadIdx.x] = x.acc;
       __syncthreads();
@@ -708,7 +675,7 @@ __device__ __forceinline__ void join_item(const JoinArgs& a, int where, int last
         x.add(ml[w * 32 + lane].x, ml[w * 32 + lane].y, acc_sh[w * 32 + lane]);
       __syncthreads();
     }
-    if (r < f.rows && (!share || warp == 0)) join_row(a, f, r, col, x);
+    if (r < f.rows && (!ALL || warp == 0)) join_row(a, f, r, col, x);
   }
 }
 
@@ -732,6 +699,109 @@ __global__ void __launch_bounds__(JOIN_THREADS, 5) attend_join_kernel(const __gr
   if (far) join_item<true>(a, __ffs(far) - 1, last_worker, warp, lane);
   const unsigned me = near_by & (0x10001u << warp);
   if (warp < a.per && me) join_item<false>(a, __ffs(me) - 1, last_worker, warp, lane);
+}
+
+// The same where a CTA is a worker and items are tall: at most an open item per CTA, few of
+// them with many parts or many with few. Every block lists the open items (they are few
+// enough to look at all of them), and the rows of all items together are shared out evenly
+// among the warps of the grid, a run of rows each: four rows at a time with two parts of
+// each on the way, or, where there are no more rows than warps, one row with eight parts.
+constexpr int TALL_CTAS = 256;  // SMs at most (every sm_103 part has fewer)
+constexpr int TALL_WARPS = 8;
+constexpr int TALL_BLOCKS = 2;  // per SM
+template <int ROWS, int U>
+__device__ __forceinline__ void join_rows(const JoinArgs& a, const Left* open, const int* first, int n, int lane) {
+  const int cols = a.D / 4, side = 32 / cols;
+  const int col = lane % cols, sub = lane / cols;
+  const int warps = gridDim.x * TALL_WARPS, run = (first[n] + warps - 1) / warps;
+  int at = (blockIdx.x * TALL_WARPS + (threadIdx.x >> 5)) * run;
+  const int end = min(first[n], at + run);
+  while (at < end) {
+    int lo = 0, hi = n;  // the item of row `at`
+    while (hi - lo > 1) {
+      const int mid = (lo + hi) / 2;
+      if (first[mid] <= at) lo = mid; else hi = mid;
+    }
+    const Left f = open[lo];
+    const int c0 = f.pad[0], parts = f.ender - c0 + 1;
+    const int r_end = min(end, first[lo + 1]) - first[lo];
+    for (int r = at - first[lo]; r < r_end; r += ROWS * side) {
+      Sum x[ROWS];
+#pragma unroll
+      for (int i = 0; i < ROWS; ++i) x[i] = {-FLT_MAX, 0.f, make_float4(0.f, 0.f, 0.f, 0.f)};
+      for (int p = 0; p < parts; p += U) {
+        float2 y[U][ROWS];
+        float4 v[U][ROWS];
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+          // (past the last part: that part again, not counted)
+          const size_t slot = p + u == 0 ? f.pad[1] : 2 * (c0 + min(p + u, parts - 1));
+#pragma unroll
+          for (int i = 0; i < ROWS; ++i) {
+            const size_t row = slot * a.R + min(r + i * side + sub, r_end - 1);
+            y[u][i] = a.part.ml[row];
+            v[u][i] = *reinterpret_cast<const float4*>(a.part.O + row * a.D + col * 4);
+          }
+        }
+#pragma unroll
+        for (int u = 0; u < U; ++u)
+#pragma unroll
+          for (int i = 0; i < ROWS; ++i)
+            if (p + u < parts && y[u][i].y > 0.f) x[i].add(y[u][i].x, y[u][i].y, v[u][i]);
+      }
+#pragma unroll
+      for (int i = 0; i < ROWS; ++i)
+        if (r + i * side + sub < r_end) join_row(a, f, r + i * side + sub, col, x[i]);
+    }
+    at = first[lo] + r_end;
+  }
+}
+
+__global__ void __launch_bounds__(32 * TALL_WARPS, TALL_BLOCKS) attend_join_tall_kernel(const __grid_constant__ JoinArgs a) {
+  ptx::grid_dependency_wait();
+  __shared__ Left open[TALL_CTAS];
+  __shared__ int first[TALL_CTAS + 1];
+  __shared__ int2 sums[TALL_WARPS];
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  int n = 0, rows = 0;  // open items and their rows so far
+  for (int c0 = 0; c0 < a.ctas; c0 += 32 * TALL_WARPS) {
+    const int c = c0 + tid;
+    Left f = {};
+    if (c < a.ctas) {
+      const Left f0 = a.part.left[2 * c], f1 = a.part.left[2 * c + 1];
+      constexpr int OPEN = PART_STARTS | PART_ENDS;
+      const bool second = (f1.flags & OPEN) == PART_STARTS;
+      f = second ? f1 : f0;
+      if ((f.flags & OPEN) != PART_STARTS) f.rows = 0;
+      f.pad[0] = c;
+      f.pad[1] = 2 * c + second;
+    }
+    const int is = f.rows > 0;
+    int k = is, r = f.rows;
+#pragma unroll
+    for (int d = 1; d < 32; d <<= 1) {
+      const int u = __shfl_up_sync(0xffffffffu, k, d), v = __shfl_up_sync(0xffffffffu, r, d);
+      if (lane >= d) { k += u; r += v; }
+    }
+    if (lane == 31) sums[warp] = make_int2(k, r);
+    __syncthreads();
+    int2 before = make_int2(n, rows);
+    for (int w = 0; w < TALL_WARPS; ++w) {
+      if (w < warp) { before.x += sums[w].x; before.y += sums[w].y; }
+      n += sums[w].x;
+      rows += sums[w].y;
+    }
+    if (is) {
+      open[before.x + k - is] = f;
+      first[before.x + k - is] = before.y + r - f.rows;
+    }
+    __syncthreads();
+  }
+  if (tid == 0) first[n] = rows;
+  __syncthreads();
+  if (n == 0) return;
+  if (rows > 2 * (int)gridDim.x * TALL_WARPS) join_rows<4, 2>(a, open, first, n, lane);
+  else join_rows<1, 8>(a, open, first, n, lane);
 }
 
 template <typename E, int D, int NTR>
@@ -766,7 +836,15 @@ fa_status run(RowsArgs& a, cudaStream_t s) {
 
 fa_status launch_join(const JoinArgs& a, cudaStream_t s) {
   host::KernelTimer t("attend_join", s);
-  return launch_programmatic(attend_join_kernel, dim3(a.ctas, a.per > 1 ? a.R / 2 : 16), dim3(JOIN_THREADS), s, a) == cudaSuccess ? FA_OK : FA_ERR_CUDA;
+  return launch_programmatic(attend_join_kernel, dim3(a.ctas, a.R / 2), dim3(JOIN_THREADS), s, a) == cudaSuccess
+             ? FA_OK : FA_ERR_CUDA;
+}
+
+fa_status launch_join_tall(const JoinArgs& a, cudaStream_t s) {
+  if (a.ctas > TALL_CTAS) return FA_ERR_UNSUPPORTED;
+  host::KernelTimer t("attend_join", s);
+  return launch_programmatic(attend_join_tall_kernel, dim3(TALL_BLOCKS * host::sm_count()), dim3(32 * TALL_WARPS), s, a) == cudaSuccess
+             ? FA_OK : FA_ERR_CUDA;
 }
 
 fa_status launch_attend_rows(const void* q, void* O, float* LSE, const int* cu, const int* slots,

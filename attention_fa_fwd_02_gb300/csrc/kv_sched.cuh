@@ -161,8 +161,8 @@ __device__ __forceinline__ Cut cut_in(const Geo& g, const Cuts& cuts, int HKV, i
 // The part of the caller's warp, worker PER * blockIdx.x + w (PER == 1: every warp gets the
 // CTA's part), and its first sequence, found by a block of NT threads. `first`: shared
 // scratch of B + 1 ints (used within the call only). All of it is latency, before the first
-// key is asked for: up to 128 sequences of a few tiles each, as in decoding, a warp finds
-// its part by itself without meeting the others (one sequence: 3000 clocks instead of 6400
+// key is asked for: up to 128 sequences of a few tiles each, as in decoding, or 32 of many, a
+// warp finds its part by itself without meeting the others (one sequence: 3000 clocks instead of 6400
 // by the block; 64: 5800 instead of 6900).
 template <int NT, int PER>
 __device__ __forceinline__ Part find_part(const Geo& g, const fakv_cache& c, const int* cu,
@@ -179,22 +179,57 @@ __device__ __forceinline__ Part find_part(const Geo& g, const fakv_cache& c, con
   Cut cut;
   const int per_lane = (B + 31) / 32;
   bool alone = per_lane <= ALONE / 32;
-  int n = 0;           // tiles of the lane's sequences
-  long long mine = 0;  // and their weight
+  int n = 0;                // tiles of the lane's sequences
+  long long mine = 0;       // a lane's weight
+  int lane_b = lane * per_lane, lane_t = 0;  // the sequence and the tile of it that a lane begins with
   if (alone) {
     bool many = false;
 #pragma unroll 1
     for (int i = 0; i < per_lane; ++i) {
       const int at = lane * per_lane + i;
       if (at >= B) break;
-      const Seq q = load_seq(c, cu, slots, at, T);
-      const int tiles = tiles_of(g, q.n);
+      s = load_seq(c, cu, slots, at, T);
+      const int tiles = tiles_of(g, s.n);
       n += tiles;
       many |= tiles > FEW;
 #pragma unroll 1
-      for (int t = 0; t < tiles && !many; ++t) mine += max(1, tile_of(g, q, t).units) + g.start;
+      for (int t = 0; t < tiles && !many; ++t) mine += max(1, tile_of(g, s, t).units) + g.start;
     }
-    alone = !__any_sync(0xffffffffu, many);
+    many = __any_sync(0xffffffffu, many);
+    alone = !many || per_lane == 1;
+    if (alone && many) {
+      // few sequences of many tiles: the tiles shared out evenly instead
+      int t_end = n;
+#pragma unroll
+      for (int d = 1; d < 32; d <<= 1) {
+        const int u = __shfl_up_sync(0xffffffffu, t_end, d);
+        if (lane >= d) t_end += u;
+      }
+      const int tiles = __shfl_sync(0xffffffffu, t_end, 31), q = (tiles + 31) / 32;
+      int t = lane * q, at = 0;  // a tile, its sequence
+      for (int k = 0; k < B; ++k) at += __shfl_sync(0xffffffffu, t_end, k) <= t;
+      lane_b = at;
+      lane_t = t - __shfl_sync(0xffffffffu, t_end - n, min(at, 31));
+      mine = 0;
+#pragma unroll 1
+      for (int i = 0; i < q; ++i, ++t) {
+        for (int k = 0; k <= B; ++k) {  // (every lane takes part in every exchange)
+          const int end = __shfl_sync(0xffffffffu, t_end, min(at, 31));
+          const bool on = t < tiles && end <= t;
+          at += on;
+          if (!__any_sync(0xffffffffu, on)) break;
+        }
+        const int from = min(at, 31);
+        Seq o;
+        o.slot = 0;
+        o.len = __shfl_sync(0xffffffffu, s.len, from);
+        o.row0 = 0;
+        o.n = __shfl_sync(0xffffffffu, s.n, from);
+        const int t_first = __shfl_sync(0xffffffffu, t_end - n, from);
+        if (t < tiles) mine += max(1, tile_of(g, o, t - t_first).units) + g.start;
+      }
+      n = max(0, min(q, tiles - lane * q));  // tiles of the lane
+    }
   }
   if (alone) {
     mine *= c.HKV;
@@ -209,16 +244,18 @@ __device__ __forceinline__ Part find_part(const Geo& g, const fakv_cache& c, con
     const Cuts cuts(__shfl_sync(0xffffffffu, w_end, 31), most);
     const int tiles = __shfl_sync(0xffffffffu, t_end, 31);
     const long long x = cuts.at(worker);
-    // the lane whose sequences each cut falls into: how many end at or before it
+    // the lane whose tiles each cut falls into: how many end at or before it
     const long long x0 = __shfl_sync(0xffffffffu, x, 0), x1 = __shfl_sync(0xffffffffu, x, 1);
     const int l0 = __popc(__ballot_sync(0xffffffffu, w_end <= x0)), l1 = __popc(__ballot_sync(0xffffffffu, w_end <= x1));
     const int from = min(31, lane > 0 ? l1 : l0);
     long long at = __shfl_sync(0xffffffffu, w_end - mine, from);
-    f = __shfl_sync(0xffffffffu, t_end - n, from);
+    int t = __shfl_sync(0xffffffffu, lane_t, from);  // tile of sequence b
+    f = __shfl_sync(0xffffffffu, t_end - n, from) - t;
+    b = __shfl_sync(0xffffffffu, lane_b, from);
     cut = {tiles, 0, 0, 0};
     if (x < cuts.total) {
-      int t = 0, of = 0;  // tile and tiles of sequence b
-      b = from * per_lane - 1;
+      s = load_seq(c, cu, slots, b, T);
+      int of = tiles_of(g, s.n);
 #pragma unroll 1
       for (;; ++t) {
         while (t >= of) {
@@ -237,6 +274,7 @@ __device__ __forceinline__ Part find_part(const Geo& g, const fakv_cache& c, con
       }
     } else {
       f = tiles;
+      b = B;
     }
   } else {
     // tiles of the sequences before each
@@ -414,7 +452,8 @@ struct JoinArgs {
   int H, Dv, out_bf16;
   Div rep;
 };
-fa_status launch_join(const JoinArgs& a, cudaStream_t s);
+fa_status launch_join(const JoinArgs& a, cudaStream_t s);        // several workers to a CTA
+fa_status launch_join_tall(const JoinArgs& a, cudaStream_t s);   // a CTA is a worker; many rows
 
 }  // namespace kv
 }  // namespace fa

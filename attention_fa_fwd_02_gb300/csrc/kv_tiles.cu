@@ -593,7 +593,7 @@ fa_status run(TilesArgs& a, const CUtensorMap& q, const CUtensorMap& k, const CU
   }
   if (st == FA_OK) {
     const JoinArgs j = {a.part, a.O, a.LSE, ctas, 1, a.g.R, D, a.H, a.c.D, a.out_bf16, a.g.rep};
-    st = launch_join(j, s);
+    st = launch_join_tall(j, s);
   }
   if (host::scratch_free(w, s) != cudaSuccess && st == FA_OK) st = FA_ERR_CUDA;
   return st;
