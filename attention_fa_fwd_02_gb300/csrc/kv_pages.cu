@@ -14,6 +14,7 @@ namespace {
 
 constexpr int PLAN = 1024;   // threads of a planning block
 constexpr int SCAN = 4;      // reference counts per thread and step
+constexpr int BRIEF = 256;   // entries of a list compared with one another
 
 // Sums saturate: no list can be served more than 2^28 pages, and beyond them only "too
 // many" matters.
@@ -123,7 +124,7 @@ struct GrowArgs {
   const int* slots;
   const int* add;
   int n, shift;
-  int* mark;   // scratch [max_slots]: first place of a slot in the list
+  int* mark;   // scratch [max_slots]: first place of a slot in the list (lists above BRIEF)
   int* fresh;  // scratch [num_pages]: the free pages, in order
   int2* pair;  // scratch [n]: pages to copy
   int* count;  // scratch: how many
@@ -141,14 +142,21 @@ __global__ void __launch_bounds__(PLAN) grow_kernel(const __grid_constant__ Grow
   __shared__ int from_sh;
   ptx::grid_launch_dependents();
   const int tid = threadIdx.x;
-  for (int i = tid; i < a.n; i += PLAN) {
-    const int s = a.slots[i];
-    if ((unsigned)s < (unsigned)a.c.max_slots) a.mark[s] = a.n;
-  }
-  __syncthreads();
-  for (int i = tid; i < a.n; i += PLAN) {
-    const int s = a.slots[i];
-    if ((unsigned)s < (unsigned)a.c.max_slots) atomicMin(&a.mark[s], i);
+  // Which entry of a slot is the first: short lists are compared in shared memory (three round
+  // trips to memory less), long ones mark their slots.
+  const bool brief = a.n <= BRIEF;
+  if (brief) {
+    if (tid < a.n) slot_of[tid] = a.slots[tid];
+  } else {
+    for (int i = tid; i < a.n; i += PLAN) {
+      const int s = a.slots[i];
+      if ((unsigned)s < (unsigned)a.c.max_slots) a.mark[s] = a.n;
+    }
+    __syncthreads();
+    for (int i = tid; i < a.n; i += PLAN) {
+      const int s = a.slots[i];
+      if ((unsigned)s < (unsigned)a.c.max_slots) atomicMin(&a.mark[s], i);
+    }
   }
   __syncthreads();
   int copies = 0;         // copies listed so far
@@ -159,9 +167,20 @@ __global__ void __launch_bounds__(PLAN) grow_kernel(const __grid_constant__ Grow
     int slot = -1, len = 0, add = 0, old = 0, tail = -1;
     unsigned need = 0;
     if (i < a.n) {
-      slot = a.slots[i];
-      if ((unsigned)slot >= (unsigned)a.c.max_slots) { raise(a.c.status, FAKV_BAD_SLOT); slot = -1; }
-      else if (a.mark[slot] != i) { raise(a.c.status, FAKV_REPEATED); slot = -1; }
+      slot = brief ? slot_of[i] : a.slots[i];
+      bool again = false;
+      if ((unsigned)slot >= (unsigned)a.c.max_slots) {
+        raise(a.c.status, FAKV_BAD_SLOT);
+        slot = -1;
+      } else if (brief) {
+        for (int j = 0; j < i; ++j) again |= slot_of[j] == slot;
+      } else {
+        again = a.mark[slot] != i;
+      }
+      if (again) {
+        raise(a.c.status, FAKV_REPEATED);
+        slot = -1;
+      }
     }
     if (slot >= 0) {
       len = length_of(a.c, slot);
@@ -348,35 +367,57 @@ struct CompactArgs {
 __global__ void __launch_bounds__(PLAN) compact_plan_kernel(const __grid_constant__ CompactArgs a) {
   ptx::grid_launch_dependents();
   const int tid = threadIdx.x, N = a.c.num_pages;
-  unsigned live = 0;
-  for (int at = tid; at < N; at += PLAN) live += a.c.refs[at] > 0;
-  unsigned L_;
-  block_scan(live, &L_);
-  const int L = (int)L_;
-  int holes = 0, movers = 0;  // ranked so far (equal in the end)
-  for (int at = 0; at < N; at += PLAN * SCAN) {
-    int h = 0, m = 0;
-    bool used[SCAN];
+  int movers = 0;
+  const int per = (N + PLAN - 1) / PLAN;
+  if (per <= 64) {
+    // a run of pages per thread, read once: which of them are used, as bits
+    const int p0 = min(N, tid * per), n = min(N, p0 + per) - p0;
+    unsigned long long used = 0;
+#pragma unroll 8
+    for (int k = 0; k < n; ++k) used |= (unsigned long long)(a.c.refs[p0 + k] > 0) << k;
+    unsigned L_;
+    block_scan((unsigned)__popcll(used), &L_);
+    const int low = max(0, min((int)L_ - p0, n));  // pages of the run below L
+    const unsigned long long below = low == 64 ? ~0ull : (1ull << low) - 1;
+    unsigned long long hole = ~used & below, mover = used & ~below;
+    unsigned moves;
+    for (int i = (int)block_scan((unsigned)__popcll(hole), &moves); hole; hole &= hole - 1)
+      a.pair[i++].y = p0 + __ffsll((long long)hole) - 1;
+    for (int i = (int)block_scan((unsigned)__popcll(mover), &moves); mover; mover &= mover - 1)
+      a.pair[i++].x = p0 + __ffsll((long long)mover) - 1;
+    for (int k = 0; k < n; ++k) a.to[p0 + k] = p0 + k;
+    movers = (int)moves;
+  } else {
+    unsigned live = 0;
+    for (int at = tid; at < N; at += PLAN) live += a.c.refs[at] > 0;
+    unsigned L_;
+    block_scan(live, &L_);
+    const int L = (int)L_;
+    int holes = 0;  // ranked so far (as many as movers in the end)
+    for (int at = 0; at < N; at += PLAN * SCAN) {
+      int h = 0, m = 0;
+      bool used[SCAN];
 #pragma unroll
-    for (int k = 0; k < SCAN; ++k) {
-      const int p = at + tid * SCAN + k;
-      used[k] = p < N && a.c.refs[p] > 0;
-      if (p < N) { h += p < L && !used[k]; m += p >= L && used[k]; }
-    }
-    // at most PLAN * SCAN of each in a step: both fit one word
-    unsigned both;
-    const unsigned r = block_scan((unsigned)(h | (m << 16)), &both);
-    int rh = holes + (int)(r & 0xffff), rm = movers + (int)(r >> 16);
+      for (int k = 0; k < SCAN; ++k) {
+        const int p = at + tid * SCAN + k;
+        used[k] = p < N && a.c.refs[p] > 0;
+        if (p < N) { h += p < L && !used[k]; m += p >= L && used[k]; }
+      }
+      // at most PLAN * SCAN of each in a step: both fit one word
+      unsigned both;
+      const unsigned r = block_scan((unsigned)(h | (m << 16)), &both);
+      int rh = holes + (int)(r & 0xffff), rm = movers + (int)(r >> 16);
 #pragma unroll
-    for (int k = 0; k < SCAN; ++k) {
-      const int p = at + tid * SCAN + k;
-      if (p >= N) break;
-      if (p < L && !used[k]) a.pair[rh++].y = p;
-      if (p >= L && used[k]) a.pair[rm++].x = p;
-      a.to[p] = p;
+      for (int k = 0; k < SCAN; ++k) {
+        const int p = at + tid * SCAN + k;
+        if (p >= N) break;
+        if (p < L && !used[k]) a.pair[rh++].y = p;
+        if (p >= L && used[k]) a.pair[rm++].x = p;
+        a.to[p] = p;
+      }
+      holes += (int)(both & 0xffff);
+      movers += (int)(both >> 16);
     }
-    holes += (int)(both & 0xffff);
-    movers += (int)(both >> 16);
   }
   __syncthreads();
   for (int i = tid; i < movers; i += PLAN) {

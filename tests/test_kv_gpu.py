@@ -344,10 +344,10 @@ def test_fork_exchanges_slots(kv):
 
 
 def test_compact_of_full_empty_and_large_caches(kv):
-    for pages, gone in ((1, 0.0), (37, 1.0), (64, 0.0), (9001, 0.4)):
+    for pages, gone in ((1, 0.0), (37, 1.0), (64, 0.0), (9001, 0.4), (65536, 0.5), (70001, 0.3)):
         g = torch.Generator().manual_seed(pages)
         used = (torch.rand(pages, generator=g) >= gone).int()
-        k = torch.arange(pages * 8 * 16).float().reshape(1, pages, 8, 1, 16).cuda()
+        k = torch.arange(pages * 8 * 16, device="cuda").float().reshape(1, pages, 8, 1, 16)
         live = torch.nonzero(used)[:, 0].int()
         live = live[torch.randperm(len(live), generator=g)]
         table = torch.full((2, pages + 1), -1, dtype=torch.int32)
