@@ -187,7 +187,7 @@ FA_API fa_status fakv_attend(const void* q, void* O, float* LSE, const int* cu, 
   st = check_tokens(cache, p, cu, slots);
   if (st != FA_OK) return st;
   if (p->H < 1 || !dtype_ok(p->out_dtype)) return FA_ERR_INVALID_ARG;
-  if (!(std::isfinite(p->scale) && p->scale > 0.f)) return FA_ERR_INVALID_ARG;
+  if (!(p->scale > 0.f && std::isfinite(p->scale * LOG2E))) return FA_ERR_INVALID_ARG;
   if ((p->causal != 0 && p->causal != 1) || p->window < 0) return FA_ERR_INVALID_ARG;
   if (p->B == 0 || p->T == 0) return FA_OK;
   for (const void* x : {q, (const void*)O, (const void*)LSE}) {
@@ -223,6 +223,7 @@ FA_API fa_status fakv_fork(const fakv_cache* cache, const int* src, const int* d
   const fa_status st = check_pages(cache);
   if (st != FA_OK) return st;
   if (n < 0 || n > MAX_SEQS) return FA_ERR_INVALID_ARG;
+  if ((long long)n * cache->max_pages > (1ll << 31)) return FA_ERR_INVALID_ARG;  // rows held meanwhile
   if (n == 0) return FA_OK;
   if (!src || !dst) return FA_ERR_INVALID_ARG;
   if (!aligned(src, 4) || !aligned(dst, 4)) return FA_ERR_ALIGNMENT;

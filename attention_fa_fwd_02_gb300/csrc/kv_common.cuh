@@ -27,7 +27,8 @@ struct Seq {
   int slot;   // -1: none
   int len;    // tokens, the new ones included
   int row0;   // first row of q
-  int n;      // new tokens
+  int n;      // new tokens; -1: cu decreases here (then sequences may overlap: no work is
+              // planned from such a cu, as its tiles could number more than an int holds)
 };
 
 __device__ __forceinline__ Seq load_seq(const fakv_cache& c, const int* cu, const int* slots, int b,
@@ -39,9 +40,10 @@ __device__ __forceinline__ Seq load_seq(const fakv_cache& c, const int* cu, cons
   const bool len_ok = len >= 0 && (long long)len <= (long long)c.max_pages * c.page_size;
   Seq s;
   s.row0 = max(0, min(r0, T));
-  s.n = max(0, min(r1, T) - s.row0);
+  s.n = r1 < r0 ? -1 : max(0, min(r1, T) - s.row0);
   s.slot = ok ? slot : -1;
   s.len = ok && len_ok ? len : 0;
+  if (s.n < 0) raise(c.status, FAKV_BAD_LENGTH);
   if (s.n > 0 && !(ok && len_ok)) raise(c.status, ok ? FAKV_BAD_LENGTH : FAKV_BAD_SLOT);
   return s;
 }
@@ -71,6 +73,13 @@ inline bool allow_smem(K* kernel, int bytes, std::atomic<uint64_t>& done) {
   if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes) != cudaSuccess) return false;
   done.fetch_or(bit, std::memory_order_release);
   return true;
+}
+
+// An allocation failed: the runtime's record of it is cleared, so that the next call's check
+// of its launches does not find it.
+inline fa_status failed() {
+  (void)cudaGetLastError();
+  return FA_ERR_CUDA;
 }
 
 inline int esize(fa_dtype t) { return t == FA_BF16 ? 2 : 4; }

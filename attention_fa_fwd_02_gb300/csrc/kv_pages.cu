@@ -67,7 +67,7 @@ __device__ __forceinline__ int length_of(const fakv_cache& c, int slot) {
 struct CopyArgs {
   char* base[2];           // K, V
   long long plane_bytes, page_bytes;  // strides
-  int planes, chunk, chunks;          // `chunk` bytes per block step, `chunks` to a page
+  int planes, chunks;                 // block steps of COPY_CHUNK bytes to a page
   int bytes;                          // of a page
 };
 
@@ -108,7 +108,6 @@ CopyArgs copy_args(const fakv_cache& c) {
   a.page_bytes = c.page_stride * es;
   a.planes = c.planes;
   a.bytes = (int)((long long)c.page_size * c.HKV * c.D * es);
-  a.chunk = COPY_CHUNK;
   a.chunks = (a.bytes + COPY_CHUNK - 1) / COPY_CHUNK;
   return a;
 }
@@ -466,7 +465,7 @@ fa_status done() { return cudaGetLastError() == cudaSuccess ? FA_OK : FA_ERR_CUD
 fa_status launch_grow(const fakv_cache& c, const int* slots, const int* add, int n, cudaStream_t s) {
   const size_t pair = 16, fresh = pair + (size_t)n * 8, mark = fresh + (size_t)c.num_pages * 4;
   Scratch w(mark + (size_t)c.max_slots * 4, s);
-  if (!w.ok) return FA_ERR_CUDA;
+  if (!w.ok) return failed();
   GrowArgs a = {c, slots, add, n, log2_of(c.page_size), reinterpret_cast<int*>(w.p + mark),
                 reinterpret_cast<int*>(w.p + fresh), reinterpret_cast<int2*>(w.p + pair),
                 reinterpret_cast<int*>(w.p)};
@@ -485,7 +484,7 @@ fa_status launch_grow(const fakv_cache& c, const int* slots, const int* add, int
 fa_status launch_fork(const fakv_cache& c, const int* src, const int* dst, int n, cudaStream_t s) {
   const size_t rows = (size_t)n * c.max_pages * 4;
   Scratch w(rows + (size_t)n * 4, s);
-  if (!w.ok) return FA_ERR_CUDA;
+  if (!w.ok) return failed();
   ListArgs a = {c, src, dst, nullptr, n, log2_of(c.page_size), reinterpret_cast<int*>(w.p),
                 reinterpret_cast<int*>(w.p + rows)};
   const int grid = n < 8 * host::sm_count() ? n : 8 * host::sm_count();
@@ -508,7 +507,7 @@ fa_status launch_free(const fakv_cache& c, const int* slots, const int* keep, in
 
 fa_status launch_compact(const fakv_cache& c, cudaStream_t s) {
   Scratch w((size_t)c.num_pages * 12 + 16, s);
-  if (!w.ok) return FA_ERR_CUDA;
+  if (!w.ok) return failed();
   CompactArgs a = {c, copy_args(c), log2_of(c.page_size), reinterpret_cast<int*>(w.p + (size_t)c.num_pages * 8),
                    reinterpret_cast<int2*>(w.p), reinterpret_cast<int*>(w.p + (size_t)c.num_pages * 12)};
   {

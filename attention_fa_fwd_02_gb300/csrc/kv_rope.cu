@@ -179,7 +179,7 @@ __global__ void __launch_bounds__(MAX_THREADS, 2) rope_kernel(const __grid_const
       if (b >= 0) {
         const Seq s = load_seq(a.c, a.cu, a.slots, b, a.T);
         pos = (long long)s.len - s.n + (t - s.row0);
-        if (s.slot >= 0 && pos >= 0) {
+        if (s.slot >= 0 && pos >= 0 && pos < s.len) {
           const int page = page_of(a.c, s.slot, (int)pos, a.shift);
           if (page >= 0)
             at = a.plane * a.c.plane_stride + page * a.c.page_stride +

@@ -186,7 +186,7 @@ __device__ __forceinline__ void finish(const RowsArgs& a, const Finish& f, const
     }
   }
   if (!whole && i == 0)
-    a.part.left[f.slot] = {PART_VALID | f.flags, f.row0, f.rho0, f.rows, f.head, f.ender, {0, 0}};
+    a.part.left[f.slot] = {f.flags, f.row0, f.rho0, f.rows, f.head, f.ender, {0, 0}};
 }
 
 template <typename E, int D, int NTR>
@@ -706,7 +706,6 @@ __global__ void __launch_bounds__(JOIN_THREADS, 5) attend_join_kernel(const __gr
 // enough to look at all of them), and the rows of all items together are shared out evenly
 // among the warps of the grid, a run of rows each: four rows at a time with two parts of
 // each on the way, or, where there are no more rows than warps, one row with eight parts.
-constexpr int TALL_CTAS = 256;  // SMs at most (every sm_103 part has fewer)
 constexpr int TALL_WARPS = 8;
 constexpr int TALL_BLOCKS = 2;  // per SM
 template <int ROWS, int U>
@@ -812,7 +811,7 @@ fa_status run(RowsArgs& a, cudaStream_t s) {
   if (!allow_smem(kernel, C::SMEM, done)) return FA_ERR_CUDA;
   const int ctas = host::sm_count() * C::CTAS_PER_SM;
   void* w = nullptr;
-  if (host::scratch_alloc(&w, partials_bytes(ctas * WARPS, C::R, D), s) != cudaSuccess) return FA_ERR_CUDA;
+  if (host::scratch_alloc(&w, partials_bytes(ctas * WARPS, C::R, D), s) != cudaSuccess) return failed();
   a.part = partials_at(w, ctas * WARPS, C::R, D);
   a.g.R = C::R;
   a.g.u_shift = log2_of(C::GROUP);
@@ -841,7 +840,6 @@ fa_status launch_join(const JoinArgs& a, cudaStream_t s) {
 }
 
 fa_status launch_join_tall(const JoinArgs& a, cudaStream_t s) {
-  if (a.ctas > TALL_CTAS) return FA_ERR_UNSUPPORTED;
   host::KernelTimer t("attend_join", s);
   return launch_programmatic(attend_join_tall_kernel, dim3(TALL_BLOCKS * host::sm_count()), dim3(32 * TALL_WARPS), s, a) == cudaSuccess
              ? FA_OK : FA_ERR_CUDA;

@@ -62,7 +62,7 @@ __device__ __forceinline__ Tile tile_of(const Geo& g, const Seq& s, int t) {
 }
 
 // tiles of a sequence of n new tokens (a division: R is no power of two)
-__device__ __forceinline__ int tiles_of(const Geo& g, int n) { return (n * g.rep.d + g.R - 1) / g.R; }
+__device__ __forceinline__ int tiles_of(const Geo& g, int n) { return (max(0, n) * g.rep.d + g.R - 1) / g.R; }
 
 // Exclusive prefix sums of two values over the block (NT threads), and their totals.
 template <int NT>
@@ -182,6 +182,7 @@ __device__ __forceinline__ Part find_part(const Geo& g, const fakv_cache& c, con
   int n = 0;                // tiles of the lane's sequences
   long long mine = 0;       // a lane's weight
   int lane_b = lane * per_lane, lane_t = 0;  // the sequence and the tile of it that a lane begins with
+  bool falls = false;       // cu decreases
   if (alone) {
     bool many = false;
 #pragma unroll 1
@@ -189,14 +190,17 @@ __device__ __forceinline__ Part find_part(const Geo& g, const fakv_cache& c, con
       const int at = lane * per_lane + i;
       if (at >= B) break;
       s = load_seq(c, cu, slots, at, T);
+      falls |= s.n < 0;
       const int tiles = tiles_of(g, s.n);
       n += tiles;
       many |= tiles > FEW;
 #pragma unroll 1
       for (int t = 0; t < tiles && !many; ++t) mine += max(1, tile_of(g, s, t).units) + g.start;
     }
-    many = __any_sync(0xffffffffu, many);
+    falls = __any_sync(0xffffffffu, falls);
+    many = __any_sync(0xffffffffu, many) && !falls;
     alone = !many || per_lane == 1;
+    if (falls) n = 0, mine = 0;
     if (alone && many) {
       // few sequences of many tiles: the tiles shared out evenly instead
       int t_end = n;
@@ -283,8 +287,14 @@ __device__ __forceinline__ Part find_part(const Geo& g, const fakv_cache& c, con
     int at = 0, tiles;
     long long total, none = 0;
 #pragma unroll 1
-    for (b = b0; b < b1; ++b) at += tiles_of(g, load_seq(c, cu, slots, b, T).n);
+    for (b = b0; b < b1; ++b) {
+      const int rows = load_seq(c, cu, slots, b, T).n;
+      falls |= rows < 0;
+      at += tiles_of(g, rows);
+    }
+    falls = __syncthreads_or(falls);
     scan2<NT>(at, none, &tiles, &total, sh.n_sums, sh.w_sums);
+    if (falls) tiles = 0;
 #pragma unroll 1
     for (b = b0; b < b1; ++b) {
       first[b] = at;
@@ -419,7 +429,7 @@ struct Walk {
 // What worker k left of an item that it did not do whole: slot 2 k (the item its part begins
 // in) or 2 k + 1 (the one it ends in); `ender` is the worker that ends the item. PART_JOINED: the CTA's workers all had one item and
 // put their results together, in the first one's slot.
-enum { PART_VALID = 1, PART_STARTS = 2, PART_ENDS = 4, PART_JOINED = 8 };
+enum { PART_STARTS = 1, PART_ENDS = 2, PART_JOINED = 4 };
 struct Left {
   int flags, row0, rho0, rows, head, ender, pad[2];
 };
@@ -452,6 +462,7 @@ struct JoinArgs {
   int H, Dv, out_bf16;
   Div rep;
 };
+constexpr int TALL_CTAS = 256;  // CTAs that launch_join_tall takes (sm_103 parts have fewer SMs)
 fa_status launch_join(const JoinArgs& a, cudaStream_t s);        // several workers to a CTA
 fa_status launch_join_tall(const JoinArgs& a, cudaStream_t s);   // a CTA is a worker; many rows
 

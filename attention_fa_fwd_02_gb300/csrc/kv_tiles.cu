@@ -552,7 +552,7 @@ __global__ void __launch_bounds__(TilesCfg<D>::THREADS, 1)
         else store_rows<D, false>(o_addr, n > 0, inv, stage, cols, ptr);
         if (!whole && threadIdx.x == 0)
           a.part.left[2 * blockIdx.x + seg.slot] = {
-              PART_VALID | (seg.starts ? PART_STARTS : 0) | (seg.ends ? PART_ENDS : 0), seg.s.row0, seg.x.rho0,
+              (seg.starts ? PART_STARTS : 0) | (seg.ends ? PART_ENDS : 0), seg.s.row0, seg.x.rho0,
               seg.x.rows, seg.head, walk.p.ender, {0, 0}};
       }
       if (q < NQ - 1) {
@@ -583,7 +583,7 @@ fa_status run(TilesArgs& a, const CUtensorMap& q, const CUtensorMap& k, const CU
   if (!allow_smem(kernel, C::SMEM, done)) return FA_ERR_CUDA;
   const int ctas = host::sm_count();
   void* w = nullptr;
-  if (host::scratch_alloc(&w, partials_bytes(ctas, a.g.R, D), s) != cudaSuccess) return FA_ERR_CUDA;
+  if (host::scratch_alloc(&w, partials_bytes(ctas, a.g.R, D), s) != cudaSuccess) return failed();
   a.part = partials_at(w, ctas, a.g.R, D);
   fa_status st = FA_OK;
   {
@@ -603,6 +603,7 @@ fa_status run(TilesArgs& a, const CUtensorMap& q, const CUtensorMap& k, const CU
 
 fa_status launch_attend_tiles(const void* q, void* O, float* LSE, const int* cu, const int* slots,
                               const fakv_cache& c, const fakv_tokens& p, cudaStream_t s) {
+  if (host::sm_count() > TALL_CTAS) return FA_ERR_UNSUPPORTED;
   TilesArgs a = {};
   const int rep = p.H / c.HKV;
   a.c = c;

@@ -18,8 +18,9 @@
  *   shares one table: the layers of a model.
  *
  * A call's new tokens are rows of q (and k, v): sequence b of the call has the rows
- * cu[b] .. cu[b + 1] - 1 (cu: B + 1 non-decreasing int32 from 0 to at most T) and is slot
- * slots[b] (slots NULL: slot b). Lengths count the new tokens: row i of a sequence with n
+ * cu[b] .. cu[b + 1] - 1 (cu: B + 1 non-decreasing int32 from 0 to at most T; attend does
+ * nothing with one that decreases) and is slot slots[b] (slots NULL: slot b; attend may
+ * name a slot for several sequences). Lengths count the new tokens: row i of a sequence with n
  * new tokens has position lens[slot] - n + i. Rows from cu[B] on belong to no sequence
  * and are neither read nor written.
  *
@@ -27,6 +28,10 @@
  * number outside [0, num_pages) where a token should be, a length beyond the row. Such
  * an entry is left out (keys read as zeros, tokens not written) and a bit is set in
  * `*status`, which the caller reads and clears. No access leaves the arrays described.
+ *
+ * Every call checks its arguments, enqueues on `stream` and returns. Temporary buffers come
+ * stream-ordered from the library's pool, so calls on different streams, and graphs, do not
+ * share them. A call may be captured once one call has run on the device outside a capture.
  */
 #ifndef FAKV_H_
 #define FAKV_H_
@@ -44,7 +49,7 @@ enum {
   FAKV_ROW_FULL = 8,   /* grow: the row's max_pages pages do not suffice; not served */
   FAKV_BAD_PAGE = 16,  /* a table entry outside [0, num_pages) where a token should be */
   FAKV_BAD_LENGTH = 32 /* a length below 0, above max_pages * page_size or, in append, below the
-                          new tokens */
+                          new tokens; a cu that decreases; a negative add or keep */
 };
 
 typedef struct {
@@ -133,7 +138,7 @@ typedef struct {
   long long q_token, q_head;   /* element strides of q, multiples of 16 bytes (attend) */
   long long k_token, k_head;   /* append: of k */
   long long v_token, v_head;   /* append: of v */
-  float scale;           /* attend: finite, > 0 */
+  float scale;           /* attend: finite (times log2 e too), > 0 */
   int causal, window;    /* attend: key j visible to position p iff (!causal || j <= p) and
                             (window == 0 || j >= p - window + 1) */
   fa_dtype out_dtype;    /* attend: dtype of O */
@@ -142,7 +147,8 @@ typedef struct {
 /* k and v [T, HKV, D] written to their tokens' places, k turned by its positions first
  * where `rope` is given, and q [T, H, D] turned likewise into q_out [T, H, D] (contiguous;
  * copied where rope is NULL). q_out does not overlap the inputs, or is q itself if that is
- * contiguous. Inputs in the cache's dtype. One launch. */
+ * contiguous. Inputs in the cache's dtype. A slot named for two sequences has two tokens for a
+ * place: which of them stays is not defined. One launch. */
 FA_API fa_status fakv_append(const void* q, const void* k, const void* v, void* q_out,
                              const int* cu, const int* slots, const fakv_rope* rope,
                              const fakv_cache* cache, const fakv_tokens* p, fa_stream_t stream);
@@ -170,7 +176,7 @@ FA_API fa_status fakv_grow(const fakv_cache* cache, const int* slots, const int*
 
 /* Slots dst[i] become copies of slots src[i], sharing their pages; what dst[i] held is
  * released. All at once: sources are read as they were before the call, so a list may
- * exchange or reorder slots. */
+ * exchange or reorder slots. n * max_pages <= 2^31. */
 FA_API fa_status fakv_fork(const fakv_cache* cache, const int* src, const int* dst, int n,
                            fa_stream_t stream);
 

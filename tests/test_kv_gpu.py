@@ -174,6 +174,12 @@ CASES = [
     ([1, 300, 1, 17], [900, 300, 64, 1024], 4, 1, 112, 256, True, 0),
     ([65], [65], 64, 1, 64, 16, True, 0),                         # 64 heads on one kv head
     ([2], [300], 128, 1, 32, 16, True, 0),
+    ([1] * 150, [(37 * i) % 211 for i in range(150)], 2, 1, 32, 16, True, 0),       # more sequences than a warp looks at
+    ([1] * 40 + [700, 1, 0, 90], [50 + i for i in range(40)] + [800, 3, 40, 90], 4, 2, 64, 16, True, 0),
+    ([0, 0, 700, 0, 300, 1], [10, 0, 700, 5, 1000, 999], 8, 2, 64, 32, True, 128),   # few sequences of many tiles
+    ([1] * 3, [5000, 4999, 1], 4, 4, 128, 8, True, 0),
+    ([8] * 5, [100, 2000, 8, 9, 700], 16, 8, 128, 16, True, 0),
+    ([4] * 6, [1000, 40, 4, 600, 601, 2222], 32, 8, 80, 64, True, 50),
 ]
 
 
@@ -274,6 +280,73 @@ def test_far_offsets_pass_32_bits(kv):
     cache.check()
     assert cache.table[0].tolist() == [0, 1, 2, 3, 4]
     assert torch.equal(k[0, :5].reshape(-1, HKV, D)[:300], x[1])
+
+
+def test_attend_the_most_sequences(kv):
+    B, D = 16384, 16
+    lens = [1 + (7 * b) % 5 for b in range(B)]
+    cache = ref.make_cache(kv, lens, 8, 1, D, BF, poison=False)
+    q = randn(B, 2, D, dtype=BF, seed=3)
+    cu = cu_of([1] * B)
+    o, lse = cache.attend(q, cu)
+    cache.check()
+    pick = list(range(0, B, 331)) + [B - 1]
+    ro, rl, bo, bl = ref.attend(cache, q[pick], [1] * len(pick), pick, 0.25, True, 0)
+    ref.close(o[pick], ro, bo, "O")
+    ref.close(lse[pick], rl, bl, "LSE")
+    one = cache.append(q, q[:, :1], q[:, 1:], cu)
+    assert torch.equal(one, q)
+    assert torch.equal(cache.k[0, cache.table[:, 0].long()[pick], [lens[b] - 1 for b in pick]], q[pick, :1])
+
+
+def test_one_slot_for_several_sequences(kv):
+    # drafts of one sequence scored from the same slot
+    cache = ref.make_cache(kv, [77, 200], 16, 2, 64, BF)
+    q = randn(6, 4, 64, dtype=BF)
+    slots = vec(1, 0, 1)
+    o, lse = cache.attend(q, cu_of([2, 2, 2]), slots)
+    ro, rl, bo, bl = ref.attend(cache, q, [2, 2, 2], [1, 0, 1], 0.125, True, 0)
+    ref.close(o, ro, bo, "O")
+
+
+@pytest.mark.parametrize("B", [3, 200])
+def test_a_cu_that_decreases_plans_no_work(kv, B):
+    cache = ref.make_cache(kv, [40] * B, 16, 1, 64, BF, poison=False)
+    q = randn(B, 2, 64, dtype=BF)
+    cu = torch.arange(B + 1, dtype=torch.int32).cuda()
+    cu[1] = B
+    o, lse = torch.full((B, 2, 64), 9.0, dtype=BF, device="cuda"), torch.full((B, 2), 9.0, device="cuda")
+    cache.attend(q, cu, out=o, lse=lse)
+    with pytest.raises(kv.CacheError):
+        cache.check()
+    assert bool((o == 9.0).all()) and bool((lse == 9.0).all())
+    k = cache.k.clone()
+    cache.append(q, q[:, :1], q[:, 1:], cu)  # (rows find the sequences that they find; no token leaves its row)
+    assert cache.k.shape == k.shape and bool(torch.isfinite(cache.k.float()).all())
+
+
+@pytest.mark.parametrize("B,n", [(4, 1), (2, 60)])
+def test_two_graphs_replayed_at_once(kv, B, n):
+    caches = [ref.make_cache(kv, [9000 - i] * B, 16, 2, 64, BF, seed=i) for i in range(2)]
+    q, cu = randn(B * n, 8, 64, dtype=BF), cu_of([n] * B)
+    want = [c.attend(q, cu) for c in caches]
+    torch.cuda.synchronize()
+    graphs, outs, streams = [], [], [torch.cuda.Stream() for _ in range(2)]
+    for c, s in zip(caches, streams):
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g, stream=s):
+            outs.append(c.attend(q, cu))
+        graphs.append(g)
+    for _ in range(20):
+        for o in outs:
+            o[0].fill_(7.0)
+        torch.cuda.synchronize()
+        for g, s in zip(graphs, streams):
+            with torch.cuda.stream(s):
+                g.replay()
+        torch.cuda.synchronize()
+        for o, w in zip(outs, want):
+            assert torch.equal(o[0], w[0]) and torch.equal(o[1], w[1])
 
 
 # ---- pages

@@ -106,7 +106,7 @@ def test_bad_tokens_are_refused(kv, kw, code):
 def test_refusals_of_attend_and_append_alone(kv):
     lib, c = kv._lib(), cache(kv)
     C = ctypes.byref(c)
-    for kw, code in ((dict(scale=0.0), 1), (dict(scale=float("nan")), 1), (dict(scale=float("inf")), 1),
+    for kw, code in ((dict(scale=0.0), 1), (dict(scale=float("nan")), 1), (dict(scale=float("inf")), 1), (dict(scale=3e38), 1),
                      (dict(causal=2), 1), (dict(window=-1), 1), (dict(out_dtype=5), 1), (dict(H=0), 1),
                      (dict(q_head=60), 3), (dict(q_token=257), 3)):
         assert lib.fakv_attend(A, A, A, A, None, C, ctypes.byref(tokens(kv, **kw)), None) == code
@@ -146,6 +146,8 @@ def test_refusals_of_the_page_calls(kv):
         assert f(C, 0, 0, 0, None) == 0
     assert lib.fakv_free(C, 0, None, 1, None) == 1 and lib.fakv_free(C, A, A + 1, 1, None) == 3
     assert lib.fakv_free(C, 0, None, 0, None) == 0
+    wide = cache(kv, max_pages=1 << 20, table_stride=1 << 20)
+    assert lib.fakv_fork(ctypes.byref(wide), A, A, 4096, None) == 1  # too many rows to hold at once
     for kw, code in ((dict(refs=0), 1), (dict(token_stride=256), 2), (dict(page_stride=1024), 1)):
         assert lib.fakv_compact(ctypes.byref(cache(kv, **kw)), None) == code
         assert lib.fakv_grow(ctypes.byref(cache(kv, **kw)), A, A, 1, None) == code
