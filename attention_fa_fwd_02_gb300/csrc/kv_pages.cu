@@ -14,6 +14,7 @@ namespace {
 
 constexpr int PLAN = 1024;   // threads of a planning block
 constexpr int SCAN = 4;      // reference counts per thread and step
+constexpr int NEAR = 4096;   // pages given to a part of a list through shared memory
 constexpr int BRIEF = 256;   // entries of a list compared with one another
 
 // Sums saturate: no list can be served more than 2^28 pages, and beyond them only "too
@@ -124,7 +125,7 @@ struct GrowArgs {
   const int* add;
   int n, shift;
   int* mark;   // scratch [max_slots]: first place of a slot in the list (lists above BRIEF)
-  int* fresh;  // scratch [num_pages]: the free pages, in order
+  int* fresh;  // scratch [num_pages]: the free pages, in order (above NEAR of them)
   int2* pair;  // scratch [n]: pages to copy
   int* count;  // scratch: how many
 };
@@ -139,8 +140,12 @@ __global__ void __launch_bounds__(PLAN) grow_kernel(const __grid_constant__ Grow
   __shared__ unsigned first[PLAN];
   __shared__ int col0[PLAN], slot_of[PLAN];  // slot_of: -1 where nothing is given
   __shared__ int from_sh;
+  __shared__ int near[NEAR];  // free pages of a part of the list that needs few
   ptx::grid_launch_dependents();
   const int tid = threadIdx.x;
+  int refs0[SCAN];  // the first counts, asked for before the list is known
+#pragma unroll
+  for (int k = 0; k < SCAN; ++k) refs0[k] = tid * SCAN + k < a.c.num_pages ? a.c.refs[tid * SCAN + k] : 1;
   // Which entry of a slot is the first: short lists are compared in shared memory (three round
   // trips to memory less), long ones mark their slots.
   const bool brief = a.n <= BRIEF;
@@ -204,6 +209,7 @@ __global__ void __launch_bounds__(PLAN) grow_kernel(const __grid_constant__ Grow
     first[tid] = place;
     if (tid == 0) from_sh = from;
     // rank the free pages until there are `total`
+    const bool few = total <= NEAR;
     unsigned got = 0;
     for (int at = from; !exhausted && got < total && at < a.c.num_pages; at += PLAN * SCAN) {
       bool open[SCAN];
@@ -211,7 +217,8 @@ __global__ void __launch_bounds__(PLAN) grow_kernel(const __grid_constant__ Grow
 #pragma unroll
       for (int k = 0; k < SCAN; ++k) {
         const int page = at + tid * SCAN + k;
-        open[k] = page < a.c.num_pages && a.c.refs[page] == 0;
+        // (counts change between the parts of a long list)
+        open[k] = at == 0 && e0 == 0 ? refs0[k] == 0 : page < a.c.num_pages && a.c.refs[page] == 0;
         mine += open[k];
       }
       unsigned rank = got + block_scan(mine, &here);
@@ -219,7 +226,8 @@ __global__ void __launch_bounds__(PLAN) grow_kernel(const __grid_constant__ Grow
       for (int k = 0; k < SCAN; ++k) {
         if (!open[k] || rank >= total) continue;
         const int page = at + tid * SCAN + k;
-        a.fresh[rank] = page;
+        if (few) near[rank] = page;
+        else a.fresh[rank] = page;
         if (++rank == total) from_sh = page + 1;
       }
       got += here;
@@ -239,14 +247,14 @@ __global__ void __launch_bounds__(PLAN) grow_kernel(const __grid_constant__ Grow
         if (first[mid] <= r) lo = mid; else hi = mid;
       }
       if (slot_of[lo] < 0) continue;
-      const int page = a.fresh[r];
+      const int page = few ? near[r] : a.fresh[r];
       a.c.table[(long long)slot_of[lo] * a.c.table_stride + col0[lo] + (int)(r - first[lo])] = page;
       a.c.refs[page] = 1;
     }
     const bool copy = served && tail >= 0;
     unsigned n_copy;
     const unsigned c_at = block_scan(copy, &n_copy);
-    if (copy) a.pair[copies + c_at] = make_int2(tail, a.fresh[place]);
+    if (copy) a.pair[copies + c_at] = make_int2(tail, few ? near[place] : a.fresh[place]);
     copies += (int)n_copy;
     if (served) a.c.lens[slot] = len + add;
     __syncthreads();
