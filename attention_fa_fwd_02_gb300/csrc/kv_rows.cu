@@ -64,7 +64,7 @@ struct RowsCfg {
   // 2 us or more at the SM's share of HBM; three CTAs where the registers allow them,
   // because more warps hide a change of items better.
   static constexpr int WANT = NTR == 1 && RB < 512 ? 3 : 2;
-  static constexpr int ROOM = WANT == 3 ? 18432 : 28672;
+  static constexpr int ROOM = WANT == 3 ? 18432 : NTR <= 2 ? 28672 : 28160;
   static constexpr bool FITS = ROOM - Q_BYTES >= 2 * SLOT;
   static constexpr int CTAS_PER_SM = FITS ? WANT : 1;
   static constexpr int NS = ((FITS ? ROOM : 56320) - Q_BYTES) / SLOT;
@@ -74,6 +74,8 @@ struct RowsCfg {
   static constexpr bool Q_REGS = !F32 && NTR == 1;
   static_assert(NS >= 2 && WARP_BYTES >= R * OS * 4, "a warp's ring also holds its O at the end");
   static_assert(SMEM >= 4 * 16385, "the plan's scratch");
+  static constexpr int STATIC = (int)sizeof(PlanShared<NTHREADS, WARPS>) + WARPS * (R * 8 + 20);
+  static_assert(CTAS_PER_SM * (SMEM + (STATIC + 1023) / 1024 * 1024 + 1024) <= 228 * 1024, "shared memory of the CTAs of an SM");
 };
 
 __device__ __forceinline__ void cp16(uint32_t dst, const void* src, bool take) {
@@ -196,7 +198,7 @@ __global__ void __launch_bounds__(NTHREADS, RowsCfg<E, D, NTR>::CTAS_PER_SM)
   constexpr int RB = C::RB, CH = C::CH, R = C::R, NS = C::NS, GROUP = C::GROUP, KT = C::KT;
   constexpr int EPC = 16 / (int)sizeof(E);  // elements of a chunk
   extern __shared__ __align__(1024) uint8_t smem[];
-  __shared__ PlanShared<WARPS> plan;
+  __shared__ PlanShared<NTHREADS, WARPS> plan;
   __shared__ float2 ml_sh[WARPS][R];
   __shared__ int4 item_sh[WARPS];  // b, tile, head, and 1: held, 2: no part, 0: neither
   __shared__ int ends_sh[WARPS];   // a held item's PART_STARTS, PART_ENDS

@@ -103,10 +103,10 @@ struct Part {
   int ender;  // the worker that ends the item (end_tile, end_head)
 };
 
-template <int PER>
+template <int NT, int PER>
 struct PlanShared {
-  long long w_sums[16];
-  int n_sums[16];
+  long long w_sums[NT / 32];
+  int n_sums[NT / 32];
   struct {       // where a cut falls: among the tiles [t0, ...) whose weights begin at `before`
     int b, t0;
     long long before;
@@ -167,7 +167,7 @@ __device__ __forceinline__ Cut cut_in(const Geo& g, const Cuts& cuts, int HKV, i
 template <int NT, int PER>
 __device__ __forceinline__ Part find_part(const Geo& g, const fakv_cache& c, const int* cu,
                                           const int* slots, int B, int T, int* first,
-                                          PlanShared<PER>& sh, Seq& seq) {
+                                          PlanShared<NT, PER>& sh, Seq& seq) {
   constexpr int FEW = 4, ALONE = 128;
   const int tid = threadIdx.x, lane = tid & 31;
   const long long most = (long long)gridDim.x * PER;

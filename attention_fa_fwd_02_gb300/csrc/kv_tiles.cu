@@ -177,7 +177,7 @@ __global__ void __launch_bounds__(TilesCfg<D>::THREADS, 1)
       bar_vempty[VST], bar_grant[NQ], bar_s[NQ], bar_o[NQ], bar_drain;
   __shared__ uint32_t tmem_base_sh;
   __shared__ int abort_sh;
-  __shared__ PlanShared<1> plan;
+  __shared__ PlanShared<C::THREADS, 1> plan;
   grid_launch_dependents();
   const int warp = warp_id(), lane = lane_id();
   volatile int* abort_flag = &abort_sh;
