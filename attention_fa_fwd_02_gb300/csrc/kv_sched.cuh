@@ -7,11 +7,11 @@
 // (what beginning an item costs a worker). The line is cut into equal parts, one per worker (a
 // CTA, or a warp), whatever the lengths are: a long sequence is spread over many workers,
 // and a worker may take many short ones; a cut that falls into an item of at most `snap` units
-// (or an eighth of a part) moves to its nearer end. Every CTA finds its workers' parts from the lengths (on the device:
-// the host knows none). A part begins or ends inside an item at most once each, so a worker
-// leaves at most two partial results (output and softmax statistics), in slots of its own;
-// attend_join_kernel puts an item's parts together in key order. Cuts depend on the lengths
-// alone, so results do too.
+// (or an eighth of a part) moves to its nearer end. Every CTA finds its workers' parts from
+// the lengths (on the device: the host knows none). A part begins or ends inside an item at
+// most once each, so a worker leaves at most two partial results (output and softmax
+// statistics), in slots of its own; the join puts an item's parts together in key order. Cuts
+// depend on the lengths alone, so results do too.
 #pragma once
 #include "kv_common.cuh"
 

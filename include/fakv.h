@@ -2,7 +2,7 @@
  * fakv.h -- C ABI of libfa.so for served and trained models' positions and key / value
  * caches: rotary positions, a paged cache, attention of new tokens over it, and the
  * cache's pages (sharing, growing, freeing, compacting). It uses fa.h's types, status
- * codes, streams and ownership rules; fa_timing_* covers its kernels too.
+ * codes, streams and ownership rules; fa_timing_* and fa_device_status cover its kernels too.
  *
  * The cache. Keys and values live in pages of `page_size` tokens. A slot is one
  * sequence: row s of `table` holds the page numbers of its tokens in order, lens[s] its

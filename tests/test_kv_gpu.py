@@ -25,6 +25,10 @@ def cu_of(new):
     return torch.tensor([0] + list(new)).cumsum(0).to(torch.int32).cuda()
 
 
+def vec(*x):
+    return torch.tensor(x, dtype=torch.int32).cuda()
+
+
 def randn(*shape, dtype=F32, seed=0, mul=1.0):
     g = torch.Generator().manual_seed(seed)
     return (torch.randn(*shape, generator=g) * mul).to(dtype).cuda()
@@ -243,6 +247,22 @@ def test_attend_pages_shared_within_a_kv_pair_tensor(kv):
     ref.close(o, ro, bo, "O")
 
 
+@pytest.mark.parametrize("n", [1, 40])
+def test_attend_broadcast_q_and_a_table_within_a_wider_one(kv, n):
+    cache = ref.make_cache(kv, [200, 333], 16, 2, 64, BF, seed=4, max_pages=30)
+    wide = torch.full((2, 50), 1 << 20, dtype=torch.int32, device="cuda")
+    wide[:, 7:7 + 30] = cache.table[:, :30]
+    other = kv.PagedCache(cache.k, cache.v, wide[:, 7:37], cache.lens, cache.refs)
+    q = randn(2 * n, 1, 64, dtype=BF, seed=5).expand(2 * n, 8, 64)
+    o, lse = other.attend(q, cu_of([n, n]))
+    other.check()
+    ro, rl, bo, bl = ref.attend(cache, q, [n, n], [0, 1], 0.125, True, 0, one_term=n > 1)
+    ref.close(o, ro, bo, "O")
+    other.fork(vec(1), vec(0))
+    assert torch.equal(wide[0, 7:7 + 21], wide[1, 7:7 + 21]) and bool((wide[:, :7] == 1 << 20).all())
+    assert bool((wide[:, 37:] == 1 << 20).all())
+
+
 def test_attend_with_bad_pages_slots_and_lengths(kv):
     cache = ref.make_cache(kv, [100, 100, 100], 16, 1, 64, BF)
     q = randn(4, 4, 64, dtype=BF)
@@ -350,8 +370,6 @@ def test_two_graphs_replayed_at_once(kv, B, n):
 
 
 # ---- pages
-def vec(*x):
-    return torch.tensor(x, dtype=torch.int32).cuda()
 
 
 @pytest.mark.parametrize("dtype,layout", [(BF, "tokens"), (F32, "heads")])
