@@ -75,7 +75,7 @@ struct RowsCfg {
   static constexpr int WARP_BYTES = NS * SLOT + Q_BYTES;
   static constexpr int SMEM = WARPS * WARP_BYTES;
   static constexpr int OS = D + 4;                // floats of a row of O in shared memory (bank spread)
-  static constexpr bool Q_REGS = !F32 && NTR == 1;
+  static constexpr bool Q_REGS = NTR == 1 && (!F32 || D == 64);  // q's fragments stay in registers
   static_assert(NS >= 2 && WARP_BYTES >= R * OS * 4, "a warp's ring also holds its O at the end");
   static_assert(SMEM >= 4 * 16385, "the plan's scratch");
   static constexpr int STATIC = (int)sizeof(PlanShared<NTHREADS, WARPS>) + WARPS * (R * 8 + 20);
@@ -115,12 +115,13 @@ __device__ __forceinline__ void mma_tf32(float (&d)[4], const uint32_t (&a)[4], 
                : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
                : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
-// x = hi + lo: hi the value rounded to tf32's 11 significant bits, lo the rest, rounded too
-// (the tensor core drops the 13 low bits, so half of their step is added first; truncated
-// terms would all err to one side: O was 2.7e-6 off instead of a third of that)
+// x = hi + lo: hi the value rounded to tf32's 11 significant bits (half of the 13 low bits'
+// step added before they go), lo the rest, of which the tensor core cuts off the low bits.
+// Rounded, hi leaves a lo of either sign, so that lo's cut and the missing lo lo products
+// do not add up (with hi cut off as well, O was 2.7e-6 off instead of 0.6e-6).
 __device__ __forceinline__ void split(uint32_t x, uint32_t& hi, uint32_t& lo) {
   hi = (x + 0x1000u) & 0xffffe000u;
-  lo = __float_as_uint(__uint_as_float(x) - __uint_as_float(hi)) + 0x1000u;
+  lo = __float_as_uint(__uint_as_float(x) - __uint_as_float(hi));
 }
 __device__ __forceinline__ uint32_t bf2(float a, float b) {
   const __nv_bfloat162 h = __floats2bfloat162_rn(a, b);
@@ -312,7 +313,8 @@ __global__ void __launch_bounds__(NTHREADS, RowsCfg<E, D, NTR>::CTAS_PER_SM)
     // that is new costs its fetch.
     uint32_t use = ring;
     float sc[KT][NTR][4];  // scores, then probabilities: keys 16 kt + oct (+ 8), rows 8 nt + 2 quad + e
-    uint32_t qr[C::Q_REGS ? D / 32 : 1][4];
+    uint32_t qr[C::Q_REGS && !C::F32 ? D / 32 : 1][4];
+    uint32_t qrh[C::Q_REGS && C::F32 ? D / 16 : 1][4], qrl[C::Q_REGS && C::F32 ? D / 16 : 1][4];
 #pragma unroll 1
     for (int j = -NS; j < 2 * n; ++j) {
       if (j >= 0) {
@@ -357,6 +359,15 @@ __global__ void __launch_bounds__(NTHREADS, RowsCfg<E, D, NTR>::CTAS_PER_SM)
           } else {
             // The tensor core cuts off what it adds to a sum below the sum's last bit: the small
             // products have sums of their own, so that the large one is cut a third as often.
+            if (C::Q_REGS && j == 0) {
+#pragma unroll
+              for (int kp = 0; kp < D / 16; ++kp) {
+                uint32_t v[4];
+                ldsm4(sq + at_rows<RB>(mr, 4 * kp + mat), v);
+#pragma unroll
+                for (int z = 0; z < 4; ++z) split(v[z], qrh[C::Q_REGS ? kp : 0][z], qrl[C::Q_REGS ? kp : 0][z]);
+              }
+            }
             float lh[KT][NTR][4], hl[KT][NTR][4];
 #pragma unroll
             for (int kt = 0; kt < KT; ++kt)
@@ -379,9 +390,14 @@ __global__ void __launch_bounds__(NTHREADS, RowsCfg<E, D, NTR>::CTAS_PER_SM)
 #pragma unroll
               for (int nt = 0; nt < NTR; ++nt) {
                 uint32_t v[4], qh[4], ql[4];
-                ldsm4(sq + at_rows<RB>(nt * 8 + mr, 4 * kp + mat), v);
+                if constexpr (C::Q_REGS) {
 #pragma unroll
-                for (int z = 0; z < 4; ++z) split(v[z], qh[z], ql[z]);
+                  for (int z = 0; z < 4; ++z) { qh[z] = qrh[kp][z]; ql[z] = qrl[kp][z]; }
+                } else {
+                  ldsm4(sq + at_rows<RB>(nt * 8 + mr, 4 * kp + mat), v);
+#pragma unroll
+                  for (int z = 0; z < 4; ++z) split(v[z], qh[z], ql[z]);
+                }
 #pragma unroll
                 for (int kt = 0; kt < KT; ++kt)
 #pragma unroll

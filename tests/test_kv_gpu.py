@@ -372,11 +372,11 @@ def test_two_graphs_replayed_at_once(kv, B, n):
 # ---- pages
 
 
-@pytest.mark.parametrize("dtype,layout", [(BF, "tokens"), (F32, "heads")])
-def test_pages_random_walk_against_the_model(kv, dtype, layout):
+@pytest.mark.parametrize("dtype,layout,max_pages", [(BF, "tokens", 9), (F32, "heads", 9), (BF, "tokens", 9000)])
+def test_pages_random_walk_against_the_model(kv, dtype, layout, max_pages):
     rng = random.Random(11)
     cache = ref.make_cache(kv, [0, 5, 16, 33, 0, 8, 1, 0], 8, 2, 16, dtype, planes=2, extra=20, layout=layout,
-                           max_pages=9)
+                           max_pages=max_pages)
     m = ref.Model(cache)
     for step in range(120):
         n = rng.randrange(1, 7)
