@@ -71,7 +71,8 @@ fa_status check_rope(const fakv_rope* r, int D) {
 }
 
 fa_status check_tokens(const fakv_cache* c, const fakv_tokens* p, const int* cu, const int* slots) {
-  if (!p || p->B < 0 || p->B > MAX_SEQS || p->T < 0 || p->T > (1 << 30) || p->H < 0) return FA_ERR_INVALID_ARG;
+  if (!p || p->B < 0 || p->B > MAX_SEQS || p->T < 0 || p->T > (1 << 30) || p->H < 0 || p->H > 65535)
+    return FA_ERR_INVALID_ARG;
   if (p->plane < 0 || p->plane >= c->planes) return FA_ERR_INVALID_ARG;
   if (p->H % c->HKV != 0 || p->H / c->HKV > 128) return FA_ERR_INVALID_ARG;
   if ((double)p->T * p->H > 1073741824.0) return FA_ERR_INVALID_ARG;
@@ -175,7 +176,9 @@ FA_API fa_status fakv_append(const void* q, const void* k, const void* v, void* 
   if (!k || !v || (p->H > 0 && (!q || !q_out))) return FA_ERR_INVALID_ARG;
   if (!aligned(k, es) || !aligned(v, es) || (p->H > 0 && (!aligned(q, es) || !aligned(q_out, es))))
     return FA_ERR_ALIGNMENT;
-  if (p->H > 0 && q == q_out && (p->q_head != cache->D || p->q_token != (long long)p->H * cache->D))
+  // in place: contiguous (the stride of one token or one head is no matter)
+  if (p->H > 0 && q == q_out &&
+      ((p->H > 1 && p->q_head != cache->D) || (p->T > 1 && p->q_token != (long long)p->H * cache->D)))
     return FA_ERR_INVALID_ARG;
   return launch_append(q, k, v, q_out, cu, slots, rope, *cache, *p, reinterpret_cast<cudaStream_t>(stream));
 }

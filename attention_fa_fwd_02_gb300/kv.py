@@ -187,7 +187,7 @@ class Rope:
         if not 0 < rotary_dim <= head_dim:
             raise ValueError("rotary_dim must be in 1 .. head_dim")
         s = dict(scaling or {"kind": "none"})
-        kind, mscale = s.pop("kind"), s.pop("mscale", None)
+        kind, mscale = s.pop("kind", None), s.pop("mscale", None)
         if kind not in KINDS:
             raise ValueError(f"scaling kind must be one of {sorted(KINDS)}")
         if kind == "yarn":

@@ -132,8 +132,8 @@ FA_API fa_status fakv_rope_apply(const void* q, const void* k, void* q_out, void
 typedef struct {
   int B;                 /* sequences in the call, 0 .. 16384 */
   int T;                 /* rows of q, k, v */
-  int H;                 /* query heads: a multiple of the cache's HKV, at most 128 HKV (append: 0
-                            for no q) */
+  int H;                 /* query heads: a multiple of the cache's HKV, at most 128 HKV and 65535
+                            (append: 0 for no q) */
   int plane;             /* the cache's plane */
   long long q_token, q_head;   /* element strides of q, multiples of 16 bytes (attend) */
   long long k_token, k_head;   /* append: of k */

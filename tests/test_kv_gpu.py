@@ -143,6 +143,20 @@ def test_append_writes_each_token_to_its_place(kv, dtype, new, lens, page, layou
     assert torch.equal(got[:T], q[:T])
 
 
+def test_append_in_place_one_token_and_one_head(kv):
+    # contiguous in memory, whatever the strides of an extent of one say
+    rope = kv.Rope(64)
+    for H, HKV, T, make in ((4, 2, 1, lambda x: x.transpose(0, 1).contiguous().transpose(0, 1)),
+                            (1, 1, 5, lambda x: x.as_strided(x.shape, (64, 256, 1)))):
+        cache = ref.make_cache(kv, [9], 8, HKV, 64, BF)
+        q, k = randn(T, H, 64, dtype=BF, seed=1), randn(T, HKV, 64, dtype=BF, seed=2)
+        want = cache.append(q, k, k, cu_of([T]), rope=rope)
+        x = make(q.clone())
+        assert x.is_contiguous() and cache.append(x, k, k, cu_of([T]), rope=rope, out=x) is x
+        assert torch.equal(x, want)
+        cache.check()
+
+
 def test_append_leaves_out_what_the_table_refuses(kv):
     cache = ref.make_cache(kv, [20, 20, 20, 20], 16, 1, 16, BF, poison=False)
     before = cache.k.clone(), cache.v.clone()

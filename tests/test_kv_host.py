@@ -230,3 +230,10 @@ def test_the_binding_refuses_what_it_can_see(kv):
         r.apply(z(2, 1, 64), None, z(2).long())
     with pytest.raises(ValueError):
         r.apply(z(2, 1, 32), None, z(2).long())
+
+
+def test_what_no_launch_could_take_is_refused(kv):
+    c, t = cache(kv, HKV=1000, token_stride=64000, page_stride=16 * 64000), tokens(kv, H=66000, T=1, B=1)
+    assert calls(kv, c, t) == (1, 1)  # more heads than a grid has rows of blocks
+    with pytest.raises(ValueError):   # a scaling without its kind
+        kv.Rope(64, scaling=dict(factor=2.0), device="cpu")
