@@ -17,7 +17,7 @@
 // sixteenth of it is the join); one sequence of 16 tokens 8.3 us and of 1021 9.5 us, which is
 // latency: 1.6 us from the launch to the cuts, 1.6 us to the first keys asked for, 0.5 us to
 // have them, 4 us the join. fp32, 12 sequences of up to 5 new tokens, window 1024, heads of
-// 64: 17 us, 48 MB; its three products per GEMM and their splits are what bounds it.
+// 64: 16.5 us, 48 MB; its three products per GEMM and their splits are what bounds it.
 //
 //   scores  S^T = K Q^T: the 16 rows of an mma tile are keys, its 8 columns rows of q, so
 //           that eight rows (a decoding step) cost eight rows. bf16 m16n8k16, fp32 sums.
