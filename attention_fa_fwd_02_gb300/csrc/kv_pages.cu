@@ -348,52 +348,58 @@ __global__ void __launch_bounds__(256) fork_give_kernel(const __grid_constant__ 
   }
 }
 
-// Short lists of short rows in one launch of one block, the sources' rows in shared memory
-// (no scratch, and half of the two launches' 8 us): a warp per entry.
-constexpr int SHORT_ROWS = 8192;  // n * max_pages
+// Short lists of short rows in one launch of one block: a warp per entry, rows in registers.
+// Three dependent look-ups and no scratch: 3 entries of 21 pages 2.3 us, 32 of 250 4.4 (two
+// launches, whose time hardly depends on either: 4.0 and 4.7).
+constexpr int SHORT_LIST = PLAN / 32;  // entries
+constexpr int SHORT_STEPS = 8;         // 32 pages each
 __global__ void __launch_bounds__(PLAN) fork_short_kernel(const __grid_constant__ ListArgs a) {
-  __shared__ int rows[SHORT_ROWS];
-  __shared__ int to[BRIEF], held[BRIEF];  // destinations; the sources' lengths, -1: left out
-  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  if (tid < a.n) to[tid] = a.dst[tid];
-  __syncthreads();
-  if (tid < a.n) {
-    const int src = a.src[tid], dst = to[tid];
-    bool again = false;
-    for (int j = 0; j < tid; ++j) again |= to[j] == dst;
-    const bool in = (unsigned)src < (unsigned)a.c.max_slots && (unsigned)dst < (unsigned)a.c.max_slots;
-    if ((unsigned)dst >= (unsigned)a.c.max_slots) raise(a.c.status, FAKV_BAD_SLOT);
-    else if (again) raise(a.c.status, FAKV_REPEATED);
-    else if (!in) raise(a.c.status, FAKV_BAD_SLOT);
-    held[tid] = in && !again ? length_of(a.c, src) : -1;
-  }
-  __syncthreads();
-  for (int i = warp; i < a.n; i += PLAN / 32) {
-    if (held[i] < 0) continue;
-    const int* row = a.c.table + (long long)a.src[i] * a.c.table_stride;
-    for (int k = lane; k < pages_of(held[i], a.shift); k += 32) {
-      const int p = row[k];
-      rows[i * a.c.max_pages + k] = p;
-      if ((unsigned)p < (unsigned)a.c.num_pages) atomicAdd(&a.c.refs[p], 1);
-      else raise(a.c.status, FAKV_BAD_PAGE);
-    }
-  }
-  __syncthreads();
-  for (int i = warp; i < a.n; i += PLAN / 32) {
-    if (held[i] < 0) continue;
-    const int old = pages_of(length_of(a.c, to[i]), a.shift), now = pages_of(held[i], a.shift);
-    int* row = a.c.table + (long long)to[i] * a.c.table_stride;
-    for (int k = lane; k < max(old, now); k += 32) {
-      if (k < old) {
-        const int p = row[k];
-        if ((unsigned)p < (unsigned)a.c.num_pages) atomicSub(&a.c.refs[p], 1);
-        else raise(a.c.status, FAKV_BAD_PAGE);
+  const int i = threadIdx.x / 32, lane = threadIdx.x & 31;
+  int dst = -1, len = -1, now = 0, was = 0;
+  int take[SHORT_STEPS], held[SHORT_STEPS];
+  if (i < a.n) {
+    const int other = lane < a.n ? a.dst[lane] : -1;
+    const int src = a.src[i];
+    dst = __shfl_sync(0xffffffffu, other, i);
+    const bool in = (unsigned)dst < (unsigned)a.c.max_slots;
+    const bool again = __any_sync(0xffffffffu, lane < i && other == dst);
+    const bool ok = in && !again && (unsigned)src < (unsigned)a.c.max_slots;
+    if (!ok && lane == 0) raise(a.c.status, in && again ? FAKV_REPEATED : FAKV_BAD_SLOT);
+    if (ok) {
+      len = length_of(a.c, src);
+      now = pages_of(len, a.shift);
+      was = pages_of(length_of(a.c, dst), a.shift);
+      const int* from = a.c.table + (long long)src * a.c.table_stride;
+      const int* to = a.c.table + (long long)dst * a.c.table_stride;
+#pragma unroll
+      for (int s = 0; s < SHORT_STEPS; ++s) {
+        const int k = 32 * s + lane;
+        take[s] = k < now ? from[k] : -1;
+        held[s] = k < was ? to[k] : -1;
       }
-      row[k] = k < now ? rows[i * a.c.max_pages + k] : -1;
+#pragma unroll
+      for (int s = 0; s < SHORT_STEPS; ++s) {
+        const int k = 32 * s + lane;
+        if (k < now) {
+          if ((unsigned)take[s] < (unsigned)a.c.num_pages) atomicAdd(&a.c.refs[take[s]], 1);
+          else raise(a.c.status, FAKV_BAD_PAGE);
+        }
+        if (k < was) {
+          if ((unsigned)held[s] < (unsigned)a.c.num_pages) atomicSub(&a.c.refs[held[s]], 1);
+          else raise(a.c.status, FAKV_BAD_PAGE);
+        }
+      }
     }
-    __syncwarp();
-    if (lane == 0) a.c.lens[to[i]] = held[i];
   }
+  __syncthreads();  // every row and length is read
+  if (len < 0) return;
+  int* row = a.c.table + (long long)dst * a.c.table_stride;
+#pragma unroll
+  for (int s = 0; s < SHORT_STEPS; ++s) {
+    const int k = 32 * s + lane;
+    if (k < max(now, was)) row[k] = take[s];
+  }
+  if (lane == 0) a.c.lens[dst] = len;
 }
 
 __global__ void __launch_bounds__(256) free_kernel(const __grid_constant__ ListArgs a) {
@@ -543,7 +549,7 @@ fa_status launch_grow(const fakv_cache& c, const int* slots, const int* add, int
 }
 
 fa_status launch_fork(const fakv_cache& c, const int* src, const int* dst, int n, cudaStream_t s) {
-  if (n <= BRIEF && (long long)n * c.max_pages <= SHORT_ROWS) {
+  if (n <= SHORT_LIST && c.max_pages <= 32 * SHORT_STEPS) {
     const ListArgs b = {c, src, dst, nullptr, n, log2_of(c.page_size), nullptr, nullptr};
     host::KernelTimer t("fork_short", s);
     fork_short_kernel<<<1, PLAN, 0, s>>>(b);

@@ -448,6 +448,22 @@ def test_fork_exchanges_slots(kv):
     assert m.rows[1] == rows[0] and m.refs.count(1) == sum(map(len, rows))
 
 
+@pytest.mark.parametrize("n,max_pages", [(32, 256), (33, 256), (32, 257), (1, 256), (200, 40)])
+def test_fork_of_lists_and_rows_of_any_size(kv, n, max_pages):
+    # full, empty and half rows; permuted, so that every slot is a source and a destination
+    cache = kv.PagedCache.create(1, n * max_pages + 4, 8, 1, 16, n + 1, max_pages)
+    m = ref.Model(cache)
+    order, add = list(range(n)), [(i % 3) * 4 * max_pages for i in range(n)]
+    add[0] = 8 * max_pages
+    m.grow(order, add)
+    cache.grow(vec(*order), vec(*add))
+    src = [(5 * i + 3) % n for i in range(n)] if n % 5 else order
+    for dst in (order, [n] + order[1:], order[::-1]):
+        m.fork(src, dst)
+        cache.fork(vec(*src), vec(*dst))
+        m.same(cache, dst[:2])
+
+
 def test_compact_of_full_empty_and_large_caches(kv):
     for pages, gone in ((1, 0.0), (37, 1.0), (64, 0.0), (9001, 0.4), (65536, 0.5), (70001, 0.3)):
         g = torch.Generator().manual_seed(pages)
