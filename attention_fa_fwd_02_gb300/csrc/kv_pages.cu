@@ -8,9 +8,10 @@
 // the same on every run.
 //
 // Measured: 96 samples forked from 32 sequences and grown, 24 MB of last pages copied in 4
-// planes: 15.9 us (take 4, give 4, plan 7, copy 5: launches and look-ups; the copy's floor is
-// 7 us); 8192 pages closed up, 1900 of them moved in 2 planes: 92 us with the two small copies
-// around it, the move itself 70 us, 490 MB at 7.0 TB/s, the rate of a copy.
+// planes: 16.1 us (fork 4.6 by two launches, plan 7, copy 5: launches and look-ups; the copy's floor
+// is 7 us); a page each for 64 slots 6.3 us in a pool of 5000 pages, 11.8 in one of 130000 and 20.3
+// of 500000, all but full; 8192 pages closed up, 1900 of them moved in 2 planes: 92 us with the
+// two small copies around it, the move itself 70 us, 490 MB at 7.0 TB/s, the rate of a copy.
 #include "kv_common.cuh"
 
 namespace fa {
@@ -19,6 +20,7 @@ namespace {
 
 constexpr int PLAN = 1024;   // threads of a planning block
 constexpr int SCAN = 4;      // reference counts per thread and step
+constexpr int WIDE = 16;     // and in grow's walk past the first of them
 constexpr int NEAR = 4096;   // pages given to a part of a list through shared memory
 constexpr int BRIEF = 256;   // entries of a list compared with one another
 
@@ -129,6 +131,7 @@ struct GrowArgs {
   const int* slots;
   const int* add;
   int n, shift;
+  bool quads;  // refs may be read four at a time
   int* mark;   // scratch [max_slots]: first place of a slot in the list (lists above BRIEF)
   int* fresh;  // scratch [num_pages]: the free pages, in order (above NEAR of them)
   int2* pair;  // scratch [n]: pages to copy
@@ -147,7 +150,7 @@ __global__ void __launch_bounds__(PLAN) grow_kernel(const __grid_constant__ Grow
   __shared__ int from_sh;
   __shared__ int near[NEAR];  // free pages of a part of the list that needs few
   ptx::grid_launch_dependents();
-  const int tid = threadIdx.x;
+  const int tid = threadIdx.x, lane = tid & 31;
   int refs0[SCAN];  // the first counts, asked for before the list is known
 #pragma unroll
   for (int k = 0; k < SCAN; ++k) refs0[k] = tid * SCAN + k < a.c.num_pages ? a.c.refs[tid * SCAN + k] : 1;
@@ -216,26 +219,54 @@ __global__ void __launch_bounds__(PLAN) grow_kernel(const __grid_constant__ Grow
     // rank the free pages until there are `total`
     const bool few = total <= NEAR;
     unsigned got = 0;
-    for (int at = from; !exhausted && got < total && at < a.c.num_pages; at += PLAN * SCAN) {
-      bool open[SCAN];
-      unsigned mine = 0, here;
-#pragma unroll
-      for (int k = 0; k < SCAN; ++k) {
-        const int page = at + tid * SCAN + k;
-        // (counts change between the parts of a long list)
-        open[k] = at == 0 && e0 == 0 ? refs0[k] == 0 : page < a.c.num_pages && a.c.refs[page] == 0;
-        mine += open[k];
-      }
-      unsigned rank = got + block_scan(mine, &here);
-#pragma unroll
-      for (int k = 0; k < SCAN; ++k) {
-        if (!open[k] || rank >= total) continue;
-        const int page = at + tid * SCAN + k;
-        if (few) near[rank] = page;
-        else a.fresh[rank] = page;
-        if (++rank == total) from_sh = page + 1;
+    auto rank = [&](int page, unsigned open) {  // this thread's next pages, a bit for each free one
+      unsigned here, r = got + block_scan(__popc(open), &here);
+      for (; open && r < total; open &= open - 1) {
+        const int free = page + __ffs(open) - 1;
+        if (few) near[r] = free;
+        else a.fresh[r] = free;
+        if (++r == total) from_sh = free + 1;
       }
       got += here;
+    };
+    int at = from & ~3;
+    if (e0 == 0 && total > 0) {
+      unsigned open = 0;
+#pragma unroll
+      for (int k = 0; k < SCAN; ++k) open |= (refs0[k] == 0) << k;
+      rank(tid * SCAN, open);
+      at = PLAN * SCAN;
+    }
+    // Pools are mostly full: a step over used pages is one load of whole lines, on its way while
+    // the step before it is looked at, and one barrier. Where a page is free, each thread takes
+    // WIDE neighbours, so that ranks follow page numbers.
+    int4 seen[WIDE / 4];
+    auto four = [&](int page) {
+      if (a.quads && page + 4 <= a.c.num_pages) return *reinterpret_cast<const int4*>(a.c.refs + page);
+      auto one = [&](int p) { return p < a.c.num_pages ? a.c.refs[p] : 1; };
+      return make_int4(one(page), one(page + 1), one(page + 2), one(page + 3));
+    };
+    auto ask = [&](int step) {
+#pragma unroll
+      for (int k = 0; k < WIDE / 4; ++k) seen[k] = four(step + (tid / 32 * WIDE + k * 4) * 32 + lane * 4);
+    };
+    const bool walk = !exhausted && got < total && at < a.c.num_pages;
+    if (walk) ask(at);
+    for (; walk && got < total && at < a.c.num_pages; at += PLAN * WIDE) {
+      bool any = false;
+#pragma unroll
+      for (int k = 0; k < WIDE / 4; ++k) any |= seen[k].x == 0 || seen[k].y == 0 || seen[k].z == 0 || seen[k].w == 0;
+      ask(at + PLAN * WIDE);
+      if (!__syncthreads_or(any)) continue;
+      const int page = at + tid * WIDE;
+      unsigned open = 0;
+#pragma unroll
+      for (int k = 0; k < WIDE; k += 4) {
+        const int4 c = four(page + k);
+        open |= ((c.x == 0) | (c.y == 0) << 1 | (c.z == 0) << 2 | (c.w == 0) << 3) << k;
+      }
+      if (page < from) open &= from - page < WIDE ? ~0u << (from - page) : 0u;
+      rank(page, open);
     }
     const unsigned found = min(got, total);
     const bool served = slot >= 0 && (need == 0 || place + need <= found);
@@ -533,7 +564,8 @@ fa_status launch_grow(const fakv_cache& c, const int* slots, const int* add, int
   const size_t pair = 16, fresh = pair + (size_t)n * 8, mark = fresh + (size_t)c.num_pages * 4;
   Scratch w(mark + (size_t)c.max_slots * 4, s);
   if (!w.ok) return failed();
-  GrowArgs a = {c, slots, add, n, log2_of(c.page_size), reinterpret_cast<int*>(w.p + mark),
+  GrowArgs a = {c, slots, add, n, log2_of(c.page_size), reinterpret_cast<uintptr_t>(c.refs) % 16 == 0,
+                reinterpret_cast<int*>(w.p + mark),
                 reinterpret_cast<int*>(w.p + fresh), reinterpret_cast<int2*>(w.p + pair),
                 reinterpret_cast<int*>(w.p)};
   {

@@ -430,6 +430,28 @@ def test_grow_long_lists_and_long_entries(kv):
     assert m.bits & 1  # (the last rounds asked for too much)
 
 
+@pytest.mark.parametrize("pages,shift", [(4095, 0), (4097, 0), (20480, 0), (20483, 1), (70001, 3)])
+def test_grow_finds_the_free_pages_of_a_mostly_full_pool(kv, pages, shift):
+    # one free page in two hundred, none among the first 4096 but two, and counts at any address
+    g = torch.Generator().manual_seed(pages)
+    used = (torch.rand(pages, generator=g) >= 0.005).int()
+    used[:4096] = 1
+    used[[7, 4094]] = 0
+    used[-1] = 0
+    whole = torch.ones(pages + shift, dtype=torch.int32, device="cuda")
+    refs = whole[shift:]
+    refs.copy_(used)
+    k = torch.zeros(1, pages, 8, 1, 16, device="cuda")
+    n = 1500
+    cache = kv.PagedCache(k, k.clone(), torch.full((n, 40), -1, dtype=torch.int32, device="cuda"),
+                          torch.zeros(n, dtype=torch.int32, device="cuda"), refs)
+    m = ref.Model(cache)
+    for slots, add in (((0, 1), (8, 17)), (range(2, 40), [9] * 38), (range(n), [1] * n)):
+        m.grow(list(slots), list(add))
+        cache.grow(vec(*slots), vec(*add))
+        m.same(cache, (pages, len(add)))
+
+
 def test_grow_refuses_more_than_any_row_or_sum_holds(kv):
     cache = kv.PagedCache.create(1, 64, 8, 1, 16, 3, 1 << 27)
     cache.grow(vec(0, 1, 2), vec((1 << 30) - 8, 1 << 30, 16))
