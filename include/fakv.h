@@ -160,7 +160,8 @@ FA_API fa_status fakv_append(const void* q, const void* k, const void* v, void* 
  * use three tf32 products per GEMM (about 22 significant bits); bf16 caches bf16 products
  * with fp32 sums, the probabilities in bf16 (two terms where there are few rows). Sums
  * over keys that are split between CTAs are joined in a fixed order: results do not
- * depend on timing. */
+ * depend on timing. A batch is served by one kernel, chosen by the average of new tokens: a few
+ * long chunks among hundreds of short decoding sequences are better given calls of their own. */
 FA_API fa_status fakv_attend(const void* q, void* O, float* LSE, const int* cu, const int* slots,
                              const fakv_cache* cache, const fakv_tokens* p, fa_stream_t stream);
 
