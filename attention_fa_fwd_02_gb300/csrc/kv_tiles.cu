@@ -16,8 +16,13 @@
 //   warp 9, 10    producers: Q and K, V (and the epilogue's stages)
 //   warp 11       relay of landed copies to the issuer; it also zeroes V's rows past a
 //                 sequence's end, whose memory may hold anything (0 x NaN)
-// P is one bf16 term here, 2^-8 at most and random in sign: about the rounding of a bf16
-// output; a second term would add half of the forward's tensor work again.
+// P is one bf16 term where O is bf16: its rounding, at most 2^-8 of a probability and
+// random in sign, adds to O about what O's own rounding does (2048 tokens over 16384: O is
+// 2.4e-3 of its size from the 64-bit values, 1.7e-3 of that its own rounding), and a second
+// term would take 560 us where one takes 341. An fp32 O has no such rounding to hide
+// behind: with one term it would be 1.7e-3 off too. There P is two terms (2^-16), the second
+// in the half of S's TMEM columns that the first leaves free: 3e-5 off, in 562 us (8192
+// tokens of a prompt: 647 against 385).
 //
 // Measured: 2048 tokens over 16384 (32 query heads on 8 of 128) 337 us with the join, 1530
 // TFLOP/s, 0.80 of the measured peak; 8192 tokens of a prompt 381 us, 0.76. A unit of 128 keys
@@ -105,13 +110,15 @@ __device__ __forceinline__ void issue_qk(uint32_t d_tmem, uint32_t sq, uint32_t 
     mma_f16_ss(d_tmem, make_sdesc(sq + off, 16, SW128_ATOM), make_sdesc(sk + off, 16, SW128_ATOM), id, kk > 0);
   }
 }
-template <class C>
+template <class C, int TERMS>
 __device__ __forceinline__ void issue_pv(uint32_t o_tmem, uint32_t p_tmem, uint32_t sv, bool accumulate) {
   constexpr uint32_t id = make_idesc(128, C::D, FMT_BF16, FMT_BF16, false, true);
 #pragma unroll
-  for (int kk = 0; kk < BLOCK_N / 16; ++kk)
-    mma_f16_ts(o_tmem, p_tmem + kk * 8, make_sdesc(sv + kk * 16 * 128, C::CB_BYTES, SW128_ATOM), id,
-               (accumulate || kk > 0) ? 1u : 0u);
+  for (int term = TERMS - 1; term >= 0; --term)
+#pragma unroll
+    for (int kk = 0; kk < BLOCK_N / 16; ++kk)
+      mma_f16_ts(o_tmem, p_tmem + term * 64 + kk * 8, make_sdesc(sv + kk * 16 * 128, C::CB_BYTES, SW128_ATOM), id,
+                 (accumulate || kk > 0 || term < TERMS - 1) ? 1u : 0u);
 }
 
 // 32 accumulator rows of a warp, times mul, to row_ptr(r) (null: not written), staged in a
@@ -174,7 +181,7 @@ __device__ __forceinline__ void store_rows(uint32_t t_addr, bool have, float mul
   fence_async_shared();  // before the copy engine writes the stage again
 }
 
-template <int D>
+template <int D, int TERMS>
 __global__ void __launch_bounds__(TilesCfg<D>::THREADS, 1)
     attend_tiles_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
                         const __grid_constant__ CUtensorMap tmV, const __grid_constant__ TilesArgs a) {
@@ -363,7 +370,7 @@ __global__ void __launch_bounds__(TilesCfg<D>::THREADS, 1)
             named_bar_sync(1 + q, 128 + 32);  // P_q(g) is in TMEM
             tc_fence_after();
             if (leader) {
-              issue_pv<C>(tmem + C::o_col(q), tmem + C::s_col(q), sV(vs), t > 0);
+              issue_pv<C, TERMS>(tmem + C::o_col(q), tmem + C::s_col(q), sV(vs), t > 0);
               if (more) {
                 issue_qk<C>(tmem + C::s_col(q), sQ(q), sK(ks));
                 tc_commit(&bar_s[q]);
@@ -511,14 +518,18 @@ __global__ void __launch_bounds__(TilesCfg<D>::THREADS, 1)
 #pragma unroll
         for (int c = 0; c < 2; ++c) {
           uint32_t pk[32];
+          uint32_t lo[TERMS > 1 ? 32 : 1];
 #pragma unroll
           for (int kk = 0; kk < 32; ++kk) {
             const float2 x = fma2(make_float2(s[c * 64 + 2 * kk], s[c * 64 + 2 * kk + 1]), sl2x2, nmx2);
             const float2 pp = make_float2(ex2(x.x), ex2(x.y));
             ls[kk & 1] = add2(ls[kk & 1], pp);
             pk[kk] = pack_bf2(pp.x, pp.y);
+            if constexpr (TERMS > 1)
+              lo[kk] = pack_bf2(pp.x - __uint_as_float(pk[kk] << 16), pp.y - __uint_as_float(pk[kk] & 0xffff0000u));
           }
           tmem_st32(s_addr + c * 32, pk);
+          if constexpr (TERMS > 1) tmem_st32(s_addr + 64 + c * 32, lo);
         }
         l += (ls[0].x + ls[1].x) + (ls[0].y + ls[1].y);
         tmem_st_wait();
@@ -584,10 +595,10 @@ __global__ void __launch_bounds__(TilesCfg<D>::THREADS, 1)
   }
 }
 
-template <int D>
+template <int D, int TERMS>
 fa_status run(TilesArgs& a, const CUtensorMap& q, const CUtensorMap& k, const CUtensorMap& v, cudaStream_t s) {
   using C = TilesCfg<D>;
-  auto* kernel = attend_tiles_kernel<D>;
+  auto* kernel = attend_tiles_kernel<D, TERMS>;
   static std::atomic<uint64_t> done{0};
   if (!allow_smem(kernel, C::SMEM, done)) return FA_ERR_CUDA;
   const int ctas = host::sm_count();
@@ -645,7 +656,8 @@ fa_status launch_attend_tiles(const void* q, void* O, float* LSE, const int* cu,
   if (!host::encode_tiled_4d(&mq, q, qd, qs, qb) || !host::encode_tiled_4d(&mk, static_cast<const char*>(c.K) + plane, kd, ks, kb) ||
       !host::encode_tiled_4d(&mv, static_cast<const char*>(c.V) + plane, kd, ks, kb))
     return FA_ERR_UNSUPPORTED;
-  return c.D <= 64 ? run<64>(a, mq, mk, mv, s) : run<128>(a, mq, mk, mv, s);
+  if (a.out_bf16) return c.D <= 64 ? run<64, 1>(a, mq, mk, mv, s) : run<128, 1>(a, mq, mk, mv, s);
+  return c.D <= 64 ? run<64, 2>(a, mq, mk, mv, s) : run<128, 2>(a, mq, mk, mv, s);
 }
 
 unsigned int read_and_clear_kv_status(cudaError_t* err) {

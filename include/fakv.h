@@ -158,7 +158,8 @@ FA_API fa_status fakv_append(const void* q, const void* k, const void* v, void* 
  * cache's dtype. A row that sees no key gets O = 0, LSE = -inf. K and V within a
  * sequence's length must be finite; page memory past it may hold anything. fp32 caches
  * use three tf32 products per GEMM (about 22 significant bits); bf16 caches bf16 products
- * with fp32 sums, the probabilities in bf16 (two terms where there are few rows). Sums
+ * with fp32 sums, the probabilities in bf16: two terms (2^-16) where O is fp32 or there are few
+ * rows, one (2^-8, about a bf16 O's own rounding) where there are many and O is bf16. Sums
  * over keys that are split between CTAs are joined in a fixed order: results do not
  * depend on timing. A batch is served by one kernel, chosen by the average of new tokens: a few
  * long chunks among hundreds of short decoding sequences are better given calls of their own. */
