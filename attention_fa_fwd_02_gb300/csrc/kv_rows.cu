@@ -145,6 +145,35 @@ __device__ __forceinline__ uint32_t transpose8(uint32_t x) {  // of an 8 x 8 mat
   return y;
 }
 
+// Sums of exponentials taken against the maximum M. L = 0: no key seen. (Tested for 0, not for
+// its sign: NaN sums, from a row of q or a page, are sums, and reach O and LSE however the item was cut.)
+struct Sum {
+  float M, L;
+  float4 acc;
+  __device__ __forceinline__ void add(float m, float l, const float4& v) {
+    const float mn = fmaxf(M, m);
+    const float fo = ptx::ex2(M - mn), fn = ptx::ex2(m - mn);
+    M = mn;
+    L = L * fo + l * fn;
+    acc.x = acc.x * fo + v.x * fn;
+    acc.y = acc.y * fo + v.y * fn;
+    acc.z = acc.z * fo + v.z * fn;
+    acc.w = acc.w * fo + v.w * fn;
+  }
+  // columns col .. col + 3 of row `at` of O [.][cols], and its LSE
+  __device__ __forceinline__ void write(void* O, float* LSE, size_t at, int col, int cols, bool bf16) const {
+    const float inv = L == 0.f ? 0.f : __fdividef(1.f, L);
+    if (col == 0) LSE[at] = L == 0.f ? -INFINITY : (M + __log2f(L)) * LN2;
+    if (col >= cols) return;
+    if (bf16)
+      *reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(O) + at * cols + col) =
+          make_uint2(bf2(acc.x * inv, acc.y * inv), bf2(acc.z * inv, acc.w * inv));
+    else
+      *reinterpret_cast<float4*>(static_cast<float*>(O) + at * cols + col) =
+          make_float4(acc.x * inv, acc.y * inv, acc.z * inv, acc.w * inv);
+  }
+};
+
 // An item's (or its part's) result from the sums of warps w0 .. w1 of the CTA, each in its own
 // shared memory: O [R][OS] not normalised, m and l in ml. By `threads` threads of which the
 // caller is number i. flags: PART_STARTS, PART_ENDS (both: the whole item), PART_JOINED.
@@ -158,38 +187,19 @@ __device__ __forceinline__ void finish(const RowsArgs& a, const Finish& f, const
   constexpr int COLS = D / 4;  // threads of a row
   const int col = i % COLS * 4;
   for (int r = i / COLS; r < f.rows; r += threads / COLS) {
-    float M = ml[w0][r].x, L = ml[w0][r].y;
-    float4 acc = *reinterpret_cast<const float4*>(
-        reinterpret_cast<const float*>(smem + w0 * C::WARP_BYTES) + r * C::OS + col);
+    auto of = [&](int w) {
+      return *reinterpret_cast<const float4*>(reinterpret_cast<const float*>(smem + w * C::WARP_BYTES) + r * C::OS + col);
+    };
+    Sum x = {ml[w0][r].x, ml[w0][r].y, of(w0)};
 #pragma unroll 1
-    for (int w = w0 + 1; w <= w1; ++w) {
-      const float2 x = ml[w][r];
-      const float4 v = *reinterpret_cast<const float4*>(
-          reinterpret_cast<const float*>(smem + w * C::WARP_BYTES) + r * C::OS + col);
-      const float mn = fmaxf(M, x.x), fo = ptx::ex2(M - mn), fn = ptx::ex2(x.x - mn);
-      M = mn;
-      L = L * fo + x.y * fn;
-      acc.x = acc.x * fo + v.x * fn;
-      acc.y = acc.y * fo + v.y * fn;
-      acc.z = acc.z * fo + v.z * fn;
-      acc.w = acc.w * fo + v.w * fn;
-    }
+    for (int w = w0 + 1; w <= w1; ++w) x.add(ml[w][r].x, ml[w][r].y, of(w));
     if (whole) {
-      const float inv = L > 0.f ? __fdividef(1.f, L) : 0.f;
       const int rho = f.rho0 + r, token = a.g.rep.of(rho);
-      const size_t at = (size_t)(f.row0 + token) * a.H + f.head * a.g.rep.d + rho - token * a.g.rep.d;
-      if (col == 0) a.LSE[at] = L > 0.f ? (M + __log2f(L)) * LN2 : -INFINITY;
-      if (col < a.c.D) {
-        if (a.out_bf16)
-          *reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(a.O) + at * a.c.D + col) =
-              make_uint2(bf2(acc.x * inv, acc.y * inv), bf2(acc.z * inv, acc.w * inv));
-        else
-          *reinterpret_cast<float4*>(static_cast<float*>(a.O) + at * a.c.D + col) =
-              make_float4(acc.x * inv, acc.y * inv, acc.z * inv, acc.w * inv);
-      }
+      x.write(a.O, a.LSE, (size_t)(f.row0 + token) * a.H + f.head * a.g.rep.d + rho - token * a.g.rep.d, col, a.c.D,
+              a.out_bf16);
     } else {
-      *reinterpret_cast<float4*>(a.part.O + ((size_t)f.slot * C::R + r) * D + col) = acc;
-      if (col == 0) a.part.ml[(size_t)f.slot * C::R + r] = make_float2(M, L);
+      *reinterpret_cast<float4*>(a.part.O + ((size_t)f.slot * C::R + r) * D + col) = x.acc;
+      if (col == 0) a.part.ml[(size_t)f.slot * C::R + r] = make_float2(x.M, x.L);
     }
   }
   if (!whole && i == 0)
@@ -614,34 +624,10 @@ __global__ void __launch_bounds__(NTHREADS, RowsCfg<E, D, NTR>::CTAS_PER_SM)
 constexpr int JOIN_WARPS = 4;
 constexpr int JOIN_THREADS = 32 * JOIN_WARPS;
 
-struct Sum {  // sums of exponentials taken against the maximum M
-  float M, L;
-  float4 acc;
-  __device__ __forceinline__ void add(float m, float l, const float4& v) {
-    const float mn = fmaxf(M, m);
-    const float fo = ptx::ex2(M - mn), fn = ptx::ex2(m - mn);
-    M = mn;
-    L = L * fo + l * fn;
-    acc.x = acc.x * fo + v.x * fn;
-    acc.y = acc.y * fo + v.y * fn;
-    acc.z = acc.z * fo + v.z * fn;
-    acc.w = acc.w * fo + v.w * fn;
-  }
-};
-
 // columns 4 col .. of row r of the item: written from its sums
 __device__ __forceinline__ void join_row(const JoinArgs& a, const Left& f, int r, int col, const Sum& x) {
-  const float inv = x.L > 0.f ? __fdividef(1.f, x.L) : 0.f;
   const int rho = f.rho0 + r, token = a.rep.of(rho);
-  const size_t at = (size_t)(f.row0 + token) * a.H + f.head * a.rep.d + rho - token * a.rep.d;
-  if (col == 0) a.LSE[at] = x.L > 0.f ? (x.M + __log2f(x.L)) * LN2 : -INFINITY;
-  if (col * 4 >= a.Dv) return;
-  if (a.out_bf16)
-    *reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(a.O) + at * a.Dv + col * 4) =
-        make_uint2(bf2(x.acc.x * inv, x.acc.y * inv), bf2(x.acc.z * inv, x.acc.w * inv));
-  else
-    *reinterpret_cast<float4*>(static_cast<float*>(a.O) + at * a.Dv + col * 4) =
-        make_float4(x.acc.x * inv, x.acc.y * inv, x.acc.z * inv, x.acc.w * inv);
+  x.write(a.O, a.LSE, (size_t)(f.row0 + token) * a.H + f.head * a.rep.d + rho - token * a.rep.d, col * 4, a.Dv, a.out_bf16);
 }
 
 // `where`: the worker of the CTA that left the item open, + 16 if in its slot 1. ALL: by all
@@ -686,7 +672,7 @@ __device__ __forceinline__ void join_item(const JoinArgs& a, int where, int last
         }
 #pragma unroll
         for (int u = 0; u < U; ++u)
-          if (p + u < p1 && y[u].y > 0.f) x.add(y[u].x, y[u].y, v[u]);
+          if (p + u < p1 && !(y[u].y == 0.f)) x.add(y[u].x, y[u].y, v[u]);
       }
     }
     if (ALL) {
@@ -769,7 +755,7 @@ __device__ __forceinline__ void join_rows(const JoinArgs& a, const Left* open, c
         for (int u = 0; u < U; ++u)
 #pragma unroll
           for (int i = 0; i < ROWS; ++i)
-            if (p + u < parts && y[u][i].y > 0.f) x[i].add(y[u][i].x, y[u][i].y, v[u][i]);
+            if (p + u < parts && !(y[u][i].y == 0.f)) x[i].add(y[u][i].x, y[u][i].y, v[u][i]);
       }
 #pragma unroll
       for (int i = 0; i < ROWS; ++i)

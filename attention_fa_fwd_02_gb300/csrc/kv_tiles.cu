@@ -563,9 +563,9 @@ __global__ void __launch_bounds__(TilesCfg<D>::THREADS, 1)
         const int cols = whole ? a.c.D : D;
         const size_t row_bytes = (size_t)cols * (bf ? 2 : 4);
         auto ptr = [&](int r) -> char* { return r < warp_rows ? to + at(wq * 32 + r) * row_bytes : nullptr; };
-        const float inv = !whole ? 1.f : l > 0.f ? __fdividef(1.f, l) : 0.f;
+        const float inv = !whole ? 1.f : l == 0.f ? 0.f : __fdividef(1.f, l);  // (NaN stays)
         if (r_in < rows) {
-          if (whole) a.LSE[at(r_in)] = l > 0.f ? (m + __log2f(l)) * LN2 : -INFINITY;
+          if (whole) a.LSE[at(r_in)] = l == 0.f ? -INFINITY : (m + __log2f(l)) * LN2;
           else a.part.ml[at(r_in)] = make_float2(m, l);
         }
         if (bf) store_rows<D, true>(o_addr, n > 0, inv, stage, cols, ptr);

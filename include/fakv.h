@@ -156,7 +156,8 @@ FA_API fa_status fakv_append(const void* q, const void* k, const void* v, void* 
 /* O [T, H, D] = softmax(scale q K^T + mask) V over the tokens of each row's sequence, LSE
  * [T, H] (natural log) fp32; contiguous. Query head h reads kv head h / (H / HKV). q in the
  * cache's dtype. A row that sees no key gets O = 0, LSE = -inf. K and V within a
- * sequence's length must be finite; page memory past it may hold anything. fp32 caches
+ * sequence's length must be finite; page memory past it may hold anything. NaN or infinity
+ * in a row of q makes that row's O and LSE NaN and no other's. fp32 caches
  * use three tf32 products per GEMM (about 22 significant bits); bf16 caches bf16 products
  * with fp32 sums, the probabilities in bf16: two terms (2^-16) where O is fp32 or there are few
  * rows, one (2^-8, about a bf16 O's own rounding) where there are many and O is bf16. Sums
