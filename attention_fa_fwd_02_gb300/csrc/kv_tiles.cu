@@ -16,6 +16,11 @@
 //   warp 9, 10    producers: Q and K, V (and the epilogue's stages)
 //   warp 11       relay of landed copies to the issuer; it also zeroes V's rows past a
 //                 sequence's end, whose memory may hold anything (0 x NaN)
+// A wait that runs out raises the CTA's abort flag. Named barriers have no limit, so their
+// rounds are all joined nevertheless: the relay and the issuer go on with whatever the stages
+// hold, and the softmax warps wait for the issuer whatever the flag says (a warp that gave up
+// between two rounds could complete a neighbour's); producers and epilogues, whose waits are
+// all on mbarriers, stop. tests/test_kv_tiles_sync_model.py replays all of it.
 // P is one bf16 term where O is bf16: its rounding, at most 2^-8 of a probability and
 // random in sign, adds to O about what O's own rounding does (2048 tokens over 16384: O is
 // 2.4e-3 of its size from the 64-bit values, 1.7e-3 of that its own rounding), and a second
@@ -77,7 +82,7 @@ struct TilesCfg {
   static constexpr uint32_t V_OFF = K_OFF + KST * TILE_BYTES;
   static constexpr uint32_t SMEM = V_OFF + VST * V_STAGE + 1024;
   static constexpr int SOFTMAX_WARPS = 8, MMA_WARP = 8, KQ_WARP = 9, V_WARP = 10, RELAY_WARP = 11;
-  static constexpr uint32_t RELAY_BAR = 3, EPI_JOIN = 6;  // named barriers (1 + q: P_q written)
+  static constexpr uint32_t RELAY_BAR = 3;  // named barrier (1 + q: P_q written)
   static constexpr int THREADS = 384;
   static constexpr uint32_t REGS_SOFTMAX = 216, REGS_CONTROL = 64;
   static_assert(2 * 128 * REGS_SOFTMAX + 128 * REGS_CONTROL <= 384 * 168, "register split exceeds the launch allocation");
@@ -190,13 +195,14 @@ __global__ void __launch_bounds__(TilesCfg<D>::THREADS, 1)
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   __shared__ __align__(8) uint64_t bar_q[NQ], bar_qfree[NQ], bar_kfull[KST], bar_kempty[KST], bar_vfull[VST],
-      bar_vempty[VST], bar_grant[NQ], bar_s[NQ], bar_o[NQ], bar_drain;
+      bar_vempty[VST], bar_grant[NQ], bar_s[NQ], bar_o[NQ], bar_join, bar_drain;
   __shared__ uint32_t tmem_base_sh;
-  __shared__ int abort_sh;
+  __shared__ int abort_sh, stuck_sh;
   __shared__ PlanShared<C::THREADS, 1> plan;
   grid_launch_dependents();
   const int warp = warp_id(), lane = lane_id();
   volatile int* abort_flag = &abort_sh;
+  volatile int* stuck_flag = &stuck_sh;
   if (threadIdx.x == 0) {
     for (int q = 0; q < NQ; ++q) {
       mbar_init(&bar_q[q], 1);
@@ -207,8 +213,9 @@ __global__ void __launch_bounds__(TilesCfg<D>::THREADS, 1)
     }
     for (int s = 0; s < KST; ++s) { mbar_init(&bar_kfull[s], 1); mbar_init(&bar_kempty[s], 1); }
     for (int s = 0; s < VST; ++s) { mbar_init(&bar_vfull[s], 1); mbar_init(&bar_vempty[s], 1); }
+    mbar_init(&bar_join, C::SOFTMAX_WARPS);
     mbar_init(&bar_drain, 1);
-    abort_sh = 0;
+    abort_sh = stuck_sh = 0;
     fence_mbar_init();
   }
   if (threadIdx.x < 2) a.part.left[2 * blockIdx.x + threadIdx.x].flags = 0;
@@ -231,6 +238,12 @@ __global__ void __launch_bounds__(TilesCfg<D>::THREADS, 1)
   auto sV = [&](int st) { return sbase + C::V_OFF + st * C::V_STAGE; };
   auto wait = [&](uint64_t* bar, uint32_t parity) {
     return mbar_wait(bar, parity, abort_flag, &g_kv_status, DEV_TIMEOUT, a.limit_ns);
+  };
+  // of a producer: a stage given back after an abort is not filled again
+  auto wait_free = [&](uint64_t* bar, uint32_t parity) { return wait(bar, parity) && !*abort_flag; };
+  // for the issuer, who goes on after an abort (all other waits have run out by twice their limit)
+  auto wait_issuer = [&](uint64_t* bar, uint32_t parity) {
+    return mbar_wait(bar, parity, stuck_flag, &g_kv_status, DEV_TIMEOUT, 2 * a.limit_ns);
   };
   auto drain = [&](uint64_t* bar, uint32_t parity) {
     const uint64_t t0 = globaltimer();
@@ -278,13 +291,13 @@ __global__ void __launch_bounds__(TilesCfg<D>::THREADS, 1)
         for (int t = 0; t < seg.n; ++t, ++g) {
           const int kt = seg.k0 + t, ks = g % KST;
           const int page_next = t + 1 < seg.n ? page_for(kt + 1) : 0;  // (on its way while this tile waits)
-          if (!(ok = __all_sync(0xffffffffu, wait(&bar_kempty[ks], ((g / KST) & 1) ^ 1)))) break;
+          if (!(ok = __all_sync(0xffffffffu, wait_free(&bar_kempty[ks], ((g / KST) & 1) ^ 1)))) break;
           load_tile(sK(ks), &tmK, &bar_kfull[ks], kt, page);
           last_k[ks] = g / KST;
           page = page_next;
           if (t == 0) {
             for (int q = 0; ok && q < NQ; ++q) {
-              if (j > 0 && !(ok = __all_sync(0xffffffffu, wait(&bar_qfree[q], (j - 1) & 1)))) break;
+              if (j > 0 && !(ok = __all_sync(0xffffffffu, wait_free(&bar_qfree[q], (j - 1) & 1)))) break;
               if (lane == 0) {
                 mbar_arrive_expect_tx(&bar_q[q], C::NCB * 128u * a.RT);
                 for (int cb = 0; cb < C::NCB; ++cb)
@@ -316,7 +329,7 @@ __global__ void __launch_bounds__(TilesCfg<D>::THREADS, 1)
       auto wait_release = [&](uint32_t p) {
         const int s = p % VST, u = p / VST;
         if (seen[s] > u) return true;
-        if (!__all_sync(0xffffffffu, wait(&bar_vempty[s], u & 1))) return false;
+        if (!__all_sync(0xffffffffu, wait_free(&bar_vempty[s], u & 1))) return false;
         seen[s] = u + 1;
         return true;
       };
@@ -440,15 +453,17 @@ __global__ void __launch_bounds__(TilesCfg<D>::THREADS, 1)
     const uint32_t s_addr = lane_addr + C::s_col(q);
     const uint32_t o_addr = lane_addr + C::o_col(q);
     const float sl2 = a.sl2;
-    bool ok = true;
+    bool ok = true, live = true;  // epilogues are granted; the issuer goes on
     int g = 0, j = 0, k = 0;
     uint32_t pos = 0;
+    // One warp gives the epilogue's stage back, once all have read their parts of it: after its
+    // next hand-off, so that the next P does not wait for it.
     bool pending = false;
-    int pend_slot = 0;
+    int pend_slot = 0, pend_item = 0;
     auto release = [&]() {
+      if (ok) ok = __all_sync(0xffffffffu, wait(&bar_join, pend_item & 1));
+      if (ok && lane == 0) mbar_arrive(&bar_vempty[pend_slot]);
       __syncwarp();
-      named_bar_sync(C::EPI_JOIN, 128 * NQ);
-      if (wq == 0 && lane == 0) mbar_arrive(&bar_vempty[pend_slot]);
       pending = false;
     };
     for (; next(); ++k) {
@@ -466,8 +481,8 @@ __global__ void __launch_bounds__(TilesCfg<D>::THREADS, 1)
       const int in_lo = a.g.window > 0 ? p1 - a.g.window + 1 : 0;
       float m = -FLT_MAX, l = 0.f;
       for (int t = 0; t < n; ++t, ++g) {
-        if (ok) ok = __all_sync(0xffffffffu, wait(&bar_s[q], g & 1));
-        if (!ok) {
+        if (live) live = __all_sync(0xffffffffu, wait_issuer(&bar_s[q], g & 1));
+        if (!live) {
           named_bar_sync(1 + q, 128 + 32);  // every round is joined, whatever happens
           if (pending) release();
           continue;
@@ -539,11 +554,12 @@ __global__ void __launch_bounds__(TilesCfg<D>::THREADS, 1)
       }
       pos += n;
       if (n > 0) {
-        if (ok) ok = __all_sync(0xffffffffu, wait(&bar_o[q], j & 1));
+        if (live) live = __all_sync(0xffffffffu, wait_issuer(&bar_o[q], j & 1));
         tc_fence_after();
         ++j;
       }
       if (pending) release();
+      ok = ok && live;
       // ---- epilogue, staged in this tile's half of the item's V ring stage
       const int slot = pos % VST;
       if (ok) ok = __all_sync(0xffffffffu, wait(&bar_grant[q], k & 1));
@@ -575,12 +591,12 @@ __global__ void __launch_bounds__(TilesCfg<D>::THREADS, 1)
               (seg.starts ? PART_STARTS : 0) | (seg.ends ? PART_ENDS : 0), seg.s.row0, seg.x.rho0,
               seg.x.rows, seg.head, walk.p.ender, {0, 0}};
       }
-      if (q < NQ - 1) {
-        if (ok) named_bar_arrive(C::EPI_JOIN, 128 * NQ);
-        else named_bar_sync(C::EPI_JOIN, 128 * NQ);
-      } else {
+      __syncwarp();
+      if (ok && lane == 0) mbar_arrive(&bar_join);  // this warp has read its part of the stage
+      if (q == NQ - 1 && wq == 0) {
         pending = true;
         pend_slot = slot;
+        pend_item = k;
       }
       pos += 1;
     }
