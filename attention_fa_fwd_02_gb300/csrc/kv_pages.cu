@@ -63,12 +63,12 @@ __device__ __forceinline__ int pages_of(int tokens, int shift) {
   return (int)(((long long)tokens + (1 << shift) - 1) >> shift);
 }
 
-// a slot's length, 0 and the status bit where it is no length of a row
+// a slot's length; -1 and the status bit where it is no length of a row: its entry is left out
 __device__ __forceinline__ int length_of(const fakv_cache& c, int slot) {
   const int len = c.lens[slot];
   if (len >= 0 && (long long)len <= (long long)c.max_pages * c.page_size) return len;
   raise(c.status, FAKV_BAD_LENGTH);
-  return 0;
+  return -1;
 }
 
 // ------------------------------------------------------------------ page copies
@@ -197,7 +197,8 @@ __global__ void __launch_bounds__(PLAN) grow_kernel(const __grid_constant__ Grow
     if (slot >= 0) {
       len = length_of(a.c, slot);
       add = a.add[i];
-      if (add < 0) { raise(a.c.status, FAKV_BAD_LENGTH); slot = -1; }
+      if (add < 0) raise(a.c.status, FAKV_BAD_LENGTH);
+      if (len < 0 || add < 0) slot = -1;
     }
     if (slot >= 0) {
       old = pages_of(len, a.shift);
@@ -342,10 +343,14 @@ __global__ void __launch_bounds__(256) fork_take_kernel(const __grid_constant__ 
       if (threadIdx.x == 0) raise(a.c.status, FAKV_BAD_SLOT);
       ok = false;
     }
-    const int len = ok ? length_of(a.c, src) : -1;
+    int len = -1;
+    if (ok) {
+      len = length_of(a.c, src);
+      if (length_of(a.c, dst) < 0) len = -1;
+    }
     if (threadIdx.x == 0) a.lens[i] = len;
     const int* row = a.c.table + (long long)src * a.c.table_stride;
-    for (int k = threadIdx.x; ok && k < pages_of(len, a.shift); k += blockDim.x) {
+    for (int k = threadIdx.x; len > 0 && k < pages_of(len, a.shift); k += blockDim.x) {
       const int p = row[k];
       a.rows[(long long)i * a.c.max_pages + k] = p;
       if ((unsigned)p < (unsigned)a.c.num_pages) atomicAdd(&a.c.refs[p], 1);
@@ -371,7 +376,7 @@ __global__ void __launch_bounds__(256) fork_give_kernel(const __grid_constant__ 
     if (len < 0) continue;
     const int dst = a.dst[i];
     int* row = a.c.table + (long long)dst * a.c.table_stride;
-    release(a.c, row, 0, pages_of(length_of(a.c, dst), a.shift));
+    release(a.c, row, 0, pages_of(a.c.lens[dst], a.shift));
     __syncthreads();
     for (int k = threadIdx.x; k < pages_of(len, a.shift); k += blockDim.x)
       row[k] = a.rows[(long long)i * a.c.max_pages + k];
@@ -398,8 +403,10 @@ __global__ void __launch_bounds__(PLAN) fork_short_kernel(const __grid_constant_
     if (!ok && lane == 0) raise(a.c.status, in && again ? FAKV_REPEATED : FAKV_BAD_SLOT);
     if (ok) {
       len = length_of(a.c, src);
-      now = pages_of(len, a.shift);
-      was = pages_of(length_of(a.c, dst), a.shift);
+      const int held_len = length_of(a.c, dst);
+      if (held_len < 0) len = -1;
+      now = len < 0 ? 0 : pages_of(len, a.shift);
+      was = len < 0 ? 0 : pages_of(held_len, a.shift);
       const int* from = a.c.table + (long long)src * a.c.table_stride;
       const int* to = a.c.table + (long long)dst * a.c.table_stride;
 #pragma unroll
@@ -438,6 +445,7 @@ __global__ void __launch_bounds__(256) free_kernel(const __grid_constant__ ListA
     const int slot = a.dst[i];
     if (!entry_ok(a.c, a.dst, i, slot)) continue;
     const int len = length_of(a.c, slot);
+    if (len < 0) continue;
     int keep = a.keep ? a.keep[i] : 0;
     if (keep < 0) {
       if (threadIdx.x == 0) raise(a.c.status, FAKV_BAD_LENGTH);

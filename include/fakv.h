@@ -26,8 +26,9 @@
  *
  * What only the device can see is checked there: a slot outside [0, max_slots), a page
  * number outside [0, num_pages) where a token should be, a length beyond the row. Such
- * an entry is left out (keys read as zeros, tokens not written) and a bit is set in
- * `*status`, which the caller reads and clears. No access leaves the arrays described.
+ * an entry is left out (keys read as zeros, tokens not written; in the page calls its
+ * slot's length, row and counts stay as they were) and a bit is set in `*status`, which
+ * the caller reads and clears. No access leaves the arrays described.
  *
  * Every call checks its arguments, enqueues on `stream` and returns. Temporary buffers come
  * stream-ordered from the library's pool, so calls on different streams, and graphs, do not
