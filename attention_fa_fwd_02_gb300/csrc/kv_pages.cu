@@ -449,7 +449,7 @@ __global__ void __launch_bounds__(256) free_kernel(const __grid_constant__ ListA
     int keep = a.keep ? a.keep[i] : 0;
     if (keep < 0) {
       if (threadIdx.x == 0) raise(a.c.status, FAKV_BAD_LENGTH);
-      keep = 0;
+      continue;
     }
     keep = min(keep, len);
     __syncthreads();  // every thread has read the length

@@ -77,3 +77,12 @@ def test_free_leaves_out_a_bad_length(kv, length):
         m.same(cache, (length, keep))
         m.bits = 0
         assert bits(kv, cache) == kv.BAD_LENGTH
+
+
+def test_free_leaves_out_a_negative_keep(kv):
+    cache = small(kv)
+    m = ref.Model(cache)
+    cache.free(vec(0, 1, 2), vec(3, -1, -(1 << 31)))
+    m.free([0], [3])
+    m.bits = kv.BAD_LENGTH
+    m.same(cache, "keep")
