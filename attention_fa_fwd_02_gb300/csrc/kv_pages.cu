@@ -208,9 +208,10 @@ __global__ void __launch_bounds__(PLAN) grow_kernel(const __grid_constant__ Grow
       } else {
         if (add > 0 && (len & (a.c.page_size - 1))) {
           const int p = page_of(a.c, slot, len, a.shift);
-          if (p >= 0 && a.c.refs[p] > 1) tail = p;
+          if (p < 0) slot = -1;  // the new tokens would have no place
+          else if (a.c.refs[p] > 1) tail = p;
         }
-        need = pages_of(len + add, a.shift) - old + (tail >= 0);
+        if (slot >= 0) need = pages_of(len + add, a.shift) - old + (tail >= 0);
       }
     }
     unsigned total;

@@ -173,8 +173,9 @@ FA_API fa_status fakv_attend(const void* q, void* O, float* LSE, const int* cu, 
 /* Room for add[i] >= 0 more tokens in slots[i], and lens grown by it. New pages are the
  * lowest free ones, in the order of the list. A last page that has room but is shared
  * (refs > 1 when the call starts) is first replaced by a copy, in every plane. An entry
- * is not served (its length stays) if its row is too short or, with the entries before
- * it, it needs more pages than were free. */
+ * is not served (its length stays) if its row is too short, if the last page that its new
+ * tokens begin in is missing or, with the entries before it, it needs more pages than were
+ * free. */
 FA_API fa_status fakv_grow(const fakv_cache* cache, const int* slots, const int* add, int n,
                            fa_stream_t stream);
 

@@ -50,6 +50,27 @@ def test_grow_leaves_out_a_bad_length(kv, length):
     m.same(cache, length)
 
 
+@pytest.mark.parametrize("page", [-1, 1 << 20, -(1 << 31)])
+def test_grow_leaves_out_a_missing_last_page(kv, page):
+    cache = small(kv)
+    cache.table[1, 1] = page  # slot 1: 9 tokens, the ninth on this page
+    before = state(cache)
+    cache.grow(vec(1), vec(3))
+    assert bits(kv, cache) == kv.BAD_PAGE and state(cache) == before
+    cache.grow(vec(1), vec(30))  # (also where new pages would come after it)
+    assert bits(kv, cache) == kv.BAD_PAGE and state(cache) == before
+    m = ref.Model(cache)
+    cache.grow(vec(1, 2, 0), vec(9, 9, 9))  # its neighbours are served, with the lowest pages
+    m.grow([2, 0], [9, 9])
+    got = state(cache)
+    assert got[0] == m.lens and got[2] == m.refs and got[1][1] == before[1][1]
+    for s in (0, 2):
+        assert [p for p in got[1][s] if p >= 0] == m.rows[s]
+    assert bits(kv, cache) == kv.BAD_PAGE
+    cache.grow(vec(1), vec(0))  # nothing new, nothing looked at
+    cache.check()
+
+
 # one launch for short lists of short rows, two for the rest
 @pytest.mark.parametrize("max_pages", [9, 300])
 @pytest.mark.parametrize("who", ["source", "destination"])
