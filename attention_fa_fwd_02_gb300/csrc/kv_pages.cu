@@ -464,7 +464,6 @@ __global__ void __launch_bounds__(256) free_kernel(const __grid_constant__ ListA
 struct CompactArgs {
   fakv_cache c;
   CopyArgs copy;
-  int shift;
   int* to;     // scratch [num_pages]: where a page went
   int2* pair;  // scratch [num_pages]
   int* count;  // scratch: how many moves
@@ -535,13 +534,17 @@ __global__ void __launch_bounds__(PLAN) compact_plan_kernel(const __grid_constan
   if (tid == 0) a.count[0] = movers;
 }
 
-// the rows renumbered and the pages moved (sources lie above every destination)
+// The rows renumbered and the pages moved (sources lie above every destination). Whole rows, a
+// step of STEP entries at a time: an entry past its row's length goes on naming its page too.
 __global__ void __launch_bounds__(COPY_THREADS) compact_move_kernel(const __grid_constant__ CompactArgs a) {
   ptx::grid_dependency_wait();
-  for (int s = blockIdx.x; s < a.c.max_slots; s += gridDim.x) {
-    int* row = a.c.table + (long long)s * a.c.table_stride;
-    const int n = min(a.c.max_pages, pages_of(max(0, a.c.lens[s]), a.shift));
-    for (int k = threadIdx.x; k < n; k += blockDim.x) {
+  constexpr int STEP = 1024;
+  const long long steps = (a.c.max_pages + STEP - 1) / STEP;
+  for (long long w = blockIdx.x; w < a.c.max_slots * steps; w += gridDim.x) {
+    const long long s = w / steps;
+    const int from = (int)(w - s * steps) * STEP;
+    int* row = a.c.table + s * a.c.table_stride;
+    for (int k = from + threadIdx.x; k < min(a.c.max_pages, from + STEP); k += blockDim.x) {
       const int p = row[k];
       if ((unsigned)p < (unsigned)a.c.num_pages) {
         const int q = a.to[p];
@@ -622,7 +625,7 @@ fa_status launch_free(const fakv_cache& c, const int* slots, const int* keep, in
 fa_status launch_compact(const fakv_cache& c, cudaStream_t s) {
   Scratch w((size_t)c.num_pages * 12 + 16, s);
   if (!w.ok) return failed();
-  CompactArgs a = {c, copy_args(c), log2_of(c.page_size), reinterpret_cast<int*>(w.p + (size_t)c.num_pages * 8),
+  CompactArgs a = {c, copy_args(c), reinterpret_cast<int*>(w.p + (size_t)c.num_pages * 8),
                    reinterpret_cast<int2*>(w.p), reinterpret_cast<int*>(w.p + (size_t)c.num_pages * 12)};
   {
     host::KernelTimer t("compact_plan", s);

@@ -7,7 +7,9 @@
  * The cache. Keys and values live in pages of `page_size` tokens. A slot is one
  * sequence: row s of `table` holds the page numbers of its tokens in order, lens[s] its
  * length in tokens. refs[p] counts the rows that hold page p (0: free), so sequences
- * with a common beginning may share pages. All of it is device memory that the caller
+ * with a common beginning may share pages. A row holds the pages of its lens[s] tokens:
+ * entries past them are -1, or are not counted on by grow, fork and free (grow writes over
+ * them), so a length is lowered by fakv_free, which releases what is no longer needed. All of it is device memory that the caller
  * owns, and every call reads lengths, tables and counts on the device: a step's calls
  * (grow, append, attend) can be captured into a CUDA graph once and replayed while the
  * lengths move on. Calls on one cache must be ordered (one stream, or events).
@@ -190,8 +192,8 @@ FA_API fa_status fakv_free(const fakv_cache* cache, const int* slots, const int*
                            fa_stream_t stream);
 
 /* With L pages in use, the used pages numbered L and above move, in order, to the free
- * numbers below L (in every plane), and all rows and counts follow: pages 0 .. L - 1 are
- * then the used ones. */
+ * numbers below L (in every plane), and all rows (over their whole width, whatever their
+ * lengths) and counts follow: pages 0 .. L - 1 are then the used ones. */
 FA_API fa_status fakv_compact(const fakv_cache* cache, fa_stream_t stream);
 
 #ifdef __cplusplus

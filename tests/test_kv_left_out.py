@@ -107,3 +107,60 @@ def test_free_leaves_out_a_negative_keep(kv):
     m.free([0], [3])
     m.bits = kv.BAD_LENGTH
     m.same(cache, "keep")
+
+
+def test_compact_leaves_rows_of_bad_lengths_in_place(kv):
+    # their pages are counted and move with the others
+    cache = small(kv)
+    m = ref.Model(cache)
+    m.free([0, 2])
+    cache.free(vec(0, 2))
+    cache.lens[1], cache.lens[3] = -3, 1 << 30
+    m.compact()
+    cache.compact()
+    m.lens[1], m.lens[3] = -3, 1 << 30
+    m.same(cache, "compact")
+
+
+def test_compact_renumbers_whole_rows(kv):
+    """Entries past a row's length (a length lowered by hand, pages in reserve) go on naming the page they named."""
+    cache = ref.make_cache(kv, [40, 70, 64, 33], 8, 1, 16, BF)
+    held = [[int(p) for p in r if p >= 0] for r in cache.table.tolist()]
+    k0 = cache.k.clone()
+    cache.free(vec(0))
+    cache.lens[1] = 17   # of 9 pages, 3 by its length
+    cache.lens[3] = 0
+    cache.compact()
+    cache.check()
+    rows = cache.table.tolist()
+    assert rows[0] == [-1] * len(rows[0])
+    live = int((cache.refs > 0).sum())
+    assert bool((cache.refs[:live] == 1).all()) and bool((cache.refs[live:] == 0).all())
+    seen = []
+    for s in (1, 2, 3):
+        now = [p for p in rows[s] if p >= 0]
+        assert len(now) == len(held[s]) and rows[s][len(now):] == [-1] * (len(rows[s]) - len(now))
+        seen += now
+        for a, b in zip(held[s], now):
+            assert torch.equal(k0[:, a].nan_to_num(nan=7.0), cache.k[:, b].nan_to_num(nan=7.0))
+    assert sorted(seen) == list(range(live))
+
+
+def test_compact_of_rows_wider_than_a_step(kv):
+    # entries on both sides of every 1024th column, in rows whose lengths end before them
+    n, pages = 3, 600
+    cache = kv.PagedCache.create(1, pages, 8, 1, 16, n, 4100)
+    at = [0, 1, 1022, 1023, 1024, 2047, 2048, 4000, 4095, 4096, 4099]
+    used = list(range(1, pages, 2))
+    table = torch.full((n, 4100), -1, dtype=torch.int32)
+    for s in range(n):
+        for i, c in enumerate(at):
+            table[s, c] = used[(s * len(at) + i) * 7]
+    cache.table.copy_(table)
+    cache.refs[used] = 1
+    m = ref.Model(cache)
+    m.rows = table.tolist()
+    m.compact()
+    cache.compact()
+    assert cache.table.tolist() == m.rows and cache.refs.tolist() == m.refs and cache.lens.tolist() == [0] * n
+    cache.check()
