@@ -8,7 +8,7 @@ CUDA kernels.
     for layer in range(layers):
         q = cache.append(q, k, v, cu, slots, rope=rope, layer=layer)   # K, V written, q and k rotated
         o, lse = cache.attend(q, cu, slots, layer=layer)
-    cache.check()                                           # raises if the device refused an entry
+    cache.check()                                           # raises if the device refused an entry, or gave up a wait
 
 Tokens of a step are the rows of ``q`` [T, H, D], ``k`` and ``v`` [T, HKV, D]; sequence b has rows
 cu[b] .. cu[b + 1] - 1 and is slot slots[b] (None: slot b). Everything that changes from step to step is
@@ -392,8 +392,16 @@ class PagedCache:
             on.leave()
 
     def check(self) -> None:
-        """Waits for the device and raises CacheError if it refused an entry since the last check."""
+        """Waits for the device (all its streams). Raises CacheError if a call on this cache refused an entry since the
+        last check, and fa.FAError if a wait in one of the library's kernels ran out: outputs may then be unwritten."""
+        torch.cuda.synchronize(self.device)
         bits = int(self.status.item())
         if bits:
             self.status.zero_()
+            torch.cuda.synchronize(self.device)
             raise CacheError(bits)
+        on = _on(self._index, None)
+        try:
+            _check(fa.fa_device_status(on.handle), "fa_device_status")
+        finally:
+            on.leave()

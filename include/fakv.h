@@ -31,6 +31,8 @@
  * an entry is left out (keys read as zeros, tokens not written; in the page calls its
  * slot's length, row and counts stay as they were) and a bit is set in `*status`, which
  * the caller reads and clears. No access leaves the arrays described.
+ * A wait inside a kernel that ran out (fa.h) is no bit of it: fa_device_status tells, and
+ * outputs of the call may then be unwritten.
  *
  * Every call checks its arguments, enqueues on `stream` and returns. Temporary buffers come
  * stream-ordered from the library's pool, so calls on different streams, and graphs, do not
