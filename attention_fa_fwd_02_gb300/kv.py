@@ -113,17 +113,21 @@ def _check(rc: int, where: str) -> None:
 
 class _on:
     """The device of a call's tensors made current for as long as the call, and the handle of its stream: ``stream``,
-    or that device's current one."""
+    or that device's current one. The memory of ``tensors`` is not handed out again before a ``stream`` of the call's
+    own has passed it (the work that makes them ready is the caller's to order)."""
 
     __slots__ = ("back", "stream", "handle")
 
-    def __init__(self, index, stream):
+    def __init__(self, index, stream, *tensors):
         self.back, self.stream = -1, stream
         current = _current_device()
         if stream is not None:
             if stream.device_index != index:
                 raise ValueError("the stream belongs to another device than the tensors")
             self.handle = stream.cuda_stream
+            for t in tensors:
+                if t is not None and t.is_cuda:
+                    t.record_stream(stream)
         else:
             self.handle = _raw_stream(index)
         if current != index:
@@ -223,7 +227,7 @@ class Rope:
         if not (wide or positions.dtype == torch.int32) or positions.shape != (T,) or positions.device != dev \
                 or not positions.is_contiguous():
             raise ValueError(f"positions must be a contiguous int32 or int64 vector of {T} on {dev}")
-        on = _on(dev.index, stream)
+        on = _on(dev.index, stream, q, k, positions, self.freqs, *(out or ()))
         try:
             if out is None:
                 qo, ko = on.empty(q, q.shape, dt), None if k is None else on.empty(q, k.shape, dt)
@@ -275,6 +279,7 @@ class PagedCache:
         self.k, self.v, self.table, self.lens, self.refs, self.device = k, v, table, lens, refs, dev
         self.planes, self.page_size, self.kv_heads, self.head_dim = k.shape[0], k.shape[t], k.shape[h], k.shape[4]
         self.slots, self.dtype, self._index = table.shape[0], k.dtype, dev.index
+        self._tensors = (k, v, table, lens, refs, self.status)
         self._c = fakv_cache(k.data_ptr(), v.data_ptr(), table.data_ptr(), lens.data_ptr(), refs.data_ptr(),
                              self.status.data_ptr(), k.stride(0), k.stride(1), k.stride(t), k.stride(h),
                              table.stride(0), k.shape[0], k.shape[1], k.shape[t], k.shape[h], k.shape[4],
@@ -320,7 +325,7 @@ class PagedCache:
             qp = q.data_ptr()
         if rope is not None and (rope.head_dim != D or rope.freqs.device != dev):
             raise ValueError("rope is for another head_dim or device")
-        on = _on(self._index, stream)
+        on = _on(self._index, stream, q, k, v, cu, slots, out, None if rope is None else rope.freqs, *self._tensors)
         try:
             if q is not None:
                 o = on.empty(q, q.shape, dt) if out is None else _out(out, "out", q.shape, dt, dev)
@@ -343,7 +348,7 @@ class PagedCache:
         odt = out_dtype if out_dtype is not None else dt if out is None else out.dtype
         if odt not in _DT:
             raise TypeError(f"unsupported output dtype {odt}")
-        on = _on(self._index, stream)
+        on = _on(self._index, stream, q, cu, slots, out, lse, *self._tensors)
         try:
             out = on.empty(q, shape, odt) if out is None else _out(out, "out", shape, odt, dev)
             lse = on.empty(q, shape[:2], torch.float32) if lse is None \
@@ -363,7 +368,7 @@ class PagedCache:
         if b is not None:
             _ints(b, names[1], n, self.device)
             bp = b.data_ptr()
-        on = _on(self._index, stream)
+        on = _on(self._index, stream, a, b, *self._tensors)
         try:
             _check(call(self._ref, a.data_ptr(), bp, n, on.handle), where)
         finally:
@@ -385,7 +390,7 @@ class PagedCache:
 
     def compact(self, stream=None):
         """Moves pages so that those in use are the lowest-numbered ones, and renumbers the table."""
-        on = _on(self._index, stream)
+        on = _on(self._index, stream, *self._tensors)
         try:
             _check(_lib().fakv_compact(self._ref, on.handle), "fakv_compact")
         finally:

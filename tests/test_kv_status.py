@@ -53,3 +53,45 @@ def test_check_waits_for_every_stream(kv):
     with pytest.raises(kv.CacheError):
         cache.check()
     cache.check()
+
+
+def test_inputs_dropped_while_another_stream_reads_them(kv):
+    """A tensor given to a call on another stream and dropped is not handed out again before the call has read it."""
+    cache = ref.make_cache(kv, [100, 900], 16, 2, 64, BF)
+    rope = kv.Rope(64)
+    cu, pos = vec(0, 3, 6), torch.arange(6).cuda()
+    keep = torch.randn(6, 8, 64, generator=torch.Generator().manual_seed(1)).to(BF).cuda()
+    want, want_l = cache.attend(keep, cu)
+    want_r = rope.apply(keep, None, pos)[0]
+    s = torch.cuda.Stream()
+    for call, expect in ((lambda x: cache.attend(x, cu, stream=s)[0], want),
+                         (lambda x: rope.apply(x, None, pos, stream=s)[0], want_r),
+                         (lambda x: cache.append(x, x[:, :2], x[:, 2:4], cu, stream=s), keep)):
+        q = keep.clone()
+        address = q.data_ptr()
+        torch.cuda.synchronize()
+        with torch.cuda.stream(s):
+            torch.cuda._sleep(100_000_000)
+        got = call(q)
+        del q
+        other = [torch.full_like(keep, 9.0) for _ in range(20)]  # on the current stream, at once
+        torch.cuda.current_stream().wait_stream(s)
+        assert all(x.data_ptr() != address for x in other)
+        assert torch.equal(got, expect)
+
+
+def test_a_cache_dropped_while_another_stream_reads_it(kv):
+    q = torch.randn(1, 4, 64, generator=torch.Generator().manual_seed(1)).to(BF).cuda()
+    cu, s = vec(0, 1), torch.cuda.Stream()
+    cache = ref.make_cache(kv, [900], 16, 2, 64, BF)
+    want = cache.attend(q, cu)[0]
+    addresses, shape = {cache.k.data_ptr(), cache.v.data_ptr()}, cache.k.shape
+    torch.cuda.synchronize()
+    with torch.cuda.stream(s):
+        torch.cuda._sleep(100_000_000)
+    got = cache.attend(q, cu, stream=s)[0]
+    del cache
+    other = [torch.full(shape, 9.0, dtype=BF, device="cuda") for _ in range(8)]
+    torch.cuda.current_stream().wait_stream(s)
+    assert not addresses & {x.data_ptr() for x in other}
+    assert torch.equal(got, want)
