@@ -173,6 +173,17 @@ __global__ void __launch_bounds__(MAX_THREADS, 2) rope_kernel(const __grid_const
     }
   }
 
+  if constexpr (APPEND) {
+    // One block looks over the whole of cu (no row need lie where it decreases): its warps but the
+    // first, whose look-ups for a token take longer.
+    const int first = blockDim.x > 32 ? 32 : 0;
+    if (blockIdx.x == 0 && blockIdx.y == 0 && threadIdx.x >= first) {
+      bool falls = false;
+      for (int b = threadIdx.x - first; b < a.B; b += blockDim.x - first) falls |= a.cu[b + 1] < a.cu[b];
+      if (falls) raise(a.c.status, FAKV_BAD_LENGTH);
+    }
+  }
+
   // positions, places, cos and sin of the block's tokens, a warp per token
   for (int k = threadIdx.x / 32; k < tokens; k += blockDim.x / 32) {
     const int t = t0 + k;

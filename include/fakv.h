@@ -152,8 +152,10 @@ typedef struct {
 /* k and v [T, HKV, D] written to their tokens' places, k turned by its positions first
  * where `rope` is given, and q [T, H, D] turned likewise into q_out [T, H, D] (contiguous;
  * copied where rope is NULL). q_out does not overlap the inputs, or is q itself if that is
- * contiguous. Inputs in the cache's dtype. A slot named for two sequences has two tokens for a
- * place: which of them stays is not defined. One launch. */
+ * contiguous. Inputs in the cache's dtype. A slot named for two sequences has two tokens for
+ * a place: which of them stays is not defined. With a cu that decreases (a status bit) a row
+ * may be taken for another sequence's; only places of that sequence's new tokens are then
+ * written. One launch. */
 FA_API fa_status fakv_append(const void* q, const void* k, const void* v, void* q_out,
                              const int* cu, const int* slots, const fakv_rope* rope,
                              const fakv_cache* cache, const fakv_tokens* p, fa_stream_t stream);

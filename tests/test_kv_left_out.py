@@ -164,3 +164,24 @@ def test_compact_of_rows_wider_than_a_step(kv):
     cache.compact()
     assert cache.table.tolist() == m.rows and cache.refs.tolist() == m.refs and cache.lens.tolist() == [0] * n
     cache.check()
+
+
+@pytest.mark.parametrize("B", [3, 200])
+def test_append_of_a_decreasing_cu_writes_no_place_but_the_sequences(kv, B):
+    """cu [0, B, 2, 3, ...]: every token that is written lies at a place of one of the slots' last tokens; all else in
+    the cache stays, and the status says so."""
+    cache = ref.make_cache(kv, [40] * B, 16, 1, 64, BF, slots=B + 1)
+    cu = torch.arange(B + 1, dtype=torch.int32).cuda()
+    cu[1] = B
+    x = torch.randn(B, 2, 64, generator=torch.Generator().manual_seed(1)).to(BF).cuda()
+    k0, v0 = cache.k.clone(), cache.v.clone()
+    cache.append(x, x[:, :1], x[:, 1:], cu)
+    with pytest.raises(kv.CacheError) as e:
+        cache.check()
+    assert e.value.bits == kv.BAD_LENGTH
+    free = torch.ones(cache.k.shape[1:3], dtype=torch.bool, device="cuda")
+    for b in range(B):  # the last tokens of a slot: as many as the call has rows, at most
+        for p in range(max(0, 40 - B), 40):
+            free[cache.table[b, p // 16].long(), p % 16] = False
+    for x0, x1 in ((k0, cache.k), (v0, cache.v)):
+        assert torch.equal(x0[0][free].nan_to_num(nan=7.0), x1[0][free].nan_to_num(nan=7.0))
