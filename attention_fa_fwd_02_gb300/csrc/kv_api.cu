@@ -135,7 +135,7 @@ FA_API fa_status fakv_rope_freqs(int rotary_dim, double base, const fakv_scaling
     const double x = turns * 18446744073709551616.0;  // 2^64, exact
     freqs[i] = x >= 18446744073709551616.0 ? 0 : (unsigned long long)x;
   }
-  *mscale = s.kind == FAKV_YARN ? (float)(0.1 * std::log(s.factor) + 1.0) : 1.f;
+  *mscale = s.kind == FAKV_YARN && s.factor > 1 ? (float)(0.1 * std::log(s.factor) + 1.0) : 1.f;
   return FA_OK;
 }
 

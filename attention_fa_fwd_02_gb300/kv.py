@@ -181,8 +181,8 @@ class Rope:
     """Rotary positions of the first ``rotary_dim`` (None: all) of ``head_dim`` columns. ``layout``: "half" (columns
     i and i + rotary_dim / 2 are a pair) or "interleaved" (2 i and 2 i + 1). ``scaling``: None, or a dict with
     ``kind`` "linear" (factor), "ntk" (factor), "bands" (factor, low, high, original) or "yarn" (factor, beta_fast,
-    beta_slow, original, and ``mscale`` to replace 0.1 ln(factor) + 1): see include/fakv.h. The frequencies are
-    computed once and kept on ``device``."""
+    beta_slow, original), and with any of them ``mscale`` to replace 1 (yarn: 0.1 ln(factor) + 1 above a factor of
+    1): see include/fakv.h. The frequencies are computed once and kept on ``device``."""
 
     def __init__(self, head_dim, rotary_dim=None, base=10000.0, layout="half", scaling=None, device="cuda"):
         rotary_dim = head_dim if rotary_dim is None else rotary_dim

@@ -92,7 +92,7 @@ typedef struct {
  *   FAKV_YARN    the ramp g_i = clamp((i - a) / (b - a), 0, 1) between a = floor(e(beta_fast))
  *                and b = ceil(e(beta_slow)), e(x) = r ln(original / 2 pi x) / (2 ln base),
  *                a >= 0, b <= r - 1 (b - a at least 0.001): g_i f_i / factor + (1 - g_i) f_i,
- *                and mscale = 0.1 ln(factor) + 1.
+ *                and mscale = 0.1 ln(factor) + 1 (1 for a factor up to 1).
  * fakv_rope_freqs (host only) writes what the kernels read: f_i as a 64-bit fraction of
  * a turn, so that p f_i modulo a whole turn is one integer product, exact for any
  * position: far positions lose nothing. The caller copies freqs to the device once. */
