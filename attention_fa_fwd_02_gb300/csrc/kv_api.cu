@@ -33,10 +33,12 @@ fa_status check_cache(const fakv_cache* c) {
     if (s <= 0 || !stride_ok(s, es)) return FA_ERR_INVALID_ARG;
     if (s * es % 16 != 0) return FA_ERR_ALIGNMENT;
   }
-  if (!stride_ok(c->plane_stride, es) || (c->planes > 1 && c->plane_stride == 0)) return FA_ERR_INVALID_ARG;
-  if (c->plane_stride * es % 16 != 0) return FA_ERR_ALIGNMENT;
-  if ((double)c->planes * c->plane_stride * es > MAX_BYTES || (double)c->num_pages * c->page_stride * es > MAX_BYTES)
-    return FA_ERR_INVALID_ARG;
+  if (c->planes > 1) {
+    if (c->plane_stride <= 0 || !stride_ok(c->plane_stride, es)) return FA_ERR_INVALID_ARG;
+    if (c->plane_stride * es % 16 != 0) return FA_ERR_ALIGNMENT;
+    if ((double)c->planes * c->plane_stride * es > MAX_BYTES) return FA_ERR_INVALID_ARG;
+  }
+  if ((double)c->num_pages * c->page_stride * es > MAX_BYTES) return FA_ERR_INVALID_ARG;
   if (c->table_stride < c->max_pages || (double)c->max_slots * c->table_stride * 4 > MAX_BYTES)
     return FA_ERR_INVALID_ARG;
   for (const void* p : {(const void*)c->K, (const void*)c->V, (const void*)c->table, (const void*)c->lens}) {

@@ -112,7 +112,7 @@ CopyArgs copy_args(const fakv_cache& c) {
   CopyArgs a;
   a.base[0] = static_cast<char*>(c.K);
   a.base[1] = static_cast<char*>(c.V);
-  a.plane_bytes = c.plane_stride * es;
+  a.plane_bytes = c.planes > 1 ? c.plane_stride * es : 0;  // (of one plane: any number)
   a.page_bytes = c.page_stride * es;
   a.planes = c.planes;
   a.bytes = (int)((long long)c.page_size * c.HKV * c.D * es);
