@@ -162,6 +162,9 @@ FA_API fa_status fakv_rope_apply(const void* q, const void* k, void* q_out, void
   // in place: element for element
   if (q == q_out && (p->q_token != p->qo_token || p->q_head != p->qo_head)) return FA_ERR_INVALID_ARG;
   if (p->HKV > 0 && k == k_out && (p->k_token != p->ko_token || p->k_head != p->ko_head)) return FA_ERR_INVALID_ARG;
+  // output rows that overlap would be written, and in place read, by several threads at once
+  if ((p->H > 1 && p->qo_head < p->D) || (p->T > 1 && p->qo_token < p->D)) return FA_ERR_INVALID_ARG;
+  if ((p->HKV > 1 && p->ko_head < p->D) || (p->HKV > 0 && p->T > 1 && p->ko_token < p->D)) return FA_ERR_INVALID_ARG;
   return launch_rope(q, k, q_out, k_out, positions, *rope, *p, reinterpret_cast<cudaStream_t>(stream));
 }
 

@@ -118,7 +118,7 @@ FA_API fa_status fakv_rope_freqs(int rotary_dim, double base, const fakv_scaling
 
 /* Rows of q [T, H, D] and k [T, HKV, D] (element strides per token and head, D without
  * gaps) turned by their positions, into q_out and k_out, which are the inputs themselves
- * (with the inputs' strides) or do not overlap them. HKV = 0: no k. positions [T] int32,
+ * (with the inputs' strides) or do not overlap them; rows of an output do not overlap. HKV = 0: no k. positions [T] int32,
  * or int64 with positions_64 = 1; any sign. inverse = 1 turns the other way: the gradient
  * of the rotation (mscale included). fp32 arithmetic, one rounding on store. */
 typedef struct {

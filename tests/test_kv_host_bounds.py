@@ -34,3 +34,23 @@ def test_the_plane_stride_of_one_plane_is_no_matter(kv, stride):
     assert lib.fakv_grow(C, A, A, 0, None) == 0 and lib.fakv_fork(C, A, A, 0, None) == 0
     c.planes = 2
     assert lib.fakv_attend(A, A, A, A, None, C, ctypes.byref(t), None) in (1, 3)
+
+
+@pytest.mark.parametrize("kw", [dict(qo_token=0), dict(qo_head=0), dict(ko_token=0), dict(ko_head=32),
+                                dict(qo_token=63), dict(T=1, qo_head=16), dict(H=1, qo_token=48)])
+def test_rope_refuses_outputs_whose_rows_overlap(kv, kw):
+    lib = kv._lib()
+
+    def call(same=False, **kw):
+        d = dict(T=3, H=4, HKV=2, D=64, dtype=1, positions_64=1, q_token=256, q_head=64, k_token=128, k_head=64,
+                 qo_token=256, qo_head=64, ko_token=128, ko_head=64)
+        d.update(kw)
+        r = kv.fakv_rope(A, 64, 0, 1.0)
+        if same:  # in place: the inputs' strides are the outputs'
+            for x in ("q", "k"):
+                for s in ("token", "head"):
+                    d[f"{x}_{s}"] = d[f"{x}o_{s}"]
+        b = 2 * A if not same else A
+        return lib.fakv_rope_apply(A, A, b, b, A, ctypes.byref(r), ctypes.byref(kv.fakv_rope_params(**d)), None)
+
+    assert call(**kw) == 1 and call(same=True, **kw) == 1
