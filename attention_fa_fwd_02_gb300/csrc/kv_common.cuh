@@ -75,11 +75,27 @@ inline bool allow_smem(K* kernel, int bytes, std::atomic<uint64_t>& done) {
   return true;
 }
 
-// An allocation failed: the runtime's record of it is cleared, so that the next call's check
-// of its launches does not find it.
+// An allocation or a launch failed: the runtime's record of it is cleared, so that the next
+// call's check of its launches does not find it.
 inline fa_status failed() {
   (void)cudaGetLastError();
   return FA_ERR_CUDA;
+}
+
+// The launch's own answer, not the runtime's record of the last error, which may be another call's.
+template <typename... KArgs, typename... Args>
+inline fa_status launch(void (*kernel)(KArgs...), dim3 grid, dim3 block, size_t smem, cudaStream_t stream, Args... args) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = grid;
+  cfg.blockDim = block;
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = stream;
+  return cudaLaunchKernelEx(&cfg, kernel, static_cast<KArgs>(args)...) == cudaSuccess ? FA_OK : failed();
+}
+// As the programmatic dependent of the launch before it (fa_common.cuh).
+template <typename... KArgs, typename... Args>
+inline fa_status launch_dependent(void (*kernel)(KArgs...), dim3 grid, dim3 block, cudaStream_t stream, Args... args) {
+  return launch_programmatic(kernel, grid, block, stream, args...) == cudaSuccess ? FA_OK : failed();
 }
 
 inline int esize(fa_dtype t) { return t == FA_BF16 ? 2 : 4; }

@@ -568,8 +568,6 @@ struct Scratch {
   ~Scratch() { if (ok) host::scratch_free(p, s); }
 };
 
-fa_status done() { return cudaGetLastError() == cudaSuccess ? FA_OK : FA_ERR_CUDA; }
-
 }  // namespace
 
 fa_status launch_grow(const fakv_cache& c, const int* slots, const int* add, int n, cudaStream_t s) {
@@ -580,24 +578,22 @@ fa_status launch_grow(const fakv_cache& c, const int* slots, const int* add, int
                 reinterpret_cast<int*>(w.p + mark),
                 reinterpret_cast<int*>(w.p + fresh), reinterpret_cast<int2*>(w.p + pair),
                 reinterpret_cast<int*>(w.p)};
+  fa_status st;
   {
     host::KernelTimer t("grow", s);
-    grow_kernel<<<1, PLAN, 0, s>>>(a);
+    st = launch(grow_kernel, 1, PLAN, 0, s, a);
   }
+  if (st != FA_OK) return st;  // (no plan: its scratch says nothing)
   const CopyArgs ca = copy_args(c);
   host::KernelTimer t("grow_copy", s);
-  if (launch_programmatic(copy_kernel, dim3(copy_grid(n, ca)), dim3(COPY_THREADS), s, ca,
-                          (const int2*)a.pair, (const int*)a.count) != cudaSuccess)
-    return FA_ERR_CUDA;
-  return done();
+  return launch_dependent(copy_kernel, copy_grid(n, ca), COPY_THREADS, s, ca, a.pair, a.count);
 }
 
 fa_status launch_fork(const fakv_cache& c, const int* src, const int* dst, int n, cudaStream_t s) {
   if (n <= SHORT_LIST && c.max_pages <= 32 * SHORT_STEPS) {
     const ListArgs b = {c, src, dst, nullptr, n, log2_of(c.page_size), nullptr, nullptr};
     host::KernelTimer t("fork_short", s);
-    fork_short_kernel<<<1, PLAN, 0, s>>>(b);
-    return done();
+    return launch(fork_short_kernel, 1, PLAN, 0, s, b);
   }
   const size_t rows = (size_t)n * c.max_pages * 4;
   Scratch w(rows + (size_t)n * 4, s);
@@ -605,21 +601,21 @@ fa_status launch_fork(const fakv_cache& c, const int* src, const int* dst, int n
   ListArgs a = {c, src, dst, nullptr, n, log2_of(c.page_size), reinterpret_cast<int*>(w.p),
                 reinterpret_cast<int*>(w.p + rows)};
   const int grid = n < 8 * host::sm_count() ? n : 8 * host::sm_count();
+  fa_status st;
   {
     host::KernelTimer t("fork_take", s);
-    fork_take_kernel<<<grid, 256, 0, s>>>(a);
+    st = launch(fork_take_kernel, grid, 256, 0, s, a);
   }
+  if (st != FA_OK) return st;
   host::KernelTimer t("fork_give", s);
-  if (launch_programmatic(fork_give_kernel, dim3(grid), dim3(256), s, a) != cudaSuccess) return FA_ERR_CUDA;
-  return done();
+  return launch_dependent(fork_give_kernel, grid, 256, s, a);
 }
 
 fa_status launch_free(const fakv_cache& c, const int* slots, const int* keep, int n, cudaStream_t s) {
   ListArgs a = {c, nullptr, slots, keep, n, log2_of(c.page_size), nullptr, nullptr};
   const int grid = n < 8 * host::sm_count() ? n : 8 * host::sm_count();
   host::KernelTimer t("free", s);
-  free_kernel<<<grid, 256, 0, s>>>(a);
-  return done();
+  return launch(free_kernel, grid, 256, 0, s, a);
 }
 
 fa_status launch_compact(const fakv_cache& c, cudaStream_t s) {
@@ -627,14 +623,14 @@ fa_status launch_compact(const fakv_cache& c, cudaStream_t s) {
   if (!w.ok) return failed();
   CompactArgs a = {c, copy_args(c), reinterpret_cast<int*>(w.p + (size_t)c.num_pages * 8),
                    reinterpret_cast<int2*>(w.p), reinterpret_cast<int*>(w.p + (size_t)c.num_pages * 12)};
+  fa_status st;
   {
     host::KernelTimer t("compact_plan", s);
-    compact_plan_kernel<<<1, PLAN, 0, s>>>(a);
+    st = launch(compact_plan_kernel, 1, PLAN, 0, s, a);
   }
+  if (st != FA_OK) return st;
   host::KernelTimer t("compact_move", s);
-  if (launch_programmatic(compact_move_kernel, dim3(copy_grid(c.num_pages, a.copy)), dim3(COPY_THREADS), s, a) != cudaSuccess)
-    return FA_ERR_CUDA;
-  return done();
+  return launch_dependent(compact_move_kernel, copy_grid(c.num_pages, a.copy), COPY_THREADS, s, a);
 }
 
 }  // namespace kv

@@ -256,7 +256,7 @@ __global__ void __launch_bounds__(MAX_THREADS, 2) rope_kernel(const __grid_const
 }
 
 template <typename E, int EV, bool APPEND>
-fa_status launch(RopeArgs& a, const char* name, cudaStream_t s) {
+fa_status run(RopeArgs& a, const char* name, cudaStream_t s) {
   // A token's units side by side, in blocks of up to MAX_THREADS; where they are few,
   // several tokens side by side. Each thread takes UB tokens if that leaves every SM two
   // blocks, else one: few rows are spread over the SMs.
@@ -274,9 +274,7 @@ fa_status launch(RopeArgs& a, const char* name, cudaStream_t s) {
   const dim3 grid((a.T + span - 1) / span, parts), block((threads + 31) / 32 * 32);
   const size_t cs = (size_t)span * pairs * sizeof(float2);
   host::KernelTimer t(name, s);
-  if (a.rot) rope_kernel<E, EV, APPEND, true><<<grid, block, cs, s>>>(a);
-  else rope_kernel<E, EV, APPEND, false><<<grid, block, cs, s>>>(a);
-  return cudaGetLastError() == cudaSuccess ? FA_OK : FA_ERR_CUDA;
+  return launch(a.rot ? rope_kernel<E, EV, APPEND, true> : rope_kernel<E, EV, APPEND, false>, grid, block, cs, s, a);
 }
 
 template <bool APPEND>
@@ -292,8 +290,8 @@ fa_status dispatch(RopeArgs& a, int D, fa_dtype dtype, bool inplace, const char*
   }
   // in place the columns behind the pairs stay where they are
   a.units = (inplace ? a.rot : D) / (wide ? 2 * ev : 2);
-  if (es == 2) return wide ? launch<__nv_bfloat16, 8, APPEND>(a, name, s) : launch<__nv_bfloat16, 1, APPEND>(a, name, s);
-  return wide ? launch<float, 4, APPEND>(a, name, s) : launch<float, 1, APPEND>(a, name, s);
+  if (es == 2) return wide ? run<__nv_bfloat16, 8, APPEND>(a, name, s) : run<__nv_bfloat16, 1, APPEND>(a, name, s);
+  return wide ? run<float, 4, APPEND>(a, name, s) : run<float, 1, APPEND>(a, name, s);
 }
 
 }  // namespace

@@ -817,7 +817,7 @@ fa_status run(RowsArgs& a, cudaStream_t s) {
   using C = RowsCfg<E, D, NTR>;
   auto* kernel = attend_rows_kernel<E, D, NTR>;
   static std::atomic<uint64_t> done{0};
-  if (!allow_smem(kernel, C::SMEM, done)) return FA_ERR_CUDA;
+  if (!allow_smem(kernel, C::SMEM, done)) return failed();
   const int ctas = host::sm_count() * C::CTAS_PER_SM;
   void* w = nullptr;
   if (host::scratch_alloc(&w, partials_bytes(ctas * WARPS, C::R, D), s) != cudaSuccess) return failed();
@@ -826,17 +826,16 @@ fa_status run(RowsArgs& a, cudaStream_t s) {
   a.g.u_shift = log2_of(C::GROUP);
   a.g.start = 4;  // groups: looking up an item's first pages and rows takes about as long
   a.g.snap = 4;
-  fa_status st = FA_OK;
+  fa_status st;
   {
     host::KernelTimer t("attend_rows", s);
-    kernel<<<ctas, NTHREADS, C::SMEM, s>>>(a);
-    if (cudaGetLastError() != cudaSuccess) st = FA_ERR_CUDA;
+    st = launch(kernel, ctas, NTHREADS, C::SMEM, s, a);
   }
   if (st == FA_OK) {
     const JoinArgs j = {a.part, a.O, a.LSE, ctas, WARPS, C::R, D, a.H, a.c.D, a.out_bf16, a.g.rep};
     st = launch_join(j, s);
   }
-  if (host::scratch_free(w, s) != cudaSuccess && st == FA_OK) st = FA_ERR_CUDA;
+  if (host::scratch_free(w, s) != cudaSuccess) st = failed();
   return st;
 }
 
@@ -844,14 +843,12 @@ fa_status run(RowsArgs& a, cudaStream_t s) {
 
 fa_status launch_join(const JoinArgs& a, cudaStream_t s) {
   host::KernelTimer t("attend_join", s);
-  return launch_programmatic(attend_join_kernel, dim3(a.ctas, a.R / 2), dim3(JOIN_THREADS), s, a) == cudaSuccess
-             ? FA_OK : FA_ERR_CUDA;
+  return launch_dependent(attend_join_kernel, dim3(a.ctas, a.R / 2), JOIN_THREADS, s, a);
 }
 
 fa_status launch_join_tall(const JoinArgs& a, cudaStream_t s) {
   host::KernelTimer t("attend_join", s);
-  return launch_programmatic(attend_join_tall_kernel, dim3(TALL_BLOCKS * host::sm_count()), dim3(32 * TALL_WARPS), s, a) == cudaSuccess
-             ? FA_OK : FA_ERR_CUDA;
+  return launch_dependent(attend_join_tall_kernel, TALL_BLOCKS * host::sm_count(), 32 * TALL_WARPS, s, a);
 }
 
 fa_status launch_attend_rows(const void* q, void* O, float* LSE, const int* cu, const int* slots,

@@ -616,22 +616,21 @@ fa_status run(TilesArgs& a, const CUtensorMap& q, const CUtensorMap& k, const CU
   using C = TilesCfg<D>;
   auto* kernel = attend_tiles_kernel<D, TERMS>;
   static std::atomic<uint64_t> done{0};
-  if (!allow_smem(kernel, C::SMEM, done)) return FA_ERR_CUDA;
+  if (!allow_smem(kernel, C::SMEM, done)) return failed();
   const int ctas = host::sm_count();
   void* w = nullptr;
   if (host::scratch_alloc(&w, partials_bytes(ctas, a.g.R, D), s) != cudaSuccess) return failed();
   a.part = partials_at(w, ctas, a.g.R, D);
-  fa_status st = FA_OK;
+  fa_status st;
   {
     host::KernelTimer t("attend_tiles", s);
-    kernel<<<ctas, C::THREADS, C::SMEM, s>>>(q, k, v, a);
-    if (cudaGetLastError() != cudaSuccess) st = FA_ERR_CUDA;
+    st = launch(kernel, ctas, C::THREADS, C::SMEM, s, q, k, v, a);
   }
   if (st == FA_OK) {
     const JoinArgs j = {a.part, a.O, a.LSE, ctas, 1, a.g.R, D, a.H, a.c.D, a.out_bf16, a.g.rep};
     st = launch_join_tall(j, s);
   }
-  if (host::scratch_free(w, s) != cudaSuccess && st == FA_OK) st = FA_ERR_CUDA;
+  if (host::scratch_free(w, s) != cudaSuccess) st = failed();
   return st;
 }
 
