@@ -1,5 +1,7 @@
 """GPU checks that the page calls leave out what they refuse: an entry with a slot, a length, a count or a page that
 is not one leaves lens, table and refs as they were and sets its status bit, and the entries beside it are served."""
+import random
+
 import pytest
 import torch
 
@@ -185,3 +187,35 @@ def test_append_of_a_decreasing_cu_writes_no_place_but_the_sequences(kv, B):
             free[cache.table[b, p // 16].long(), p % 16] = False
     for x0, x1 in ((k0, cache.k), (v0, cache.v)):
         assert torch.equal(x0[0][free].nan_to_num(nan=7.0), x1[0][free].nan_to_num(nan=7.0))
+
+
+@pytest.mark.parametrize("n", [257, 1500, 2500])
+def test_long_lists_with_repeated_and_bad_slots(kv, n):
+    """Above 256 entries grow marks slots in memory, above 1024 it takes the list part by part; free and fork look
+    back over the whole list."""
+    slots, rng = n // 2, random.Random(n)
+    cache = kv.PagedCache.create(1, 4 * n, 8, 1, 16, slots, 12)
+    m = ref.Model(cache)
+
+    def some():
+        return [rng.randrange(-2, slots + 2) if rng.random() < 0.2 else rng.randrange(slots) for _ in range(n)]
+
+    for step in range(6):
+        at, add = some(), [rng.choice([0, 1, 5, 9, 20]) for _ in range(n)]
+        m.grow(at, add)
+        cache.grow(vec(*at), vec(*add))
+        m.same(cache, ("grow", step))
+        src, dst = [rng.randrange(slots) for _ in range(n)], some()
+        m.fork(src, dst)
+        cache.fork(vec(*src), vec(*dst))
+        m.same(cache, ("fork", step))
+        at, keep = some(), [rng.choice([0, 3, 8, 17]) for _ in range(n)]
+        m.free(at, keep)
+        cache.free(vec(*at), vec(*keep))
+        m.same(cache, ("free", step))
+    assert m.bits & (kv.REPEATED | kv.BAD_SLOT) == kv.REPEATED | kv.BAD_SLOT
+    everyone = list(range(slots)) * 2
+    m.free(everyone)
+    cache.free(vec(*everyone))
+    m.same(cache, "all")
+    assert m.refs.count(0) == len(m.refs)
