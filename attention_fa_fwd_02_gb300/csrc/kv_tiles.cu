@@ -512,7 +512,9 @@ __global__ void __launch_bounds__(TilesCfg<D>::THREADS, 1)
 #pragma unroll
         for (int kk = 0; kk < 8; ++kk) mx[kk] = fmaxf(mx[kk], s[120 + kk]);
         const float mt = max3(max3(mx[0], mx[1], mx[2]), max3(mx[3], mx[4], mx[5]), fmaxf(mx[6], mx[7])) * sl2;
-        if (__any_sync(0xffffffffu, mt > m + RESCALE_THRESHOLD)) {
+        // (rows past the item's have no say: they are another sequence's, or whatever lay in the stage, and a
+        // maximum that moved earlier would round the others' probabilities differently)
+        if (__any_sync(0xffffffffu, r_in < rows && mt > m + RESCALE_THRESHOLD)) {
           const float m_new = fmaxf(m, mt);
           const float corr = ex2(m - m_new);
           l *= corr;
