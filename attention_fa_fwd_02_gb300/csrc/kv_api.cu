@@ -208,7 +208,10 @@ FA_API fa_status fakv_attend(const void* q, void* O, float* LSE, const int* cu, 
   if (t.window >= cache->max_pages * cache->page_size) t.window = 0;  // hides nothing
   // Above 16 rows per sequence and kv head (on average: the lengths are on the device) tensor-core
   // tiles, if the copy engine can take the tensors' strides. 16 sequences of 8192 tokens (32
-  // query heads on 8 of 128): 16 rows 65 us by rows, 84 by tiles; 32 rows 104 and 77.
+  // query heads on 8 of 128): 16 rows 65 us by rows, 84 by tiles; 32 rows 104 and 77. An average
+  // serves a mixed batch badly on both sides: 256 sequences decoding and a chunk, over 4096
+  // tokens each, take 890 us by rows just below the limit (a chunk of 700), 748 in two calls;
+  // over 1024, 274 by tiles just above it (1100) and 238.
   if (cache->dtype == FA_BF16 && (long long)t.T * (t.H / cache->HKV) > 16ll * t.B) {
     st = launch_attend_tiles(q, O, LSE, cu, slots, *cache, t, reinterpret_cast<cudaStream_t>(stream));
     if (st != FA_ERR_UNSUPPORTED) return st;

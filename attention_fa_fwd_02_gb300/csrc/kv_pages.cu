@@ -10,8 +10,9 @@
 // Measured: 96 samples forked from 32 sequences and grown, 24 MB of last pages copied in 4
 // planes: 16.1 us (fork 4.6 by two launches, plan 7, copy 5: launches and look-ups; the copy's floor
 // is 7 us); a page each for 64 slots 6.3 us in a pool of 5000 pages, 11.8 in one of 130000 and 20.3
-// of 500000, all but full; 8192 pages closed up, 1900 of them moved in 2 planes: 92 us with the
-// two small copies around it, the move itself 70 us, 490 MB at 7.0 TB/s, the rate of a copy.
+// of 500000, all but full; 64 slots of 1024 pages freed 3.5 us, 16384 of 4 pages 59 (each entry is
+// looked for in the list before it); 8192 pages closed up, 1900 of them moved in 2 planes: 92 us with
+// the two small copies around it, the move itself 71 us, 490 MB at 6.9 TB/s, the rate of a copy.
 #include "kv_common.cuh"
 
 namespace fa {

@@ -13,9 +13,9 @@
 // all heads, in shared memory (by itself a unit would need EV sincos per 32 bytes moved,
 // more issue slots than the copy leaves). Measured: 8192 tokens of 32 + 8 heads of 128 in bf16
 // 28.6 us, 168 MB at 5.9 TB/s, 32768 tokens 99 us, 6.8 TB/s (UB 2 or 8: 33, 41 us); one token
-// 2.8 us. Append: 17000 tokens of 32 + 2 x 8 heads 74 us (floor 66); 4100 tokens 11.4 us with
-// their 59 MB in L2 and 15.9 without (floor 8.7), where finding the tokens' pages (three
-// dependent look-ups) and a last wave of blocks a third full show; a step of 48 tokens 3.9 us.
+// 2.8 us. Append: 17000 tokens of 32 + 2 x 8 heads 74 us (floor 66); 4100 tokens 11.6 us with
+// their 59 MB in L2 and 16.7 without (floor 8.7), where finding the tokens' pages (three
+// dependent look-ups) and a last wave of blocks a third full show; a step of 48 tokens 4.2 us.
 #include <cmath>
 #include "kv_common.cuh"
 

@@ -13,11 +13,13 @@
 // together in shared memory, so that a long sequence leaves a part per CTA to join.
 //
 // Measured (32 query heads on 8 kv heads of 128, one new token each, pages of 16): 64 sequences
-// of up to 16384 tokens 337 us, 2.15 GB at 6.4 TB/s, 0.94 of the measured copy rate (a
-// sixteenth of it is the join); one sequence of 16 tokens 8.3 us and of 1021 9.5 us, which is
+// of up to 16384 tokens 337 to 350 us, 2.15 GB at 6.1 to 6.4 TB/s, 0.91 to 0.94 of the measured
+// copy rate (a sixteenth of it is the join); 64 of up to 1024 36 us (floor 20), 16 of up to 8192
+// 58 (44); one sequence of 16 tokens 8.3 us and of 1021 9.7 us, which is
 // latency: 1.6 us from the launch to the cuts, 1.6 us to the first keys asked for, 0.5 us to
-// have them, 4 us the join. fp32, 12 sequences of up to 5 new tokens, window 1024, heads of
-// 64: 16.5 us, 48 MB; its three products per GEMM and their splits are what bounds it.
+// have them, 4 us the join. fp32: 64 sequences of up to 8192 346 us, 2.15 GB; 12 of up to 5 new
+// tokens, window 1024, heads of 64: 16.8 us with their 48 MB in L2 and 20.9 without; its three
+// products per GEMM and their splits are what bounds it.
 //
 //   scores  S^T = K Q^T: the 16 rows of an mma tile are keys, its 8 columns rows of q, so
 //           that eight rows (a decoding step) cost eight rows. bf16 m16n8k16, fp32 sums.

@@ -18,7 +18,8 @@
 namespace fa {
 namespace kv {
 
-// n / d for 0 <= n < 2^31 by a product (d fixed for a launch): with s = ceil(log2 d) and
+// n / d for 0 <= n < 2^31 by a product (d fixed for a launch; Granlund and Montgomery's
+// division by invariant integers): with s = ceil(log2 d) and
 // m = floor(2^32 (2^s - d) / d) + 1, t = high word of m n, it is (t + (n - t) / 2) / 2^(s - 1).
 struct Div {
   unsigned m;

@@ -24,13 +24,14 @@
 // P is one bf16 term where O is bf16: its rounding, at most 2^-8 of a probability and
 // random in sign, adds to O about what O's own rounding does (2048 tokens over 16384: O is
 // 2.4e-3 of its size from the 64-bit values, 1.7e-3 of that its own rounding), and a second
-// term would take 560 us where one takes 341. An fp32 O has no such rounding to hide
+// term would take 560 to 600 us where one takes 341. An fp32 O has no such rounding to hide
 // behind: with one term it would be 1.7e-3 off too. There P is two terms (2^-16), the second
-// in the half of S's TMEM columns that the first leaves free: 3e-5 off, in 562 us (8192
-// tokens of a prompt: 647 against 385).
+// in the half of S's TMEM columns that the first leaves free: 3e-5 off (8192 tokens of a
+// prompt: 650 to 690 us against 385). It is not the tensor pipe that fills then (60 %) but
+// the softmax warps' extra terms and TMEM stores.
 //
 // Measured: 2048 tokens over 16384 (32 query heads on 8 of 128) 337 us with the join, 1530
-// TFLOP/s, 0.80 of the measured peak; 8192 tokens of a prompt 381 us, 0.76. A unit of 128 keys
+// TFLOP/s, 0.80 of the measured peak; 8192 tokens of a prompt 385 us, 0.75. A unit of 128 keys
 // takes a CTA 2720 clocks, of which its MMAs fill 2240: a tile's softmax (1130 clocks: 62 to
 // load the scores, 320 for the maximum, 690 for the exponentials) and the hand-offs on both
 // sides of it are longer than the other tile's MMAs. Tried, and slower: two threads to a row

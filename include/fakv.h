@@ -23,8 +23,9 @@
  * cu[b] .. cu[b + 1] - 1 (cu: B + 1 non-decreasing int32 from 0 to at most T; attend does
  * nothing with one that decreases) and is slot slots[b] (slots NULL: slot b; attend may
  * name a slot for several sequences). Lengths count the new tokens: row i of a sequence with n
- * new tokens has position lens[slot] - n + i. Rows from cu[B] on belong to no sequence
- * and are neither read nor written.
+ * new tokens has position lens[slot] - n + i. Rows from cu[B] on belong to no sequence:
+ * their outputs are not written, and no output depends on what they hold, but they may
+ * be read.
  *
  * What only the device can see is checked there: a slot outside [0, max_slots), a page
  * number outside [0, num_pages) where a token should be, a length beyond the row. Such
@@ -163,14 +164,18 @@ FA_API fa_status fakv_append(const void* q, const void* k, const void* v, void* 
 /* O [T, H, D] = softmax(scale q K^T + mask) V over the tokens of each row's sequence, LSE
  * [T, H] (natural log) fp32; contiguous. Query head h reads kv head h / (H / HKV). q in the
  * cache's dtype. A row that sees no key gets O = 0, LSE = -inf. K and V within a
- * sequence's length must be finite; page memory past it may hold anything. NaN or infinity
- * in a row of q makes that row's O and LSE NaN and no other's. fp32 caches
+ * sequence's length must be finite, K below 2^127 and V below 2^80 in size (probabilities of
+ * up to 2^8 times V are summed over the keys in fp32); page memory past it may hold anything.
+ * NaN or infinity in a row of q makes that row's O and LSE NaN and no other's. fp32 caches
  * use three tf32 products per GEMM (about 22 significant bits); bf16 caches bf16 products
  * with fp32 sums, the probabilities in bf16: two terms (2^-16) where O is fp32 or there are few
  * rows, one (2^-8, about a bf16 O's own rounding) where there are many and O is bf16. Sums
  * over keys that are split between CTAs are joined in a fixed order: results do not
- * depend on timing. A batch is served by one kernel, chosen by the average of new tokens: a few
- * long chunks among hundreds of short decoding sequences are better given calls of their own. */
+ * depend on timing. A batch is served by one kernel, chosen by the average T / B of rows to a
+ * sequence (what the host knows: rows from cu[B] on count). So a few long chunks among
+ * hundreds of decoding sequences are better given calls of their own, and T is better the
+ * step's own row count than a buffer's: padding a decoding step above 16 rows per sequence and
+ * kv head takes the kernel of chunks, with a bf16 O's one-term probabilities. */
 FA_API fa_status fakv_attend(const void* q, void* O, float* LSE, const int* cu, const int* slots,
                              const fakv_cache* cache, const fakv_tokens* p, fa_stream_t stream);
 
@@ -187,7 +192,9 @@ FA_API fa_status fakv_grow(const fakv_cache* cache, const int* slots, const int*
 
 /* Slots dst[i] become copies of slots src[i], sharing their pages; what dst[i] held is
  * released. All at once: sources are read as they were before the call, so a list may
- * exchange or reorder slots. n * max_pages <= 2^31. */
+ * exchange or reorder slots. n * max_pages <= 2^31; above 32 entries, or 256 pages to a row,
+ * the rows are held meanwhile in 4 n max_pages bytes of scratch. An entry of a row that
+ * names no page is copied as it is, counted nowhere (BAD_PAGE). */
 FA_API fa_status fakv_fork(const fakv_cache* cache, const int* src, const int* dst, int n,
                            fa_stream_t stream);
 
