@@ -254,8 +254,8 @@ class PagedCache:
     """Key / value pages of sequences in slots. ``k``, ``v``: [planes, pages, page_size, kv heads, D] (or without the
     planes; ``layout`` "heads": [planes, pages, kv heads, page_size, D]), bf16 or fp32, alike in shape and strides;
     ``table`` [slots, max_pages] int32 page numbers (-1: none), ``lens`` [slots] int32, ``refs`` [pages] int32: how
-    many rows hold a page. The tensors stay the caller's; the methods change them in place. ``status`` [1] int32
-    collects what the device refused (``check``)."""
+    many rows hold a page. The tensors stay the caller's; the methods change them in place (a length is lowered with
+    ``free``, which releases the pages). ``status`` [1] int32 collects what the device refused (``check``)."""
 
     def __init__(self, k, v, table, lens, refs, layout="tokens", status=None):
         if layout not in ("tokens", "heads"):
