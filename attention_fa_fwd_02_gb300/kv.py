@@ -376,7 +376,8 @@ class PagedCache:
 
     def grow(self, slots, add, stream=None):
         """Room for add[i] more tokens in slots[i] (the lengths grow by it): new pages, and a copy of a shared last
-        page that has room."""
+        page that has room. An entry that cannot be served (``check`` tells) keeps its length; an append that counts
+        on it would write over the slot's last tokens."""
         self._list(_lib().fakv_grow, "fakv_grow", slots, ("slots", "add"), add, stream)
 
     def fork(self, src, dst, stream=None):

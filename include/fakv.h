@@ -186,7 +186,8 @@ FA_API fa_status fakv_attend(const void* q, void* O, float* LSE, const int* cu, 
  * (refs > 1 when the call starts) is first replaced by a copy, in every plane. An entry
  * is not served (its length stays) if its row is too short, if the last page that its new
  * tokens begin in is missing or, with the entries before it, it needs more pages than were
- * free. */
+ * free. Its step is then to be left out too: an append that counts on the pages would take the
+ * slot's last tokens for the new ones and write over them. */
 FA_API fa_status fakv_grow(const fakv_cache* cache, const int* slots, const int* add, int n,
                            fa_stream_t stream);
 
