@@ -19,7 +19,8 @@ CSRC = os.path.join(PKG, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 OUT = os.path.join(PKG, "libfa.so")
 OBJ_DIR = os.path.join(PKG, "_build")
-SOURCES = ["fa_fwd.cu", "fa_bwd.cu", "fa_api.cu", "kv_api.cu", "kv_rope.cu", "kv_pages.cu", "kv_rows.cu", "kv_tiles.cu"]
+SOURCES = ["fa_fwd.cu", "fa_bwd.cu", "fa_api.cu", "kv_api.cu", "kv_rope.cu", "kv_pages.cu", "kv_rows.cu", "kv_tiles.cu", "kv_quant.cu",
+           "kv_qrows.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 
 

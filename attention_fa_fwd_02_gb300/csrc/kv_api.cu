@@ -1,7 +1,7 @@
 // kv_api.cu -- the extern "C" boundary of include/fakv.h: argument checks and dispatch.
 #include <cmath>
 #include <initializer_list>
-#include "kv_common.cuh"
+#include "kv_quant.cuh"
 
 namespace fa {
 namespace kv {
@@ -72,18 +72,146 @@ fa_status check_rope(const fakv_rope* r, int D) {
   return aligned(r->freqs, 8) ? FA_OK : FA_ERR_ALIGNMENT;
 }
 
-fa_status check_tokens(const fakv_cache* c, const fakv_tokens* p, const int* cu, const int* slots) {
+// (dtype: of q, k and v)
+fa_status check_tokens(const fakv_cache* c, fa_dtype dtype, const fakv_tokens* p, const int* cu, const int* slots) {
   if (!p || p->B < 0 || p->B > MAX_SEQS || p->T < 0 || p->T > (1 << 30) || p->H < 0 || p->H > 65535)
     return FA_ERR_INVALID_ARG;
   if (p->plane < 0 || p->plane >= c->planes) return FA_ERR_INVALID_ARG;
   if (p->H % c->HKV != 0 || p->H / c->HKV > 128) return FA_ERR_INVALID_ARG;
   if ((double)p->T * p->H > 1073741824.0) return FA_ERR_INVALID_ARG;
-  const int es = esize(c->dtype);
+  const int es = esize(dtype);
   for (long long s : {p->q_token, p->q_head, p->k_token, p->k_head, p->v_token, p->v_head})
     if (!stride_ok(s, es) || (double)p->T * s * es > MAX_BYTES) return FA_ERR_INVALID_ARG;
   if (p->B > 0 && p->T > 0 && !cu) return FA_ERR_INVALID_ARG;
   if (!aligned(cu, 4) || !aligned(slots, 4)) return FA_ERR_ALIGNMENT;
   return FA_OK;
+}
+
+fa_status check_append(const void* q, const void* k, const void* v, const void* q_out, fa_dtype dtype, int D,
+                       const fakv_tokens* p) {
+  const int es = esize(dtype);
+  if (!k || !v || (p->H > 0 && (!q || !q_out))) return FA_ERR_INVALID_ARG;
+  if (!aligned(k, es) || !aligned(v, es) || (p->H > 0 && (!aligned(q, es) || !aligned(q_out, es))))
+    return FA_ERR_ALIGNMENT;
+  // in place: contiguous (the stride of one token or one head is no matter)
+  if (p->H > 0 && q == q_out && ((p->H > 1 && p->q_head != D) || (p->T > 1 && p->q_token != (long long)p->H * D)))
+    return FA_ERR_INVALID_ARG;
+  return FA_OK;
+}
+
+fa_status check_attend(const fakv_tokens* p) {
+  if (p->H < 1 || !dtype_ok(p->out_dtype)) return FA_ERR_INVALID_ARG;
+  if (!(p->scale > 0.f && std::isfinite(p->scale * LOG2E))) return FA_ERR_INVALID_ARG;
+  if ((p->causal != 0 && p->causal != 1) || p->window < 0) return FA_ERR_INVALID_ARG;
+  return FA_OK;
+}
+
+fa_status check_attend_rows(const void* q, const void* O, const void* LSE, fa_dtype dtype, const fakv_tokens* p) {
+  for (const void* x : {q, O, LSE}) {
+    if (!x) return FA_ERR_INVALID_ARG;
+    if (!aligned(x, 16)) return FA_ERR_ALIGNMENT;
+  }
+  const int es = esize(dtype);
+  return p->q_token * es % 16 != 0 || p->q_head * es % 16 != 0 ? FA_ERR_ALIGNMENT : FA_OK;
+}
+
+bool quant_ok(int page_size, int D, int bits, int group) {
+  if (page_size < 8 || page_size > 1024 || (page_size & (page_size - 1)) != 0) return false;
+  if (D < 16 || D % 16 != 0 || D > 128 || (bits != 4 && bits != 8)) return false;
+  return group == D || (D == 128 && group == 64);
+}
+// bytes of a token of one head
+int quant_token(int D, int bits, int group) { return 16 * q_chunks(D, bits) + 4 * (D / group); }
+
+// A cache in 4 or 8 bits as the page calls see it: one of 32-bit words, a token of one head as wide as
+// its codes and params. (A block is page_size such tokens; which of its bytes are whose is no matter.)
+fa_status check_qcache(const fakv_qcache* c, fakv_cache* pages) {
+  if (!c || !dtype_ok(c->dtype)) return FA_ERR_INVALID_ARG;
+  if (c->planes < 1 || c->num_pages < 1 || c->HKV < 1 || c->D < 1 || c->max_slots < 1 || c->max_pages < 1 ||
+      c->page_size < 1 || c->group < 1)
+    return FA_ERR_INVALID_ARG;
+  if (!quant_ok(c->page_size, c->D, c->bits, c->group)) return FA_ERR_UNSUPPORTED;
+  const int token = quant_token(c->D, c->bits, c->group);
+  if (c->head_stride < token * c->page_size) return FA_ERR_INVALID_ARG;
+  for (long long s : {c->page_stride, c->head_stride, c->planes > 1 ? c->plane_stride : 0})
+    if (s % 16 != 0) return FA_ERR_ALIGNMENT;
+  fakv_cache v = {};
+  v.K = c->K;
+  v.V = c->V;
+  v.table = c->table;
+  v.lens = c->lens;
+  v.refs = c->refs;
+  v.status = c->status;
+  v.plane_stride = c->plane_stride / 4;
+  v.page_stride = c->page_stride / 4;
+  v.token_stride = 16;  // (tokens have none: what check_cache accepts)
+  v.head_stride = c->head_stride / 4;
+  v.table_stride = c->table_stride;
+  v.planes = c->planes;
+  v.num_pages = c->num_pages;
+  v.page_size = c->page_size;
+  v.HKV = c->HKV;
+  v.D = 16;
+  v.max_slots = c->max_slots;
+  v.max_pages = c->max_pages;
+  v.dtype = FA_F32;
+  const fa_status st = check_cache(&v);
+  if (st != FA_OK) return st;
+  v.D = token / 4;
+  *pages = v;
+  return FA_OK;
+}
+
+// The calls that count or move pages
+fa_status check_qpages(const fakv_qcache* c, fakv_cache* pages) {
+  const fa_status st = check_qcache(c, pages);
+  if (st != FA_OK) return st;
+  if (!c->refs) return FA_ERR_INVALID_ARG;
+  const long long block = (long long)quant_token(c->D, c->bits, c->group) * c->page_size;
+  if (c->HKV > 1 && c->head_stride != block) return FA_ERR_UNSUPPORTED;
+  if (block * c->HKV > (1ll << 30)) return FA_ERR_UNSUPPORTED;
+  return c->page_stride < block * c->HKV ? FA_ERR_INVALID_ARG : FA_OK;
+}
+
+QCache qcache_of(const fakv_qcache& c, const fakv_cache& pages, int plane) {
+  QCache q;
+  q.c = pages;
+  q.c.D = c.D;
+  q.c.dtype = c.dtype;
+  q.K = static_cast<uint8_t*>(c.K) + plane * (c.planes > 1 ? c.plane_stride : 0);
+  q.V = static_cast<uint8_t*>(c.V) + plane * (c.planes > 1 ? c.plane_stride : 0);
+  q.page = c.page_stride;
+  q.head = c.head_stride;
+  q.bits = c.bits;
+  q.chunks = q_chunks(c.D, c.bits);
+  q.groups = c.D / c.group;
+  q.params = c.page_size * q.chunks * 16;
+  return q;
+}
+
+fa_status grow(const fakv_cache& c, const int* slots, const int* add, int n, fa_stream_t stream) {
+  if (n < 0 || n > MAX_SEQS) return FA_ERR_INVALID_ARG;
+  if (n == 0) return FA_OK;
+  if (!slots || !add) return FA_ERR_INVALID_ARG;
+  if (!aligned(slots, 4) || !aligned(add, 4)) return FA_ERR_ALIGNMENT;
+  return launch_grow(c, slots, add, n, reinterpret_cast<cudaStream_t>(stream));
+}
+
+fa_status fork(const fakv_cache& c, const int* src, const int* dst, int n, fa_stream_t stream) {
+  if (n < 0 || n > MAX_SEQS) return FA_ERR_INVALID_ARG;
+  if ((long long)n * c.max_pages > (1ll << 31)) return FA_ERR_INVALID_ARG;  // rows held meanwhile
+  if (n == 0) return FA_OK;
+  if (!src || !dst) return FA_ERR_INVALID_ARG;
+  if (!aligned(src, 4) || !aligned(dst, 4)) return FA_ERR_ALIGNMENT;
+  return launch_fork(c, src, dst, n, reinterpret_cast<cudaStream_t>(stream));
+}
+
+fa_status release(const fakv_cache& c, const int* slots, const int* keep, int n, fa_stream_t stream) {
+  if (n < 0 || n > MAX_SEQS) return FA_ERR_INVALID_ARG;
+  if (n == 0) return FA_OK;
+  if (!slots) return FA_ERR_INVALID_ARG;
+  if (!aligned(slots, 4) || !aligned(keep, 4)) return FA_ERR_ALIGNMENT;
+  return launch_free(c, slots, keep, n, reinterpret_cast<cudaStream_t>(stream));
 }
 
 }  // namespace
@@ -173,18 +301,11 @@ FA_API fa_status fakv_append(const void* q, const void* k, const void* v, void* 
                              const fakv_cache* cache, const fakv_tokens* p, fa_stream_t stream) {
   fa_status st = check_cache(cache);
   if (st != FA_OK) return st;
-  st = check_tokens(cache, p, cu, slots);
+  st = check_tokens(cache, cache->dtype, p, cu, slots);
   if (st != FA_OK) return st;
   if (rope && (st = check_rope(rope, cache->D)) != FA_OK) return st;
   if (p->B == 0 || p->T == 0) return FA_OK;
-  const int es = esize(cache->dtype);
-  if (!k || !v || (p->H > 0 && (!q || !q_out))) return FA_ERR_INVALID_ARG;
-  if (!aligned(k, es) || !aligned(v, es) || (p->H > 0 && (!aligned(q, es) || !aligned(q_out, es))))
-    return FA_ERR_ALIGNMENT;
-  // in place: contiguous (the stride of one token or one head is no matter)
-  if (p->H > 0 && q == q_out &&
-      ((p->H > 1 && p->q_head != cache->D) || (p->T > 1 && p->q_token != (long long)p->H * cache->D)))
-    return FA_ERR_INVALID_ARG;
+  if ((st = check_append(q, k, v, q_out, cache->dtype, cache->D, p)) != FA_OK) return st;
   return launch_append(q, k, v, q_out, cu, slots, rope, *cache, *p, reinterpret_cast<cudaStream_t>(stream));
 }
 
@@ -192,18 +313,11 @@ FA_API fa_status fakv_attend(const void* q, void* O, float* LSE, const int* cu, 
                              const fakv_cache* cache, const fakv_tokens* p, fa_stream_t stream) {
   fa_status st = check_cache(cache);
   if (st != FA_OK) return st;
-  st = check_tokens(cache, p, cu, slots);
+  st = check_tokens(cache, cache->dtype, p, cu, slots);
   if (st != FA_OK) return st;
-  if (p->H < 1 || !dtype_ok(p->out_dtype)) return FA_ERR_INVALID_ARG;
-  if (!(p->scale > 0.f && std::isfinite(p->scale * LOG2E))) return FA_ERR_INVALID_ARG;
-  if ((p->causal != 0 && p->causal != 1) || p->window < 0) return FA_ERR_INVALID_ARG;
+  if ((st = check_attend(p)) != FA_OK) return st;
   if (p->B == 0 || p->T == 0) return FA_OK;
-  for (const void* x : {q, (const void*)O, (const void*)LSE}) {
-    if (!x) return FA_ERR_INVALID_ARG;
-    if (!aligned(x, 16)) return FA_ERR_ALIGNMENT;
-  }
-  const int es = esize(cache->dtype);
-  if (p->q_token * es % 16 != 0 || p->q_head * es % 16 != 0) return FA_ERR_ALIGNMENT;
+  if ((st = check_attend_rows(q, O, LSE, cache->dtype, p)) != FA_OK) return st;
   fakv_tokens t = *p;
   if (t.window >= cache->max_pages * cache->page_size) t.window = 0;  // hides nothing
   // Above 16 rows per sequence and kv head (on average: the lengths are on the device) tensor-core
@@ -222,41 +336,108 @@ FA_API fa_status fakv_attend(const void* q, void* O, float* LSE, const int* cu, 
 FA_API fa_status fakv_grow(const fakv_cache* cache, const int* slots, const int* add, int n,
                            fa_stream_t stream) {
   const fa_status st = check_pages(cache);
-  if (st != FA_OK) return st;
-  if (n < 0 || n > MAX_SEQS) return FA_ERR_INVALID_ARG;
-  if (n == 0) return FA_OK;
-  if (!slots || !add) return FA_ERR_INVALID_ARG;
-  if (!aligned(slots, 4) || !aligned(add, 4)) return FA_ERR_ALIGNMENT;
-  return launch_grow(*cache, slots, add, n, reinterpret_cast<cudaStream_t>(stream));
+  return st != FA_OK ? st : grow(*cache, slots, add, n, stream);
 }
 
 FA_API fa_status fakv_fork(const fakv_cache* cache, const int* src, const int* dst, int n,
                            fa_stream_t stream) {
   const fa_status st = check_pages(cache);
-  if (st != FA_OK) return st;
-  if (n < 0 || n > MAX_SEQS) return FA_ERR_INVALID_ARG;
-  if ((long long)n * cache->max_pages > (1ll << 31)) return FA_ERR_INVALID_ARG;  // rows held meanwhile
-  if (n == 0) return FA_OK;
-  if (!src || !dst) return FA_ERR_INVALID_ARG;
-  if (!aligned(src, 4) || !aligned(dst, 4)) return FA_ERR_ALIGNMENT;
-  return launch_fork(*cache, src, dst, n, reinterpret_cast<cudaStream_t>(stream));
+  return st != FA_OK ? st : kv::fork(*cache, src, dst, n, stream);
 }
 
 FA_API fa_status fakv_free(const fakv_cache* cache, const int* slots, const int* keep, int n,
                            fa_stream_t stream) {
   const fa_status st = check_pages(cache);
-  if (st != FA_OK) return st;
-  if (n < 0 || n > MAX_SEQS) return FA_ERR_INVALID_ARG;
-  if (n == 0) return FA_OK;
-  if (!slots) return FA_ERR_INVALID_ARG;
-  if (!aligned(slots, 4) || !aligned(keep, 4)) return FA_ERR_ALIGNMENT;
-  return launch_free(*cache, slots, keep, n, reinterpret_cast<cudaStream_t>(stream));
+  return st != FA_OK ? st : release(*cache, slots, keep, n, stream);
 }
 
 FA_API fa_status fakv_compact(const fakv_cache* cache, fa_stream_t stream) {
   const fa_status st = check_pages(cache);
   if (st != FA_OK) return st;
   return launch_compact(*cache, reinterpret_cast<cudaStream_t>(stream));
+}
+
+// ------------------------------------------------------------------ the cache in 4 or 8 bits
+FA_API long long fakv_qblock_bytes(int page_size, int D, int bits, int group) {
+  return quant_ok(page_size, D, bits, group) ? (long long)page_size * quant_token(D, bits, group) : 0;
+}
+
+FA_API fa_status fakv_qappend(const void* q, const void* k, const void* v, void* q_out,
+                              const int* cu, const int* slots, const fakv_rope* rope,
+                              const fakv_qcache* cache, const fakv_tokens* p, fa_stream_t stream) {
+  fakv_cache pages;
+  fa_status st = check_qcache(cache, &pages);
+  if (st != FA_OK) return st;
+  if ((st = check_tokens(&pages, cache->dtype, p, cu, slots)) != FA_OK) return st;
+  if (rope && (st = check_rope(rope, cache->D)) != FA_OK) return st;
+  if (p->B == 0 || p->T == 0) return FA_OK;
+  if ((st = check_append(q, k, v, q_out, cache->dtype, cache->D, p)) != FA_OK) return st;
+  return launch_qappend(q, k, v, q_out, cu, slots, rope, qcache_of(*cache, pages, p->plane), *p,
+                        reinterpret_cast<cudaStream_t>(stream));
+}
+
+FA_API fa_status fakv_qread(void* K_out, void* V_out, const int* cu, const int* slots,
+                            const int* first, const fakv_qcache* cache, const fakv_tokens* p,
+                            fa_stream_t stream) {
+  fakv_cache pages;
+  fa_status st = check_qcache(cache, &pages);
+  if (st != FA_OK) return st;
+  if (!p) return FA_ERR_INVALID_ARG;
+  fakv_tokens t = {};
+  t.B = p->B;
+  t.T = p->T;
+  t.plane = p->plane;
+  t.out_dtype = p->out_dtype;
+  if ((st = check_tokens(&pages, cache->dtype, &t, cu, slots)) != FA_OK) return st;
+  if (!dtype_ok(t.out_dtype) || (double)t.T * cache->HKV > 1073741824.0) return FA_ERR_INVALID_ARG;
+  if (!aligned(first, 4)) return FA_ERR_ALIGNMENT;
+  if (t.B == 0 || t.T == 0) return FA_OK;
+  if (!K_out || !V_out) return FA_ERR_INVALID_ARG;
+  if (!aligned(K_out, 16) || !aligned(V_out, 16)) return FA_ERR_ALIGNMENT;
+  return launch_qread(K_out, V_out, cu, slots, first, qcache_of(*cache, pages, t.plane), t,
+                      reinterpret_cast<cudaStream_t>(stream));
+}
+
+FA_API fa_status fakv_qattend(const void* q, void* O, float* LSE, const int* cu, const int* slots,
+                              const fakv_qcache* cache, const fakv_tokens* p, fa_stream_t stream) {
+  fakv_cache pages;
+  fa_status st = check_qcache(cache, &pages);
+  if (st != FA_OK) return st;
+  if ((st = check_tokens(&pages, cache->dtype, p, cu, slots)) != FA_OK) return st;
+  if ((st = check_attend(p)) != FA_OK) return st;
+  if (p->B == 0 || p->T == 0) return FA_OK;
+  if ((st = check_attend_rows(q, O, LSE, cache->dtype, p)) != FA_OK) return st;
+  fakv_tokens t = *p;
+  if (t.window >= cache->max_pages * cache->page_size) t.window = 0;  // hides nothing
+  return launch_qattend_rows(q, O, LSE, cu, slots, qcache_of(*cache, pages, p->plane), t,
+                             reinterpret_cast<cudaStream_t>(stream));
+}
+
+FA_API fa_status fakv_qgrow(const fakv_qcache* cache, const int* slots, const int* add, int n,
+                            fa_stream_t stream) {
+  fakv_cache pages;
+  const fa_status st = check_qpages(cache, &pages);
+  return st != FA_OK ? st : grow(pages, slots, add, n, stream);
+}
+
+FA_API fa_status fakv_qfork(const fakv_qcache* cache, const int* src, const int* dst, int n,
+                            fa_stream_t stream) {
+  fakv_cache pages;
+  const fa_status st = check_qpages(cache, &pages);
+  return st != FA_OK ? st : kv::fork(pages, src, dst, n, stream);
+}
+
+FA_API fa_status fakv_qfree(const fakv_qcache* cache, const int* slots, const int* keep, int n,
+                            fa_stream_t stream) {
+  fakv_cache pages;
+  const fa_status st = check_qpages(cache, &pages);
+  return st != FA_OK ? st : release(pages, slots, keep, n, stream);
+}
+
+FA_API fa_status fakv_qcompact(const fakv_qcache* cache, fa_stream_t stream) {
+  fakv_cache pages;
+  const fa_status st = check_qpages(cache, &pages);
+  return st != FA_OK ? st : launch_compact(pages, reinterpret_cast<cudaStream_t>(stream));
 }
 
 }  // extern "C"

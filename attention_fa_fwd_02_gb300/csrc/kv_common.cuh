@@ -56,6 +56,37 @@ __device__ __forceinline__ int page_of(const fakv_cache& c, int slot, int pos, i
   return -1;
 }
 
+// cos and sin of pos * freq turns (see the head of kv_rope.cu)
+__device__ __forceinline__ float2 turn(long long pos, unsigned long long freq) {
+  const unsigned long long t = (unsigned long long)pos * freq;
+  const unsigned quarter = (unsigned)((t + (1ull << 61)) >> 62);
+  const long long rest = (long long)(t - ((unsigned long long)quarter << 62));
+  float s, c;
+  sincospif((float)(int)(rest >> 30) * 0x1p-33f, &s, &c);  // the angle in units of pi
+  if (quarter & 1) { const float x = c; c = -s; s = x; }
+  if (quarter & 2) { c = -c; s = -s; }
+  return make_float2(c, s);
+}
+
+// The sequence of row t: the last b with cu[b] <= t (32 probes per round, one warp), or
+// -1 for rows past the last sequence. cu is probed inside [0, B] whatever it holds.
+__device__ __forceinline__ int find_seq(const int* cu, int B, int t) {
+  const int lane = ptx::lane_id();
+  if (t >= cu[B]) return -1;
+  int lo = 0, n = B;  // the answer lies in [lo, lo + n)
+  while (n > 1) {
+    const int step = (n + 31) / 32;
+    const int at = lo + lane * step;
+    const bool below = lane * step < n && cu[at] <= t;
+    const int hits = __popc(__ballot_sync(0xffffffffu, below));
+    if (hits == 0) return -1;
+    const int first = (hits - 1) * step;
+    n = min(step, n - first);
+    lo += first;
+  }
+  return cu[lo] <= t ? lo : -1;
+}
+
 inline int log2_of(int x) {
   int s = 0;
   while ((1 << s) < x) ++s;

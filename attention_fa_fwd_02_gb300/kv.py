@@ -14,6 +14,8 @@ Tokens of a step are the rows of ``q`` [T, H, D], ``k`` and ``v`` [T, HKV, D]; s
 cu[b] .. cu[b + 1] - 1 and is slot slots[b] (None: slot b). Everything that changes from step to step is
 read on the device, so a step can be captured into a CUDA graph and replayed.
 
+A cache held in 4 or 8 bits is ``QuantCache``: the same calls, and ``read``, which gives its tokens back as K and V.
+
 A training step rotates with ``rope.apply`` and its gradient with ``rope.backward``.
 """
 from __future__ import annotations
@@ -31,7 +33,8 @@ STATUS_BITS = {NO_PAGES: "too few free pages", BAD_SLOT: "slot out of range", RE
                BAD_LENGTH: "length out of range"}
 KINDS = {"none": 0, "linear": 1, "ntk": 2, "bands": 3, "yarn": 4}
 EXPORTS = ("fakv_rope_freqs", "fakv_rope_apply", "fakv_append", "fakv_attend", "fakv_grow", "fakv_fork",
-           "fakv_free", "fakv_compact")
+           "fakv_free", "fakv_compact", "fakv_qblock_bytes", "fakv_qappend", "fakv_qread", "fakv_qattend", "fakv_qgrow",
+           "fakv_qfork", "fakv_qfree", "fakv_qcompact")
 _DT = {torch.float32: fa.FA_F32, torch.bfloat16: fa.FA_BF16}
 _i, _ll, _vp = ctypes.c_int, ctypes.c_longlong, ctypes.c_void_p
 
@@ -49,6 +52,13 @@ class fakv_cache(ctypes.Structure):
                 + [(n, _ll) for n in ("plane_stride", "page_stride", "token_stride", "head_stride", "table_stride")]
                 + [(n, _i) for n in ("planes", "num_pages", "page_size", "HKV", "D", "max_slots", "max_pages",
                                      "dtype")])
+
+
+class fakv_qcache(ctypes.Structure):
+    _fields_ = ([(n, _vp) for n in ("K", "V", "table", "lens", "refs", "status")]
+                + [(n, _ll) for n in ("plane_stride", "page_stride", "head_stride", "table_stride")]
+                + [(n, _i) for n in ("planes", "num_pages", "page_size", "HKV", "D", "max_slots", "max_pages", "bits",
+                                     "group", "dtype")])
 
 
 class fakv_scaling(ctypes.Structure):
@@ -98,10 +108,18 @@ def _lib():
                 ("fakv_grow", [P(fakv_cache), _vp, _vp, _i, _vp]),
                 ("fakv_fork", [P(fakv_cache), _vp, _vp, _i, _vp]),
                 ("fakv_free", [P(fakv_cache), _vp, _vp, _i, _vp]),
-                ("fakv_compact", [P(fakv_cache), _vp])):
+                ("fakv_compact", [P(fakv_cache), _vp]),
+                ("fakv_qappend", [_vp] * 6 + [P(fakv_rope), P(fakv_qcache), _vp, _vp]),
+                ("fakv_qread", [_vp] * 5 + [P(fakv_qcache), _vp, _vp]),
+                ("fakv_qattend", [_vp] * 5 + [P(fakv_qcache), _vp, _vp]),
+                ("fakv_qgrow", [P(fakv_qcache), _vp, _vp, _i, _vp]),
+                ("fakv_qfork", [P(fakv_qcache), _vp, _vp, _i, _vp]),
+                ("fakv_qfree", [P(fakv_qcache), _vp, _vp, _i, _vp]),
+                ("fakv_qcompact", [P(fakv_qcache), _vp]),
+                ("fakv_qblock_bytes", [_i] * 4)):
             f = getattr(lib, name)
             f.argtypes = args
-            f.restype = _i
+            f.restype = _ll if name == "fakv_qblock_bytes" else _i
         _bound = lib
     return _bound
 
@@ -250,26 +268,11 @@ class Rope:
         return self.apply(dq, dk, positions, True, out, stream)
 
 
-class PagedCache:
-    """Key / value pages of sequences in slots. ``k``, ``v``: [planes, pages, page_size, kv heads, D] (or without the
-    planes; ``layout`` "heads": [planes, pages, kv heads, page_size, D]), bf16 or fp32, alike in shape and strides;
-    ``table`` [slots, max_pages] int32 page numbers (-1: none), ``lens`` [slots] int32, ``refs`` [pages] int32: how
-    many rows hold a page. The tensors stay the caller's; the methods change them in place (a length is lowered with
-    ``free``, which releases the pages). ``status`` [1] int32 collects what the device refused (``check``)."""
+class _Pages:
+    """What caches have in common: their tensors, and the calls that are theirs whatever a page holds."""
 
-    def __init__(self, k, v, table, lens, refs, layout="tokens", status=None):
-        if layout not in ("tokens", "heads"):
-            raise ValueError('layout must be "tokens" or "heads"')
-        if k.dim() == 4 and v.dim() == 4:
-            k, v = k[None], v[None]
-        if k.dim() != 5 or k.shape != v.shape or k.dtype != v.dtype or k.device != v.device or k.dtype not in _DT:
-            raise ValueError("k and v must be alike, bf16 or fp32, [planes, pages, page_size, kv heads, D]")
-        if k.stride() != v.stride() or k.stride(4) != 1:
-            raise ValueError("k and v must have the same strides and contiguous columns")
+    def _init_pages(self, k, v, table, lens, refs, status):
         dev = k.device
-        if not k.is_cuda:
-            raise ValueError("the cache must be on a CUDA device")
-        t, h = (2, 3) if layout == "tokens" else (3, 2)
         if table.dim() != 2 or table.dtype != torch.int32 or table.device != dev or table.stride(1) != 1:
             raise ValueError("table must be an int32 matrix with contiguous rows, on the cache's device")
         _ints(lens, "lens", table.shape[0], dev)
@@ -277,24 +280,8 @@ class PagedCache:
         self.status = torch.zeros(1, dtype=torch.int32, device=dev) if status is None \
             else _ints(status, "status", 1, dev)
         self.k, self.v, self.table, self.lens, self.refs, self.device = k, v, table, lens, refs, dev
-        self.planes, self.page_size, self.kv_heads, self.head_dim = k.shape[0], k.shape[t], k.shape[h], k.shape[4]
-        self.slots, self.dtype, self._index = table.shape[0], k.dtype, dev.index
+        self.slots, self._index = table.shape[0], dev.index
         self._tensors = (k, v, table, lens, refs, self.status)
-        self._c = fakv_cache(k.data_ptr(), v.data_ptr(), table.data_ptr(), lens.data_ptr(), refs.data_ptr(),
-                             self.status.data_ptr(), k.stride(0), k.stride(1), k.stride(t), k.stride(h),
-                             table.stride(0), k.shape[0], k.shape[1], k.shape[t], k.shape[h], k.shape[4],
-                             table.shape[0], table.shape[1], _DT[k.dtype])
-        self._ref = ctypes.byref(self._c)
-
-    @classmethod
-    def create(cls, planes, pages, page_size, kv_heads, head_dim, slots, max_pages, dtype=torch.bfloat16,
-               layout="tokens", device="cuda"):
-        """An empty cache (its page memory zeroed)."""
-        inner = (page_size, kv_heads) if layout == "tokens" else (kv_heads, page_size)
-        k = torch.zeros(planes, pages, *inner, head_dim, dtype=dtype, device=device)
-        return cls(k, torch.zeros_like(k), torch.full((slots, max_pages), -1, dtype=torch.int32, device=device),
-                   torch.zeros(slots, dtype=torch.int32, device=device),
-                   torch.zeros(pages, dtype=torch.int32, device=device), layout)
 
     def _batch(self, cu, slots, layer):
         """Sequences of a call and the address of its slots."""
@@ -330,10 +317,10 @@ class PagedCache:
             if q is not None:
                 o = on.empty(q, q.shape, dt) if out is None else _out(out, "out", q.shape, dt, dev)
                 op = o.data_ptr()
-            _check(_lib().fakv_append(
+            _check(getattr(_lib(), self._entry + "append")(
                 qp, k.data_ptr(), v.data_ptr(), op, cu.data_ptr(), sp, None if rope is None else rope._ref, self._ref,
                 _pack_tokens(B, T, H, layer, sq[0], sq[1], sk[0], sk[1], sv[0], sv[1], 1.0, 1, 0, 0), on.handle),
-                "fakv_append")
+                self._entry + "append")
         finally:
             on.leave()
         return o
@@ -353,16 +340,17 @@ class PagedCache:
             out = on.empty(q, shape, odt) if out is None else _out(out, "out", shape, odt, dev)
             lse = on.empty(q, shape[:2], torch.float32) if lse is None \
                 else _out(lse, "lse", shape[:2], torch.float32, dev)
-            _check(_lib().fakv_attend(
+            _check(getattr(_lib(), self._entry + "attend")(
                 q.data_ptr(), out.data_ptr(), lse.data_ptr(), cu.data_ptr(), sp, self._ref,
                 _pack_tokens(B, shape[0], shape[1], layer, sq[0], sq[1], 0, 0, 0, 0,
                              D ** -0.5 if scale is None else scale, bool(causal), window, _DT[odt]), on.handle),
-                "fakv_attend")
+                self._entry + "attend")
         finally:
             on.leave()
         return out, lse
 
-    def _list(self, call, where, a, names, b, stream):
+    def _list(self, what, a, names, b, stream):
+        where = self._entry + what
         n = _ints(a, names[0], None, self.device)
         bp = None
         if b is not None:
@@ -370,7 +358,7 @@ class PagedCache:
             bp = b.data_ptr()
         on = _on(self._index, stream, a, b, *self._tensors)
         try:
-            _check(call(self._ref, a.data_ptr(), bp, n, on.handle), where)
+            _check(getattr(_lib(), where)(self._ref, a.data_ptr(), bp, n, on.handle), where)
         finally:
             on.leave()
 
@@ -378,22 +366,22 @@ class PagedCache:
         """Room for add[i] more tokens in slots[i] (the lengths grow by it): new pages, and a copy of a shared last
         page that has room. An entry that cannot be served (``check`` tells) keeps its length; an append that counts
         on it would write over the slot's last tokens."""
-        self._list(_lib().fakv_grow, "fakv_grow", slots, ("slots", "add"), add, stream)
+        self._list("grow", slots, ("slots", "add"), add, stream)
 
     def fork(self, src, dst, stream=None):
         """Slots dst[i] become copies of slots src[i] that share their pages; sources are read as they were before
         the call."""
-        self._list(_lib().fakv_fork, "fakv_fork", src, ("src", "dst"), dst, stream)
+        self._list("fork", src, ("src", "dst"), dst, stream)
 
     def free(self, slots, keep=None, stream=None):
         """Slots cut to their first keep[i] tokens (None: emptied); pages that no slot holds any more are free."""
-        self._list(_lib().fakv_free, "fakv_free", slots, ("slots", "keep"), keep, stream)
+        self._list("free", slots, ("slots", "keep"), keep, stream)
 
     def compact(self, stream=None):
         """Moves pages so that those in use are the lowest-numbered ones, and renumbers the table."""
         on = _on(self._index, stream, *self._tensors)
         try:
-            _check(_lib().fakv_compact(self._ref, on.handle), "fakv_compact")
+            _check(getattr(_lib(), self._entry + "compact")(self._ref, on.handle), self._entry + "compact")
         finally:
             on.leave()
 
@@ -411,3 +399,130 @@ class PagedCache:
             _check(fa.fa_device_status(on.handle), "fa_device_status")
         finally:
             on.leave()
+
+
+class PagedCache(_Pages):
+    """Key / value pages of sequences in slots. ``k``, ``v``: [planes, pages, page_size, kv heads, D] (or without the
+    planes; ``layout`` "heads": [planes, pages, kv heads, page_size, D]), bf16 or fp32, alike in shape and strides;
+    ``table`` [slots, max_pages] int32 page numbers (-1: none), ``lens`` [slots] int32, ``refs`` [pages] int32: how
+    many rows hold a page. The tensors stay the caller's; the methods change them in place (a length is lowered with
+    ``free``, which releases the pages). ``status`` [1] int32 collects what the device refused (``check``)."""
+
+    _entry = "fakv_"
+
+    def __init__(self, k, v, table, lens, refs, layout="tokens", status=None):
+        if layout not in ("tokens", "heads"):
+            raise ValueError('layout must be "tokens" or "heads"')
+        if k.dim() == 4 and v.dim() == 4:
+            k, v = k[None], v[None]
+        if k.dim() != 5 or k.shape != v.shape or k.dtype != v.dtype or k.device != v.device or k.dtype not in _DT:
+            raise ValueError("k and v must be alike, bf16 or fp32, [planes, pages, page_size, kv heads, D]")
+        if k.stride() != v.stride() or k.stride(4) != 1:
+            raise ValueError("k and v must have the same strides and contiguous columns")
+        dev = k.device
+        if not k.is_cuda:
+            raise ValueError("the cache must be on a CUDA device")
+        t, h = (2, 3) if layout == "tokens" else (3, 2)
+        self._init_pages(k, v, table, lens, refs, status)
+        self.planes, self.page_size, self.kv_heads, self.head_dim = k.shape[0], k.shape[t], k.shape[h], k.shape[4]
+        self.dtype = k.dtype
+        self._c = fakv_cache(k.data_ptr(), v.data_ptr(), table.data_ptr(), lens.data_ptr(), refs.data_ptr(),
+                             self.status.data_ptr(), k.stride(0), k.stride(1), k.stride(t), k.stride(h),
+                             table.stride(0), k.shape[0], k.shape[1], k.shape[t], k.shape[h], k.shape[4],
+                             table.shape[0], table.shape[1], _DT[k.dtype])
+        self._ref = ctypes.byref(self._c)
+
+    @classmethod
+    def create(cls, planes, pages, page_size, kv_heads, head_dim, slots, max_pages, dtype=torch.bfloat16,
+               layout="tokens", device="cuda"):
+        """An empty cache (its page memory zeroed)."""
+        inner = (page_size, kv_heads) if layout == "tokens" else (kv_heads, page_size)
+        k = torch.zeros(planes, pages, *inner, head_dim, dtype=dtype, device=device)
+        return cls(k, torch.zeros_like(k), torch.full((slots, max_pages), -1, dtype=torch.int32, device=device),
+                   torch.zeros(slots, dtype=torch.int32, device=device),
+                   torch.zeros(pages, dtype=torch.int32, device=device), layout)
+
+
+class QuantCache(_Pages):
+    """A paged cache held in ``bits`` (4 or 8): each ``group`` of columns of a token's K (or V) row of one head has a
+    scale and an offset, each column a code (include/fakv.h has the format and what it costs in precision). ``k``,
+    ``v``: uint8 [planes, pages, kv heads, ``block_bytes``] (or without the planes); ``group``: head_dim, or 64 where
+    that is 128 (None: 64 there); ``dtype``: of q, k and v. The rest as in PagedCache, and the same methods."""
+
+    _entry = "fakv_q"
+
+    def __init__(self, k, v, table, lens, refs, page_size, head_dim, bits=4, group=None, dtype=torch.bfloat16, status=None):
+        group = _group(head_dim, group)
+        block = self.block_bytes(page_size, head_dim, bits, group)
+        if k.dim() == 3 and v.dim() == 3:
+            k, v = k[None], v[None]
+        if k.dim() != 4 or k.shape != v.shape or k.dtype != torch.uint8 or v.dtype != torch.uint8 or k.device != v.device:
+            raise ValueError("k and v must be alike, uint8, [planes, pages, kv heads, block_bytes]")
+        if k.shape[3] != block:
+            raise ValueError(f"blocks of {block} bytes are wanted, not of {k.shape[3]}")
+        if k.stride() != v.stride() or k.stride(3) != 1:
+            raise ValueError("k and v must have the same strides and contiguous blocks")
+        if dtype not in _DT:
+            raise TypeError(f"unsupported dtype {dtype}")
+        if not k.is_cuda:
+            raise ValueError("the cache must be on a CUDA device")
+        self._init_pages(k, v, table, lens, refs, status)
+        self.planes, self.page_size, self.kv_heads, self.head_dim = k.shape[0], page_size, k.shape[2], head_dim
+        self.bits, self.group, self.dtype = bits, group, dtype
+        self._c = fakv_qcache(k.data_ptr(), v.data_ptr(), table.data_ptr(), lens.data_ptr(), refs.data_ptr(),
+                              self.status.data_ptr(), k.stride(0), k.stride(1), k.stride(2), table.stride(0), k.shape[0],
+                              k.shape[1], page_size, k.shape[2], head_dim, table.shape[0], table.shape[1], bits, group,
+                              _DT[dtype])
+        self._ref = ctypes.byref(self._c)
+
+    @staticmethod
+    def block_bytes(page_size, head_dim, bits=4, group=None):
+        """Bytes of a page of one head."""
+        n = _lib().fakv_qblock_bytes(page_size, head_dim, bits, _group(head_dim, group))
+        if n == 0:
+            raise ValueError("page_size must be a power of two, 8 .. 1024, head_dim a multiple of 16 up to 128, bits 4 "
+                             "or 8, group head_dim (or 64 where that is 128)")
+        return n
+
+    @classmethod
+    def create(cls, planes, pages, page_size, kv_heads, head_dim, slots, max_pages, bits=4, group=None,
+               dtype=torch.bfloat16, device="cuda"):
+        """An empty cache (its page memory zeroed)."""
+        k = torch.zeros(planes, pages, kv_heads, cls.block_bytes(page_size, head_dim, bits, group), dtype=torch.uint8,
+                        device=device)
+        return cls(k, torch.zeros_like(k), torch.full((slots, max_pages), -1, dtype=torch.int32, device=device),
+                   torch.zeros(slots, dtype=torch.int32, device=device),
+                   torch.zeros(pages, dtype=torch.int32, device=device), page_size, head_dim, bits, group, dtype)
+
+    def read(self, cu, rows, slots=None, first=None, layer=0, out_dtype=None, out=None, stream=None):
+        """K and V [rows, HKV, D] that the cache stands for: row cu[b] + i is position first[b] + i of sequence b's
+        slot (``first`` None: its last tokens, as ``append`` counts them). Rows past cu[-1] are not written; those of
+        tokens that do not exist are zeros (``check`` tells). ``out``: a pair of contiguous tensors to write."""
+        dev = self.device
+        B, sp = self._batch(cu, slots, layer)
+        if rows < 0:
+            raise ValueError("rows must not be negative")
+        fp = None
+        if first is not None:
+            _ints(first, "first", B, dev)
+            fp = first.data_ptr()
+        shape = (rows, self.kv_heads, self.head_dim)
+        odt = out_dtype if out_dtype is not None else self.dtype if out is None else out[0].dtype
+        if odt not in _DT:
+            raise TypeError(f"unsupported output dtype {odt}")
+        on = _on(self._index, stream, cu, slots, first, *(out or ()), *self._tensors)
+        try:
+            if out is None:
+                k, v = on.empty(self.k, shape, odt), on.empty(self.k, shape, odt)
+            else:
+                k, v = (_out(t, f"out[{i}]", shape, odt, dev) for i, t in enumerate(out))
+            _check(_lib().fakv_qread(
+                k.data_ptr(), v.data_ptr(), cu.data_ptr(), sp, fp, self._ref,
+                _pack_tokens(B, rows, 0, layer, 0, 0, 0, 0, 0, 0, 1.0, 1, 0, _DT[odt]), on.handle), "fakv_qread")
+        finally:
+            on.leave()
+        return k, v
+
+
+def _group(head_dim, group):
+    return (64 if head_dim == 128 else head_dim) if group is None else group

@@ -1,7 +1,8 @@
 /*
  * fakv.h -- C ABI of libfa.so for served and trained models' positions and key / value
  * caches: rotary positions, a paged cache, attention of new tokens over it, and the
- * cache's pages (sharing, growing, freeing, compacting). It uses fa.h's types, status
+ * cache's pages (sharing, growing, freeing, compacting); and the same for a cache held in 4 or
+ * 8 bits. It uses fa.h's types, status
  * codes, streams and ownership rules; fa_timing_* and fa_device_status cover its kernels too.
  *
  * The cache. Keys and values live in pages of `page_size` tokens. A slot is one
@@ -207,6 +208,85 @@ FA_API fa_status fakv_free(const fakv_cache* cache, const int* slots, const int*
  * numbers below L (in every plane), and all rows (over their whole width, whatever their
  * lengths) and counts follow: pages 0 .. L - 1 are then the used ones. */
 FA_API fa_status fakv_compact(const fakv_cache* cache, fa_stream_t stream);
+
+/* ---- the cache in 4 or 8 bits
+ * A cache like the one above whose pages hold codes. Of a token's K (or V) row of one head, each
+ * group of `group` columns x has a scale s and an offset z, both bf16, and a code per column:
+ *
+ *   z = the largest bf16 <= min x         s = the smallest bf16 >= (max x - z) / (2^bits - 1)
+ *   c = (x - z) / s, to the nearest integer (ties to even), at most 2^bits - 1    (s = 0: c = 0)
+ *
+ * (the differences and quotients are fp32, rounded to nearest), and stands for s c + z: at most
+ * s / 2 from x, where s is (max x - min x) / (2^bits - 1) but for the roundings of s and z
+ * (2^-7 of it, and 2^-7 |min x| / (2^bits - 1)). A group that holds NaN, infinity or a value of
+ * 2^126 or more has no such scale: its s and z are NaN, and so is all that it stands for.
+ *
+ * Memory, in bytes. Page p, head h in plane l is a block at K + l * plane_stride + p * page_stride
+ * + h * head_stride, of page_size * (16 chunks + 4 groups) bytes with chunks = ceil(D * bits / 128)
+ * and groups = D / group:
+ *   codes   [page_size / 8][chunks][8 tokens][16]: chunk k of a token has its columns
+ *           k * 128 / bits and on, in order, lowest bits first (columns from D on: 0)
+ *   params  [page_size][groups]: s in the low, z in the high 16 bits of a 32-bit word
+ * Slots, tables, lengths, counts, status, ownership, ordering, capture and what is refused are as
+ * above. */
+typedef struct {
+  void* K;                 /* 16-byte aligned */
+  void* V;
+  int* table;              /* [max_slots] rows of max_pages, table_stride apart; -1: no page */
+  int* lens;               /* [max_slots] */
+  int* refs;               /* [num_pages] */
+  int* status;             /* one word, or NULL */
+  long long plane_stride;  /* bytes; each but the planes' of one plane is a positive multiple */
+  long long page_stride;   /* of 16, and head_stride at least a block */
+  long long head_stride;
+  long long table_stride;  /* >= max_pages */
+  int planes;              /* >= 1 */
+  int num_pages;           /* >= 1 */
+  int page_size;           /* a power of two, 8 .. 1024 */
+  int HKV;
+  int D;                   /* a multiple of 16, 16 .. 128 */
+  int max_slots;
+  int max_pages;           /* max_pages * page_size <= 2^30 */
+  int bits;                /* 4 or 8 */
+  int group;               /* D, or 64 where D is 128 */
+  fa_dtype dtype;          /* of q, k and v */
+} fakv_qcache;
+
+/* Bytes of a block (a page of one head), or 0 for sizes that no cache has. */
+FA_API long long fakv_qblock_bytes(int page_size, int D, int bits, int group);
+
+/* fakv_append into such a cache: k turned by its positions where `rope` is given, in fp32 and
+ * without a rounding before its codes are formed; v; and q into q_out as fakv_append does. */
+FA_API fa_status fakv_qappend(const void* q, const void* k, const void* v, void* q_out,
+                              const int* cu, const int* slots, const fakv_rope* rope,
+                              const fakv_qcache* cache, const fakv_tokens* p, fa_stream_t stream);
+
+/* What the cache stands for, s c + z in fp32 with one rounding on store, as contiguous
+ * K_out, V_out [T, HKV, D] of out_dtype (16-byte aligned): row i of sequence b is position
+ * first[b] + i of its slot (first NULL: the slot's last tokens, position lens - n + i). Rows of a
+ * sequence whose token does not exist (a bad slot, a position outside [0, lens), no page) are
+ * zeros and set the status bit; rows from cu[B] on are not written. Of `p` the call reads B, T,
+ * plane and out_dtype. One launch. */
+FA_API fa_status fakv_qread(void* K_out, void* V_out, const int* cu, const int* slots,
+                            const int* first, const fakv_qcache* cache, const fakv_tokens* p,
+                            fa_stream_t stream);
+
+/* fakv_attend over what such a cache stands for. A key whose group is NaN makes O and LSE of the
+ * rows that see it NaN (a value: their O, in the group's columns), and of no other row. Scores:
+ * bf16 queries times codes, exact products with fp32 sums (fp32 queries in three bf16 terms, 2^-24),
+ * scaled and offset in fp32. The probabilities enter the second product times a key's scale, in two
+ * bf16 terms (2^-16). */
+FA_API fa_status fakv_qattend(const void* q, void* O, float* LSE, const int* cu, const int* slots,
+                              const fakv_qcache* cache, const fakv_tokens* p, fa_stream_t stream);
+
+/* The page calls. */
+FA_API fa_status fakv_qgrow(const fakv_qcache* cache, const int* slots, const int* add, int n,
+                            fa_stream_t stream);
+FA_API fa_status fakv_qfork(const fakv_qcache* cache, const int* src, const int* dst, int n,
+                            fa_stream_t stream);
+FA_API fa_status fakv_qfree(const fakv_qcache* cache, const int* slots, const int* keep, int n,
+                            fa_stream_t stream);
+FA_API fa_status fakv_qcompact(const fakv_qcache* cache, fa_stream_t stream);
 
 #ifdef __cplusplus
 }
