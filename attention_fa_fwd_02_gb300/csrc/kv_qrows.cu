@@ -4,16 +4,20 @@
 // Workers, parts, copies and joins are those of kv_rows.cu. With s, z of a key's group g and codes
 // c = centre + x (centre 8 or 128), its K and V are s x + z', z' = z + centre s, so that
 //
-//   scores  S = sum_g s_g (sum_{d in g} q_d x_d) + z'_g (sum_{d in g} q_d): codes are the exact bf16
-//           operands of the products, a key's scales come after them, in fp32
-//   O^T     O_d = sum_k (p_k s_k) x_kd + sum_k p_k z'_k: the scales enter the probabilities (two bf16
-//           terms), the offsets are one more sum per row and group
+//   scores  S = sum_g s_g (sum_{d in g} q_d c_d) + z_g (sum_{d in g} q_d): codes are exact fp16
+//           operands, a key's scales come after the products, in fp32. q times a power of two per row
+//           that brings its largest value to 2^14 is fp16 too, exactly but for what is 2^-28 of that
+//   O^T     O_d = sum_k (p_k s_k) x_kd + sum_k p_k z'_k: the scales enter the probabilities, times a power
+//           of two that keeps the largest scale so far just below 2^7; the offsets are one more sum
+//           per row and group. p s is one fp16 term where O is bf16 (2^-12 of itself, an eighth of O's
+//           own rounding), two (2^-23) where O is fp32; what is below 2^-30 of the largest p s rounds to
+//           2^-40 of it
 //
-// so nothing of the cache is rounded again. A code costs less than an instruction (kv_quant.cuh):
+// so nothing of the cache is rounded again. A code costs about an instruction (kv_quant.cuh):
 //   K  columns are what is summed over, in any order: a thread takes the 8 (4) columns of one
 //      32-bit word of its key, and q's fragments are laid out to match
-//   V  keys are summed over, two of each register: the halves of two keys' words are put side by side
-//      first (one permute), so that every nibble pair is one column of two keys
+//   V  keys are summed over, two of each register: the codes of two keys' words are put side by side
+//      first (permutes), so that every pair is one column of two keys
 #include <algorithm>
 #include "kv_quant.cuh"
 #include "kv_rows.cuh"
@@ -38,13 +42,14 @@ struct QRowsArgs {
   Partials part;
 };
 
-template <typename E, int BITS, int D, int NTR>
+template <typename E, bool OUT_BF, int BITS, int D, int NG_, int NTR>
 struct QRowsCfg {
   static constexpr bool F32 = sizeof(E) == 4;
-  static constexpr int TERMS = F32 ? 3 : 1;       // bf16 terms of q
+  static constexpr int TERMS = F32 ? 2 : 1;       // fp16 terms of q
+  static constexpr int PT = OUT_BF ? 1 : 2;       // and of P times a key's scale
   static constexpr int R = 8 * NTR;               // rows of an item
   static constexpr int CH = D * BITS / 128;       // 16-byte chunks of a key's codes
-  static constexpr int NG = D / 64;               // groups of a key
+  static constexpr int NG = NG_;                  // groups of a key
   static constexpr int KS = D / 16;               // k16 steps of q
   static constexpr int GROUP = 32;                // keys of a step
   static constexpr int KT = GROUP / 16;
@@ -55,31 +60,48 @@ struct QRowsCfg {
   static constexpr int OS = D + 4;                // floats of a row of O in shared memory (bank spread)
   static constexpr int CTAS_PER_SM = Q_REGS ? 3 : 2;
   static constexpr int ROOM = CTAS_PER_SM == 3 ? 18432 : 28160;
-  static constexpr int NS = std::min(12, (ROOM - Q_BYTES) / SLOT);
-  static constexpr int WARP_BYTES = std::max({NS * SLOT + Q_BYTES, R * OS * 4, 16400});
+  static constexpr int NP = std::min(6, (ROOM - Q_BYTES) / (2 * SLOT));  // steps of the ring
+  static constexpr int WARP_BYTES = std::max({NP * 2 * SLOT + Q_BYTES, R * OS * 4, 16512});
   static constexpr int SMEM = WARPS * WARP_BYTES;
-  static_assert(NS >= 2 && WARP_BYTES % 16 == 0 && SLOT % 16 == 0, "the ring");
+  static_assert(NP >= 2 && WARP_BYTES % 128 == 0 && SLOT % 128 == 0 && Q_BYTES % 128 == 0, "the ring");
   static_assert(SMEM >= 4 * 16385, "the plan's scratch");
   static constexpr int STATIC = (int)sizeof(PlanShared<NTHREADS, WARPS>) + WARPS * (R * 8 + 20);
   static_assert(CTAS_PER_SM * (SMEM + (STATIC + 1023) / 1024 * 1024 + 1024) <= 228 * 1024, "shared memory of the CTAs of an SM");
 };
 
-// x = sum of three bf16 terms
-__device__ __forceinline__ void split3(float x, float (&t)[3]) {
-#pragma unroll
-  for (int i = 0; i < 3; ++i) {
-    t[i] = __bfloat162float(__float2bfloat16_rn(x));
-    x -= t[i];
-  }
+__device__ __forceinline__ void mma_f16(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+  asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
+      : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
+// a and b as fp16 (low, high); rest: what is left of them
+__device__ __forceinline__ uint32_t half2_of(float a, float b, float2* rest = nullptr) {
+  const __half2 h = __floats2half2_rn(a, b);
+  if (rest) {
+    const float2 f = __half22float2(h);
+    *rest = make_float2(a - f.x, b - f.y);
+  }
+  return *reinterpret_cast<const uint32_t*>(&h);
+}
+__device__ __forceinline__ void cp16z(uint32_t dst, const void* src, int bytes) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
+}
+__device__ __forceinline__ void cp16z_if(bool go, uint32_t dst, const void* src, int bytes) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %3, 0;\n\t"
+      "@p cp.async.cg.shared.global [%0], [%1], 16, %2;\n\t}" ::"r"(dst), "l"(src), "r"(bytes), "r"((int)go)
+      : "memory");
+}
+__device__ __forceinline__ float pow2(int e) { return __int_as_float((e + 127) << 23); }  // -126 <= e <= 127
+__device__ __forceinline__ int exponent(float x) { return (__float_as_int(x) >> 23) - 127; }  // of x > 0
 
-template <typename E, int BITS, int D, int NTR>
-__global__ void __launch_bounds__(NTHREADS, QRowsCfg<E, BITS, D, NTR>::CTAS_PER_SM)
+template <typename E, bool OUT_BF, int BITS, int D, int NG_, int NTR>
+__global__ void __launch_bounds__(NTHREADS, QRowsCfg<E, OUT_BF, BITS, D, NG_, NTR>::CTAS_PER_SM)
     qattend_rows_kernel(const __grid_constant__ QRowsArgs a) {
-  using C = QRowsCfg<E, BITS, D, NTR>;
-  constexpr int CH = C::CH, R = C::R, NS = C::NS, GROUP = C::GROUP, KT = C::KT, NG = C::NG, KS = C::KS;
-  constexpr int TERMS = C::TERMS;
-  constexpr bool CENTRED = C::F32;  // K's codes: centred before the product, or their constant taken off after it
+  using C = QRowsCfg<E, OUT_BF, BITS, D, NG_, NTR>;
+  constexpr int CH = C::CH, R = C::R, NP = C::NP, GROUP = C::GROUP, KT = C::KT, NG = C::NG, KS = C::KS;
+  constexpr int TERMS = C::TERMS, PT = C::PT;
+  constexpr bool CENTRED = !OUT_BF;  // K's codes: centred before the product, or their constant (1024) taken off after it
   constexpr float CENTRE = BITS == 4 ? 8.f : 128.f;
   constexpr int WH = CH / 2;          // V words of a lane and key
   constexpr int J = BITS == 4 ? 4 : 2;  // output tiles of a word: columns j and j + J of each lane's
@@ -91,7 +113,7 @@ __global__ void __launch_bounds__(NTHREADS, QRowsCfg<E, BITS, D, NTR>::CTAS_PER_
   const int quad = lane & 3, oct = lane >> 2;  // mma fragments: columns 2 quad, 2 quad + 1; row oct
   const fakv_cache& c = a.c;
   const Geo& g = a.g;
-  const int chunks = a.qc.chunks, ng = a.qc.groups;
+  const int chunks = a.qc.chunks;
   Seq seq;
   const Part part = find_part<NTHREADS, WARPS>(g, c, a.cu, a.slots, a.B, a.T, reinterpret_cast<int*>(smem), plan, seq);
   Walk walk(part, seq);
@@ -100,12 +122,24 @@ __global__ void __launch_bounds__(NTHREADS, QRowsCfg<E, BITS, D, NTR>::CTAS_PER_
   if (lane == 0) ends_sh.item[warp] = make_int4(walk.p.b, walk.p.tile, walk.p.head, 2);
   uint8_t* const mine = smem + warp * C::WARP_BYTES;
   const uint32_t sq = ptx::smem_u32(mine);
-  const uint32_t ring = sq + C::Q_BYTES;
+  // params of key 16 kt + 8 e + oct
+  auto params = [&](const uint8_t* slot, int kt, int e, uint32_t (&p)[NG]) {
+    const uint8_t* const at = slot + C::CODES + (kt * 16 + e * 8 + oct) * NG * 4;
+    if constexpr (NG == 2) {
+      const uint2 v = *reinterpret_cast<const uint2*>(at);
+      p[0] = v.x;
+      p[1] = v.y;
+    } else {
+      p[0] = *reinterpret_cast<const uint32_t*>(at);
+    }
+  };
   const long long v_minus_k = a.qc.V - a.qc.K;
   // V: lanes of the upper four octs read the odd key of a pair first (their banks are those that the
   // lower ones' even keys leave free), and put the halves together the other way round
   const int odd = oct >> 2;
-  const uint32_t sel_lo = odd ? 0x1054u : 0x5410u, sel_hi = odd ? 0x3276u : 0x7632u;
+  const int v_at = odd * 128 + (2 * quad + odd) * 16 + (oct & 3) * 4, v_other = odd ? -16 : 16;
+  const uint32_t sel_lo = BITS == 4 ? (odd ? 0x1054u : 0x5410u) : odd ? 0x1504u : 0x5140u;
+  const uint32_t sel_hi = BITS == 4 ? (odd ? 0x3276u : 0x7632u) : odd ? 0x3726u : 0x7362u;
   Seg seg = {};
   Finish fin;
   bool held = false;  // the worker's only item, not done whole: its result waits for the others'
@@ -114,11 +148,12 @@ __global__ void __launch_bounds__(NTHREADS, QRowsCfg<E, BITS, D, NTR>::CTAS_PER_
     const Seq& s = seg.s;
     const Tile& x = seg.x;
 
-    // ---- pages of the next 32 octets of keys, an octet per lane, and of the 32 after those:
-    // look-ups are never waited for in the loop
+    // ---- where the next 32 octets of keys lie, an octet per lane, and the pages of the 32 after
+    // those: look-ups are never waited for in the loop
     const int first = seg.k0 * GROUP;
     const int n = max(0, min(seg.k0 + seg.n, (x.hi + GROUP - 1) / GROUP) - seg.k0);  // steps
     const int* const row = c.table + (long long)s.slot * c.table_stride;
+    const uint8_t* const head = a.qc.K + seg.head * a.qc.head;
     auto lookup = [&](int octet) {
       const int j = first + octet * 8;
       if (octet >= n * (GROUP / 8) || j >= x.hi || j + 8 <= x.lo) return -1;  // no row sees it
@@ -127,128 +162,147 @@ __global__ void __launch_bounds__(NTHREADS, QRowsCfg<E, BITS, D, NTR>::CTAS_PER_
       raise(c.status, FAKV_BAD_PAGE);
       return -1;
     };
-    int page = -1, page_next = lookup(lane);
+    int page_next = lookup(lane);
+    unsigned there = 0;             // which of the 32 octets have a page
+    const uint8_t* block = a.qc.K;  // the lane's octet's
 
-    // ---- copies of half-step j: K (j even) or V of step j / 2, octet by octet, each in a page
-    const uint8_t* base[GROUP / 8];  // codes of the step's octets (null: zeros)
-    const uint8_t* base_p = nullptr; // the lane's piece of the params
-    uint32_t fill = ring;
-    auto load = [&](int j) {
-      if (j < 2 * n) {
-        const bool is_v = j & 1;
-        const long long v = is_v ? v_minus_k : 0;
-        if (!is_v) {
-          const int octet0 = (j >> 1) * (GROUP / 8);
-          if ((octet0 & 31) == 0) {
-            page = page_next;
-            page_next = lookup(octet0 + 32 + lane);
-          }
+    // ---- copies of step i's K, then its V, octet by octet, each in a page (zeros for an octet that has
+    // none); `at`: the step's place in the ring
+    const uint8_t* src[GROUP / 8];   // the lane's piece of the codes of the step's octets
+    const uint8_t* src_p = nullptr;  // and of the params
+    unsigned have = 0;               // of the step's octets
+    int piece[(CH + 3) / 4];         // bytes of the lane's pieces (0: past the last chunk)
 #pragma unroll
-          for (int k = 0; k < GROUP / 8; ++k) {
-            const int t = (first + (octet0 + k) * 8) & (c.page_size - 1);
-            const int p = __shfl_sync(0xffffffffu, page, (octet0 + k) & 31);
-            base[k] = p < 0 ? nullptr : a.qc.K + seg.head * a.qc.head + p * a.qc.page + t * chunks * 16;
-          }
-          const int k = lane / (2 * ng);  // (an octet's params are 2 ng pieces)
-          const int t = (first + (octet0 + k) * 8) & (c.page_size - 1);
-          const int p = __shfl_sync(0xffffffffu, page, (octet0 + min(k, GROUP / 8 - 1)) & 31);
-          base_p = p < 0 ? nullptr
-                         : a.qc.K + seg.head * a.qc.head + p * a.qc.page + a.qc.params + t * ng * 4 + (lane - k * 2 * ng) * 16;
+    for (int z = 0; z < (CH + 3) / 4; ++z) piece[z] = z * 32 + lane < chunks * 8 ? 16 : 0;
+    auto copy = [&](uint32_t at) {
+#pragma unroll
+      for (int k = 0; k < GROUP / 8; ++k)
+#pragma unroll
+        for (int z = 0; z < (CH + 3) / 4; ++z)
+          cp16z_if(CH % 4 == 0 || lane < CH * 8, at + (k * CH * 8 + z * 32 + lane) * 16, src[k] + z * 512,
+                   have >> k & 1 ? piece[z] : 0);
+      cp16z_if(lane < GROUP / 8 * 2 * NG, at + C::CODES + lane * 16, src_p, have >> (lane / (2 * NG)) & 1 ? 16 : 0);
+    };
+    auto load_k = [&](int i, uint32_t at) {
+      if (i < n) {
+        const int octet0 = i * (GROUP / 8);
+        if ((octet0 & 31) == 0) {
+          there = __ballot_sync(0xffffffffu, page_next >= 0);
+          block = page_next < 0 ? a.qc.K : head + page_next * a.qc.page;
+          page_next = lookup(octet0 + 32 + lane);
         }
+        have = there >> (octet0 & 31);
+        auto block_of = [&](int k) {
+          return reinterpret_cast<const uint8_t*>(
+              __shfl_sync(0xffffffffu, reinterpret_cast<unsigned long long>(block), (octet0 + k) & 31));
+        };
+        auto token_of = [&](int k) { return (first + (octet0 + k) * 8) & (c.page_size - 1); };
 #pragma unroll
-        for (int k = 0; k < GROUP / 8; ++k)
+        for (int k = 0; k < GROUP / 8; ++k) src[k] = block_of(k) + (token_of(k) * chunks + lane) * 16;
+        const int k = lane / (2 * NG);  // (an octet's params are 2 NG pieces)
+        src_p = block_of(k) + (a.qc.params + token_of(k) * NG * 4 + (lane - k * 2 * NG) * 16);
+        copy(at);
+      }
+      cp_commit();
+    };
+    auto load_v = [&](int i, uint32_t at) {
+      if (i < n) {
 #pragma unroll
-          for (int z = 0; z < (CH + 3) / 4; ++z) {
-            const int piece = z * 32 + lane;
-            if (piece < chunks * 8)
-              cp16(fill + k * CH * 128 + piece * 16, base[k] ? base[k] + v + piece * 16 : a.qc.K, base[k] != nullptr);
-          }
-        if (lane < GROUP / 8 * 2 * ng) cp16(fill + C::CODES + lane * 16, base_p ? base_p + v : a.qc.K, base_p != nullptr);
-        fill = fill + C::SLOT == ring + NS * C::SLOT ? ring : fill + C::SLOT;
+        for (int k = 0; k < GROUP / 8; ++k) src[k] += v_minus_k;
+        src_p += v_minus_k;
+        copy(at + C::SLOT);
       }
       cp_commit();
     };
 
-    // ---- q: fragments of its rows (zeros behind the item's rows and the tensor's columns), and of
-    // rows 8 nt + 2 quad + e the sums over each group: of q, and (not centred) of q times its codes' constants
+    // ---- q: fragments of its rows (zeros behind the item's rows and the tensor's columns), each row
+    // times a power of two; of rows 8 nt + 2 quad + e the sums over each group: of q, and (not centred) of
+    // q times its codes' constants; and what makes logits (log2) of their scores
     uint4 qr[C::Q_REGS ? KS / 2 : 1];
-    float qs[NTR][NG][2], qb[NTR][NG][2];
+    float2 qs[NTR][NG], qb[NTR][NG], ql[NTR];
 #pragma unroll
     for (int nt = 0; nt < NTR; ++nt) {
       const int r = nt * 8 + oct;
       const int rho = x.rho0 + min(r, x.rows - 1), token = g.rep.of(rho);
-      const E* const src = static_cast<const E*>(a.q) + (s.row0 + token) * a.q_token +
-                           (seg.head * g.rep.d + rho - token * g.rep.d) * a.q_head;
-      float sum[NG], bias[NG];
+      const E* const from = static_cast<const E*>(a.q) + (s.row0 + token) * a.q_token +
+                            (seg.head * g.rep.d + rho - token * g.rep.d) * a.q_head;
+      float y[KS / 2][8];
+      float top = 0.f;
 #pragma unroll
-      for (int i = 0; i < NG; ++i) sum[i] = bias[i] = 0.f;
-#pragma unroll
-      for (int i = 0; i < KS / 2; ++i) {  // two k16 steps: 4 bits: 8 columns of block i; 8 bits: 4 of chunks 2 i and 2 i + 1
-        float y[8];
-#pragma unroll
-        for (int e = 0; e < 8; ++e) y[e] = 0.f;
+      for (int i = 0; i < KS / 2; ++i)  // two k16 steps: 4 bits: 8 columns of block i; 8 bits: 4 of chunks 2 i and 2 i + 1
 #pragma unroll
         for (int e = 0; e < 2; ++e) {  // four columns each
           const int col = BITS == 4 ? i * 32 + quad * 8 + e * 4 : (2 * i + e) * 16 + quad * 4;
+          float* const to = &y[i][4 * e];
+          to[0] = to[1] = to[2] = to[3] = 0.f;
           if (r < x.rows && col < c.D) {
             if constexpr (C::F32) {
-              const float4 v = *reinterpret_cast<const float4*>(src + col);
-              y[4 * e] = v.x; y[4 * e + 1] = v.y; y[4 * e + 2] = v.z; y[4 * e + 3] = v.w;
+              const float4 v = *reinterpret_cast<const float4*>(from + col);
+              to[0] = v.x; to[1] = v.y; to[2] = v.z; to[3] = v.w;
             } else {
-              const uint2 v = *reinterpret_cast<const uint2*>(src + col);
-              y[4 * e] = __uint_as_float(v.x << 16); y[4 * e + 1] = __uint_as_float(v.x & 0xffff0000u);
-              y[4 * e + 2] = __uint_as_float(v.y << 16); y[4 * e + 3] = __uint_as_float(v.y & 0xffff0000u);
+              const uint2 v = *reinterpret_cast<const uint2*>(from + col);
+              to[0] = __uint_as_float(v.x << 16); to[1] = __uint_as_float(v.x & 0xffff0000u);
+              to[2] = __uint_as_float(v.y << 16); to[3] = __uint_as_float(v.y & 0xffff0000u);
             }
           }
+#pragma unroll
+          for (int k = 0; k < 4; ++k) top = fmaxf(top, fabsf(to[k]));
+        }
+      top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
+      top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
+      const int e = min(max(exponent(top), -100), 127);
+      const float down = pow2(14 - e), up = a.sl2 * pow2(e - 14);
+      // (infinity in a row makes all that it sees NaN, whatever the codes)
+      float sum[NG], bias[NG];
+#pragma unroll
+      for (int i = 0; i < NG; ++i) {
+        sum[i] = top < INFINITY ? 0.f : __int_as_float(0x7fffffff);
+        bias[i] = 0.f;
+      }
+#pragma unroll
+      for (int i = 0; i < KS / 2; ++i) {
+        // of the code pairs: 4 bits (0, 4), (1, 5), (2, 6), (3, 7); 8 bits (0, 1), (2, 3) of each chunk
+        uint32_t f[2][4];
+#pragma unroll
+        for (int z = 0; z < 4; ++z) {
+          const int c0 = BITS == 4 ? z : 2 * z, c1 = BITS == 4 ? z + 4 : 2 * z + 1;
+          const float by = down / q_factor<BITS>(z);
+          float2 v = make_float2(y[i][c0] * by, y[i][c1] * by);
+          sum[NG > 1 ? i / 2 : 0] += (v.x + v.y) * q_factor<BITS>(z);
+          bias[NG > 1 ? i / 2 : 0] -= (v.x + v.y) * 1024.f;
+          f[0][z] = half2_of(v.x, v.y, &v);
+          f[1][z] = half2_of(v.x, v.y);
         }
 #pragma unroll
-        for (int e = 0; e < 8; ++e) {
-          sum[i / 2] += y[e];
-          // 4 bits: column e is nibble e, of pair e % 4; 8 bits: byte e % 4's nibbles, of pairs 2 (e % 2) and + 1
-          bias[i / 2] += y[e] * (BITS == 4 ? q_bias(e & 3) : 256.f + q_bias(2 * (e & 1)));
-        }
-        // pairs: 4 bits (0, 4), (1, 5), (2, 6), (3, 7); 8 bits (0, 2), (1, 3) of each chunk
-        constexpr int A0[4] = {0, 1, BITS == 4 ? 2 : 4, BITS == 4 ? 3 : 5}, GAP = BITS == 4 ? 4 : 2;
-        if constexpr (C::Q_REGS) {
-          qr[i] = make_uint4(bf2(y[A0[0]], y[A0[0] + GAP]), bf2(y[A0[1]], y[A0[1] + GAP]), bf2(y[A0[2]], y[A0[2] + GAP]),
-                             bf2(y[A0[3]], y[A0[3] + GAP]));
-        } else {
-          float t[8][3];
-#pragma unroll
-          for (int e = 0; e < 8; ++e) {
-            if constexpr (C::F32) split3(y[e], t[e]);
-            else t[e][0] = y[e];
-          }
-#pragma unroll
-          for (int m = 0; m < TERMS; ++m)
-            ptx::st_shared_v4(sq + ((nt * TERMS + m) * (KS / 2) + i) * 512 + lane * 16, bf2(t[A0[0]][m], t[A0[0] + GAP][m]),
-                              bf2(t[A0[1]][m], t[A0[1] + GAP][m]), bf2(t[A0[2]][m], t[A0[2] + GAP][m]),
-                              bf2(t[A0[3]][m], t[A0[3] + GAP][m]));
+        for (int t = 0; t < TERMS; ++t) {
+          if constexpr (C::Q_REGS) qr[i] = make_uint4(f[0][0], f[0][1], f[0][2], f[0][3]);
+          else ptx::st_shared_v4(sq + ((nt * TERMS + t) * (KS / 2) + i) * 512 + lane * 16, f[t][0], f[t][1], f[t][2], f[t][3]);
         }
       }
+      // (a row's own lanes' value, to the lanes that have the row's scores)
+      auto of_row = [&](float v) { return make_float2(__shfl_sync(0xffffffffu, v, 8 * quad), __shfl_sync(0xffffffffu, v, 8 * quad + 4)); };
 #pragma unroll
       for (int i = 0; i < NG; ++i) {
         sum[i] += __shfl_xor_sync(0xffffffffu, sum[i], 1);
         sum[i] += __shfl_xor_sync(0xffffffffu, sum[i], 2);
         bias[i] += __shfl_xor_sync(0xffffffffu, bias[i], 1);
         bias[i] += __shfl_xor_sync(0xffffffffu, bias[i], 2);
-#pragma unroll
-        for (int e = 0; e < 2; ++e) {
-          qs[nt][i][e] = __shfl_sync(0xffffffffu, sum[i], (2 * quad + e) * 4);
-          qb[nt][i][e] = __shfl_sync(0xffffffffu, bias[i], (2 * quad + e) * 4);
-        }
+        qs[nt][i] = of_row(sum[i]);
+        qb[nt][i] = of_row(bias[i]);
       }
+      ql[nt] = of_row(up);
     }
     __syncwarp();
 
     // rows 8 nt + 2 quad + e; o: columns (h's) base + j, base + j + J
-    float m[NTR][2], l[NTR][2], o[WH][J][NTR][4], oz[NTR][NG][2];
+    float o[WH][J][NTR][4];
+    float2 m[NTR], l[NTR], oz[NTR][NG];
 #pragma unroll
     for (int nt = 0; nt < NTR; ++nt) {
-      m[nt][0] = m[nt][1] = -FLT_MAX;
-      l[nt][0] = l[nt][1] = 0.f;
+      m[nt] = make_float2(-FLT_MAX, -FLT_MAX);
+      l[nt] = make_float2(0.f, 0.f);
 #pragma unroll
-      for (int i = 0; i < NG; ++i) oz[nt][i][0] = oz[nt][i][1] = 0.f;
+      for (int i = 0; i < NG; ++i) oz[nt][i] = make_float2(0.f, 0.f);
 #pragma unroll
       for (int h = 0; h < WH; ++h)
 #pragma unroll
@@ -262,231 +316,260 @@ __global__ void __launch_bounds__(NTHREADS, QRowsCfg<E, BITS, D, NTR>::CTAS_PER_
       in_lo = g.window > 0 ? pb - g.window + 1 : 0;
     }
 
-    // Half-steps K_0, V_0, K_1, ...: a slot is filled again as soon as it is read, NS half-steps
-    // ahead. The first NS rounds only load.
-    uint32_t use = ring;
-    float sc[KT][NTR][4];  // scores, then probabilities: keys 16 kt + oct (+ 8), rows 8 nt + 2 quad + e
+    // Steps of 32 keys. K's and V's places are filled again as soon as each is read, NP steps ahead; the
+    // first NP rounds only load.
+    uint32_t use = C::Q_BYTES;  // of the step, in the warp's shared memory
+    float cap = 0.f, lift = 1.f;  // V's scales so far are at most cap; times lift they are below 2^7
 #pragma unroll 1
-    for (int j = -NS; j < 2 * n; ++j) {
-      if (j >= 0) {
-        cp_wait<NS - 1>();
+    for (int i = -NP; i < n; ++i) {
+      const int j0 = first + i * GROUP;
+      const bool edge = j0 < in_lo || j0 + GROUP - 1 > in_hi;
+      float2 sc[KT][NTR][2];  // scores, then probabilities: keys 16 kt + 8 z + oct, rows 8 nt + 2 quad, + 1
+      if (i >= 0) {
+        cp_wait<2 * NP - 1>();
         __syncwarp();
-        const int j0 = first + (j >> 1) * GROUP;
-        const bool edge = j0 < in_lo || j0 + GROUP - 1 > in_hi;
-        // s and z' of key 16 kt + 8 e + oct, group i
-        auto params = [&](int kt, int e, float (&ps)[NG], float (&pz)[NG], bool centred) {
-          const uint32_t at = use + C::CODES + (kt * 16 + e * 8 + oct) * ng * 4;
+        const uint8_t* const slot = mine + use;
+        // -------- scores
+        // (chunks that the cache does not have: whatever lies in the slot, finite codes, times q's zeros)
+        float acc[NG][KT][NTR][4];
 #pragma unroll
-          for (int i = 0; i < NG; ++i) {
-            const uint32_t p = lds32(at + (i && ng > 1 ? 4 : 0));
-            ps[i] = q_scale(p);
-            pz[i] = centred ? fmaf(ps[i], CENTRE, q_offset(p)) : q_offset(p);
-          }
-        };
-        if ((j & 1) == 0) {
-          // -------- scores of step j / 2
-          float acc[NG][KT][NTR][4];
+        for (int k = 0; k < NG; ++k)
 #pragma unroll
-          for (int i = 0; i < NG; ++i)
+          for (int kt = 0; kt < KT; ++kt)
 #pragma unroll
-            for (int kt = 0; kt < KT; ++kt)
+            for (int nt = 0; nt < NTR; ++nt)
 #pragma unroll
-              for (int nt = 0; nt < NTR; ++nt)
+              for (int e = 0; e < 4; ++e) acc[k][kt][nt][e] = CENTRED ? 0.f : e & 1 ? qb[nt][k].y : qb[nt][k].x;
 #pragma unroll
-                for (int e = 0; e < 4; ++e) acc[i][kt][nt][e] = CENTRED ? 0.f : -qb[nt][i][e & 1];
+        for (int w = 0; w < CH; ++w) {
+          const int k = NG == 1 ? 0 : BITS == 4 ? w / 2 : w / 4;  // the chunk's group
 #pragma unroll
-          for (int w = 0; w < CH; ++w) {
-            if (w >= chunks) break;
-            uint32_t word[KT][2];
+          for (int kt = 0; kt < KT; ++kt) {
+            uint32_t word[2];
 #pragma unroll
-            for (int kt = 0; kt < KT; ++kt)
-#pragma unroll
-              for (int e = 0; e < 2; ++e) word[kt][e] = lds32(use + ((kt * 2 + e) * CH + w) * 128 + lane * 4);
-            constexpr int PER = BITS == 4 ? 2 : 1;  // k16 steps of q for a chunk
+            for (int e = 0; e < 2; ++e)
+              word[e] = *reinterpret_cast<const uint32_t*>(slot + ((kt * 2 + e) * CH + w) * 128 + lane * 4);
+            auto product = [&](auto pair, uint32_t b0, uint32_t b1, int nt) {  // code pairs `pair` and + 1
+              constexpr int P = decltype(pair)::value;
+              uint32_t f[4] = {q_raise<BITS, P>(word[0]), q_raise<BITS, P>(word[1]), q_raise<BITS, P + 1>(word[0]),
+                               q_raise<BITS, P + 1>(word[1])};
+              if constexpr (CENTRED) {
+                f[0] = q_centred<BITS, P>(f[0]); f[1] = q_centred<BITS, P>(f[1]);
+                f[2] = q_centred<BITS, P + 1>(f[2]); f[3] = q_centred<BITS, P + 1>(f[3]);
+              }
+              mma_f16(acc[k][kt][nt], f, b0, b1);
+            };
 #pragma unroll
             for (int nt = 0; nt < NTR; ++nt)
 #pragma unroll
               for (int t = TERMS - 1; t >= 0; --t) {
-                const int step = w * PER;
+                const int step = BITS == 4 ? w : w / 2;
                 uint4 v;
-                if constexpr (C::Q_REGS) v = qr[step / 2];
-                else {
-                  const float4 f = ptx::ld_shared_v4(sq + ((nt * TERMS + t) * (KS / 2) + step / 2) * 512 + lane * 16);
-                  v = make_uint4(__float_as_uint(f.x), __float_as_uint(f.y), __float_as_uint(f.z), __float_as_uint(f.w));
-                }
-                const uint32_t b0 = step & 1 ? v.z : v.x, b1 = step & 1 ? v.w : v.y;
-#pragma unroll
-                for (int kt = 0; kt < KT; ++kt) {
-                  const uint32_t lo = word[kt][0], hi = word[kt][1];
-                  float(&d)[4] = acc[BITS == 4 ? w / 2 : w / 4][kt][nt];
-                  if constexpr (BITS == 4) {
-                    uint32_t f0[4], f1[4];
-                    if constexpr (CENTRED) {
-                      f0[0] = q_centred4<0>(lo); f0[1] = q_centred4<0>(hi); f0[2] = q_centred4<1>(lo); f0[3] = q_centred4<1>(hi);
-                      f1[0] = q_centred4<2>(lo); f1[1] = q_centred4<2>(hi); f1[2] = q_centred4<3>(lo); f1[3] = q_centred4<3>(hi);
-                    } else {
-                      f0[0] = q_pair<0>(lo); f0[1] = q_pair<0>(hi); f0[2] = q_pair<1>(lo); f0[3] = q_pair<1>(hi);
-                      f1[0] = q_pair<2>(lo); f1[1] = q_pair<2>(hi); f1[2] = q_pair<3>(lo); f1[3] = q_pair<3>(hi);
-                    }
-                    mma_bf16(d, f0, v.x, v.y);
-                    mma_bf16(d, f1, v.z, v.w);
-                  } else if constexpr (CENTRED) {
-                    const uint32_t f[4] = {q_centred8<0>(lo), q_centred8<0>(hi), q_centred8<1>(lo), q_centred8<1>(hi)};
-                    mma_bf16(d, f, b0, b1);
-                  } else {
-                    const uint32_t f0[4] = {q_pair<0>(lo), q_pair<0>(hi), q_pair<2>(lo), q_pair<2>(hi)};
-                    const uint32_t f1[4] = {q_pair16<1>(lo), q_pair16<1>(hi), q_pair16<3>(lo), q_pair16<3>(hi)};
-                    mma_bf16(d, f0, b0, b1);
-                    mma_bf16(d, f1, b0, b1);
-                  }
+                if constexpr (C::Q_REGS) v = qr[step];
+                else v = *reinterpret_cast<const uint4*>(mine + ((nt * TERMS + t) * (KS / 2) + step) * 512 + lane * 16);
+                if constexpr (BITS == 4) {
+                  product(std::integral_constant<int, 0>(), v.x, v.y, nt);
+                  product(std::integral_constant<int, 2>(), v.z, v.w, nt);
+                } else {
+                  product(std::integral_constant<int, 0>(), w & 1 ? v.z : v.x, w & 1 ? v.w : v.y, nt);
                 }
               }
           }
+        }
 #pragma unroll
-          for (int kt = 0; kt < KT; ++kt)
+        for (int kt = 0; kt < KT; ++kt)
 #pragma unroll
-            for (int z = 0; z < 2; ++z) {
-              float ps[NG], pz[NG];
-              params(kt, z, ps, pz, CENTRED);
+          for (int z = 0; z < 2; ++z) {
+            uint32_t p[NG];
+            params(slot, kt, z, p);
 #pragma unroll
-              for (int nt = 0; nt < NTR; ++nt)
+            for (int nt = 0; nt < NTR; ++nt) {
+              float2 v = make_float2(0.f, 0.f);
 #pragma unroll
-                for (int e = 0; e < 2; ++e) {
-                  float v = pz[0] * qs[nt][0][e];
-#pragma unroll
-                  for (int i = 0; i < NG; ++i) {
-                    if (i > 0) v = fmaf(pz[i], qs[nt][i][e], v);
-                    v = fmaf(ps[i], acc[i][kt][nt][2 * z + e], v);
-                  }
-                  sc[kt][nt][2 * z + e] = v;
-                }
+              for (int k = 0; k < NG; ++k) {
+                const float ps = q_scale(p[k]), pz = CENTRED ? fmaf(ps, CENTRE, q_offset(p[k])) : q_offset(p[k]);
+                v.x = k == 0 ? pz * qs[nt][k].x : fmaf(pz, qs[nt][k].x, v.x);
+                v.y = k == 0 ? pz * qs[nt][k].y : fmaf(pz, qs[nt][k].y, v.y);
+                v.x = fmaf(ps, acc[k][kt][nt][2 * z], v.x);
+                v.y = fmaf(ps, acc[k][kt][nt][2 * z + 1], v.y);
+              }
+              sc[kt][nt][z] = v;
             }
-          if (edge) {
-#pragma unroll
-            for (int nt = 0; nt < NTR; ++nt)
-#pragma unroll
-              for (int e = 0; e < 2; ++e) {
-                // row 8 nt + 2 quad + e sees keys [lo, hi]
-                const int p = s.len - s.n + g.rep.of(x.rho0 + min(nt * 8 + quad * 2 + e, x.rows - 1));
-                const int hi = g.causal ? min(p, s.len - 1) : s.len - 1;
-                const int lo = g.window > 0 ? p - g.window + 1 : 0;
-#pragma unroll
-                for (int kt = 0; kt < KT; ++kt)
-#pragma unroll
-                  for (int z = 0; z < 2; ++z) {
-                    const int key = j0 + kt * 16 + z * 8 + oct;
-                    if (key < lo || key > hi) sc[kt][nt][2 * z + e] = -INFINITY;
-                  }
-              }
           }
-          // -------- probabilities; m where it has to move
-          float mx[NTR][2];
-          bool grow = false;
+        if (edge) {
 #pragma unroll
           for (int nt = 0; nt < NTR; ++nt)
 #pragma unroll
             for (int e = 0; e < 2; ++e) {
-              float v = fmaxf(sc[0][nt][e], sc[0][nt][e + 2]);
+              // row 8 nt + 2 quad + e sees keys [lo, hi]
+              const int p = s.len - s.n + g.rep.of(x.rho0 + min(nt * 8 + quad * 2 + e, x.rows - 1));
+              const int hi = g.causal ? min(p, s.len - 1) : s.len - 1;
+              const int lo = g.window > 0 ? p - g.window + 1 : 0;
 #pragma unroll
-              for (int kt = 1; kt < KT; ++kt) v = ptx::max3(v, sc[kt][nt][e], sc[kt][nt][e + 2]);
-              mx[nt][e] = v * a.sl2;
-              grow |= mx[nt][e] > m[nt][e] + RESCALE_THRESHOLD;
+              for (int kt = 0; kt < KT; ++kt)
+#pragma unroll
+                for (int z = 0; z < 2; ++z) {
+                  const int key = j0 + kt * 16 + z * 8 + oct;
+                  if (key < lo || key > hi) (e ? sc[kt][nt][z].y : sc[kt][nt][z].x) = -INFINITY;
+                }
             }
-          if (__any_sync(0xffffffffu, grow)) {
+        }
+        // -------- probabilities; m where it has to move
+        float2 mx[NTR];
+        bool grow = false;
 #pragma unroll
-            for (int nt = 0; nt < NTR; ++nt)
+        for (int nt = 0; nt < NTR; ++nt) {
+          mx[nt] = make_float2(fmaxf(sc[0][nt][0].x, sc[0][nt][1].x), fmaxf(sc[0][nt][0].y, sc[0][nt][1].y));
 #pragma unroll
-              for (int e = 0; e < 2; ++e) {
-                float v = fmaxf(mx[nt][e], __shfl_xor_sync(0xffffffffu, mx[nt][e], 4));
-                v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 8));
-                v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 16));
-                const float mn = fmaxf(m[nt][e], v);
-                const float f = ptx::ex2(m[nt][e] - mn);
-                m[nt][e] = mn;
-                l[nt][e] *= f;
+          for (int kt = 1; kt < KT; ++kt)
+            mx[nt] = make_float2(ptx::max3(mx[nt].x, sc[kt][nt][0].x, sc[kt][nt][1].x), ptx::max3(mx[nt].y, sc[kt][nt][0].y, sc[kt][nt][1].y));
+          mx[nt] = make_float2(mx[nt].x * ql[nt].x, mx[nt].y * ql[nt].y);
+          grow |= mx[nt].x > m[nt].x + RESCALE_THRESHOLD || mx[nt].y > m[nt].y + RESCALE_THRESHOLD;
+        }
+        if (__any_sync(0xffffffffu, grow)) {
 #pragma unroll
-                for (int i = 0; i < NG; ++i) oz[nt][i][e] *= f;
+          for (int nt = 0; nt < NTR; ++nt) {
+            float2 f;
 #pragma unroll
-                for (int h = 0; h < WH; ++h)
+            for (int e = 0; e < 2; ++e) {
+              float v = e ? mx[nt].y : mx[nt].x;
+              v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 4));
+              v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 8));
+              v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 16));
+              float& was = e ? m[nt].y : m[nt].x;
+              const float mn = fmaxf(was, v);
+              (e ? f.y : f.x) = ptx::ex2(was - mn);
+              was = mn;
+            }
+            l[nt] = ptx::mul2(l[nt], f);
 #pragma unroll
-                  for (int t = 0; t < J; ++t) {
-                    o[h][t][nt][e] *= f;
-                    o[h][t][nt][e + 2] *= f;
-                  }
-              }
+            for (int k = 0; k < NG; ++k) oz[nt][k] = ptx::mul2(oz[nt][k], f);
+#pragma unroll
+            for (int h = 0; h < WH; ++h)
+#pragma unroll
+              for (int t = 0; t < J; ++t)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) o[h][t][nt][e] *= e & 1 ? f.y : f.x;
           }
+        }
 #pragma unroll
-          for (int kt = 0; kt < KT; ++kt)
+        for (int kt = 0; kt < KT; ++kt)
 #pragma unroll
-            for (int nt = 0; nt < NTR; ++nt)
-#pragma unroll
-              for (int e = 0; e < 4; ++e) {
-                const float p = ptx::ex2(fmaf(sc[kt][nt][e], a.sl2, -m[nt][e & 1]));
-                sc[kt][nt][e] = p;
-                l[nt][e & 1] += p;
-              }
-        } else {
-          // -------- O^T += V^T (s P)^T, and the offsets' sums
-#pragma unroll
-          for (int kt = 0; kt < KT; ++kt) {
-            uint32_t ph[NG][NTR][2], pl[NG][NTR][2];  // keys low, high
+          for (int nt = 0; nt < NTR; ++nt)
 #pragma unroll
             for (int z = 0; z < 2; ++z) {
-              float ps[NG], pz[NG];
-              params(kt, z, ps, pz, true);
+              const float2 v = ptx::fma2(sc[kt][nt][z], ql[nt], make_float2(-m[nt].x, -m[nt].y));
+              sc[kt][nt][z] = make_float2(ptx::ex2(v.x), ptx::ex2(v.y));
+              l[nt] = ptx::add2(l[nt], sc[kt][nt][z]);
+            }
+        __syncwarp();  // K's codes are read
+      }
+      load_k(i + NP, sq + use);
+      if (i >= 0) {
+        cp_wait<2 * NP - 1>();
+        __syncwarp();
+        const uint8_t* const slot = mine + use + C::SLOT;
+        // -------- O^T += V^T (s P)^T, and the offsets' sums
+        uint32_t pv[KT][2][NG];
+        float most = 0.f;
+#pragma unroll
+        for (int kt = 0; kt < KT; ++kt)
+#pragma unroll
+          for (int z = 0; z < 2; ++z) {
+            params(slot, kt, z, pv[kt][z]);
+            if (edge) {  // (what no row sees need be no token)
+              const int key = j0 + kt * 16 + z * 8 + oct;
+#pragma unroll
+              for (int k = 0; k < NG; ++k) pv[kt][z][k] = key >= x.lo && key < x.hi ? pv[kt][z][k] : 0u;
+            }
+#pragma unroll
+            for (int k = 0; k < NG; ++k) most = fmaxf(most, q_scale(pv[kt][z][k]));  // (NaN is passed over)
+          }
+        if (__any_sync(0xffffffffu, most > cap)) {
+          const int e = min(max(exponent(__uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(most)))), -100), 126);
+          cap = pow2(e + 1);  // (twice the largest may come before the next move)
+          const float f = pow2(5 - e) / lift;
+          lift = pow2(5 - e);
+#pragma unroll
+          for (int h = 0; h < WH; ++h)
+#pragma unroll
+            for (int t = 0; t < J; ++t)
 #pragma unroll
               for (int nt = 0; nt < NTR; ++nt)
 #pragma unroll
-                for (int i = 0; i < NG; ++i) {
-                  const float p0 = sc[kt][nt][2 * z], p1 = sc[kt][nt][2 * z + 1];
-                  float s0 = p0 * ps[i], s1 = p1 * ps[i], z0 = p0 * pz[i], z1 = p1 * pz[i];
-                  if (edge) {  // a key that a row does not see may be anything
-                    if (p0 == 0.f) s0 = z0 = 0.f;
-                    if (p1 == 0.f) s1 = z1 = 0.f;
-                  }
-                  oz[nt][i][0] += z0;
-                  oz[nt][i][1] += z1;
-                  const uint32_t hi = bf2(s0, s1);
-                  ph[i][nt][z] = transpose8(hi);
-                  pl[i][nt][z] = transpose8(bf2(s0 - __uint_as_float(hi << 16), s1 - __uint_as_float(hi & 0xffff0000u)));
-                }
-            }
+                for (int k = 0; k < 4; ++k) o[h][t][nt][k] *= f;
+        }
+        uint32_t pf[KT][NG][NTR][PT][2];  // terms of s P; keys low, high
+        auto weigh = [&](auto masked) {
 #pragma unroll
-            for (int h = 0; h < WH; ++h) {
-              if (2 * h >= chunks) break;
-              const int i = BITS == 4 ? h : h / 2;  // the words' group
-              uint32_t half[2][2];  // keys low, high: the words' low and high halves, of two keys
+          for (int kt = 0; kt < KT; ++kt)
 #pragma unroll
-              for (int z = 0; z < 2; ++z) {
-                // (an odd number of chunks: the upper octs read the last one again, for columns that do not exist)
-                const uint32_t at = use + ((kt * 2 + z) * CH + min(2 * h + odd, chunks - 1)) * 128 + quad * 32 + (oct & 3) * 4;
-                const uint32_t p = lds32(at + odd * 16), q = lds32(at + 16 - odd * 16);
-                half[z][0] = __byte_perm(p, q, sel_lo);
-                half[z][1] = __byte_perm(p, q, sel_hi);
-              }
-              auto tile = [&](auto jj) {
-                constexpr int t = decltype(jj)::value;
-                const uint32_t va[4] = {q_centred<BITS, t>(half[0][0]), q_centred<BITS, t>(half[0][1]),
-                                        q_centred<BITS, t>(half[1][0]), q_centred<BITS, t>(half[1][1])};
+            for (int z = 0; z < 2; ++z)
+#pragma unroll
+              for (int k = 0; k < NG; ++k) {
+                const float ps = q_scale(pv[kt][z][k]), pz = fmaf(ps, CENTRE, q_offset(pv[kt][z][k])), pl = ps * lift;
 #pragma unroll
                 for (int nt = 0; nt < NTR; ++nt) {
-                  mma_bf16(o[h][t][nt], va, pl[i < NG ? i : 0][nt][0], pl[i < NG ? i : 0][nt][1]);
-                  mma_bf16(o[h][t][nt], va, ph[i < NG ? i : 0][nt][0], ph[i < NG ? i : 0][nt][1]);
+                  const float2 p = sc[kt][nt][z];
+                  float2 sp;
+                  if constexpr (decltype(masked)::value) {  // a key that a row does not see may be anything
+                    sp = make_float2(p.x == 0.f ? 0.f : p.x * pl, p.y == 0.f ? 0.f : p.y * pl);
+                    oz[nt][k].x += p.x == 0.f ? 0.f : p.x * pz;
+                    oz[nt][k].y += p.y == 0.f ? 0.f : p.y * pz;
+                  } else {
+                    sp = make_float2(p.x * pl, p.y * pl);
+                    oz[nt][k].x = fmaf(p.x, pz, oz[nt][k].x);
+                    oz[nt][k].y = fmaf(p.y, pz, oz[nt][k].y);
+                  }
+#pragma unroll
+                  for (int t = 0; t < PT; ++t) pf[kt][k][nt][t][z] = transpose8(half2_of(sp.x, sp.y, &sp));
                 }
-              };
-              tile(std::integral_constant<int, 0>());
-              tile(std::integral_constant<int, 1>());
-              if constexpr (BITS == 4) {
-                tile(std::integral_constant<int, 2>());
-                tile(std::integral_constant<int, 3>());
               }
+        };
+        if (edge) weigh(std::true_type());
+        else weigh(std::false_type());
+#pragma unroll
+        for (int kt = 0; kt < KT; ++kt) {
+#pragma unroll
+          for (int h = 0; h < WH; ++h) {
+            const int k = NG == 1 ? 0 : BITS == 4 ? h : h / 2;  // the words' group
+            uint32_t half[2][2];  // of keys low, high: two keys' codes side by side, of the words' low halves and of their high ones
+#pragma unroll
+            for (int z = 0; z < 2; ++z) {
+              const uint8_t* const at = slot + v_at + ((kt * 2 + z) * CH + 2 * h) * 128;
+              const uint32_t p = *reinterpret_cast<const uint32_t*>(at), q = *reinterpret_cast<const uint32_t*>(at + v_other);
+              half[z][0] = __byte_perm(p, q, sel_lo);
+              half[z][1] = __byte_perm(p, q, sel_hi);
+            }
+            auto tile = [&](auto jj) {
+              constexpr int t = decltype(jj)::value;
+              const uint32_t va[4] = {q_centred<BITS, t>(q_raise<BITS, t>(half[0][0])), q_centred<BITS, t>(q_raise<BITS, t>(half[0][1])),
+                                      q_centred<BITS, t>(q_raise<BITS, t>(half[1][0])), q_centred<BITS, t>(q_raise<BITS, t>(half[1][1]))};
+#pragma unroll
+              for (int nt = 0; nt < NTR; ++nt) {
+                if constexpr (PT == 1) {
+                  mma_f16(o[h][t][nt], va, pf[kt][k][nt][0][0], pf[kt][k][nt][0][1]);
+                } else {  // a sum per 16 keys, added to O in fp32: O itself is not cut off at every product
+                  float add[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+                  for (int b = PT - 1; b >= 0; --b) mma_f16(add, va, pf[kt][k][nt][b][0], pf[kt][k][nt][b][1]);
+#pragma unroll
+                  for (int e = 0; e < 4; ++e) o[h][t][nt][e] += add[e];
+                }
+              }
+            };
+            tile(std::integral_constant<int, 0>());
+            tile(std::integral_constant<int, 1>());
+            if constexpr (BITS == 4) {
+              tile(std::integral_constant<int, 2>());
+              tile(std::integral_constant<int, 3>());
             }
           }
         }
-        __syncwarp();  // the slot is read
-        use = use + C::SLOT == ring + NS * C::SLOT ? ring : use + C::SLOT;
+        __syncwarp();  // V's codes are read
       }
-      load(j + NS);
+      load_v(i + NP, sq + use);
+      use = use + 2 * C::SLOT == C::Q_BYTES + NP * 2 * C::SLOT ? C::Q_BYTES : use + 2 * C::SLOT;
     }
     cp_wait<0>();
     __syncwarp();  // (every lane's copies have landed: the ring may be used for what comes next)
@@ -501,20 +584,20 @@ __global__ void __launch_bounds__(NTHREADS, QRowsCfg<E, BITS, D, NTR>::CTAS_PER_
           v += __shfl_xor_sync(0xffffffffu, v, 8);
           return v + __shfl_xor_sync(0xffffffffu, v, 16);
         };
-        const float v = over_keys(l[nt][e]);
+        const float v = over_keys(e ? l[nt].y : l[nt].x);
         float z[NG];
 #pragma unroll
-        for (int i = 0; i < NG; ++i) z[i] = over_keys(oz[nt][i][e]);
+        for (int i = 0; i < NG; ++i) z[i] = over_keys(e ? oz[nt][i].y : oz[nt][i].x);
         const int r = nt * 8 + quad * 2 + e;
-        if (oct == 0) ends_sh.ml[warp][r] = make_float2(m[nt][e], v);
+        if (oct == 0) ends_sh.ml[warp][r] = make_float2(e ? m[nt].y : m[nt].x, v);
         float* const to = reinterpret_cast<float*>(mine) + r * C::OS + oct * 2 * J;
 #pragma unroll
         for (int h = 0; h < WH; ++h)
 #pragma unroll
           for (int t = 0; t < J; ++t) {
-            const float zh = z[(BITS == 4 ? h : h / 2) % NG];
-            to[h * 16 * J + t] = o[h][t][nt][e] + zh;
-            to[h * 16 * J + t + J] = o[h][t][nt][e + 2] + zh;
+            const float zh = z[NG == 1 ? 0 : BITS == 4 ? h : h / 2], by = 1.f / (lift * q_factor<BITS>(t));
+            to[h * 16 * J + t] = fmaf(o[h][t][nt][e], by, zh);
+            to[h * 16 * J + t + J] = fmaf(o[h][t][nt][e + 2], by, zh);
           }
       }
     fin = {s.row0, x.rho0, x.rows, seg.head, walk.p.ender,
@@ -530,10 +613,10 @@ __global__ void __launch_bounds__(NTHREADS, QRowsCfg<E, BITS, D, NTR>::CTAS_PER_
   finish_held<C, D>(a, fin, held, walk.moved, smem, ends_sh);
 }
 
-template <typename E, int BITS, int D, int NTR>
+template <typename E, bool OUT_BF, int BITS, int D, int NG, int NTR>
 fa_status run(QRowsArgs& a, cudaStream_t s) {
-  using C = QRowsCfg<E, BITS, D, NTR>;
-  auto* kernel = qattend_rows_kernel<E, BITS, D, NTR>;
+  using C = QRowsCfg<E, OUT_BF, BITS, D, NG, NTR>;
+  auto* kernel = qattend_rows_kernel<E, OUT_BF, BITS, D, NG, NTR>;
   static std::atomic<uint64_t> done{0};
   if (!allow_smem(kernel, C::SMEM, done)) return failed();
   const int ctas = host::sm_count() * C::CTAS_PER_SM;
@@ -557,10 +640,15 @@ fa_status run(QRowsArgs& a, cudaStream_t s) {
   return st;
 }
 
-template <typename E, int BITS>
+template <typename E, bool OUT_BF, int BITS, int NTR>
+fa_status pick(QRowsArgs& a, cudaStream_t s) {
+  if (a.c.D <= 64) return run<E, OUT_BF, BITS, 64, 1, NTR>(a, s);
+  return a.qc.groups == 1 ? run<E, OUT_BF, BITS, 128, 1, NTR>(a, s) : run<E, OUT_BF, BITS, 128, 2, NTR>(a, s);
+}
+template <typename E, bool OUT_BF>
 fa_status pick(QRowsArgs& a, long long rows, cudaStream_t s) {
-  if (a.c.D <= 64) return rows <= 8 ? run<E, BITS, 64, 1>(a, s) : run<E, BITS, 64, 2>(a, s);
-  return rows <= 8 ? run<E, BITS, 128, 1>(a, s) : run<E, BITS, 128, 2>(a, s);
+  if (a.qc.bits == 4) return rows <= 8 ? pick<E, OUT_BF, 4, 1>(a, s) : pick<E, OUT_BF, 4, 2>(a, s);
+  return rows <= 8 ? pick<E, OUT_BF, 8, 1>(a, s) : pick<E, OUT_BF, 8, 2>(a, s);
 }
 
 }  // namespace
@@ -590,8 +678,8 @@ fa_status launch_qattend_rows(const void* q, void* O, float* LSE, const int* cu,
   a.out_bf16 = p.out_dtype == FA_BF16;
   // Items of 8 or 16 rows: what a sequence's rows fit on average
   const long long rows = ((long long)p.T * rep + p.B - 1) / p.B;
-  if (c.dtype == FA_BF16) return qc.bits == 4 ? pick<__nv_bfloat16, 4>(a, rows, s) : pick<__nv_bfloat16, 8>(a, rows, s);
-  return qc.bits == 4 ? pick<float, 4>(a, rows, s) : pick<float, 8>(a, rows, s);
+  if (c.dtype == FA_BF16) return a.out_bf16 ? pick<__nv_bfloat16, true>(a, rows, s) : pick<__nv_bfloat16, false>(a, rows, s);
+  return pick<float, false>(a, rows, s);
 }
 
 }  // namespace kv
