@@ -282,10 +282,10 @@ FA_API fa_status fa_bwd_dsmat(const void* Q, const void* K, const void* V, const
 FA_API fa_status fa_device_status(fa_stream_t stream) {
   if (cudaStreamSynchronize(reinterpret_cast<cudaStream_t>(stream)) != cudaSuccess)
     return FA_ERR_CUDA;
-  cudaError_t e1 = cudaSuccess, e2 = cudaSuccess, e3 = cudaSuccess;
+  cudaError_t e1 = cudaSuccess, e2 = cudaSuccess, e3 = cudaSuccess, e4 = cudaSuccess;
   const unsigned int v = read_and_clear_fwd_status(&e1) | read_and_clear_bwd_status(&e2) |
-                         kv::read_and_clear_kv_status(&e3);
-  if (e1 != cudaSuccess || e2 != cudaSuccess || e3 != cudaSuccess) return FA_ERR_CUDA;
+                         kv::read_and_clear_kv_status(&e3) | kv::read_and_clear_kvq_status(&e4);
+  if (e1 != cudaSuccess || e2 != cudaSuccess || e3 != cudaSuccess || e4 != cudaSuccess) return FA_ERR_CUDA;
   if (v & DEV_LAYOUT) return FA_ERR_LAYOUT;
   return (v & DEV_TIMEOUT) ? FA_ERR_TIMEOUT : FA_OK;
 }

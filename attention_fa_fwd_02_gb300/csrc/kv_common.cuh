@@ -146,6 +146,7 @@ fa_status launch_fork(const fakv_cache& c, const int* src, const int* dst, int n
 fa_status launch_free(const fakv_cache& c, const int* slots, const int* keep, int n, cudaStream_t s);
 fa_status launch_compact(const fakv_cache& c, cudaStream_t s);
 unsigned int read_and_clear_kv_status(cudaError_t* err);
+unsigned int read_and_clear_kvq_status(cudaError_t* err);
 
 }  // namespace kv
 }  // namespace fa

@@ -1,7 +1,9 @@
 // kv_qrows.cu -- attention over the cache in 4 or 8 bits for few rows per sequence (decoding), and for
 // fp32 queries: codes streamed once, made bf16 in registers, mma.sync.
 //
-// Workers, parts, copies and joins are those of kv_rows.cu. With s, z of a key's group g and codes
+// Workers, parts and joins are those of kv_rows.cu. A page of a head is one block of memory, its codes one
+// after another: the copy engine brings a step's 32 keys in a few copies (two a page), which the lanes issue
+// whose pages they are, and every wait for one has a limit. With s, z of a key's group g and codes
 // c = centre + x (centre 8 or 128), its K and V are s x + z', z' = z + centre s, so that
 //
 //   scores  S = sum_g s_g (sum_{d in g} q_d c_d) + z_g (sum_{d in g} q_d): codes are exact fp16
@@ -16,14 +18,17 @@
 // so nothing of the cache is rounded again. A code costs about an instruction (kv_quant.cuh):
 //   K  columns are what is summed over, in any order: a thread takes the 8 (4) columns of one
 //      32-bit word of its key, and q's fragments are laid out to match
-//   V  keys are summed over, two of each register: the codes of two keys' words are put side by side
-//      first (permutes), so that every pair is one column of two keys
+//   V  keys are summed over, two of each register: the cache holds the codes of two tokens side by side,
+//      so that every pair is one column of two keys
 #include <algorithm>
 #include "kv_quant.cuh"
 #include "kv_rows.cuh"
 
 namespace fa {
 namespace kv {
+
+static __device__ unsigned int g_kvq_status = 0;
+
 namespace {
 
 struct QRowsArgs {
@@ -38,7 +43,9 @@ struct QRowsArgs {
   long long q_token, q_head;
   Geo g;
   float sl2;  // scale * log2(e)
+  uint32_t raised;  // Q_RAISED
   int out_bf16;
+  int run_shift;  // log2 of the keys of a run: of a step, in one page, one after another in memory
   Partials part;
 };
 
@@ -65,7 +72,7 @@ struct QRowsCfg {
   static constexpr int SMEM = WARPS * WARP_BYTES;
   static_assert(NP >= 2 && WARP_BYTES % 128 == 0 && SLOT % 128 == 0 && Q_BYTES % 128 == 0, "the ring");
   static_assert(SMEM >= 4 * 16385, "the plan's scratch");
-  static constexpr int STATIC = (int)sizeof(PlanShared<NTHREADS, WARPS>) + WARPS * (R * 8 + 20);
+  static constexpr int STATIC = (int)sizeof(PlanShared<NTHREADS, WARPS>) + WARPS * (R * 8 + 20 + NP * 16) + 8;
   static_assert(CTAS_PER_SM * (SMEM + (STATIC + 1023) / 1024 * 1024 + 1024) <= 228 * 1024, "shared memory of the CTAs of an SM");
 };
 
@@ -83,14 +90,10 @@ __device__ __forceinline__ uint32_t half2_of(float a, float b, float2* rest = nu
   }
   return *reinterpret_cast<const uint32_t*>(&h);
 }
-__device__ __forceinline__ void cp16z(uint32_t dst, const void* src, int bytes) {
-  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
-}
-__device__ __forceinline__ void cp16z_if(bool go, uint32_t dst, const void* src, int bytes) {
-  asm volatile(
-      "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %3, 0;\n\t"
-      "@p cp.async.cg.shared.global [%0], [%1], 16, %2;\n\t}" ::"r"(dst), "l"(src), "r"(bytes), "r"((int)go)
-      : "memory");
+// bytes (a multiple of 16, all of it aligned to 16) into shared memory, counted by `bar`
+__device__ __forceinline__ void bulk_load(uint32_t dst, const void* src, uint32_t bytes, uint64_t* bar) {
+  asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(dst),
+               "l"(src), "r"(bytes), "r"(ptx::smem_u32(bar)) : "memory");
 }
 __device__ __forceinline__ float pow2(int e) { return __int_as_float((e + 127) << 23); }  // -126 <= e <= 127
 __device__ __forceinline__ int exponent(float x) { return (__float_as_int(x) >> 23) - 127; }  // of x > 0
@@ -103,17 +106,25 @@ __global__ void __launch_bounds__(NTHREADS, QRowsCfg<E, OUT_BF, BITS, D, NG_, NT
   constexpr int TERMS = C::TERMS, PT = C::PT;
   constexpr bool CENTRED = !OUT_BF;  // K's codes: centred before the product, or their constant (1024) taken off after it
   constexpr float CENTRE = BITS == 4 ? 8.f : 128.f;
-  constexpr int WH = CH / 2;          // V words of a lane and key
-  constexpr int J = BITS == 4 ? 4 : 2;  // output tiles of a word: columns j and j + J of each lane's
+  constexpr int VT = BITS == 4 ? 2 : 1;  // output tiles of a chunk: code pairs 2 t and 2 t + 1 of a word of V
   extern __shared__ __align__(1024) uint8_t smem[];
   __shared__ PlanShared<NTHREADS, WARPS> plan;
   __shared__ Ends<R> ends_sh;
+  __shared__ __align__(8) uint64_t bars[WARPS][NP][2];  // of a step's K and V
+  __shared__ int abort_sh;
   ptx::grid_launch_dependents();
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int quad = lane & 3, oct = lane >> 2;  // mma fragments: columns 2 quad, 2 quad + 1; row oct
   const fakv_cache& c = a.c;
   const Geo& g = a.g;
   const int chunks = a.qc.chunks;
+  const int runs_shift = 5 - a.run_shift;  // log2 of the runs of a step
+  static_assert(GROUP == 32, "runs_shift");
+  const uint32_t run_codes = chunks * 16 << a.run_shift, run_params = NG * 4 << a.run_shift;  // bytes
+  if (lane < 2 * NP) ptx::mbar_init(bars[warp][lane / 2] + (lane & 1), 1 << runs_shift);
+  if (tid == 0) abort_sh = 0;
+  ptx::fence_mbar_init();
+  __syncthreads();
   Seq seq;
   const Part part = find_part<NTHREADS, WARPS>(g, c, a.cu, a.slots, a.B, a.T, reinterpret_cast<int*>(smem), plan, seq);
   Walk walk(part, seq);
@@ -134,12 +145,12 @@ __global__ void __launch_bounds__(NTHREADS, QRowsCfg<E, OUT_BF, BITS, D, NG_, NT
     }
   };
   const long long v_minus_k = a.qc.V - a.qc.K;
-  // V: lanes of the upper four octs read the odd key of a pair first (their banks are those that the
-  // lower ones' even keys leave free), and put the halves together the other way round
-  const int odd = oct >> 2;
-  const int v_at = odd * 128 + (2 * quad + odd) * 16 + (oct & 3) * 4, v_other = odd ? -16 : 16;
-  const uint32_t sel_lo = BITS == 4 ? (odd ? 0x1054u : 0x5410u) : odd ? 0x1504u : 0x5140u;
-  const uint32_t sel_hi = BITS == 4 ? (odd ? 0x3276u : 0x7632u) : odd ? 0x3726u : 0x7362u;
+  int ring = 0, parity = 0;  // the next step's place, and how often (mod 2) it was filled before
+  auto wait = [&](uint64_t* bar) {
+    if (__all_sync(0xffffffffu, ptx::mbar_try_wait(bar, parity))) return true;
+    return __all_sync(0xffffffffu, ptx::mbar_wait(bar, parity, &abort_sh, &g_kvq_status, DEV_TIMEOUT, WAIT_LIMIT_NS)) != 0;
+  };
+  bool ok = true;
   Seg seg = {};
   Finish fin;
   bool held = false;  // the worker's only item, not done whole: its result waits for the others'
@@ -148,71 +159,59 @@ __global__ void __launch_bounds__(NTHREADS, QRowsCfg<E, OUT_BF, BITS, D, NG_, NT
     const Seq& s = seg.s;
     const Tile& x = seg.x;
 
-    // ---- where the next 32 octets of keys lie, an octet per lane, and the pages of the 32 after
-    // those: look-ups are never waited for in the loop
+    // ---- where the next 32 runs of keys lie (a run: keys of a step that lie in one page, one after
+    // another), a run per lane, and the pages of the 32 after those: look-ups are never waited for in the loop
     const int first = seg.k0 * GROUP;
     const int n = max(0, min(seg.k0 + seg.n, (x.hi + GROUP - 1) / GROUP) - seg.k0);  // steps
     const int* const row = c.table + (long long)s.slot * c.table_stride;
-    const uint8_t* const head = a.qc.K + seg.head * a.qc.head;
-    auto lookup = [&](int octet) {
-      const int j = first + octet * 8;
-      if (octet >= n * (GROUP / 8) || j >= x.hi || j + 8 <= x.lo) return -1;  // no row sees it
+    constexpr int UNSEEN = -1, MISSING = -2;
+    auto lookup = [&](int r) {
+      const int j = first + (r << a.run_shift);
+      if (r >= n << runs_shift || j >= x.hi || j + (1 << a.run_shift) <= x.lo) return UNSEEN;  // no row sees it
       const int p = row[j >> a.shift];
       if ((unsigned)p < (unsigned)c.num_pages) return p;
       raise(c.status, FAKV_BAD_PAGE);
-      return -1;
+      return MISSING;
     };
-    int page_next = lookup(lane);
-    unsigned there = 0;             // which of the 32 octets have a page
-    const uint8_t* block = a.qc.K;  // the lane's octet's
+    int page = UNSEEN, page_next = lookup(lane);
+    const uint8_t *codes = a.qc.K, *params_of = a.qc.K;  // of the lane's run in K
+    ptx::fence_async_shared();  // what was written to the ring by threads comes before the copies
+    __syncwarp();
 
-    // ---- copies of step i's K, then its V, octet by octet, each in a page (zeros for an octet that has
-    // none); `at`: the step's place in the ring
-    const uint8_t* src[GROUP / 8];   // the lane's piece of the codes of the step's octets
-    const uint8_t* src_p = nullptr;  // and of the params
-    unsigned have = 0;               // of the step's octets
-    int piece[(CH + 3) / 4];         // bytes of the lane's pieces (0: past the last chunk)
-#pragma unroll
-    for (int z = 0; z < (CH + 3) / 4; ++z) piece[z] = z * 32 + lane < chunks * 8 ? 16 : 0;
-    auto copy = [&](uint32_t at) {
-#pragma unroll
-      for (int k = 0; k < GROUP / 8; ++k)
-#pragma unroll
-        for (int z = 0; z < (CH + 3) / 4; ++z)
-          cp16z_if(CH % 4 == 0 || lane < CH * 8, at + (k * CH * 8 + z * 32 + lane) * 16, src[k] + z * 512,
-                   have >> k & 1 ? piece[z] : 0);
-      cp16z_if(lane < GROUP / 8 * 2 * NG, at + C::CODES + lane * 16, src_p, have >> (lane / (2 * NG)) & 1 ? 16 : 0);
-    };
-    auto load_k = [&](int i, uint32_t at) {
-      if (i < n) {
-        const int octet0 = i * (GROUP / 8);
-        if ((octet0 & 31) == 0) {
-          there = __ballot_sync(0xffffffffu, page_next >= 0);
-          block = page_next < 0 ? a.qc.K : head + page_next * a.qc.page;
-          page_next = lookup(octet0 + 32 + lane);
+    // ---- copies of step i's K, then its V, a run by each lane whose run is one of the step's: the keys that no
+    // row sees stay what they are, those of a missing page are zeros. `at`: the step's place in the ring
+    auto copy = [&](int i, uint32_t at, uint64_t* bar, long long v) {
+      if ((lane >> runs_shift) == (i & (31 >> runs_shift))) {
+        const int r = lane & ((1 << runs_shift) - 1);
+        const uint32_t to = at + r * (CH * 16 << a.run_shift), to_p = at + C::CODES + r * (NG * 4 << a.run_shift);
+        if (page >= 0) {
+          ptx::mbar_arrive_expect_tx(bar, run_codes + run_params);
+          bulk_load(to, codes + v, run_codes, bar);
+          bulk_load(to_p, params_of + v, run_params, bar);
+        } else {
+          if (page == MISSING) {
+            for (uint32_t k = 0; k < run_codes; k += 16) ptx::st_shared_v4(to + k, 0, 0, 0, 0);
+            for (uint32_t k = 0; k < run_params; k += 16) ptx::st_shared_v4(to_p + k, 0, 0, 0, 0);
+            ptx::fence_async_shared();
+          }
+          ptx::mbar_arrive(bar);
         }
-        have = there >> (octet0 & 31);
-        auto block_of = [&](int k) {
-          return reinterpret_cast<const uint8_t*>(
-              __shfl_sync(0xffffffffu, reinterpret_cast<unsigned long long>(block), (octet0 + k) & 31));
-        };
-        auto token_of = [&](int k) { return (first + (octet0 + k) * 8) & (c.page_size - 1); };
-#pragma unroll
-        for (int k = 0; k < GROUP / 8; ++k) src[k] = block_of(k) + (token_of(k) * chunks + lane) * 16;
-        const int k = lane / (2 * NG);  // (an octet's params are 2 NG pieces)
-        src_p = block_of(k) + (a.qc.params + token_of(k) * NG * 4 + (lane - k * 2 * NG) * 16);
-        copy(at);
       }
-      cp_commit();
     };
-    auto load_v = [&](int i, uint32_t at) {
-      if (i < n) {
-#pragma unroll
-        for (int k = 0; k < GROUP / 8; ++k) src[k] += v_minus_k;
-        src_p += v_minus_k;
-        copy(at + C::SLOT);
+    auto load_k = [&](int i, uint32_t at, uint64_t* bar) {
+      if (i >= n) return;
+      if ((i & (31 >> runs_shift)) == 0) {
+        page = page_next;
+        const int r = (i << runs_shift) + lane, t = (first + (r << a.run_shift)) & (c.page_size - 1);
+        const uint8_t* const block = a.qc.K + seg.head * a.qc.head + max(page, 0) * a.qc.page;
+        codes = block + t * chunks * 16;
+        params_of = block + a.qc.params + t * NG * 4;
+        page_next = lookup(r + 32);
       }
-      cp_commit();
+      copy(i, at, bar, 0);
+    };
+    auto load_v = [&](int i, uint32_t at, uint64_t* bar) {
+      if (i < n) copy(i, at + C::SLOT, bar + 1, v_minus_k);
     };
 
     // ---- q: fragments of its rows (zeros behind the item's rows and the tensor's columns), each row
@@ -294,8 +293,8 @@ __global__ void __launch_bounds__(NTHREADS, QRowsCfg<E, OUT_BF, BITS, D, NG_, NT
     }
     __syncwarp();
 
-    // rows 8 nt + 2 quad + e; o: columns (h's) base + j, base + j + J
-    float o[WH][J][NTR][4];
+    // rows 8 nt + 2 quad + e; o: of each tile, two adjacent columns of the lane's
+    float o[CH][VT][NTR][4];
     float2 m[NTR], l[NTR], oz[NTR][NG];
 #pragma unroll
     for (int nt = 0; nt < NTR; ++nt) {
@@ -304,9 +303,9 @@ __global__ void __launch_bounds__(NTHREADS, QRowsCfg<E, OUT_BF, BITS, D, NG_, NT
 #pragma unroll
       for (int i = 0; i < NG; ++i) oz[nt][i] = make_float2(0.f, 0.f);
 #pragma unroll
-      for (int h = 0; h < WH; ++h)
+      for (int w = 0; w < CH; ++w)
 #pragma unroll
-        for (int j = 0; j < J; ++j) o[h][j][nt][0] = o[h][j][nt][1] = o[h][j][nt][2] = o[h][j][nt][3] = 0.f;
+        for (int t = 0; t < VT; ++t) o[w][t][nt][0] = o[w][t][nt][1] = o[w][t][nt][2] = o[w][t][nt][3] = 0.f;
     }
     // keys that every row sees need no mask
     int in_lo, in_hi;
@@ -316,18 +315,24 @@ __global__ void __launch_bounds__(NTHREADS, QRowsCfg<E, OUT_BF, BITS, D, NG_, NT
       in_lo = g.window > 0 ? pb - g.window + 1 : 0;
     }
 
-    // Steps of 32 keys. K's and V's places are filled again as soon as each is read, NP steps ahead; the
-    // first NP rounds only load.
-    uint32_t use = C::Q_BYTES;  // of the step, in the warp's shared memory
+    // Steps of 32 keys. K's and V's places are filled again as soon as each is read, NP steps ahead.
     float cap = 0.f, lift = 1.f;  // V's scales so far are at most cap; times lift they are below 2^7
 #pragma unroll 1
-    for (int i = -NP; i < n; ++i) {
+    for (int k = 0; k < min(n, NP); ++k) {
+      const int at = ring + k < NP ? ring + k : ring + k - NP;
+      load_k(k, sq + C::Q_BYTES + at * 2 * C::SLOT, bars[warp][at]);
+      load_v(k, sq + C::Q_BYTES + at * 2 * C::SLOT, bars[warp][at]);
+    }
+    int i = 0;
+#pragma unroll 1
+    for (; i < n; ++i) {
       const int j0 = first + i * GROUP;
       const bool edge = j0 < in_lo || j0 + GROUP - 1 > in_hi;
+      const uint32_t use = C::Q_BYTES + ring * 2 * C::SLOT;  // the step's place in the warp's shared memory
+      uint64_t* const bar = bars[warp][ring];
       float2 sc[KT][NTR][2];  // scores, then probabilities: keys 16 kt + 8 z + oct, rows 8 nt + 2 quad, + 1
-      if (i >= 0) {
-        cp_wait<2 * NP - 1>();
-        __syncwarp();
+      if (!(ok = wait(bar))) break;
+      {
         const uint8_t* const slot = mine + use;
         // -------- scores
         // (chunks that the cache does not have: whatever lies in the slot, finite codes, times q's zeros)
@@ -351,8 +356,8 @@ __global__ void __launch_bounds__(NTHREADS, QRowsCfg<E, OUT_BF, BITS, D, NG_, NT
               word[e] = *reinterpret_cast<const uint32_t*>(slot + ((kt * 2 + e) * CH + w) * 128 + lane * 4);
             auto product = [&](auto pair, uint32_t b0, uint32_t b1, int nt) {  // code pairs `pair` and + 1
               constexpr int P = decltype(pair)::value;
-              uint32_t f[4] = {q_raise<BITS, P>(word[0]), q_raise<BITS, P>(word[1]), q_raise<BITS, P + 1>(word[0]),
-                               q_raise<BITS, P + 1>(word[1])};
+              uint32_t f[4] = {q_raise<BITS, P>(word[0], a.raised), q_raise<BITS, P>(word[1], a.raised), q_raise<BITS, P + 1>(word[0], a.raised),
+                               q_raise<BITS, P + 1>(word[1], a.raised)};
               if constexpr (CENTRED) {
                 f[0] = q_centred<BITS, P>(f[0]); f[1] = q_centred<BITS, P>(f[1]);
                 f[2] = q_centred<BITS, P + 1>(f[2]); f[3] = q_centred<BITS, P + 1>(f[3]);
@@ -445,11 +450,11 @@ __global__ void __launch_bounds__(NTHREADS, QRowsCfg<E, OUT_BF, BITS, D, NG_, NT
 #pragma unroll
             for (int k = 0; k < NG; ++k) oz[nt][k] = ptx::mul2(oz[nt][k], f);
 #pragma unroll
-            for (int h = 0; h < WH; ++h)
+            for (int w = 0; w < CH; ++w)
 #pragma unroll
-              for (int t = 0; t < J; ++t)
+              for (int t = 0; t < VT; ++t)
 #pragma unroll
-                for (int e = 0; e < 4; ++e) o[h][t][nt][e] *= e & 1 ? f.y : f.x;
+                for (int e = 0; e < 4; ++e) o[w][t][nt][e] *= e & 1 ? f.y : f.x;
           }
         }
 #pragma unroll
@@ -464,10 +469,9 @@ __global__ void __launch_bounds__(NTHREADS, QRowsCfg<E, OUT_BF, BITS, D, NG_, NT
             }
         __syncwarp();  // K's codes are read
       }
-      load_k(i + NP, sq + use);
-      if (i >= 0) {
-        cp_wait<2 * NP - 1>();
-        __syncwarp();
+      load_k(i + NP, sq + use, bar);
+      if (!(ok = wait(bar + 1))) break;
+      {
         const uint8_t* const slot = mine + use + C::SLOT;
         // -------- O^T += V^T (s P)^T, and the offsets' sums
         uint32_t pv[KT][2][NG];
@@ -491,13 +495,13 @@ __global__ void __launch_bounds__(NTHREADS, QRowsCfg<E, OUT_BF, BITS, D, NG_, NT
           const float f = pow2(5 - e) / lift;
           lift = pow2(5 - e);
 #pragma unroll
-          for (int h = 0; h < WH; ++h)
+          for (int w = 0; w < CH; ++w)
 #pragma unroll
-            for (int t = 0; t < J; ++t)
+            for (int t = 0; t < VT; ++t)
 #pragma unroll
               for (int nt = 0; nt < NTR; ++nt)
 #pragma unroll
-                for (int k = 0; k < 4; ++k) o[h][t][nt][k] *= f;
+                for (int k = 0; k < 4; ++k) o[w][t][nt][k] *= f;
         }
         uint32_t pf[KT][NG][NTR][PT][2];  // terms of s P; keys low, high
         auto weigh = [&](auto masked) {
@@ -531,48 +535,53 @@ __global__ void __launch_bounds__(NTHREADS, QRowsCfg<E, OUT_BF, BITS, D, NG_, NT
 #pragma unroll
         for (int kt = 0; kt < KT; ++kt) {
 #pragma unroll
-          for (int h = 0; h < WH; ++h) {
-            const int k = NG == 1 ? 0 : BITS == 4 ? h : h / 2;  // the words' group
-            uint32_t half[2][2];  // of keys low, high: two keys' codes side by side, of the words' low halves and of their high ones
+          for (int w = 0; w < CH; ++w) {
+            const int k = NG == 1 ? 0 : BITS == 4 ? w / 2 : w / 4;  // the chunk's group
+            uint32_t word[2];  // of keys low, high: codes of two keys side by side
 #pragma unroll
-            for (int z = 0; z < 2; ++z) {
-              const uint8_t* const at = slot + v_at + ((kt * 2 + z) * CH + 2 * h) * 128;
-              const uint32_t p = *reinterpret_cast<const uint32_t*>(at), q = *reinterpret_cast<const uint32_t*>(at + v_other);
-              half[z][0] = __byte_perm(p, q, sel_lo);
-              half[z][1] = __byte_perm(p, q, sel_hi);
-            }
+            for (int z = 0; z < 2; ++z)
+              word[z] = *reinterpret_cast<const uint32_t*>(slot + ((kt * 2 + z) * CH + w) * 128 + quad * 32 + oct * 4);
             auto tile = [&](auto jj) {
-              constexpr int t = decltype(jj)::value;
-              const uint32_t va[4] = {q_centred<BITS, t>(q_raise<BITS, t>(half[0][0])), q_centred<BITS, t>(q_raise<BITS, t>(half[0][1])),
-                                      q_centred<BITS, t>(q_raise<BITS, t>(half[1][0])), q_centred<BITS, t>(q_raise<BITS, t>(half[1][1]))};
+              constexpr int t = decltype(jj)::value, P = 2 * t;
+              const uint32_t va[4] = {q_centred<BITS, P>(q_raise<BITS, P>(word[0], a.raised)), q_centred<BITS, P + 1>(q_raise<BITS, P + 1>(word[0], a.raised)),
+                                      q_centred<BITS, P>(q_raise<BITS, P>(word[1], a.raised)), q_centred<BITS, P + 1>(q_raise<BITS, P + 1>(word[1], a.raised))};
 #pragma unroll
               for (int nt = 0; nt < NTR; ++nt) {
                 if constexpr (PT == 1) {
-                  mma_f16(o[h][t][nt], va, pf[kt][k][nt][0][0], pf[kt][k][nt][0][1]);
+                  mma_f16(o[w][t][nt], va, pf[kt][k][nt][0][0], pf[kt][k][nt][0][1]);
                 } else {  // a sum per 16 keys, added to O in fp32: O itself is not cut off at every product
                   float add[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
                   for (int b = PT - 1; b >= 0; --b) mma_f16(add, va, pf[kt][k][nt][b][0], pf[kt][k][nt][b][1]);
 #pragma unroll
-                  for (int e = 0; e < 4; ++e) o[h][t][nt][e] += add[e];
+                  for (int e = 0; e < 4; ++e) o[w][t][nt][e] += add[e];
                 }
               }
             };
             tile(std::integral_constant<int, 0>());
-            tile(std::integral_constant<int, 1>());
-            if constexpr (BITS == 4) {
-              tile(std::integral_constant<int, 2>());
-              tile(std::integral_constant<int, 3>());
-            }
+            if constexpr (BITS == 4) tile(std::integral_constant<int, 1>());
           }
         }
         __syncwarp();  // V's codes are read
       }
-      load_v(i + NP, sq + use);
-      use = use + 2 * C::SLOT == C::Q_BYTES + NP * 2 * C::SLOT ? C::Q_BYTES : use + 2 * C::SLOT;
+      load_v(i + NP, sq + use, bar);
+      if (++ring == NP) {
+        ring = 0;
+        parity ^= 1;
+      }
     }
-    cp_wait<0>();
-    __syncwarp();  // (every lane's copies have landed: the ring may be used for what comes next)
+    if (!ok) {
+      // a wait ran out: nothing more is asked for, and what is in flight is given time to land
+      for (int k = i; k < min(n, i + NP + 1); ++k) {
+        const int at = ring + k - i;
+        for (int v = 0; v < (k == i + NP ? 1 : 2); ++v) {
+          const uint64_t t0 = ptx::globaltimer();
+          while (!ptx::mbar_try_wait(bars[warp][at % NP] + v, parity ^ (at / NP & 1)) && ptx::globaltimer() - t0 < WAIT_LIMIT_NS / 16) {}
+        }
+      }
+      held = false;
+      break;
+    }
 
     // ---- this warp's sums into its shared memory
 #pragma unroll
@@ -590,15 +599,16 @@ __global__ void __launch_bounds__(NTHREADS, QRowsCfg<E, OUT_BF, BITS, D, NG_, NT
         for (int i = 0; i < NG; ++i) z[i] = over_keys(e ? oz[nt][i].y : oz[nt][i].x);
         const int r = nt * 8 + quad * 2 + e;
         if (oct == 0) ends_sh.ml[warp][r] = make_float2(e ? m[nt].y : m[nt].x, v);
-        float* const to = reinterpret_cast<float*>(mine) + r * C::OS + oct * 2 * J;
+        float* const to = reinterpret_cast<float*>(mine) + r * C::OS + oct * 2 * VT;
+        const float by = 1.f / lift;
 #pragma unroll
-        for (int h = 0; h < WH; ++h)
+        for (int w = 0; w < CH; ++w) {
+          const float zw = z[NG == 1 ? 0 : BITS == 4 ? w / 2 : w / 4];
 #pragma unroll
-          for (int t = 0; t < J; ++t) {
-            const float zh = z[NG == 1 ? 0 : BITS == 4 ? h : h / 2], by = 1.f / (lift * q_factor<BITS>(t));
-            to[h * 16 * J + t] = fmaf(o[h][t][nt][e], by, zh);
-            to[h * 16 * J + t + J] = fmaf(o[h][t][nt][e + 2], by, zh);
-          }
+          for (int t = 0; t < VT; ++t)
+            *reinterpret_cast<float2*>(to + w * 16 * VT + 2 * t) =
+                make_float2(fmaf(o[w][t][nt][e], by, zw), fmaf(o[w][t][nt][e + 2], by / q_factor<BITS>(1), zw));
+        }
       }
     fin = {s.row0, x.rho0, x.rows, seg.head, walk.p.ender,
            (seg.starts ? PART_STARTS : 0) | (seg.ends ? PART_ENDS : 0), 2 * worker + seg.slot};
@@ -623,6 +633,8 @@ fa_status run(QRowsArgs& a, cudaStream_t s) {
   void* w = nullptr;
   if (host::scratch_alloc(&w, partials_bytes(ctas * WARPS, C::R, D), s) != cudaSuccess) return failed();
   a.part = partials_at(w, ctas * WARPS, C::R, D);
+  // (fewer chunks than the slots have room for: their octets are not one after another there)
+  a.run_shift = a.qc.chunks == C::CH ? std::min(a.shift, log2_of(C::GROUP)) : 3;
   a.g.R = C::R;
   a.g.u_shift = log2_of(C::GROUP);
   a.g.start = 4;  // steps: looking up an item's first pages and rows takes about as long
@@ -675,11 +687,19 @@ fa_status launch_qattend_rows(const void* q, void* O, float* LSE, const int* cu,
   a.g.causal = p.causal;
   a.g.window = p.window;
   a.sl2 = p.scale * LOG2E;
+  a.raised = Q_RAISED;
   a.out_bf16 = p.out_dtype == FA_BF16;
   // Items of 8 or 16 rows: what a sequence's rows fit on average
   const long long rows = ((long long)p.T * rep + p.B - 1) / p.B;
   if (c.dtype == FA_BF16) return a.out_bf16 ? pick<__nv_bfloat16, true>(a, rows, s) : pick<__nv_bfloat16, false>(a, rows, s);
   return pick<float, false>(a, rows, s);
+}
+
+unsigned int read_and_clear_kvq_status(cudaError_t* err) {
+  unsigned int v = 0, zero = 0;
+  *err = cudaMemcpyFromSymbol(&v, g_kvq_status, sizeof(v));
+  if (*err == cudaSuccess) *err = cudaMemcpyToSymbol(g_kvq_status, &zero, sizeof(zero));
+  return v;
 }
 
 }  // namespace kv

@@ -261,7 +261,8 @@ __global__ void __launch_bounds__(THREADS) qappend_kernel(const __grid_constant_
         uint32_t v = 0;
 #pragma unroll
         for (int n = 0; n < 8; ++n) v |= code[n] << (4 * n);
-        *reinterpret_cast<uint32_t*>(block + q_code_at(a.q.chunks, sh.at[k], w) + quad * 4) = v;
+        if (which == 1) *reinterpret_cast<uint32_t*>(block + q_k_at(a.q.chunks, sh.at[k], w, quad)) = v;
+        else q_v_store<4>(block + q_v_at(4, a.q.chunks, sh.at[k], w, quad), v);
       } else {
         uint2 v = make_uint2(0, 0);
 #pragma unroll
@@ -269,7 +270,13 @@ __global__ void __launch_bounds__(THREADS) qappend_kernel(const __grid_constant_
           v.x |= code[n] << (8 * n);
           v.y |= code[4 + n] << (8 * n);
         }
-        *reinterpret_cast<uint2*>(block + q_code_at(a.q.chunks, sh.at[k], 2 * w + quad / 2) + (quad & 1) * 8) = v;
+        const int chunk = 2 * w + quad / 2, word = quad % 2 * 2;
+        if (which == 1) {
+          *reinterpret_cast<uint2*>(block + q_k_at(a.q.chunks, sh.at[k], chunk, word)) = v;
+        } else {
+          q_v_store<8>(block + q_v_at(8, a.q.chunks, sh.at[k], chunk, word), v.x);
+          q_v_store<8>(block + q_v_at(8, a.q.chunks, sh.at[k], chunk, word + 1), v.y);
+        }
       }
     }
     if (quad < a.q.groups) {
@@ -302,10 +309,18 @@ __global__ void __launch_bounds__(THREADS) qread_kernel(const __grid_constant__ 
     for (int w = 0; w < NW; ++w) {
       code[w] = make_uint2(0u, 0u);
       if (!there || w * 32 + quad * 8 >= a.D) continue;
-      if constexpr (BITS == 4)
-        code[w].x = *reinterpret_cast<const uint32_t*>(block + q_code_at(a.q.chunks, sh.at[k], w) + quad * 4);
-      else
-        code[w] = *reinterpret_cast<const uint2*>(block + q_code_at(a.q.chunks, sh.at[k], 2 * w + quad / 2) + (quad & 1) * 8);
+      if constexpr (BITS == 4) {
+        code[w].x = which == 0 ? *reinterpret_cast<const uint32_t*>(block + q_k_at(a.q.chunks, sh.at[k], w, quad))
+                               : q_v_load<4>(block + q_v_at(4, a.q.chunks, sh.at[k], w, quad));
+      } else {
+        const int chunk = 2 * w + quad / 2, word = quad % 2 * 2;
+        if (which == 0) {
+          code[w] = *reinterpret_cast<const uint2*>(block + q_k_at(a.q.chunks, sh.at[k], chunk, word));
+        } else {
+          code[w].x = q_v_load<8>(block + q_v_at(8, a.q.chunks, sh.at[k], chunk, word));
+          code[w].y = q_v_load<8>(block + q_v_at(8, a.q.chunks, sh.at[k], chunk, word + 1));
+        }
+      }
     }
     if (there) {
       const uint32_t* const p = reinterpret_cast<const uint32_t*>(block + a.q.params + sh.at[k] * a.q.groups * 4);

@@ -23,20 +23,48 @@ struct QCache {
 
 inline int q_chunks(int D, int bits) { return (D * bits + 127) / 128; }
 
-// of codes: 16-byte chunk k of token t (both of a block)
-__host__ __device__ __forceinline__ int q_code_at(int chunks, int t, int k) {
-  return ((t >> 3) * chunks + k) * 128 + (t & 7) * 16;
+// Where the codes of token t of a block are that belong to chunk k's 32-bit word `word` (8 or 4 columns): K's
+// are the word; V's are its four bytes, in pieces of 2 bytes (4 bits) or of 1, each as far from the next as two pieces.
+__device__ __forceinline__ int q_k_at(int chunks, int t, int k, int word) {
+  return ((t >> 3) * chunks + k) * 128 + (t & 7) * 16 + word * 4;
+}
+__device__ __forceinline__ int q_v_at(int bits, int chunks, int t, int k, int word) {
+  return ((t >> 3) * chunks + k) * 128 + (t & 7) / 2 * 32 + word * 8 + (t & 1) * (bits == 4 ? 2 : 1);
+}
+// A token's word of V codes, and its place in memory
+template <int BITS>
+__device__ __forceinline__ void q_v_store(uint8_t* at, uint32_t w) {
+  if constexpr (BITS == 4) {
+    reinterpret_cast<uint16_t*>(at)[0] = (uint16_t)w;
+    reinterpret_cast<uint16_t*>(at)[2] = (uint16_t)(w >> 16);
+  } else {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) at[2 * i] = (uint8_t)(w >> (8 * i));
+  }
+}
+template <int BITS>
+__device__ __forceinline__ uint32_t q_v_load(const uint8_t* at) {
+  if constexpr (BITS == 4) {
+    const uint16_t* const p = reinterpret_cast<const uint16_t*>(at);
+    return p[0] | (uint32_t)p[2] << 16;
+  } else {
+    // (both tokens' codes in two aligned words)
+    const uint2 v = *reinterpret_cast<const uint2*>(reinterpret_cast<uintptr_t>(at) & ~(uintptr_t)7);
+    return __byte_perm(v.x, v.y, reinterpret_cast<uintptr_t>(at) & 1 ? 0x7531 : 0x6420);
+  }
 }
 
 __device__ __forceinline__ float q_scale(uint32_t p) { return __uint_as_float(p << 16); }
 __device__ __forceinline__ float q_offset(uint32_t p) { return __uint_as_float(p & 0xffff0000u); }
 
 // Two codes of a word as 1024 + code, and 1024 + 16 code for nibbles 1 and 3 of a half. 4 bits: nibbles
-// R and R + 4 (R = 0 .. 3). 8 bits: bytes 2 R and 2 R + 1 (R = 0, 1).
+// R and R + 4 (R = 0 .. 3). 8 bits: bytes 2 R and 2 R + 1 (R = 0, 1). `raised`: Q_RAISED, from where the
+// compiler does not see its value: it would make two instructions of an and with one constant and an or with another.
+constexpr uint32_t Q_RAISED = 0x64006400u;
 template <int BITS, int R>
-__device__ __forceinline__ uint32_t q_raise(uint32_t w) {
-  if constexpr (BITS == 8) return __byte_perm(w, 0x64646464u, R == 0 ? 0x4140 : 0x4342);
-  else return ((R < 2 ? w : w >> 8) & (R % 2 ? 0x00f000f0u : 0x000f000fu)) | 0x64006400u;
+__device__ __forceinline__ uint32_t q_raise(uint32_t w, uint32_t raised) {
+  if constexpr (BITS == 8) return __byte_perm(w, raised, R == 0 ? 0x5150 : 0x5352);
+  else return ((R < 2 ? w : w >> 8) & (R % 2 ? 0x00f000f0u : 0x000f000fu)) | raised;
 }
 template <int BITS>
 __host__ __device__ constexpr float q_factor(int r) { return BITS == 4 && r % 2 ? 16.f : 1.f; }

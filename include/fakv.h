@@ -224,8 +224,10 @@ FA_API fa_status fakv_compact(const fakv_cache* cache, fa_stream_t stream);
  * Memory, in bytes. Page p, head h in plane l is a block at K + l * plane_stride + p * page_stride
  * + h * head_stride, of page_size * (16 chunks + 4 groups) bytes with chunks = ceil(D * bits / 128)
  * and groups = D / group:
- *   codes   [page_size / 8][chunks][8 tokens][16]: chunk k of a token has its columns
+ *   K codes [page_size / 8][chunks][8 tokens][16]: chunk k of a token has its columns
  *           k * 128 / bits and on, in order, lowest bits first (columns from D on: 0)
+ *   V codes [page_size / 8][chunks][4][32]: the same for two tokens, 2 i and 2 i + 1, side by
+ *           side: in turn 16 bits (4 bits a code) or 8 bits (8) of each
  *   params  [page_size][groups]: s in the low, z in the high 16 bits of a 32-bit word
  * Slots, tables, lengths, counts, status, ownership, ordering, capture and what is refused are as
  * above. */

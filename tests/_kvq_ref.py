@@ -28,14 +28,26 @@ def quantise(x, bits, group):
     return c.flatten(-2), s.masked_fill(bad, math.nan), z.masked_fill(bad, math.nan), bad
 
 
+def tokens(codes, page, chunks, bits, is_v):
+    """The code bytes of blocks [pages, heads, bytes], token by token: [pages, heads, page, chunks * 16]."""
+    P = codes.shape[0]
+    if is_v:
+        part = 2 if bits == 4 else 1  # bytes of one of two tokens in turn
+        x = codes.reshape(P, -1, page // 8, chunks, 4, 16 // part, 2, part)
+        x = x.permute(0, 1, 2, 4, 6, 3, 5, 7)  # octet, pair, token, chunk, pieces
+    else:
+        x = codes.reshape(P, -1, page // 8, chunks, 8, 16).transpose(3, 4)
+    return x.reshape(P, -1, page, chunks * 16)
+
+
 def unpack(cache, plane=0):
     """What the pages' memory holds: for K and V codes [pages, page, HKV, D], scales and offsets [.., groups]."""
     out = []
     P, S, D, bits, ng = cache.k.shape[1], cache.page_size, cache.head_dim, cache.bits, cache.head_dim // cache.group
     chunks = -(-D * bits // 128)
-    for x in (cache.k, cache.v):
+    for x, is_v in ((cache.k, False), (cache.v, True)):
         b = x[plane].cpu()  # [pages, heads, bytes]
-        codes = b[..., :S * chunks * 16].reshape(P, -1, S // 8, chunks, 8, 16).transpose(3, 4).reshape(P, -1, S, chunks * 16)
+        codes = tokens(b[..., :S * chunks * 16], S, chunks, bits, is_v)
         if bits == 4:
             codes = torch.stack([codes & 15, codes >> 4], -1).flatten(-2)
         words = b[..., S * chunks * 16:].reshape(P, -1, S, ng, 2, 2).contiguous().view(torch.int16)[..., 0].contiguous()

@@ -74,12 +74,11 @@ def test_append_holds_the_definition_bit_for_bit(kv, dtype, D, bits, group):
         for i in range(lens[b] - n, lens[b]):
             live[int(cache.table[order[b], i // page]), i % page] = True
     chunks = -(-D * bits // 128)
-    for now, before in ((cache.k[1].cpu(), k0[1].cpu()), (cache.v[1].cpu(), v0[1].cpu())):
-        c, c0 = (t[..., :page * chunks * 16].reshape(-1, HKV, page // 8, chunks, 8, 16).permute(0, 2, 4, 1, 3, 5).flatten(1, 2)
-                 for t in (now, before))
+    for now, before, is_v in ((cache.k[1].cpu(), k0[1].cpu(), False), (cache.v[1].cpu(), v0[1].cpu(), True)):
+        c, c0 = (ref.tokens(t[..., :page * chunks * 16], page, chunks, bits, is_v).transpose(1, 2) for t in (now, before))
         p, p0 = (t[..., page * chunks * 16:].reshape(-1, HKV, page, 4 * (D // group)).transpose(1, 2) for t in (now, before))
         assert torch.equal(c[~live], c0[~live]) and torch.equal(p[~live], p0[~live])
-        assert not bool(c[live].flatten(-2)[..., D * bits // 8:].any())  # columns that do not exist
+        assert not bool(c[live][..., D * bits // 8:].any())  # columns that do not exist
 
 
 @pytest.mark.parametrize("dtype", [BF, F32])
