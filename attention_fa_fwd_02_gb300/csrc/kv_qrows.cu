@@ -58,7 +58,8 @@ struct QRowsCfg {
   static constexpr int CH = D * BITS / 128;       // 16-byte chunks of a key's codes
   static constexpr int NG = NG_;                  // groups of a key
   static constexpr int KS = D / 16;               // k16 steps of q
-  static constexpr int GROUP = 32;                // keys of a step
+  static constexpr int GROUP = NTR == 1 && OUT_BF && D * BITS <= 512 ? 64 : 32;  // keys of a step
+  static constexpr int GROUP_SHIFT = GROUP == 64 ? 6 : 5;
   static constexpr int KT = GROUP / 16;
   static constexpr int CODES = GROUP * CH * 16;
   static constexpr int SLOT = CODES + GROUP * NG * 4;  // K (or V) of a step
@@ -118,8 +119,7 @@ __global__ void __launch_bounds__(NTHREADS, QRowsCfg<E, OUT_BF, BITS, D, NG_, NT
   const fakv_cache& c = a.c;
   const Geo& g = a.g;
   const int chunks = a.qc.chunks;
-  const int runs_shift = 5 - a.run_shift;  // log2 of the runs of a step
-  static_assert(GROUP == 32, "runs_shift");
+  const int runs_shift = C::GROUP_SHIFT - a.run_shift;  // log2 of the runs of a step
   const uint32_t run_codes = chunks * 16 << a.run_shift, run_params = NG * 4 << a.run_shift;  // bytes
   if (lane < 2 * NP) ptx::mbar_init(bars[warp][lane / 2] + (lane & 1), 1 << runs_shift);
   if (tid == 0) abort_sh = 0;
