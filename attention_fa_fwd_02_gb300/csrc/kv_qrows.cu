@@ -73,7 +73,7 @@ struct QRowsCfg {
   static constexpr int SMEM = WARPS * WARP_BYTES;
   static_assert(NP >= 2 && WARP_BYTES % 128 == 0 && SLOT % 128 == 0 && Q_BYTES % 128 == 0, "the ring");
   static_assert(SMEM >= 4 * 16385, "the plan's scratch");
-  static constexpr int STATIC = (int)sizeof(PlanShared<NTHREADS, WARPS>) + WARPS * (R * 8 + 20 + NP * 16) + 8;
+  static constexpr int STATIC = (int)sizeof(PlanShared<NTHREADS, WARPS>) + WARPS * (R * 8 + 20 + NP * 8) + 8;
   static_assert(CTAS_PER_SM * (SMEM + (STATIC + 1023) / 1024 * 1024 + 1024) <= 228 * 1024, "shared memory of the CTAs of an SM");
 };
 
@@ -111,7 +111,7 @@ __global__ void __launch_bounds__(NTHREADS, QRowsCfg<E, OUT_BF, BITS, D, NG_, NT
   extern __shared__ __align__(1024) uint8_t smem[];
   __shared__ PlanShared<NTHREADS, WARPS> plan;
   __shared__ Ends<R> ends_sh;
-  __shared__ __align__(8) uint64_t bars[WARPS][NP][2];  // of a step's K and V
+  __shared__ __align__(8) uint64_t bars[WARPS][NP];  // of a step's K and V
   __shared__ int abort_sh;
   ptx::grid_launch_dependents();
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -121,7 +121,7 @@ __global__ void __launch_bounds__(NTHREADS, QRowsCfg<E, OUT_BF, BITS, D, NG_, NT
   const int chunks = a.qc.chunks;
   const int runs_shift = C::GROUP_SHIFT - a.run_shift;  // log2 of the runs of a step
   const uint32_t run_codes = chunks * 16 << a.run_shift, run_params = NG * 4 << a.run_shift;  // bytes
-  if (lane < 2 * NP) ptx::mbar_init(bars[warp][lane / 2] + (lane & 1), 1 << runs_shift);
+  if (lane < NP) ptx::mbar_init(&bars[warp][lane], 1 << runs_shift);
   if (tid == 0) abort_sh = 0;
   ptx::fence_mbar_init();
   __syncthreads();
@@ -178,27 +178,9 @@ __global__ void __launch_bounds__(NTHREADS, QRowsCfg<E, OUT_BF, BITS, D, NG_, NT
     ptx::fence_async_shared();  // what was written to the ring by threads comes before the copies
     __syncwarp();
 
-    // ---- copies of step i's K, then its V, a run by each lane whose run is one of the step's: the keys that no
-    // row sees stay what they are, those of a missing page are zeros. `at`: the step's place in the ring
-    auto copy = [&](int i, uint32_t at, uint64_t* bar, long long v) {
-      if ((lane >> runs_shift) == (i & (31 >> runs_shift))) {
-        const int r = lane & ((1 << runs_shift) - 1);
-        const uint32_t to = at + r * (CH * 16 << a.run_shift), to_p = at + C::CODES + r * (NG * 4 << a.run_shift);
-        if (page >= 0) {
-          ptx::mbar_arrive_expect_tx(bar, run_codes + run_params);
-          bulk_load(to, codes + v, run_codes, bar);
-          bulk_load(to_p, params_of + v, run_params, bar);
-        } else {
-          if (page == MISSING) {
-            for (uint32_t k = 0; k < run_codes; k += 16) ptx::st_shared_v4(to + k, 0, 0, 0, 0);
-            for (uint32_t k = 0; k < run_params; k += 16) ptx::st_shared_v4(to_p + k, 0, 0, 0, 0);
-            ptx::fence_async_shared();
-          }
-          ptx::mbar_arrive(bar);
-        }
-      }
-    };
-    auto load_k = [&](int i, uint32_t at, uint64_t* bar) {
+    // ---- copies of step i's K and V, a run by each lane whose run is one of the step's: the keys that no row
+    // sees stay what they are, those of a missing page are zeros. `at`: the step's place in the ring
+    auto load = [&](int i, uint32_t at, uint64_t* bar) {
       if (i >= n) return;
       if ((i & (31 >> runs_shift)) == 0) {
         page = page_next;
@@ -208,10 +190,26 @@ __global__ void __launch_bounds__(NTHREADS, QRowsCfg<E, OUT_BF, BITS, D, NG_, NT
         params_of = block + a.qc.params + t * NG * 4;
         page_next = lookup(r + 32);
       }
-      copy(i, at, bar, 0);
-    };
-    auto load_v = [&](int i, uint32_t at, uint64_t* bar) {
-      if (i < n) copy(i, at + C::SLOT, bar + 1, v_minus_k);
+      if ((lane >> runs_shift) == (i & (31 >> runs_shift))) {
+        const int r = lane & ((1 << runs_shift) - 1);
+        const uint32_t to = at + r * (CH * 16 << a.run_shift), to_p = at + C::CODES + r * (NG * 4 << a.run_shift);
+        if (page >= 0) {
+          ptx::mbar_arrive_expect_tx(bar, 2 * (run_codes + run_params));
+          bulk_load(to, codes, run_codes, bar);
+          bulk_load(to_p, params_of, run_params, bar);
+          bulk_load(to + C::SLOT, codes + v_minus_k, run_codes, bar);
+          bulk_load(to_p + C::SLOT, params_of + v_minus_k, run_params, bar);
+        } else {
+          if (page == MISSING) {
+            for (int v = 0; v < 2; ++v) {
+              for (uint32_t k = 0; k < run_codes; k += 16) ptx::st_shared_v4(to + v * C::SLOT + k, 0, 0, 0, 0);
+              for (uint32_t k = 0; k < run_params; k += 16) ptx::st_shared_v4(to_p + v * C::SLOT + k, 0, 0, 0, 0);
+            }
+            ptx::fence_async_shared();
+          }
+          ptx::mbar_arrive(bar);
+        }
+      }
     };
 
     // ---- q: fragments of its rows (zeros behind the item's rows and the tensor's columns), each row
@@ -315,13 +313,12 @@ __global__ void __launch_bounds__(NTHREADS, QRowsCfg<E, OUT_BF, BITS, D, NG_, NT
       in_lo = g.window > 0 ? pb - g.window + 1 : 0;
     }
 
-    // Steps of 32 keys. K's and V's places are filled again as soon as each is read, NP steps ahead.
+    // Steps of GROUP keys, whose place is filled again as soon as it is read, NP steps ahead.
     float cap = 0.f, lift = 1.f;  // V's scales so far are at most cap; times lift they are below 2^7
 #pragma unroll 1
     for (int k = 0; k < min(n, NP); ++k) {
       const int at = ring + k < NP ? ring + k : ring + k - NP;
-      load_k(k, sq + C::Q_BYTES + at * 2 * C::SLOT, bars[warp][at]);
-      load_v(k, sq + C::Q_BYTES + at * 2 * C::SLOT, bars[warp][at]);
+      load(k, sq + C::Q_BYTES + at * 2 * C::SLOT, &bars[warp][at]);
     }
     int i = 0;
 #pragma unroll 1
@@ -329,9 +326,10 @@ __global__ void __launch_bounds__(NTHREADS, QRowsCfg<E, OUT_BF, BITS, D, NG_, NT
       const int j0 = first + i * GROUP;
       const bool edge = j0 < in_lo || j0 + GROUP - 1 > in_hi;
       const uint32_t use = C::Q_BYTES + ring * 2 * C::SLOT;  // the step's place in the warp's shared memory
-      uint64_t* const bar = bars[warp][ring];
+      uint64_t* const bar = &bars[warp][ring];
       float2 sc[KT][NTR][2];  // scores, then probabilities: keys 16 kt + 8 z + oct, rows 8 nt + 2 quad, + 1
       if (!(ok = wait(bar))) break;
+      const uint8_t* const slot_v = mine + use + C::SLOT;
       {
         const uint8_t* const slot = mine + use;
         // -------- scores
@@ -419,9 +417,21 @@ __global__ void __launch_bounds__(NTHREADS, QRowsCfg<E, OUT_BF, BITS, D, NG_, NT
                 }
             }
         }
-        // -------- probabilities; m where it has to move
+        // -------- probabilities; m, and the power of two on V's scales, where they have to move
+        float most = 0.f;
+#pragma unroll
+        for (int kt = 0; kt < KT; ++kt)
+#pragma unroll
+          for (int z = 0; z < 2; ++z) {
+            const int key = j0 + kt * 16 + z * 8 + oct;
+            uint32_t p[NG];
+            params(slot_v, kt, z, p);
+#pragma unroll
+            for (int k = 0; k < NG; ++k)  // (what no row sees need be no token; NaN is passed over)
+              if (!edge || (key >= x.lo && key < x.hi)) most = fmaxf(most, q_scale(p[k]));
+          }
         float2 mx[NTR];
-        bool grow = false;
+        bool grow = most > cap;
 #pragma unroll
         for (int nt = 0; nt < NTR; ++nt) {
           mx[nt] = make_float2(fmaxf(sc[0][nt][0].x, sc[0][nt][1].x), fmaxf(sc[0][nt][0].y, sc[0][nt][1].y));
@@ -432,6 +442,14 @@ __global__ void __launch_bounds__(NTHREADS, QRowsCfg<E, OUT_BF, BITS, D, NG_, NT
           grow |= mx[nt].x > m[nt].x + RESCALE_THRESHOLD || mx[nt].y > m[nt].y + RESCALE_THRESHOLD;
         }
         if (__any_sync(0xffffffffu, grow)) {
+          most = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(most)));
+          float fv = 1.f;
+          if (most > cap) {
+            const int e = min(max(exponent(most), -100), 126);
+            cap = pow2(e + 1);  // (twice the largest may come before the next move)
+            fv = pow2(5 - e) / lift;
+            lift = pow2(5 - e);
+          }
 #pragma unroll
           for (int nt = 0; nt < NTR; ++nt) {
             float2 f;
@@ -449,6 +467,7 @@ __global__ void __launch_bounds__(NTHREADS, QRowsCfg<E, OUT_BF, BITS, D, NG_, NT
             l[nt] = ptx::mul2(l[nt], f);
 #pragma unroll
             for (int k = 0; k < NG; ++k) oz[nt][k] = ptx::mul2(oz[nt][k], f);
+            f = ptx::mul2(f, make_float2(fv, fv));
 #pragma unroll
             for (int w = 0; w < CH; ++w)
 #pragma unroll
@@ -467,42 +486,7 @@ __global__ void __launch_bounds__(NTHREADS, QRowsCfg<E, OUT_BF, BITS, D, NG_, NT
               sc[kt][nt][z] = make_float2(ptx::ex2(v.x), ptx::ex2(v.y));
               l[nt] = ptx::add2(l[nt], sc[kt][nt][z]);
             }
-        __syncwarp();  // K's codes are read
-      }
-      load_k(i + NP, sq + use, bar);
-      if (!(ok = wait(bar + 1))) break;
-      {
-        const uint8_t* const slot = mine + use + C::SLOT;
         // -------- O^T += V^T (s P)^T, and the offsets' sums
-        uint32_t pv[KT][2][NG];
-        float most = 0.f;
-#pragma unroll
-        for (int kt = 0; kt < KT; ++kt)
-#pragma unroll
-          for (int z = 0; z < 2; ++z) {
-            params(slot, kt, z, pv[kt][z]);
-            if (edge) {  // (what no row sees need be no token)
-              const int key = j0 + kt * 16 + z * 8 + oct;
-#pragma unroll
-              for (int k = 0; k < NG; ++k) pv[kt][z][k] = key >= x.lo && key < x.hi ? pv[kt][z][k] : 0u;
-            }
-#pragma unroll
-            for (int k = 0; k < NG; ++k) most = fmaxf(most, q_scale(pv[kt][z][k]));  // (NaN is passed over)
-          }
-        if (__any_sync(0xffffffffu, most > cap)) {
-          const int e = min(max(exponent(__uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(most)))), -100), 126);
-          cap = pow2(e + 1);  // (twice the largest may come before the next move)
-          const float f = pow2(5 - e) / lift;
-          lift = pow2(5 - e);
-#pragma unroll
-          for (int w = 0; w < CH; ++w)
-#pragma unroll
-            for (int t = 0; t < VT; ++t)
-#pragma unroll
-              for (int nt = 0; nt < NTR; ++nt)
-#pragma unroll
-                for (int k = 0; k < 4; ++k) o[w][t][nt][k] *= f;
-        }
         uint32_t pf[KT][NG][NTR][PT][2];  // terms of s P; keys low, high
         auto weigh = [&](auto masked) {
 #pragma unroll
@@ -511,7 +495,9 @@ __global__ void __launch_bounds__(NTHREADS, QRowsCfg<E, OUT_BF, BITS, D, NG_, NT
             for (int z = 0; z < 2; ++z)
 #pragma unroll
               for (int k = 0; k < NG; ++k) {
-                const float ps = q_scale(pv[kt][z][k]), pz = fmaf(ps, CENTRE, q_offset(pv[kt][z][k])), pl = ps * lift;
+                uint32_t pv[NG];
+                params(slot_v, kt, z, pv);
+                const float ps = q_scale(pv[k]), pz = fmaf(ps, CENTRE, q_offset(pv[k])), pl = ps * lift;
 #pragma unroll
                 for (int nt = 0; nt < NTR; ++nt) {
                   const float2 p = sc[kt][nt][z];
@@ -540,7 +526,7 @@ __global__ void __launch_bounds__(NTHREADS, QRowsCfg<E, OUT_BF, BITS, D, NG_, NT
             uint32_t word[2];  // of keys low, high: codes of two keys side by side
 #pragma unroll
             for (int z = 0; z < 2; ++z)
-              word[z] = *reinterpret_cast<const uint32_t*>(slot + ((kt * 2 + z) * CH + w) * 128 + quad * 32 + oct * 4);
+              word[z] = *reinterpret_cast<const uint32_t*>(slot_v + ((kt * 2 + z) * CH + w) * 128 + quad * 32 + oct * 4);
             auto tile = [&](auto jj) {
               constexpr int t = decltype(jj)::value, P = 2 * t;
               const uint32_t va[4] = {q_centred<BITS, P>(q_raise<BITS, P>(word[0], a.raised)), q_centred<BITS, P + 1>(q_raise<BITS, P + 1>(word[0], a.raised)),
@@ -562,9 +548,9 @@ __global__ void __launch_bounds__(NTHREADS, QRowsCfg<E, OUT_BF, BITS, D, NG_, NT
             if constexpr (BITS == 4) tile(std::integral_constant<int, 1>());
           }
         }
-        __syncwarp();  // V's codes are read
       }
-      load_v(i + NP, sq + use, bar);
+      __syncwarp();  // the codes are read
+      load(i + NP, sq + use, bar);
       if (++ring == NP) {
         ring = 0;
         parity ^= 1;
@@ -572,12 +558,10 @@ __global__ void __launch_bounds__(NTHREADS, QRowsCfg<E, OUT_BF, BITS, D, NG_, NT
     }
     if (!ok) {
       // a wait ran out: nothing more is asked for, and what is in flight is given time to land
-      for (int k = i; k < min(n, i + NP + 1); ++k) {
+      for (int k = i; k < min(n, i + NP); ++k) {
         const int at = ring + k - i;
-        for (int v = 0; v < (k == i + NP ? 1 : 2); ++v) {
-          const uint64_t t0 = ptx::globaltimer();
-          while (!ptx::mbar_try_wait(bars[warp][at % NP] + v, parity ^ (at / NP & 1)) && ptx::globaltimer() - t0 < WAIT_LIMIT_NS / 16) {}
-        }
+        const uint64_t t0 = ptx::globaltimer();
+        while (!ptx::mbar_try_wait(&bars[warp][at % NP], parity ^ (at / NP & 1)) && ptx::globaltimer() - t0 < WAIT_LIMIT_NS / 16) {}
       }
       held = false;
       break;
