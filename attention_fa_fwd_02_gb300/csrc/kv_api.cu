@@ -409,6 +409,12 @@ FA_API fa_status fakv_qattend(const void* q, void* O, float* LSE, const int* cu,
   if ((st = check_attend_rows(q, O, LSE, cache->dtype, p)) != FA_OK) return st;
   fakv_tokens t = *p;
   if (t.window >= cache->max_pages * cache->page_size) t.window = 0;  // hides nothing
+  // Above 16 rows per sequence and kv head tensor-core tiles, as in fakv_attend
+  if (cache->dtype == FA_BF16 && (long long)t.T * (t.H / cache->HKV) > 16ll * t.B) {
+    st = launch_qattend_tiles(q, O, LSE, cu, slots, qcache_of(*cache, pages, p->plane), t,
+                              reinterpret_cast<cudaStream_t>(stream));
+    if (st != FA_ERR_UNSUPPORTED) return st;
+  }
   return launch_qattend_rows(q, O, LSE, cu, slots, qcache_of(*cache, pages, p->plane), t,
                              reinterpret_cast<cudaStream_t>(stream));
 }

@@ -96,9 +96,6 @@ __device__ __forceinline__ void bulk_load(uint32_t dst, const void* src, uint32_
   asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(dst),
                "l"(src), "r"(bytes), "r"(ptx::smem_u32(bar)) : "memory");
 }
-__device__ __forceinline__ float pow2(int e) { return __int_as_float((e + 127) << 23); }  // -126 <= e <= 127
-__device__ __forceinline__ int exponent(float x) { return (__float_as_int(x) >> 23) - 127; }  // of x > 0
-
 template <typename E, bool OUT_BF, int BITS, int D, int NG_, int NTR>
 __global__ void __launch_bounds__(NTHREADS, QRowsCfg<E, OUT_BF, BITS, D, NG_, NTR>::CTAS_PER_SM)
     qattend_rows_kernel(const __grid_constant__ QRowsArgs a) {
@@ -247,8 +244,8 @@ __global__ void __launch_bounds__(NTHREADS, QRowsCfg<E, OUT_BF, BITS, D, NG_, NT
         }
       top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
       top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
-      const int e = min(max(exponent(top), -100), 127);
-      const float down = pow2(14 - e), up = a.sl2 * pow2(e - 14);
+      const int e = min(max(q_exponent(top), -100), 127);
+      const float down = q_pow2(14 - e), up = fmaxf(a.sl2 * q_pow2(e - 14), FLT_MIN);  // (a masked score is -infinity times it)
       // (infinity in a row makes all that it sees NaN, whatever the codes)
       float sum[NG], bias[NG];
 #pragma unroll
@@ -445,10 +442,10 @@ __global__ void __launch_bounds__(NTHREADS, QRowsCfg<E, OUT_BF, BITS, D, NG_, NT
           most = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(most)));
           float fv = 1.f;
           if (most > cap) {
-            const int e = min(max(exponent(most), -100), 126);
-            cap = pow2(e + 1);  // (twice the largest may come before the next move)
-            fv = pow2(5 - e) / lift;
-            lift = pow2(5 - e);
+            const int e = min(max(q_exponent(most), -100), 126);
+            cap = q_pow2(e + 1);  // (twice the largest may come before the next move)
+            fv = q_pow2(5 - e) / lift;
+            lift = q_pow2(5 - e);
           }
 #pragma unroll
           for (int nt = 0; nt < NTR; ++nt) {

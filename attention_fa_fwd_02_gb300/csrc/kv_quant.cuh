@@ -79,12 +79,26 @@ __device__ __forceinline__ uint32_t q_centred(uint32_t raised) {
   return d;
 }
 
+__device__ __forceinline__ uint32_t q_fma2(uint32_t a, uint32_t b, uint32_t c) {
+  uint32_t d;
+  asm("fma.rn.f16x2 %0, %1, %2, %3;" : "=r"(d) : "r"(a), "r"(b), "r"(c));
+  return d;
+}
+__device__ __forceinline__ uint32_t q_half2(float lo, float hi) {
+  const __half2 h = __floats2half2_rn(lo, hi);
+  return *reinterpret_cast<const uint32_t*>(&h);
+}
+__device__ __forceinline__ float q_pow2(int e) { return __int_as_float((e + 127) << 23); }      // -126 <= e <= 127
+__device__ __forceinline__ int q_exponent(float x) { return (__float_as_int(x) >> 23) - 127; }  // of x > 0
+
 fa_status launch_qappend(const void* q, const void* k, const void* v, void* qo, const int* cu, const int* slots,
                          const fakv_rope* r, const QCache& c, const fakv_tokens& p, cudaStream_t s);
 fa_status launch_qread(void* K, void* V, const int* cu, const int* slots, const int* first, const QCache& c,
                        const fakv_tokens& p, cudaStream_t s);
 fa_status launch_qattend_rows(const void* q, void* O, float* LSE, const int* cu, const int* slots, const QCache& c,
                               const fakv_tokens& p, cudaStream_t s);
+fa_status launch_qattend_tiles(const void* q, void* O, float* LSE, const int* cu, const int* slots, const QCache& c,
+                               const fakv_tokens& p, cudaStream_t s);
 
 }  // namespace kv
 }  // namespace fa

@@ -41,6 +41,7 @@
 #include <algorithm>
 #include <cfloat>
 #include <cmath>
+#include "kv_quant.cuh"
 #include "kv_sched.cuh"
 
 namespace fa {
@@ -53,6 +54,9 @@ using namespace ptx;
 
 struct TilesArgs {
   fakv_cache c;
+  QCache qc;         // codes
+  uint32_t raised;   // Q_RAISED
+  const float* qf;   // codes: what makes logits (log2) of a row's scores, [T][H]
   void* O;
   float* LSE;
   const int* cu;
@@ -67,10 +71,11 @@ struct TilesArgs {
   unsigned long long limit_ns;
 };
 
-template <int D_>
+template <int D_, int BITS>  // BITS: of the cache's codes; 0: bf16 pages
 struct TilesCfg {
   static constexpr int D = D_;
   static constexpr int NQ = 2;
+  static constexpr uint32_t FMT = BITS ? FMT_F16 : FMT_BF16;
   static constexpr int NCB = D / 64;                      // 64-column blocks
   static constexpr uint32_t CB_BYTES = 128u * 128u;       // one block of a 128-row tile
   static constexpr uint32_t TILE_BYTES = NCB * CB_BYTES;
@@ -84,9 +89,12 @@ struct TilesCfg {
   static constexpr uint32_t SMEM = V_OFF + VST * V_STAGE + 1024;
   static constexpr int SOFTMAX_WARPS = 8, MMA_WARP = 8, KQ_WARP = 9, V_WARP = 10, RELAY_WARP = 11;
   static constexpr uint32_t RELAY_BAR = 3;  // named barrier (1 + q: P_q written)
-  static constexpr int THREADS = 384;
-  static constexpr uint32_t REGS_SOFTMAX = 216, REGS_CONTROL = 64;
-  static_assert(2 * 128 * REGS_SOFTMAX + 128 * REGS_CONTROL <= 384 * 168, "register split exceeds the launch allocation");
+  static constexpr int CODE_WARP = 12;  // codes: two warps for K's tiles, two for V's, half a tile each
+  static constexpr int THREADS = BITS ? 512 : 384;
+  static constexpr uint32_t REGS_SOFTMAX = BITS ? 192 : 216, REGS_CONTROL = BITS ? 48 : 64, REGS_CODES = 80;
+  static_assert(2 * 128 * REGS_SOFTMAX + 128 * REGS_CONTROL + (BITS ? 128 * REGS_CODES : 0) <= THREADS * (BITS ? 128 : 168),
+                "register split exceeds the launch allocation");
+  static constexpr uint32_t FILLERS = BITS ? 2 : 1;  // arrivals at a landed tile's barrier, and at a grant
   static constexpr uint32_t TMEM_COLS = 512;
   __host__ __device__ static constexpr uint32_t s_col(int q) { return 128u * q; }
   __host__ __device__ static constexpr uint32_t o_col(int q) { return 256u + (uint32_t)D * q; }
@@ -109,7 +117,7 @@ __device__ __forceinline__ uint32_t pack_bf2(float lo, float hi) {
 
 template <class C>
 __device__ __forceinline__ void issue_qk(uint32_t d_tmem, uint32_t sq, uint32_t sk) {
-  constexpr uint32_t id = make_idesc(128, 128, FMT_BF16, FMT_BF16, false, false);
+  constexpr uint32_t id = make_idesc(128, 128, C::FMT, C::FMT, false, false);
 #pragma unroll
   for (int kk = 0; kk < C::D / 16; ++kk) {
     const uint32_t off = (kk / 4) * C::CB_BYTES + (kk % 4) * 32;
@@ -118,7 +126,7 @@ __device__ __forceinline__ void issue_qk(uint32_t d_tmem, uint32_t sq, uint32_t 
 }
 template <class C, int TERMS>
 __device__ __forceinline__ void issue_pv(uint32_t o_tmem, uint32_t p_tmem, uint32_t sv, bool accumulate) {
-  constexpr uint32_t id = make_idesc(128, C::D, FMT_BF16, FMT_BF16, false, true);
+  constexpr uint32_t id = make_idesc(128, C::D, C::FMT, C::FMT, false, true);
 #pragma unroll
   for (int term = TERMS - 1; term >= 0; --term)
 #pragma unroll
@@ -187,11 +195,62 @@ __device__ __forceinline__ void store_rows(uint32_t t_addr, bool have, float mul
   fence_async_shared();  // before the copy engine writes the stage again
 }
 
-template <int D, int TERMS>
-__global__ void __launch_bounds__(TilesCfg<D>::THREADS, 1)
+// ---- tiles of codes
+// A batch of a warp's part of a tile: BO octets of keys, 16-byte pieces of codes for each lane. K: the lane's piece is
+// chunk `chunk` of token lane % 8. V: half a pair's chunk, both tokens'.
+template <int BITS, int D>
+struct CodeBatch {
+  static constexpr int CH = D * BITS / 128;            // chunks of a key
+  static constexpr int PIECES = CH >= 4 ? CH / 4 : 1;  // of an octet, for each lane
+  static constexpr int BO = 4 / PIECES;                // octets of a batch
+  uint4 w[BO][PIECES];
+};
+constexpr int TILE_INFO = 8;  // tiles whose powers of two are kept: K's codes are at most five tiles ahead of the softmax
+
+// q as fp16, each row times a power of two that brings its largest value to 2^14 (exactly, but for what is 2^-28 of
+// that), and what undoes it, times the softmax scale. Sixteen lanes to a row. A row with NaN or infinity becomes NaN.
+constexpr int QROWS_THREADS = 256;
+__global__ void __launch_bounds__(QROWS_THREADS) qattend_q_kernel(const __nv_bfloat16* q, long long q_token, long long q_head,
+                                                                  int rows, Div heads, int D, float sl2, uint16_t* out,
+                                                                  float* factor) {
+  grid_launch_dependents();
+  const int lane = threadIdx.x & 15, row = blockIdx.x * (QROWS_THREADS / 16) + threadIdx.x / 16;
+  const int token = heads.of(min(row, rows - 1)), col = lane * 8;
+  uint4 v = make_uint4(0, 0, 0, 0);
+  if (row < rows && col < D)
+    v = *reinterpret_cast<const uint4*>(q + token * q_token + (row - token * heads.d) * q_head + col);
+  const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+  float x[8], top = 0.f;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    x[2 * i] = __uint_as_float(w[i] << 16);
+    x[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
+  }
+  bool fine = true;
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    top = fmaxf(top, fabsf(x[i]));
+    fine = fine && fabsf(x[i]) < INFINITY;
+  }
+#pragma unroll
+  for (int d = 1; d < 16; d <<= 1) {
+    top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, d));
+    fine = __shfl_xor_sync(0xffffffffu, (int)fine, d) && fine;
+  }
+  const int e = min(max(q_exponent(top), -60), 127);
+  const float by = fine ? q_pow2(14 - e) : __int_as_float(0x7fffffff);
+  if (row >= rows) return;
+  if (col < D)
+    *reinterpret_cast<uint4*>(out + (size_t)row * D + col) = make_uint4(q_half2(x[0] * by, x[1] * by), q_half2(x[2] * by, x[3] * by),
+                                                                        q_half2(x[4] * by, x[5] * by), q_half2(x[6] * by, x[7] * by));
+  if (lane == 0) factor[row] = sl2 * q_pow2(e - 14);
+}
+
+template <int D, int TERMS, int BITS>
+__global__ void __launch_bounds__(TilesCfg<D, BITS>::THREADS, 1)
     attend_tiles_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
                         const __grid_constant__ CUtensorMap tmV, const __grid_constant__ TilesArgs a) {
-  using C = TilesCfg<D>;
+  using C = TilesCfg<D, BITS>;
   constexpr int NQ = C::NQ, KST = C::KST, VST = C::VST;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
@@ -199,6 +258,7 @@ __global__ void __launch_bounds__(TilesCfg<D>::THREADS, 1)
       bar_vempty[VST], bar_grant[NQ], bar_s[NQ], bar_o[NQ], bar_join, bar_drain;
   __shared__ uint32_t tmem_base_sh;
   __shared__ int abort_sh, stuck_sh;
+  __shared__ float2 info_sh[BITS ? TILE_INFO : 1][2];  // codes: of each half of a tile, K's power of two and V's exponent
   __shared__ PlanShared<C::THREADS, 1> plan;
   grid_launch_dependents();
   const int warp = warp_id(), lane = lane_id();
@@ -210,10 +270,10 @@ __global__ void __launch_bounds__(TilesCfg<D>::THREADS, 1)
       mbar_init(&bar_qfree[q], 1);
       mbar_init(&bar_s[q], 1);
       mbar_init(&bar_o[q], 1);
-      mbar_init(&bar_grant[q], 1);
+      mbar_init(&bar_grant[q], C::FILLERS);
     }
-    for (int s = 0; s < KST; ++s) { mbar_init(&bar_kfull[s], 1); mbar_init(&bar_kempty[s], 1); }
-    for (int s = 0; s < VST; ++s) { mbar_init(&bar_vfull[s], 1); mbar_init(&bar_vempty[s], 1); }
+    for (int s = 0; s < KST; ++s) { mbar_init(&bar_kfull[s], C::FILLERS); mbar_init(&bar_kempty[s], 1); }
+    for (int s = 0; s < VST; ++s) { mbar_init(&bar_vfull[s], C::FILLERS); mbar_init(&bar_vempty[s], 1); }
     mbar_init(&bar_join, C::SOFTMAX_WARPS);
     mbar_init(&bar_drain, 1);
     abort_sh = stuck_sh = 0;
@@ -227,6 +287,7 @@ __global__ void __launch_bounds__(TilesCfg<D>::THREADS, 1)
   }
   Seq seq;
   const Part part = find_part<C::THREADS, 1>(a.g, a.c, a.cu, a.slots, a.B, a.T, reinterpret_cast<int*>(smem), plan, seq);
+  if constexpr (BITS != 0) grid_dependency_wait();  // (q as fp16)
   // (the plan's scratch lies in the tiles: its generic accesses before the copies' writes)
   fence_async_shared();
   tc_fence_before();
@@ -278,9 +339,275 @@ __global__ void __launch_bounds__(TilesCfg<D>::THREADS, 1)
     __syncwarp();
   };
 
-  if (warp >= C::SOFTMAX_WARPS) {
+  if (BITS && warp >= C::CODE_WARP) {
+    // ------------------------------------------------------------ codes of K, of V
+    // Each of two warps writes 64 keys of every tile, as the copies of bf16 pages would have laid them down, in fp16:
+    // times a power of two that keeps the largest of the 64 keys' values just below 2^8 (K: undone in the scores) or
+    // 2^7 (V: undone in the probabilities); 2^-12 of a value, or 2^-32 of the largest, is rounded off. A batch's loads are on
+    // their way while the one before it is turned into numbers. Keys that no row sees, and those of a missing page,
+    // are zeros; a key whose scale is NaN, in K or in V, is NaN in K and zeros in V, so that rows that see it become NaN
+    // and the tile's others do not.
+    regs_decrease<C::REGS_CODES>();
+    if constexpr (BITS != 0) {
+      auto fill_tiles = [&](auto is_v) {
+        constexpr bool IS_V = decltype(is_v)::value;
+        using T = CodeBatch<BITS, D>;
+        constexpr int BO = T::BO, PIECES = T::PIECES, BATCHES = 8 / BO, NG = D / 64;
+        constexpr float CENTRE = BITS == 4 ? 8.f : 128.f, STEPS = BITS == 4 ? 15.f : 255.f;
+        const int half = (warp - C::CODE_WARP) & 1;  // of the tile
+        const int chunks = a.qc.chunks, ng = a.qc.groups;
+        const uint8_t* const base = IS_V ? a.qc.V : a.qc.K;
+        // the lane's piece: 16 bytes of an octet's 128 a chunk
+        const int chunk0 = lane >> 3;
+        const int token = IS_V ? 2 * (lane & 3) : lane & 7, side = (lane >> 2) & 1;
+        const int at = chunk0 * 128 + (IS_V ? (lane & 3) * 32 + side * 16 : (lane & 7) * 16);
+        auto octet_page = [&](int kt) {  // of octet lane % 8 of the warp's half: -1: unseen or missing
+          const int j = kt * BLOCK_N + half * 64 + (lane & 7) * 8;
+          if (j >= seg.x.hi || j + 8 <= seg.x.lo) return -1;
+          const int p = a.c.table[(long long)seg.s.slot * a.c.table_stride + (j >> a.shift)];
+          if ((unsigned)p < (unsigned)a.c.num_pages) return p;
+          raise(a.c.status, FAKV_BAD_PAGE);
+          return -1;
+        };
+        // params of keys lane and lane + 32 of the half, K's and V's (V's warps: V's)
+        struct Params {
+          uint32_t k[2][NG], v[2][NG];
+        };
+        auto ask_params = [&](Params& b, int kt, int page) {
+#pragma unroll
+          for (int i = 0; i < 2; ++i) {
+            const int p = __shfl_sync(0xffffffffu, page, i * 4 + lane / 8);
+            const int key = kt * BLOCK_N + half * 64 + i * 32 + lane;
+            const long long off = p * a.qc.page + seg.head * a.qc.head + a.qc.params + (key & (a.c.page_size - 1)) * ng * 4;
+            const bool in = p >= 0 && key >= seg.x.lo && key < seg.x.hi;
+#pragma unroll
+            for (int j = 0; j < NG; ++j) {
+              const int w = NG > 1 && ng > 1 ? j * 4 : 0;
+              b.v[i][j] = in ? __ldg(reinterpret_cast<const uint32_t*>(a.qc.V + off + w)) : 0u;
+              if constexpr (!IS_V) b.k[i][j] = in ? __ldg(reinterpret_cast<const uint32_t*>(a.qc.K + off + w)) : 0u;
+            }
+          }
+        };
+        auto ask = [&](T& b, int kt, int page, int batch) {
+#pragma unroll
+          for (int o = 0; o < BO; ++o) {
+            const int p = __shfl_sync(0xffffffffu, page, batch * BO + o);
+            const int t = (kt * BLOCK_N + half * 64 + (batch * BO + o) * 8) & (a.c.page_size - 1);
+            const uint8_t* const from = base + p * a.qc.page + seg.head * a.qc.head + t * chunks * 16 + at;
+#pragma unroll
+            for (int z = 0; z < PIECES; ++z)
+              b.w[o][z] = p >= 0 && chunk0 + 4 * z < chunks ? __ldg(reinterpret_cast<const uint4*>(from + z * 512)) : make_uint4(0, 0, 0, 0);
+          }
+        };
+        // scale (low) and z' (high) of keys lane and lane + 32, as fp16 times the half's power of two
+        struct Factors {
+          uint32_t f[2][NG];
+        };
+        auto nan = [](uint32_t p) { return (p & 0x7fffu) > 0x7f80u; };
+        auto exponent_of = [&](const uint32_t (&p)[2][NG]) {  // of the largest value that the half's keys can hold
+          float top = 0.f;
+#pragma unroll
+          for (int i = 0; i < 2; ++i) {
+            bool skip = false;
+#pragma unroll
+            for (int j = 0; j < NG; ++j) skip |= nan(p[i][j]);
+#pragma unroll
+            for (int j = 0; j < NG; ++j) {
+              const float s = q_scale(p[i][j]), z = q_offset(p[i][j]);
+              if (!skip) top = fmaxf(top, fmaxf(fabsf(z), fabsf(fmaf(s, STEPS, z))));
+            }
+          }
+          top = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(top)));
+          return min(max(q_exponent(top), -50), 126);
+        };
+        auto factors = [&](const Params& b, float2* info) {
+          const int ev = exponent_of(b.v) - 6, e = IS_V ? ev : exponent_of(b.k) - 7;
+          if (!IS_V && lane == 0) *info = make_float2(q_pow2(e), (float)ev);
+          const float by = q_pow2(-e);
+          Factors f;
+#pragma unroll
+          for (int i = 0; i < 2; ++i) {
+            bool bad = false;
+#pragma unroll
+            for (int j = 0; j < NG; ++j) bad |= nan(b.v[i][j]) || (!IS_V && nan(b.k[i][j]));
+#pragma unroll
+            for (int j = 0; j < NG; ++j) {
+              const uint32_t p = IS_V ? b.v[i][j] : b.k[i][j];
+              const float s = q_scale(p);
+              f.f[i][j] = bad ? (IS_V ? 0u : 0x7fff7fffu) : q_half2(s * by, fmaf(s, CENTRE, q_offset(p)) * by);
+            }
+          }
+          return f;
+        };
+        auto write = [&](const T& b, const Factors& f, uint32_t tile, int batch) {
+#pragma unroll
+          for (int o = 0; o < BO; ++o) {
+            const int octet = batch * BO + o, r = half * 64 + octet * 8 + token;  // row of the tile
+            uint32_t sz[NG][IS_V ? 2 : 1];
+#pragma unroll
+            for (int j = 0; j < NG; ++j)
+#pragma unroll
+              for (int e = 0; e < (IS_V ? 2 : 1); ++e) sz[j][e] = __shfl_sync(0xffffffffu, f.f[octet >> 2][j], (octet & 3) * 8 + token + e);
+#pragma unroll
+            for (int z = 0; z < PIECES; ++z) {
+              const int col = (chunk0 + 4 * z) * (128 / BITS);
+              if (col >= D) continue;
+              // 16-byte piece c of row r + e
+              auto put = [&](int e, int c, uint32_t x0, uint32_t x1, uint32_t x2, uint32_t x3) {
+                st_shared_v4(tile + (c >> 3) * C::CB_BYTES + (r + e) * 128 + (((c & 7) ^ ((r + e) & 7)) << 4), x0, x1, x2, x3);
+              };
+              const bool upper = NG > 1 && col >= 64;
+              const uint32_t p0 = upper ? sz[NG - 1][0] : sz[0][0], p1 = IS_V ? (upper ? sz[NG - 1][IS_V] : sz[0][IS_V]) : p0;
+              const uint32_t s = __byte_perm(p0, p1, 0x5410), zz = __byte_perm(p0, p1, 0x7632);
+              const uint32_t words[4] = {b.w[o][z].x, b.w[o][z].y, b.w[o][z].z, b.w[o][z].w};
+              if constexpr (BITS == 4) {
+                const uint32_t s16 = q_fma2(s, 0x2c002c00u, 0u);  // s / 16
+                // the four pairs of a word: K: columns n and n + 4; V: column n of both tokens
+                auto pairs = [&](uint32_t w, uint32_t (&x)[4]) {
+                  x[0] = q_fma2(q_centred<4, 0>(q_raise<4, 0>(w, a.raised)), s, zz);
+                  x[1] = q_fma2(q_centred<4, 1>(q_raise<4, 1>(w, a.raised)), s16, zz);
+                  x[2] = q_fma2(q_centred<4, 2>(q_raise<4, 2>(w, a.raised)), s, zz);
+                  x[3] = q_fma2(q_centred<4, 3>(q_raise<4, 3>(w, a.raised)), s16, zz);
+                };
+                if constexpr (!IS_V) {
+#pragma unroll
+                  for (int i = 0; i < 4; ++i) {
+                    uint32_t x[4];
+                    pairs(words[i], x);
+                    put(0, col / 8 + i, __byte_perm(x[0], x[1], 0x5410), __byte_perm(x[2], x[3], 0x5410),
+                        __byte_perm(x[0], x[1], 0x7632), __byte_perm(x[2], x[3], 0x7632));
+                  }
+                } else {
+#pragma unroll
+                  for (int i = 0; i < 2; ++i) {
+                    // (the two sides' lanes take their words in turn, so that eight lanes' pieces lie in different banks)
+                    const int k = i ^ side;
+                    uint32_t x[4], y[4];
+                    pairs(k ? words[2] : words[0], x);
+                    pairs(k ? words[3] : words[1], y);
+                    put(0, col / 8 + side * 2 + k, __byte_perm(x[0], x[1], 0x5410), __byte_perm(x[2], x[3], 0x5410),
+                        __byte_perm(y[0], y[1], 0x5410), __byte_perm(y[2], y[3], 0x5410));
+                    put(1, col / 8 + side * 2 + k, __byte_perm(x[0], x[1], 0x7632), __byte_perm(x[2], x[3], 0x7632),
+                        __byte_perm(y[0], y[1], 0x7632), __byte_perm(y[2], y[3], 0x7632));
+                  }
+                }
+              } else {
+                uint32_t x[4][2];  // of each word, K: columns 0, 1 and 2, 3; V: column 0 and column 1 of both tokens
+#pragma unroll
+                for (int k = 0; k < 4; ++k) {
+                  x[k][0] = q_fma2(q_centred<8, 0>(q_raise<8, 0>(words[k], a.raised)), s, zz);
+                  x[k][1] = q_fma2(q_centred<8, 1>(q_raise<8, 1>(words[k], a.raised)), s, zz);
+                }
+                if constexpr (!IS_V) {
+                  put(0, col / 8, x[0][0], x[0][1], x[1][0], x[1][1]);
+                  put(0, col / 8 + 1, x[2][0], x[2][1], x[3][0], x[3][1]);
+                } else {
+#pragma unroll
+                  for (int e = 0; e < 2; ++e) {
+                    const uint32_t sel = e ? 0x7632 : 0x5410;
+                    put(e, col / 8 + side, __byte_perm(x[0][0], x[0][1], sel), __byte_perm(x[1][0], x[1][1], sel),
+                        __byte_perm(x[2][0], x[2][1], sel), __byte_perm(x[3][0], x[3][1], sel));
+                  }
+                }
+              }
+            }
+          }
+        };
+        // tile kt of the item, its params asked for before, its stage waited for by `free`; asks for the next one's
+        Params params;
+        int page = -1;
+        auto begin = [&](int kt) {
+          page = octet_page(kt);
+          ask_params(params, kt, page);
+        };
+        auto tile = [&](int kt, bool more, uint32_t to, uint64_t* full, float2* info, auto free) {
+          T b[2];
+          ask(b[0], kt, page, 0);
+          const int page_next = more ? octet_page(kt + 1) : -1;
+          if (!free()) return false;
+          const Factors f = factors(params, info);
+#pragma unroll
+          for (int i = 0; i < BATCHES; ++i) {
+            if (i + 1 < BATCHES) ask(b[(i + 1) & 1], kt, page, i + 1);
+            else if (more) ask_params(params, kt + 1, page_next);
+            write(b[i & 1], f, to, i);
+          }
+          page = page_next;
+          fence_async_shared();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(full);
+          return true;
+        };
+        bool ok = true;
+        if constexpr (!IS_V) {
+          int g = 0;
+          while (ok && next()) {
+            if (seg.n > 0) begin(seg.k0);
+            for (int t = 0; ok && t < seg.n; ++t, ++g) {
+              const int ks = g % KST;
+              ok = tile(seg.k0 + t, t + 1 < seg.n, sK(ks), &bar_kfull[ks], &info_sh[g % TILE_INFO][half],
+                        [&] { return __all_sync(0xffffffffu, wait_free(&bar_kempty[ks], ((g / KST) & 1) ^ 1)) != 0; });
+            }
+          }
+        } else {
+          // (a stage's uses -- key tiles, and per item one epilogue staging -- have positions in
+          // order; each of the two warps waits for their releases in that order)
+          uint32_t pos = 0;
+          int seen[VST];
+          for (int s = 0; s < VST; ++s) seen[s] = 0;
+          int prev_stage = -1;
+          auto wait_release = [&](uint32_t p) {
+            const int s = p % VST, u = p / VST;
+            if (seen[s] > u) return true;
+            if (!__all_sync(0xffffffffu, wait_free(&bar_vempty[s], u & 1))) return false;
+            seen[s] = u + 1;
+            return true;
+          };
+          while (ok && next()) {
+            if (seg.n > 0) begin(seg.k0);
+            for (int t = 0; ok && t < seg.n; ++t, ++pos)
+              ok = tile(seg.k0 + t, t + 1 < seg.n, sV(pos % VST), &bar_vfull[pos % VST], nullptr,
+                        [&] { return pos < (uint32_t)VST || wait_release(pos - VST); });
+            if (!ok) break;
+            if (pos >= (uint32_t)VST && !(ok = wait_release(pos - VST))) break;
+            if (prev_stage >= 0 && !(ok = wait_release((uint32_t)prev_stage))) break;
+            if (lane == 0)
+              for (int q = 0; q < NQ; ++q) mbar_arrive(&bar_grant[q]);
+            __syncwarp();
+            prev_stage = (int)pos;
+            ++pos;
+          }
+        }
+      };
+      if (warp < C::CODE_WARP + 2) fill_tiles(std::false_type());
+      else fill_tiles(std::true_type());
+    }
+  } else if (warp >= C::SOFTMAX_WARPS) {
     regs_decrease<C::REGS_CONTROL>();
-    if (warp == C::KQ_WARP) {
+    if (BITS && warp == C::KQ_WARP) {
+      // ---------------------------------------------------------- Q producer (the codes have their own)
+      int j = 0;
+      bool ok = true;
+      while (ok && next()) {
+        if (seg.n == 0) continue;
+        for (int q = 0; ok && q < NQ; ++q) {
+          if (j > 0 && !(ok = __all_sync(0xffffffffu, wait_free(&bar_qfree[q], (j - 1) & 1)))) break;
+          if (lane == 0) {
+            mbar_arrive_expect_tx(&bar_q[q], C::NCB * 128u * a.RT);
+            for (int cb = 0; cb < C::NCB; ++cb)
+              tma_load_4d(sQ(q) + cb * C::CB_BYTES, &tmQ, &bar_q[q], cb * 64, 0,
+                          seg.s.row0 + a.g.rep.of(seg.x.rho0) + q * a.tpt, seg.head);
+          }
+          __syncwarp();
+        }
+        if (ok) ++j;
+      }
+      // every issued copy must land before the CTA may exit (those of an item that was given up, for as long as the limit)
+      if (j > 0)
+        for (int q = 0; q < NQ; ++q) drain(&bar_q[q], (j - 1) & 1);
+      if (!ok)
+        for (int q = 0; q < NQ; ++q) drain(&bar_q[q], j & 1);
+    } else if (!BITS && warp == C::KQ_WARP) {
       // ---------------------------------------------------------- Q / K producer
       int g = 0, j = 0;  // key tiles, items with keys
       int last_k[KST], last_q = -1;
@@ -318,7 +645,7 @@ __global__ void __launch_bounds__(TilesCfg<D>::THREADS, 1)
         if (last_k[s] >= 0) drain(&bar_kfull[s], last_k[s] & 1);
       if (last_q >= 0)
         for (int q = 0; q < NQ; ++q) drain(&bar_q[q], last_q & 1);
-    } else if (warp == C::V_WARP) {
+    } else if (!BITS && warp == C::V_WARP) {
       // ---------------------------------------------------------- V producer
       // (a stage's uses -- key tiles, and per item one epilogue staging -- have positions in
       // order, and this warp alone waits for their releases, in that order)
@@ -433,7 +760,7 @@ __global__ void __launch_bounds__(TilesCfg<D>::THREADS, 1)
                                              (!more || wait(&bar_kfull[(g + 1) % KST], ((g + 1) / KST) & 1)));
           ++vc[vs];
           const int end = seg.s.len - (seg.k0 + t) * BLOCK_N;  // tokens from here on are past the sequence
-          if (ok && end < BLOCK_N) {
+          if (!BITS && ok && end < BLOCK_N) {
             for (int i = end * 8 + lane; i < BLOCK_N * 8; i += 32)
               for (int cb = 0; cb < C::NCB; ++cb) st_shared_v4(sV(vs) + cb * C::CB_BYTES + i * 16, 0, 0, 0, 0);
             fence_async_shared();
@@ -481,6 +808,12 @@ __global__ void __launch_bounds__(TilesCfg<D>::THREADS, 1)
       const int in_hi = a.g.causal ? min(p0, last) : last;  // keys that every row sees
       const int in_lo = a.g.window > 0 ? p1 - a.g.window + 1 : 0;
       float m = -FLT_MAX, l = 0.f;
+      // codes: the row's factor, and the exponent that the probabilities are taken against (O is O * 2^v_ref)
+      float qf = 0.f, v_ref = 0.f;
+      if (BITS && r_in < rows) {
+        const int token = a.g.rep.of(rho0 + r_in);
+        qf = a.qf[(size_t)(seg.s.row0 + token) * a.H + seg.head * a.g.rep.d + rho0 + r_in - token * a.g.rep.d];
+      }
       for (int t = 0; t < n; ++t, ++g) {
         if (live) live = __all_sync(0xffffffffu, wait_issuer(&bar_s[q], g & 1));
         if (!live) {
@@ -503,6 +836,62 @@ __global__ void __launch_bounds__(TilesCfg<D>::THREADS, 1)
         }
         const int c0 = (seg.k0 + t) * BLOCK_N;
         if (c0 < in_lo || c0 + BLOCK_N - 1 > in_hi) mask_outside<128>(s, lo_i - c0, hi_i - c0);
+        if constexpr (BITS != 0) {
+          const float2 i0 = info_sh[g % TILE_INFO][0], i1 = info_sh[g % TILE_INFO][1];
+          // (positive whatever the row: a masked score is -infinity times it)
+          const float k_half[2] = {fmaxf(qf * i0.x, FLT_MIN), fmaxf(qf * i1.x, FLT_MIN)}, v_half[2] = {i0.y, i1.y};
+          float mh[2];
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            float mx[4];
+#pragma unroll
+            for (int kk = 0; kk < 4; ++kk) mx[kk] = max3(s[64 * h + kk], s[64 * h + 4 + kk], s[64 * h + 8 + kk]);
+#pragma unroll
+            for (int c = 12; c < 60; c += 8)
+#pragma unroll
+              for (int kk = 0; kk < 4; ++kk) mx[kk] = max3(mx[kk], s[64 * h + c + kk], s[64 * h + c + 4 + kk]);
+#pragma unroll
+            for (int kk = 0; kk < 4; ++kk) mx[kk] = fmaxf(mx[kk], s[64 * h + 60 + kk]);
+            mh[h] = fmaxf(max3(mx[0], mx[1], mx[2]), mx[3]) * k_half[h];
+          }
+          const float mt = fmaxf(mh[0], mh[1]), v_top = fmaxf(v_half[0], v_half[1]);
+          // (2^8 of a probability and 2^6 of V's exponent beyond v_ref: P stays below 2^15)
+          const bool v_grow = t == 0 || v_top > v_ref + 6.f;
+          if (__any_sync(0xffffffffu, (r_in < rows && mt > m + RESCALE_THRESHOLD) || v_grow)) {
+            const float m_new = fmaxf(m, mt), v_new = v_grow ? v_top : v_ref;
+            const float corr = ex2(m - m_new);
+            l *= corr;
+            if (t > 0) {
+              const float by = corr * ex2(v_ref - v_new);
+#pragma unroll
+              for (int c = 0; c < D / 32; ++c) {
+                uint32_t r[32];
+                tmem_ld32(o_addr + c * 32, r);
+#pragma unroll
+                for (int kk = 0; kk < 32; ++kk) r[kk] = __float_as_uint(__uint_as_float(r[kk]) * by);
+                tmem_st32(o_addr + c * 32, r);
+              }
+            }
+            m = m_new;
+            v_ref = v_new;
+          }
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            const float up = fmaxf(v_half[h] - v_ref, -60.f);  // (far below that, P is 0 in fp16)
+            const float2 by = make_float2(k_half[h], k_half[h]), off = make_float2(up - m, up - m);
+            float2 ls[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
+            uint32_t pk[32];
+#pragma unroll
+            for (int kk = 0; kk < 32; ++kk) {
+              const float2 x = fma2(make_float2(s[h * 64 + 2 * kk], s[h * 64 + 2 * kk + 1]), by, off);
+              const float2 pp = make_float2(ex2(x.x), ex2(x.y));
+              ls[kk & 1] = add2(ls[kk & 1], pp);
+              pk[kk] = pack_half2(pp.x, pp.y);
+            }
+            tmem_st32(s_addr + h * 32, pk);
+            l = fmaf((ls[0].x + ls[1].x) + (ls[0].y + ls[1].y), ex2(-up), l);
+          }
+        } else {
         float mx[8];
 #pragma unroll
         for (int kk = 0; kk < 8; ++kk) mx[kk] = max3(s[kk], s[8 + kk], s[16 + kk]);
@@ -550,6 +939,7 @@ __global__ void __launch_bounds__(TilesCfg<D>::THREADS, 1)
           if constexpr (TERMS > 1) tmem_st32(s_addr + 64 + c * 32, lo);
         }
         l += (ls[0].x + ls[1].x) + (ls[0].y + ls[1].y);
+        }
         tmem_st_wait();
         tc_fence_before();
         named_bar_arrive(1 + q, 128 + 32);
@@ -582,7 +972,7 @@ __global__ void __launch_bounds__(TilesCfg<D>::THREADS, 1)
         const int cols = whole ? a.c.D : D;
         const size_t row_bytes = (size_t)cols * (bf ? 2 : 4);
         auto ptr = [&](int r) -> char* { return r < warp_rows ? to + at(wq * 32 + r) * row_bytes : nullptr; };
-        const float inv = !whole ? 1.f : l == 0.f ? 0.f : __fdividef(1.f, l);  // (NaN stays)
+        const float inv = (!whole ? 1.f : l == 0.f ? 0.f : __fdividef(1.f, l)) * (BITS ? ex2(v_ref) : 1.f);  // (NaN stays)
         if (r_in < rows) {
           if (whole) a.LSE[at(r_in)] = l == 0.f ? -INFINITY : (m + __log2f(l)) * LN2;
           else a.part.ml[at(r_in)] = make_float2(m, l);
@@ -614,10 +1004,10 @@ __global__ void __launch_bounds__(TilesCfg<D>::THREADS, 1)
   }
 }
 
-template <int D, int TERMS>
+template <int D, int TERMS, int BITS>
 fa_status run(TilesArgs& a, const CUtensorMap& q, const CUtensorMap& k, const CUtensorMap& v, cudaStream_t s) {
-  using C = TilesCfg<D>;
-  auto* kernel = attend_tiles_kernel<D, TERMS>;
+  using C = TilesCfg<D, BITS>;
+  auto* kernel = attend_tiles_kernel<D, TERMS, BITS>;
   static std::atomic<uint64_t> done{0};
   if (!allow_smem(kernel, C::SMEM, done)) return failed();
   const int ctas = host::sm_count();
@@ -626,8 +1016,9 @@ fa_status run(TilesArgs& a, const CUtensorMap& q, const CUtensorMap& k, const CU
   a.part = partials_at(w, ctas, a.g.R, D);
   fa_status st;
   {
-    host::KernelTimer t("attend_tiles", s);
-    st = launch(kernel, ctas, C::THREADS, C::SMEM, s, q, k, v, a);
+    host::KernelTimer t(BITS ? "qattend_tiles" : "attend_tiles", s);
+    if (BITS) st = launch_programmatic_smem(kernel, ctas, C::THREADS, C::SMEM, s, q, k, v, a) == cudaSuccess ? FA_OK : failed();
+    else st = launch(kernel, ctas, C::THREADS, C::SMEM, s, q, k, v, a);
   }
   if (st == FA_OK) {
     const JoinArgs j = {a.part, a.O, a.LSE, ctas, 1, a.g.R, D, a.H, a.c.D, a.out_bf16, a.g.rep};
@@ -637,11 +1028,16 @@ fa_status run(TilesArgs& a, const CUtensorMap& q, const CUtensorMap& k, const CU
   return st;
 }
 
-}  // namespace
+// q as [HKV][T][rep][D]
+bool map_q(CUtensorMap* m, const TilesArgs& a, const void* q, long long token, long long head) {
+  const int rep = a.g.rep.d;
+  const uint64_t qd[4] = {(uint64_t)a.c.D, (uint64_t)rep, (uint64_t)a.T, (uint64_t)a.c.HKV};
+  const uint64_t qs[3] = {(uint64_t)head * 2, (uint64_t)token * 2, (uint64_t)head * rep * 2};
+  const uint32_t qb[4] = {64, (uint32_t)rep, (uint32_t)a.tpt, 1};
+  return host::encode_tiled_4d(m, q, qd, qs, qb);
+}
 
-fa_status launch_attend_tiles(const void* q, void* O, float* LSE, const int* cu, const int* slots,
-                              const fakv_cache& c, const fakv_tokens& p, cudaStream_t s) {
-  if (host::sm_count() > TALL_CTAS) return FA_ERR_UNSUPPORTED;
+TilesArgs args_of(void* O, float* LSE, const int* cu, const int* slots, const fakv_cache& c, const fakv_tokens& p) {
   TilesArgs a = {};
   const int rep = p.H / c.HKV;
   a.c = c;
@@ -661,21 +1057,54 @@ fa_status launch_attend_tiles(const void* q, void* O, float* LSE, const int* cu,
   a.sl2 = p.scale * LOG2E;
   a.out_bf16 = p.out_dtype == FA_BF16;
   a.limit_ns = WAIT_LIMIT_NS;
+  return a;
+}
+
+}  // namespace
+
+fa_status launch_attend_tiles(const void* q, void* O, float* LSE, const int* cu, const int* slots,
+                              const fakv_cache& c, const fakv_tokens& p, cudaStream_t s) {
+  if (host::sm_count() > TALL_CTAS) return FA_ERR_UNSUPPORTED;
+  TilesArgs a = args_of(O, LSE, cu, slots, c, p);
   const uint64_t d = c.D, b2 = 2;
   CUtensorMap mq, mk, mv;
-  // q as [HKV][T][rep][D], the pages as [page][head][token][D]
-  const uint64_t qd[4] = {d, (uint64_t)rep, (uint64_t)p.T, (uint64_t)c.HKV};
-  const uint64_t qs[3] = {(uint64_t)p.q_head * b2, (uint64_t)p.q_token * b2, (uint64_t)p.q_head * rep * b2};
-  const uint32_t qb[4] = {64, (uint32_t)rep, (uint32_t)a.tpt, 1};
+  // the pages as [page][head][token][D]
   const uint64_t kd[4] = {d, (uint64_t)c.page_size, (uint64_t)c.HKV, (uint64_t)c.num_pages};
   const uint64_t ks[3] = {(uint64_t)c.token_stride * b2, (uint64_t)c.head_stride * b2, (uint64_t)c.page_stride * b2};
   const uint32_t kb[4] = {64, (uint32_t)a.box, 1, 1};
   const long long plane = p.plane * c.plane_stride * 2;
-  if (!host::encode_tiled_4d(&mq, q, qd, qs, qb) || !host::encode_tiled_4d(&mk, static_cast<const char*>(c.K) + plane, kd, ks, kb) ||
+  if (!map_q(&mq, a, q, p.q_token, p.q_head) || !host::encode_tiled_4d(&mk, static_cast<const char*>(c.K) + plane, kd, ks, kb) ||
       !host::encode_tiled_4d(&mv, static_cast<const char*>(c.V) + plane, kd, ks, kb))
     return FA_ERR_UNSUPPORTED;
-  if (a.out_bf16) return c.D <= 64 ? run<64, 1>(a, mq, mk, mv, s) : run<128, 1>(a, mq, mk, mv, s);
-  return c.D <= 64 ? run<64, 2>(a, mq, mk, mv, s) : run<128, 2>(a, mq, mk, mv, s);
+  if (a.out_bf16) return c.D <= 64 ? run<64, 1, 0>(a, mq, mk, mv, s) : run<128, 1, 0>(a, mq, mk, mv, s);
+  return c.D <= 64 ? run<64, 2, 0>(a, mq, mk, mv, s) : run<128, 2, 0>(a, mq, mk, mv, s);
+}
+
+fa_status launch_qattend_tiles(const void* q, void* O, float* LSE, const int* cu, const int* slots,
+                               const QCache& qc, const fakv_tokens& p, cudaStream_t s) {
+  if (host::sm_count() > TALL_CTAS) return FA_ERR_UNSUPPORTED;
+  TilesArgs a = args_of(O, LSE, cu, slots, qc.c, p);
+  a.qc = qc;
+  a.raised = Q_RAISED;
+  const int D = qc.c.D, rows = p.T * p.H;
+  const size_t row_bytes = ((size_t)rows * D * 2 + 255) & ~(size_t)255;
+  void* w = nullptr;
+  if (host::scratch_alloc(&w, row_bytes + (size_t)rows * 4, s) != cudaSuccess) return failed();
+  float* const qf = reinterpret_cast<float*>(static_cast<char*>(w) + row_bytes);
+  a.qf = qf;
+  CUtensorMap mq;
+  fa_status st = map_q(&mq, a, w, (long long)p.H * D, D) ? FA_OK : FA_ERR_UNSUPPORTED;
+  if (st == FA_OK) {
+    host::KernelTimer t("qattend_q", s);
+    st = launch(qattend_q_kernel, (rows + QROWS_THREADS / 16 - 1) / (QROWS_THREADS / 16), QROWS_THREADS, 0, s,
+                static_cast<const __nv_bfloat16*>(q), p.q_token, p.q_head, rows, div_by(p.H), D, a.sl2,
+                static_cast<uint16_t*>(w), qf);
+  }
+  // (no map of K and V is looked at)
+  if (st == FA_OK && qc.bits == 4) st = D <= 64 ? run<64, 1, 4>(a, mq, mq, mq, s) : run<128, 1, 4>(a, mq, mq, mq, s);
+  else if (st == FA_OK) st = D <= 64 ? run<64, 1, 8>(a, mq, mq, mq, s) : run<128, 1, 8>(a, mq, mq, mq, s);
+  if (host::scratch_free(w, s) != cudaSuccess) st = failed();
+  return st;
 }
 
 unsigned int read_and_clear_kv_status(cudaError_t* err) {

@@ -117,8 +117,9 @@ def attend(cache, q, new, slots, scale, causal, window, plane=0, tiles=False):
     s x, x the centred code) and p z' in fp32; ex2.approx adds 2^-22; sums over n keys (n / 16 + 32) 2^-23 and, for the
     offsets, n 2^-24, each of M_d = sum_j p_j (s |x| + |z'|).
 
-    Many rows (`tiles`): K and V are rounded to bf16 after the formula x s + z', z' rounded too: each value is off by at
-    most 2^-8 of (|value| + |z'|); P is one bf16 term where the output is bf16 (2^-8)."""
+    Many rows (`tiles`): K, V and P are rounded to fp16 (half a step 2^-11): K and V after x s + z', s and z' rounded
+    too: a value is off by at most 2^-11 of (|value| + |z'| + s |x|), and by 2^-24 of the largest of 64 keys where it is
+    below 2^-14 of that (bounded here by the largest of all); q is fp16 exactly but for 2^-25 of its row's largest."""
     T, H, D = q.shape
     q = q.double().cpu()
     rep = H // cache.kv_heads
@@ -145,8 +146,9 @@ def attend(cache, q, new, slots, scale, causal, window, plane=0, tiles=False):
                 continue
             z = (scale * qh @ k[:, i].T).masked_fill(~see, -math.inf)
             if tiles:
-                off = qa @ (k[:, i].abs() + (kz + mid * ks)[:, i].abs()).T * 2.0 ** -8
-                e = scale * (off + qa @ k[:, i].abs().T * D * 2.0 ** -23)
+                size_k = k[:, i].abs() + (kz + mid * ks)[:, i].abs() + (ks * (kc - mid).abs())[:, i]
+                off = qa @ (size_k * 2.0 ** -11 + size_k.max() * 2.0 ** -24).T + qa.amax(1, keepdim=True) * 2.0 ** -25 * size_k.sum(1)
+                e = scale * (off + qa @ size_k.T * D * 2.0 ** -23)
             else:
                 m = qa @ (ks * (kc + 2 * const))[:, i].T
                 e = scale * (3 * D * 2.0 ** -23 * m + 2.0 ** -22 * (m + qa @ kz[:, i].abs().T))
@@ -158,8 +160,10 @@ def attend(cache, q, new, slots, scale, causal, window, plane=0, tiles=False):
             mass = vs * (vc - mid).abs() + (vz + mid * vs).abs()
             up = 2.0 ** -16 + 2.0 ** -22 + (size / 16 + 32) * 2.0 ** -23 + size * 2.0 ** -24
             if tiles:
-                up += 2.0 ** -8 + 2.0 ** -8
+                up += 2.0 ** -11 + 2.0 ** -11
             bo[at:at + n, h] = 2 * e * (w @ v[:, i].abs()) + up * (w @ mass[:, i])
+            if tiles:
+                bo[at:at + n, h] += 2.0 ** -24 * mass[:, i].max()
             bl[at:at + n, h] = e[:, 0] + (size / 16 + 32) * 2.0 ** -23 + lse.nan_to_num(neginf=0.0).abs() * 2.0 ** -22
         at += n
     return O, L, bo, bl

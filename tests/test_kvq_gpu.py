@@ -259,3 +259,22 @@ def test_attend_strided_queries_and_forked_slots(kv, dtype, bits):
     want, want_l, bo, bl = ref.attend(cache, q, [1, 1], [0, 0], 64 ** -0.5, True, 0)
     _kv_ref.close(o.cpu(), want, bo, "O")
     assert bool(((lse.cpu().double() - want_l).abs() <= bl).all())
+
+
+# ---- chunks of a prompt (tensor-core tiles)
+@pytest.mark.parametrize("D,bits,group", ref.SHAPES)
+def test_attend_chunks(kv, D, bits, group):
+    check_attend(kv, BF, [70, 40, 0, 90], [70, 300, 20, 217], 16, 8, 2, D, bits, group, tiles=True, shift=0.2, pad=3)
+
+
+@pytest.mark.parametrize("bits,group", [(4, 64), (8, 128), (4, 128)])
+@pytest.mark.parametrize("new,lens,page,H,HKV,kw", [
+    ([300], [300], 8, 4, 4, {}),
+    ([129, 65], [1000, 65], 32, 16, 2, {"window": 100}),
+    ([200, 64], [700, 131], 64, 4, 1, {"causal": False}),
+    ([90, 17], [513, 512], 256, 5, 5, {"window": 1}),
+    ([33, 31], [1040, 50], 1024, 24, 3, {"pad": 50, "scale": 0.3}),
+    ([100, 0, 35], [190, 0, 35], 16, 6, 2, {"causal": False, "window": 20, "pad": 2}),
+    ([150], [2000], 128, 7, 1, {"out_dtype": F32})])
+def test_attend_chunks_masks_and_shapes(kv, bits, group, new, lens, page, H, HKV, kw):
+    check_attend(kv, BF, new, lens, page, H, HKV, 128, bits, group, tiles=True, **kw)
