@@ -91,9 +91,10 @@ struct TilesCfg {
   static constexpr uint32_t RELAY_BAR = 3;  // named barrier (1 + q: P_q written)
   static constexpr int CODE_WARP = 12;  // codes: two warps for K's tiles, two for V's, half a tile each
   static constexpr int THREADS = BITS ? 512 : 384;
-  static constexpr uint32_t REGS_SOFTMAX = BITS ? 192 : 216, REGS_CONTROL = BITS ? 48 : 64, REGS_CODES = 80;
-  static_assert(2 * 128 * REGS_SOFTMAX + 128 * REGS_CONTROL + (BITS ? 128 * REGS_CODES : 0) <= THREADS * (BITS ? 128 : 168),
-                "register split exceeds the launch allocation");
+  // (codes: every warp keeps the 128 registers that 512 threads leave; the softmax reads its scores twice instead of
+  // holding them all)
+  static constexpr uint32_t REGS_SOFTMAX = 216, REGS_CONTROL = 64;
+  static_assert(BITS || 2 * 128 * REGS_SOFTMAX + 128 * REGS_CONTROL <= 384 * 168, "register split exceeds the launch allocation");
   static constexpr uint32_t FILLERS = BITS ? 2 : 1;  // arrivals at a landed tile's barrier, and at a grant
   static constexpr uint32_t TMEM_COLS = 512;
   __host__ __device__ static constexpr uint32_t s_col(int q) { return 128u * q; }
@@ -347,7 +348,6 @@ __global__ void __launch_bounds__(TilesCfg<D, BITS>::THREADS, 1)
     // their way while the one before it is turned into numbers. Keys that no row sees, and those of a missing page,
     // are zeros; a key whose scale is NaN, in K or in V, is NaN in K and zeros in V, so that rows that see it become NaN
     // and the tile's others do not.
-    regs_decrease<C::REGS_CODES>();
     if constexpr (BITS != 0) {
       auto fill_tiles = [&](auto is_v) {
         constexpr bool IS_V = decltype(is_v)::value;
@@ -440,6 +440,7 @@ __global__ void __launch_bounds__(TilesCfg<D, BITS>::THREADS, 1)
           return f;
         };
         auto write = [&](const T& b, const Factors& f, uint32_t tile, int batch) {
+          const bool late = batch * BO >= 4;  // keys 32 .. 63 of the half
 #pragma unroll
           for (int o = 0; o < BO; ++o) {
             const int octet = batch * BO + o, r = half * 64 + octet * 8 + token;  // row of the tile
@@ -447,7 +448,7 @@ __global__ void __launch_bounds__(TilesCfg<D, BITS>::THREADS, 1)
 #pragma unroll
             for (int j = 0; j < NG; ++j)
 #pragma unroll
-              for (int e = 0; e < (IS_V ? 2 : 1); ++e) sz[j][e] = __shfl_sync(0xffffffffu, f.f[octet >> 2][j], (octet & 3) * 8 + token + e);
+              for (int e = 0; e < (IS_V ? 2 : 1); ++e) sz[j][e] = __shfl_sync(0xffffffffu, late ? f.f[1][j] : f.f[0][j], (octet & 3) * 8 + token + e);
 #pragma unroll
             for (int z = 0; z < PIECES; ++z) {
               const int col = (chunk0 + 4 * z) * (128 / BITS);
@@ -513,25 +514,29 @@ __global__ void __launch_bounds__(TilesCfg<D, BITS>::THREADS, 1)
             }
           }
         };
-        // tile kt of the item, its params asked for before, its stage waited for by `free`; asks for the next one's
+        // tile kt of the item, its params and first batch asked for before, its stage waited for by `free`; asks
+        // for the next one's. (A loop, not unrolled: its instructions are to stay near, as the softmax's take their room.)
         Params params;
+        T now;
         int page = -1;
         auto begin = [&](int kt) {
           page = octet_page(kt);
           ask_params(params, kt, page);
+          ask(now, kt, page, 0);
         };
         auto tile = [&](int kt, bool more, uint32_t to, uint64_t* full, float2* info, auto free) {
-          T b[2];
-          ask(b[0], kt, page, 0);
           const int page_next = more ? octet_page(kt + 1) : -1;
           if (!free()) return false;
           const Factors f = factors(params, info);
-#pragma unroll
+#pragma unroll 1
           for (int i = 0; i < BATCHES; ++i) {
-            if (i + 1 < BATCHES) ask(b[(i + 1) & 1], kt, page, i + 1);
-            else if (more) ask_params(params, kt + 1, page_next);
-            write(b[i & 1], f, to, i);
+            T next;
+            const bool last = i + 1 == BATCHES;
+            ask(next, last ? kt + 1 : kt, last ? page_next : page, last ? 0 : i + 1);
+            write(now, f, to, i);
+            now = next;
           }
+          ask_params(params, kt + 1, page_next);
           page = page_next;
           fence_async_shared();
           __syncwarp();
@@ -583,7 +588,7 @@ __global__ void __launch_bounds__(TilesCfg<D, BITS>::THREADS, 1)
       else fill_tiles(std::true_type());
     }
   } else if (warp >= C::SOFTMAX_WARPS) {
-    regs_decrease<C::REGS_CONTROL>();
+    if constexpr (!BITS) regs_decrease<C::REGS_CONTROL>();
     if (BITS && warp == C::KQ_WARP) {
       // ---------------------------------------------------------- Q producer (the codes have their own)
       int j = 0;
@@ -774,7 +779,7 @@ __global__ void __launch_bounds__(TilesCfg<D, BITS>::THREADS, 1)
     }
   } else {
     // ------------------------------------------------------------ softmax / epilogue
-    regs_increase<C::REGS_SOFTMAX>();
+    if constexpr (!BITS) regs_increase<C::REGS_SOFTMAX>();
     const int q = warp / 4, wq = warp % 4;
     const int r_in = wq * 32 + lane;
     const uint32_t lane_addr = tmem + ((uint32_t)(wq * 32) << 16);
@@ -822,36 +827,36 @@ __global__ void __launch_bounds__(TilesCfg<D, BITS>::THREADS, 1)
           continue;
         }
         tc_fence_after();
-        float s[128];
-        {
-          uint32_t v0[32], v1[32], v2[32], v3[32];
-          tmem_ld32x4(s_addr, s_addr + 32, s_addr + 64, s_addr + 96, v0, v1, v2, v3);
-#pragma unroll
-          for (int kk = 0; kk < 32; ++kk) {
-            s[kk] = __uint_as_float(v0[kk]);
-            s[32 + kk] = __uint_as_float(v1[kk]);
-            s[64 + kk] = __uint_as_float(v2[kk]);
-            s[96 + kk] = __uint_as_float(v3[kk]);
-          }
-        }
-        const int c0 = (seg.k0 + t) * BLOCK_N;
-        if (c0 < in_lo || c0 + BLOCK_N - 1 > in_hi) mask_outside<128>(s, lo_i - c0, hi_i - c0);
         if constexpr (BITS != 0) {
           const float2 i0 = info_sh[g % TILE_INFO][0], i1 = info_sh[g % TILE_INFO][1];
           // (positive whatever the row: a masked score is -infinity times it)
           const float k_half[2] = {fmaxf(qf * i0.x, FLT_MIN), fmaxf(qf * i1.x, FLT_MIN)}, v_half[2] = {i0.y, i1.y};
+          const int c0 = (seg.k0 + t) * BLOCK_N;
+          const bool edge = c0 < in_lo || c0 + BLOCK_N - 1 > in_hi;
+          auto scores = [&](int h, float (&s)[64]) {
+            uint32_t v0[32], v1[32];
+            tmem_ld32x2(s_addr + h * 64, s_addr + h * 64 + 32, v0, v1);
+#pragma unroll
+            for (int kk = 0; kk < 32; ++kk) {
+              s[kk] = __uint_as_float(v0[kk]);
+              s[32 + kk] = __uint_as_float(v1[kk]);
+            }
+            if (edge) mask_outside<64>(s, lo_i - c0 - 64 * h, hi_i - c0 - 64 * h);
+          };
           float mh[2];
 #pragma unroll
           for (int h = 0; h < 2; ++h) {
+            float s[64];
+            scores(h, s);
             float mx[4];
 #pragma unroll
-            for (int kk = 0; kk < 4; ++kk) mx[kk] = max3(s[64 * h + kk], s[64 * h + 4 + kk], s[64 * h + 8 + kk]);
+            for (int kk = 0; kk < 4; ++kk) mx[kk] = max3(s[kk], s[4 + kk], s[8 + kk]);
 #pragma unroll
             for (int c = 12; c < 60; c += 8)
 #pragma unroll
-              for (int kk = 0; kk < 4; ++kk) mx[kk] = max3(mx[kk], s[64 * h + c + kk], s[64 * h + c + 4 + kk]);
+              for (int kk = 0; kk < 4; ++kk) mx[kk] = max3(mx[kk], s[c + kk], s[c + 4 + kk]);
 #pragma unroll
-            for (int kk = 0; kk < 4; ++kk) mx[kk] = fmaxf(mx[kk], s[64 * h + 60 + kk]);
+            for (int kk = 0; kk < 4; ++kk) mx[kk] = fmaxf(mx[kk], s[60 + kk]);
             mh[h] = fmaxf(max3(mx[0], mx[1], mx[2]), mx[3]) * k_half[h];
           }
           const float mt = fmaxf(mh[0], mh[1]), v_top = fmaxf(v_half[0], v_half[1]);
@@ -880,10 +885,12 @@ __global__ void __launch_bounds__(TilesCfg<D, BITS>::THREADS, 1)
             const float up = fmaxf(v_half[h] - v_ref, -60.f);  // (far below that, P is 0 in fp16)
             const float2 by = make_float2(k_half[h], k_half[h]), off = make_float2(up - m, up - m);
             float2 ls[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
+            float s[64];
+            scores(h, s);
             uint32_t pk[32];
 #pragma unroll
             for (int kk = 0; kk < 32; ++kk) {
-              const float2 x = fma2(make_float2(s[h * 64 + 2 * kk], s[h * 64 + 2 * kk + 1]), by, off);
+              const float2 x = fma2(make_float2(s[2 * kk], s[2 * kk + 1]), by, off);
               const float2 pp = make_float2(ex2(x.x), ex2(x.y));
               ls[kk & 1] = add2(ls[kk & 1], pp);
               pk[kk] = pack_half2(pp.x, pp.y);
@@ -892,6 +899,20 @@ __global__ void __launch_bounds__(TilesCfg<D, BITS>::THREADS, 1)
             l = fmaf((ls[0].x + ls[1].x) + (ls[0].y + ls[1].y), ex2(-up), l);
           }
         } else {
+        float s[128];
+        {
+          uint32_t v0[32], v1[32], v2[32], v3[32];
+          tmem_ld32x4(s_addr, s_addr + 32, s_addr + 64, s_addr + 96, v0, v1, v2, v3);
+#pragma unroll
+          for (int kk = 0; kk < 32; ++kk) {
+            s[kk] = __uint_as_float(v0[kk]);
+            s[32 + kk] = __uint_as_float(v1[kk]);
+            s[64 + kk] = __uint_as_float(v2[kk]);
+            s[96 + kk] = __uint_as_float(v3[kk]);
+          }
+        }
+        const int c0 = (seg.k0 + t) * BLOCK_N;
+        if (c0 < in_lo || c0 + BLOCK_N - 1 > in_hi) mask_outside<128>(s, lo_i - c0, hi_i - c0);
         float mx[8];
 #pragma unroll
         for (int kk = 0; kk < 8; ++kk) mx[kk] = max3(s[kk], s[8 + kk], s[16 + kk]);
