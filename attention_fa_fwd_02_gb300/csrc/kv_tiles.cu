@@ -203,7 +203,7 @@ template <int BITS, int D>
 struct CodeBatch {
   static constexpr int CH = D * BITS / 128;            // chunks of a key
   static constexpr int PIECES = CH >= 4 ? CH / 4 : 1;  // of an octet, for each lane
-  static constexpr int BO = 4 / PIECES;                // octets of a batch
+  static constexpr int BO = 2 / PIECES;                // octets of a batch
   uint4 w[BO][PIECES];
 };
 constexpr int TILE_INFO = 8;  // tiles whose powers of two are kept: K's codes are at most five tiles ahead of the softmax
@@ -448,7 +448,7 @@ __global__ void __launch_bounds__(TilesCfg<D, BITS>::THREADS, 1)
 #pragma unroll
             for (int j = 0; j < NG; ++j)
 #pragma unroll
-              for (int e = 0; e < (IS_V ? 2 : 1); ++e) sz[j][e] = __shfl_sync(0xffffffffu, late ? f.f[1][j] : f.f[0][j], (octet & 3) * 8 + token + e);
+              for (int e = 0; e < (IS_V ? 2 : 1); ++e) sz[j][e] = __shfl_sync(0xffffffffu, late ? f.f[1][j] : f.f[0][j], (octet * 8 & 31) + token + e);
 #pragma unroll
             for (int z = 0; z < PIECES; ++z) {
               const int col = (chunk0 + 4 * z) * (128 / BITS);
@@ -516,13 +516,16 @@ __global__ void __launch_bounds__(TilesCfg<D, BITS>::THREADS, 1)
         };
         // tile kt of the item, its params and first batch asked for before, its stage waited for by `free`; asks
         // for the next one's. (A loop, not unrolled: its instructions are to stay near, as the softmax's take their room.)
+        // Two batches are on their way.
         Params params;
-        T now;
+        T now, soon;
         int page = -1;
+        static_assert(BATCHES >= 2, "two batches of a tile");
         auto begin = [&](int kt) {
           page = octet_page(kt);
           ask_params(params, kt, page);
           ask(now, kt, page, 0);
+          ask(soon, kt, page, 1);
         };
         auto tile = [&](int kt, bool more, uint32_t to, uint64_t* full, float2* info, auto free) {
           const int page_next = more ? octet_page(kt + 1) : -1;
@@ -530,11 +533,12 @@ __global__ void __launch_bounds__(TilesCfg<D, BITS>::THREADS, 1)
           const Factors f = factors(params, info);
 #pragma unroll 1
           for (int i = 0; i < BATCHES; ++i) {
-            T next;
-            const bool last = i + 1 == BATCHES;
-            ask(next, last ? kt + 1 : kt, last ? page_next : page, last ? 0 : i + 1);
+            T later;
+            const bool over = i + 2 >= BATCHES;
+            ask(later, over ? kt + 1 : kt, over ? page_next : page, over ? i + 2 - BATCHES : i + 2);
             write(now, f, to, i);
-            now = next;
+            now = soon;
+            soon = later;
           }
           ask_params(params, kt + 1, page_next);
           page = page_next;
@@ -843,8 +847,9 @@ __global__ void __launch_bounds__(TilesCfg<D, BITS>::THREADS, 1)
             }
             if (edge) mask_outside<64>(s, lo_i - c0 - 64 * h, hi_i - c0 - 64 * h);
           };
-          float mh[2];
-#pragma unroll
+          // (halves in loops: see the code warps)
+          float mt = -INFINITY;
+#pragma unroll 1
           for (int h = 0; h < 2; ++h) {
             float s[64];
             scores(h, s);
@@ -857,9 +862,9 @@ __global__ void __launch_bounds__(TilesCfg<D, BITS>::THREADS, 1)
               for (int kk = 0; kk < 4; ++kk) mx[kk] = max3(mx[kk], s[c + kk], s[c + 4 + kk]);
 #pragma unroll
             for (int kk = 0; kk < 4; ++kk) mx[kk] = fmaxf(mx[kk], s[60 + kk]);
-            mh[h] = fmaxf(max3(mx[0], mx[1], mx[2]), mx[3]) * k_half[h];
+            mt = fmaxf(mt, fmaxf(max3(mx[0], mx[1], mx[2]), mx[3]) * (h ? k_half[1] : k_half[0]));
           }
-          const float mt = fmaxf(mh[0], mh[1]), v_top = fmaxf(v_half[0], v_half[1]);
+          const float v_top = fmaxf(v_half[0], v_half[1]);
           // (2^8 of a probability and 2^6 of V's exponent beyond v_ref: P stays below 2^15)
           const bool v_grow = t == 0 || v_top > v_ref + 6.f;
           if (__any_sync(0xffffffffu, (r_in < rows && mt > m + RESCALE_THRESHOLD) || v_grow)) {
@@ -880,10 +885,11 @@ __global__ void __launch_bounds__(TilesCfg<D, BITS>::THREADS, 1)
             m = m_new;
             v_ref = v_new;
           }
-#pragma unroll
+#pragma unroll 1
           for (int h = 0; h < 2; ++h) {
-            const float up = fmaxf(v_half[h] - v_ref, -60.f);  // (far below that, P is 0 in fp16)
-            const float2 by = make_float2(k_half[h], k_half[h]), off = make_float2(up - m, up - m);
+            const float up = fmaxf((h ? v_half[1] : v_half[0]) - v_ref, -60.f);  // (far below that, P is 0 in fp16)
+            const float kh = h ? k_half[1] : k_half[0];
+            const float2 by = make_float2(kh, kh), off = make_float2(up - m, up - m);
             float2 ls[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
             float s[64];
             scores(h, s);
