@@ -80,13 +80,16 @@ struct TilesCfg {
   static constexpr uint32_t CB_BYTES = 128u * 128u;       // one block of a 128-row tile
   static constexpr uint32_t TILE_BYTES = NCB * CB_BYTES;
   static constexpr int KST = D == 128 ? 2 : 3;
-  static constexpr int VST = 3;
+  static constexpr int VST = BITS ? 2 : 3;
   static constexpr uint32_t EPI_BOX = 32u * 128u;         // a warp's staging: 32 rows x 128 bytes
   static constexpr uint32_t V_STAGE = std::max(TILE_BYTES, 4 * NQ * EPI_BOX);
   static constexpr uint32_t Q_OFF = 0;
   static constexpr uint32_t K_OFF = Q_OFF + NQ * TILE_BYTES;
   static constexpr uint32_t V_OFF = K_OFF + KST * TILE_BYTES;
-  static constexpr uint32_t SMEM = V_OFF + VST * V_STAGE + 1024;
+  static constexpr uint32_t OCTET = D * BITS;              // bytes of eight keys' codes
+  static constexpr uint32_t RING = 8 * OCTET;              // of a code warp: eight octets
+  static constexpr uint32_t CODES_OFF = V_OFF + VST * V_STAGE;
+  static constexpr uint32_t SMEM = CODES_OFF + 4 * RING + 1024;
   static constexpr int SOFTMAX_WARPS = 8, MMA_WARP = 8, KQ_WARP = 9, V_WARP = 10, RELAY_WARP = 11;
   static constexpr uint32_t RELAY_BAR = 3;  // named barrier (1 + q: P_q written)
   static constexpr int CODE_WARP = 12;  // codes: two warps for K's tiles, two for V's, half a tile each
@@ -197,15 +200,10 @@ __device__ __forceinline__ void store_rows(uint32_t t_addr, bool have, float mul
 }
 
 // ---- tiles of codes
-// A batch of a warp's part of a tile: BO octets of keys, 16-byte pieces of codes for each lane. K: the lane's piece is
-// chunk `chunk` of token lane % 8. V: half a pair's chunk, both tokens'.
-template <int BITS, int D>
-struct CodeBatch {
-  static constexpr int CH = D * BITS / 128;            // chunks of a key
-  static constexpr int PIECES = CH >= 4 ? CH / 4 : 1;  // of an octet, for each lane
-  static constexpr int BO = 2 / PIECES;                // octets of a batch
-  uint4 w[BO][PIECES];
-};
+// 16 bytes into shared memory, or zeros
+__device__ __forceinline__ void cp_piece(uint32_t dst, const void* src, bool take) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(take ? 16 : 0) : "memory");
+}
 constexpr int TILE_INFO = 8;  // tiles whose powers of two are kept: K's codes are at most five tiles ahead of the softmax
 
 // q as fp16, each row times a power of two that brings its largest value to 2^14 (exactly, but for what is 2^-28 of
@@ -351,13 +349,15 @@ __global__ void __launch_bounds__(TilesCfg<D, BITS>::THREADS, 1)
     if constexpr (BITS != 0) {
       auto fill_tiles = [&](auto is_v) {
         constexpr bool IS_V = decltype(is_v)::value;
-        using T = CodeBatch<BITS, D>;
-        constexpr int BO = T::BO, PIECES = T::PIECES, BATCHES = 8 / BO, NG = D / 64;
+        constexpr int CH = D * BITS / 128, PIECES = CH >= 4 ? CH / 4 : 1;  // chunks of a key; a lane's pieces of an octet
+        constexpr int NG = D / 64;
         constexpr float CENTRE = BITS == 4 ? 8.f : 128.f, STEPS = BITS == 4 ? 15.f : 255.f;
         const int half = (warp - C::CODE_WARP) & 1;  // of the tile
         const int chunks = a.qc.chunks, ng = a.qc.groups;
         const uint8_t* const base = IS_V ? a.qc.V : a.qc.K;
-        // the lane's piece: 16 bytes of an octet's 128 a chunk
+        const uint32_t ring = sbase + C::CODES_OFF + (warp - C::CODE_WARP) * C::RING;
+        // the lane's piece, 16 bytes of an octet's 128 a chunk. K: chunk chunk0 of token lane % 8. V: half a pair's
+        // chunk, both tokens'.
         const int chunk0 = lane >> 3;
         const int token = IS_V ? 2 * (lane & 3) : lane & 7, side = (lane >> 2) & 1;
         const int at = chunk0 * 128 + (IS_V ? (lane & 3) * 32 + side * 16 : (lane & 7) * 16);
@@ -388,16 +388,16 @@ __global__ void __launch_bounds__(TilesCfg<D, BITS>::THREADS, 1)
             }
           }
         };
-        auto ask = [&](T& b, int kt, int page, int batch) {
+        auto ask = [&](int kt, int page, int octet) {  // (each piece read by the lane that asked for it)
+          const int p = __shfl_sync(0xffffffffu, page, octet);
+          const int t = (kt * BLOCK_N + half * 64 + octet * 8) & (a.c.page_size - 1);
+          const uint8_t* const from = base + max(p, 0) * a.qc.page + seg.head * a.qc.head + t * chunks * 16;
 #pragma unroll
-          for (int o = 0; o < BO; ++o) {
-            const int p = __shfl_sync(0xffffffffu, page, batch * BO + o);
-            const int t = (kt * BLOCK_N + half * 64 + (batch * BO + o) * 8) & (a.c.page_size - 1);
-            const uint8_t* const from = base + p * a.qc.page + seg.head * a.qc.head + t * chunks * 16 + at;
-#pragma unroll
-            for (int z = 0; z < PIECES; ++z)
-              b.w[o][z] = p >= 0 && chunk0 + 4 * z < chunks ? __ldg(reinterpret_cast<const uint4*>(from + z * 512)) : make_uint4(0, 0, 0, 0);
+          for (int z = 0; z < PIECES; ++z) {
+            const bool take = p >= 0 && chunk0 + 4 * z < chunks;
+            if (chunk0 + 4 * z < CH) cp_piece(ring + octet * C::OCTET + at + z * 512, take ? from + at + z * 512 : base, take);
           }
+          asm volatile("cp.async.commit_group;" ::: "memory");
         };
         // scale (low) and z' (high) of keys lane and lane + 32, as fp16 times the half's power of two
         struct Factors {
@@ -439,11 +439,9 @@ __global__ void __launch_bounds__(TilesCfg<D, BITS>::THREADS, 1)
           }
           return f;
         };
-        auto write = [&](const T& b, const Factors& f, uint32_t tile, int batch) {
-          const bool late = batch * BO >= 4;  // keys 32 .. 63 of the half
-#pragma unroll
-          for (int o = 0; o < BO; ++o) {
-            const int octet = batch * BO + o, r = half * 64 + octet * 8 + token;  // row of the tile
+        auto write = [&](const Factors& f, uint32_t tile, int octet) {
+            const bool late = octet >= 4;  // keys 32 .. 63 of the half
+            const int r = half * 64 + octet * 8 + token;  // row of the tile
             uint32_t sz[NG][IS_V ? 2 : 1];
 #pragma unroll
             for (int j = 0; j < NG; ++j)
@@ -460,7 +458,8 @@ __global__ void __launch_bounds__(TilesCfg<D, BITS>::THREADS, 1)
               const bool upper = NG > 1 && col >= 64;
               const uint32_t p0 = upper ? sz[NG - 1][0] : sz[0][0], p1 = IS_V ? (upper ? sz[NG - 1][IS_V] : sz[0][IS_V]) : p0;
               const uint32_t s = __byte_perm(p0, p1, 0x5410), zz = __byte_perm(p0, p1, 0x7632);
-              const uint32_t words[4] = {b.w[o][z].x, b.w[o][z].y, b.w[o][z].z, b.w[o][z].w};
+              const float4 piece = ld_shared_v4(ring + octet * C::OCTET + at + z * 512);
+              const uint32_t words[4] = {__float_as_uint(piece.x), __float_as_uint(piece.y), __float_as_uint(piece.z), __float_as_uint(piece.w)};
               if constexpr (BITS == 4) {
                 const uint32_t s16 = q_fma2(s, 0x2c002c00u, 0u);  // s / 16
                 // the four pairs of a word: K: columns n and n + 4; V: column n of both tokens
@@ -512,36 +511,34 @@ __global__ void __launch_bounds__(TilesCfg<D, BITS>::THREADS, 1)
                 }
               }
             }
-          }
         };
-        // tile kt of the item, its params and first batch asked for before, its stage waited for by `free`; asks
-        // for the next one's. (A loop, not unrolled: its instructions are to stay near, as the softmax's take their room.)
-        // Two batches are on their way.
-        Params params;
-        T now, soon;
-        int page = -1;
-        static_assert(BATCHES >= 2, "two batches of a tile");
-        auto begin = [&](int kt) {
+        // tile kt of the item (`left`: and how many after it), its params and first octets asked for before, its stage
+        // waited for by `free`; asks for the next one's, and for the pages of the one after that: nothing of it waits for
+        // a round trip to L2. (A loop, not unrolled, here and in the softmax: the warps of an SM
+        // run three programs at once, and the whole of it unrolled spent its time waiting for instructions, 1097 us
+        // where this takes a third.)
+        Params params, params_next;
+        int page = -1, page_next = -1;
+        auto begin = [&](int kt, int left) {
           page = octet_page(kt);
+          page_next = left > 0 ? octet_page(kt + 1) : -1;
           ask_params(params, kt, page);
-          ask(now, kt, page, 0);
-          ask(soon, kt, page, 1);
+          for (int i = 0; i < 8; ++i) ask(kt, page, i);
         };
-        auto tile = [&](int kt, bool more, uint32_t to, uint64_t* full, float2* info, auto free) {
-          const int page_next = more ? octet_page(kt + 1) : -1;
+        auto tile = [&](int kt, int left, uint32_t to, uint64_t* full, float2* info, auto free) {
+          ask_params(params_next, kt + 1, page_next);
+          const int page_after = left > 1 ? octet_page(kt + 2) : -1;
           if (!free()) return false;
           const Factors f = factors(params, info);
 #pragma unroll 1
-          for (int i = 0; i < BATCHES; ++i) {
-            T later;
-            const bool over = i + 2 >= BATCHES;
-            ask(later, over ? kt + 1 : kt, over ? page_next : page, over ? i + 2 - BATCHES : i + 2);
-            write(now, f, to, i);
-            now = soon;
-            soon = later;
+          for (int i = 0; i < 8; ++i) {
+            asm volatile("cp.async.wait_group 7;" ::: "memory");
+            write(f, to, i);
+            ask(kt + 1, page_next, i);
           }
-          ask_params(params, kt + 1, page_next);
+          params = params_next;
           page = page_next;
+          page_next = page_after;
           fence_async_shared();
           __syncwarp();
           if (lane == 0) mbar_arrive(full);
@@ -551,10 +548,10 @@ __global__ void __launch_bounds__(TilesCfg<D, BITS>::THREADS, 1)
         if constexpr (!IS_V) {
           int g = 0;
           while (ok && next()) {
-            if (seg.n > 0) begin(seg.k0);
+            if (seg.n > 0) begin(seg.k0, seg.n - 1);
             for (int t = 0; ok && t < seg.n; ++t, ++g) {
               const int ks = g % KST;
-              ok = tile(seg.k0 + t, t + 1 < seg.n, sK(ks), &bar_kfull[ks], &info_sh[g % TILE_INFO][half],
+              ok = tile(seg.k0 + t, seg.n - 1 - t, sK(ks), &bar_kfull[ks], &info_sh[g % TILE_INFO][half],
                         [&] { return __all_sync(0xffffffffu, wait_free(&bar_kempty[ks], ((g / KST) & 1) ^ 1)) != 0; });
             }
           }
@@ -573,9 +570,9 @@ __global__ void __launch_bounds__(TilesCfg<D, BITS>::THREADS, 1)
             return true;
           };
           while (ok && next()) {
-            if (seg.n > 0) begin(seg.k0);
+            if (seg.n > 0) begin(seg.k0, seg.n - 1);
             for (int t = 0; ok && t < seg.n; ++t, ++pos)
-              ok = tile(seg.k0 + t, t + 1 < seg.n, sV(pos % VST), &bar_vfull[pos % VST], nullptr,
+              ok = tile(seg.k0 + t, seg.n - 1 - t, sV(pos % VST), &bar_vfull[pos % VST], nullptr,
                         [&] { return pos < (uint32_t)VST || wait_release(pos - VST); });
             if (!ok) break;
             if (pos >= (uint32_t)VST && !(ok = wait_release(pos - VST))) break;
@@ -590,6 +587,7 @@ __global__ void __launch_bounds__(TilesCfg<D, BITS>::THREADS, 1)
       };
       if (warp < C::CODE_WARP + 2) fill_tiles(std::false_type());
       else fill_tiles(std::true_type());
+      asm volatile("cp.async.wait_all;" ::: "memory");
     }
   } else if (warp >= C::SOFTMAX_WARPS) {
     if constexpr (!BITS) regs_decrease<C::REGS_CONTROL>();
@@ -837,32 +835,28 @@ __global__ void __launch_bounds__(TilesCfg<D, BITS>::THREADS, 1)
           const float k_half[2] = {fmaxf(qf * i0.x, FLT_MIN), fmaxf(qf * i1.x, FLT_MIN)}, v_half[2] = {i0.y, i1.y};
           const int c0 = (seg.k0 + t) * BLOCK_N;
           const bool edge = c0 < in_lo || c0 + BLOCK_N - 1 > in_hi;
-          auto scores = [&](int h, float (&s)[64]) {
-            uint32_t v0[32], v1[32];
-            tmem_ld32x2(s_addr + h * 64, s_addr + h * 64 + 32, v0, v1);
+          auto scores = [&](int c, float (&s)[32]) {  // of 32 keys
+            uint32_t v[32];
+            tmem_ld32(s_addr + c * 32, v);
 #pragma unroll
-            for (int kk = 0; kk < 32; ++kk) {
-              s[kk] = __uint_as_float(v0[kk]);
-              s[32 + kk] = __uint_as_float(v1[kk]);
-            }
-            if (edge) mask_outside<64>(s, lo_i - c0 - 64 * h, hi_i - c0 - 64 * h);
+            for (int kk = 0; kk < 32; ++kk) s[kk] = __uint_as_float(v[kk]);
+            if (edge) mask_outside<32>(s, lo_i - c0 - 32 * c, hi_i - c0 - 32 * c);
           };
-          // (halves in loops: see the code warps)
           float mt = -INFINITY;
 #pragma unroll 1
-          for (int h = 0; h < 2; ++h) {
-            float s[64];
-            scores(h, s);
+          for (int c = 0; c < 4; ++c) {
+            float s[32];
+            scores(c, s);
             float mx[4];
 #pragma unroll
             for (int kk = 0; kk < 4; ++kk) mx[kk] = max3(s[kk], s[4 + kk], s[8 + kk]);
 #pragma unroll
-            for (int c = 12; c < 60; c += 8)
+            for (int k = 12; k < 28; k += 8)
 #pragma unroll
-              for (int kk = 0; kk < 4; ++kk) mx[kk] = max3(mx[kk], s[c + kk], s[c + 4 + kk]);
+              for (int kk = 0; kk < 4; ++kk) mx[kk] = max3(mx[kk], s[k + kk], s[k + 4 + kk]);
 #pragma unroll
-            for (int kk = 0; kk < 4; ++kk) mx[kk] = fmaxf(mx[kk], s[60 + kk]);
-            mt = fmaxf(mt, fmaxf(max3(mx[0], mx[1], mx[2]), mx[3]) * (h ? k_half[1] : k_half[0]));
+            for (int kk = 0; kk < 4; ++kk) mx[kk] = fmaxf(mx[kk], s[28 + kk]);
+            mt = fmaxf(mt, fmaxf(max3(mx[0], mx[1], mx[2]), mx[3]) * (c < 2 ? k_half[0] : k_half[1]));
           }
           const float v_top = fmaxf(v_half[0], v_half[1]);
           // (2^8 of a probability and 2^6 of V's exponent beyond v_ref: P stays below 2^15)
@@ -886,22 +880,22 @@ __global__ void __launch_bounds__(TilesCfg<D, BITS>::THREADS, 1)
             v_ref = v_new;
           }
 #pragma unroll 1
-          for (int h = 0; h < 2; ++h) {
-            const float up = fmaxf((h ? v_half[1] : v_half[0]) - v_ref, -60.f);  // (far below that, P is 0 in fp16)
-            const float kh = h ? k_half[1] : k_half[0];
+          for (int c = 0; c < 4; ++c) {
+            const float up = fmaxf((c < 2 ? v_half[0] : v_half[1]) - v_ref, -60.f);  // (far below that, P is 0 in fp16)
+            const float kh = c < 2 ? k_half[0] : k_half[1];
             const float2 by = make_float2(kh, kh), off = make_float2(up - m, up - m);
             float2 ls[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
-            float s[64];
-            scores(h, s);
-            uint32_t pk[32];
+            float s[32];
+            scores(c, s);
+            uint32_t pk[16];
 #pragma unroll
-            for (int kk = 0; kk < 32; ++kk) {
+            for (int kk = 0; kk < 16; ++kk) {
               const float2 x = fma2(make_float2(s[2 * kk], s[2 * kk + 1]), by, off);
               const float2 pp = make_float2(ex2(x.x), ex2(x.y));
               ls[kk & 1] = add2(ls[kk & 1], pp);
               pk[kk] = pack_half2(pp.x, pp.y);
             }
-            tmem_st32(s_addr + h * 32, pk);
+            tmem_st16(s_addr + c * 16, pk);
             l = fmaf((ls[0].x + ls[1].x) + (ls[0].y + ls[1].y), ex2(-up), l);
           }
         } else {
