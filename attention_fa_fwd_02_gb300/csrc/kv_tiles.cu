@@ -207,11 +207,12 @@ __device__ __forceinline__ void cp_piece(uint32_t dst, const void* src, bool tak
 constexpr int TILE_INFO = 8;  // tiles whose powers of two are kept: K's codes are at most five tiles ahead of the softmax
 
 // q as fp16, each row times a power of two that brings its largest value to 2^14 (exactly, but for what is 2^-28 of
-// that), and what undoes it, times the softmax scale. Sixteen lanes to a row. A row with NaN or infinity becomes NaN.
+// that), and what undoes it, times the softmax scale; `pairs`: each eight columns in the order 0 4 1 5 2 6 3 7, which is
+// that of K's 4-bit codes. Sixteen lanes to a row. A row with NaN or infinity becomes NaN.
 constexpr int QROWS_THREADS = 256;
 __global__ void __launch_bounds__(QROWS_THREADS) qattend_q_kernel(const __nv_bfloat16* q, long long q_token, long long q_head,
-                                                                  int rows, Div heads, int D, float sl2, uint16_t* out,
-                                                                  float* factor) {
+                                                                  int rows, Div heads, int D, float sl2, bool pairs,
+                                                                  uint16_t* out, float* factor) {
   grid_launch_dependents();
   const int lane = threadIdx.x & 15, row = blockIdx.x * (QROWS_THREADS / 16) + threadIdx.x / 16;
   const int token = heads.of(min(row, rows - 1)), col = lane * 8;
@@ -239,9 +240,13 @@ __global__ void __launch_bounds__(QROWS_THREADS) qattend_q_kernel(const __nv_bfl
   const int e = min(max(q_exponent(top), -60), 127);
   const float by = fine ? q_pow2(14 - e) : __int_as_float(0x7fffffff);
   if (row >= rows) return;
-  if (col < D)
-    *reinterpret_cast<uint4*>(out + (size_t)row * D + col) = make_uint4(q_half2(x[0] * by, x[1] * by), q_half2(x[2] * by, x[3] * by),
-                                                                        q_half2(x[4] * by, x[5] * by), q_half2(x[6] * by, x[7] * by));
+  if (col < D) {
+    uint32_t y[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      y[i] = q_half2((pairs ? x[i] : x[2 * i]) * by, (pairs ? x[i + 4] : x[2 * i + 1]) * by);
+    *reinterpret_cast<uint4*>(out + (size_t)row * D + col) = make_uint4(y[0], y[1], y[2], y[3]);
+  }
   if (lane == 0) factor[row] = sl2 * q_pow2(e - 14);
 }
 
@@ -474,8 +479,7 @@ __global__ void __launch_bounds__(TilesCfg<D, BITS>::THREADS, 1)
                   for (int i = 0; i < 4; ++i) {
                     uint32_t x[4];
                     pairs(words[i], x);
-                    put(0, col / 8 + i, __byte_perm(x[0], x[1], 0x5410), __byte_perm(x[2], x[3], 0x5410),
-                        __byte_perm(x[0], x[1], 0x7632), __byte_perm(x[2], x[3], 0x7632));
+                    put(0, col / 8 + i, x[0], x[1], x[2], x[3]);  // (columns 0 4 1 5 2 6 3 7, as q's are laid)
                   }
                 } else {
 #pragma unroll
@@ -1118,7 +1122,7 @@ fa_status launch_qattend_tiles(const void* q, void* O, float* LSE, const int* cu
   if (st == FA_OK) {
     host::KernelTimer t("qattend_q", s);
     st = launch(qattend_q_kernel, (rows + QROWS_THREADS / 16 - 1) / (QROWS_THREADS / 16), QROWS_THREADS, 0, s,
-                static_cast<const __nv_bfloat16*>(q), p.q_token, p.q_head, rows, div_by(p.H), D, a.sl2,
+                static_cast<const __nv_bfloat16*>(q), p.q_token, p.q_head, rows, div_by(p.H), D, a.sl2, qc.bits == 4,
                 static_cast<uint16_t*>(w), qf);
   }
   // (no map of K and V is looked at)
