@@ -87,18 +87,17 @@ struct TilesCfg {
   static constexpr uint32_t K_OFF = Q_OFF + NQ * TILE_BYTES;
   static constexpr uint32_t V_OFF = K_OFF + KST * TILE_BYTES;
   static constexpr uint32_t OCTET = D * BITS;              // bytes of eight keys' codes
-  static constexpr uint32_t RING = 8 * OCTET;              // of a code warp: eight octets
+  static constexpr uint32_t RING = 4 * OCTET;              // of a code warp: its octets of a tile
   static constexpr uint32_t CODES_OFF = V_OFF + VST * V_STAGE;
-  static constexpr uint32_t SMEM = CODES_OFF + 4 * RING + 1024;
+  static constexpr uint32_t SMEM = CODES_OFF + 8 * RING + 1024;
   static constexpr int SOFTMAX_WARPS = 8, MMA_WARP = 8, KQ_WARP = 9, V_WARP = 10, RELAY_WARP = 11;
   static constexpr uint32_t RELAY_BAR = 3;  // named barrier (1 + q: P_q written)
-  static constexpr int CODE_WARP = 12;  // codes: two warps for K's tiles, two for V's, half a tile each
-  static constexpr int THREADS = BITS ? 512 : 384;
-  // (codes: every warp keeps the 128 registers that 512 threads leave; the softmax reads its scores twice instead of
-  // holding them all)
+  static constexpr int CODE_WARP = 12;  // codes: four warps for K's tiles, four for V's, a quarter of a tile each
+  static constexpr int THREADS = BITS ? 640 : 384;
+  // (codes: every warp keeps the 96 registers that 640 threads leave; the softmax takes its scores 32 at a time)
   static constexpr uint32_t REGS_SOFTMAX = 216, REGS_CONTROL = 64;
   static_assert(BITS || 2 * 128 * REGS_SOFTMAX + 128 * REGS_CONTROL <= 384 * 168, "register split exceeds the launch allocation");
-  static constexpr uint32_t FILLERS = BITS ? 2 : 1;  // arrivals at a landed tile's barrier, and at a grant
+  static constexpr uint32_t FILLERS = BITS ? 4 : 1;  // arrivals at a landed tile's barrier, and at a grant
   static constexpr uint32_t TMEM_COLS = 512;
   __host__ __device__ static constexpr uint32_t s_col(int q) { return 128u * q; }
   __host__ __device__ static constexpr uint32_t o_col(int q) { return 256u + (uint32_t)D * q; }
@@ -262,7 +261,7 @@ __global__ void __launch_bounds__(TilesCfg<D, BITS>::THREADS, 1)
       bar_vempty[VST], bar_grant[NQ], bar_s[NQ], bar_o[NQ], bar_join, bar_drain;
   __shared__ uint32_t tmem_base_sh;
   __shared__ int abort_sh, stuck_sh;
-  __shared__ float2 info_sh[BITS ? TILE_INFO : 1][2];  // codes: of each half of a tile, K's power of two and V's exponent
+  __shared__ float2 info_sh[BITS ? TILE_INFO : 1][4];  // codes: of each quarter of a tile, K's power of two and V's exponent
   __shared__ PlanShared<C::THREADS, 1> plan;
   grid_launch_dependents();
   const int warp = warp_id(), lane = lane_id();
@@ -345,10 +344,10 @@ __global__ void __launch_bounds__(TilesCfg<D, BITS>::THREADS, 1)
 
   if (BITS && warp >= C::CODE_WARP) {
     // ------------------------------------------------------------ codes of K, of V
-    // Each of two warps writes 64 keys of every tile, as the copies of bf16 pages would have laid them down, in fp16:
-    // times a power of two that keeps the largest of the 64 keys' values just below 2^8 (K: undone in the scores) or
-    // 2^7 (V: undone in the probabilities); 2^-12 of a value, or 2^-32 of the largest, is rounded off. A batch's loads are on
-    // their way while the one before it is turned into numbers. Keys that no row sees, and those of a missing page,
+    // Each of four warps writes 32 keys of every tile, as the copies of bf16 pages would have laid them down, in fp16:
+    // times a power of two that keeps the largest of the 32 keys' values just below 2^8 (K: undone in the scores) or
+    // 2^7 (V: undone in the probabilities); 2^-12 of a value, or 2^-32 of the largest, is rounded off. A tile's codes are
+    // on their way while the one before it is turned into numbers. Keys that no row sees, and those of a missing page,
     // are zeros; a key whose scale is NaN, in K or in V, is NaN in K and zeros in V, so that rows that see it become NaN
     // and the tile's others do not.
     if constexpr (BITS != 0) {
@@ -357,7 +356,7 @@ __global__ void __launch_bounds__(TilesCfg<D, BITS>::THREADS, 1)
         constexpr int CH = D * BITS / 128, PIECES = CH >= 4 ? CH / 4 : 1;  // chunks of a key; a lane's pieces of an octet
         constexpr int NG = D / 64;
         constexpr float CENTRE = BITS == 4 ? 8.f : 128.f, STEPS = BITS == 4 ? 15.f : 255.f;
-        const int half = (warp - C::CODE_WARP) & 1;  // of the tile
+        const int quarter = (warp - C::CODE_WARP) & 3;  // of the tile
         const int chunks = a.qc.chunks, ng = a.qc.groups;
         const uint8_t* const base = IS_V ? a.qc.V : a.qc.K;
         const uint32_t ring = sbase + C::CODES_OFF + (warp - C::CODE_WARP) * C::RING;
@@ -366,36 +365,32 @@ __global__ void __launch_bounds__(TilesCfg<D, BITS>::THREADS, 1)
         const int chunk0 = lane >> 3;
         const int token = IS_V ? 2 * (lane & 3) : lane & 7, side = (lane >> 2) & 1;
         const int at = chunk0 * 128 + (IS_V ? (lane & 3) * 32 + side * 16 : (lane & 7) * 16);
-        auto octet_page = [&](int kt) {  // of octet lane % 8 of the warp's half: -1: unseen or missing
-          const int j = kt * BLOCK_N + half * 64 + (lane & 7) * 8;
+        auto octet_page = [&](int kt) {  // of octet lane / 8 of the warp's quarter: -1: unseen or missing
+          const int j = kt * BLOCK_N + quarter * 32 + (lane & ~7);
           if (j >= seg.x.hi || j + 8 <= seg.x.lo) return -1;
           const int p = a.c.table[(long long)seg.s.slot * a.c.table_stride + (j >> a.shift)];
           if ((unsigned)p < (unsigned)a.c.num_pages) return p;
           raise(a.c.status, FAKV_BAD_PAGE);
           return -1;
         };
-        // params of keys lane and lane + 32 of the half, K's and V's (V's warps: V's)
+        // params of key `lane` of the quarter, K's and V's (V's warps: V's)
         struct Params {
-          uint32_t k[2][NG], v[2][NG];
+          uint32_t k[NG], v[NG];
         };
         auto ask_params = [&](Params& b, int kt, int page) {
+          const int key = kt * BLOCK_N + quarter * 32 + lane;
+          const long long off = page * a.qc.page + seg.head * a.qc.head + a.qc.params + (key & (a.c.page_size - 1)) * ng * 4;
+          const bool in = page >= 0 && key >= seg.x.lo && key < seg.x.hi;
 #pragma unroll
-          for (int i = 0; i < 2; ++i) {
-            const int p = __shfl_sync(0xffffffffu, page, i * 4 + lane / 8);
-            const int key = kt * BLOCK_N + half * 64 + i * 32 + lane;
-            const long long off = p * a.qc.page + seg.head * a.qc.head + a.qc.params + (key & (a.c.page_size - 1)) * ng * 4;
-            const bool in = p >= 0 && key >= seg.x.lo && key < seg.x.hi;
-#pragma unroll
-            for (int j = 0; j < NG; ++j) {
-              const int w = NG > 1 && ng > 1 ? j * 4 : 0;
-              b.v[i][j] = in ? __ldg(reinterpret_cast<const uint32_t*>(a.qc.V + off + w)) : 0u;
-              if constexpr (!IS_V) b.k[i][j] = in ? __ldg(reinterpret_cast<const uint32_t*>(a.qc.K + off + w)) : 0u;
-            }
+          for (int j = 0; j < NG; ++j) {
+            const int w = NG > 1 && ng > 1 ? j * 4 : 0;
+            b.v[j] = in ? __ldg(reinterpret_cast<const uint32_t*>(a.qc.V + off + w)) : 0u;
+            if constexpr (!IS_V) b.k[j] = in ? __ldg(reinterpret_cast<const uint32_t*>(a.qc.K + off + w)) : 0u;
           }
         };
         auto ask = [&](int kt, int page, int octet) {  // (each piece read by the lane that asked for it)
-          const int p = __shfl_sync(0xffffffffu, page, octet);
-          const int t = (kt * BLOCK_N + half * 64 + octet * 8) & (a.c.page_size - 1);
+          const int p = __shfl_sync(0xffffffffu, page, octet * 8);
+          const int t = (kt * BLOCK_N + quarter * 32 + octet * 8) & (a.c.page_size - 1);
           const uint8_t* const from = base + max(p, 0) * a.qc.page + seg.head * a.qc.head + t * chunks * 16;
 #pragma unroll
           for (int z = 0; z < PIECES; ++z) {
@@ -404,24 +399,22 @@ __global__ void __launch_bounds__(TilesCfg<D, BITS>::THREADS, 1)
           }
           asm volatile("cp.async.commit_group;" ::: "memory");
         };
-        // scale (low) and z' (high) of keys lane and lane + 32, as fp16 times the half's power of two
+        // scale (low) and z' (high) of key `lane`, as fp16 times the quarter's power of two
         struct Factors {
-          uint32_t f[2][NG];
+          uint32_t f[NG];
         };
-        auto nan = [](uint32_t p) { return (p & 0x7fffu) > 0x7f80u; };
-        auto exponent_of = [&](const uint32_t (&p)[2][NG]) {  // of the largest value that the half's keys can hold
+        auto nan = [](const uint32_t (&p)[NG]) {
+          bool bad = false;
+#pragma unroll
+          for (int j = 0; j < NG; ++j) bad |= (p[j] & 0x7fffu) > 0x7f80u;
+          return bad;
+        };
+        auto exponent_of = [&](const uint32_t (&p)[NG]) {  // of the largest value that the quarter's keys can hold
           float top = 0.f;
 #pragma unroll
-          for (int i = 0; i < 2; ++i) {
-            bool skip = false;
-#pragma unroll
-            for (int j = 0; j < NG; ++j) skip |= nan(p[i][j]);
-#pragma unroll
-            for (int j = 0; j < NG; ++j) {
-              const float s = q_scale(p[i][j]), z = q_offset(p[i][j]);
-              if (!skip) top = fmaxf(top, fmaxf(fabsf(z), fabsf(fmaf(s, STEPS, z))));
-            }
-          }
+          for (int j = 0; j < NG; ++j)
+            top = fmaxf(top, fmaxf(fabsf(q_offset(p[j])), fabsf(fmaf(q_scale(p[j]), STEPS, q_offset(p[j])))));
+          if (nan(p)) top = 0.f;
           top = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(top)));
           return min(max(q_exponent(top), -50), 126);
         };
@@ -429,29 +422,23 @@ __global__ void __launch_bounds__(TilesCfg<D, BITS>::THREADS, 1)
           const int ev = exponent_of(b.v) - 6, e = IS_V ? ev : exponent_of(b.k) - 7;
           if (!IS_V && lane == 0) *info = make_float2(q_pow2(e), (float)ev);
           const float by = q_pow2(-e);
+          const bool bad = nan(b.v) || (!IS_V && nan(b.k));
           Factors f;
 #pragma unroll
-          for (int i = 0; i < 2; ++i) {
-            bool bad = false;
-#pragma unroll
-            for (int j = 0; j < NG; ++j) bad |= nan(b.v[i][j]) || (!IS_V && nan(b.k[i][j]));
-#pragma unroll
-            for (int j = 0; j < NG; ++j) {
-              const uint32_t p = IS_V ? b.v[i][j] : b.k[i][j];
-              const float s = q_scale(p);
-              f.f[i][j] = bad ? (IS_V ? 0u : 0x7fff7fffu) : q_half2(s * by, fmaf(s, CENTRE, q_offset(p)) * by);
-            }
+          for (int j = 0; j < NG; ++j) {
+            const uint32_t p = IS_V ? b.v[j] : b.k[j];
+            const float s = q_scale(p);
+            f.f[j] = bad ? (IS_V ? 0u : 0x7fff7fffu) : q_half2(s * by, fmaf(s, CENTRE, q_offset(p)) * by);
           }
           return f;
         };
         auto write = [&](const Factors& f, uint32_t tile, int octet) {
-            const bool late = octet >= 4;  // keys 32 .. 63 of the half
-            const int r = half * 64 + octet * 8 + token;  // row of the tile
+            const int r = quarter * 32 + octet * 8 + token;  // row of the tile
             uint32_t sz[NG][IS_V ? 2 : 1];
 #pragma unroll
             for (int j = 0; j < NG; ++j)
 #pragma unroll
-              for (int e = 0; e < (IS_V ? 2 : 1); ++e) sz[j][e] = __shfl_sync(0xffffffffu, late ? f.f[1][j] : f.f[0][j], (octet * 8 & 31) + token + e);
+              for (int e = 0; e < (IS_V ? 2 : 1); ++e) sz[j][e] = __shfl_sync(0xffffffffu, f.f[j], octet * 8 + token + e);
 #pragma unroll
             for (int z = 0; z < PIECES; ++z) {
               const int col = (chunk0 + 4 * z) * (128 / BITS);
@@ -527,7 +514,7 @@ __global__ void __launch_bounds__(TilesCfg<D, BITS>::THREADS, 1)
           page = octet_page(kt);
           page_next = left > 0 ? octet_page(kt + 1) : -1;
           ask_params(params, kt, page);
-          for (int i = 0; i < 8; ++i) ask(kt, page, i);
+          for (int i = 0; i < 4; ++i) ask(kt, page, i);
         };
         auto tile = [&](int kt, int left, uint32_t to, uint64_t* full, float2* info, auto free) {
           ask_params(params_next, kt + 1, page_next);
@@ -535,8 +522,8 @@ __global__ void __launch_bounds__(TilesCfg<D, BITS>::THREADS, 1)
           if (!free()) return false;
           const Factors f = factors(params, info);
 #pragma unroll 1
-          for (int i = 0; i < 8; ++i) {
-            asm volatile("cp.async.wait_group 7;" ::: "memory");
+          for (int i = 0; i < 4; ++i) {
+            asm volatile("cp.async.wait_group 3;" ::: "memory");
             write(f, to, i);
             ask(kt + 1, page_next, i);
           }
@@ -555,13 +542,13 @@ __global__ void __launch_bounds__(TilesCfg<D, BITS>::THREADS, 1)
             if (seg.n > 0) begin(seg.k0, seg.n - 1);
             for (int t = 0; ok && t < seg.n; ++t, ++g) {
               const int ks = g % KST;
-              ok = tile(seg.k0 + t, seg.n - 1 - t, sK(ks), &bar_kfull[ks], &info_sh[g % TILE_INFO][half],
+              ok = tile(seg.k0 + t, seg.n - 1 - t, sK(ks), &bar_kfull[ks], &info_sh[g % TILE_INFO][quarter],
                         [&] { return __all_sync(0xffffffffu, wait_free(&bar_kempty[ks], ((g / KST) & 1) ^ 1)) != 0; });
             }
           }
         } else {
           // (a stage's uses -- key tiles, and per item one epilogue staging -- have positions in
-          // order; each of the two warps waits for their releases in that order)
+          // order; each of the four warps waits for their releases in that order)
           uint32_t pos = 0;
           int seen[VST];
           for (int s = 0; s < VST; ++s) seen[s] = 0;
@@ -589,7 +576,7 @@ __global__ void __launch_bounds__(TilesCfg<D, BITS>::THREADS, 1)
           }
         }
       };
-      if (warp < C::CODE_WARP + 2) fill_tiles(std::false_type());
+      if (warp < C::CODE_WARP + 4) fill_tiles(std::false_type());
       else fill_tiles(std::true_type());
       asm volatile("cp.async.wait_all;" ::: "memory");
     }
@@ -834,23 +821,40 @@ __global__ void __launch_bounds__(TilesCfg<D, BITS>::THREADS, 1)
         }
         tc_fence_after();
         if constexpr (BITS != 0) {
-          const float2 i0 = info_sh[g % TILE_INFO][0], i1 = info_sh[g % TILE_INFO][1];
+          const float2* const info = info_sh[g % TILE_INFO];
           // (positive whatever the row: a masked score is -infinity times it)
-          const float k_half[2] = {fmaxf(qf * i0.x, FLT_MIN), fmaxf(qf * i1.x, FLT_MIN)}, v_half[2] = {i0.y, i1.y};
+          auto k_of = [&](int c) { return fmaxf(qf * info[c].x, FLT_MIN); };
           const int c0 = (seg.k0 + t) * BLOCK_N;
           const bool edge = c0 < in_lo || c0 + BLOCK_N - 1 > in_hi;
-          auto scores = [&](int c, float (&s)[32]) {  // of 32 keys
-            uint32_t v[32];
-            tmem_ld32(s_addr + c * 32, v);
+          const float v_top = fmaxf(fmaxf(info[0].y, info[1].y), fmaxf(info[2].y, info[3].y));
+          auto rescale = [&](float by) {  // of O's row
+#pragma unroll 1
+            for (int c = 0; c < D / 32; ++c) {
+              uint32_t r[32];
+              tmem_ld32(o_addr + c * 32, r);
 #pragma unroll
-            for (int kk = 0; kk < 32; ++kk) s[kk] = __uint_as_float(v[kk]);
-            if (edge) mask_outside<32>(s, lo_i - c0 - 32 * c, hi_i - c0 - 32 * c);
+              for (int kk = 0; kk < 32; ++kk) r[kk] = __float_as_uint(__uint_as_float(r[kk]) * by);
+              tmem_st32(o_addr + c * 32, r);
+            }
           };
-          float mt = -INFINITY;
+          // (2^8 of a probability and 2^6 of V's exponent beyond v_ref: P stays below 2^15)
+          if (t == 0 || v_top > v_ref + 6.f) {
+            if (t > 0) rescale(ex2(v_ref - v_top));
+            v_ref = v_top;
+          }
+          // 32 keys at a time, in a loop (see the code warps), P in the place of scores that are read. m moves by whole
+          // powers of two: where it does, O, l and what is written of P follow exactly.
 #pragma unroll 1
           for (int c = 0; c < 4; ++c) {
             float s[32];
-            scores(c, s);
+            {
+              uint32_t v[32];
+              tmem_ld32(s_addr + c * 32, v);
+#pragma unroll
+              for (int kk = 0; kk < 32; ++kk) s[kk] = __uint_as_float(v[kk]);
+            }
+            if (edge) mask_outside<32>(s, lo_i - c0 - 32 * c, hi_i - c0 - 32 * c);
+            const float kc = k_of(c), up = fmaxf(info[c].y - v_ref, -60.f);  // (far below that, P is 0 in fp16)
             float mx[4];
 #pragma unroll
             for (int kk = 0; kk < 4; ++kk) mx[kk] = max3(s[kk], s[4 + kk], s[8 + kk]);
@@ -860,37 +864,27 @@ __global__ void __launch_bounds__(TilesCfg<D, BITS>::THREADS, 1)
               for (int kk = 0; kk < 4; ++kk) mx[kk] = max3(mx[kk], s[k + kk], s[k + 4 + kk]);
 #pragma unroll
             for (int kk = 0; kk < 4; ++kk) mx[kk] = fmaxf(mx[kk], s[28 + kk]);
-            mt = fmaxf(mt, fmaxf(max3(mx[0], mx[1], mx[2]), mx[3]) * (c < 2 ? k_half[0] : k_half[1]));
-          }
-          const float v_top = fmaxf(v_half[0], v_half[1]);
-          // (2^8 of a probability and 2^6 of V's exponent beyond v_ref: P stays below 2^15)
-          const bool v_grow = t == 0 || v_top > v_ref + 6.f;
-          if (__any_sync(0xffffffffu, (r_in < rows && mt > m + RESCALE_THRESHOLD) || v_grow)) {
-            const float m_new = fmaxf(m, mt), v_new = v_grow ? v_top : v_ref;
-            const float corr = ex2(m - m_new);
-            l *= corr;
-            if (t > 0) {
-              const float by = corr * ex2(v_ref - v_new);
-#pragma unroll
-              for (int c = 0; c < D / 32; ++c) {
-                uint32_t r[32];
-                tmem_ld32(o_addr + c * 32, r);
-#pragma unroll
-                for (int kk = 0; kk < 32; ++kk) r[kk] = __float_as_uint(__uint_as_float(r[kk]) * by);
-                tmem_st32(o_addr + c * 32, r);
-              }
-            }
-            m = m_new;
-            v_ref = v_new;
-          }
+            const float mt = fmaxf(max3(mx[0], mx[1], mx[2]), mx[3]) * kc;
+            // (each row for itself: no row's bits depend on another's)
+            const bool grow = r_in < rows && mt > m + RESCALE_THRESHOLD;
+            if (__any_sync(0xffffffffu, grow)) {
+              const float m_new = grow ? ceilf(mt) : m, corr = ex2(m - m_new);
+              l *= corr;
+              if (t > 0) rescale(corr);
+              const uint32_t by = pack_half2(corr, corr);
+              tmem_st_wait();
 #pragma unroll 1
-          for (int c = 0; c < 4; ++c) {
-            const float up = fmaxf((c < 2 ? v_half[0] : v_half[1]) - v_ref, -60.f);  // (far below that, P is 0 in fp16)
-            const float kh = c < 2 ? k_half[0] : k_half[1];
-            const float2 by = make_float2(kh, kh), off = make_float2(up - m, up - m);
+              for (int b = 0; b < c; ++b) {
+                uint32_t r[16];
+                tmem_ld16(s_addr + b * 16, r);
+#pragma unroll
+                for (int kk = 0; kk < 16; ++kk) r[kk] = q_fma2(r[kk], by, 0u);
+                tmem_st16(s_addr + b * 16, r);
+              }
+              m = m_new;
+            }
+            const float2 by = make_float2(kc, kc), off = make_float2(up - m, up - m);
             float2 ls[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
-            float s[32];
-            scores(c, s);
             uint32_t pk[16];
 #pragma unroll
             for (int kk = 0; kk < 16; ++kk) {
