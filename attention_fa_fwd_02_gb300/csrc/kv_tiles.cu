@@ -94,9 +94,9 @@ struct TilesCfg {
   static constexpr uint32_t RELAY_BAR = 3;  // named barrier (1 + q: P_q written)
   static constexpr int CODE_WARP = 12;  // codes: four warps for K's tiles, four for V's, a quarter of a tile each
   static constexpr int THREADS = BITS ? 640 : 384;
-  // (codes: every warp keeps the 96 registers that 640 threads leave; the softmax takes its scores 32 at a time)
-  static constexpr uint32_t REGS_SOFTMAX = 216, REGS_CONTROL = 64;
-  static_assert(BITS || 2 * 128 * REGS_SOFTMAX + 128 * REGS_CONTROL <= 384 * 168, "register split exceeds the launch allocation");
+  static constexpr uint32_t REGS_SOFTMAX = BITS ? 128 : 216, REGS_CONTROL = BITS ? 48 : 64, REGS_CODES = 88;
+  static_assert(2 * 128 * REGS_SOFTMAX + 128 * REGS_CONTROL + (BITS ? 256 * REGS_CODES : 0) <= (BITS ? 640 * 96 : 384 * 168),
+                "register split exceeds the launch allocation");
   static constexpr uint32_t FILLERS = BITS ? 4 : 1;  // arrivals at a landed tile's barrier, and at a grant
   static constexpr uint32_t TMEM_COLS = 512;
   __host__ __device__ static constexpr uint32_t s_col(int q) { return 128u * q; }
@@ -350,6 +350,7 @@ __global__ void __launch_bounds__(TilesCfg<D, BITS>::THREADS, 1)
     // on their way while the one before it is turned into numbers. Keys that no row sees, and those of a missing page,
     // are zeros; a key whose scale is NaN, in K or in V, is NaN in K and zeros in V, so that rows that see it become NaN
     // and the tile's others do not.
+    regs_decrease<C::REGS_CODES>();
     if constexpr (BITS != 0) {
       auto fill_tiles = [&](auto is_v) {
         constexpr bool IS_V = decltype(is_v)::value;
@@ -581,7 +582,7 @@ __global__ void __launch_bounds__(TilesCfg<D, BITS>::THREADS, 1)
       asm volatile("cp.async.wait_all;" ::: "memory");
     }
   } else if (warp >= C::SOFTMAX_WARPS) {
-    if constexpr (!BITS) regs_decrease<C::REGS_CONTROL>();
+    regs_decrease<C::REGS_CONTROL>();
     if (BITS && warp == C::KQ_WARP) {
       // ---------------------------------------------------------- Q producer (the codes have their own)
       int j = 0;
@@ -772,7 +773,7 @@ __global__ void __launch_bounds__(TilesCfg<D, BITS>::THREADS, 1)
     }
   } else {
     // ------------------------------------------------------------ softmax / epilogue
-    if constexpr (!BITS) regs_increase<C::REGS_SOFTMAX>();
+    regs_increase<C::REGS_SOFTMAX>();
     const int q = warp / 4, wq = warp % 4;
     const int r_in = wq * 32 + lane;
     const uint32_t lane_addr = tmem + ((uint32_t)(wq * 32) << 16);
@@ -822,8 +823,6 @@ __global__ void __launch_bounds__(TilesCfg<D, BITS>::THREADS, 1)
         tc_fence_after();
         if constexpr (BITS != 0) {
           const float2* const info = info_sh[g % TILE_INFO];
-          // (positive whatever the row: a masked score is -infinity times it)
-          auto k_of = [&](int c) { return fmaxf(qf * info[c].x, FLT_MIN); };
           const int c0 = (seg.k0 + t) * BLOCK_N;
           const bool edge = c0 < in_lo || c0 + BLOCK_N - 1 > in_hi;
           const float v_top = fmaxf(fmaxf(info[0].y, info[1].y), fmaxf(info[2].y, info[3].y));
@@ -842,59 +841,71 @@ __global__ void __launch_bounds__(TilesCfg<D, BITS>::THREADS, 1)
             if (t > 0) rescale(ex2(v_ref - v_top));
             v_ref = v_top;
           }
-          // 32 keys at a time, in a loop (see the code warps), P in the place of scores that are read. m moves by whole
+          // 64 keys at a time, in a loop (see the code warps), P in the place of scores that are read. m moves by whole
           // powers of two: where it does, O, l and what is written of P follow exactly.
 #pragma unroll 1
-          for (int c = 0; c < 4; ++c) {
-            float s[32];
+          for (int h = 0; h < 2; ++h) {
+            const float2 i0 = info[2 * h], i1 = info[2 * h + 1];
+            float s[64];
             {
-              uint32_t v[32];
-              tmem_ld32(s_addr + c * 32, v);
+              uint32_t v[32], u[32];
+              tmem_ld32x2(s_addr + h * 64, s_addr + h * 64 + 32, v, u);
 #pragma unroll
-              for (int kk = 0; kk < 32; ++kk) s[kk] = __uint_as_float(v[kk]);
+              for (int kk = 0; kk < 32; ++kk) {
+                s[kk] = __uint_as_float(v[kk]);
+                s[32 + kk] = __uint_as_float(u[kk]);
+              }
             }
-            if (edge) mask_outside<32>(s, lo_i - c0 - 32 * c, hi_i - c0 - 32 * c);
-            const float kc = k_of(c), up = fmaxf(info[c].y - v_ref, -60.f);  // (far below that, P is 0 in fp16)
-            float mx[4];
+            if (edge) mask_outside<64>(s, lo_i - c0 - 64 * h, hi_i - c0 - 64 * h);
+            // (positive whatever the row: a masked score is -infinity times it)
+            const float kc[2] = {fmaxf(qf * i0.x, FLT_MIN), fmaxf(qf * i1.x, FLT_MIN)};
+            const float up[2] = {fmaxf(i0.y - v_ref, -60.f), fmaxf(i1.y - v_ref, -60.f)};  // (far below that, P is 0 in fp16)
+            float mt = -INFINITY;
 #pragma unroll
-            for (int kk = 0; kk < 4; ++kk) mx[kk] = max3(s[kk], s[4 + kk], s[8 + kk]);
+            for (int b = 0; b < 2; ++b) {
+              float mx[4];
 #pragma unroll
-            for (int k = 12; k < 28; k += 8)
+              for (int kk = 0; kk < 4; ++kk) mx[kk] = max3(s[32 * b + kk], s[32 * b + 4 + kk], s[32 * b + 8 + kk]);
 #pragma unroll
-              for (int kk = 0; kk < 4; ++kk) mx[kk] = max3(mx[kk], s[k + kk], s[k + 4 + kk]);
+              for (int k = 12; k < 28; k += 8)
 #pragma unroll
-            for (int kk = 0; kk < 4; ++kk) mx[kk] = fmaxf(mx[kk], s[28 + kk]);
-            const float mt = fmaxf(max3(mx[0], mx[1], mx[2]), mx[3]) * kc;
+                for (int kk = 0; kk < 4; ++kk) mx[kk] = max3(mx[kk], s[32 * b + k + kk], s[32 * b + k + 4 + kk]);
+#pragma unroll
+              for (int kk = 0; kk < 4; ++kk) mx[kk] = fmaxf(mx[kk], s[32 * b + 28 + kk]);
+              mt = fmaxf(mt, fmaxf(max3(mx[0], mx[1], mx[2]), mx[3]) * kc[b]);
+            }
             // (each row for itself: no row's bits depend on another's)
             const bool grow = r_in < rows && mt > m + RESCALE_THRESHOLD;
             if (__any_sync(0xffffffffu, grow)) {
               const float m_new = grow ? ceilf(mt) : m, corr = ex2(m - m_new);
               l *= corr;
               if (t > 0) rescale(corr);
-              const uint32_t by = pack_half2(corr, corr);
-              tmem_st_wait();
-#pragma unroll 1
-              for (int b = 0; b < c; ++b) {
-                uint32_t r[16];
-                tmem_ld16(s_addr + b * 16, r);
+              if (h > 0) {
+                const uint32_t by = pack_half2(corr, corr);
+                tmem_st_wait();
+                uint32_t r[32];
+                tmem_ld32(s_addr, r);
 #pragma unroll
-                for (int kk = 0; kk < 16; ++kk) r[kk] = q_fma2(r[kk], by, 0u);
-                tmem_st16(s_addr + b * 16, r);
+                for (int kk = 0; kk < 32; ++kk) r[kk] = q_fma2(r[kk], by, 0u);
+                tmem_st32(s_addr, r);
               }
               m = m_new;
             }
-            const float2 by = make_float2(kc, kc), off = make_float2(up - m, up - m);
-            float2 ls[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
-            uint32_t pk[16];
+            uint32_t pk[32];
 #pragma unroll
-            for (int kk = 0; kk < 16; ++kk) {
-              const float2 x = fma2(make_float2(s[2 * kk], s[2 * kk + 1]), by, off);
-              const float2 pp = make_float2(ex2(x.x), ex2(x.y));
-              ls[kk & 1] = add2(ls[kk & 1], pp);
-              pk[kk] = pack_half2(pp.x, pp.y);
+            for (int b = 0; b < 2; ++b) {
+              const float2 by = make_float2(kc[b], kc[b]), off = make_float2(up[b] - m, up[b] - m);
+              float2 ls[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
+#pragma unroll
+              for (int kk = 0; kk < 16; ++kk) {
+                const float2 x = fma2(make_float2(s[32 * b + 2 * kk], s[32 * b + 2 * kk + 1]), by, off);
+                const float2 pp = make_float2(ex2(x.x), ex2(x.y));
+                ls[kk & 1] = add2(ls[kk & 1], pp);
+                pk[16 * b + kk] = pack_half2(pp.x, pp.y);
+              }
+              l = fmaf((ls[0].x + ls[1].x) + (ls[0].y + ls[1].y), ex2(-up[b]), l);
             }
-            tmem_st16(s_addr + c * 16, pk);
-            l = fmaf((ls[0].x + ls[1].x) + (ls[0].y + ls[1].y), ex2(-up), l);
+            tmem_st32(s_addr + h * 32, pk);
           }
         } else {
         float s[128];
