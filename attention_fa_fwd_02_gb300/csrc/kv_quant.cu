@@ -18,7 +18,7 @@ namespace {
 
 constexpr int THREADS = 256;
 constexpr int ROWS = 8;    // of a warp
-constexpr int SPAN = 8;    // tokens of a block at most
+constexpr int SPAN = THREADS / 8;  // tokens of a block at most (eight lanes look each up)
 constexpr float LARGE = 8.507059173023462e37f;  // 2^126
 
 struct MoveArgs {
@@ -28,7 +28,7 @@ struct MoveArgs {
   void* dst[3];
   long long token[3], head[3];  // strides of src (append)
   int H, T, B, D, shift;
-  int span, per;  // tokens of a block; rows of a token in it (gridDim.y parts)
+  int span, span_shift, per;  // tokens of a block (and their log2); rows of a token in it (gridDim.y parts)
   int rot, interleaved, wide;
   const unsigned long long* freqs;
   float mscale;
@@ -45,19 +45,24 @@ __device__ __forceinline__ float load1(const __nv_bfloat16* p) { return __bfloat
 template <>
 __device__ __forceinline__ float load1(const float* p) { return *p; }
 
-__device__ __forceinline__ void load8(const __nv_bfloat16* p, float (&x)[8]) {
-  const uint4 v = *reinterpret_cast<const uint4*>(p);
-  const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+template <typename E>
+__device__ __forceinline__ void unpack8(const uint4 (&v)[sizeof(E) / 2], float (&x)[8]) {
+  if constexpr (sizeof(E) == 2) {
+    const uint32_t w[4] = {v[0].x, v[0].y, v[0].z, v[0].w};
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    x[2 * i] = __uint_as_float(w[i] << 16);
-    x[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
+    for (int i = 0; i < 4; ++i) {
+      x[2 * i] = __uint_as_float(w[i] << 16);
+      x[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      x[4 * i] = __uint_as_float(v[i].x);
+      x[4 * i + 1] = __uint_as_float(v[i].y);
+      x[4 * i + 2] = __uint_as_float(v[i].z);
+      x[4 * i + 3] = __uint_as_float(v[i].w);
+    }
   }
-}
-__device__ __forceinline__ void load8(const float* p, float (&x)[8]) {
-  const float4 a = *reinterpret_cast<const float4*>(p), b = *reinterpret_cast<const float4*>(p + 4);
-  x[0] = a.x; x[1] = a.y; x[2] = a.z; x[3] = a.w;
-  x[4] = b.x; x[5] = b.y; x[6] = b.z; x[7] = b.w;
 }
 __device__ __forceinline__ uint32_t bf16x2(float a, float b) {
   const __nv_bfloat162 h = __floats2bfloat162_rn(a, b);
@@ -88,36 +93,67 @@ __device__ __forceinline__ Grid grid_of(float lo, float hi, float steps, bool fi
   if (!fine) g.s = g.z = __int_as_float(0x7fff0000);  // NaN
   return g;
 }
-__device__ __forceinline__ uint32_t code_of(float x, const Grid& g, float steps) {
-  const float c = rintf(__fdiv_rn(__fsub_rn(x, g.z), g.s));
-  return g.s > 0.f ? (uint32_t)fminf(fmaxf(c, 0.f), steps) : 0u;
+// The codes of eight columns: quotients rounded to integers. A product with 1 / s (exact, as the fused operations take
+// it) is off from the quotient by less than 2^-14 (of up to 256: 2^-23 of it and of 1 / s), so it rounds to the same
+// integer unless it lies that near to the middle between two; there, one value in some hundreds, the quotient itself is
+// formed. The integers stand in the low bits of 1.5 * 2^23 and more.
+__device__ __forceinline__ void codes_of(const float (&x)[8], const Grid& g, float inv, uint32_t (&code)[8]) {
+  constexpr float MAGIC = 12582912.f;
+  bool near = false;
+#pragma unroll
+  for (int n = 0; n < 8; ++n) {
+    const float d = __fsub_rn(x[n], g.z), y = __fmaf_rn(d, inv, MAGIC);
+    const float off = __fmaf_rn(d, inv, -__fsub_rn(y, MAGIC));
+    near |= !(fabsf(off) <= 0.5f - 0x1p-13f);  // (NaN too: s may be 0, or too small for 1 / s)
+    code[n] = __float_as_uint(y);
+  }
+  if (near) {
+#pragma unroll
+    for (int n = 0; n < 8; ++n)
+      code[n] = g.s > 0.f ? __float_as_uint(__fadd_rn(rintf(__fdiv_rn(__fsub_rn(x[n], g.z), g.s)), MAGIC)) : 0u;
+  }
 }
 
 // Place of the block's tokens in a page: page number and token, or page -1 (no such token); live: the row
-// belongs to a sequence.
+// belongs to a sequence; its position there.
 struct Places {
   int page[SPAN], at[SPAN], live[SPAN];
+  long long pos[SPAN];
 };
 
-// Row t's position in its sequence and its place, by a warp
+// The places of rows t0 .. t0 + tokens - 1, eight lanes to a row: its sequence is the last b with cu[b] <= t, eight
+// probes to a round (cu is probed inside [0, B] whatever it holds).
 template <bool READ>
-__device__ __forceinline__ long long find_place(const MoveArgs& a, int t, int k, Places& sh) {
+__device__ __forceinline__ void find_places(const MoveArgs& a, int t0, int tokens, Places& sh) {
   const fakv_cache& c = a.q.c;
-  const int b = find_seq(a.cu, a.B, t);
+  const int k = threadIdx.x / 8, sub = threadIdx.x & 7, t = t0 + min(k, tokens - 1);
+  if (threadIdx.x / 32 * 4 >= tokens) return;  // (whole warps)
+  int lo = 0, n = a.B;  // the answer lies in [lo, lo + n)
+  const int end = a.cu[a.B];
+  bool live = t < end;
+  while (__any_sync(0xffffffffu, n > 1)) {
+    const int step = (n + 7) / 8;
+    const bool below = sub * step < n && a.cu[lo + sub * step] <= t;
+    const int hits = __popc(__ballot_sync(0xffffffffu, below) >> (threadIdx.x & 24) & 0xffu);
+    const int first = max(hits - 1, 0) * step;
+    n = min(step, n - first);
+    lo += first;
+  }
+  live = live && a.cu[lo] <= t;
   int page = -1;
   long long pos = 0;
-  if (b >= 0) {
-    const Seq s = load_seq(c, a.cu, a.slots, b, a.T);
-    pos = READ && a.first ? (long long)a.first[b] + (t - s.row0) : (long long)s.len - s.n + (t - s.row0);
+  if (live && k < tokens) {
+    const Seq s = load_seq(c, a.cu, a.slots, lo, a.T);
+    pos = READ && a.first ? (long long)a.first[lo] + (t - s.row0) : (long long)s.len - s.n + (t - s.row0);
     if (s.slot >= 0 && pos >= 0 && pos < s.len) page = page_of(c, s.slot, (int)pos, a.shift);
     else if (s.slot >= 0) raise(c.status, FAKV_BAD_LENGTH);
   }
-  if (ptx::lane_id() == 0) {
+  if (k < tokens && sub == 0) {
     sh.page[k] = page;
     sh.at[k] = (int)pos & (c.page_size - 1);
-    sh.live[k] = b >= 0;
+    sh.live[k] = live;
+    sh.pos[k] = pos;
   }
-  return pos;
 }
 
 // a decreasing cu, looked for by one block (its warps but the first)
@@ -129,7 +165,7 @@ __device__ __forceinline__ void check_cu(const MoveArgs& a) {
 }
 
 template <typename E, int BITS, int NW>  // NW: blocks of 32 columns at most
-__global__ void __launch_bounds__(THREADS) qappend_kernel(const __grid_constant__ MoveArgs a) {
+__global__ void __launch_bounds__(THREADS, 2) qappend_kernel(const __grid_constant__ MoveArgs a) {
   extern __shared__ float2 cs[];  // [tokens][pairs]
   __shared__ Places sh;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, quad = lane & 3;
@@ -138,18 +174,45 @@ __global__ void __launch_bounds__(THREADS) qappend_kernel(const __grid_constant_
   const int heads = a.H + 2 * HKV;  // of a token: q's, k's, v's
   const int h0 = blockIdx.y * a.per, mine = min(a.per, heads - h0);
   check_cu(a);
-  for (int k = warp; k < tokens; k += THREADS / 32) {
-    const long long pos = find_place<false>(a, t0 + k, k, sh);
-    for (int i = lane; i < pairs; i += 32) {
-      const float2 v = turn(pos, a.freqs[i]);
-      cs[k * pairs + i] = make_float2(v.x * a.mscale, v.y * a.mscale);
+  // Row r of the block: head h of token k, the lane's blocks of columns of it and (half pairs) of its pairs' other halves.
+  // The first ones are on their way while the places are found.
+  constexpr int PARTS = sizeof(E) / 2;  // 16-byte pieces of eight columns
+  struct Raw {
+    uint4 x[NW][PARTS], y[NW][PARTS];
+  };
+  auto load = [&](int r, Raw& v) {
+    const int k = r & (a.span - 1), h = h0 + (r >> a.span_shift);
+    if (!a.wide || k >= tokens || h >= h0 + mine) return;
+    const int which = h < a.H ? 0 : h < a.H + HKV ? 1 : 2;
+    const int head = h - (which == 0 ? 0 : which == 1 ? a.H : a.H + HKV);
+    const E* const row = static_cast<const E*>(a.src[which]) + (t0 + k) * a.token[which] + head * a.head[which];
+#pragma unroll
+    for (int w = 0; w < NW; ++w) {
+      const int c0 = w * 32 + quad * 8;
+      if (c0 >= a.D) continue;
+#pragma unroll
+      for (int i = 0; i < PARTS; ++i) v.x[w][i] = reinterpret_cast<const uint4*>(row + c0)[i];
+      if (which < 2 && c0 < a.rot && !a.interleaved) {
+        const E* const other = row + (c0 >= pairs ? c0 - pairs : c0 + pairs);
+#pragma unroll
+        for (int i = 0; i < PARTS; ++i) v.y[w][i] = reinterpret_cast<const uint4*>(other)[i];
+      }
     }
+  };
+  Raw raw;
+  load(warp * ROWS + lane / 4, raw);
+  find_places<false>(a, t0, tokens, sh);
+  __syncthreads();
+  for (int i = threadIdx.x; i < tokens * pairs; i += THREADS) {
+    const float2 v = turn(sh.pos[i / pairs], a.freqs[i % pairs]);
+    cs[i] = make_float2(v.x * a.mscale, v.y * a.mscale);
   }
   __syncthreads();
   // (all lanes of a warp take part in its shuffles)
   for (int r0 = warp * ROWS; r0 < mine * a.span; r0 += THREADS / 32 * ROWS) {
     const int r = r0 + lane / 4;
-    const int k = r % a.span, h = h0 + r / a.span;
+    if (r0 != warp * ROWS) load(r, raw);
+    const int k = r & (a.span - 1), h = h0 + (r >> a.span_shift);
     const bool in = k < tokens && h < h0 + mine;
     const int which = h < a.H ? 0 : h < a.H + HKV ? 1 : 2;
     const int head = h - (which == 0 ? 0 : which == 1 ? a.H : a.H + HKV);
@@ -164,7 +227,7 @@ __global__ void __launch_bounds__(THREADS) qappend_kernel(const __grid_constant_
       if (!in || c0 >= a.D) continue;
       const float2* const turns = cs + k * pairs;
       if (a.wide) {
-        load8(row + c0, x[w]);
+        unpack8<E>(raw.x[w], x[w]);
         if (turned && c0 < a.rot) {
           if (a.interleaved) {
 #pragma unroll
@@ -177,7 +240,7 @@ __global__ void __launch_bounds__(THREADS) qappend_kernel(const __grid_constant_
           } else {
             const bool second = c0 >= pairs;
             float y[8];
-            load8(row + (second ? c0 - pairs : c0 + pairs), y);
+            unpack8<E>(raw.y[w], y);
 #pragma unroll
             for (int n = 0; n < 8; ++n) {
               const float2 q = turns[(second ? c0 - pairs : c0) + n];
@@ -219,10 +282,11 @@ __global__ void __launch_bounds__(THREADS) qappend_kernel(const __grid_constant_
         }
       }
     }
+    if (!__any_sync(0xffffffffu, in && which > 0)) continue;
     // ---- minimum and maximum of blocks 0, 1 and of 2, 3: of the groups, or both of the whole head
     constexpr float steps = BITS == 4 ? 15.f : 255.f;
     float lo[2] = {INFINITY, INFINITY}, hi[2] = {-INFINITY, -INFINITY};
-    bool fine[2] = {true, true};
+    float nil[2] = {0.f, 0.f};  // (NaN where a value is NaN or infinite: the minimum and maximum pass over NaN)
 #pragma unroll
     for (int w = 0; w < NW; ++w) {
       if (w * 32 + quad * 8 >= a.D) continue;
@@ -230,48 +294,68 @@ __global__ void __launch_bounds__(THREADS) qappend_kernel(const __grid_constant_
       for (int n = 0; n < 8; ++n) {
         lo[w / 2] = fminf(lo[w / 2], x[w][n]);
         hi[w / 2] = fmaxf(hi[w / 2], x[w][n]);
-        fine[w / 2] = fine[w / 2] && fabsf(x[w][n]) < LARGE;
+        nil[w / 2] = fmaf(x[w][n], 0.f, nil[w / 2]);
       }
     }
     if (a.q.groups == 1) {
       lo[0] = lo[1] = fminf(lo[0], lo[1]);
       hi[0] = hi[1] = fmaxf(hi[0], hi[1]);
-      fine[0] = fine[1] = fine[0] && fine[1];
+      nil[0] = nil[1] = nil[0] + nil[1];
     }
     Grid g[2];
+    float inv[2];
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
 #pragma unroll
       for (int d = 1; d < 4; d <<= 1) {
         lo[i] = fminf(lo[i], __shfl_xor_sync(0xffffffffu, lo[i], d));
         hi[i] = fmaxf(hi[i], __shfl_xor_sync(0xffffffffu, hi[i], d));
-        fine[i] = __shfl_xor_sync(0xffffffffu, (int)fine[i], d) && fine[i];
+        nil[i] += __shfl_xor_sync(0xffffffffu, nil[i], d);
       }
-      g[i] = grid_of(lo[i], hi[i], steps, fine[i]);
+      g[i] = grid_of(lo[i], hi[i], steps, nil[i] == 0.f && hi[i] < LARGE && lo[i] > -LARGE);
+      inv[i] = __fdiv_rn(1.f, g[i].s);
     }
-    if (which == 0 || !in || sh.page[k] < 0) continue;
-    uint8_t* const block = (which == 1 ? a.q.K : a.q.V) + sh.page[k] * a.q.page + head * a.q.head;
+    // V's tokens lie in pairs: where the lanes four off have the pair's other one, each writes half of what both have
+    const int k2 = k ^ 1;
+    const bool paired = a.span > 1 && in && which == 2 && k2 < tokens && sh.page[k] >= 0 && sh.page[k2] == sh.page[k] &&
+                        (sh.at[k] ^ 1) == sh.at[k2] && (sh.at[k] & 1) == (k & 1);
+    const bool skip = which == 0 || !in || sh.page[k] < 0;
+    uint8_t* const block = (which == 1 ? a.q.K : a.q.V) + (skip ? 0 : sh.page[k] * a.q.page + head * a.q.head);
 #pragma unroll
     for (int w = 0; w < NW; ++w) {
-      if (BITS == 4 ? w >= a.q.chunks : 2 * w + quad / 2 >= a.q.chunks) continue;
+      const bool none = skip || (BITS == 4 ? w >= a.q.chunks : 2 * w + quad / 2 >= a.q.chunks);
       uint32_t code[8];
+      codes_of(x[w], g[w / 2], inv[w / 2], code);
+      if (w * 32 + quad * 8 >= a.D) {
 #pragma unroll
-      for (int n = 0; n < 8; ++n) code[n] = w * 32 + quad * 8 < a.D ? code_of(x[w][n], g[w / 2], steps) : 0u;
+        for (int n = 0; n < 8; ++n) code[n] = 0u;
+      }
       if constexpr (BITS == 4) {
-        uint32_t v = 0;
-#pragma unroll
-        for (int n = 0; n < 8; ++n) v |= code[n] << (4 * n);
-        if (which == 1) *reinterpret_cast<uint32_t*>(block + q_k_at(a.q.chunks, sh.at[k], w, quad)) = v;
+        // (bytes of columns 0, 2, 4, 6 and of 1, 3, 5, 7)
+        const uint32_t e = __byte_perm(__byte_perm(code[0], code[2], 0x0040), __byte_perm(code[4], code[6], 0x0040), 0x5410);
+        const uint32_t d = __byte_perm(__byte_perm(code[1], code[3], 0x0040), __byte_perm(code[5], code[7], 0x0040), 0x5410);
+        const uint32_t v = e | d << 4;
+        const uint32_t o = __shfl_xor_sync(0xffffffffu, v, 4);
+        if (none) continue;
+        if (paired) {
+          // (the even token's lane the words' low halves, the odd one's their high ones)
+          uint32_t* const to = reinterpret_cast<uint32_t*>(block + q_v_at(4, a.q.chunks, sh.at[k] & ~1, w, quad));
+          if (k & 1) to[1] = __byte_perm(o, v, 0x7632);
+          else to[0] = __byte_perm(v, o, 0x5410);
+        } else if (which == 1) *reinterpret_cast<uint32_t*>(block + q_k_at(a.q.chunks, sh.at[k], w, quad)) = v;
         else q_v_store<4>(block + q_v_at(4, a.q.chunks, sh.at[k], w, quad), v);
       } else {
-        uint2 v = make_uint2(0, 0);
-#pragma unroll
-        for (int n = 0; n < 4; ++n) {
-          v.x |= code[n] << (8 * n);
-          v.y |= code[4 + n] << (8 * n);
-        }
+        const uint2 v = make_uint2(__byte_perm(__byte_perm(code[0], code[1], 0x0040), __byte_perm(code[2], code[3], 0x0040), 0x5410),
+                                   __byte_perm(__byte_perm(code[4], code[5], 0x0040), __byte_perm(code[6], code[7], 0x0040), 0x5410));
         const int chunk = 2 * w + quad / 2, word = quad % 2 * 2;
-        if (which == 1) {
+        const uint32_t o = __shfl_xor_sync(0xffffffffu, k & 1 ? v.x : v.y, 4);
+        if (none) continue;
+        if (paired) {
+          // (the even token's lane the first words, the odd one's the second)
+          const uint32_t e = k & 1 ? o : v.x, d = k & 1 ? v.y : o;
+          *reinterpret_cast<uint2*>(block + q_v_at(8, a.q.chunks, sh.at[k] & ~1, chunk, word + (k & 1))) =
+              make_uint2(__byte_perm(e, d, 0x5140), __byte_perm(e, d, 0x7362));
+        } else if (which == 1) {
           *reinterpret_cast<uint2*>(block + q_k_at(a.q.chunks, sh.at[k], chunk, word)) = v;
         } else {
           q_v_store<8>(block + q_v_at(8, a.q.chunks, sh.at[k], chunk, word), v.x);
@@ -279,7 +363,7 @@ __global__ void __launch_bounds__(THREADS) qappend_kernel(const __grid_constant_
         }
       }
     }
-    if (quad < a.q.groups) {
+    if (!skip && quad < a.q.groups) {
       const Grid& m = g[NW > 2 ? quad & 1 : 0];
       *reinterpret_cast<uint32_t*>(block + a.q.params + (sh.at[k] * a.q.groups + quad) * 4) =
           (__float_as_uint(m.s) >> 16) | (__float_as_uint(m.z) & 0xffff0000u);
@@ -295,10 +379,10 @@ __global__ void __launch_bounds__(THREADS) qread_kernel(const __grid_constant__ 
   const int HKV = a.q.c.HKV, heads = 2 * HKV;
   const int h0 = blockIdx.y * a.per, mine = min(a.per, heads - h0);
   check_cu(a);
-  for (int k = warp; k < tokens; k += THREADS / 32) find_place<true>(a, t0 + k, k, sh);
+  find_places<true>(a, t0, tokens, sh);
   __syncthreads();
   for (int r = warp * ROWS + lane / 4; r < mine * a.span; r += THREADS / 32 * ROWS) {
-    const int k = r % a.span, h = h0 + r / a.span;
+    const int k = r & (a.span - 1), h = h0 + (r >> a.span_shift);
     if (k >= tokens || !sh.live[k]) continue;
     const int which = h < HKV ? 0 : 1, head = h - which * HKV;
     const bool there = sh.page[k] >= 0;
@@ -344,9 +428,9 @@ __global__ void __launch_bounds__(THREADS) qread_kernel(const __grid_constant__ 
   }
 }
 
-// Tokens of a block: as many as leave every SM two blocks, and so few tokens are spread over their heads
+// Tokens of a block: as many as leave every SM three blocks, and so few tokens are spread over their heads
 void shape(MoveArgs& a, int heads, dim3* grid) {
-  const int want = 2 * host::sm_count();
+  const int want = 3 * host::sm_count();
   a.span = SPAN;
   while (a.span > 1 && (a.T + a.span - 1) / a.span < want) a.span /= 2;
   const int blocks = (a.T + a.span - 1) / a.span;
@@ -354,6 +438,7 @@ void shape(MoveArgs& a, int heads, dim3* grid) {
   // (a part has a warp's rows for each of its warps at least)
   while (parts * blocks < want && heads * a.span > 2 * parts * ROWS) parts *= 2;
   a.per = (heads + parts - 1) / parts;
+  a.span_shift = log2_of(a.span);
   *grid = dim3(blocks, (heads + a.per - 1) / a.per);
 }
 
