@@ -417,7 +417,7 @@ __global__ void __launch_bounds__(TilesCfg<D, BITS>::THREADS, 1)
             top = fmaxf(top, fmaxf(fabsf(q_offset(p[j])), fabsf(fmaf(q_scale(p[j]), STEPS, q_offset(p[j])))));
           if (nan(p)) top = 0.f;
           top = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(top)));
-          return min(max(q_exponent(top), -50), 126);
+          return min(max(q_exponent(top), -100), 126);
         };
         auto factors = [&](const Params& b, float2* info) {
           const int ev = exponent_of(b.v) - 6, e = IS_V ? ev : exponent_of(b.k) - 7;

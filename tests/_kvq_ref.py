@@ -105,26 +105,30 @@ def held(cache, slot, plane=0):
     return out
 
 
-def attend(cache, q, new, slots, scale, causal, window, plane=0, tiles=False):
+def attend(cache, q, new, slots, scale, causal, window, plane=0, tiles=False, out_f32=None):
     """O, LSE of the rows (fp64, on the CPU), and bounds on |O - ref| (before the output's rounding) and |LSE - ref|.
 
-    Few rows. The product of q and codes: bf16 queries are exact, fp32 ones are three bf16 terms (2^-24 of |q|); codes
-    carry a constant of up to 128 (4 bits) or 384 (8 bits), taken off after the sum, so the sums of D + 1 terms (three
-    times as many for fp32 queries), each cut off at 2^-23 of a partial sum, are off by at most (3 D) 2^-23 of
-    m = sum |q| (c + 2 * constant) in codes, s m in scores; scaling and offset are two fused operations a group,
-    below 4 * 2^-24 of s m + |z| sum |q|. A score error e moves its probability by the factor exp(e): O_d by at
-    most 2 e A_d, A_d = sum_j p_j |v_jd|, the LSE by e. Probabilities times scales enter as two bf16 terms (2^-16 of
-    s x, x the centred code) and p z' in fp32; ex2.approx adds 2^-22; sums over n keys (n / 16 + 32) 2^-23 and, for the
-    offsets, n 2^-24, each of M_d = sum_j p_j (s |x| + |z'|).
+    Few rows. q enters as fp16 times a power of two (2^-35 of its row's largest is lost), fp32 q in two terms (2^-22). A
+    product with codes of D columns takes D / 16 steps of the tensor cores (for each term), each of which cuts off at
+    2^-23 of a partial sum twice at most; where O is bf16 the codes carry a constant, 1024 (1024 / 16 a sixteenth of
+    it in places), taken off before the first step: the partial sums are at most m = sum |q| (c + 2048). Where O is fp32
+    they are centred codes x: m = sum |q| |x|. A score is s m 2^-23 (D / 8 + 2) (times the terms) off from that, and
+    two fused operations a group, below 4 * 2^-24 of s m + |z| sum |q|. A score error e moves its probability by the
+    factor exp(e): O_d by at most 2 e A_d, A_d = sum_j p_j |v_jd|, the LSE by e. Probabilities times scales enter as one
+    fp16 term (2^-11; O in bf16) or two (2^-22) of s x, and what lies under 2^-30 of the largest scale s' is lost (n keys,
+    the sum of probabilities being at least 1 as they are taken); p z' in fp32; ex2.approx adds 2^-22; sums over n keys
+    (n / 16 + 32) 2^-23 and, for the offsets, n 2^-24, each of M_d = sum_j p_j (s |x| + |z'|).
 
     Many rows (`tiles`): K, V and P are rounded to fp16 (half a step 2^-11): K and V after x s + z', s and z' rounded
     too: a value is off by at most 2^-11 of (|value| + |z'| + s |x|), and by 2^-24 of the largest of 64 keys where it is
     below 2^-14 of that (bounded here by the largest of all); q is fp16 exactly but for 2^-25 of its row's largest."""
     T, H, D = q.shape
+    f32 = q.dtype == torch.float32
     q = q.double().cpu()
     rep = H // cache.kv_heads
     mid = 8.0 if cache.bits == 4 else 128.0
-    const = 128.0 if cache.bits == 4 else 384.0
+    out_f32 = f32 if out_f32 is None else out_f32
+    terms = 2 if f32 else 1
     O = torch.zeros(T, H, D, dtype=torch.float64)
     L = torch.full((T, H), -math.inf, dtype=torch.float64)
     bo, bl = torch.zeros_like(O), torch.zeros(T, H, dtype=torch.float64)
@@ -150,18 +154,23 @@ def attend(cache, q, new, slots, scale, causal, window, plane=0, tiles=False):
                 off = qa @ (size_k * 2.0 ** -11 + size_k.max() * 2.0 ** -24).T + qa.amax(1, keepdim=True) * 2.0 ** -25 * size_k.sum(1)
                 e = scale * (off + qa @ size_k.T * D * 2.0 ** -23)
             else:
-                m = qa @ (ks * (kc + 2 * const))[:, i].T
-                e = scale * (3 * D * 2.0 ** -23 * m + 2.0 ** -22 * (m + qa @ kz[:, i].abs().T))
+                sizes = ks * ((kc - mid).abs() if out_f32 else kc + 2048.0)
+                m = qa @ sizes[:, i].T
+                e = scale * (terms * (D / 8 + 2) * 2.0 ** -23 * m + 2.0 ** -22 * (m + qa @ (kz.abs() + mid * ks)[:, i].T)
+                             + qa.amax(1, keepdim=True) * 2.0 ** -35 * (ks * (kc + mid))[:, i].sum(1))
+                if f32:
+                    e = e + scale * 2.0 ** -22 * (qa @ (k[:, i].abs() + ks[:, i] * mid).T)
             e = e.masked_fill(~see, 0.0).amax(1, keepdim=True)
             lse = torch.logsumexp(z, 1)
             w = torch.where(see, torch.exp(z - lse.nan_to_num(neginf=0.0)[:, None]), 0.0)
             O[at:at + n, h] = w @ v[:, i]
             L[at:at + n, h] = lse
             mass = vs * (vc - mid).abs() + (vz + mid * vs).abs()
-            up = 2.0 ** -16 + 2.0 ** -22 + (size / 16 + 32) * 2.0 ** -23 + size * 2.0 ** -24
+            up = (2.0 ** -22 if out_f32 else 2.0 ** -11) + 2.0 ** -22 + (size / 16 + 32) * 2.0 ** -23 + size * 2.0 ** -24
             if tiles:
                 up += 2.0 ** -11 + 2.0 ** -11
-            bo[at:at + n, h] = 2 * e * (w @ v[:, i].abs()) + up * (w @ mass[:, i])
+            lost = size * 2.0 ** -30 * float(vs[:, i].max()) * mid
+            bo[at:at + n, h] = 2 * e * (w @ v[:, i].abs()) + up * (w @ mass[:, i]) + lost
             if tiles:
                 bo[at:at + n, h] += 2.0 ** -24 * mass[:, i].max()
             bl[at:at + n, h] = e[:, 0] + (size / 16 + 32) * 2.0 ** -23 + lse.nan_to_num(neginf=0.0).abs() * 2.0 ** -22

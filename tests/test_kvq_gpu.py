@@ -191,17 +191,20 @@ def check_attend(kv, dtype, new, lens, page, H, HKV, D, bits, group, causal=True
     out, lse = torch.full((T + pad, H, D), 7.0, dtype=odt, device="cuda"), torch.full((T + pad, H), 7.0, device="cuda")
     cache.attend(q, cu_of(new), vec(*order), scale, causal, window, layer=1, out=out, lse=lse)
     cache.check()
-    want, want_l, bo, bl = ref.attend(cache, q[:T], new, order, D ** -0.5 if scale is None else scale, causal, window, 1, tiles)
+    want, want_l, bo, bl = ref.attend(cache, q[:T], new, order, D ** -0.5 if scale is None else scale, causal, window, 1, tiles,
+                                      odt == F32)
     _kv_ref.close(out[:T].cpu(), want, bo, "O")
     seen = torch.isfinite(want_l)
     assert torch.equal(lse[:T].cpu() == -math.inf, ~seen)
     err = (lse[:T].cpu().double() - want_l)[seen].abs()
     assert bool((err <= bl[seen]).all()), float(err.max())
     assert bool((out[T:] == 7.0).all()) and bool((lse[T:] == 7.0).all())
-    # ... and as near as such arithmetic usually is: an order of magnitude inside the worst case
+    # ... and as near as such arithmetic usually is, which is far inside the worst case: a bf16 output is its own rounding
+    # (2^-8 / sqrt(12) of O's powers of two: 1.7e-3) and little more; probabilities of scores that are four times as
+    # large as usual (scale 0.3) move four times as far with the rounding of tiles' K
     if T and bool(seen.any()):
         off = float((out[:T].cpu().double() - want).norm() / want.norm())
-        assert off < (5e-3 if odt == BF or tiles else 1e-5), off
+        assert off < (2.5e-3 if odt == BF else 2e-3 if tiles else 2e-6), off
     return cache, q, out, lse
 
 
