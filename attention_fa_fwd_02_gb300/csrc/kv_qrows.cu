@@ -260,9 +260,9 @@ __global__ void __launch_bounds__(NTHREADS, QRowsCfg<E, OUT_BF, BITS, D, NG_, NT
 #pragma unroll
         for (int z = 0; z < 4; ++z) {
           const int c0 = BITS == 4 ? z : 2 * z, c1 = BITS == 4 ? z + 4 : 2 * z + 1;
-          const float by = down / q_factor<BITS>(z);
-          float2 v = make_float2(y[i][c0] * by, y[i][c1] * by);
-          sum[NG > 1 ? i / 2 : 0] += (v.x + v.y) * q_factor<BITS>(z);
+          constexpr float FACTOR = q_factor<BITS>(1);
+          float2 v = make_float2(y[i][c0] * (down / FACTOR), y[i][c1] * (down / FACTOR));
+          sum[NG > 1 ? i / 2 : 0] += (v.x + v.y) * FACTOR;
           bias[NG > 1 ? i / 2 : 0] -= (v.x + v.y) * 1024.f;
           f[0][z] = half2_of(v.x, v.y, &v);
           f[1][z] = half2_of(v.x, v.y);
@@ -351,11 +351,11 @@ __global__ void __launch_bounds__(NTHREADS, QRowsCfg<E, OUT_BF, BITS, D, NG_, NT
               word[e] = *reinterpret_cast<const uint32_t*>(slot + ((kt * 2 + e) * CH + w) * 128 + lane * 4);
             auto product = [&](auto pair, uint32_t b0, uint32_t b1, int nt) {  // code pairs `pair` and + 1
               constexpr int P = decltype(pair)::value;
-              uint32_t f[4] = {q_raise<BITS, P>(word[0], a.raised), q_raise<BITS, P>(word[1], a.raised), q_raise<BITS, P + 1>(word[0], a.raised),
-                               q_raise<BITS, P + 1>(word[1], a.raised)};
+              uint32_t f[4] = {q_raise16<BITS, P>(word[0], a.raised), q_raise16<BITS, P>(word[1], a.raised),
+                               q_raise16<BITS, P + 1>(word[0], a.raised), q_raise16<BITS, P + 1>(word[1], a.raised)};
               if constexpr (CENTRED) {
-                f[0] = q_centred<BITS, P>(f[0]); f[1] = q_centred<BITS, P>(f[1]);
-                f[2] = q_centred<BITS, P + 1>(f[2]); f[3] = q_centred<BITS, P + 1>(f[3]);
+#pragma unroll
+                for (int e = 0; e < 4; ++e) f[e] = q_centred<BITS, 1>(f[e]);  // (all with the factor)
               }
               mma_f16(acc[k][kt][nt], f, b0, b1);
             };
