@@ -53,14 +53,14 @@ bool encode_tiled_3d(CUtensorMap* map, CUtensorMapDataType dt, int esize, const 
 }
 
 bool encode_tiled_4d(CUtensorMap* map, const void* base, const uint64_t (&dims)[4],
-                     const uint64_t (&strides)[3], const uint32_t (&box)[4]) {
+                     const uint64_t (&strides)[3], const uint32_t (&box)[4], bool swizzle) {
   if (!load_encoder()) return false;
   const cuuint64_t d[4] = {dims[0], dims[1], dims[2], dims[3]};
   const cuuint64_t st[3] = {strides[0], strides[1], strides[2]};
   const cuuint32_t b[4] = {box[0], box[1], box[2], box[3]}, es[4] = {1, 1, 1, 1};
   return g_encode(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, const_cast<void*>(base), d, st, b, es,
-                  CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_128B,
-                  CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+                  CU_TENSOR_MAP_INTERLEAVE_NONE, swizzle ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_NONE,
+                  CU_TENSOR_MAP_L2_PROMOTION_L2_128B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
 static cudaError_t pool_for_current_device(cudaMemPool_t* out) {

@@ -10,9 +10,9 @@
 namespace fa {
 namespace host {
 // A 4-D tensor map of 16-bit elements (innermost dimension without gaps, the others'
-// strides in bytes), 128-byte swizzle, zeros outside.
+// strides in bytes), 128-byte swizzle or none, zeros outside.
 bool encode_tiled_4d(CUtensorMap* map, const void* base, const uint64_t (&dims)[4],
-                     const uint64_t (&strides)[3], const uint32_t (&box)[4]);
+                     const uint64_t (&strides)[3], const uint32_t (&box)[4], bool swizzle = true);
 }  // namespace host
 
 namespace kv {

@@ -76,20 +76,28 @@ struct TilesCfg {
   static constexpr int D = D_;
   static constexpr int NQ = 2;
   static constexpr uint32_t FMT = BITS ? FMT_F16 : FMT_BF16;
+  static constexpr bool CODES = BITS != 0;
   static constexpr int NCB = D / 64;                      // 64-column blocks
   static constexpr uint32_t CB_BYTES = 128u * 128u;       // one block of a 128-row tile
   static constexpr uint32_t TILE_BYTES = NCB * CB_BYTES;
-  static constexpr int KST = D == 128 ? 2 : 3;
+  // codes of 8 bits: K in two planes (see the code warps), of a stage
+  static constexpr int PLANES = BITS == 8 ? 2 : 1;
+  static constexpr int KST = BITS == 8 ? (D == 128 ? 1 : 2) : D == 128 ? 2 : 3;
+  static constexpr uint32_t K_STAGE = PLANES * TILE_BYTES;
   static constexpr int VST = BITS ? 2 : 3;
   static constexpr uint32_t EPI_BOX = 32u * 128u;         // a warp's staging: 32 rows x 128 bytes
   static constexpr uint32_t V_STAGE = std::max(TILE_BYTES, 4 * NQ * EPI_BOX);
   static constexpr uint32_t Q_OFF = 0;
   static constexpr uint32_t K_OFF = Q_OFF + NQ * TILE_BYTES;
-  static constexpr uint32_t V_OFF = K_OFF + KST * TILE_BYTES;
+  static constexpr uint32_t V_OFF = K_OFF + KST * K_STAGE;
   static constexpr uint32_t OCTET = D * BITS;              // bytes of eight keys' codes
-  static constexpr uint32_t RING = 4 * OCTET;              // of a code warp: its octets of a tile
+  static constexpr int AHEAD = PLANES == 2 ? 2 : 4;        // octets on their way to a code warp (four to a tile)
+  static constexpr uint32_t RING = AHEAD * OCTET;
   static constexpr uint32_t CODES_OFF = V_OFF + VST * V_STAGE;
-  static constexpr uint32_t SMEM = CODES_OFF + 8 * RING + 1024;
+  // codes: eight columns more of Q and K, for the offsets (and eight of zeros to make up the product's sixteen)
+  static constexpr uint32_t MORE = 128u * 16u;
+  static constexpr uint32_t QMORE_OFF = CODES_OFF + 8 * RING, KMORE_OFF = QMORE_OFF + NQ * MORE, ZERO_OFF = KMORE_OFF + KST * MORE;
+  static constexpr uint32_t SMEM = (BITS ? ZERO_OFF + MORE : CODES_OFF) + 1024;
   static constexpr int SOFTMAX_WARPS = 8, MMA_WARP = 8, KQ_WARP = 9, V_WARP = 10, RELAY_WARP = 11;
   static constexpr uint32_t RELAY_BAR = 3;  // named barrier (1 + q: P_q written)
   static constexpr int CODE_WARP = 12;  // codes: four warps for K's tiles, four for V's, a quarter of a tile each
@@ -119,13 +127,18 @@ __device__ __forceinline__ uint32_t pack_bf2(float lo, float hi) {
 }
 
 template <class C>
-__device__ __forceinline__ void issue_qk(uint32_t d_tmem, uint32_t sq, uint32_t sk) {
+__device__ __forceinline__ void issue_qk(uint32_t d_tmem, uint32_t sq, uint32_t sk, uint32_t q_more, uint32_t k_more, uint32_t zero) {
   constexpr uint32_t id = make_idesc(128, 128, C::FMT, C::FMT, false, false);
+  // (rows of 16 bytes, without a swizzle: eight rows 128 bytes on, the next eight columns -- zeros -- where `zero` is)
+  if (C::CODES) mma_f16_ss(d_tmem, make_sdesc(q_more, zero - q_more, 128, 0), make_sdesc(k_more, zero - k_more, 128, 0), id, 0);
 #pragma unroll
-  for (int kk = 0; kk < C::D / 16; ++kk) {
-    const uint32_t off = (kk / 4) * C::CB_BYTES + (kk % 4) * 32;
-    mma_f16_ss(d_tmem, make_sdesc(sq + off, 16, SW128_ATOM), make_sdesc(sk + off, 16, SW128_ATOM), id, kk > 0);
-  }
+  for (int plane = 0; plane < C::PLANES; ++plane)
+#pragma unroll
+    for (int kk = 0; kk < C::D / 16; ++kk) {
+      const uint32_t off = (kk / 4) * C::CB_BYTES + (kk % 4) * 32;
+      mma_f16_ss(d_tmem, make_sdesc(sq + off, 16, SW128_ATOM), make_sdesc(sk + plane * C::TILE_BYTES + off, 16, SW128_ATOM), id,
+                 kk > 0 || C::CODES);
+    }
 }
 template <class C, int TERMS>
 __device__ __forceinline__ void issue_pv(uint32_t o_tmem, uint32_t p_tmem, uint32_t sv, bool accumulate) {
@@ -207,11 +220,14 @@ constexpr int TILE_INFO = 8;  // tiles whose powers of two are kept: K's codes a
 
 // q as fp16, each row times a power of two that brings its largest value to 2^14 (exactly, but for what is 2^-28 of
 // that), and what undoes it, times the softmax scale; `pairs`: each eight columns in the order 0 4 1 5 2 6 3 7, which is
-// that of K's 4-bit codes. Sixteen lanes to a row. A row with NaN or infinity becomes NaN.
+// that of K's 4-bit codes. Beside it eight columns more, for K's offsets: of each group the sum S of q, times 2^-8, as
+// two fp16 terms, high, low and high again (for the offset's high, high and low term). Sixteen lanes to a row. A row with
+// NaN or infinity becomes NaN.
 constexpr int QROWS_THREADS = 256;
+constexpr float Q_SUM = 0x1p-8f;
 __global__ void __launch_bounds__(QROWS_THREADS) qattend_q_kernel(const __nv_bfloat16* q, long long q_token, long long q_head,
-                                                                  int rows, Div heads, int D, float sl2, bool pairs,
-                                                                  uint16_t* out, float* factor) {
+                                                                  int rows, Div heads, int D, int groups, float sl2, bool pairs,
+                                                                  uint16_t* out, uint4* more, float* factor) {
   grid_launch_dependents();
   const int lane = threadIdx.x & 15, row = blockIdx.x * (QROWS_THREADS / 16) + threadIdx.x / 16;
   const int token = heads.of(min(row, rows - 1)), col = lane * 8;
@@ -238,21 +254,38 @@ __global__ void __launch_bounds__(QROWS_THREADS) qattend_q_kernel(const __nv_bfl
   }
   const int e = min(max(q_exponent(top), -60), 127);
   const float by = fine ? q_pow2(14 - e) : __int_as_float(0x7fffffff);
-  if (row >= rows) return;
-  if (col < D) {
-    uint32_t y[4];
+  uint32_t y[4];
+  float sum = 0.f;
 #pragma unroll
-    for (int i = 0; i < 4; ++i)
-      y[i] = q_half2((pairs ? x[i] : x[2 * i]) * by, (pairs ? x[i + 4] : x[2 * i + 1]) * by);
-    *reinterpret_cast<uint4*>(out + (size_t)row * D + col) = make_uint4(y[0], y[1], y[2], y[3]);
+  for (int i = 0; i < 4; ++i) {
+    y[i] = q_half2((pairs ? x[i] : x[2 * i]) * by, (pairs ? x[i + 4] : x[2 * i + 1]) * by);
+    const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&y[i]));
+    sum += f.x + f.y;
   }
-  if (lane == 0) factor[row] = sl2 * q_pow2(e - 14);
+#pragma unroll
+  for (int d = 1; d < 8; d <<= 1) sum += __shfl_xor_sync(0xffffffffu, sum, d);
+  float other = __shfl_xor_sync(0xffffffffu, sum, 8);  // (of the second group, in the first lane)
+  if (groups == 1) {
+    sum += other;
+    other = 0.f;
+  }
+  if (row >= rows) return;
+  if (col < D) *reinterpret_cast<uint4*>(out + (size_t)row * D + col) = make_uint4(y[0], y[1], y[2], y[3]);
+  if (lane == 0) {
+    const uint32_t h = q_half2(sum * Q_SUM, other * Q_SUM);  // (low half: first group)
+    const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&h));
+    const uint32_t l = q_half2(sum * Q_SUM - f.x, other * Q_SUM - f.y);
+    // h0 l0 | h0 h1 | l1 h1 | 0 0
+    more[row] = make_uint4(__byte_perm(h, l, 0x5410), h, __byte_perm(l, h, 0x7632), 0u);
+    factor[row] = sl2 * q_pow2(e - 14);
+  }
 }
 
 template <int D, int TERMS, int BITS>
 __global__ void __launch_bounds__(TilesCfg<D, BITS>::THREADS, 1)
     attend_tiles_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
                         const __grid_constant__ CUtensorMap tmV, const __grid_constant__ TilesArgs a) {
+  // (codes: K and V have no map; tmK is that of q's columns more)
   using C = TilesCfg<D, BITS>;
   constexpr int NQ = C::NQ, KST = C::KST, VST = C::VST;
   extern __shared__ uint8_t smem_raw[];
@@ -290,7 +323,10 @@ __global__ void __launch_bounds__(TilesCfg<D, BITS>::THREADS, 1)
   }
   Seq seq;
   const Part part = find_part<C::THREADS, 1>(a.g, a.c, a.cu, a.slots, a.B, a.T, reinterpret_cast<int*>(smem), plan, seq);
-  if constexpr (BITS != 0) grid_dependency_wait();  // (q as fp16)
+  if constexpr (BITS != 0) {
+    if (threadIdx.x < C::MORE / 16) st_shared_v4(smem_u32(smem) + C::ZERO_OFF + threadIdx.x * 16, 0, 0, 0, 0);
+    grid_dependency_wait();  // (q as fp16)
+  }
   // (the plan's scratch lies in the tiles: its generic accesses before the copies' writes)
   fence_async_shared();
   tc_fence_before();
@@ -299,7 +335,9 @@ __global__ void __launch_bounds__(TilesCfg<D, BITS>::THREADS, 1)
   const uint32_t tmem = tmem_base_sh;
   const uint32_t sbase = smem_u32(smem);
   auto sQ = [&](int q) { return sbase + C::Q_OFF + q * C::TILE_BYTES; };
-  auto sK = [&](int st) { return sbase + C::K_OFF + st * C::TILE_BYTES; };
+  auto sK = [&](int st) { return sbase + C::K_OFF + st * C::K_STAGE; };
+  auto sQmore = [&](int q) { return sbase + C::QMORE_OFF + q * C::MORE; };
+  auto sKmore = [&](int st) { return sbase + C::KMORE_OFF + st * C::MORE; };
   auto sV = [&](int st) { return sbase + C::V_OFF + st * C::V_STAGE; };
   auto wait = [&](uint64_t* bar, uint32_t parity) {
     return mbar_wait(bar, parity, abort_flag, &g_kv_status, DEV_TIMEOUT, a.limit_ns);
@@ -345,9 +383,12 @@ __global__ void __launch_bounds__(TilesCfg<D, BITS>::THREADS, 1)
   if (BITS && warp >= C::CODE_WARP) {
     // ------------------------------------------------------------ codes of K, of V
     // Each of four warps writes 32 keys of every tile, as the copies of bf16 pages would have laid them down, in fp16:
-    // times a power of two that keeps the largest of the 32 keys' values just below 2^8 (K: undone in the scores) or
-    // 2^7 (V: undone in the probabilities); 2^-12 of a value, or 2^-32 of the largest, is rounded off. A tile's codes are
-    // on their way while the one before it is turned into numbers. Keys that no row sees, and those of a missing page,
+    // times a power of two that keeps the largest of the 32 keys' values just below 2^4 (K: undone in the scores) or
+    // 2^7 (V: undone in the probabilities). V is x s + z', rounded to 2^-12 of it. A score's error moves a probability by
+    // its factor, so K is not rounded: x s of a nibble x in -8 .. 7 has the eleven bits of fp16 (of a byte it is two such
+    // terms, 16 (h - 8) s and (l - 8) s, in two planes), and z' (two terms) is multiplied with the row's sum of q in one
+    // step of the product more. (K as x s + z' in one term had LSEs 8e-6 off, and 3e-5 where few keys were seen.) The
+    // codes are on their way while those before are turned into numbers. Keys that no row sees, and those of a missing page,
     // are zeros; a key whose scale is NaN, in K or in V, is NaN in K and zeros in V, so that rows that see it become NaN
     // and the tile's others do not.
     regs_decrease<C::REGS_CODES>();
@@ -356,7 +397,7 @@ __global__ void __launch_bounds__(TilesCfg<D, BITS>::THREADS, 1)
         constexpr bool IS_V = decltype(is_v)::value;
         constexpr int CH = D * BITS / 128, PIECES = CH >= 4 ? CH / 4 : 1;  // chunks of a key; a lane's pieces of an octet
         constexpr int NG = D / 64;
-        constexpr float CENTRE = BITS == 4 ? 8.f : 128.f, STEPS = BITS == 4 ? 15.f : 255.f;
+        constexpr float V_CENTRE = BITS == 4 ? 8.f : 128.f, K_CENTRE = BITS == 4 ? 8.f : 136.f, STEPS = BITS == 4 ? 15.f : 255.f;
         const int quarter = (warp - C::CODE_WARP) & 3;  // of the tile
         const int chunks = a.qc.chunks, ng = a.qc.groups;
         const uint8_t* const base = IS_V ? a.qc.V : a.qc.K;
@@ -396,13 +437,14 @@ __global__ void __launch_bounds__(TilesCfg<D, BITS>::THREADS, 1)
 #pragma unroll
           for (int z = 0; z < PIECES; ++z) {
             const bool take = p >= 0 && chunk0 + 4 * z < chunks;
-            if (chunk0 + 4 * z < CH) cp_piece(ring + octet * C::OCTET + at + z * 512, take ? from + at + z * 512 : base, take);
+            if (chunk0 + 4 * z < CH) cp_piece(ring + octet % C::AHEAD * C::OCTET + at + z * 512, take ? from + at + z * 512 : base, take);
           }
           asm volatile("cp.async.commit_group;" ::: "memory");
         };
         // scale (low) and z' (high) of key `lane`, as fp16 times the quarter's power of two
         struct Factors {
           uint32_t f[NG];
+          float z[IS_V ? 1 : 2];  // K: z' in fp32, of the first and of the second group
         };
         auto nan = [](const uint32_t (&p)[NG]) {
           bool bad = false;
@@ -420,16 +462,18 @@ __global__ void __launch_bounds__(TilesCfg<D, BITS>::THREADS, 1)
           return min(max(q_exponent(top), -100), 126);
         };
         auto factors = [&](const Params& b, float2* info) {
-          const int ev = exponent_of(b.v) - 6, e = IS_V ? ev : exponent_of(b.k) - 7;
+          const int ev = exponent_of(b.v) - 6, e = IS_V ? ev : exponent_of(b.k) - 3;
           if (!IS_V && lane == 0) *info = make_float2(q_pow2(e), (float)ev);
           const float by = q_pow2(-e);
           const bool bad = nan(b.v) || (!IS_V && nan(b.k));
           Factors f;
+          if constexpr (!IS_V) f.z[0] = f.z[1] = 0.f;
 #pragma unroll
           for (int j = 0; j < NG; ++j) {
             const uint32_t p = IS_V ? b.v[j] : b.k[j];
-            const float s = q_scale(p);
-            f.f[j] = bad ? (IS_V ? 0u : 0x7fff7fffu) : q_half2(s * by, fmaf(s, CENTRE, q_offset(p)) * by);
+            const float s = q_scale(p), z = fmaf(s, IS_V ? V_CENTRE : K_CENTRE, q_offset(p)) * by;
+            f.f[j] = bad ? (IS_V ? 0u : 0x7fff7fffu) : q_half2(s * by, z);
+            if constexpr (!IS_V) f.z[j] = bad || (j > 0 && ng == 1) ? 0.f : z;
           }
           return f;
         };
@@ -445,22 +489,23 @@ __global__ void __launch_bounds__(TilesCfg<D, BITS>::THREADS, 1)
               const int col = (chunk0 + 4 * z) * (128 / BITS);
               if (col >= D) continue;
               // 16-byte piece c of row r + e
-              auto put = [&](int e, int c, uint32_t x0, uint32_t x1, uint32_t x2, uint32_t x3) {
-                st_shared_v4(tile + (c >> 3) * C::CB_BYTES + (r + e) * 128 + (((c & 7) ^ ((r + e) & 7)) << 4), x0, x1, x2, x3);
+              auto put = [&](int e, int c, uint32_t x0, uint32_t x1, uint32_t x2, uint32_t x3, uint32_t plane = 0) {
+                st_shared_v4(tile + plane + (c >> 3) * C::CB_BYTES + (r + e) * 128 + (((c & 7) ^ ((r + e) & 7)) << 4), x0, x1, x2, x3);
               };
               const bool upper = NG > 1 && col >= 64;
               const uint32_t p0 = upper ? sz[NG - 1][0] : sz[0][0], p1 = IS_V ? (upper ? sz[NG - 1][IS_V] : sz[0][IS_V]) : p0;
               const uint32_t s = __byte_perm(p0, p1, 0x5410), zz = __byte_perm(p0, p1, 0x7632);
-              const float4 piece = ld_shared_v4(ring + octet * C::OCTET + at + z * 512);
+              const float4 piece = ld_shared_v4(ring + octet % C::AHEAD * C::OCTET + at + z * 512);
               const uint32_t words[4] = {__float_as_uint(piece.x), __float_as_uint(piece.y), __float_as_uint(piece.z), __float_as_uint(piece.w)};
               if constexpr (BITS == 4) {
-                const uint32_t s16 = q_fma2(s, 0x2c002c00u, 0u);  // s / 16
+                const uint32_t s16 = q_mul2(s, 0x2c002c00u);  // s / 16
                 // the four pairs of a word: K: columns n and n + 4; V: column n of both tokens
+                auto number = [&](uint32_t x, uint32_t by) { return IS_V ? q_fma2(x, by, zz) : q_mul2(x, by); };
                 auto pairs = [&](uint32_t w, uint32_t (&x)[4]) {
-                  x[0] = q_fma2(q_centred<4, 0>(q_raise<4, 0>(w, a.raised)), s, zz);
-                  x[1] = q_fma2(q_centred<4, 1>(q_raise<4, 1>(w, a.raised)), s16, zz);
-                  x[2] = q_fma2(q_centred<4, 2>(q_raise<4, 2>(w, a.raised)), s, zz);
-                  x[3] = q_fma2(q_centred<4, 3>(q_raise<4, 3>(w, a.raised)), s16, zz);
+                  x[0] = number(q_centred<4, 0>(q_raise<4, 0>(w, a.raised)), s);
+                  x[1] = number(q_centred<4, 1>(q_raise<4, 1>(w, a.raised)), s16);
+                  x[2] = number(q_centred<4, 2>(q_raise<4, 2>(w, a.raised)), s);
+                  x[3] = number(q_centred<4, 3>(q_raise<4, 3>(w, a.raised)), s16);
                 };
                 if constexpr (!IS_V) {
 #pragma unroll
@@ -485,15 +530,24 @@ __global__ void __launch_bounds__(TilesCfg<D, BITS>::THREADS, 1)
                 }
               } else {
                 uint32_t x[4][2];  // of each word, K: columns 0, 1 and 2, 3; V: column 0 and column 1 of both tokens
-#pragma unroll
-                for (int k = 0; k < 4; ++k) {
-                  x[k][0] = q_fma2(q_centred<8, 0>(q_raise<8, 0>(words[k], a.raised)), s, zz);
-                  x[k][1] = q_fma2(q_centred<8, 1>(q_raise<8, 1>(words[k], a.raised)), s, zz);
-                }
                 if constexpr (!IS_V) {
-                  put(0, col / 8, x[0][0], x[0][1], x[1][0], x[1][1]);
-                  put(0, col / 8 + 1, x[2][0], x[2][1], x[3][0], x[3][1]);
+#pragma unroll
+                  for (int plane = 0; plane < 2; ++plane) {  // 16 h, then l
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) {
+                      const uint32_t r0 = q_raise<8, 0>(words[k], a.raised), r1 = q_raise<8, 1>(words[k], a.raised);
+                      x[k][0] = q_mul2(plane ? q_centred<4, 0>(r0 & 0xff0fff0fu) : q_centred<4, 1>(r0 & 0xfff0fff0u), s);
+                      x[k][1] = q_mul2(plane ? q_centred<4, 0>(r1 & 0xff0fff0fu) : q_centred<4, 1>(r1 & 0xfff0fff0u), s);
+                    }
+                    put(0, col / 8, x[0][0], x[0][1], x[1][0], x[1][1], plane * C::TILE_BYTES);
+                    put(0, col / 8 + 1, x[2][0], x[2][1], x[3][0], x[3][1], plane * C::TILE_BYTES);
+                  }
                 } else {
+#pragma unroll
+                  for (int k = 0; k < 4; ++k) {
+                    x[k][0] = q_fma2(q_centred<8, 0>(q_raise<8, 0>(words[k], a.raised)), s, zz);
+                    x[k][1] = q_fma2(q_centred<8, 1>(q_raise<8, 1>(words[k], a.raised)), s, zz);
+                  }
 #pragma unroll
                   for (int e = 0; e < 2; ++e) {
                     const uint32_t sel = e ? 0x7632 : 0x5410;
@@ -515,18 +569,28 @@ __global__ void __launch_bounds__(TilesCfg<D, BITS>::THREADS, 1)
           page = octet_page(kt);
           page_next = left > 0 ? octet_page(kt + 1) : -1;
           ask_params(params, kt, page);
-          for (int i = 0; i < 4; ++i) ask(kt, page, i);
+          asm volatile("cp.async.wait_all;" ::: "memory");  // (what the last item's end asked for beyond it: zeros)
+          for (int i = 0; i < C::AHEAD; ++i) ask(kt, page, i);
         };
-        auto tile = [&](int kt, int left, uint32_t to, uint64_t* full, float2* info, auto free) {
+        auto tile = [&](int kt, int left, uint32_t to, uint32_t more, uint64_t* full, float2* info, auto free) {
           ask_params(params_next, kt + 1, page_next);
           const int page_after = left > 1 ? octet_page(kt + 2) : -1;
           if (!free()) return false;
           const Factors f = factors(params, info);
+          if constexpr (!IS_V) {
+            // z' 2^8 of key `lane`, high, high and low term of each group (for the high, low and high one of q's sums)
+            const uint32_t h = q_half2(f.z[0] / Q_SUM, f.z[1] / Q_SUM);
+            const float2 g = __half22float2(*reinterpret_cast<const __half2*>(&h));
+            const uint32_t l = q_half2(f.z[0] / Q_SUM - g.x, f.z[1] / Q_SUM - g.y);
+            // h0 h0 | l0 h1 | h1 l1 | 0 0
+            st_shared_v4(more + (quarter * 32 + lane) * 16, __byte_perm(h, h, 0x1010), __byte_perm(l, h, 0x7610), __byte_perm(h, l, 0x7632), 0u);
+          }
 #pragma unroll 1
           for (int i = 0; i < 4; ++i) {
-            asm volatile("cp.async.wait_group 3;" ::: "memory");
+            asm volatile("cp.async.wait_group %0;" ::"n"(C::AHEAD - 1) : "memory");
             write(f, to, i);
-            ask(kt + 1, page_next, i);
+            const bool over = i + C::AHEAD >= 4;
+            ask(over ? kt + 1 : kt, over ? page_next : page, (i + C::AHEAD) & 3);
           }
           params = params_next;
           page = page_next;
@@ -543,7 +607,7 @@ __global__ void __launch_bounds__(TilesCfg<D, BITS>::THREADS, 1)
             if (seg.n > 0) begin(seg.k0, seg.n - 1);
             for (int t = 0; ok && t < seg.n; ++t, ++g) {
               const int ks = g % KST;
-              ok = tile(seg.k0 + t, seg.n - 1 - t, sK(ks), &bar_kfull[ks], &info_sh[g % TILE_INFO][quarter],
+              ok = tile(seg.k0 + t, seg.n - 1 - t, sK(ks), sKmore(ks), &bar_kfull[ks], &info_sh[g % TILE_INFO][quarter],
                         [&] { return __all_sync(0xffffffffu, wait_free(&bar_kempty[ks], ((g / KST) & 1) ^ 1)) != 0; });
             }
           }
@@ -564,7 +628,7 @@ __global__ void __launch_bounds__(TilesCfg<D, BITS>::THREADS, 1)
           while (ok && next()) {
             if (seg.n > 0) begin(seg.k0, seg.n - 1);
             for (int t = 0; ok && t < seg.n; ++t, ++pos)
-              ok = tile(seg.k0 + t, seg.n - 1 - t, sV(pos % VST), &bar_vfull[pos % VST], nullptr,
+              ok = tile(seg.k0 + t, seg.n - 1 - t, sV(pos % VST), 0u, &bar_vfull[pos % VST], nullptr,
                         [&] { return pos < (uint32_t)VST || wait_release(pos - VST); });
             if (!ok) break;
             if (pos >= (uint32_t)VST && !(ok = wait_release(pos - VST))) break;
@@ -592,10 +656,10 @@ __global__ void __launch_bounds__(TilesCfg<D, BITS>::THREADS, 1)
         for (int q = 0; ok && q < NQ; ++q) {
           if (j > 0 && !(ok = __all_sync(0xffffffffu, wait_free(&bar_qfree[q], (j - 1) & 1)))) break;
           if (lane == 0) {
-            mbar_arrive_expect_tx(&bar_q[q], C::NCB * 128u * a.RT);
-            for (int cb = 0; cb < C::NCB; ++cb)
-              tma_load_4d(sQ(q) + cb * C::CB_BYTES, &tmQ, &bar_q[q], cb * 64, 0,
-                          seg.s.row0 + a.g.rep.of(seg.x.rho0) + q * a.tpt, seg.head);
+            mbar_arrive_expect_tx(&bar_q[q], (C::NCB * 128u + 16u) * a.RT);
+            const int row = seg.s.row0 + a.g.rep.of(seg.x.rho0) + q * a.tpt;
+            for (int cb = 0; cb < C::NCB; ++cb) tma_load_4d(sQ(q) + cb * C::CB_BYTES, &tmQ, &bar_q[q], cb * 64, 0, row, seg.head);
+            tma_load_4d(sQmore(q), &tmK, &bar_q[q], 0, 0, row, seg.head);
           }
           __syncwarp();
         }
@@ -694,7 +758,7 @@ __global__ void __launch_bounds__(TilesCfg<D, BITS>::THREADS, 1)
           named_bar_sync(C::RELAY_BAR, 64);
           tc_fence_after();
           if (leader) {
-            issue_qk<C>(tmem + C::s_col(q), sQ(q), sK(k0));
+            issue_qk<C>(tmem + C::s_col(q), sQ(q), sK(k0), sQmore(q), sKmore(k0), sbase + C::ZERO_OFF);
             tc_commit(&bar_s[q]);
             if (n == 1) tc_commit(&bar_qfree[q]);
           }
@@ -712,7 +776,7 @@ __global__ void __launch_bounds__(TilesCfg<D, BITS>::THREADS, 1)
             if (leader) {
               issue_pv<C, TERMS>(tmem + C::o_col(q), tmem + C::s_col(q), sV(vs), t > 0);
               if (more) {
-                issue_qk<C>(tmem + C::s_col(q), sQ(q), sK(ks));
+                issue_qk<C>(tmem + C::s_col(q), sQ(q), sK(ks), sQmore(q), sKmore(ks), sbase + C::ZERO_OFF);
                 tc_commit(&bar_s[q]);
                 if (t + 2 == n) tc_commit(&bar_qfree[q]);
               } else {
@@ -1058,13 +1122,13 @@ fa_status run(TilesArgs& a, const CUtensorMap& q, const CUtensorMap& k, const CU
   return st;
 }
 
-// q as [HKV][T][rep][D]
-bool map_q(CUtensorMap* m, const TilesArgs& a, const void* q, long long token, long long head) {
+// q as [HKV][T][rep][D] (`columns` D; or 8 more, of 16 bytes to a row and without a swizzle)
+bool map_q(CUtensorMap* m, const TilesArgs& a, const void* q, long long token, long long head, int columns) {
   const int rep = a.g.rep.d;
-  const uint64_t qd[4] = {(uint64_t)a.c.D, (uint64_t)rep, (uint64_t)a.T, (uint64_t)a.c.HKV};
+  const uint64_t qd[4] = {(uint64_t)columns, (uint64_t)rep, (uint64_t)a.T, (uint64_t)a.c.HKV};
   const uint64_t qs[3] = {(uint64_t)head * 2, (uint64_t)token * 2, (uint64_t)head * rep * 2};
-  const uint32_t qb[4] = {64, (uint32_t)rep, (uint32_t)a.tpt, 1};
-  return host::encode_tiled_4d(m, q, qd, qs, qb);
+  const uint32_t qb[4] = {columns == 8 ? 8u : 64u, (uint32_t)rep, (uint32_t)a.tpt, 1};
+  return host::encode_tiled_4d(m, q, qd, qs, qb, columns != 8);
 }
 
 TilesArgs args_of(void* O, float* LSE, const int* cu, const int* slots, const fakv_cache& c, const fakv_tokens& p) {
@@ -1103,7 +1167,7 @@ fa_status launch_attend_tiles(const void* q, void* O, float* LSE, const int* cu,
   const uint64_t ks[3] = {(uint64_t)c.token_stride * b2, (uint64_t)c.head_stride * b2, (uint64_t)c.page_stride * b2};
   const uint32_t kb[4] = {64, (uint32_t)a.box, 1, 1};
   const long long plane = p.plane * c.plane_stride * 2;
-  if (!map_q(&mq, a, q, p.q_token, p.q_head) || !host::encode_tiled_4d(&mk, static_cast<const char*>(c.K) + plane, kd, ks, kb) ||
+  if (!map_q(&mq, a, q, p.q_token, p.q_head, c.D) || !host::encode_tiled_4d(&mk, static_cast<const char*>(c.K) + plane, kd, ks, kb) ||
       !host::encode_tiled_4d(&mv, static_cast<const char*>(c.V) + plane, kd, ks, kb))
     return FA_ERR_UNSUPPORTED;
   if (a.out_bf16) return c.D <= 64 ? run<64, 1, 0>(a, mq, mk, mv, s) : run<128, 1, 0>(a, mq, mk, mv, s);
@@ -1117,22 +1181,22 @@ fa_status launch_qattend_tiles(const void* q, void* O, float* LSE, const int* cu
   a.qc = qc;
   a.raised = Q_RAISED;
   const int D = qc.c.D, rows = p.T * p.H;
-  const size_t row_bytes = ((size_t)rows * D * 2 + 255) & ~(size_t)255;
+  const size_t row_bytes = ((size_t)rows * D * 2 + 255) & ~(size_t)255, more_bytes = ((size_t)rows * 16 + 255) & ~(size_t)255;
   void* w = nullptr;
-  if (host::scratch_alloc(&w, row_bytes + (size_t)rows * 4, s) != cudaSuccess) return failed();
-  float* const qf = reinterpret_cast<float*>(static_cast<char*>(w) + row_bytes);
+  if (host::scratch_alloc(&w, row_bytes + more_bytes + (size_t)rows * 4, s) != cudaSuccess) return failed();
+  char* const more = static_cast<char*>(w) + row_bytes;
+  float* const qf = reinterpret_cast<float*>(more + more_bytes);
   a.qf = qf;
-  CUtensorMap mq;
-  fa_status st = map_q(&mq, a, w, (long long)p.H * D, D) ? FA_OK : FA_ERR_UNSUPPORTED;
+  CUtensorMap mq, mm;
+  fa_status st = map_q(&mq, a, w, (long long)p.H * D, D, D) && map_q(&mm, a, more, (long long)p.H * 8, 8, 8) ? FA_OK : FA_ERR_UNSUPPORTED;
   if (st == FA_OK) {
     host::KernelTimer t("qattend_q", s);
     st = launch(qattend_q_kernel, (rows + QROWS_THREADS / 16 - 1) / (QROWS_THREADS / 16), QROWS_THREADS, 0, s,
-                static_cast<const __nv_bfloat16*>(q), p.q_token, p.q_head, rows, div_by(p.H), D, a.sl2, qc.bits == 4,
-                static_cast<uint16_t*>(w), qf);
+                static_cast<const __nv_bfloat16*>(q), p.q_token, p.q_head, rows, div_by(p.H), D, qc.groups, a.sl2, qc.bits == 4,
+                static_cast<uint16_t*>(w), reinterpret_cast<uint4*>(more), qf);
   }
-  // (no map of K and V is looked at)
-  if (st == FA_OK && qc.bits == 4) st = D <= 64 ? run<64, 1, 4>(a, mq, mq, mq, s) : run<128, 1, 4>(a, mq, mq, mq, s);
-  else if (st == FA_OK) st = D <= 64 ? run<64, 1, 8>(a, mq, mq, mq, s) : run<128, 1, 8>(a, mq, mq, mq, s);
+  if (st == FA_OK && qc.bits == 4) st = D <= 64 ? run<64, 1, 4>(a, mq, mm, mm, s) : run<128, 1, 4>(a, mq, mm, mm, s);
+  else if (st == FA_OK) st = D <= 64 ? run<64, 1, 8>(a, mq, mm, mm, s) : run<128, 1, 8>(a, mq, mm, mm, s);
   if (host::scratch_free(w, s) != cudaSuccess) st = failed();
   return st;
 }

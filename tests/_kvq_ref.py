@@ -119,9 +119,10 @@ def attend(cache, q, new, slots, scale, causal, window, plane=0, tiles=False, ou
     the sum of probabilities being at least 1 as they are taken); p z' in fp32; ex2.approx adds 2^-22; sums over n keys
     (n / 16 + 32) 2^-23 and, for the offsets, n 2^-24, each of M_d = sum_j p_j (s |x| + |z'|).
 
-    Many rows (`tiles`): K, V and P are rounded to fp16 (half a step 2^-11): K and V after x s + z', s and z' rounded
-    too: a value is off by at most 2^-11 of (|value| + |z'| + s |x|), and by 2^-24 of the largest of 64 keys where it is
-    below 2^-14 of that (bounded here by the largest of all); q is fp16 exactly but for 2^-25 of its row's largest."""
+    Many rows (`tiles`): q as above; K is x s (nibbles: exact in fp16, but for 2^-25 of 2^-4 of the largest of 32 keys) and
+    z' in two terms (2^-22 of it, and of q's sum, which is two terms too); 8 bits take a second plane of as many steps. V
+    and P are rounded to fp16 (half a step 2^-11): V after x s + z', s and z' rounded too, so it is off by at most 2^-11 of
+    s |x| + |z'| and by 2^-32 of the largest."""
     T, H, D = q.shape
     f32 = q.dtype == torch.float32
     q = q.double().cpu()
@@ -150,9 +151,10 @@ def attend(cache, q, new, slots, scale, causal, window, plane=0, tiles=False, ou
                 continue
             z = (scale * qh @ k[:, i].T).masked_fill(~see, -math.inf)
             if tiles:
-                size_k = k[:, i].abs() + (kz + mid * ks)[:, i].abs() + (ks * (kc - mid).abs())[:, i]
-                off = qa @ (size_k * 2.0 ** -11 + size_k.max() * 2.0 ** -24).T + qa.amax(1, keepdim=True) * 2.0 ** -25 * size_k.sum(1)
-                e = scale * (off + qa @ size_k.T * D * 2.0 ** -23)
+                size_k = (ks * (kc - mid).abs() + (kz + mid * ks).abs() + ks * mid)[:, i]
+                m = qa @ size_k.T
+                e = scale * (m * ((D / 4 + 4) * 2.0 ** -23 + 2.0 ** -21) + size_k.max() * 2.0 ** -29 * qa.sum(1, keepdim=True)
+                             + qa.amax(1, keepdim=True) * 2.0 ** -35 * size_k.sum(1))
             else:
                 sizes = ks * ((kc - mid).abs() if out_f32 else kc + 2048.0)
                 m = qa @ sizes[:, i].T
@@ -172,7 +174,7 @@ def attend(cache, q, new, slots, scale, causal, window, plane=0, tiles=False, ou
             lost = size * 2.0 ** -30 * float(vs[:, i].max()) * mid
             bo[at:at + n, h] = 2 * e * (w @ v[:, i].abs()) + up * (w @ mass[:, i]) + lost
             if tiles:
-                bo[at:at + n, h] += 2.0 ** -24 * mass[:, i].max()
+                bo[at:at + n, h] += size * 2.0 ** -30 * mass[:, i].max()
             bl[at:at + n, h] = e[:, 0] + (size / 16 + 32) * 2.0 ** -23 + lse.nan_to_num(neginf=0.0).abs() * 2.0 ** -22
         at += n
     return O, L, bo, bl
