@@ -457,7 +457,7 @@ __global__ void __launch_bounds__(NTHREADS, QRowsCfg<E, OUT_BF, BITS, D, NG_, NT
               v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 8));
               v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 16));
               float& was = e ? m[nt].y : m[nt].x;
-              const float mn = fmaxf(was, v);
+              const float mn = v > was + RESCALE_THRESHOLD ? v : was;  // (a row by itself: not as its neighbours' scores fall)
               (e ? f.y : f.x) = ptx::ex2(was - mn);
               was = mn;
             }
