@@ -100,12 +100,12 @@ struct TilesCfg {
   static constexpr uint32_t SMEM = (BITS ? ZERO_OFF + MORE : CODES_OFF) + 1024;
   static constexpr int SOFTMAX_WARPS = 8, MMA_WARP = 8, KQ_WARP = 9, V_WARP = 10, RELAY_WARP = 11;
   static constexpr uint32_t RELAY_BAR = 3;  // named barrier (1 + q: P_q written)
-  static constexpr int CODE_WARP = 12;  // codes: four warps for K's tiles, four for V's, a quarter of a tile each
+  static constexpr int CODE_WARP = 12;  // codes: eight warps, an eighth of each tile
   static constexpr int THREADS = BITS ? 640 : 384;
   static constexpr uint32_t REGS_SOFTMAX = BITS ? 128 : 216, REGS_CONTROL = BITS ? 48 : 64, REGS_CODES = 88;
   static_assert(2 * 128 * REGS_SOFTMAX + 128 * REGS_CONTROL + (BITS ? 256 * REGS_CODES : 0) <= (BITS ? 640 * 96 : 384 * 168),
                 "register split exceeds the launch allocation");
-  static constexpr uint32_t FILLERS = BITS ? 4 : 1;  // arrivals at a landed tile's barrier, and at a grant
+  static constexpr uint32_t FILLERS = BITS ? 8 : 1;  // arrivals at a landed tile's barrier, and at a grant
   static constexpr uint32_t TMEM_COLS = 512;
   __host__ __device__ static constexpr uint32_t s_col(int q) { return 128u * q; }
   __host__ __device__ static constexpr uint32_t o_col(int q) { return 256u + (uint32_t)D * q; }
@@ -126,28 +126,36 @@ __device__ __forceinline__ uint32_t pack_bf2(float lo, float hi) {
   return *reinterpret_cast<const uint32_t*>(&h);
 }
 
+// One lane of a converged warp, the same one each time. (The MMAs' operands are then known to be the same for all
+// lanes that get there: chunks in 4 bits 489 us with lane 0 by comparison, 480 with this; in 8 bits 95 and 92.)
+__device__ __forceinline__ bool elect_one() {
+  uint32_t p;
+  asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(p)::"memory");
+  return p != 0;
+}
 template <class C>
 __device__ __forceinline__ void issue_qk(uint32_t d_tmem, uint32_t sq, uint32_t sk, uint32_t q_more, uint32_t k_more, uint32_t zero) {
   constexpr uint32_t id = make_idesc(128, 128, C::FMT, C::FMT, false, false);
   // (rows of 16 bytes, without a swizzle: eight rows 128 bytes on, the next eight columns -- zeros -- where `zero` is)
   if (C::CODES) mma_f16_ss(d_tmem, make_sdesc(q_more, zero - q_more, 128, 0), make_sdesc(k_more, zero - k_more, 128, 0), id, 0);
+  const uint64_t dq = make_sdesc(sq, 16, SW128_ATOM), dk = make_sdesc(sk, 16, SW128_ATOM);
 #pragma unroll
   for (int plane = 0; plane < C::PLANES; ++plane)
 #pragma unroll
-    for (int kk = 0; kk < C::D / 16; ++kk) {
+    for (int kk = 0; kk < C::D / 16; ++kk) {  // (no address carries past its field)
       const uint32_t off = (kk / 4) * C::CB_BYTES + (kk % 4) * 32;
-      mma_f16_ss(d_tmem, make_sdesc(sq + off, 16, SW128_ATOM), make_sdesc(sk + plane * C::TILE_BYTES + off, 16, SW128_ATOM), id,
-                 kk > 0 || C::CODES);
+      mma_f16_ss(d_tmem, dq + off / 16, dk + (plane * C::TILE_BYTES + off) / 16, id, kk > 0 || C::CODES);
     }
 }
 template <class C, int TERMS>
 __device__ __forceinline__ void issue_pv(uint32_t o_tmem, uint32_t p_tmem, uint32_t sv, bool accumulate) {
   constexpr uint32_t id = make_idesc(128, C::D, C::FMT, C::FMT, false, true);
+  const uint64_t dv = make_sdesc(sv, C::CB_BYTES, SW128_ATOM);
 #pragma unroll
   for (int term = TERMS - 1; term >= 0; --term)
 #pragma unroll
     for (int kk = 0; kk < BLOCK_N / 16; ++kk)
-      mma_f16_ts(o_tmem, p_tmem + term * 64 + kk * 8, make_sdesc(sv + kk * 16 * 128, C::CB_BYTES, SW128_ATOM), id,
+      mma_f16_ts(o_tmem, p_tmem + term * 64 + kk * 8, dv + kk * 128, id,
                  (accumulate || kk > 0 || term < TERMS - 1) ? 1u : 0u);
 }
 
@@ -393,20 +401,16 @@ __global__ void __launch_bounds__(TilesCfg<D, BITS>::THREADS, 1)
     // and the tile's others do not.
     regs_decrease<C::REGS_CODES>();
     if constexpr (BITS != 0) {
-      auto fill_tiles = [&](auto is_v) {
-        constexpr bool IS_V = decltype(is_v)::value;
         constexpr int CH = D * BITS / 128, PIECES = CH >= 4 ? CH / 4 : 1;  // chunks of a key; a lane's pieces of an octet
         constexpr int NG = D / 64;
         constexpr float V_CENTRE = BITS == 4 ? 8.f : 128.f, K_CENTRE = BITS == 4 ? 8.f : 136.f, STEPS = BITS == 4 ? 15.f : 255.f;
-        const int quarter = (warp - C::CODE_WARP) & 3;  // of the tile
+        const int quarter = (warp - C::CODE_WARP) >> 1, half = warp & 1;  // of the tile; of the quarter
         const int chunks = a.qc.chunks, ng = a.qc.groups;
-        const uint8_t* const base = IS_V ? a.qc.V : a.qc.K;
         const uint32_t ring = sbase + C::CODES_OFF + (warp - C::CODE_WARP) * C::RING;
         // the lane's piece, 16 bytes of an octet's 128 a chunk. K: chunk chunk0 of token lane % 8. V: half a pair's
         // chunk, both tokens'.
-        const int chunk0 = lane >> 3;
-        const int token = IS_V ? 2 * (lane & 3) : lane & 7, side = (lane >> 2) & 1;
-        const int at = chunk0 * 128 + (IS_V ? (lane & 3) * 32 + side * 16 : (lane & 7) * 16);
+        const int chunk0 = lane >> 3, side = (lane >> 2) & 1;
+        auto piece_at = [&](bool is_v) { return chunk0 * 128 + (is_v ? (lane & 3) * 32 + side * 16 : (lane & 7) * 16); };
         auto octet_page = [&](int kt) {  // of octet lane / 8 of the warp's quarter: -1: unseen or missing
           const int j = kt * BLOCK_N + quarter * 32 + (lane & ~7);
           if (j >= seg.x.hi || j + 8 <= seg.x.lo) return -1;
@@ -415,7 +419,7 @@ __global__ void __launch_bounds__(TilesCfg<D, BITS>::THREADS, 1)
           raise(a.c.status, FAKV_BAD_PAGE);
           return -1;
         };
-        // params of key `lane` of the quarter, K's and V's (V's warps: V's)
+        // params of key `lane` of the quarter, K's and V's
         struct Params {
           uint32_t k[NG], v[NG];
         };
@@ -427,24 +431,28 @@ __global__ void __launch_bounds__(TilesCfg<D, BITS>::THREADS, 1)
           for (int j = 0; j < NG; ++j) {
             const int w = NG > 1 && ng > 1 ? j * 4 : 0;
             b.v[j] = in ? __ldg(reinterpret_cast<const uint32_t*>(a.qc.V + off + w)) : 0u;
-            if constexpr (!IS_V) b.k[j] = in ? __ldg(reinterpret_cast<const uint32_t*>(a.qc.K + off + w)) : 0u;
+            b.k[j] = in ? __ldg(reinterpret_cast<const uint32_t*>(a.qc.K + off + w)) : 0u;
           }
         };
-        auto ask = [&](int kt, int page, int octet) {  // (each piece read by the lane that asked for it)
+        // a warp's octets of a tile, in turn: two of K, two of V (each piece read by the lane that asked for it)
+        auto ask = [&](int kt, int page, int turn) {
+          const int octet = 2 * half + (turn & 1);
+          const uint8_t* const base = turn < 2 ? a.qc.K : a.qc.V;
+          const int at = piece_at(turn >= 2);
           const int p = __shfl_sync(0xffffffffu, page, octet * 8);
           const int t = (kt * BLOCK_N + quarter * 32 + octet * 8) & (a.c.page_size - 1);
           const uint8_t* const from = base + max(p, 0) * a.qc.page + seg.head * a.qc.head + t * chunks * 16;
 #pragma unroll
           for (int z = 0; z < PIECES; ++z) {
             const bool take = p >= 0 && chunk0 + 4 * z < chunks;
-            if (chunk0 + 4 * z < CH) cp_piece(ring + octet % C::AHEAD * C::OCTET + at + z * 512, take ? from + at + z * 512 : base, take);
+            if (chunk0 + 4 * z < CH) cp_piece(ring + turn % C::AHEAD * C::OCTET + at + z * 512, take ? from + at + z * 512 : base, take);
           }
           asm volatile("cp.async.commit_group;" ::: "memory");
         };
         // scale (low) and z' (high) of key `lane`, as fp16 times the quarter's power of two
         struct Factors {
           uint32_t f[NG];
-          float z[IS_V ? 1 : 2];  // K: z' in fp32, of the first and of the second group
+          float z[2];  // K: z' in fp32, of the first and of the second group
         };
         auto nan = [](const uint32_t (&p)[NG]) {
           bool bad = false;
@@ -461,13 +469,14 @@ __global__ void __launch_bounds__(TilesCfg<D, BITS>::THREADS, 1)
           top = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(top)));
           return min(max(q_exponent(top), -100), 126);
         };
-        auto factors = [&](const Params& b, float2* info) {
+        auto factors = [&](auto is_v, const Params& b, float2* info) {
+          constexpr bool IS_V = decltype(is_v)::value;
           const int ev = exponent_of(b.v) - 6, e = IS_V ? ev : exponent_of(b.k) - 3;
-          if (!IS_V && lane == 0) *info = make_float2(q_pow2(e), (float)ev);
+          if (!IS_V && half == 0 && lane == 0) *info = make_float2(q_pow2(e), (float)ev);
           const float by = q_pow2(-e);
           const bool bad = nan(b.v) || (!IS_V && nan(b.k));
           Factors f;
-          if constexpr (!IS_V) f.z[0] = f.z[1] = 0.f;
+          f.z[0] = f.z[1] = 0.f;
 #pragma unroll
           for (int j = 0; j < NG; ++j) {
             const uint32_t p = IS_V ? b.v[j] : b.k[j];
@@ -477,7 +486,9 @@ __global__ void __launch_bounds__(TilesCfg<D, BITS>::THREADS, 1)
           }
           return f;
         };
-        auto write = [&](const Factors& f, uint32_t tile, int octet) {
+        auto write = [&](auto is_v, const Factors& f, uint32_t tile, int turn) {
+            constexpr bool IS_V = decltype(is_v)::value;
+            const int octet = 2 * half + (turn & 1), token = IS_V ? 2 * (lane & 3) : lane & 7, at = piece_at(IS_V);
             const int r = quarter * 32 + octet * 8 + token;  // row of the tile
             uint32_t sz[NG][IS_V ? 2 : 1];
 #pragma unroll
@@ -495,7 +506,7 @@ __global__ void __launch_bounds__(TilesCfg<D, BITS>::THREADS, 1)
               const bool upper = NG > 1 && col >= 64;
               const uint32_t p0 = upper ? sz[NG - 1][0] : sz[0][0], p1 = IS_V ? (upper ? sz[NG - 1][IS_V] : sz[0][IS_V]) : p0;
               const uint32_t s = __byte_perm(p0, p1, 0x5410), zz = __byte_perm(p0, p1, 0x7632);
-              const float4 piece = ld_shared_v4(ring + octet % C::AHEAD * C::OCTET + at + z * 512);
+              const float4 piece = ld_shared_v4(ring + turn % C::AHEAD * C::OCTET + at + z * 512);
               const uint32_t words[4] = {__float_as_uint(piece.x), __float_as_uint(piece.y), __float_as_uint(piece.z), __float_as_uint(piece.w)};
               if constexpr (BITS == 4) {
                 const uint32_t s16 = q_mul2(s, 0x2c002c00u);  // s / 16
@@ -558,11 +569,10 @@ __global__ void __launch_bounds__(TilesCfg<D, BITS>::THREADS, 1)
               }
             }
         };
-        // tile kt of the item (`left`: and how many after it), its params and first octets asked for before, its stage
-        // waited for by `free`; asks for the next one's, and for the pages of the one after that: nothing of it waits for
-        // a round trip to L2. (A loop, not unrolled, here and in the softmax: the warps of an SM
-        // run three programs at once, and the whole of it unrolled spent its time waiting for instructions, 1097 us
-        // where this takes a third.)
+        // tile kt of the item (`left`: and how many after it), its params and first octets asked for before; asks for the
+        // next one's, and for the pages of the one after that: nothing of it waits for a round trip to L2. (A loop, not
+        // unrolled, here and in the softmax: the warps of an SM run three programs at once, and the whole of it
+        // unrolled spent its time waiting for instructions: more than twice as long.)
         Params params, params_next;
         int page = -1, page_next = -1;
         auto begin = [&](int kt, int left) {
@@ -572,77 +582,70 @@ __global__ void __launch_bounds__(TilesCfg<D, BITS>::THREADS, 1)
           asm volatile("cp.async.wait_all;" ::: "memory");  // (what the last item's end asked for beyond it: zeros)
           for (int i = 0; i < C::AHEAD; ++i) ask(kt, page, i);
         };
-        auto tile = [&](int kt, int left, uint32_t to, uint32_t more, uint64_t* full, float2* info, auto free) {
-          ask_params(params_next, kt + 1, page_next);
-          const int page_after = left > 1 ? octet_page(kt + 2) : -1;
-          if (!free()) return false;
-          const Factors f = factors(params, info);
-          if constexpr (!IS_V) {
-            // z' 2^8 of key `lane`, high, high and low term of each group (for the high, low and high one of q's sums)
-            const uint32_t h = q_half2(f.z[0] / Q_SUM, f.z[1] / Q_SUM);
-            const float2 g = __half22float2(*reinterpret_cast<const __half2*>(&h));
-            const uint32_t l = q_half2(f.z[0] / Q_SUM - g.x, f.z[1] / Q_SUM - g.y);
-            // h0 h0 | l0 h1 | h1 l1 | 0 0
-            st_shared_v4(more + (quarter * 32 + lane) * 16, __byte_perm(h, h, 0x1010), __byte_perm(l, h, 0x7610), __byte_perm(h, l, 0x7632), 0u);
-          }
+        auto two = [&](auto is_v, const Factors& f, uint32_t to, int kt) {
+          constexpr int FIRST = decltype(is_v)::value ? 2 : 0;
 #pragma unroll 1
-          for (int i = 0; i < 4; ++i) {
+          for (int i = FIRST; i < FIRST + 2; ++i) {
             asm volatile("cp.async.wait_group %0;" ::"n"(C::AHEAD - 1) : "memory");
-            write(f, to, i);
+            write(is_v, f, to, i);
             const bool over = i + C::AHEAD >= 4;
             ask(over ? kt + 1 : kt, over ? page_next : page, (i + C::AHEAD) & 3);
           }
-          params = params_next;
-          page = page_next;
-          page_next = page_after;
           fence_async_shared();
           __syncwarp();
-          if (lane == 0) mbar_arrive(full);
+        };
+        // (V: a stage's uses -- key tiles, and per item one epilogue staging -- have positions in
+        // order; each of the warps waits for their releases in that order)
+        int g = 0;
+        uint32_t pos = 0;
+        int seen[VST];
+        for (int s = 0; s < VST; ++s) seen[s] = 0;
+        int prev_stage = -1;
+        auto wait_release = [&](uint32_t p) {
+          const int s = p % VST, u = p / VST;
+          if (seen[s] > u) return true;
+          if (!__all_sync(0xffffffffu, wait_free(&bar_vempty[s], u & 1))) return false;
+          seen[s] = u + 1;
           return true;
         };
         bool ok = true;
-        if constexpr (!IS_V) {
-          int g = 0;
-          while (ok && next()) {
-            if (seg.n > 0) begin(seg.k0, seg.n - 1);
-            for (int t = 0; ok && t < seg.n; ++t, ++g) {
-              const int ks = g % KST;
-              ok = tile(seg.k0 + t, seg.n - 1 - t, sK(ks), sKmore(ks), &bar_kfull[ks], &info_sh[g % TILE_INFO][quarter],
-                        [&] { return __all_sync(0xffffffffu, wait_free(&bar_kempty[ks], ((g / KST) & 1) ^ 1)) != 0; });
+        while (ok && next()) {
+          if (seg.n > 0) begin(seg.k0, seg.n - 1);
+          for (int t = 0; t < seg.n; ++t, ++g, ++pos) {
+            const int kt = seg.k0 + t, left = seg.n - 1 - t, ks = g % KST, vs = pos % VST;
+            ask_params(params_next, kt + 1, page_next);
+            const int page_after = left > 1 ? octet_page(kt + 2) : -1;
+            if (!(ok = __all_sync(0xffffffffu, wait_free(&bar_kempty[ks], ((g / KST) & 1) ^ 1)) != 0)) break;
+            {
+              const Factors f = factors(std::false_type(), params, &info_sh[g % TILE_INFO][quarter]);
+              if (lane >> 4 == half) {
+                // z' 2^8 of key `lane`, high, high and low term of each group (for the high, low and high one of q's sums)
+                const uint32_t h = q_half2(f.z[0] / Q_SUM, f.z[1] / Q_SUM);
+                const float2 hf = __half22float2(*reinterpret_cast<const __half2*>(&h));
+                const uint32_t l = q_half2(f.z[0] / Q_SUM - hf.x, f.z[1] / Q_SUM - hf.y);
+                // h0 h0 | l0 h1 | h1 l1 | 0 0
+                st_shared_v4(sKmore(ks) + (quarter * 32 + lane) * 16, __byte_perm(h, h, 0x1010), __byte_perm(l, h, 0x7610),
+                             __byte_perm(h, l, 0x7632), 0u);
+              }
+              two(std::false_type(), f, sK(ks), kt);
             }
-          }
-        } else {
-          // (a stage's uses -- key tiles, and per item one epilogue staging -- have positions in
-          // order; each of the four warps waits for their releases in that order)
-          uint32_t pos = 0;
-          int seen[VST];
-          for (int s = 0; s < VST; ++s) seen[s] = 0;
-          int prev_stage = -1;
-          auto wait_release = [&](uint32_t p) {
-            const int s = p % VST, u = p / VST;
-            if (seen[s] > u) return true;
-            if (!__all_sync(0xffffffffu, wait_free(&bar_vempty[s], u & 1))) return false;
-            seen[s] = u + 1;
-            return true;
-          };
-          while (ok && next()) {
-            if (seg.n > 0) begin(seg.k0, seg.n - 1);
-            for (int t = 0; ok && t < seg.n; ++t, ++pos)
-              ok = tile(seg.k0 + t, seg.n - 1 - t, sV(pos % VST), 0u, &bar_vfull[pos % VST], nullptr,
-                        [&] { return pos < (uint32_t)VST || wait_release(pos - VST); });
-            if (!ok) break;
+            if (lane == 0) mbar_arrive(&bar_kfull[ks]);
             if (pos >= (uint32_t)VST && !(ok = wait_release(pos - VST))) break;
-            if (prev_stage >= 0 && !(ok = wait_release((uint32_t)prev_stage))) break;
-            if (lane == 0)
-              for (int q = 0; q < NQ; ++q) mbar_arrive(&bar_grant[q]);
-            __syncwarp();
-            prev_stage = (int)pos;
-            ++pos;
+            two(std::true_type(), factors(std::true_type(), params, nullptr), sV(vs), kt);
+            if (lane == 0) mbar_arrive(&bar_vfull[vs]);
+            params = params_next;
+            page = page_next;
+            page_next = page_after;
           }
+          if (!ok) break;
+          if (pos >= (uint32_t)VST && !(ok = wait_release(pos - VST))) break;
+          if (prev_stage >= 0 && !(ok = wait_release((uint32_t)prev_stage))) break;
+          if (lane == 0)
+            for (int q = 0; q < NQ; ++q) mbar_arrive(&bar_grant[q]);
+          __syncwarp();
+          prev_stage = (int)pos;
+          ++pos;
         }
-      };
-      if (warp < C::CODE_WARP + 4) fill_tiles(std::false_type());
-      else fill_tiles(std::true_type());
       asm volatile("cp.async.wait_all;" ::: "memory");
     }
   } else if (warp >= C::SOFTMAX_WARPS) {
@@ -747,7 +750,6 @@ __global__ void __launch_bounds__(TilesCfg<D, BITS>::THREADS, 1)
         if (loads[s] > 0) drain(&bar_vfull[s], (loads[s] - 1) & 1);
     } else if (warp == C::MMA_WARP) {
       // ---------------------------------------------------------- MMA issuer
-      const bool leader = lane == 0;
       int g = 0, j = 0;
       uint32_t pos = 0;
       while (next()) {
@@ -757,14 +759,14 @@ __global__ void __launch_bounds__(TilesCfg<D, BITS>::THREADS, 1)
         for (int q = 0; q < NQ; ++q) {
           named_bar_sync(C::RELAY_BAR, 64);
           tc_fence_after();
-          if (leader) {
+          if (elect_one()) {
             issue_qk<C>(tmem + C::s_col(q), sQ(q), sK(k0), sQmore(q), sKmore(k0), sbase + C::ZERO_OFF);
             tc_commit(&bar_s[q]);
             if (n == 1) tc_commit(&bar_qfree[q]);
           }
           __syncwarp();
         }
-        if (leader) tc_commit(&bar_kempty[k0]);
+        if (elect_one()) tc_commit(&bar_kempty[k0]);
         __syncwarp();
         for (int t = 0; t < n; ++t, ++g, ++pos) {
           const int vs = pos % VST, ks = (g + 1) % KST;
@@ -773,7 +775,7 @@ __global__ void __launch_bounds__(TilesCfg<D, BITS>::THREADS, 1)
           for (int q = 0; q < NQ; ++q) {
             named_bar_sync(1 + q, 128 + 32);  // P_q(g) is in TMEM
             tc_fence_after();
-            if (leader) {
+            if (elect_one()) {
               issue_pv<C, TERMS>(tmem + C::o_col(q), tmem + C::s_col(q), sV(vs), t > 0);
               if (more) {
                 issue_qk<C>(tmem + C::s_col(q), sQ(q), sK(ks), sQmore(q), sKmore(ks), sbase + C::ZERO_OFF);
@@ -785,7 +787,7 @@ __global__ void __launch_bounds__(TilesCfg<D, BITS>::THREADS, 1)
             }
             __syncwarp();
           }
-          if (leader) {
+          if (elect_one()) {
             tc_commit(&bar_vempty[vs]);
             if (more) tc_commit(&bar_kempty[ks]);
           }
@@ -794,7 +796,7 @@ __global__ void __launch_bounds__(TilesCfg<D, BITS>::THREADS, 1)
         pos += 1;
         ++j;
       }
-      if (j > 0 && leader) {
+      if (j > 0 && elect_one()) {
         tc_commit(&bar_drain);  // no MMA may still be running when TMEM is released
         drain(&bar_drain, 0);
       }
