@@ -1,8 +1,8 @@
 // kv_qrows.cu -- attention over the cache in 4 or 8 bits for few rows per sequence (decoding), and for
-// fp32 queries: codes streamed once, made bf16 in registers, mma.sync.
+// fp32 queries: codes streamed once, made fp16 in registers, mma.sync.
 //
 // Workers, parts and joins are those of kv_rows.cu. A page of a head is one block of memory, its codes one
-// after another: the copy engine brings a step's 32 keys in a few copies (two a page), which the lanes issue
+// after another: the copy engine brings a step's 64 or 32 keys in a few copies (two a page), which the lanes issue
 // whose pages they are, and every wait for one has a limit. With s, z of a key's group g and codes
 // c = centre + x (centre 8 or 128), its K and V are s x + z', z' = z + centre s, so that
 //
@@ -11,8 +11,8 @@
 //           that brings its largest value to 2^14 is fp16 too, exactly but for what is 2^-28 of that
 //   O^T     O_d = sum_k (p_k s_k) x_kd + sum_k p_k z'_k: the scales enter the probabilities, times a power
 //           of two that keeps the largest scale so far just below 2^7; the offsets are one more sum
-//           per row and group. p s is one fp16 term where O is bf16 (2^-12 of itself, an eighth of O's
-//           own rounding), two (2^-23) where O is fp32; what is below 2^-30 of the largest p s rounds to
+//           per row and group. p s is one fp16 term where O is bf16 (2^-11 of itself, an eighth of O's
+//           own rounding), two (2^-22) where O is fp32; what is below 2^-30 of the largest p s rounds to
 //           2^-40 of it
 //
 // so nothing of the cache is rounded again. A code costs about an instruction (kv_quant.cuh):
@@ -20,6 +20,14 @@
 //      32-bit word of its key, and q's fragments are laid out to match
 //   V  keys are summed over, two of each register: the cache holds the codes of two tokens side by side,
 //      so that every pair is one column of two keys
+//
+// Measured (device, data in L2 where they fit; floor: bytes at the measured copy rate): 64 sequences of up to 16384 tokens in
+// 4 bits, D 128, 143 us (floor 89); 32 of up to 8192 in 8 bits 60 (42; 70 cold); one of 1021 12; 16 of up to 8192
+// with 4 drafted tokens each 40 (12). Not HBM but the instructions that make numbers of codes bound it: 335 to 16 keys of
+// a head (a half of them on the ALU), 54 % of what the warps' schedulers can issue, with three warps to each: more do not fit
+// (128 registers for 16 warps an SM spilled: 153 us). Sixteen rows take those instructions once for two rows' tiles;
+// with more rows they are taken again for every sixteen, and kv_tiles.cu takes over where that costs more. 64 keys to a step
+// where there is room: 153 -> 140 us.
 #include <algorithm>
 #include "kv_quant.cuh"
 #include "kv_rows.cuh"

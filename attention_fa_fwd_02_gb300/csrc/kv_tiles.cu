@@ -1,5 +1,5 @@
-// kv_tiles.cu -- attention over a bf16 paged cache for many rows per sequence (chunks of a
-// prompt): TMA from the pages, tcgen05, TMEM.
+// kv_tiles.cu -- attention over a bf16 paged cache, or one in 4 or 8 bits, for many rows per sequence (chunks of
+// a prompt): TMA from the pages (codes: warps that make fp16 of them), tcgen05, TMEM.
 //
 // Many rows per key make the work 4 D flops per (row, key) on the tensor cores. An item is
 // two 128-row tiles of one sequence and kv head: the rows of a tile are tpt tokens x the
@@ -38,6 +38,21 @@
 // (640 threads leave 96 registers each: it spilled, 633 us), and P handed over in two halves
 // (2820 clocks). An item costs 4 us besides its units (epilogue, first scores), which the
 // schedule counts as three units; the start of the kernel 8 us.
+//
+// Codes of 4 or 8 bits (640 threads). Four roles are different:
+//   warps 12 - 19 codes: each writes an eighth of K's and of V's tile as fp16, in turn, where bf16's copies would have
+//                 laid them (the comment at their branch has the numbers' form)
+//   warp 9        producer of q alone, which qattend_q_kernel has made fp16 before; warp 10 has nothing to do
+//   warps 0 - 7   the softmax takes 64 keys at a time, its 128 registers having no room for more; P is fp16
+// Three programs at once run an SM's warps out of instruction memory, so the loops over octets and over 64 keys are not
+// unrolled (2048 tokens over 16384 in 4 bits: 1097 us with all unrolled, 479 now). That is 0.56 of the tensor
+// peak at 2.4 us to a unit, of which its MMAs, K's offsets among them, fill 1.45; without turning codes into
+// numbers it takes 424, with half of a softmax 380, without either 338. Eight bits: K's two planes double the first product
+// and leave room for one stage of K, so that a unit is its codes, then S, then the other (4 us; six chunks of up to
+// 500 tokens 92 us). Tried, and slower or the same: 640 threads split 136/48/80 and 128/64/80 registers, three octets of
+// 8-bit codes ahead, products over the columns that there are (the issuer's branches cost 577 us for 479), four warps for K
+// and four for V (511; K's are then what all wait for), codes in registers a tile ahead. tests/test_kvq_tiles_sync_model.py
+// replays these hand-offs.
 #include <algorithm>
 #include <cfloat>
 #include <cmath>
@@ -392,7 +407,7 @@ __global__ void __launch_bounds__(TilesCfg<D, BITS>::THREADS, 1)
     // ------------------------------------------------------------ codes of K, of V
     // Each of four warps writes 32 keys of every tile, as the copies of bf16 pages would have laid them down, in fp16:
     // times a power of two that keeps the largest of the 32 keys' values just below 2^4 (K: undone in the scores) or
-    // 2^7 (V: undone in the probabilities). V is x s + z', rounded to 2^-12 of it. A score's error moves a probability by
+    // 2^7 (V: undone in the probabilities). V is x s + z', rounded to 2^-11 of it. A score's error moves a probability by
     // its factor, so K is not rounded: x s of a nibble x in -8 .. 7 has the eleven bits of fp16 (of a byte it is two such
     // terms, 16 (h - 8) s and (l - 8) s, in two planes), and z' (two terms) is multiplied with the row's sum of q in one
     // step of the product more. (K as x s + z' in one term had LSEs 8e-6 off, and 3e-5 where few keys were seen.) The

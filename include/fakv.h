@@ -258,7 +258,8 @@ typedef struct {
 FA_API long long fakv_qblock_bytes(int page_size, int D, int bits, int group);
 
 /* fakv_append into such a cache: k turned by its positions where `rope` is given, in fp32 and
- * without a rounding before its codes are formed; v; and q into q_out as fakv_append does. */
+ * without a rounding before its codes are formed; v; and q into q_out as fakv_append does. (A slot named
+ * for two sequences: a place's codes may be of one token and its scale of the other.) */
 FA_API fa_status fakv_qappend(const void* q, const void* k, const void* v, void* q_out,
                               const int* cu, const int* slots, const fakv_rope* rope,
                               const fakv_qcache* cache, const fakv_tokens* p, fa_stream_t stream);
@@ -273,11 +274,19 @@ FA_API fa_status fakv_qread(void* K_out, void* V_out, const int* cu, const int* 
                             const int* first, const fakv_qcache* cache, const fakv_tokens* p,
                             fa_stream_t stream);
 
-/* fakv_attend over what such a cache stands for. A key whose group is NaN makes O and LSE of the
- * rows that see it NaN (a value: their O, in the group's columns), and of no other row. Scores:
- * bf16 queries times codes, exact products with fp32 sums (fp32 queries in three bf16 terms, 2^-24),
- * scaled and offset in fp32. The probabilities enter the second product times a key's scale, in two
- * bf16 terms (2^-16). */
+/* fakv_attend over what such a cache stands for, s c + z; K and V below 2^80 in size (what is below
+ * 2^-100 may count for less than it is). Precision, beyond that of the codes:
+ *   few rows to a sequence, and every fp32 q: q times a power of two in fp16 (a bf16 q exactly but for
+ *     what is 2^-28 of its row's largest value; an fp32 q in two terms, 2^-22), codes exactly, scales and
+ *     offsets in fp32, fp32 sums; a probability times its key's scale in fp16, one term (2^-11) where O is
+ *     bf16, two (2^-22) where it is fp32
+ *   many rows (bf16 q): K and q as above, so that LSE is too; V to 2^-11 of the value and of its two parts,
+ *     codes times scale and offset, and a probability to 2^-11: of an fp32 O too, whose last bits are better
+ *     had from fp32 queries or from fewer rows to a call
+ * NaN or infinity in a row of q makes that row's O and LSE NaN and no other's. A key that stands for NaN makes
+ * the rows that see it NaN (K: O and LSE; V: their O in the group's columns, and where there are many
+ * rows all of O, and LSE) and no other. Which kernel is chosen, T and a batch of both kinds: as for fakv_attend,
+ * but with 32 (4 bits) or 48 (8 bits) rows per sequence and kv head as the limit. */
 FA_API fa_status fakv_qattend(const void* q, void* O, float* LSE, const int* cu, const int* slots,
                               const fakv_qcache* cache, const fakv_tokens* p, fa_stream_t stream);
 

@@ -312,7 +312,7 @@ def test_bad_slots_lengths_and_cu(kv):
     assert e.value.bits == kv.BAD_LENGTH
 
 
-@pytest.mark.parametrize("new", [1, 24])
+@pytest.mark.parametrize("new", [1, 24, 40])
 def test_offsets_past_32_bits(kv, new):
     """A plane whose pages lie up to 9 GB from its beginning."""
     page, HKV, D, pages = 64, 4, 128, 256000

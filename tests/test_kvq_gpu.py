@@ -223,7 +223,10 @@ def test_attend_decoding(kv, dtype, D, bits, group):
     ([2, 1], [513, 512], 256, 5, 5, {"window": 1}),
     ([1, 3], [40, 50], 1024, 24, 3, {"pad": 5, "scale": 0.3}),
     ([7, 0, 2], [90, 0, 9], 16, 6, 2, {"causal": False, "window": 20, "pad": 2}),
-    ([1] * 40, [1 + 37 * i for i in range(40)], 16, 4, 1, {})])
+    ([1] * 40, [1 + 37 * i for i in range(40)], 16, 4, 1, {}),
+    ([6], [600], 16, 5, 1, {}),                                 # more rows than one pass over the keys takes, fewer than tiles
+    ([4, 3], [333, 90], 64, 16, 2, {"window": 50}),
+    ([1, 0, 0, 0, 0, 0, 0, 0], [70, 0, 3, 4, 5, 6, 7, 8], 8, 128, 1, {})])  # 128 heads to one of the cache
 def test_attend_masks_and_shapes(kv, dtype, bits, group, new, lens, page, H, HKV, kw):
     check_attend(kv, dtype, new, lens, page, H, HKV, 128, bits, group, **kw)
 
@@ -278,6 +281,9 @@ def test_attend_chunks(kv, D, bits, group):
     ([90, 17], [513, 512], 256, 5, 5, {"window": 1}),
     ([33, 31], [1040, 50], 1024, 24, 3, {"pad": 50, "scale": 0.3}),
     ([100, 0, 35], [190, 0, 35], 16, 6, 2, {"causal": False, "window": 20, "pad": 2}),
-    ([150], [2000], 128, 7, 1, {"out_dtype": F32})])
+    ([150], [2000], 128, 7, 1, {"out_dtype": F32}),
+    ([2, 1], [50, 1100], 1024, 128, 1, {}),                     # a tile to each token
+    ([1], [77], 8, 96, 1, {"window": 60}),
+    ([200], [200], 16, 100, 50, {"scale": 0.02})])
 def test_attend_chunks_masks_and_shapes(kv, bits, group, new, lens, page, H, HKV, kw):
     check_attend(kv, BF, new, lens, page, H, HKV, 128, bits, group, tiles=True, **kw)
