@@ -30,9 +30,10 @@
 // prompt: 650 to 690 us against 385). It is not the tensor pipe that fills then (60 %) but
 // the softmax warps' extra terms and TMEM stores.
 //
-// Measured: 2048 tokens over 16384 (32 query heads on 8 of 128) 337 us with the join, 1530
-// TFLOP/s, 0.80 of the measured peak; 8192 tokens of a prompt 385 us, 0.75. A unit of 128 keys
-// takes a CTA 2720 clocks, of which its MMAs fill 2240: a tile's softmax (1130 clocks: 62 to
+// Measured: 2048 tokens over 16384 (32 query heads on 8 of 128) 309 us with the join, 1670
+// TFLOP/s, 0.86 of the measured peak (337 with the MMAs issued by lane 0 and each descriptor put together anew; the
+// figures that follow, and those of two terms above, are of that form); 8192 tokens of a prompt 385 us, 0.75. A unit of 128
+// keys takes a CTA 2720 clocks, of which its MMAs fill 2240: a tile's softmax (1130 clocks: 62 to
 // load the scores, 320 for the maximum, 690 for the exponentials) and the hand-offs on both
 // sides of it are longer than the other tile's MMAs. Tried, and slower: two threads to a row
 // (640 threads leave 96 registers each: it spilled, 633 us), and P handed over in two halves
@@ -45,12 +46,13 @@
 //   warp 9        producer of q alone, which qattend_q_kernel has made fp16 before; warp 10 has nothing to do
 //   warps 0 - 7   the softmax takes 64 keys at a time, its 128 registers having no room for more; P is fp16
 // Three programs at once run an SM's warps out of instruction memory, so the loops over octets and over 64 keys are not
-// unrolled (2048 tokens over 16384 in 4 bits: 1097 us with all unrolled, 479 now). That is 0.56 of the tensor
+// unrolled (2048 tokens over 16384 in 4 bits: 1097 us with all unrolled, 475 now). That is 0.56 of the tensor
 // peak at 2.4 us to a unit, of which its MMAs, K's offsets among them, fill 1.45; without turning codes into
 // numbers it takes 424, with half of a softmax 380, without either 338. Eight bits: K's two planes double the first product
-// and leave room for one stage of K, so that a unit is its codes, then S, then the other (4 us; six chunks of up to
-// 500 tokens 92 us). Tried, and slower or the same: 640 threads split 136/48/80 and 128/64/80 registers, three octets of
-// 8-bit codes ahead, products over the columns that there are (the issuer's branches cost 577 us for 479), four warps for K
+// and leave room for one stage of K, so that a unit is its codes, then both tiles' products, in turn (3.9 us; six
+// chunks of up to 500 tokens 89 us; 91 with the factors formed after the wait for the stage). Tried, and slower or the same: 640 threads split 136/48/80 and 128/64/80 registers, three octets of
+// 8-bit codes ahead, products over the columns that there are (96 of 128 by a branch in the issuer: 577 us for 479; by a kernel of its own 86 for
+// 89, too little for two more), four warps for K
 // and four for V (511; K's are then what all wait for), codes in registers a tile ahead. tests/test_kvq_tiles_sync_model.py
 // replays these hand-offs.
 #include <algorithm>
@@ -630,9 +632,10 @@ __global__ void __launch_bounds__(TilesCfg<D, BITS>::THREADS, 1)
             const int kt = seg.k0 + t, left = seg.n - 1 - t, ks = g % KST, vs = pos % VST;
             ask_params(params_next, kt + 1, page_next);
             const int page_after = left > 1 ? octet_page(kt + 2) : -1;
-            if (!(ok = __all_sync(0xffffffffu, wait_free(&bar_kempty[ks], ((g / KST) & 1) ^ 1)) != 0)) break;
             {
+              // (what the stage is not needed for, before it is waited for; all have read tile g - 5's info, the place's last one's long before)
               const Factors f = factors(std::false_type(), params, &info_sh[g % TILE_INFO][quarter]);
+              if (!(ok = __all_sync(0xffffffffu, wait_free(&bar_kempty[ks], ((g / KST) & 1) ^ 1)) != 0)) break;
               if (lane >> 4 == half) {
                 // z' 2^8 of key `lane`, high, high and low term of each group (for the high, low and high one of q's sums)
                 const uint32_t h = q_half2(f.z[0] / Q_SUM, f.z[1] / Q_SUM);
@@ -645,8 +648,9 @@ __global__ void __launch_bounds__(TilesCfg<D, BITS>::THREADS, 1)
               two(std::false_type(), f, sK(ks), kt);
             }
             if (lane == 0) mbar_arrive(&bar_kfull[ks]);
+            const Factors f = factors(std::true_type(), params, nullptr);
             if (pos >= (uint32_t)VST && !(ok = wait_release(pos - VST))) break;
-            two(std::true_type(), factors(std::true_type(), params, nullptr), sV(vs), kt);
+            two(std::true_type(), f, sV(vs), kt);
             if (lane == 0) mbar_arrive(&bar_vfull[vs]);
             params = params_next;
             page = page_next;

@@ -360,3 +360,22 @@ def test_thousands_of_sequences(kv):
         assert torch.equal(x, y)
     cache.check()
     apart.check()
+
+
+@pytest.mark.parametrize("bits", [4, 8])
+def test_thousands_of_sequences_chunks(kv, bits):
+    """More sequences than the tile kernel has threads, each with new tokens of its own."""
+    B, D, page = 1500, 16, 8
+    lens = [(i * 7) % 41 if i % 3 else 90 for i in range(B)]
+    new = [n if i % 3 else 70 for i, n in enumerate(lens)]
+    cache, _ = ref.make(kv, lens, page, 1, D, bits, D, BF)
+    T = sum(new)
+    q = randn(T, 2, D, dtype=BF, mul=1.5)
+    assert T * 2 > 48 * B
+    o, lse = cache.attend(q, cu_of(new))
+    cache.check()
+    for i in (0, 1, 2, 640, 1001, 1498, 1499):
+        a = sum(new[:i])
+        want, want_l, bo, bl = ref.attend(cache, q[a:a + new[i]], [new[i]], [i], D ** -0.5, True, 0, 0, True)
+        _kv_ref.close(o[a:a + new[i]].cpu(), want, bo, i)
+        assert bool(((lse[a:a + new[i]].cpu().double() - want_l).abs() <= bl).all())

@@ -97,12 +97,12 @@ def run(items, KST, VST, seed, lose=None, early=None, grants=FILL):
         for k, n in enumerate(items):
             for _ in range(n):
                 s = g % KST
+                if w % 2 == 0:
+                    info[g % INFO][w // 2] = g
                 if not (yield ("m", ("kempty", s), ((g // KST) & 1) ^ 1)) or abort[0]:
                     return
                 was = smem_k[s][w]
                 check(was is None or k_read.get(was, 0) == NQ, f"K {was} written over")
-                if w % 2 == 0:
-                    info[g % INFO][w // 2] = g
                 yield None
                 smem_k[s][w] = g
                 yield None
