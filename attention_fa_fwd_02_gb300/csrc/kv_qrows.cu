@@ -110,7 +110,8 @@ __global__ void __launch_bounds__(NTHREADS, QRowsCfg<E, OUT_BF, BITS, D, NG_, NT
   using C = QRowsCfg<E, OUT_BF, BITS, D, NG_, NTR>;
   constexpr int CH = C::CH, R = C::R, NP = C::NP, GROUP = C::GROUP, KT = C::KT, NG = C::NG, KS = C::KS;
   constexpr int TERMS = C::TERMS, PT = C::PT;
-  constexpr bool CENTRED = !OUT_BF;  // K's codes: centred before the product, or their constant (1024) taken off after it
+  // K's codes: 2^-24 times the code (q_small), or, where O is fp32, centred: an instruction more, and sums of an eighth
+  constexpr bool CENTRED = !OUT_BF;
   constexpr float CENTRE = BITS == 4 ? 8.f : 128.f;
   constexpr int VT = BITS == 4 ? 2 : 1;  // output tiles of a chunk: code pairs 2 t and 2 t + 1 of a word of V
   extern __shared__ __align__(1024) uint8_t smem[];
@@ -218,10 +219,10 @@ __global__ void __launch_bounds__(NTHREADS, QRowsCfg<E, OUT_BF, BITS, D, NG_, NT
     };
 
     // ---- q: fragments of its rows (zeros behind the item's rows and the tensor's columns), each row
-    // times a power of two; of rows 8 nt + 2 quad + e the sums over each group: of q, and (not centred) of
-    // q times its codes' constants; and what makes logits (log2) of their scores
+    // times a power of two; of rows 8 nt + 2 quad + e the sums over each group, and what makes logits (log2) of
+    // their scores
     uint4 qr[C::Q_REGS ? KS / 2 : 1];
-    float2 qs[NTR][NG], qb[NTR][NG], ql[NTR];
+    float2 qs[NTR][NG], ql[NTR];
 #pragma unroll
     for (int nt = 0; nt < NTR; ++nt) {
       const int r = nt * 8 + oct;
@@ -255,12 +256,9 @@ __global__ void __launch_bounds__(NTHREADS, QRowsCfg<E, OUT_BF, BITS, D, NG_, NT
       const int e = min(max(q_exponent(top), -100), 127);
       const float down = q_pow2(14 - e), up = fmaxf(a.sl2 * q_pow2(e - 14), FLT_MIN);  // (a masked score is -infinity times it)
       // (infinity in a row makes all that it sees NaN, whatever the codes)
-      float sum[NG], bias[NG];
+      float sum[NG];
 #pragma unroll
-      for (int i = 0; i < NG; ++i) {
-        sum[i] = top < INFINITY ? 0.f : __int_as_float(0x7fffffff);
-        bias[i] = 0.f;
-      }
+      for (int i = 0; i < NG; ++i) sum[i] = top < INFINITY ? 0.f : __int_as_float(0x7fffffff);
 #pragma unroll
       for (int i = 0; i < KS / 2; ++i) {
         // of the code pairs: 4 bits (0, 4), (1, 5), (2, 6), (3, 7); 8 bits (0, 1), (2, 3) of each chunk
@@ -268,10 +266,9 @@ __global__ void __launch_bounds__(NTHREADS, QRowsCfg<E, OUT_BF, BITS, D, NG_, NT
 #pragma unroll
         for (int z = 0; z < 4; ++z) {
           const int c0 = BITS == 4 ? z : 2 * z, c1 = BITS == 4 ? z + 4 : 2 * z + 1;
-          constexpr float FACTOR = q_factor<BITS>(1);
-          float2 v = make_float2(y[i][c0] * (down / FACTOR), y[i][c1] * (down / FACTOR));
-          sum[NG > 1 ? i / 2 : 0] += (v.x + v.y) * FACTOR;
-          bias[NG > 1 ? i / 2 : 0] -= (v.x + v.y) * 1024.f;
+          const float factor = q_factor<BITS>(CENTRED ? 1 : z);
+          float2 v = make_float2(y[i][c0] * (down / factor), y[i][c1] * (down / factor));
+          sum[NG > 1 ? i / 2 : 0] += (v.x + v.y) * factor;
           f[0][z] = half2_of(v.x, v.y, &v);
           f[1][z] = half2_of(v.x, v.y);
         }
@@ -287,10 +284,7 @@ __global__ void __launch_bounds__(NTHREADS, QRowsCfg<E, OUT_BF, BITS, D, NG_, NT
       for (int i = 0; i < NG; ++i) {
         sum[i] += __shfl_xor_sync(0xffffffffu, sum[i], 1);
         sum[i] += __shfl_xor_sync(0xffffffffu, sum[i], 2);
-        bias[i] += __shfl_xor_sync(0xffffffffu, bias[i], 1);
-        bias[i] += __shfl_xor_sync(0xffffffffu, bias[i], 2);
         qs[nt][i] = of_row(sum[i]);
-        qb[nt][i] = of_row(bias[i]);
       }
       ql[nt] = of_row(up);
     }
@@ -347,7 +341,7 @@ __global__ void __launch_bounds__(NTHREADS, QRowsCfg<E, OUT_BF, BITS, D, NG_, NT
 #pragma unroll
             for (int nt = 0; nt < NTR; ++nt)
 #pragma unroll
-              for (int e = 0; e < 4; ++e) acc[k][kt][nt][e] = CENTRED ? 0.f : e & 1 ? qb[nt][k].y : qb[nt][k].x;
+              for (int e = 0; e < 4; ++e) acc[k][kt][nt][e] = 0.f;
 #pragma unroll
         for (int w = 0; w < CH; ++w) {
           const int k = NG == 1 ? 0 : BITS == 4 ? w / 2 : w / 4;  // the chunk's group
@@ -359,11 +353,11 @@ __global__ void __launch_bounds__(NTHREADS, QRowsCfg<E, OUT_BF, BITS, D, NG_, NT
               word[e] = *reinterpret_cast<const uint32_t*>(slot + ((kt * 2 + e) * CH + w) * 128 + lane * 4);
             auto product = [&](auto pair, uint32_t b0, uint32_t b1, int nt) {  // code pairs `pair` and + 1
               constexpr int P = decltype(pair)::value;
-              uint32_t f[4] = {q_raise16<BITS, P>(word[0], a.raised), q_raise16<BITS, P>(word[1], a.raised),
-                               q_raise16<BITS, P + 1>(word[0], a.raised), q_raise16<BITS, P + 1>(word[1], a.raised)};
-              if constexpr (CENTRED) {
+              uint32_t f[4];
 #pragma unroll
-                for (int e = 0; e < 4; ++e) f[e] = q_centred<BITS, 1>(f[e]);  // (all with the factor)
+              for (int e = 0; e < 2; ++e) {
+                f[e] = CENTRED ? q_centred<BITS, 1>(q_raise16<BITS, P>(word[e], a.raised)) : q_small<BITS, P>(word[e]);
+                f[2 + e] = CENTRED ? q_centred<BITS, 1>(q_raise16<BITS, P + 1>(word[e], a.raised)) : q_small<BITS, P + 1>(word[e]);
               }
               mma_f16(acc[k][kt][nt], f, b0, b1);
             };
@@ -395,7 +389,7 @@ __global__ void __launch_bounds__(NTHREADS, QRowsCfg<E, OUT_BF, BITS, D, NG_, NT
               float2 v = make_float2(0.f, 0.f);
 #pragma unroll
               for (int k = 0; k < NG; ++k) {
-                const float ps = q_scale(p[k]), pz = CENTRED ? fmaf(ps, CENTRE, q_offset(p[k])) : q_offset(p[k]);
+                const float ps = CENTRED ? q_scale(p[k]) : q_scale24(p[k]), pz = CENTRED ? fmaf(ps, CENTRE, q_offset(p[k])) : q_offset(p[k]);
                 v.x = k == 0 ? pz * qs[nt][k].x : fmaf(pz, qs[nt][k].x, v.x);
                 v.y = k == 0 ? pz * qs[nt][k].y : fmaf(pz, qs[nt][k].y, v.y);
                 v.x = fmaf(ps, acc[k][kt][nt][2 * z], v.x);

@@ -66,13 +66,22 @@ __device__ __forceinline__ uint32_t q_raise(uint32_t w, uint32_t raised) {
   if constexpr (BITS == 8) return __byte_perm(w, raised, R == 0 ? 0x5150 : 0x5352);
   else return ((R < 2 ? w : w >> 8) & (R % 2 ? 0x00f000f0u : 0x000f000fu)) | raised;
 }
-// The same for the product whose constant is taken off as a sum: all nibbles as 1024 + 16 n, so that it is 64 times q
-// and not 1024 (two shifts more, 138.5 -> 143 us where kv_qrows.cu's figure is; the LSE of 16384 keys was 2e-6 off, and is 1e-7).
+// The same with all nibbles as 1024 + 16 n, so that one factor serves all (two shifts more).
 template <int BITS, int R>
 __device__ __forceinline__ uint32_t q_raise16(uint32_t w, uint32_t raised) {
   if constexpr (BITS == 8) return q_raise<8, R>(w, raised);
   else return ((R == 0 ? w << 4 : R == 1 ? w : w >> (4 * R - 4)) & 0x00f000f0u) | raised;
 }
+// Two codes of a word as fp16 numbers below the normal ones, 2^-24 times the code (times 16 for nibbles 1 and 3 of a
+// half): nothing to set and no constant to take off. (fp16 products are exact for these too.)
+template <int BITS, int R>
+__device__ __forceinline__ uint32_t q_small(uint32_t w) {
+  if constexpr (BITS == 8) return __byte_perm(w, 0u, R == 0 ? 0x4140 : 0x4342);
+  else return (R < 2 ? w : w >> 8) & (R % 2 ? 0x00f000f0u : 0x000f000fu);
+}
+// A scale times 2^24 (one multiply-add; of zero it is 2^-103, whose codes are all zero, and of NaN a number, whose offset
+// is NaN)
+__device__ __forceinline__ float q_scale24(uint32_t p) { return __uint_as_float(p * 65536u + (24u << 23)); }
 template <int BITS>
 __host__ __device__ constexpr float q_factor(int r) { return BITS == 4 && r % 2 ? 16.f : 1.f; }
 

@@ -110,8 +110,7 @@ def attend(cache, q, new, slots, scale, causal, window, plane=0, tiles=False, ou
 
     Few rows. q enters as fp16 times a power of two (2^-35 of its row's largest is lost), fp32 q in two terms (2^-22). A
     product with codes of D columns takes D / 16 steps of the tensor cores (for each term), each of which cuts off at
-    2^-23 of a partial sum twice at most; where O is bf16 the codes carry a constant, 1024 (1024 / 16 a sixteenth of
-    it in places), taken off before the first step: the partial sums are at most m = sum |q| (c + 2048). Where O is fp32
+    2^-23 of a partial sum twice at most: the partial sums are at most m = sum |q| c. Where O is fp32
     they are centred codes x: m = sum |q| |x|. A score is s m 2^-23 (D / 8 + 2) (times the terms) off from that, and
     two fused operations a group, below 4 * 2^-24 of s m + |z| sum |q|. A score error e moves its probability by the
     factor exp(e): O_d by at most 2 e A_d, A_d = sum_j p_j |v_jd|, the LSE by e. Probabilities times scales enter as one
@@ -156,7 +155,7 @@ def attend(cache, q, new, slots, scale, causal, window, plane=0, tiles=False, ou
                 e = scale * (m * ((D / 4 + 4) * 2.0 ** -23 + 2.0 ** -21) + size_k.max() * 2.0 ** -29 * qa.sum(1, keepdim=True)
                              + qa.amax(1, keepdim=True) * 2.0 ** -35 * size_k.sum(1))
             else:
-                sizes = ks * ((kc - mid).abs() if out_f32 else kc + 2048.0)
+                sizes = ks * ((kc - mid).abs() if out_f32 else kc)
                 m = qa @ sizes[:, i].T
                 e = scale * (terms * (D / 8 + 2) * 2.0 ** -23 * m + 2.0 ** -22 * (m + qa @ (kz.abs() + mid * ks)[:, i].T)
                              + qa.amax(1, keepdim=True) * 2.0 ** -35 * (ks * (kc + mid))[:, i].sum(1))
