@@ -31,7 +31,7 @@
 // (128 registers for 16 warps an SM spilled: 153 us). Sixteen rows take those instructions once for two rows' tiles;
 // with more rows they are taken again for every sixteen, and kv_tiles.cu takes over where that costs more. 64 keys to a step
 // where there is room: 153 -> 140 us, of what was 140 then. V's codes are x and not c: their sums over thousands of keys
-// would lose to c's mean what the tensor cores cut off at each product.
+// would lose to c's mean what the tensor cores cut off at each product (c, and the mean taken off by a second product: 137).
 #include <algorithm>
 #include "kv_quant.cuh"
 #include "kv_rows.cuh"
