@@ -30,7 +30,7 @@
 // a head (a half of them on the ALU), 56 % of what the warps' schedulers can issue, with three warps to each: more do not fit
 // (128 registers for 16 warps an SM spilled: 153 us). Sixteen rows take those instructions once for two rows' tiles;
 // with more rows they are taken again for every sixteen, and kv_tiles.cu takes over where that costs more. 64 keys to a step
-// where there is room: 153 -> 140 us, of what was 140 then. V's codes are x and not c: their sums over thousands of keys
+// where there is room: 153 -> 140 us when that was done. V's codes are x and not c: their sums over thousands of keys
 // would lose to c's mean what the tensor cores cut off at each product (c, and the mean taken off by a second product: 137).
 #include <algorithm>
 #include "kv_quant.cuh"
