@@ -412,7 +412,7 @@ FA_API fa_status fakv_qattend(const void* q, void* O, float* LSE, const int* cu,
   // Above this many rows per sequence and kv head (on average) tensor-core tiles, whose time hardly depends on how many
   // there are, where kv_qrows.cu makes numbers of all codes again for every 16. D 128, 8 kv heads, us (rows, tiles):
   //   4 bits  16 sequences of up to 8192: 27 rows 82, 96; 35 rows 99, 97     one of 16384: 48 rows 32, 35; 64 rows 38, 35
-  //   8 bits  35 rows 103, 119; 71 rows 181, 122                             48 rows 33, 41; 64 rows 39, 41
+  //   8 bits  27 rows 87, 119; 35 rows 103, 119                              48 rows 33, 41; 64 rows 39, 41
   const long long limit = cache->bits == 4 ? 32 : 48;
   if (cache->dtype == FA_BF16 && (long long)t.T * (t.H / cache->HKV) > limit * t.B) {
     st = launch_qattend_tiles(q, O, LSE, cu, slots, qcache_of(*cache, pages, p->plane), t,
