@@ -920,6 +920,7 @@ __global__ void __launch_bounds__(TilesCfg<D, BITS>::THREADS, 1)
               for (int kk = 0; kk < 32; ++kk) r[kk] = __float_as_uint(__uint_as_float(r[kk]) * by);
               tmem_st32(o_addr + c * 32, r);
             }
+            tmem_st_wait();  // (a tile may do it three times: a load is not ordered behind a store by itself)
           };
           // (2^8 of a probability and 2^6 of V's exponent beyond v_ref: P stays below 2^15)
           if (t == 0 || v_top > v_ref + 6.f) {

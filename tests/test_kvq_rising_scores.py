@@ -1,0 +1,67 @@
+"""Chunks over the cache in 4 or 8 bits whose rows' references move again and again: scores that rise in both halves of a
+tile's keys, V's size that grows in the same tile. What was summed up before has to follow each move."""
+import pytest
+import torch
+
+import _kv_ref
+import _kvq_ref as ref
+import _kvq_seen as seen
+
+pytestmark = pytest.mark.gpu
+BF, F32 = torch.bfloat16, torch.float32
+
+
+@pytest.fixture(scope="module")
+def kv():
+    import __graft_entry__
+    __graft_entry__.build_library()
+    assert torch.cuda.is_available(), "GPU tests need a CUDA device"
+    from attention_fa_fwd_02_gb300 import kv as m
+    return m
+
+
+def rising(kv, bits, n, score, value, rows, H=2, D=128, seed=0):
+    """A cache of one sequence, two groups of V's columns, and queries whose scores of key j are about score[j] (log2); V is
+    `value[j]` in size in the second group, and about 1 in the first one for keys of the first two tiles, then zero."""
+    g = torch.Generator().manual_seed(seed)
+    cache, _ = ref.make(kv, [n], 16, 1, D, bits, 64, BF, stored=False)
+    way = torch.randn(D, generator=g).sign()
+    k = score[:, None] * way * (1 + 0.05 * torch.rand(n, D, generator=g)) / D
+    v = torch.randn(n, D, generator=g)
+    v[256:, :64] = 0.0
+    v[:, 64:] *= value[:, None]
+    cache.append(None, k[:, None].to(BF).cuda(), v[:, None].to(BF).cuda(), torch.tensor([0, n], dtype=torch.int32).cuda())
+    q = (way * (1 + 0.02 * torch.randn(rows, H, D, generator=g))).to(BF).cuda()
+    return cache, q, 0.6931471805599453  # (of which a score's log2 is the product of q and k)
+
+
+def check(cache, q, scale, causal, out_dtype):
+    """The same sequence and queries 320 times in one call: more items than CTAs, so that many are not shared out tile by
+    tile (one whose tiles have a CTA each never moves a reference)."""
+    rows, B = q.shape[0], 320
+    o, l = cache.attend(q.repeat(B, 1, 1), torch.arange(B + 1, dtype=torch.int32).cuda() * rows,
+                        torch.zeros(B, dtype=torch.int32).cuda(), scale=scale, causal=causal, out_dtype=out_dtype)
+    cache.check()
+    want, want_l, bo, bl = seen.attend(cache, q, [rows], [0], scale, causal, 0, 0, True, out_dtype == F32)
+    o, l = o.cpu().unflatten(0, (B, rows)), l.cpu().unflatten(0, (B, rows))
+    _kv_ref.close(o, want, bo, "O")
+    assert bool(((l.double() - want_l).abs() <= bl).all())
+    return o.double(), want.expand_as(o)
+
+
+@pytest.mark.parametrize("out_dtype", [BF, F32])
+@pytest.mark.parametrize("causal", [False, True])
+@pytest.mark.parametrize("bits", [4, 8])
+@pytest.mark.parametrize("grown", [0, 8])
+def test_references_that_move_in_both_halves_of_a_tile(kv, bits, causal, grown, out_dtype):
+    """From the third tile on scores rise by 2^10 (more than the 2^8 that a reference waits for) with each half, and V by
+    2^grown with each tile: O is rescaled twice, or three times, to a tile. The first group's columns are made of the first two
+    tiles' keys alone: of them a factor that was lost would be all that is left."""
+    n, rows = 128 * 5, 60
+    half, tile = torch.arange(n) // 64, torch.arange(n) // 128
+    cache, q, scale = rising(kv, bits, n, 10.0 * (half - 3).clamp(min=0).float(), 2.0 ** (grown * (tile - 1).clamp(min=0)), rows)
+    o, want = check(cache, q, scale, causal, out_dtype)
+    # (nearer than the worst case: P and V's roundings, 2^-11 each, and a bf16 output's)
+    first = slice(0, 64)
+    assert float((o[..., first] - want[..., first]).norm() / want[..., first].norm()) < 4e-3
+    assert float((o - want).norm() / want.norm()) < 4e-3
