@@ -13,10 +13,11 @@
 //           a pair.) q times a power of two per row that brings its largest value to 2^14 is fp16 too, exactly but for
 //           what is 2^-28 of that
 //   O^T     O_d = sum_k (p_k s_k) x_kd + sum_k p_k z'_k: the scales enter the probabilities, times a power
-//           of two that keeps the largest scale so far just below 2^7; the offsets are one more sum
+//           of two that keeps the largest scale that the row has seen at most 2^6; the offsets are one more sum
 //           per row and group. p s is one fp16 term where O is bf16 (2^-11 of itself, an eighth of O's
 //           own rounding), two (2^-22) where O is fp32; what is below 2^-30 of the largest p s rounds to
-//           2^-40 of it
+//           2^-40 of it. (A power of two to a row: with one for an item, a key that a row does not see and whose V is
+//           2^31 times as large took from it all that codes stand for)
 //
 // so nothing of the cache is rounded again. A code costs about an instruction (kv_quant.cuh):
 //   K  columns are what is summed over, in any order: a thread takes the 8 (4) columns of one
@@ -117,6 +118,7 @@ __global__ void __launch_bounds__(NTHREADS, QRowsCfg<E, OUT_BF, BITS, D, NG_, NT
   // K's codes: 2^-24 times the code (q_small), or, where O is fp32, centred: an instruction more, and sums of an eighth
   constexpr bool CENTRED = !OUT_BF;
   constexpr float CENTRE = BITS == 4 ? 8.f : 128.f;
+  constexpr float NO_LIFT = 0x1p126f;
   constexpr int VT = BITS == 4 ? 2 : 1;  // output tiles of a chunk: code pairs 2 t and 2 t + 1 of a word of V
   extern __shared__ __align__(1024) uint8_t smem[];
   __shared__ PlanShared<NTHREADS, WARPS> plan;
@@ -317,7 +319,10 @@ __global__ void __launch_bounds__(NTHREADS, QRowsCfg<E, OUT_BF, BITS, D, NG_, NT
     }
 
     // Steps of GROUP keys, whose place is filled again as soon as it is read, NP steps ahead.
-    float cap = 0.f, lift = 1.f;  // V's scales so far are at most cap; times lift they are below 2^7
+    // V's scales that a row has seen, times its lift, are at most 2^6 (before the first one: any is above it)
+    float2 lift[NTR];
+#pragma unroll
+    for (int nt = 0; nt < NTR; ++nt) lift[nt] = make_float2(NO_LIFT, NO_LIFT);
 #pragma unroll 1
     for (int k = 0; k < min(n, NP); ++k) {
       const int at = ring + k < NP ? ring + k : ring + k - NP;
@@ -402,39 +407,49 @@ __global__ void __launch_bounds__(NTHREADS, QRowsCfg<E, OUT_BF, BITS, D, NG_, NT
               sc[kt][nt][z] = v;
             }
           }
-        if (edge) {
+        // (what a row does not see has no part in it: scores -infinity; V's scales, which may be those of no token, passed over)
+        float2 most[NTR];  // the largest of V's scales among the lane's keys that the row sees (NaN is passed over)
+        {
+          float top[KT][2];
 #pragma unroll
-          for (int nt = 0; nt < NTR; ++nt)
+          for (int kt = 0; kt < KT; ++kt)
 #pragma unroll
-            for (int e = 0; e < 2; ++e) {
-              // row 8 nt + 2 quad + e sees keys [lo, hi]
-              const int p = s.len - s.n + g.rep.of(x.rho0 + min(nt * 8 + quad * 2 + e, x.rows - 1));
-              const int hi = g.causal ? min(p, s.len - 1) : s.len - 1;
-              const int lo = g.window > 0 ? p - g.window + 1 : 0;
-#pragma unroll
-              for (int kt = 0; kt < KT; ++kt)
-#pragma unroll
-                for (int z = 0; z < 2; ++z) {
-                  const int key = j0 + kt * 16 + z * 8 + oct;
-                  if (key < lo || key > hi) (e ? sc[kt][nt][z].y : sc[kt][nt][z].x) = -INFINITY;
-                }
+            for (int z = 0; z < 2; ++z) {
+              uint32_t p[NG];
+              params(slot_v, kt, z, p);
+              top[kt][z] = NG == 1 ? q_scale(p[0]) : fmaxf(q_scale(p[0]), q_scale(p[NG - 1]));
             }
+          if (edge) {
+#pragma unroll
+            for (int nt = 0; nt < NTR; ++nt)
+#pragma unroll
+              for (int e = 0; e < 2; ++e) {
+                // row 8 nt + 2 quad + e sees keys [lo, hi]
+                const int p = s.len - s.n + g.rep.of(x.rho0 + min(nt * 8 + quad * 2 + e, x.rows - 1));
+                const int hi = g.causal ? min(p, s.len - 1) : s.len - 1;
+                const int lo = g.window > 0 ? p - g.window + 1 : 0;
+                float all = 0.f;
+#pragma unroll
+                for (int kt = 0; kt < KT; ++kt)
+#pragma unroll
+                  for (int z = 0; z < 2; ++z) {
+                    const int key = j0 + kt * 16 + z * 8 + oct;
+                    if (key < lo || key > hi) (e ? sc[kt][nt][z].y : sc[kt][nt][z].x) = -INFINITY;
+                    else all = fmaxf(all, top[kt][z]);
+                  }
+                (e ? most[nt].y : most[nt].x) = all;
+              }
+          } else {
+            float all = 0.f;
+#pragma unroll
+            for (int kt = 0; kt < KT; ++kt) all = ptx::max3(all, top[kt][0], top[kt][1]);
+#pragma unroll
+            for (int nt = 0; nt < NTR; ++nt) most[nt] = make_float2(all, all);
+          }
         }
         // -------- probabilities; m, and the power of two on V's scales, where they have to move
-        float most = 0.f;
-#pragma unroll
-        for (int kt = 0; kt < KT; ++kt)
-#pragma unroll
-          for (int z = 0; z < 2; ++z) {
-            const int key = j0 + kt * 16 + z * 8 + oct;
-            uint32_t p[NG];
-            params(slot_v, kt, z, p);
-#pragma unroll
-            for (int k = 0; k < NG; ++k)  // (what no row sees need be no token; NaN is passed over)
-              if (!edge || (key >= x.lo && key < x.hi)) most = fmaxf(most, q_scale(p[k]));
-          }
         float2 mx[NTR];
-        bool grow = most > cap;
+        bool grow = false;
 #pragma unroll
         for (int nt = 0; nt < NTR; ++nt) {
           mx[nt] = make_float2(fmaxf(sc[0][nt][0].x, sc[0][nt][1].x), fmaxf(sc[0][nt][0].y, sc[0][nt][1].y));
@@ -443,34 +458,35 @@ __global__ void __launch_bounds__(NTHREADS, QRowsCfg<E, OUT_BF, BITS, D, NG_, NT
             mx[nt] = make_float2(ptx::max3(mx[nt].x, sc[kt][nt][0].x, sc[kt][nt][1].x), ptx::max3(mx[nt].y, sc[kt][nt][0].y, sc[kt][nt][1].y));
           mx[nt] = make_float2(mx[nt].x * ql[nt].x, mx[nt].y * ql[nt].y);
           grow |= mx[nt].x > m[nt].x + RESCALE_THRESHOLD || mx[nt].y > m[nt].y + RESCALE_THRESHOLD;
+          grow |= most[nt].x * lift[nt].x > 64.f || most[nt].y * lift[nt].y > 64.f;
         }
         if (__any_sync(0xffffffffu, grow)) {
-          most = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(most)));
-          float fv = 1.f;
-          if (most > cap) {
-            const int e = min(max(q_exponent(most), -100), 126);
-            cap = q_pow2(e + 1);  // (twice the largest may come before the next move)
-            fv = q_pow2(5 - e) / lift;
-            lift = q_pow2(5 - e);
-          }
 #pragma unroll
           for (int nt = 0; nt < NTR; ++nt) {
-            float2 f;
+            float2 f, fv;
 #pragma unroll
             for (int e = 0; e < 2; ++e) {
-              float v = e ? mx[nt].y : mx[nt].x;
-              v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 4));
-              v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 8));
-              v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 16));
+              auto over_keys = [](float v) {
+                v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 4));
+                v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 8));
+                return fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 16));
+              };
+              // (a row by itself, and by the keys that it sees: not as its neighbours' scores fall, or a key's V that is theirs)
+              const float v = over_keys(e ? mx[nt].y : mx[nt].x), top = over_keys(e ? most[nt].y : most[nt].x);
+              float& had = e ? lift[nt].y : lift[nt].x;
+              float to = had;
+              if (top * had > 64.f) to = q_pow2(5 - min(max(q_exponent(top), -100), 126));  // (twice as large may come before the next move)
+              (e ? fv.y : fv.x) = to / had;
+              had = to;
               float& was = e ? m[nt].y : m[nt].x;
-              const float mn = v > was + RESCALE_THRESHOLD ? v : was;  // (a row by itself: not as its neighbours' scores fall)
+              const float mn = v > was + RESCALE_THRESHOLD ? v : was;
               (e ? f.y : f.x) = ptx::ex2(was - mn);
               was = mn;
             }
             l[nt] = ptx::mul2(l[nt], f);
 #pragma unroll
             for (int k = 0; k < NG; ++k) oz[nt][k] = ptx::mul2(oz[nt][k], f);
-            f = ptx::mul2(f, make_float2(fv, fv));
+            f = ptx::mul2(f, fv);
 #pragma unroll
             for (int w = 0; w < CH; ++w)
 #pragma unroll
@@ -500,17 +516,17 @@ __global__ void __launch_bounds__(NTHREADS, QRowsCfg<E, OUT_BF, BITS, D, NG_, NT
               for (int k = 0; k < NG; ++k) {
                 uint32_t pv[NG];
                 params(slot_v, kt, z, pv);
-                const float ps = q_scale(pv[k]), pz = fmaf(ps, CENTRE, q_offset(pv[k])), pl = ps * lift;
+                const float ps = q_scale(pv[k]), pz = fmaf(ps, CENTRE, q_offset(pv[k]));
 #pragma unroll
                 for (int nt = 0; nt < NTR; ++nt) {
-                  const float2 p = sc[kt][nt][z];
+                  const float2 p = sc[kt][nt][z], pl = ptx::mul2(make_float2(ps, ps), lift[nt]);
                   float2 sp;
                   if constexpr (decltype(masked)::value) {  // a key that a row does not see may be anything
-                    sp = make_float2(p.x == 0.f ? 0.f : p.x * pl, p.y == 0.f ? 0.f : p.y * pl);
+                    sp = make_float2(p.x == 0.f ? 0.f : p.x * pl.x, p.y == 0.f ? 0.f : p.y * pl.y);
                     oz[nt][k].x += p.x == 0.f ? 0.f : p.x * pz;
                     oz[nt][k].y += p.y == 0.f ? 0.f : p.y * pz;
                   } else {
-                    sp = make_float2(p.x * pl, p.y * pl);
+                    sp = ptx::mul2(p, pl);
                     oz[nt][k].x = fmaf(p.x, pz, oz[nt][k].x);
                     oz[nt][k].y = fmaf(p.y, pz, oz[nt][k].y);
                   }
@@ -587,7 +603,7 @@ __global__ void __launch_bounds__(NTHREADS, QRowsCfg<E, OUT_BF, BITS, D, NG_, NT
         const int r = nt * 8 + quad * 2 + e;
         if (oct == 0) ends_sh.ml[warp][r] = make_float2(e ? m[nt].y : m[nt].x, v);
         float* const to = reinterpret_cast<float*>(mine) + r * C::OS + oct * 2 * VT;
-        const float by = 1.f / lift;
+        const float by = 1.f / (e ? lift[nt].y : lift[nt].x);
 #pragma unroll
         for (int w = 0; w < CH; ++w) {
           const float zw = z[NG == 1 ? 0 : BITS == 4 ? w / 2 : w / 4];

@@ -283,9 +283,9 @@ FA_API fa_status fakv_qread(void* K_out, void* V_out, const int* cu, const int* 
  *   many rows (bf16 q): K and q as above, so that LSE is too; V to 2^-11 of the value and of its two parts,
  *     codes times scale and offset, and a probability to 2^-11: of an fp32 O too, whose last bits are better
  *     had from fp32 queries or from fewer rows to a call
- * Products of a probability and a key's V are taken against the largest V of the keys gone through so far: those
- * 2^-14 of it and smaller lose bits, those below 2^-30 count for nothing (an O that is made of them alone, beside far
- * larger V, is good to that, and not to 2^-11 of itself).
+ * Products of a probability and a key's V are taken against the largest V of the keys gone through so far (few rows: of
+ * those that the row sees): those 2^-14 of it and smaller lose bits, those below 2^-30 count for nothing (an O that is
+ * made of them alone, beside far larger V, is good to that, and not to 2^-11 of itself).
  * NaN or infinity in a row of q makes that row's O and LSE NaN and no other's. A key that stands for NaN makes
  * the rows that see it NaN (K: O and LSE; V: their O in the group's columns, and where there are many
  * rows all of O, and LSE) and no other. Which kernel is chosen, T and a batch of both kinds: as for fakv_attend,

@@ -13,11 +13,12 @@ can have a weight (those whose score is e^50 and more below the LSE, error and a
 value is added for them).
 
 A product of a probability and V, few rows: probability times scale in fp16 (one term 2^-11, two 2^-22), of which what is under
-2^-30 of the largest scale S so far is lost, taken against the largest score so far: 2^-30 mid S exp(top - LSE). Many
-rows: V to 2^-11 twice (z', then s x + z'), P to 2^-11, and P's floor in fp16: at most three roundings of 2^-25 where V's
-largest so far (or up to 2^3 of it, of a neighbour that is hidden) is brought to 2^7: below 2^-19 of it, and 2 for a
-reference that is a whole power of two: 2^-18 V exp(top - LSE). A group of keys that is gone through at once has 128 (few
-rows: up to 64) of them; a part that begins later has seen less, and smaller."""
+2^-30 of the largest scale S so far is lost, taken against the largest score so far: 2^-30 |x| S exp(top - LSE) of a code x
+(of a scale that is not 0). Many rows: V to 2^-11 twice (z', then s x + z'), P to 2^-11, and P's floor in fp16, at most three
+roundings of 2^-25, P being p 2^(E - R): E the exponent that brings the key's largest value U below 2^7 (so 2^-E < 2^7 / U), R
+at most that of the largest value V so far (2^R <= 2^-6 V), or up to 3 more (of a neighbour that is hidden): 2^-23 2^(R - E)
+of a value v, and 2 for a reference that is a whole power of two: 2^-18 V |v| / U exp(top - LSE). A group of keys that is gone
+through at once has 128 (few rows: up to 64) of them; a part that begins later has seen less, and smaller."""
 import math
 
 import torch
@@ -78,12 +79,14 @@ def attend(cache, q, new, slots, scale, causal=True, window=0, plane=0, tiles=Fa
             mass = (vs * (vc - mid).abs() + (vz + mid * vs).abs())[:, i]
             seen = lambda x: torch.where(see, x[None], 0.0)  # noqa: E731
             top = torch.exp(so_far(z) - base)
-            if tiles:
-                up, lost, value = 3 * 2.0 ** -11, 2.0 ** -18, torch.maximum(vz.abs(), (vs * steps + vz).abs())
-            else:
-                up, lost, value = 2.0 ** -22 if out_f32 else 2.0 ** -11, 2.0 ** -30 * mid, vs
+            up = 3 * 2.0 ** -11 if tiles else 2.0 ** -22 if out_f32 else 2.0 ** -11
             up += 2.0 ** -22 + (size / 16 + 32) * 2.0 ** -23 + size * 2.0 ** -24
-            floor = torch.where(see, lost * so_far(seen(value[:, i].amax(1))) * top, 0.0).sum(1, keepdim=True)
+            size_v = (torch.maximum(vz.abs(), (vs * steps + vz).abs()) if tiles else vs)[:, i].amax(1)
+            largest = so_far(seen(size_v)) * top * see
+            if tiles:
+                floor = 2.0 ** -18 * (largest / size_v.clamp(min=1e-100)) @ mass
+            else:
+                floor = 2.0 ** -30 * largest @ ((vc - mid).abs() * (vs > 0))[:, i]
             none = size * math.exp(-50.0) * seen(mass.amax(1)).amax(1, keepdim=True)
             bo[at:at + n, h] = 2 * e * (w @ v[:, i].abs()) + up * (w @ mass) + floor + none
             bl[at:at + n, h] = e[:, 0] + (size / 16 + 32) * 2.0 ** -23 + lse.nan_to_num(neginf=0.0).abs() * 2.0 ** -22
