@@ -449,6 +449,7 @@ __global__ void __launch_bounds__(NTHREADS, QRowsCfg<E, OUT_BF, BITS, D, NG_, NT
         }
         // -------- probabilities; m, and the power of two on V's scales, where they have to move
         float2 mx[NTR];
+        float2 by[NTR];  // (ql, or 1 where the scores have been multiplied with it)
         bool grow = false;
 #pragma unroll
         for (int nt = 0; nt < NTR; ++nt) {
@@ -459,6 +460,8 @@ __global__ void __launch_bounds__(NTHREADS, QRowsCfg<E, OUT_BF, BITS, D, NG_, NT
           mx[nt] = make_float2(mx[nt].x * ql[nt].x, mx[nt].y * ql[nt].y);
           grow |= mx[nt].x > m[nt].x + RESCALE_THRESHOLD || mx[nt].y > m[nt].y + RESCALE_THRESHOLD;
           grow |= most[nt].x * lift[nt].x > 64.f || most[nt].y * lift[nt].y > 64.f;
+          grow |= fabsf(m[nt].x) > Q_LARGE || fabsf(m[nt].y) > Q_LARGE;
+          by[nt] = ql[nt];
         }
         if (__any_sync(0xffffffffu, grow)) {
 #pragma unroll
@@ -482,6 +485,14 @@ __global__ void __launch_bounds__(NTHREADS, QRowsCfg<E, OUT_BF, BITS, D, NG_, NT
               const float mn = v > was + RESCALE_THRESHOLD ? v : was;
               (e ? f.y : f.x) = ptx::ex2(was - mn);
               was = mn;
+              if (fabsf(mn) > Q_LARGE) {
+                const float l = e ? ql[nt].y : ql[nt].x;
+#pragma unroll
+                for (int kt = 0; kt < KT; ++kt)
+#pragma unroll
+                  for (int z = 0; z < 2; ++z) (e ? sc[kt][nt][z].y : sc[kt][nt][z].x) *= l;
+                (e ? by[nt].y : by[nt].x) = 1.f;
+              }
             }
             l[nt] = ptx::mul2(l[nt], f);
 #pragma unroll
@@ -501,7 +512,7 @@ __global__ void __launch_bounds__(NTHREADS, QRowsCfg<E, OUT_BF, BITS, D, NG_, NT
           for (int nt = 0; nt < NTR; ++nt)
 #pragma unroll
             for (int z = 0; z < 2; ++z) {
-              const float2 v = ptx::fma2(sc[kt][nt][z], ql[nt], make_float2(-m[nt].x, -m[nt].y));
+              const float2 v = ptx::fma2(sc[kt][nt][z], by[nt], make_float2(-m[nt].x, -m[nt].y));
               sc[kt][nt][z] = make_float2(ptx::ex2(v.x), ptx::ex2(v.y));
               l[nt] = ptx::add2(l[nt], sc[kt][nt][z]);
             }

@@ -109,6 +109,10 @@ __device__ __forceinline__ uint32_t q_half2(float lo, float hi) {
   const __half2 h = __floats2half2_rn(lo, hi);
   return *reinterpret_cast<const uint32_t*>(&h);
 }
+// From here on a score (log2) is rounded before its row's reference m, one such score, is taken off. Below it the two are one
+// fused operation, in which the largest score keeps what m was rounded by, half an ulp of m: 2^5 of 2^30, by which its
+// probability would be 2^32, or 2^-32 and the row's sum 0.
+constexpr float Q_LARGE = 0x1p20f;
 __device__ __forceinline__ float q_pow2(int e) { return __int_as_float((e + 127) << 23); }      // -126 <= e <= 127
 __device__ __forceinline__ int q_exponent(float x) { return (__float_as_int(x) >> 23) - 127; }  // of x > 0
 

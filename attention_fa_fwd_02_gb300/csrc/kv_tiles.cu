@@ -944,7 +944,7 @@ __global__ void __launch_bounds__(TilesCfg<D, BITS>::THREADS, 1)
             }
             if (edge) mask_outside<64>(s, lo_i - c0 - 64 * h, hi_i - c0 - 64 * h);
             // (positive whatever the row: a masked score is -infinity times it)
-            const float kc[2] = {fmaxf(qf * i0.x, FLT_MIN), fmaxf(qf * i1.x, FLT_MIN)};
+            float kc[2] = {fmaxf(qf * i0.x, FLT_MIN), fmaxf(qf * i1.x, FLT_MIN)};
             const float up[2] = {fmaxf(i0.y - v_ref, -60.f), fmaxf(i1.y - v_ref, -60.f)};  // (far below that, P is 0 in fp16)
             float mt = -INFINITY;
 #pragma unroll
@@ -977,10 +977,20 @@ __global__ void __launch_bounds__(TilesCfg<D, BITS>::THREADS, 1)
               }
               m = m_new;
             }
+            float less = m;  // (what is still to be taken off)
+            if (const bool large = fabsf(m) > Q_LARGE && m > -FLT_MAX; __any_sync(0xffffffffu, large)) {
+              const float f[2] = {large ? kc[0] : 1.f, large ? kc[1] : 1.f}, now = large ? m : 0.f;
+#pragma unroll
+              for (int kk = 0; kk < 64; ++kk) s[kk] = __fsub_rn(__fmul_rn(s[kk], f[kk / 32]), now);
+              if (large) {
+                kc[0] = kc[1] = 1.f;
+                less = 0.f;
+              }
+            }
             uint32_t pk[32];
 #pragma unroll
             for (int b = 0; b < 2; ++b) {
-              const float2 by = make_float2(kc[b], kc[b]), off = make_float2(up[b] - m, up[b] - m);
+              const float2 by = make_float2(kc[b], kc[b]), off = make_float2(up[b] - less, up[b] - less);
               float2 ls[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
 #pragma unroll
               for (int kk = 0; kk < 16; ++kk) {

@@ -286,6 +286,8 @@ FA_API fa_status fakv_qread(void* K_out, void* V_out, const int* cu, const int* 
  * Products of a probability and a key's V are taken against the largest V of the keys gone through so far (few rows: of
  * those that the row sees): those 2^-14 of it and smaller lose bits, those below 2^-30 count for nothing (an O that is
  * made of them alone, beside far larger V, is good to that, and not to 2^-11 of itself).
+ * Scores (times log2 e) are below 2^127 in size; of 2^20 and more they are rounded to 24 bits each before the largest is
+ * taken off.
  * NaN or infinity in a row of q makes that row's O and LSE NaN and no other's. A key that stands for NaN makes
  * the rows that see it NaN (K: O and LSE; V: their O in the group's columns, and where there are many
  * rows all of O, and LSE) and no other. Which kernel is chosen, T and a batch of both kinds: as for fakv_attend,

@@ -8,9 +8,10 @@ e_j = scale (terms (D / 8 + 2) 2^-23 m_j + 2^-22 (m_j + |z'| sum |q|)), m_j = su
 scales exact in fp16 or to 2^-21 of the key's own size, offsets and sums of q in two terms (2^-22 each): with m_j = sum |q| (s |x| +
 |z'| + s mid), e_j = scale m_j ((D / 4 + 4) 2^-23 + 2^-20).
 
-A score error e moves a probability by exp(e), O by 2 e A with A = sum w |v|, the LSE by e: the largest e_j of the keys that
-can have a weight (those whose score is e^50 and more below the LSE, error and all, have none; n e^-50 of the largest
-value is added for them).
+A score error e moves a probability by exp(e), O by 2 e A with A = sum w |v - O| (e up to 1/4; beyond that O is some mean of
+the V that may have a weight, unless that is one key's alone), the LSE by e: the largest e_j of the keys that may have a
+weight. Those whose score, with its error, is 50 and more below what the largest one's is at least have none, and n e^-50 of
+the largest value is added for them.
 
 A product of a probability and V, few rows: probability times scale in fp16 (one term 2^-11, two 2^-22), of which what is under
 2^-30 of the largest scale S so far is lost, taken against the largest score so far: 2^-30 |x| S exp(top - LSE) of a code x
@@ -73,7 +74,9 @@ def attend(cache, q, new, slots, scale, causal=True, window=0, plane=0, tiles=Fa
             lse = torch.logsumexp(z, 1)
             base = lse.nan_to_num(neginf=0.0)[:, None]
             w = torch.where(see, torch.exp(z - base), 0.0)
-            e = torch.where(see & (z + e > base - 50.0), e, 0.0).amax(1, keepdim=True)
+            may = see & (z + e > (z - e).amax(1, keepdim=True) - 50.0)
+            e = torch.where(may, e, 0.0).amax(1, keepdim=True)
+            several = (may.sum(1, keepdim=True) > 1) & (e > 0.25)
             O[at:at + n, h] = w @ v[:, i]
             L[at:at + n, h] = lse
             mass = (vs * (vc - mid).abs() + (vz + mid * vs).abs())[:, i]
@@ -87,8 +90,10 @@ def attend(cache, q, new, slots, scale, causal=True, window=0, plane=0, tiles=Fa
                 floor = 2.0 ** -18 * (largest / size_v.clamp(min=1e-100)) @ mass
             else:
                 floor = 2.0 ** -30 * largest @ ((vc - mid).abs() * (vs > 0))[:, i]
+            moved = torch.stack([(w[r, :, None] * (v[:, i] - O[at + r, h]).abs()).sum(0) for r in range(n)])
+            moved = torch.where(several, 2 * seen(v[:, i].abs().amax(1)).amax(1, keepdim=True), 2 * e * moved)
             none = size * math.exp(-50.0) * seen(mass.amax(1)).amax(1, keepdim=True)
-            bo[at:at + n, h] = 2 * e * (w @ v[:, i].abs()) + up * (w @ mass) + floor + none
+            bo[at:at + n, h] = moved + up * (w @ mass) + floor + none
             bl[at:at + n, h] = e[:, 0] + (size / 16 + 32) * 2.0 ** -23 + lse.nan_to_num(neginf=0.0).abs() * 2.0 ** -22
         at += n
     return O, L, bo, bl
