@@ -242,6 +242,8 @@ __device__ __forceinline__ void cp_piece(uint32_t dst, const void* src, bool tak
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(take ? 16 : 0) : "memory");
 }
 constexpr int TILE_INFO = 8;  // tiles whose powers of two are kept: K's codes are at most five tiles ahead of the softmax
+constexpr int SPREAD = 3;     // log2 of how far below the largest of 32 keys a key may be and share its powers of two
+constexpr float OWN = 1024.f; // added to V's exponent of 32 keys that have their own
 
 // q as fp16, each row times a power of two that brings its largest value to 2^14 (exactly, but for what is 2^-28 of
 // that), and what undoes it, times the softmax scale; `pairs`: each eight columns in the order 0 4 1 5 2 6 3 7, which is
@@ -319,7 +321,10 @@ __global__ void __launch_bounds__(TilesCfg<D, BITS>::THREADS, 1)
       bar_vempty[VST], bar_grant[NQ], bar_s[NQ], bar_o[NQ], bar_join, bar_drain;
   __shared__ uint32_t tmem_base_sh;
   __shared__ int abort_sh, stuck_sh;
-  __shared__ float2 info_sh[BITS ? TILE_INFO : 1][4];  // codes: of each quarter of a tile, K's power of two and V's exponent
+  // codes: of each quarter of a tile, K's power of two and V's exponent, or 1 and V's exponent + OWN, and of each key of that
+  // quarter K's power of two (the high half is its bits) and V's (the low half)
+  __shared__ float2 info_sh[BITS ? TILE_INFO : 1][4];
+  __shared__ uint32_t keys_sh[BITS ? TILE_INFO : 1][BITS ? 128 : 1];
   __shared__ PlanShared<C::THREADS, 1> plan;
   grid_launch_dependents();
   const int warp = warp_id(), lane = lane_id();
@@ -412,7 +417,9 @@ __global__ void __launch_bounds__(TilesCfg<D, BITS>::THREADS, 1)
     // 2^7 (V: undone in the probabilities). V is x s + z', rounded to 2^-11 of it. A score's error moves a probability by
     // its factor, so K is not rounded: x s of a nibble x in -8 .. 7 has the eleven bits of fp16 (of a byte it is two such
     // terms, 16 (h - 8) s and (l - 8) s, in two planes), and z' (two terms) is multiplied with the row's sum of q in one
-    // step of the product more. (K as x s + z' in one term had LSEs 8e-6 off, and 3e-5 where few keys were seen.) The
+    // step of the product more. (K as x s + z' in one term had LSEs 8e-6 off, and 3e-5 where few keys were seen.) Where one
+    // of the 32 keys is 2^SPREAD below the largest, or K's scale too small to be exact, each key has powers of two of its
+    // own, which the softmax undoes key by key: no key costs another's bits, least of all one that a row does not see. The
     // codes are on their way while those before are turned into numbers. Keys that no row sees, and those of a missing page,
     // are zeros; a key whose scale is NaN, in K or in V, is NaN in K and zeros in V, so that rows that see it become NaN
     // and the tile's others do not.
@@ -477,19 +484,41 @@ __global__ void __launch_bounds__(TilesCfg<D, BITS>::THREADS, 1)
           for (int j = 0; j < NG; ++j) bad |= (p[j] & 0x7fffu) > 0x7f80u;
           return bad;
         };
-        auto exponent_of = [&](const uint32_t (&p)[NG]) {  // of the largest value that the quarter's keys can hold
+        auto exponent_of = [&](const uint32_t (&p)[NG]) {  // of the largest value that the key can hold
           float top = 0.f;
 #pragma unroll
           for (int j = 0; j < NG; ++j)
             top = fmaxf(top, fmaxf(fabsf(q_offset(p[j])), fabsf(fmaf(q_scale(p[j]), STEPS, q_offset(p[j])))));
           if (nan(p)) top = 0.f;
-          top = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(top)));
           return min(max(q_exponent(top), -100), 126);
         };
-        auto factors = [&](auto is_v, const Params& b, float2* info) {
+        // the exponents that key `lane` of the quarter is written with: the largest of the 32, or its own
+        struct Exponents {
+          int k, v;
+        };
+        auto exponents = [&](const Params& b, int kt, int g) {
+          const int own_k = exponent_of(b.k), own_v = exponent_of(b.v), key = kt * BLOCK_N + quarter * 32 + lane;
+          Exponents e = {__reduce_max_sync(0xffffffffu, own_k), __reduce_max_sync(0xffffffffu, own_v)};
+          const float by = q_pow2(3 - e.k);
+          // (a K of zeros is as good with any exponent; a V of zeros that some row sees is not to stand for a larger one. A key
+          // that is NaN has no say: rows that see it are NaN)
+          bool apart = (own_k > -100 && own_k < e.k - SPREAD) ||
+                       (own_v < e.v - SPREAD && key >= seg.x.lo && key < seg.x.hi && !nan(b.k) && !nan(b.v));
+#pragma unroll
+          for (int j = 0; j < NG; ++j) apart |= q_scale(b.k[j]) > 0.f && q_scale(b.k[j]) * by < 0x1p-17f;
+          const float v_top = (float)(e.v - 6);
+          if (__any_sync(0xffffffffu, apart)) {
+            e = {own_k, own_v};
+            if (half == 0) keys_sh[g % TILE_INFO][quarter * 32 + lane] = (uint32_t)(own_k + 124) << 23 | (uint32_t)(own_v + 121) << 7;
+            if (half == 0 && lane == 0) info_sh[g % TILE_INFO][quarter] = make_float2(1.f, v_top + OWN);
+          } else if (half == 0 && lane == 0) {
+            info_sh[g % TILE_INFO][quarter] = make_float2(q_pow2(e.k - 3), v_top);
+          }
+          return e;
+        };
+        auto factors = [&](auto is_v, const Params& b, const Exponents& exps) {
           constexpr bool IS_V = decltype(is_v)::value;
-          const int ev = exponent_of(b.v) - 6, e = IS_V ? ev : exponent_of(b.k) - 3;
-          if (!IS_V && half == 0 && lane == 0) *info = make_float2(q_pow2(e), (float)ev);
+          const int e = IS_V ? exps.v - 6 : exps.k - 3;
           const float by = q_pow2(-e);
           const bool bad = nan(b.v) || (!IS_V && nan(b.k));
           Factors f;
@@ -632,9 +661,11 @@ __global__ void __launch_bounds__(TilesCfg<D, BITS>::THREADS, 1)
             const int kt = seg.k0 + t, left = seg.n - 1 - t, ks = g % KST, vs = pos % VST;
             ask_params(params_next, kt + 1, page_next);
             const int page_after = left > 1 ? octet_page(kt + 2) : -1;
+            Exponents exps;
             {
               // (what the stage is not needed for, before it is waited for; all have read tile g - 5's info, the place's last one's long before)
-              const Factors f = factors(std::false_type(), params, &info_sh[g % TILE_INFO][quarter]);
+              exps = exponents(params, kt, g);
+              const Factors f = factors(std::false_type(), params, exps);
               if (!(ok = __all_sync(0xffffffffu, wait_free(&bar_kempty[ks], ((g / KST) & 1) ^ 1)) != 0)) break;
               if (lane >> 4 == half) {
                 // z' 2^8 of key `lane`, high, high and low term of each group (for the high, low and high one of q's sums)
@@ -648,7 +679,7 @@ __global__ void __launch_bounds__(TilesCfg<D, BITS>::THREADS, 1)
               two(std::false_type(), f, sK(ks), kt);
             }
             if (lane == 0) mbar_arrive(&bar_kfull[ks]);
-            const Factors f = factors(std::true_type(), params, nullptr);
+            const Factors f = factors(std::true_type(), params, exps);
             if (pos >= (uint32_t)VST && !(ok = wait_release(pos - VST))) break;
             two(std::true_type(), f, sV(vs), kt);
             if (lane == 0) mbar_arrive(&bar_vfull[vs]);
@@ -891,7 +922,7 @@ __global__ void __launch_bounds__(TilesCfg<D, BITS>::THREADS, 1)
       const int lo_i = a.g.window > 0 ? p - a.g.window + 1 : 0;
       const int in_hi = a.g.causal ? min(p0, last) : last;  // keys that every row sees
       const int in_lo = a.g.window > 0 ? p1 - a.g.window + 1 : 0;
-      float m = -FLT_MAX, l = 0.f;
+      float m = BITS && r_in >= rows ? 0.f : -FLT_MAX, l = 0.f;
       // codes: the row's factor, and the exponent that the probabilities are taken against (O is O * 2^v_ref)
       float qf = 0.f, v_ref = 0.f;
       if (BITS && r_in < rows) {
@@ -922,10 +953,34 @@ __global__ void __launch_bounds__(TilesCfg<D, BITS>::THREADS, 1)
             }
             tmem_st_wait();  // (a tile may do it three times: a load is not ordered behind a store by itself)
           };
-          // (2^8 of a probability and 2^6 of V's exponent beyond v_ref: P stays below 2^15)
-          if (t == 0 || v_top > v_ref + 6.f) {
-            if (t > 0) rescale(ex2(v_ref - v_top));
-            v_ref = v_top;
+          // (2^8 of a probability and 2^6 of V's exponent beyond v_ref: P stays below 2^15. v_ref is the row's, and goes by
+          // the keys that it sees: of 32 that share an exponent those of which it sees one)
+          if (__any_sync(0xffffffffu, t == 0 || v_top > v_ref + 6.f)) {
+            float v_row = -106.f;
+#pragma unroll 1
+            for (int b = 0; b < 4; ++b) {
+              const float y = info[b].y;
+              if (y < OWN / 2) {
+                if (c0 + 32 * b <= hi_i && c0 + 32 * b + 31 >= lo_i) v_row = fmaxf(v_row, y);
+              } else {
+                const uint32_t* const keys = &keys_sh[g % TILE_INFO][32 * b];
+#pragma unroll 1
+                for (int kk = max(0, lo_i - c0 - 32 * b); kk <= min(31, hi_i - c0 - 32 * b); ++kk)
+                  v_row = fmaxf(v_row, (float)q_exponent(q_scale(keys[kk])));
+#pragma unroll 1
+                for (int c = 0; c < 32; c += 16) {
+                  uint32_t r[16];
+                  tmem_ld16(s_addr + 32 * b + c, r);
+#pragma unroll
+                  for (int kk = 0; kk < 16; ++kk) r[kk] = __float_as_uint(__uint_as_float(r[kk]) * q_offset(keys[c + kk]));
+                  tmem_st16(s_addr + 32 * b + c, r);
+                }
+                tmem_st_wait();
+              }
+            }
+            const bool more = t == 0 || v_row > v_ref + 6.f;
+            if (t > 0 && __any_sync(0xffffffffu, more)) rescale(more ? ex2(v_ref - v_row) : 1.f);
+            if (more) v_ref = v_row;
           }
           // 64 keys at a time, in a loop (see the code warps), P in the place of scores that are read. m moves by whole
           // powers of two: where it does, O, l and what is written of P follow exactly.
@@ -945,7 +1000,8 @@ __global__ void __launch_bounds__(TilesCfg<D, BITS>::THREADS, 1)
             if (edge) mask_outside<64>(s, lo_i - c0 - 64 * h, hi_i - c0 - 64 * h);
             // (positive whatever the row: a masked score is -infinity times it)
             float kc[2] = {fmaxf(qf * i0.x, FLT_MIN), fmaxf(qf * i1.x, FLT_MIN)};
-            const float up[2] = {fmaxf(i0.y - v_ref, -60.f), fmaxf(i1.y - v_ref, -60.f)};  // (far below that, P is 0 in fp16)
+            // (far below that, P is 0 in fp16; above it no key that the row sees)
+            const float up[2] = {fminf(fmaxf(i0.y - v_ref, -60.f), 6.f), fminf(fmaxf(i1.y - v_ref, -60.f), 6.f)};
             float mt = -INFINITY;
 #pragma unroll
             for (int b = 0; b < 2; ++b) {
@@ -962,7 +1018,8 @@ __global__ void __launch_bounds__(TilesCfg<D, BITS>::THREADS, 1)
             }
             // (each row for itself: no row's bits depend on another's)
             const bool grow = r_in < rows && mt > m + RESCALE_THRESHOLD;
-            if (__any_sync(0xffffffffu, grow)) {
+            float less = m;  // (what is to be taken off in one operation with the product)
+            if (__any_sync(0xffffffffu, grow || fabsf(m) > Q_LARGE)) {
               const float m_new = grow ? ceilf(mt) : m, corr = ex2(m - m_new);
               l *= corr;
               if (t > 0) rescale(corr);
@@ -975,14 +1032,10 @@ __global__ void __launch_bounds__(TilesCfg<D, BITS>::THREADS, 1)
                 for (int kk = 0; kk < 32; ++kk) r[kk] = q_fma2(r[kk], by, 0u);
                 tmem_st32(s_addr, r);
               }
-              m = m_new;
-            }
-            float less = m;  // (what is still to be taken off)
-            if (const bool large = fabsf(m) > Q_LARGE && m > -FLT_MAX; __any_sync(0xffffffffu, large)) {
-              const float f[2] = {large ? kc[0] : 1.f, large ? kc[1] : 1.f}, now = large ? m : 0.f;
+              less = m = m_new;
+              if (fabsf(m) > Q_LARGE) {
 #pragma unroll
-              for (int kk = 0; kk < 64; ++kk) s[kk] = __fsub_rn(__fmul_rn(s[kk], f[kk / 32]), now);
-              if (large) {
+                for (int kk = 0; kk < 64; ++kk) s[kk] = __fsub_rn(__fmul_rn(s[kk], kc[kk / 32]), m);
                 kc[0] = kc[1] = 1.f;
                 less = 0.f;
               }
@@ -1002,6 +1055,23 @@ __global__ void __launch_bounds__(TilesCfg<D, BITS>::THREADS, 1)
               l = fmaf((ls[0].x + ls[1].x) + (ls[0].y + ls[1].y), ex2(-up[b]), l);
             }
             tmem_st32(s_addr + h * 32, pk);
+          }
+          // P of keys that have exponents of their own, which were taken to be 6 beyond v_ref
+          if (__any_sync(0xffffffffu, v_top > OWN / 2)) {
+            tmem_st_wait();
+#pragma unroll 1
+            for (int b = 0; b < 4; ++b) {
+              if (info[b].y < OWN / 2) continue;
+              const uint32_t* const keys = &keys_sh[g % TILE_INFO][32 * b];
+              uint32_t r[16];
+              tmem_ld16(s_addr + 16 * b, r);
+#pragma unroll
+              for (int kk = 0; kk < 16; ++kk) {
+                auto by = [&](int k) { return ex2(fminf((float)q_exponent(q_scale(keys[k])) - 6.f - v_ref, 0.f)); };
+                r[kk] = q_mul2(r[kk], q_half2(by(2 * kk), by(2 * kk + 1)));
+              }
+              tmem_st16(s_addr + 16 * b, r);
+            }
           }
         } else {
         float s[128];

@@ -10,7 +10,7 @@ import _kvq_seen as seen
 
 pytestmark = pytest.mark.gpu
 BF, F32 = torch.bfloat16, torch.float32
-KINDS = [(BF, BF, 4), (BF, F32, 4), (F32, F32, 4), (F32, BF, 4), (BF, BF, 7)]  # q, O, rows
+KINDS = [(BF, BF, 4), (BF, F32, 4), (F32, F32, 4), (F32, BF, 4), (BF, BF, 7), (BF, BF, 70), (BF, F32, 70)]  # q, O, rows
 
 
 @pytest.fixture(scope="module")
@@ -45,7 +45,7 @@ def run(kv, dtype, out_dtype, rows, D, bits, group, which, factor, at, n, causal
 
 
 @pytest.mark.parametrize("dtype,out_dtype,rows", KINDS)
-@pytest.mark.parametrize("which", ["v"])
+@pytest.mark.parametrize("which", ["v", "k"])
 @pytest.mark.parametrize("bits", [4, 8])
 @pytest.mark.parametrize("factor", [2.0 ** 16, 2.0 ** 31, -2.0 ** 60])
 def test_a_large_token_behind_a_row(kv, dtype, out_dtype, rows, which, bits, factor):
@@ -55,10 +55,31 @@ def test_a_large_token_behind_a_row(kv, dtype, out_dtype, rows, which, bits, fac
 
 
 @pytest.mark.parametrize("dtype,out_dtype,rows", KINDS)
-@pytest.mark.parametrize("which", ["v"])
+@pytest.mark.parametrize("which", ["v", "k"])
 @pytest.mark.parametrize("bits", [4, 8])
 @pytest.mark.parametrize("causal", [False, True])
 def test_a_large_token_before_a_rows_window(kv, dtype, out_dtype, rows, which, bits, causal):
     """A token that the first rows' windows hold and the last rows' do not."""
     n = 300 + rows
     run(kv, dtype, out_dtype, rows, 64, bits, 64, which, 2.0 ** 45, n - 40 - rows // 2, n, causal, 40)
+
+
+@pytest.mark.parametrize("dtype,out_dtype,rows", KINDS)
+@pytest.mark.parametrize("bits", [4, 8])
+def test_small_keys_beside_large_ones(kv, dtype, out_dtype, rows, bits):
+    """K of very different sizes, all seen: the large ones' scores far below the others', so that these alone make O."""
+    D, n, H = 64, 130 + rows, 2
+    cache, given = ref.make(kv, [n], 16, 1, D, bits, D, dtype, seed=4, stored=False)
+    g = torch.Generator().manual_seed(9)
+    q = (1 + 0.3 * torch.randn(rows, H, D, generator=g)).to(dtype).cuda()
+    k = torch.randn(n, 1, D, generator=g)
+    k[5::7] = -(2.0 ** 20) * (1 + 0.2 * torch.rand(k[5::7].shape, generator=g))
+    k[3::31] *= 2.0 ** -20
+    v = torch.randn(n, 1, D, generator=g)
+    cache.append(None, k.to(dtype).cuda(), v.to(dtype).cuda(), torch.tensor([0, n], dtype=torch.int32).cuda())
+    o, l = cache.attend(q, torch.tensor([0, rows], dtype=torch.int32).cuda(), out_dtype=out_dtype)
+    cache.check()
+    want, want_l, bo, bl = seen.attend(cache, q, [rows], [0], D ** -0.5, True, 0, 0, dtype == BF and rows > 16, out_dtype == F32)
+    _kv_ref.close(o.cpu(), want, bo, "O")
+    assert bool(((l.cpu().double() - want_l).abs() <= bl).all()), float((l.cpu().double() - want_l).abs().max())
+    assert float(want_l.abs().max()) < 50

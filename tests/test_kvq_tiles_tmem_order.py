@@ -6,7 +6,7 @@ import re
 
 ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
 SOURCE = os.path.join(ROOT, "attention_fa_fwd_02_gb300", "csrc", "kv_tiles.cu")
-CALL = re.compile(r"\b(rescale|tmem_ld32x4|tmem_ld32x2|tmem_ld32|tmem_st32|tmem_st_wait)\(([^;]*?)\)?;")
+CALL = re.compile(r"\b(rescale|tmem_ld32x4|tmem_ld32x2|tmem_ld32|tmem_ld16|tmem_st32|tmem_st16|tmem_st_wait)\(([^;]*?)\)?;")
 
 
 def block(text, at):
@@ -32,7 +32,7 @@ def unordered(calls):
     for i, (what, where) in enumerate(calls):
         if what == "tmem_st_wait":
             pending.clear()
-        elif what == "tmem_st32":
+        elif what.startswith("tmem_st"):
             pending.add(where)
         elif where in pending:
             bad.append((i, what, where))
@@ -40,7 +40,7 @@ def unordered(calls):
 
 
 def softmax_over_codes():
-    """The accesses of one tile, every branch taken: the exponent's move, then twice the loop over 64 keys."""
+    """The accesses of one tile, every branch taken: the exponent's move, twice the loop over 64 keys, what follows it."""
     with open(SOURCE) as f:
         text = f.read()
     tile = block(text, text.index("if constexpr (BITS != 0)", text.index("// ------------------------------------------------------------ softmax")))
@@ -48,11 +48,11 @@ def softmax_over_codes():
     body = block(tile, tile.index("{", tile.index(")", name)))
     rest = tile.replace(body, "", 1)
     loop = block(rest, rest.index("for (int h = 0; h < 2; ++h)"))
-    before = rest[:rest.index("for (int h = 0; h < 2; ++h)")]
+    before, after = rest.split(loop)
     moves = accesses(body)
     assert moves and {c for c, _ in moves} >= {"tmem_ld32", "tmem_st32"}
     out = []
-    for call in accesses(before) + 2 * accesses(loop):
+    for call in accesses(before) + 2 * accesses(loop) + accesses(after.split("} else {")[0]):
         out += moves if call[0] == "rescale" else [call]
     assert sum(c == ("tmem_ld32", "o") for c in out) >= 3 and sum(c == ("tmem_st32", "s") for c in out) >= 4
     return out
