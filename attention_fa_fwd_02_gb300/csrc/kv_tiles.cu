@@ -978,7 +978,8 @@ __global__ void __launch_bounds__(TilesCfg<D, BITS>::THREADS, 1)
                 tmem_st_wait();
               }
             }
-            const bool more = t == 0 || v_row > v_ref + 6.f;
+            v_row -= 5.f;  // (room for one more: what is under 2^-30 of the largest V is lost in P, not 2^-25)
+            const bool more = t == 0 || v_row > v_ref + 1.f;
             if (t > 0 && __any_sync(0xffffffffu, more)) rescale(more ? ex2(v_ref - v_row) : 1.f);
             if (more) v_ref = v_row;
           }
@@ -1024,12 +1025,14 @@ __global__ void __launch_bounds__(TilesCfg<D, BITS>::THREADS, 1)
               l *= corr;
               if (t > 0) rescale(corr);
               if (h > 0) {
-                const uint32_t by = pack_half2(corr, corr);
+                // (P is up to 2^14, so corr is not to be lost before it: 2^-14 of it, and the rest)
+                const float most = fmaxf(corr, 0x1p-14f), rest = corr * (1.f / most);
+                const uint32_t by = pack_half2(most, most), by2 = pack_half2(rest, rest);
                 tmem_st_wait();
                 uint32_t r[32];
                 tmem_ld32(s_addr, r);
 #pragma unroll
-                for (int kk = 0; kk < 32; ++kk) r[kk] = q_fma2(r[kk], by, 0u);
+                for (int kk = 0; kk < 32; ++kk) r[kk] = q_mul2(q_mul2(r[kk], by), by2);
                 tmem_st32(s_addr, r);
               }
               less = m = m_new;

@@ -17,8 +17,8 @@ A product of a probability and V, few rows: probability times scale in fp16 (one
 2^-30 of the largest scale S so far is lost, taken against the largest score so far: 2^-30 |x| S exp(top - LSE) of a code x
 (of a scale that is not 0). Many rows: V to 2^-11 twice (z', then s x + z'), P to 2^-11, and P's floor in fp16, at most three
 roundings of 2^-25, P being p 2^(E - R): E the exponent that brings the key's largest value U below 2^7 (so 2^-E < 2^7 / U), R
-at most that of the largest value V so far (2^R <= 2^-6 V), or up to 3 more (of a neighbour that is hidden): 2^-23 2^(R - E)
-of a value v, and 2 for a reference that is a whole power of two: 2^-18 V |v| / U exp(top - LSE). A group of keys that is gone
+at most 5 less than that of the largest value V so far (2^R <= 2^-11 V), or up to 3 more (of a neighbour that is hidden): 2^-23
+2^(R - E) of a value v, and 2 for a reference that is a whole power of two: 2^-23 V |v| / U exp(top - LSE). A group of keys that is gone
 through at once has 128 (few rows: up to 64) of them; a part that begins later has seen less, and smaller."""
 import math
 
@@ -87,7 +87,7 @@ def attend(cache, q, new, slots, scale, causal=True, window=0, plane=0, tiles=Fa
             size_v = (torch.maximum(vz.abs(), (vs * steps + vz).abs()) if tiles else vs)[:, i].amax(1)
             largest = so_far(seen(size_v)) * top * see
             if tiles:
-                floor = 2.0 ** -18 * (largest / size_v.clamp(min=1e-100)) @ mass
+                floor = 2.0 ** -23 * (largest / size_v.clamp(min=1e-100)) @ mass
             else:
                 floor = 2.0 ** -30 * largest @ ((vc - mid).abs() * (vs > 0))[:, i]
             moved = torch.stack([(w[r, :, None] * (v[:, i] - O[at + r, h]).abs()).sum(0) for r in range(n)])
