@@ -279,7 +279,7 @@ __global__ void __launch_bounds__(QROWS_THREADS) qattend_q_kernel(const __nv_bfl
     top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, d));
     fine = __shfl_xor_sync(0xffffffffu, (int)fine, d) && fine;
   }
-  const int e = min(max(q_exponent(top), -60), 127);
+  const int e = min(max(q_exponent(top), -100), 127);
   const float by = fine ? q_pow2(14 - e) : __int_as_float(0x7fffffff);
   uint32_t y[4];
   float sum = 0.f;

@@ -37,3 +37,20 @@ def test_rows_of_large_scores(kv, dtype, rows, bits, k, q):
         want, want_l, bo, bl = seen.attend(cache, x, [rows], [0], D ** -0.5, True, 0, 0, dtype == BF and rows > 16, odt == F32)
         _kv_ref.close(o.cpu(), want, bo, "O")
         assert bool(((l.cpu().double() - want_l).abs() <= bl).all())
+
+
+@pytest.mark.parametrize("dtype,rows", [(BF, 1), (BF, 6), (F32, 3), (BF, 60)])
+@pytest.mark.parametrize("bits", [4, 8])
+def test_queries_far_below_one(kv, dtype, rows, bits):
+    """q of 2^-90, as exact as any other, with K of 2^70 and a softmax scale of 2^20: ordinary scores."""
+    D, n, H = 64, 300, 4
+    cache, given = ref.make(kv, [n], 16, 1, D, bits, D, dtype, seed=7)
+    cache.append(None, given[0][0] * 2.0 ** 70, given[0][1], torch.tensor([0, n], dtype=torch.int32).cuda())
+    g = torch.Generator().manual_seed(8)
+    q = (torch.randn(rows, H, D, generator=g) * 2.0 ** -90).to(dtype).cuda()
+    scale = 2.0 ** 20 * D ** -0.5
+    o, l = cache.attend(q, torch.tensor([0, rows], dtype=torch.int32).cuda(), scale=scale)
+    cache.check()
+    want, want_l, bo, bl = seen.attend(cache, q, [rows], [0], scale, True, 0, 0, dtype == BF and rows > 16)
+    _kv_ref.close(o.cpu(), want, bo, "O")
+    assert bool(((l.cpu().double() - want_l).abs() <= bl).all())
