@@ -394,6 +394,8 @@ FA_API fa_status fakv_qread(void* K_out, void* V_out, const int* cu, const int* 
   if (t.B == 0 || t.T == 0) return FA_OK;
   if (!K_out || !V_out) return FA_ERR_INVALID_ARG;
   if (!aligned(K_out, 16) || !aligned(V_out, 16)) return FA_ERR_ALIGNMENT;
+  const uintptr_t k = reinterpret_cast<uintptr_t>(K_out), v = reinterpret_cast<uintptr_t>(V_out);
+  if ((k > v ? k - v : v - k) < (uintptr_t)t.T * cache->HKV * cache->D * esize(t.out_dtype)) return FA_ERR_INVALID_ARG;
   return launch_qread(K_out, V_out, cu, slots, first, qcache_of(*cache, pages, t.plane), t,
                       reinterpret_cast<cudaStream_t>(stream));
 }

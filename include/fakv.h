@@ -265,7 +265,7 @@ FA_API fa_status fakv_qappend(const void* q, const void* k, const void* v, void*
                               const fakv_qcache* cache, const fakv_tokens* p, fa_stream_t stream);
 
 /* What the cache stands for, s c + z in fp32 with one rounding on store, as contiguous
- * K_out, V_out [T, HKV, D] of out_dtype (16-byte aligned): row i of sequence b is position
+ * K_out, V_out [T, HKV, D] of out_dtype (16-byte aligned, not overlapping): row i of sequence b is position
  * first[b] + i of its slot (first NULL: the slot's last tokens, position lens - n + i). Rows of a
  * sequence whose token does not exist (a bad slot, a position outside [0, lens), no page) are
  * zeros and set the status bit; rows from cu[B] on are not written. Of `p` the call reads B, T,
