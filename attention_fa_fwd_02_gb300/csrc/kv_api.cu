@@ -412,10 +412,15 @@ FA_API fa_status fakv_qattend(const void* q, void* O, float* LSE, const int* cu,
   fakv_tokens t = *p;
   if (t.window >= cache->max_pages * cache->page_size) t.window = 0;  // hides nothing
   // Above this many rows per sequence and kv head (on average) tensor-core tiles, whose time hardly depends on how many
-  // there are, where kv_qrows.cu makes numbers of all codes again for every 16. D 128, 8 kv heads, us (rows, tiles):
-  //   4 bits  16 sequences of up to 8192: 27 rows 82, 96; 35 rows 99, 97     one of 16384: 48 rows 32, 35; 64 rows 38, 35
-  //   8 bits  27 rows 87, 119; 35 rows 103, 119                              48 rows 33, 41; 64 rows 39, 41
-  const long long limit = cache->bits == 4 ? 32 : 48;
+  // there are, where kv_qrows.cu makes numbers of all codes again for every 16. 8 kv heads, us (rows, tiles):
+  //                                 4 bits: 32 rows  48 rows   64 rows   80 rows     8 bits: 48 rows   64 rows   80 rows
+  //   16 sequences of up to 8192       74,  95  108,  98  134, 101  163, 100            118, 121  141, 123  174, 122
+  //   64 of up to 2048                 85, 114  116, 117  148, 118  179, 121            123, 135  154, 138  189, 140
+  //   4 of up to 65536                121, 172  172, 172  223, 172  269, 175            176, 207  232, 208  275, 211
+  //   one of 16384                     28,  36   34,  36   40,  36   44,  36             35,  41   40,  41   46,  42
+  //   16 of up to 8192, D 64           51,  92   70,  92   88,  95  107,  94             73,  85   90,  88  112,  87
+  // One short sequence is better served by rows for longer (4096 tokens: up to 100), but lengths are on the device.
+  const long long limit = cache->D > 64 ? 48 : 64;
   if (cache->dtype == FA_BF16 && (long long)t.T * (t.H / cache->HKV) > limit * t.B) {
     st = launch_qattend_tiles(q, O, LSE, cu, slots, qcache_of(*cache, pages, p->plane), t,
                               reinterpret_cast<cudaStream_t>(stream));

@@ -293,7 +293,7 @@ FA_API fa_status fakv_qread(void* K_out, void* V_out, const int* cu, const int* 
  * NaN or infinity in a row of q makes that row's O and LSE NaN and no other's. A key that stands for NaN makes
  * the rows that see it NaN (K: O and LSE; V: their O in the group's columns, and where there are many
  * rows all of O, and LSE) and no other. Which kernel is chosen, T and a batch of both kinds: as for fakv_attend,
- * but with 32 (4 bits) or 48 (8 bits) rows per sequence and kv head as the limit. */
+ * but with 48 rows per sequence and kv head (64 where D is at most 64) as the limit. */
 FA_API fa_status fakv_qattend(const void* q, void* O, float* LSE, const int* cu, const int* slots,
                               const fakv_qcache* cache, const fakv_tokens* p, fa_stream_t stream);
 
