@@ -1,7 +1,7 @@
 """Build libfa.so (the sm_103a attention library) in-tree with nvcc.
 
-Three translation units (forward kernels, backward kernels, C-ABI host code) are
-compiled in parallel for ``sm_103a`` only and linked into
+The translation units of ``SOURCES`` (the contiguous forward and backward, the paged cache's kernels,
+C-ABI host code) are compiled in parallel for ``sm_103a`` only and linked into
 ``attention_fa_fwd_02_gb300/libfa.so`` with the static CUDA runtime. Run as
 ``python -m attention_fa_fwd_02_gb300.build`` or through ``__graft_entry__.build()``.
 """

@@ -505,6 +505,7 @@ __global__ void __launch_bounds__(NTHREADS, QRowsCfg<E, OUT_BF, BITS, D, NG_, NT
 #pragma unroll
                 for (int e = 0; e < 4; ++e) o[w][t][nt][e] *= e & 1 ? f.y : f.x;
           }
+          __syncwarp();  // (rows move by themselves: together again for the products)
         }
 #pragma unroll
         for (int kt = 0; kt < KT; ++kt)

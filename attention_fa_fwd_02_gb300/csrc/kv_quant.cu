@@ -102,8 +102,8 @@ __device__ __forceinline__ Grid grid_of(float lo, float hi, float steps, bool fi
 }
 // The codes of eight columns: quotients rounded to integers. A product with 1 / s (exact, as the fused operations take
 // it) is off from the quotient by less than 2^-14 (of up to 256: 2^-23 of it and of 1 / s), so it rounds to the same
-// integer unless it lies that near to the middle between two; there, one value in some hundreds, the quotient itself is
-// formed. The integers stand in the low bits of 1.5 * 2^23 and more.
+// integer unless it lies that near to the middle between two; there, one value in some thousands, the quotients of its eight
+// columns are formed. The integers stand in the low bits of 1.5 * 2^23 and more.
 __device__ __forceinline__ void codes_of(const float (&x)[8], const Grid& g, float inv, uint32_t (&code)[8]) {
   constexpr float MAGIC = 12582912.f;
   bool near = false;
@@ -413,7 +413,7 @@ __global__ void __launch_bounds__(THREADS) qread_kernel(const __grid_constant__ 
           code[w][i] = *reinterpret_cast<const uint16_t*>(at);
         } else {
           code[w][i] = which == 0 ? *reinterpret_cast<const uint32_t*>(block + q_k_at(a.q.chunks, sh.at[k], chunk, word))
-                                  : q_v_load<8>(block + q_v_at(8, a.q.chunks, sh.at[k], chunk, word));
+                                  : q_v_load8(block + q_v_at(8, a.q.chunks, sh.at[k], chunk, word));
         }
       }
     if (there) {
@@ -451,7 +451,7 @@ void shape(MoveArgs& a, int heads, dim3* grid) {
   while (a.span > 1 && (a.T + a.span - 1) / a.span < want) a.span /= 2;
   const int blocks = (a.T + a.span - 1) / a.span;
   int parts = 1;
-  // (a part has a warp's rows for each of its warps at least)
+  // (a part keeps more than the eight rows of one warp; the block's other warps may have none, as in a step of few tokens)
   while (parts * blocks < want && heads * a.span > 2 * parts * ROWS) parts *= 2;
   a.per = (heads + parts - 1) / parts;
   a.span_shift = log2_of(a.span);

@@ -42,16 +42,10 @@ __device__ __forceinline__ void q_v_store(uint8_t* at, uint32_t w) {
     for (int i = 0; i < 4; ++i) at[2 * i] = (uint8_t)(w >> (8 * i));
   }
 }
-template <int BITS>
-__device__ __forceinline__ uint32_t q_v_load(const uint8_t* at) {
-  if constexpr (BITS == 4) {
-    const uint16_t* const p = reinterpret_cast<const uint16_t*>(at);
-    return p[0] | (uint32_t)p[2] << 16;
-  } else {
-    // (both tokens' codes in two aligned words)
-    const uint2 v = *reinterpret_cast<const uint2*>(reinterpret_cast<uintptr_t>(at) & ~(uintptr_t)7);
-    return __byte_perm(v.x, v.y, reinterpret_cast<uintptr_t>(at) & 1 ? 0x7531 : 0x6420);
-  }
+// (8 bits: both tokens' codes in two aligned words)
+__device__ __forceinline__ uint32_t q_v_load8(const uint8_t* at) {
+  const uint2 v = *reinterpret_cast<const uint2*>(reinterpret_cast<uintptr_t>(at) & ~(uintptr_t)7);
+  return __byte_perm(v.x, v.y, reinterpret_cast<uintptr_t>(at) & 1 ? 0x7531 : 0x6420);
 }
 
 __device__ __forceinline__ float q_scale(uint32_t p) { return __uint_as_float(p << 16); }

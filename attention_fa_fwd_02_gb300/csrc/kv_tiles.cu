@@ -967,6 +967,7 @@ __global__ void __launch_bounds__(TilesCfg<D, BITS>::THREADS, 1)
 #pragma unroll 1
                 for (int kk = max(0, lo_i - c0 - 32 * b); kk <= min(31, hi_i - c0 - 32 * b); ++kk)
                   v_row = fmaxf(v_row, (float)q_exponent(q_scale(keys[kk])));
+                __syncwarp();  // (rows see different keys: together again for tensor memory)
 #pragma unroll 1
                 for (int c = 0; c < 32; c += 16) {
                   uint32_t r[16];
@@ -1042,6 +1043,7 @@ __global__ void __launch_bounds__(TilesCfg<D, BITS>::THREADS, 1)
                 kc[0] = kc[1] = 1.f;
                 less = 0.f;
               }
+              __syncwarp();
             }
             uint32_t pk[32];
 #pragma unroll
