@@ -9,7 +9,7 @@
 //   scores  S = sum_g s_g (sum_{d in g} q_d c_d) + z_g (sum_{d in g} q_d): codes are exact fp16
 //           operands, 2^-24 c, the numbers that fp16 has below its normal ones: an and of the word makes two, and
 //           there is no constant to take off, which for 1024 + c left LSEs up to 2.8e-6 of themselves off and took 144 us where
-//           this takes 135; a key's scales come after the products, in fp32. (O in fp32: x, which costs an addition
+//           this took 135; a key's scales come after the products, in fp32. (O in fp32: x, which costs an addition
 //           a pair.) q times a power of two per row that brings its largest value to 2^14 is fp16 too, exactly but for
 //           what is 2^-28 of that
 //   O^T     O_d = sum_k (p_k s_k) x_kd + sum_k p_k z'_k: the scales enter the probabilities, times a power
@@ -26,8 +26,8 @@
 //      so that every pair is one column of two keys
 //
 // Measured (device, data in L2 where they fit; floor: bytes at the measured copy rate): 64 sequences of up to 16384 tokens in
-// 4 bits, D 128, 135 us (floor 89); 32 of up to 8192 in 8 bits 59 (42; 70 cold); one of 1021 12; 16 of up to 8192
-// with 4 drafted tokens each 39 (12). Not HBM but the instructions that make numbers of codes bound it: 316 to 16 keys of
+// 4 bits, D 128, 130 us (floor 89); 32 of up to 8192 in 8 bits 60 (42; 70 cold); one of 1021 12; 16 of up to 8192
+// with 4 drafted tokens each 41 (12; two warps to a scheduler, 37 % of issue). Not HBM but the instructions that make numbers of codes bound it: 304 to 16 keys of
 // a head (a half of them on the ALU), 56 % of what the warps' schedulers can issue, with three warps to each: more do not fit
 // (128 registers for 16 warps an SM spilled: 153 us). Sixteen rows take those instructions once for two rows' tiles;
 // with more rows they are taken again for every sixteen, and kv_tiles.cu takes over where that costs more. 64 keys to a step

@@ -30,8 +30,8 @@
 // prompt: 650 to 690 us against 385). It is not the tensor pipe that fills then (60 %) but
 // the softmax warps' extra terms and TMEM stores.
 //
-// Measured: 2048 tokens over 16384 (32 query heads on 8 of 128) 309 us with the join, 1670
-// TFLOP/s, 0.86 of the measured peak (337 with the MMAs issued by lane 0 and each descriptor put together anew; the
+// Measured: 2048 tokens over 16384 (32 query heads on 8 of 128) 305 to 317 us with the join, 1660
+// TFLOP/s, 0.86 of the measured peak (333 to 337 with the MMAs issued by lane 0 and each descriptor put together anew; the
 // figures that follow, and those of two terms above, are of that form); 8192 tokens of a prompt 385 us, 0.75. A unit of 128
 // keys takes a CTA 2720 clocks, of which its MMAs fill 2240: a tile's softmax (1130 clocks: 62 to
 // load the scores, 320 for the maximum, 690 for the exponentials) and the hand-offs on both
@@ -46,11 +46,14 @@
 //   warp 9        producer of q alone, which qattend_q_kernel has made fp16 before; warp 10 has nothing to do
 //   warps 0 - 7   the softmax takes 64 keys at a time, its 128 registers having no room for more; P is fp16
 // Three programs at once run an SM's warps out of instruction memory, so the loops over octets and over 64 keys are not
-// unrolled (2048 tokens over 16384 in 4 bits: 1097 us with all unrolled, 475 now). That is 0.56 of the tensor
-// peak at 2.4 us to a unit, of which its MMAs, K's offsets among them, fill 1.45; without turning codes into
-// numbers it takes 424, with half of a softmax 380, without either 338. Eight bits: K's two planes double the first product
+// unrolled, and what keys of very different sizes need (powers of two of their own) goes through tensor memory in small loops
+// behind one vote (2048 tokens over 16384 in 4 bits: 1097 us with all unrolled, 487 now; 514 with a branch on what the code warps had written).
+// That is 0.55 of the tensor peak at 2.4 us to a unit, of which its MMAs, K's offsets among them, fill 1.45. In the form of 475
+// us, without powers of two by key and row: without turning codes into numbers 424, with half of a softmax 380, without either
+// 338. Eight bits: K's two planes double the first product
 // and leave room for one stage of K, so that a unit is its codes, then both tiles' products, in turn (3.9 us; six
-// chunks of up to 500 tokens 89 us; 91 with the factors formed after the wait for the stage). Tried, and slower or the same: 640 threads split 136/48/80 and 128/64/80 registers, three octets of
+// chunks of up to 500 tokens 89 us; 91 with the factors formed after the wait for the stage). Tried, and slower or the same
+// (the codes' form of 479 us): 640 threads split 136/48/80 and 128/64/80 registers, three octets of
 // 8-bit codes ahead, products over the columns that there are (96 of 128 by a branch in the issuer: 577 us for 479; by a kernel of its own 86 for
 // 89, too little for two more), four warps for K
 // and four for V (511; K's are then what all wait for), codes in registers a tile ahead. tests/test_kvq_tiles_sync_model.py
@@ -953,7 +956,7 @@ __global__ void __launch_bounds__(TilesCfg<D, BITS>::THREADS, 1)
             }
             tmem_st_wait();  // (a tile may do it three times: a load is not ordered behind a store by itself)
           };
-          // (2^8 of a probability and 2^6 of V's exponent beyond v_ref: P stays below 2^15. v_ref is the row's, and goes by
+          // (2^8 of a probability and 2^6 of V's exponent beyond v_ref: P is 2^14 at most. v_ref is the row's, and goes by
           // the keys that it sees: of 32 that share an exponent those of which it sees one)
           if (__any_sync(0xffffffffu, t == 0 || v_top > v_ref + 6.f)) {
             float v_row = -106.f;

@@ -280,16 +280,17 @@ FA_API fa_status fakv_qread(void* K_out, void* V_out, const int* cu, const int* 
  *     what is 2^-28 of its row's largest value; an fp32 q in two terms, 2^-22), codes exactly, scales and
  *     offsets in fp32, fp32 sums; a probability times its key's scale in fp16, one term (2^-11) where O is
  *     bf16, two (2^-22) where it is fp32
- *   many rows (bf16 q): K and q as above (scales of K to 2^-21 of the key's largest value), so that LSE is too; V to 2^-11 of the value and of its two parts,
- *     codes times scale and offset, and a probability to 2^-11: of an fp32 O too, whose last bits are better
- *     had from fp32 queries or from fewer rows to a call
- * Products of a probability and a key's V are taken against the largest V of the keys that the row has gone through so far:
- * those 2^-14 of it and smaller lose bits, those below 2^-30 count for nothing (an O that is made of them alone, beside
- * far larger V, is good to that, and not to 2^-11 of itself). Keys that a row does not see have no part in it, whatever
- * their size (many rows: V up to 2^3 times as large as that of a key next to it that the row does see may be what its products are taken
- * against).
- * Scores (times log2 e) are below 2^127 in size; of 2^20 and more they are rounded to 24 bits each before the largest is
- * taken off.
+ *   many rows (bf16 q): K and q as above (scales of K to 2^-21 of the key's largest value), so that LSE
+ *     is too; V to 2^-11 of the value and of its two parts, codes times scale and offset, and a
+ *     probability to 2^-11: of an fp32 O too, whose last bits are better had from fp32 queries or from
+ *     fewer rows to a call
+ * Products of a probability and a key's V are taken against the largest V of the keys that the row has
+ * gone through so far: those 2^-14 of it and smaller lose bits, those below 2^-30 count for nothing (an
+ * O that is made of them alone, beside far larger V, is good to that, and not to 2^-11 of itself). Keys
+ * that a row does not see have no part in it, whatever their size (many rows: V up to 2^3 times as large
+ * as that of a key next to it that the row does see may be what its products are taken against).
+ * Scores (times log2 e) are below 2^127 in size; of 2^20 and more they are rounded to 24 bits each before
+ * the largest is taken off.
  * NaN or infinity in a row of q makes that row's O and LSE NaN and no other's. A key that stands for NaN makes
  * the rows that see it NaN (K: O and LSE; V: their O in the group's columns, and where there are many
  * rows all of O, and LSE) and no other. Which kernel is chosen, T and a batch of both kinds: as for fakv_attend,
